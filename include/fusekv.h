@@ -67,8 +67,9 @@ typedef enum {
   FUSE_ERR_WORKSPACE = 4,     /* workspace null or smaller than fuse_workspace_size */
   FUSE_ERR_CUDA = 5,          /* a CUDA runtime call or launch failed              */
   FUSE_ERR_TIMEOUT = 6,       /* (device) a bounded wait gave up                   */
-  FUSE_ERR_DEVICE_BOUNDS = 7  /* (device) an index read from device memory was out
+  FUSE_ERR_DEVICE_BOUNDS = 7, /* (device) an index read from device memory was out
                                  of range or out of order; the access was skipped  */
+  FUSE_ERR_NO_PAGES = 8       /* (device) a pool has too few free pages; nothing changed */
 } fuse_status_t;
 
 typedef enum { FUSE_F32 = 0, FUSE_BF16 = 1, FUSE_U8_ASYM = 2, FUSE_U4_ASYM = 3 } fuse_dtype_t;
@@ -433,6 +434,144 @@ fuse_status_t fuse_pic_precompute(const fuse_layer_desc_t* desc, const fuse_chun
  * launch. */
 fuse_status_t fuse_kivi_quantize(const fuse_layer_desc_t* desc, const fuse_chunks_t* src,
                                  const fuse_chunks_t* dst, fuse_stream_t stream);
+
+/* ---------------------------------------------------------------------- */
+/* Attention without a fused cache: new tokens over the chunk caches as they
+ * are stored, and whole packed prompts.                                    */
+
+/* Attention of the last n_new tokens of every request straight over its
+ * chunk caches in their storage form (codes of 4 or 8 bits, or layer type;
+ * contiguous or paged): what fuse_stitch_rerotate, fuse_recompute_selected's
+ * scatter and a causal attention over the fused cache give, without writing
+ * that cache.  For request r with its chunks (those whose rows lie in
+ * [row0, row0 + N_r)), the new token u (0 <= u < n_new) is its query token
+ * j = Qn_r - n_new + u, and with s over the keys that it sees
+ *   O[r * n_new + u, h] = softmax_s(q_{u,h} . k_s[h/g] / sqrt(d)) v_s[h/g]:
+ *   - every chunk token at a request position not in idx_r:
+ *     k = R^{pos} K_i[t], v = V_i[t], dequantised, in fp32 (never rounded to
+ *     the layer type);
+ *   - the k_r refreshed rows of the selected positions and the query tokens
+ *     0 .. j (j included): rows of Ks and Vs, already rotated.
+ * R^{pos} and the keys' scales are applied to q (q . R^pos k = R^-pos q . k),
+ * so each code is read once and used as it is.
+ *   Q, O    [n_req * n_new, Hq, d]  request-major; Q rotated at its positions.
+ *   idx     as for fuse_recompute_selected (may be NULL when every k_r is 0).
+ *   Ks, Vs  [R_total, Hkv, d] in desc->dtype, request r's rows at [out0,
+ *           out0 + k_r + Qn_r): its k_r refreshed context tokens, then its
+ *           query tokens (the prompt's query and what was generated since).
+ *           out0 may leave room between requests, so that Qn_r can grow.
+ * Chunk storage: FUSE_U4_ASYM, FUSE_U8_ASYM or desc->dtype.  Requirements
+ * (else FUSE_ERR_INVALID_ARG): 1 <= n_new <= 8 and n_new <= Qn_r; requests
+ * in row order and disjoint; chunks sorted by dst_row, not overlapping, each
+ * inside one request's context.  A block id outside the pool drops its
+ * tokens, a selected index out of range or order is ignored; both are
+ * recorded as FUSE_ERR_DEVICE_BOUNDS.  Softmax statistics and sums are fp32;
+ * no atomics: equal inputs give equal outputs.  The workspace (of
+ * fuse_attend_workspace_size, convention as for fuse_workspace_size) is
+ * written before it is read. */
+#define FUSE_ATTEND_MAX_NEW 8
+fuse_status_t fuse_attend_workspace_size(const fuse_layer_desc_t* desc, const fuse_chunks_t* chunks,
+                                         const fuse_requests_t* reqs, int32_t n_new, size_t* bytes);
+fuse_status_t fuse_attend_chunks(const fuse_layer_desc_t* desc, const fuse_chunks_t* chunks,
+                                 const fuse_requests_t* reqs, int32_t n_new, const void* Q,
+                                 const int32_t* idx, const void* Ks, const void* Vs, void* O,
+                                 void* ws, size_t ws_bytes, fuse_stream_t stream);
+
+/* Causal attention of whole prompts packed back to back ([KVBoost] section
+ * 3.1, Eq. 2, on every row): request r's rows are [row0, row0 + T_r),
+ * T_r = N_r + Qn_r (N_r and Qn_r only add up here; k, sel0, out0 and score0
+ * are not used), and row s of it
+ *   O[row0 + s, h] = softmax_{j <= s}(q_{s,h} . K[row0 + j, h/g] / sqrt(d)) V[row0 + j, h/g].
+ * With one request per chunk it is the attention inside independently
+ * computed chunks ([QCFuse] Eq. 3), with one per prompt that of a prompt
+ * without reuse.  Q, O: [T_total, Hq, d]; K, V: [T_total, Hkv, d]; Q and K
+ * rotated by the caller.  Rows outside every request are neither read nor
+ * written, and nothing that a row does not see reaches it, infinities and
+ * NaN included.  Requests must be in row order and disjoint (else
+ * FUSE_ERR_INVALID_ARG).  O may not overlap Q, K or V.  Needs the workspace
+ * of fuse_workspace_size. */
+fuse_status_t fuse_attend_prompt(const fuse_layer_desc_t* desc, const fuse_requests_t* reqs,
+                                 const void* Q, const void* K, const void* V, void* O, void* ws,
+                                 size_t ws_bytes, fuse_stream_t stream);
+
+/* ---------------------------------------------------------------------- */
+/* Upkeep of a paged cache.  A pool has n_pool_blocks pages of block_size
+ * tokens; sequences name them in block tables (fuse_chunk_t.block_table and
+ * len of a FUSE_KV_PAGED chunk table; its other fields are not used here).
+ * refs [n_pool_blocks] int32 (device) counts the table entries that name
+ * each page; 0 is a free page.  Fork, free and compact keep tables and refs;
+ * what has to be copied goes to a move list,
+ *   moves [2 + 2 * max_moves] int32 (device): the number of moves, the number
+ *   of live pages after the call, then (source page, destination page) pairs,
+ * which fuse_pages_copy applies to each layer's pool.  Every table that names
+ * pages of the pool has to be in the table given to fuse_pages_compact.
+ * Workspace: fuse_pages_workspace_size of the same chunk table (NULL: what
+ * fuse_pages_free and fuse_pages_copy need, its header); calls on different
+ * streams need their own. */
+
+/* Bytes of workspace for fork and compact on these tables. */
+fuse_status_t fuse_pages_workspace_size(const fuse_chunks_t* tables, size_t* bytes);
+
+/* Branch off sequences: dst's table i (device memory that is written,
+ * ceil(len / block_size) entries) shares the full pages of src's table i
+ * (refs + 1) and gets a page of its own in place of a partly filled last one:
+ * the lowest-numbered free pages, in table order, listed in moves.  The same
+ * source may appear any number of times; no dst table may overlap another or
+ * a source.  src and dst have the same lengths.  max_moves must be at least
+ * the number of partly filled last pages (else FUSE_ERR_WORKSPACE).  When a
+ * source entry is outside the pool or names a free page
+ * (FUSE_ERR_DEVICE_BOUNDS), or too few pages are free (FUSE_ERR_NO_PAGES),
+ * nothing changes and the move list is empty. */
+fuse_status_t fuse_pages_fork(const fuse_chunks_t* src, const fuse_chunks_t* dst, int32_t* refs,
+                              int32_t* moves, int32_t max_moves, void* ws, size_t ws_bytes,
+                              fuse_stream_t stream);
+
+/* Drop sequences: every entry of every table gives up one reference.  An
+ * entry outside the pool, or past the references that its page has, is
+ * recorded as FUSE_ERR_DEVICE_BOUNDS and changes nothing.  The tables
+ * themselves are left as they are. */
+fuse_status_t fuse_pages_free(const fuse_chunks_t* tables, int32_t* refs, void* ws, size_t ws_bytes,
+                              fuse_stream_t stream);
+
+/* Pack the pool: with n live pages, the live pages at ids n and above move,
+ * in order, to the free ids below n (as few moves as can be; sources and
+ * destinations are disjoint); tables and refs are rewritten.  max_moves must
+ * be at least n_pool_blocks / 2 (else FUSE_ERR_WORKSPACE).  An entry outside
+ * the pool or naming a free page is recorded as FUSE_ERR_DEVICE_BOUNDS, and
+ * then nothing changes and the move list is empty. */
+fuse_status_t fuse_pages_compact(const fuse_chunks_t* tables, int32_t* refs, int32_t* moves,
+                                 int32_t max_moves, void* ws, size_t ws_bytes,
+                                 fuse_stream_t stream);
+
+/* The pages of one layer: k, v [n_blocks, block_size, Hkv, d] (d / 2 bytes
+ * for FUSE_U4_ASYM), v_scale, v_zero [n_blocks, block_size, Hkv] fp16 for
+ * coded storage (as the PAGED fields of fuse_chunk_t). */
+typedef struct {
+  void* k;
+  void* v;
+  void* v_scale;
+  void* v_zero;
+} fuse_pool_t;
+
+typedef struct {
+  int32_t n_pools;
+  int32_t kv_storage;   /* fuse_dtype_t */
+  int32_t block_size;
+  int32_t reserved;     /* must be 0 */
+  int64_t n_blocks;
+  const fuse_pool_t* h_pools;   /* host [n_pools] */
+} fuse_pools_t;
+
+/* Copy whole pages within every pool: for each pair of the move list, page
+ * src to page dst (rows past a sequence's end included).  moves is read on
+ * the device, so the list of a fork or compaction enqueued just before
+ * applies.  No destination may be another pair's source or destination (the
+ * lists of fork and compact never are; otherwise those pages' contents are
+ * unspecified).  A count above max_moves copies nothing, a page outside the
+ * pool skips its pair; both are recorded as FUSE_ERR_DEVICE_BOUNDS. */
+fuse_status_t fuse_pages_copy(const fuse_layer_desc_t* desc, const fuse_pools_t* pools,
+                              const int32_t* moves, int32_t max_moves, void* ws, size_t ws_bytes,
+                              fuse_stream_t stream);
 
 /* Synchronise the stream, read the workspace's error word, clear it, and
  * return it (FUSE_OK if no device-side error was recorded).  If detail is

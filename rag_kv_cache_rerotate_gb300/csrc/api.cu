@@ -7,6 +7,7 @@
 #include <new>
 #include <vector>
 
+#include "checks.h"
 #include "common.cuh"
 #include "launch.h"
 #include "trace.h"
@@ -61,10 +62,14 @@ cudaError_t launch_attention_tc(const fuse_layer_desc_t& d, const fuse_requests_
                                 void* O, void* tiles_ws, bool tiles_ready, uint32_t* err,
                                 cudaStream_t s);
 
+// ---- argument checks shared by the files of entry points (checks.h) ------
+
 namespace {
 
 constexpr int kMaxPosition = 1 << 24;   // positions stay exact in fp32
 constexpr int kMaxRequests = 65535;      // launch grids give each request one y index
+
+}  // namespace
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -104,15 +109,7 @@ RopeFreqs make_freqs(const fuse_layer_desc_t& d) {
   return f;
 }
 
-struct ReqInfo {
-  fuse_totals_t tot;   // extents implied by the offsets (max over requests)
-  int n_req;
-  bool sorted;         // row0 ascending, request row ranges disjoint
-  int64_t n_qrows;     // sum of n_query: the packed query rows of the scorer
-  int32_t max_query;   // max n_query
-};
-
-fuse_status_t check_reqs(const fuse_requests_t* r, ReqInfo* info, bool need_device = true) {
+fuse_status_t check_reqs(const fuse_requests_t* r, ReqInfo* info, bool need_device) {
   if (!r || r->n_req < 0) return FUSE_ERR_INVALID_ARG;
   if (r->n_req > kMaxRequests) return FUSE_ERR_UNSUPPORTED;   // one grid row per request
   std::memset(info, 0, sizeof(*info));
@@ -178,6 +175,15 @@ fuse_status_t check_chunks(const fuse_layer_desc_t& d, const fuse_chunks_t* c, i
   return FUSE_OK;
 }
 
+fuse_status_t check_ws(void* ws, size_t ws_bytes, size_t need) {
+  if (!ws) return FUSE_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return FUSE_ERR_MISALIGNED;
+  if (ws_bytes < need) return FUSE_ERR_WORKSPACE;
+  return FUSE_OK;
+}
+
+namespace {
+
 // Workspace regions (each 256-byte aligned).
 struct WsLayout {
   size_t partial, keys, map, rows, rope, q, hs, tiles;
@@ -238,13 +244,6 @@ template <typename T> T* at(void* ws, size_t off) {
 }
 
 fuse_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? FUSE_OK : FUSE_ERR_CUDA; }
-
-fuse_status_t check_ws(void* ws, size_t ws_bytes, size_t need) {
-  if (!ws) return FUSE_ERR_WORKSPACE;
-  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return FUSE_ERR_MISALIGNED;
-  if (ws_bytes < need) return FUSE_ERR_WORKSPACE;
-  return FUSE_OK;
-}
 
 // ---- the steps (validated arguments) ------------------------------------
 
@@ -1029,6 +1028,7 @@ const char* fuse_status_string(fuse_status_t s) {
     case FUSE_ERR_CUDA: return "CUDA error";
     case FUSE_ERR_TIMEOUT: return "device wait timed out";
     case FUSE_ERR_DEVICE_BOUNDS: return "device-detected index out of range or order";
+    case FUSE_ERR_NO_PAGES: return "too few free pages";
   }
   return "unknown status";
 }

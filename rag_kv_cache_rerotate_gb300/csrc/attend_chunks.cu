@@ -1,0 +1,615 @@
+// Attention of new tokens over chunk caches in their storage form: the entry
+// points, the CUDA-core kernel and the kernel that joins the items.
+//
+// QCFuse (section 2.1.2, Eq. 4): a chunk's keys, computed at local positions,
+// belong at R^pos K; (section 2.1.3, Eq. 6): selected positions hold
+// refreshed entries.  KVBoost (section 4.5, Eq. 7): x = zero + code * scale.
+//
+// The rotation and the scales move to the query, once per chunk and head:
+//   q . R^pos (z + c * s) = (R^-pos q) . z + ((R^-pos q) * s) . c
+// (z, s per channel), so that a key costs its codes only.  A value's scale
+// and zero are per token: sum_t p_t (z_t + s_t c_t) = sum p_t z_t + sum (p_t
+// s_t) c_t.  Keys are split over many items (attend_chunks.h); with an item's
+// maximum m_i, sum l_i and unnormalised output o_i,
+//   O = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,   M = max_i m_i.
+// The new tokens' own keys (at most 8 per request, the only ones that some
+// of the new tokens see and others do not) are taken by the joining kernel,
+// so items need no causal mask and no row is left without a key.
+#include <algorithm>
+#include <cmath>
+#include <vector>
+
+#include "attend_chunks.h"
+#include "checks.h"
+#include "launch.h"
+#include "trace.h"
+
+namespace fusekv {
+
+namespace {
+
+constexpr int kWarps = 4;                 // items of a CTA of the CUDA-core kernel
+
+// Eight consecutive stored elements as fp32.
+template <int ST> __device__ __forceinline__ void load8(const uint8_t* row, int e, float (&x)[8]) {
+  if constexpr (ST == FUSE_F32) {
+    Vec8<float>::load(reinterpret_cast<const float*>(row) + e, x);
+  } else if constexpr (ST == FUSE_BF16) {
+    Vec8<__nv_bfloat16>::load(reinterpret_cast<const __nv_bfloat16*>(row) + e, x);
+  } else if constexpr (ST == FUSE_U8_ASYM) {
+    const uint2 w = *reinterpret_cast<const uint2*>(row + e);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = (float)((w.x >> (8 * i)) & 0xFFu);
+      x[4 + i] = (float)((w.y >> (8 * i)) & 0xFFu);
+    }
+  } else {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(row + e / 2);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = (float)((w >> (4 * i)) & 15u);
+  }
+}
+
+// EL = 2 or 4 consecutive stored elements as fp32.
+template <int ST, int EL>
+__device__ __forceinline__ void load_el(const uint8_t* row, int e, float (&x)[EL]) {
+  if constexpr (ST == FUSE_F32) {
+#pragma unroll
+    for (int i = 0; i < EL; ++i) x[i] = reinterpret_cast<const float*>(row)[e + i];
+  } else if constexpr (ST == FUSE_BF16) {
+#pragma unroll
+    for (int i = 0; i < EL; ++i) x[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[e + i]);
+  } else if constexpr (ST == FUSE_U8_ASYM) {
+#pragma unroll
+    for (int i = 0; i < EL; ++i) x[i] = (float)row[e + i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < EL; i += 2) {
+      const uint32_t b = row[(e + i) / 2];
+      x[i] = (float)(b & 15u);
+      x[i + 1] = (float)(b >> 4);
+    }
+  }
+}
+
+template <int ST> constexpr bool coded() { return ST == FUSE_U8_ASYM || ST == FUSE_U4_ASYM; }
+template <int ST> constexpr int row_bytes(int d) {
+  return ST == FUSE_F32 ? 4 * d : ST == FUSE_BF16 ? 2 * d : ST == FUSE_U8_ASYM ? d : d / 2;
+}
+
+// The keys of an item.
+struct Keys {
+  const uint8_t *k, *v;                   // row 0, head 0
+  const __half *vs, *vz;
+  const int32_t* table;                   // paged: block ids
+  int t0, t1;                             // rows [t0, t1)
+  int n_skip;                             // selected positions (chunks), ascending
+  const int32_t* skip;
+  int pos0;                               // request position of row 0 (chunks)
+};
+
+// One warp, one item: 32 keys at a time, a lane per key for the scores, then
+// a lane per D / 32 channels for the sums.
+template <typename T, int ST, int D>
+__device__ void attend_item(const AttendArgs& a, const RopeFreqs& f, const Keys& y, bool rotate,
+                            int pos, const __half* ks, const __half* kz, int r, int h, int vg,
+                            int64_t slot, float (*s_q)[D], float (*s_p)[kVecs]) {
+  constexpr int EL = D / 32;
+  const int lane = threadIdx.x % 32;
+  const int n_vec = a.g * a.n_new;
+  float cst[kVecs];
+  // the query vectors, turned back by the chunk's offset and scaled
+#pragma unroll 1
+  for (int v = 0; v < kVecs; ++v) {
+    const int vi = vg * kVecs + v;
+    float z = 0.f;
+    for (int j = lane; j < D / 2; j += 32) {
+      float x0 = 0.f, x1 = 0.f;
+      if (vi < n_vec) {
+        const T* q = reinterpret_cast<const T*>(a.Q) +
+                     ((int64_t)(r * a.n_new + vi / a.g) * a.n_q_heads + h * a.g + vi % a.g) * D;
+        const float q0 = (float)q[j] * a.scale, q1 = (float)q[j + D / 2] * a.scale;
+        float c = 1.f, s = 0.f;
+        if (rotate) rope_cos_sin(pos, f.hi[j], f.mid[j], f.lo[j], c, s);
+        x0 = q0 * c + q1 * s;
+        x1 = q1 * c - q0 * s;
+        if (coded<ST>() && ks) {
+          z += x0 * __half2float(kz[h * D + j]) + x1 * __half2float(kz[h * D + j + D / 2]);
+          x0 *= __half2float(ks[h * D + j]);
+          x1 *= __half2float(ks[h * D + j + D / 2]);
+        }
+      }
+      s_q[v][j] = x0;
+      s_q[v][j + D / 2] = x1;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    cst[v] = z;
+  }
+  __syncwarp();
+  float m[kVecs], l[kVecs], zs[kVecs], acc[kVecs][EL];
+#pragma unroll
+  for (int v = 0; v < kVecs; ++v) {
+    m[v] = -INFINITY;
+    l[v] = zs[v] = 0.f;
+#pragma unroll
+    for (int e = 0; e < EL; ++e) acc[v][e] = 0.f;
+  }
+  constexpr int RB = row_bytes<ST>(D);
+  const int64_t stride = (int64_t)a.n_kv_heads * RB;
+  for (int t = y.t0; t < y.t1; t += 32) {
+    const int key = t + lane;
+    bool ok = key < y.t1;
+    int64_t row = key;
+    if (ok && y.table) {
+      const int b = y.table[key / a.block_size];
+      if (b < 0 || b >= a.n_pool_blocks) {
+        report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_ATTEND_BLOCK, (uint32_t)b);
+        ok = false;
+      } else {
+        row = (int64_t)b * a.block_size + key % a.block_size;
+      }
+    }
+    if (ok && y.n_skip > 0) {              // is the position selected?
+      const int p = y.pos0 + key;
+      int lo = 0, hi = y.n_skip;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (y.skip[mid] < p) lo = mid + 1; else hi = mid;
+      }
+      ok = !(lo < y.n_skip && y.skip[lo] == p);
+    }
+    float s[kVecs];
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) s[v] = ok ? cst[v] : -INFINITY;
+    if (ok) {
+      const uint8_t* kr = y.k + row * stride + h * RB;
+#pragma unroll 2
+      for (int e = 0; e < D; e += 8) {
+        float x[8];
+        load8<ST>(kr, e, x);
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s[v] = fmaf(s_q[v][e + i], x[i], s[v]);
+      }
+    }
+    float vs = 1.f, vz = 0.f;
+    if (coded<ST>() && ok) {
+      vs = __half2float(y.vs[row * a.n_kv_heads + h]);
+      vz = __half2float(y.vz[row * a.n_kv_heads + h]);
+    }
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+      float mt = s[v];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+      const float mn = fmaxf(m[v], mt);
+      const float ref = mn == -INFINITY ? 0.f : mn;
+      const float al = exp2f(m[v] - ref), p = ok ? exp2f(s[v] - ref) : 0.f;
+      m[v] = mn;
+      l[v] = l[v] * al + p;
+      zs[v] = zs[v] * al + p * vz;
+      s_p[lane][v] = p * vs;
+#pragma unroll
+      for (int e = 0; e < EL; ++e) acc[v][e] *= al;
+    }
+    __syncwarp();
+    const int64_t at = ok ? row : -1;
+    for (int i = 0; i < 32; ++i) {
+      const int64_t ri = __shfl_sync(0xffffffffu, at, i);
+      if (ri < 0) continue;
+      float x[EL];
+      load_el<ST, EL>(y.v + ri * stride + h * RB, lane * EL, x);
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+        for (int e = 0; e < EL; ++e) acc[v][e] = fmaf(s_p[i][v], x[e], acc[v][e]);
+    }
+    __syncwarp();
+  }
+  const int64_t at = ((slot * a.n_kv_heads + h) * a.nvg + vg) * kVecs;
+#pragma unroll
+  for (int v = 0; v < kVecs; ++v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      l[v] += __shfl_xor_sync(0xffffffffu, l[v], o);
+      zs[v] += __shfl_xor_sync(0xffffffffu, zs[v], o);
+    }
+    if (lane == 0) a.part_ml[at + v] = make_float2(m[v], l[v]);
+#pragma unroll
+    for (int e = 0; e < EL; ++e) a.part_o[(at + v) * D + lane * EL + e] = acc[v][e] + zs[v];
+  }
+}
+
+template <typename T, int ST, int D>
+__global__ void __launch_bounds__(kWarps * 32)
+    attend_simt_kernel(const AttendArgs a, const __grid_constant__ ChunkOwners owners,
+                       const __grid_constant__ RopeFreqs f, int side_ctas, int n_side_ctas) {
+  __shared__ float s_q[kWarps][kVecs][D];
+  __shared__ float s_p[kWarps][32][kVecs];
+  const int warp = threadIdx.x / 32;
+  constexpr int TS = sizeof(T) == 4 ? FUSE_F32 : FUSE_BF16;
+  pdl_trigger();
+  pdl_wait();
+  const int per_seg = a.n_kv_heads * a.nvg;
+  if ((int)blockIdx.x < n_side_ctas) {
+    // side rows: those before the new tokens
+    const int r = a.req0 + blockIdx.x / side_ctas;
+    const int i = (blockIdx.x % side_ctas) * kWarps + warp;
+    const int seg = i / per_seg, h = i % per_seg / a.nvg, vg = i % a.nvg;
+    const fuse_request_t R = a.reqs[r];
+    const int n = R.k + R.n_query - a.n_new;
+    const int t0 = seg * a.sseg;
+    if (seg >= a.nside || t0 >= n) return;
+    Keys y;
+    constexpr int RB = row_bytes<TS>(D);
+    y.k = reinterpret_cast<const uint8_t*>(a.Ks) + R.out0 * a.n_kv_heads * RB;
+    y.v = reinterpret_cast<const uint8_t*>(a.Vs) + R.out0 * a.n_kv_heads * RB;
+    y.vs = y.vz = nullptr;
+    y.table = nullptr;
+    y.t0 = t0;
+    y.t1 = min(n, t0 + a.sseg);
+    y.n_skip = 0;
+    if (h == 0 && vg == 0) {               // the selection, checked where its rows are read
+      for (int t = y.t0 + threadIdx.x % 32; t < min(y.t1, R.k); t += 32) {
+        const int v = a.idx[R.sel0 + t];
+        if (v < 0 || v >= R.n_ctx || (t > 0 && a.idx[R.sel0 + t - 1] >= v))
+          report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_ATTEND_SEL, (uint32_t)t);
+      }
+    }
+    attend_item<T, TS, D>(a, f, y, false, 0, nullptr, nullptr, r, h, vg,
+                          a.chunk_slots + (int64_t)r * a.nside + seg, s_q[warp], s_p[warp]);
+    return;
+  }
+  const int ctas = (a.nsub * per_seg + kWarps - 1) / kWarps;
+  const int b = blockIdx.x - n_side_ctas;
+  const int ci = b / ctas;
+  const int i = (b % ctas) * kWarps + warp;
+  const int seg = i / per_seg, h = i % per_seg / a.nvg, vg = i % a.nvg;
+  const fuse_chunk_t C = a.chunks[a.chunk0 + ci];
+  const int t0 = seg * a.seg;
+  if (seg >= a.nsub || t0 >= C.len) return;
+  const int r = owners.req[ci];
+  const fuse_request_t R = a.reqs[r];
+  Keys y;
+  y.k = reinterpret_cast<const uint8_t*>(C.k);
+  y.v = reinterpret_cast<const uint8_t*>(C.v);
+  y.vs = reinterpret_cast<const __half*>(C.v_scale);
+  y.vz = reinterpret_cast<const __half*>(C.v_zero);
+  y.table = a.block_size > 0 ? C.block_table : nullptr;
+  y.t0 = t0;
+  y.t1 = min(C.len, t0 + a.seg);
+  y.n_skip = R.k;
+  y.skip = a.idx + R.sel0;
+  y.pos0 = (int)(C.dst_row - R.row0);
+  attend_item<T, ST, D>(a, f, y, C.pos != 0, C.pos, reinterpret_cast<const __half*>(C.k_scale),
+                        reinterpret_cast<const __half*>(C.k_zero), r, h, vg,
+                        (int64_t)(a.chunk0 + ci) * a.nsub + seg, s_q[warp], s_p[warp]);
+}
+
+// Joins the items of one query vector (blockIdx.x = new token * Hq + head)
+// of one request with the new tokens' own keys, and writes its output row.
+// Threads: D channels x kJoin slices of the items.
+constexpr int kJoin = 4;
+constexpr int kJoinTile = 512;            // items whose weights are held at a time
+
+template <typename T, int D>
+__global__ void __launch_bounds__(D * kJoin)
+    attend_combine_kernel(const AttendArgs a, const __grid_constant__ RequestChunks rc) {
+  __shared__ float s_w[kJoinTile];
+  __shared__ float s_own[FUSE_ATTEND_MAX_NEW];
+  __shared__ float s_red[32];
+  __shared__ float s_o[kJoin][D];
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  constexpr int kThreads = D * kJoin;
+  const int r = a.req0 + blockIdx.y;
+  const int u = blockIdx.x / a.n_q_heads, hq = blockIdx.x % a.n_q_heads;
+  const int h = hq / a.g;
+  const int vi = u * a.g + hq % a.g;      // vector of its KV head
+  const fuse_request_t R = a.reqs[r];
+  const int c0 = rc.first[blockIdx.y];
+  const int n_seg = (rc.first[blockIdx.y + 1] - c0) * a.nsub;
+  const int n_side = R.k + R.n_query - a.n_new;           // side rows in items
+  const int n = n_seg + (n_side + a.sseg - 1) / a.sseg;
+  pdl_wait();
+  // item e's slot, or -1 for a segment past its chunk's end
+  auto slot_of = [&](int e) -> int64_t {
+    if (e >= n_seg) return a.chunk_slots + (int64_t)r * a.nside + (e - n_seg);
+    const int c = c0 + e / a.nsub, sub = e % a.nsub;
+    return sub * a.seg < a.chunks[c].len ? (int64_t)c * a.nsub + sub : -1;
+  };
+  auto part = [&](int64_t slot) { return ((slot * a.n_kv_heads + h) * a.nvg + vi / kVecs) * kVecs + vi % kVecs; };
+  // own keys: warp w takes new token w
+  const T* Ks = reinterpret_cast<const T*>(a.Ks);
+  const T* Vs = reinterpret_cast<const T*>(a.Vs);
+  const T* q = reinterpret_cast<const T*>(a.Q) + ((int64_t)(r * a.n_new + u) * a.n_q_heads + hq) * D;
+  const int64_t own0 = R.out0 + n_side;
+  for (int j = warp; j <= u; j += kThreads / 32) {
+    float s = 0.f;
+    for (int e = lane; e < D; e += 32)
+      s = fmaf((float)q[e], (float)Ks[((own0 + j) * a.n_kv_heads + h) * D + e], s);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) s_own[j] = s * a.scale;
+  }
+  // the largest maximum
+  float M = -INFINITY;
+  for (int e = tid; e < n; e += kThreads) {
+    const int64_t sl = slot_of(e);
+    if (sl >= 0) M = fmaxf(M, a.part_ml[part(sl)].x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) s_red[warp] = M;
+  __syncthreads();
+  M = s_red[0];
+  for (int w = 1; w < kThreads / 32; ++w) M = fmaxf(M, s_red[w]);
+  for (int j = 0; j <= u; ++j) M = fmaxf(M, s_own[j]);
+  const float ref = M == -INFINITY ? 0.f : M;
+  const int ch = tid % D, slice = tid / D;
+  float acc = 0.f, l = 0.f;
+  for (int e0 = 0; e0 < n; e0 += kJoinTile) {
+    const int m = min(kJoinTile, n - e0);
+    __syncthreads();
+    for (int e = tid; e < m; e += kThreads) {
+      const int64_t sl = slot_of(e0 + e);
+      float w = -1.f;                     // no such item
+      if (sl >= 0) {
+        const float2 ml = a.part_ml[part(sl)];
+        w = exp2f(ml.x - ref);
+        l = fmaf(w, ml.y, l);
+      }
+      s_w[e] = w;
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int e = slice; e < m; e += kJoin) {
+      const float w = s_w[e];
+      // an item without keys (weight 0) holds zeros
+      if (w != -1.f) acc = fmaf(w, a.part_o[part(slot_of(e0 + e)) * D + ch], acc);
+    }
+  }
+  s_o[slice][ch] = acc;
+  // the sum of the items' sums
+  __syncthreads();
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (lane == 0) s_red[warp] = l;
+  __syncthreads();
+  if (slice > 0) return;
+  l = 0.f;
+  for (int w = 0; w < kThreads / 32; ++w) l += s_red[w];
+  acc = ((s_o[0][ch] + s_o[1][ch]) + s_o[2][ch]) + s_o[3][ch];
+  for (int j = 0; j <= u; ++j) {
+    const float p = exp2f(s_own[j] - ref);
+    l += p;
+    acc = fmaf(p, (float)Vs[((own0 + j) * a.n_kv_heads + h) * D + ch], acc);
+  }
+  reinterpret_cast<T*>(a.O)[((int64_t)(r * a.n_new + u) * a.n_q_heads + hq) * D + ch] = (T)(acc / l);
+}
+
+template <typename T, int ST, int D>
+cudaError_t launch_simt_t(const AttendArgs& a, const ChunkOwners& o, const RopeFreqs& f,
+                          int side_reqs, cudaStream_t s) {
+  const int per_seg = a.n_kv_heads * a.nvg;
+  const int side = (a.nside * per_seg + kWarps - 1) / kWarps;
+  const int ctas = (a.nsub * per_seg + kWarps - 1) / kWarps;
+  const int64_t grid = (int64_t)side * side_reqs + (int64_t)ctas * a.n_chunks;
+  if (grid == 0) return cudaSuccess;
+  return launch_pdl(attend_simt_kernel<T, ST, D>, dim3((unsigned)grid), dim3(kWarps * 32), 0, s, a,
+                    o, f, std::max(side, 1), side * side_reqs);
+}
+
+template <typename T, int D>
+cudaError_t launch_simt_d(int st, const AttendArgs& a, const ChunkOwners& o, const RopeFreqs& f,
+                          int side_reqs, cudaStream_t s) {
+  constexpr int TS = sizeof(T) == 4 ? FUSE_F32 : FUSE_BF16;
+  if (st == FUSE_U4_ASYM) return launch_simt_t<T, FUSE_U4_ASYM, D>(a, o, f, side_reqs, s);
+  if (st == FUSE_U8_ASYM) return launch_simt_t<T, FUSE_U8_ASYM, D>(a, o, f, side_reqs, s);
+  return launch_simt_t<T, TS, D>(a, o, f, side_reqs, s);
+}
+
+// ---- host side ---------------------------------------------------------------
+
+constexpr int64_t kItems = 152 * 16;      // warps that one wave of the GPU's 152 SMs holds
+
+int cut(int64_t keys, int64_t items, int step) {     // keys per item, a multiple of step
+  const int64_t k = (keys + items - 1) / items;
+  return (int)std::max<int64_t>(step, (k + step - 1) / step * step);
+}
+
+// Checks everything that needs no tensor; owner[c]: request of chunk c,
+// first[r]: first chunk of request r (n_req + 1 entries).
+fuse_status_t plan_attend(const fuse_layer_desc_t* desc, const fuse_chunks_t* chunks,
+                          const fuse_requests_t* reqs, int n_new, bool need_device, ReqInfo* info,
+                          AttendPlan* P, uint16_t* owner, int32_t* first) {
+  fuse_status_t st = check_desc(desc);
+  if (st != FUSE_OK) return st;
+  st = check_reqs(reqs, info, need_device);
+  if (st != FUSE_OK) return st;
+  if (!chunks || n_new < 1 || n_new > FUSE_ATTEND_MAX_NEW) return FUSE_ERR_INVALID_ARG;
+  if (reqs->n_req > 0 && !info->sorted) return FUSE_ERR_INVALID_ARG;
+  if (chunks->kv_storage != FUSE_U4_ASYM && chunks->kv_storage != FUSE_U8_ASYM &&
+      chunks->kv_storage != desc->dtype)
+    return FUSE_ERR_UNSUPPORTED;
+  fuse_chunks_t c = *chunks;
+  if (!need_device && !c.d_chunks) c.d_chunks = c.h_chunks;    // only its presence is checked
+  int max_len = 0;
+  st = check_chunks(*desc, &c, info->tot.n_tok, &max_len);
+  if (st != FUSE_OK) return st;
+  int64_t n_ctx = 0, n_side = 0, max_side = 0;
+  int r = 0;
+  if (first) first[0] = 0;
+  const fuse_request_t* R = reqs->h_req;
+  int64_t end = 0;
+  for (int i = 0; i < chunks->n_chunks; ++i) {
+    const fuse_chunk_t& q = chunks->h_chunks[i];
+    if (i > 0 && q.dst_row < end) return FUSE_ERR_INVALID_ARG;
+    end = q.dst_row + q.len;
+    // the request whose context holds the chunk (an empty one goes with the
+    // request before it)
+    while (r < reqs->n_req && q.dst_row + (q.len > 0) > R[r].row0 + R[r].n_ctx) {
+      ++r;
+      if (first) first[r] = i;
+    }
+    if (q.len > 0 && (r >= reqs->n_req || q.dst_row < R[r].row0 || end > R[r].row0 + R[r].n_ctx))
+      return FUSE_ERR_INVALID_ARG;
+    if (owner) owner[i] = (uint16_t)std::min(r, std::max(0, reqs->n_req - 1));
+    n_ctx += q.len;
+  }
+  if (first)
+    for (int k = r + 1; k <= reqs->n_req; ++k) first[k] = chunks->n_chunks;
+  for (int i = 0; i < reqs->n_req; ++i) {
+    if (R[i].n_query < n_new) return FUSE_ERR_INVALID_ARG;
+    const int64_t n = (int64_t)R[i].k + R[i].n_query - n_new;
+    n_side += n;
+    max_side = std::max(max_side, n);
+  }
+  const int g = desc->n_q_heads / desc->n_kv_heads;
+  P->nvg = (g * n_new + kVecs - 1) / kVecs;
+  const int64_t per = (int64_t)desc->n_kv_heads * P->nvg;
+  int seg = cut(n_ctx * per, kItems, 32);
+  P->nsub = std::max(1, (max_len + seg - 1) / seg);
+  P->seg = cut(std::max(max_len, 1), P->nsub, 32);
+  int sseg = cut(n_side * per, kItems, 32);
+  P->nside = (int)((max_side + sseg - 1) / sseg);
+  P->sseg = sseg;
+  P->chunk_slots = (int64_t)chunks->n_chunks * P->nsub;
+  P->slots = P->chunk_slots + (int64_t)reqs->n_req * P->nside;
+  const size_t vecs = (size_t)P->slots * per * kVecs;
+  P->part_ml = sizeof(WsHeader);
+  P->part_o = align_up(P->part_ml + vecs * sizeof(float2), 256);
+  P->total = align_up(P->part_o + vecs * desc->head_dim * sizeof(float), 256);
+  // an item count past a launch's grid is far past what a card holds
+  if (P->slots * per > INT32_MAX) return FUSE_ERR_UNSUPPORTED;
+  return FUSE_OK;
+}
+
+template <typename T> T* at(void* ws, size_t off) {
+  return reinterpret_cast<T*>(reinterpret_cast<char*>(ws) + off);
+}
+
+fuse_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? FUSE_OK : FUSE_ERR_CUDA; }
+
+}  // namespace
+
+cudaError_t launch_attend_simt(const fuse_layer_desc_t& d, int st, const AttendArgs& a,
+                               const ChunkOwners& o, const RopeFreqs& f, int side_reqs,
+                               cudaStream_t s) {
+  if (d.dtype == FUSE_BF16)
+    return d.head_dim == 128 ? launch_simt_d<__nv_bfloat16, 128>(st, a, o, f, side_reqs, s)
+                             : launch_simt_d<__nv_bfloat16, 64>(st, a, o, f, side_reqs, s);
+  return d.head_dim == 128 ? launch_simt_d<float, 128>(st, a, o, f, side_reqs, s)
+                           : launch_simt_d<float, 64>(st, a, o, f, side_reqs, s);
+}
+
+cudaError_t launch_attend_combine(const fuse_layer_desc_t& d, const AttendArgs& a,
+                                  const RequestChunks& rc, cudaStream_t s) {
+  const dim3 grid(a.n_new * a.n_q_heads, a.n_req);
+  auto go = [&](auto kernel) {
+    return launch_pdl(kernel, grid, dim3(d.head_dim * kJoin), 0, s, a, rc);
+  };
+  if (d.dtype == FUSE_BF16)
+    return d.head_dim == 128 ? go(attend_combine_kernel<__nv_bfloat16, 128>)
+                             : go(attend_combine_kernel<__nv_bfloat16, 64>);
+  return d.head_dim == 128 ? go(attend_combine_kernel<float, 128>)
+                           : go(attend_combine_kernel<float, 64>);
+}
+
+}  // namespace fusekv
+
+using namespace fusekv;
+
+extern "C" {
+
+fuse_status_t fuse_attend_workspace_size(const fuse_layer_desc_t* desc, const fuse_chunks_t* chunks,
+                                         const fuse_requests_t* reqs, int32_t n_new,
+                                         size_t* bytes) {
+  if (!bytes) return FUSE_ERR_INVALID_ARG;
+  ReqInfo info;
+  AttendPlan P;
+  const fuse_status_t st = plan_attend(desc, chunks, reqs, n_new, false, &info, &P, nullptr, nullptr);
+  if (st != FUSE_OK) return st;
+  *bytes = P.total;
+  return FUSE_OK;
+}
+
+fuse_status_t fuse_attend_chunks(const fuse_layer_desc_t* desc, const fuse_chunks_t* chunks,
+                                 const fuse_requests_t* reqs, int32_t n_new, const void* Q,
+                                 const int32_t* idx, const void* Ks, const void* Vs, void* O,
+                                 void* ws, size_t ws_bytes, fuse_stream_t stream) {
+  if (!chunks || chunks->n_chunks < 0 || !reqs || reqs->n_req < 0) return FUSE_ERR_INVALID_ARG;
+  ReqInfo info;
+  AttendPlan P;
+  std::vector<uint16_t> owner;
+  std::vector<int32_t> first;
+  try {
+    owner.resize(chunks->n_chunks);
+    first.resize((size_t)reqs->n_req + 1);
+  } catch (...) {
+    return FUSE_ERR_INVALID_ARG;
+  }
+  fuse_status_t st = plan_attend(desc, chunks, reqs, n_new, true, &info, &P, owner.data(), first.data());
+  if (st != FUSE_OK) return st;
+  if (reqs->n_req > 0 && (!Q || !Ks || !Vs || !O)) return FUSE_ERR_INVALID_ARG;
+  if (info.tot.n_sel > 0 && !idx) return FUSE_ERR_INVALID_ARG;
+  if (!aligned16(Q) || !aligned16(Ks) || !aligned16(Vs) || !aligned16(O)) return FUSE_ERR_MISALIGNED;
+  if (reinterpret_cast<uintptr_t>(idx) & 3u) return FUSE_ERR_MISALIGNED;
+  st = check_ws(ws, ws_bytes, P.total);
+  if (st != FUSE_OK) return st;
+  if (reqs->n_req == 0) return FUSE_OK;
+  const RopeFreqs f = make_freqs(*desc);
+  AttendArgs a;
+  a.chunks = chunks->d_chunks;
+  a.reqs = reqs->d_req;
+  a.Q = Q;
+  a.idx = idx;
+  a.Ks = Ks;
+  a.Vs = Vs;
+  a.O = O;
+  a.part_o = at<float>(ws, P.part_o);
+  a.part_ml = at<float2>(ws, P.part_ml);
+  a.err = at<uint32_t>(ws, 0);
+  a.n_pool_blocks = chunks->n_pool_blocks;
+  a.chunk_slots = P.chunk_slots;
+  a.n_q_heads = desc->n_q_heads;
+  a.n_kv_heads = desc->n_kv_heads;
+  a.g = desc->n_q_heads / desc->n_kv_heads;
+  a.n_new = n_new;
+  a.nvg = P.nvg;
+  a.seg = P.seg;
+  a.nsub = P.nsub;
+  a.sseg = P.sseg;
+  a.nside = P.nside;
+  a.block_size = chunks->kv_layout == FUSE_KV_PAGED ? chunks->block_size : 0;
+  a.scale = 1.4426950408889634f / std::sqrt((float)desc->head_dim);
+  cudaStream_t s = (cudaStream_t)stream;
+  // the side rows of all requests and the first chunks; then the other chunks
+  ChunkOwners owners;
+  a.req0 = 0;
+  a.n_req = reqs->n_req;
+  for (int c0 = 0; c0 == 0 || c0 < chunks->n_chunks; c0 += kChunkBatch) {
+    a.chunk0 = c0;
+    a.n_chunks = std::min(kChunkBatch, chunks->n_chunks - c0);
+    std::copy(owner.begin() + c0, owner.begin() + c0 + a.n_chunks, owners.req);
+    st = cuda_status(traced("attend_chunks", s, [&] {
+      return launch_attend_simt(*desc, chunks->kv_storage, a, owners, f, c0 == 0 ? a.n_req : 0, s);
+    }));
+    if (st != FUSE_OK) return st;
+  }
+  for (int r0 = 0; r0 < reqs->n_req; r0 += kReqBatch) {
+    RequestChunks rc;
+    a.req0 = r0;
+    a.n_req = std::min(kReqBatch, reqs->n_req - r0);
+    std::copy(first.begin() + r0, first.begin() + r0 + a.n_req + 1, rc.first);
+    st = cuda_status(traced("attend_combine", s, [&] {
+      return launch_attend_combine(*desc, a, rc, s);
+    }));
+    if (st != FUSE_OK) return st;
+  }
+  return FUSE_OK;
+}
+
+}  // extern "C"

@@ -27,6 +27,7 @@ FUSE_ERR_WORKSPACE = 4
 FUSE_ERR_CUDA = 5
 FUSE_ERR_TIMEOUT = 6
 FUSE_ERR_DEVICE_BOUNDS = 7
+FUSE_ERR_NO_PAGES = 8
 
 # fuse_dtype_t, fuse_kv_layout_t, fuse_pos_encoding_t
 FUSE_F32, FUSE_BF16, FUSE_U8_ASYM, FUSE_U4_ASYM = 0, 1, 2, 3
@@ -86,6 +87,16 @@ class PipelineOp(_c.Structure):
 OP_WAIT_FREE, OP_COPY, OP_MARK_READY, OP_WAIT_READY, OP_COMPUTE, OP_MARK_FREE = range(6)
 
 
+class Pool(_c.Structure):
+    _fields_ = [("k", _c.c_void_p), ("v", _c.c_void_p), ("v_scale", _c.c_void_p),
+                ("v_zero", _c.c_void_p)]
+
+
+class Pools(_c.Structure):
+    _fields_ = [("n_pools", _c.c_int32), ("kv_storage", _c.c_int32), ("block_size", _c.c_int32),
+                ("reserved", _c.c_int32), ("n_blocks", _c.c_int64), ("h_pools", _c.c_void_p)]
+
+
 class Totals(_c.Structure):
     _fields_ = [("n_tok", _c.c_int64), ("n_ctx", _c.c_int64), ("n_sel", _c.c_int64),
                 ("n_out", _c.c_int64), ("max_ctx", _c.c_int32), ("max_tok", _c.c_int32)]
@@ -132,6 +143,15 @@ _SIGS = {
                                            _c.c_size_t, _P, _c.POINTER(_c.c_void_p)]),
     "fuse_graph_launch": (_c.c_int, [_c.c_void_p, _P]),
     "fuse_graph_destroy": (None, [_c.c_void_p]),
+    "fuse_attend_workspace_size": (_c.c_int, [_P, _P, _P, _c.c_int32, _c.POINTER(_c.c_size_t)]),
+    "fuse_attend_chunks": (_c.c_int, [_P, _P, _P, _c.c_int32, _P, _P, _P, _P, _P, _P, _c.c_size_t,
+                                      _P]),
+    "fuse_attend_prompt": (_c.c_int, [_P, _P, _P, _P, _P, _P, _P, _c.c_size_t, _P]),
+    "fuse_pages_workspace_size": (_c.c_int, [_P, _c.POINTER(_c.c_size_t)]),
+    "fuse_pages_fork": (_c.c_int, [_P, _P, _P, _P, _c.c_int32, _P, _c.c_size_t, _P]),
+    "fuse_pages_free": (_c.c_int, [_P, _P, _P, _c.c_size_t, _P]),
+    "fuse_pages_compact": (_c.c_int, [_P, _P, _P, _c.c_int32, _P, _c.c_size_t, _P]),
+    "fuse_pages_copy": (_c.c_int, [_P, _P, _P, _c.c_int32, _P, _c.c_size_t, _P]),
     "fuse_check_errors": (_c.c_int, [_P, _P, _c.POINTER(_c.c_uint32)]),
     "fuse_static_select_count": (_c.c_int, [_P, _P, _c.c_int32, _c.c_int32, _P]),
     "fuse_static_select": (_c.c_int, [_P, _P, _c.c_int32, _c.c_int32, _P, _P]),
@@ -201,7 +221,7 @@ def _to_device_bytes(arr, device) -> torch.Tensor:
 
 
 class RequestTable:
-    """Host and device copies of a ``fuse_request_t`` array."""
+    """Host and device copies of a ``fuse_request_t`` array (fixed once built)."""
 
     def __init__(self, reqs: Sequence[Request], device="cuda"):
         self.host = (Request * max(1, len(reqs)))(*reqs)
@@ -209,6 +229,13 @@ class RequestTable:
         self.dev = _to_device_bytes(self.host, device) if device is not None else None
         self.c = Requests(self.n, _c.addressof(self.host),
                           self.dev.data_ptr() if self.dev is not None and self.dev.numel() else None)
+        self._totals = None
+
+    def extents(self) -> Totals:
+        """``totals`` of the table as first asked for."""
+        if self._totals is None:
+            self._totals = self.totals()
+        return self._totals
 
     def totals(self) -> Totals:
         t = Totals()
@@ -454,6 +481,172 @@ def kivi_quantize(desc, src: ChunkTable, dst: ChunkTable, stream=None):
     Eq. 7): input preparation for the int8 / int4 storage modes."""
     _check(load().fuse_kivi_quantize(_c.byref(desc), _c.byref(src.c), _c.byref(dst.c),
                                      _stream(stream)), "fuse_kivi_quantize")
+
+
+def _tensor(t, name, dtype=None, shape=None, optional=False):
+    """Refuse what the raw pointer would hide: a tensor of another type, shape,
+    stride or device than the call reads."""
+    if t is None and optional:
+        return
+    if t is None or not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: a tensor is needed")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name}: {t.dtype}, {dtype} is needed")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor is needed")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, {tuple(shape)} is needed")
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, which is not the current device")
+    if not t.is_cuda and torch.cuda.is_available():
+        raise ValueError(f"{name}: not on a CUDA device")
+
+
+_TORCH_DTYPE = {FUSE_F32: torch.float32, FUSE_BF16: torch.bfloat16}
+
+
+def attend_workspace_size(desc: LayerDesc, chunks: ChunkTable, reqs: RequestTable,
+                          n_new: int) -> int:
+    n = _c.c_size_t(0)
+    _check(load().fuse_attend_workspace_size(_c.byref(desc), _c.byref(chunks.c), _c.byref(reqs.c),
+                                             int(n_new), _c.byref(n)), "fuse_attend_workspace_size")
+    return int(n.value)
+
+
+def alloc_attend_workspace(desc: LayerDesc, chunks: ChunkTable, reqs: RequestTable, n_new: int,
+                           device="cuda") -> torch.Tensor:
+    """A zeroed workspace for ``attend_chunks`` on these tables."""
+    return torch.zeros(attend_workspace_size(desc, chunks, reqs, n_new), dtype=torch.uint8,
+                       device=device)
+
+
+def attend_chunks(desc: LayerDesc, chunks: ChunkTable, reqs: RequestTable, n_new: int, Q, idx,
+                  Ks, Vs, O, ws, stream=None):
+    """Attention of the last ``n_new`` tokens of every request over its chunk
+    caches as stored (codes or layer type), the selected positions ``idx``
+    replaced by the refreshed rows of ``Ks``, ``Vs`` (QCFuse Eqs. 4, 6)."""
+    dt = _TORCH_DTYPE.get(desc.dtype)
+    tot = reqs.extents()
+    _tensor(Q, "Q", dt, (reqs.n * int(n_new), desc.n_q_heads, desc.head_dim))
+    _tensor(O, "O", dt, Q.shape)
+    _tensor(idx, "idx", torch.int32, optional=tot.n_sel == 0)
+    if idx is not None and idx.numel() < tot.n_sel:
+        raise ValueError(f"idx: {idx.numel()} entries, {tot.n_sel} are needed")
+    for t, name in ((Ks, "Ks"), (Vs, "Vs")):
+        _tensor(t, name, dt)
+        if t.dim() != 3 or t.shape[0] < tot.n_out or tuple(t.shape[1:]) != (desc.n_kv_heads,
+                                                                            desc.head_dim):
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, at least {tot.n_out} rows of "
+                             f"{desc.n_kv_heads} heads of {desc.head_dim} are needed")
+    _check(load().fuse_attend_chunks(_c.byref(desc), _c.byref(chunks.c), _c.byref(reqs.c),
+                                     int(n_new), _ptr(Q), _ptr(idx), _ptr(Ks), _ptr(Vs), _ptr(O),
+                                     _ptr(ws), ws.numel(), _stream(stream)), "fuse_attend_chunks")
+
+
+def attend_prompt(desc: LayerDesc, reqs: RequestTable, Q, K, V, O, ws, stream=None):
+    """Causal attention inside every request's rows (whole prompts, packed)."""
+    dt = _TORCH_DTYPE.get(desc.dtype)
+    n_tok = reqs.extents().n_tok
+    for t, name, h in ((Q, "Q", desc.n_q_heads), (K, "K", desc.n_kv_heads),
+                       (V, "V", desc.n_kv_heads), (O, "O", desc.n_q_heads)):
+        _tensor(t, name, dt)
+        if t.dim() != 3 or t.shape[0] < n_tok or tuple(t.shape[1:]) != (h, desc.head_dim):
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, at least {n_tok} rows of {h} heads "
+                             f"of {desc.head_dim} are needed")
+    _check(load().fuse_attend_prompt(_c.byref(desc), _c.byref(reqs.c), _ptr(Q), _ptr(K), _ptr(V),
+                                     _ptr(O), _ptr(ws), ws.numel(), _stream(stream)),
+           "fuse_attend_prompt")
+
+
+class PagePools:
+    """The K and V page pools of one or more layers that share their block
+    tables (``fuse_pools_t``); for coded storage also the scale and zero pools."""
+
+    def __init__(self, k: Sequence[torch.Tensor], v: Sequence[torch.Tensor], kv_storage: int,
+                 block_size: int, v_scale: Sequence[torch.Tensor] = (),
+                 v_zero: Sequence[torch.Tensor] = ()):
+        quant = kv_storage in (FUSE_U8_ASYM, FUSE_U4_ASYM)
+        dt = _TORCH_DTYPE.get(kv_storage, torch.uint8)
+        if len(k) != len(v) or (quant and not len(k) == len(v_scale) == len(v_zero)):
+            raise ValueError("every pool needs its K and V (and for codes its scale and zero)")
+        self.host = (Pool * max(1, len(k)))()
+        self.keep = [list(k), list(v), list(v_scale), list(v_zero)]
+        self.block_size, self.kv_storage = int(block_size), int(kv_storage)
+        self.n_blocks = int(k[0].shape[0]) if len(k) else 1
+        self.shape = tuple(k[0].shape) if len(k) else None
+        for i in range(len(k)):
+            _tensor(k[i], "k", dt, self.shape)
+            _tensor(v[i], "v", dt, self.shape)
+            if self.shape[1] != self.block_size:
+                raise ValueError(f"k: pages of {self.shape[1]} tokens, not {self.block_size}")
+            self.host[i] = Pool(_ptr(k[i]), _ptr(v[i]), None, None)
+            if quant:
+                _tensor(v_scale[i], "v_scale", torch.float16, self.shape[:3])
+                _tensor(v_zero[i], "v_zero", torch.float16, self.shape[:3])
+                self.host[i].v_scale, self.host[i].v_zero = _ptr(v_scale[i]), _ptr(v_zero[i])
+        self.c = Pools(len(k), self.kv_storage, self.block_size, 0, self.n_blocks,
+                       _c.addressof(self.host))
+
+
+def alloc_moves(max_moves: int, device="cuda") -> torch.Tensor:
+    """An empty move list: count, live pages, then room for ``max_moves`` pairs."""
+    return torch.zeros(2 + 2 * int(max_moves), dtype=torch.int32, device=device)
+
+
+def alloc_pages_workspace(tables: Optional[ChunkTable], device="cuda") -> torch.Tensor:
+    """A zeroed workspace for the page calls on ``tables`` (None: copy and free only)."""
+    n = _c.c_size_t(0)
+    _check(load().fuse_pages_workspace_size(_c.byref(tables.c) if tables is not None else None,
+                                            _c.byref(n)), "fuse_pages_workspace_size")
+    return torch.zeros(int(n.value), dtype=torch.uint8, device=device)
+
+
+def _max_moves(moves) -> int:
+    _tensor(moves, "moves", torch.int32)
+    if moves.numel() < 2:
+        raise ValueError("moves: count and live pages need two entries")
+    return (moves.numel() - 2) // 2
+
+
+def _refs(refs, tables):
+    _tensor(refs, "refs", torch.int32)
+    if refs.numel() < tables.c.n_pool_blocks:
+        raise ValueError(f"refs: {refs.numel()} entries for {tables.c.n_pool_blocks} pages")
+
+
+def pages_fork(src: ChunkTable, dst: ChunkTable, refs, moves, ws, stream=None):
+    """Branch off ``src``'s sequences into ``dst``'s tables: full pages shared,
+    partly filled last pages listed in ``moves`` for ``pages_copy``."""
+    _refs(refs, src)
+    _check(load().fuse_pages_fork(_c.byref(src.c), _c.byref(dst.c), _ptr(refs), _ptr(moves),
+                                  _max_moves(moves), _ptr(ws), ws.numel(), _stream(stream)),
+           "fuse_pages_fork")
+
+
+def pages_free(tables: ChunkTable, refs, ws, stream=None):
+    """Every entry of ``tables`` gives up one reference."""
+    _refs(refs, tables)
+    _check(load().fuse_pages_free(_c.byref(tables.c), _ptr(refs), _ptr(ws), ws.numel(),
+                                  _stream(stream)), "fuse_pages_free")
+
+
+def pages_compact(tables: ChunkTable, refs, moves, ws, stream=None):
+    """Pack the live pages to the front: tables and refs rewritten, the page
+    copies listed in ``moves`` for ``pages_copy``."""
+    _refs(refs, tables)
+    _check(load().fuse_pages_compact(_c.byref(tables.c), _ptr(refs), _ptr(moves),
+                                     _max_moves(moves), _ptr(ws), ws.numel(), _stream(stream)),
+           "fuse_pages_compact")
+
+
+def pages_copy(desc: LayerDesc, pools: PagePools, moves, ws, stream=None):
+    """Apply a move list to every pool."""
+    per = desc.head_dim // 2 if pools.kv_storage == FUSE_U4_ASYM else desc.head_dim
+    if pools.shape is not None and pools.shape[2:] != (desc.n_kv_heads, per):
+        raise ValueError(f"pools: pages of {pools.shape[2:]}, {(desc.n_kv_heads, per)} are needed")
+    _check(load().fuse_pages_copy(_c.byref(desc), _c.byref(pools.c), _ptr(moves),
+                                  _max_moves(moves), _ptr(ws), ws.numel(), _stream(stream)),
+           "fuse_pages_copy")
 
 
 def check_errors(ws, stream=None):

@@ -1,0 +1,194 @@
+"""fuse_attend_chunks on the GPU against its fp64 statement: every storage,
+layout, type and head layout, ragged and empty chunks, selections that leave a
+request's chunks without a key, several new tokens, and what must not reach a
+row (selected tokens, unused pages and rows, later tokens)."""
+
+import numpy as np
+import pytest
+import torch
+
+from rag_kv_cache_rerotate_gb300 import fusekv as fk
+
+from cache_ops import Attend, AttendCase, f64
+
+pytestmark = pytest.mark.gpu
+
+
+def check(a: Attend, O=None):
+    O = a.run() if O is None else O
+    fk.check_errors(a.ws)
+    want, tol = a.reference()
+    err = np.abs(f64(O) - want)
+    bad = ~(err <= tol)
+    assert not bad.any(), (int(bad.sum()), float(np.nanmax(err / tol)), np.argwhere(bad)[:3].tolist())
+
+
+RAGGED = dict(lens=[[33, 1, 64], [7], [16, 0, 129, 31]], n_query=[5, 9, 17], k=[13, 0, 60])
+
+
+@pytest.mark.parametrize("storage", ["u4", "u8", "bf16"])
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("heads", [(8, 2, 128), (8, 8, 128), (16, 2, 64), (6, 3, 128)])
+def test_bf16_layers(storage, paged, heads):
+    check(Attend(AttendCase(**RAGGED, storage=storage, paged=paged, heads=heads, gap=3)))
+
+
+@pytest.mark.parametrize("storage", ["u4", "u8", "f32"])
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("heads", [(4, 2, 64), (8, 1, 128)])
+def test_fp32_layers(storage, paged, heads):
+    check(Attend(AttendCase(**RAGGED, storage=storage, paged=paged, heads=heads, dtype="f32", base=1e4)))
+
+
+@pytest.mark.parametrize("new", [2, 3, 8])
+@pytest.mark.parametrize("dtype,storage,heads", [("bf16", "u4", (8, 1, 128)), ("bf16", "u8", (4, 4, 64)),
+                                                 ("bf16", "bf16", (8, 2, 128)), ("f32", "u4", (4, 1, 64))])
+def test_several_new_tokens(new, dtype, storage, heads):
+    check(Attend(AttendCase(**{**RAGGED, "n_query": [new, 9, 17]}, storage=storage, dtype=dtype,
+                            heads=heads, new=new, paged=True, block_size=24, gap=1)))
+
+
+@pytest.mark.parametrize("storage", ["u4", "bf16"])
+def test_requests_without_context_or_with_everything_selected(storage):
+    lens = [[], [40, 25], [0], [1]]
+    check(Attend(AttendCase(lens=lens, n_query=[1, 1, 2, 1], k=[0, 65, 0, 1], storage=storage)))
+
+
+@pytest.mark.parametrize("block_size", [1, 5, 16, 24, 128])
+def test_pages_that_end_inside_a_segment(block_size):
+    check(Attend(AttendCase(lens=[[100, 37]], n_query=[3], k=[20], paged=True, block_size=block_size,
+                            heads=(4, 2, 128))))
+
+
+def test_far_positions():
+    # angles of positions near 2^23 keep their accuracy
+    check(Attend(AttendCase(lens=[[50, 70]], n_query=[2], k=[9], pos_shift=(1 << 23) + 12345,
+                            dtype="f32", heads=(4, 2, 64), base=1e4)))
+
+
+@pytest.mark.parametrize("storage", ["u4", "u8", "bf16"])
+def test_longer_contexts(storage):
+    # several segments per chunk, several requests a wave
+    check(Attend(AttendCase(lens=[[700, 513, 900], [1025]], n_query=[40, 3], k=[300, 100],
+                            storage=storage, heads=(8, 2, 128))))
+
+
+def test_many_requests_and_chunks():
+    # more than one launch's tables of requests and of chunks
+    n = 530
+    check(Attend(AttendCase(lens=[[3, 2, 4, 1]] * n, n_query=[1 + i % 3 for i in range(n)],
+                            k=[i % 5 for i in range(n)], heads=(2, 1, 64))))
+
+
+def test_constant_values_and_keys():
+    # groups with scale 0, as a KIVI constant group stores them
+    a = Attend(AttendCase(lens=[[48]], n_query=[2], k=[0], heads=(4, 2, 128)))
+    a.vs.zero_()
+    a.ks[:, 0].zero_()
+    a.keys = [np.where(np.arange(2)[:, None] == 0, f64(a.kz)[0], a.keys[0])]
+    a.vals = [np.broadcast_to(f64(a.vz)[..., None], a.vals[0].shape)]
+    check(a)
+
+
+@pytest.mark.parametrize("storage", ["u4", "bf16"])
+@pytest.mark.parametrize("paged", [False, True])
+def test_selected_tokens_do_not_reach_a_row(storage, paged):
+    a = Attend(AttendCase(lens=[[60, 45]], n_query=[4], k=[30], storage=storage, paged=paged,
+                          heads=(4, 2, 128)))
+    bs, flat = 16, [60, 45]
+    for p in a.idx_list[0]:
+        i, t = (0, p) if p < 60 else (1, p - 60)
+        at = (int(a.tables[i][t // bs]), t % bs) if paged else (int(p),)
+        if storage == "bf16":
+            a.K[at], a.V[at] = float("nan"), float("inf")
+        else:
+            a.vs[at], a.vz[at] = float("nan"), float("inf")
+    check(a)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_later_tokens_do_not_reach_a_row(dtype):
+    c = AttendCase(lens=[[40]], n_query=[9], k=[5], new=4, dtype=dtype, heads=(4, 2, 64))
+    a = Attend(c)
+    want, tol = a.reference()
+    n = 5 + 9
+    a.Vs[n - 2:n] = float("nan")                         # values of the last two new tokens
+    a.Ks[n - 1] = float("inf")
+    got = f64(a.run())
+    assert (np.abs(got[:2] - want[:2]) <= tol[:2]).all()
+    assert np.isnan(got[2:]).all()
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_what_is_seen_does_reach_a_row(value):
+    a = Attend(AttendCase(lens=[[40]], n_query=[2], k=[0], storage="bf16", heads=(4, 2, 128)))
+    a.V[7, 0, 3] = value
+    got = f64(a.run())
+    assert not np.isfinite(got[0, :2, 3]).any() and np.isfinite(got[0, 2:]).all()
+    assert np.isfinite(np.delete(got[0, :2], 3, -1)).all()
+
+
+@pytest.mark.parametrize("storage", ["u4", "bf16"])
+def test_block_ids_outside_the_pool_are_dropped_and_reported(storage):
+    a = Attend(AttendCase(lens=[[40, 20]], n_query=[2], k=[0], paged=True, storage=storage,
+                          heads=(4, 2, 128)))
+    a.tables[0][1] = a.n_blocks + 5
+    a.tables[1][0] = -3
+    a.run()
+    with pytest.raises(fk.FuseError) as e:
+        fk.check_errors(a.ws)
+    assert e.value.status == fk.FUSE_ERR_DEVICE_BOUNDS
+    want = Attend.__new__(Attend)
+    want.__dict__.update(a.__dict__)
+    gone = np.r_[16:32, 40:56]
+    want.idx_list = [gone]                                # as if selected, with no refreshed row
+    O, tol = want.reference()
+    assert (np.abs(f64(a.O) - O) <= tol).all()
+    a.run()                                               # the error word was cleared, the call repeats
+    with pytest.raises(fk.FuseError):
+        fk.check_errors(a.ws)
+
+
+def test_unordered_or_outside_selection_is_reported():
+    for bad in ([5, 5, 9], [9, 4, 20], [3, 8, 40], [-1, 2, 3]):
+        a = Attend(AttendCase(lens=[[40]], n_query=[2], k=[3], heads=(4, 2, 64)))
+        a.idx.copy_(torch.tensor(bad, dtype=torch.int32))
+        a.run()
+        with pytest.raises(fk.FuseError) as e:
+            fk.check_errors(a.ws)
+        assert e.value.status == fk.FUSE_ERR_DEVICE_BOUNDS
+
+
+def test_cache_past_four_gigabytes():
+    # pages whose byte offsets pass 2^32 and whose element offsets pass 2^31
+    check(Attend(AttendCase(lens=[[70, 33]], n_query=[2], k=[10], storage="bf16", paged=True,
+                            heads=(8, 8, 128), spare_blocks=140000)))
+
+
+def test_repeated_runs_are_equal_bit_for_bit_and_other_memory_is_left():
+    a = Attend(AttendCase(**RAGGED, gap=2))
+    one = a.run().clone()
+    a.O.zero_()
+    a.ws[256:].fill_(0xA5)                               # scratch is written before it is read
+    assert torch.equal(a.run(), one)
+
+
+def test_other_stream_and_graph():
+    a = Attend(AttendCase(**RAGGED, paged=True))
+    want = a.run().clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    a.O.zero_()
+    torch.cuda.synchronize()
+    a.run(stream=s)
+    s.synchronize()
+    assert torch.equal(a.O, want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        a.run(stream=s)
+    for seed in (1, 2):
+        q = torch.randn(a.Q.shape, generator=torch.Generator().manual_seed(seed)).to(a.Q.dtype)
+        a.Q.copy_(q)
+        g.replay()
+        got = a.O.clone()
+        assert torch.equal(a.run(), got)
