@@ -172,7 +172,9 @@ cudaError_t launch_prompt_simt_t(const PromptArgs& a, const PromptTable& p, cuda
 }
 
 // Rows of a request that one tile holds.
-int prompt_rtile(const fuse_layer_desc_t& d) { return kRows / (d.n_q_heads / d.n_kv_heads); }
+int prompt_rtile(const fuse_layer_desc_t& d, bool tc) {
+  return (tc ? 128 : kRows) / (d.n_q_heads / d.n_kv_heads);
+}
 
 // A table of requests (row0, len), longest first.
 fuse_status_t make_table(const std::pair<int32_t, int32_t>* r, int n, int rtile, PromptTable* p) {
@@ -199,9 +201,6 @@ cudaError_t launch_prompt_simt(const fuse_layer_desc_t& d, const PromptTable& p,
                                const void* K, const void* V, void* O, cudaStream_t s) {
   const PromptArgs a{Q, K, V, O, d.n_q_heads, d.n_kv_heads, d.n_q_heads / d.n_kv_heads,
                      1.4426950408889634f / std::sqrt((float)d.head_dim)};
-  if (d.dtype == FUSE_BF16)
-    return d.head_dim == 128 ? launch_prompt_simt_t<__nv_bfloat16, 128>(a, p, s)
-                             : launch_prompt_simt_t<__nv_bfloat16, 64>(a, p, s);
   return d.head_dim == 128 ? launch_prompt_simt_t<float, 128>(a, p, s)
                            : launch_prompt_simt_t<float, 64>(a, p, s);
 }
@@ -236,14 +235,18 @@ extern "C" fuse_status_t fuse_attend_prompt(const fuse_layer_desc_t* desc,
   }
   std::stable_sort(rows.begin(), rows.end(), [](auto& x, auto& y) { return x.second > y.second; });
   cudaStream_t s = (cudaStream_t)stream;
+  const bool tc = prompt_tc_supported(*desc);
+  if (!tc && desc->dtype != FUSE_F32) return FUSE_ERR_UNSUPPORTED;   // no tensor maps: no driver
   for (size_t r0 = 0; r0 < rows.size(); r0 += kPromptBatch) {
     PromptTable p;
     st = make_table(rows.data() + r0, (int)std::min<size_t>(kPromptBatch, rows.size() - r0),
-                    prompt_rtile(*desc), &p);
+                    prompt_rtile(*desc, tc), &p);
     if (st != FUSE_OK) return st;
     if ((int64_t)p.n_tiles * desc->n_kv_heads > INT32_MAX) return FUSE_ERR_UNSUPPORTED;
-    st = cuda_status(traced("attend_prompt_simt", s, [&] {
-      return launch_prompt_simt(*desc, p, Q, K, V, O, s);
+    st = cuda_status(traced(tc ? "attend_prompt_tc" : "attend_prompt_simt", s, [&] {
+      return tc ? launch_prompt_tc(*desc, p, info.tot.n_tok, Q, K, V, O,
+                                   reinterpret_cast<uint32_t*>(ws), s)
+                : launch_prompt_simt(*desc, p, Q, K, V, O, s);
     }));
     if (st != FUSE_OK) return st;
   }

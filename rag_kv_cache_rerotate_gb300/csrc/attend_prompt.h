@@ -50,4 +50,10 @@ __host__ __device__ inline PromptTile prompt_tile(const PromptTable& p, int rtil
 cudaError_t launch_prompt_simt(const fuse_layer_desc_t& d, const PromptTable& p, const void* Q,
                                const void* K, const void* V, void* O, cudaStream_t s);
 
+// bf16 layers: tcgen05 tensor cores (attend_prompt_tc.cu).
+bool prompt_tc_supported(const fuse_layer_desc_t& d);
+cudaError_t launch_prompt_tc(const fuse_layer_desc_t& d, const PromptTable& p, int64_t n_tok,
+                             const void* Q, const void* K, const void* V, void* O, uint32_t* err,
+                             cudaStream_t s);
+
 }  // namespace fusekv

@@ -1,0 +1,666 @@
+// Packed-prompt causal attention on tcgen05 tensor cores (bf16 layers,
+// head_dim 64 or 128).
+//
+// KVBoost (section 3.1, Eq. 2): softmax(q K^T / sqrt(d)) V over j <= s, for
+// every row s of every request.
+//
+// Work unit: one KV head and a tile of 128 / g consecutive rows of one
+// request, whose g query heads share that KV head, packed as the M = 128 rows
+// of the MMA (row r, head hh -> M row r * g + hh).  Keys stream in blocks of
+// 128 from the request's first row up to the tile's last one; as 128 / g
+// divides 128, all rows of a tile lie in its last block, which alone needs a
+// mask.  Per block b:
+//   S = Q K_b^T          tcgen05.mma into TMEM buffer b % 3
+//   P = 2^(S - m)        eight warps in registers, bf16, written back over S
+//   O += P V_b           tcgen05.mma with A = P in TMEM, V MN-major in shared
+//                        memory, O in TMEM columns [384, 384 + d)
+// The running maximum m is raised only when a block exceeds it by more than
+// 2^16 (then O and the running sum are rescaled).  In the last block both
+// products stop at the multiple of 16 keys after the tile's last row.
+// Roles, each behind its own mbarriers: warp 0 loads Q (two buffers) and K
+// blocks, warp 2 V blocks, warp 1 issues the S MMAs, warp 3 the P.V MMAs,
+// warps 4-11 the softmax, warps 12-15 write O / l while the next unit runs.
+// The kernel is persistent: one CTA per SM, units heaviest first, the CTAs
+// visited up and down in turn.
+//
+// What a row does not see must not reach it.  Scores are replaced where they
+// are masked, whatever they were; but 0 * V is not 0 for an infinite or NaN
+// V.  So before the last block's P.V its warp (idle until the softmax is
+// done) clears the V rows behind the tile's last row, which may be another
+// request's, and any element that is not finite in the rows that some rows of
+// the tile see and others do not; the output warps then add those elements
+// back to the rows that do see them.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "attend_prompt.h"
+#include "launch.h"
+#include "tc_ptx.cuh"
+
+namespace fusekv {
+
+bool tma_encode_available();
+bool make_map_3d(CUtensorMap* m, const void* base, const uint64_t dims[3], const uint64_t strides[2],
+                 const uint32_t box[3]);
+
+namespace {
+
+constexpr int kKB = 128;                      // keys per block
+constexpr int kHalf = 128 * 64 * 2;           // 64 columns of a 128-row tile (16 KB)
+constexpr int kQBufs = 2;
+constexpr int kSBufs = 3;
+constexpr int kWarpQK = 0, kWarpS = 1, kWarpV = 2, kWarpPV = 3, kWarpSoft = 4, kWarpOut = 12;
+constexpr int kSoftThreads = 256;
+constexpr int kThreads = 16 * 32;
+constexpr int kTmemCols = 512;                // S0 | S1 | S2 | O
+constexpr int kColO = 384;
+// P is rounded to bf16 and summed in fp32 at the same relative precision
+// whatever its size: a reference up to 2^16 below the true maximum costs no
+// accuracy and saves rescales.
+constexpr float kRescaleThreshold = 16.0f;
+// Reference maximum above every masked score (-1e30 * scale) and below every
+// real one, so masked probabilities are exactly 0.
+constexpr float kFloor = -1.0e29f;
+
+// Ring depths: what fits beside two Q tiles in 227 KB.
+template <int D> struct Ring {
+  static constexpr int tile = (D / 64) * kHalf;
+  static constexpr int K = D == 128 ? 3 : 5;
+  static constexpr int V = D == 128 ? 2 : 5;
+};
+constexpr int kMaxStages = 5;
+
+struct Ctl {
+  uint64_t q_full[kQBufs], q_empty[kQBufs];
+  uint64_t k_full[kMaxStages], k_empty[kMaxStages];
+  uint64_t v_full[kMaxStages], v_empty[kMaxStages];
+  uint64_t s_full[kSBufs], p_full[kSBufs], pv_done[kSBufs];   // [block % 3]
+  uint64_t o_full, o_empty, l_full, fix_full;                  // once per unit
+  uint32_t tmem_base;
+  volatile int abort_flag;
+  volatile int fix;       // the unit's last V block held elements that are not finite
+  float xl[128];          // [row] softmax row sum of the unit being written
+};
+
+template <int D> constexpr int smem_bytes() {
+  return (kQBufs + Ring<D>::K + Ring<D>::V) * Ring<D>::tile + 1024 + (int)sizeof(Ctl);
+}
+static_assert(smem_bytes<128>() <= 227 * 1024 && smem_bytes<64>() <= 227 * 1024, "shared memory");
+
+struct PromptTcArgs {
+  const __nv_bfloat16* V;
+  __nv_bfloat16* O;
+  int Hq, Hkv, g, rtile;
+  int n_units;
+  float scale_log2;       // log2(e) / sqrt(d)
+  uint32_t* err;
+  int st32;               // O 32-byte aligned: 256-bit stores
+};
+
+// Which wait gave up: info = wait id << 20 | CTA (8 bits) << 12 | key block (12 bits).
+enum PromptWait : uint32_t {
+  W_Q_EMPTY = 1, W_K_EMPTY, W_V_EMPTY, W_Q_FULL, W_K_FULL, W_S_FREE, W_P_FULL, W_O_EMPTY,
+  W_V_FULL, W_S_FULL, W_PV_DONE, W_O_FULL, W_L_FULL, W_FIX
+};
+
+__device__ __forceinline__ bool wait1(uint64_t* bar, uint32_t parity, Ctl* ctl, uint32_t* err,
+                                      uint32_t which, int j) {
+  if (tc::mbar_wait(bar, parity, &ctl->abort_flag)) return true;
+  const bool first = ctl->abort_flag == 0;
+  ctl->abort_flag = 1;
+  if (first)
+    report_error(err, FUSE_ERR_TIMEOUT, SITE_PROMPT_TIMEOUT,
+                 (which << 20) | ((blockIdx.x & 0xFFu) << 12) | ((uint32_t)j & 0xFFFu));
+  return false;
+}
+
+// The same by every lane of a warp that goes on to warp-collective instructions.
+__device__ __forceinline__ bool wait32(uint64_t* bar, uint32_t parity, Ctl* ctl, uint32_t* err,
+                                       uint32_t which, int j) {
+  return __all_sync(0xffffffffu, wait1(bar, parity, ctl, err, which, j));
+}
+
+// The unit of a CTA's i-th round: rounds visit the CTAs upwards and downwards in turn.
+__device__ __forceinline__ int unit_at(int i) {
+  const int G = (int)gridDim.x, c = (int)blockIdx.x;
+  return i * G + ((i & 1) ? G - 1 - c : c);
+}
+
+struct Unit {
+  PromptTile t;
+  int kvh;
+  int nkb;                // key blocks
+};
+
+__device__ __forceinline__ Unit unit_rec(const PromptTcArgs& a, const PromptTable& p, int u) {
+  Unit r;
+  r.kvh = u % a.Hkv;
+  r.t = prompt_tile(p, a.rtile, u / a.Hkv);
+  r.nkb = (r.t.first + r.t.rows - 1) / kKB + 1;
+  return r;
+}
+
+// Keys of block j that the tile sees, rounded up to the MMAs' step of 16.
+__device__ __forceinline__ int block_keys(const Unit& u, int j) {
+  return min(kKB, (u.t.first + u.t.rows - j * kKB + 15) & ~15);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Packed pairs of floats: one instruction does the operation on both halves.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// K-step kk (16 columns) of a 128-row K-major tile stored in 64-column halves.
+__device__ __forceinline__ uint64_t kmajor_step(uint32_t tile, int kk) {
+  return tc::smem_desc_k128(tile + (kk >> 2) * kHalf + (kk & 3) * 32);
+}
+
+__device__ __forceinline__ uint32_t drop_nonfinite(uint32_t w, bool* found) {
+  if ((w & 0x7F80u) == 0x7F80u) { w &= 0xFFFF0000u; *found = true; }
+  if ((w & 0x7F800000u) == 0x7F800000u) { w &= 0xFFFFu; *found = true; }
+  return w;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
+                     const __grid_constant__ CUtensorMap mapV, const PromptTcArgs a,
+                     const __grid_constant__ PromptTable table) {
+  constexpr int kTile = Ring<D>::tile, kKS = Ring<D>::K, kVS = Ring<D>::V;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sK = smem + kQBufs * kTile;
+  uint8_t* sV = sK + kKS * kTile;
+  Ctl* ctl = reinterpret_cast<Ctl*>(sV + kVS * kTile);
+  const int warp = threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  pdl_trigger();
+
+  if (threadIdx.x == 0) {
+    for (int q = 0; q < kQBufs; ++q) {
+      tc::mbar_init(&ctl->q_full[q], 1);
+      tc::mbar_init(&ctl->q_empty[q], 1);
+    }
+    for (int s = 0; s < kKS; ++s) {
+      tc::mbar_init(&ctl->k_full[s], 1);
+      tc::mbar_init(&ctl->k_empty[s], 1);
+    }
+    for (int s = 0; s < kVS; ++s) {
+      tc::mbar_init(&ctl->v_full[s], 1);
+      tc::mbar_init(&ctl->v_empty[s], 1);
+    }
+    for (int s = 0; s < kSBufs; ++s) {
+      tc::mbar_init(&ctl->s_full[s], 1);
+      tc::mbar_init(&ctl->p_full[s], kSoftThreads);
+      tc::mbar_init(&ctl->pv_done[s], 1);
+    }
+    tc::mbar_init(&ctl->o_full, 1);
+    tc::mbar_init(&ctl->o_empty, 128);
+    tc::mbar_init(&ctl->l_full, kSoftThreads);
+    tc::mbar_init(&ctl->fix_full, 1);
+    ctl->abort_flag = 0;
+    tc::fence_barrier_init();
+    tc::tma_prefetch_desc(&mapQ);
+    tc::tma_prefetch_desc(&mapK);
+    tc::tma_prefetch_desc(&mapV);
+  }
+  if (warp == kWarpS) tc::tmem_alloc(&ctl->tmem_base, kTmemCols);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  const int n_units = a.n_units;
+  pdl_wait();                 // inputs of the previous kernel complete and visible
+
+  if (warp == kWarpQK) {
+    // --------------------------- Q and K loads ---------------------------
+    if (lane == 0) {
+      uint32_t kc = 0;
+      int i = 0;
+      bool ok = true;
+      for (; unit_at(i) < n_units && ok; ++i) {
+        const Unit cur = unit_rec(a, table, unit_at(i));
+        const int qb = i % kQBufs;
+        if (!wait1(&ctl->q_empty[qb], ((i / kQBufs) & 1) ^ 1, ctl, a.err, W_Q_EMPTY, 0)) break;
+        uint8_t* q = sQ + qb * kTile;
+        tc::mbar_arrive_expect_tx(&ctl->q_full[qb], kTile);
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h)
+          tc::tma_load_3d(q + h * kHalf, &mapQ, &ctl->q_full[qb], 64 * h, cur.kvh * a.g,
+                          cur.t.row0 + cur.t.first);
+        for (int j = 0; j < cur.nkb; ++j, ++kc) {
+          const int st = kc % kKS;
+          if (!wait1(&ctl->k_empty[st], ((kc / kKS) & 1) ^ 1, ctl, a.err, W_K_EMPTY, j)) {
+            ok = false;
+            break;
+          }
+          tc::mbar_arrive_expect_tx(&ctl->k_full[st], kTile);
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            tc::tma_load_3d(sK + st * kTile + h * kHalf, &mapK, &ctl->k_full[st], 64 * h, cur.kvh,
+                            cur.t.row0 + j * kKB);
+        }
+      }
+      // let copies in flight land before the CTA may exit
+      for (int k = (i > kQBufs ? i - kQBufs : 0); k < i; ++k)
+        tc::mbar_wait(&ctl->q_full[k % kQBufs], (k / kQBufs) & 1);
+      for (uint32_t c = (kc > (uint32_t)kKS ? kc - kKS : 0); c < kc; ++c)
+        tc::mbar_wait(&ctl->k_full[c % kKS], (c / kKS) & 1);
+    }
+  } else if (warp == kWarpV) {
+    // ------------------------------ V loads ------------------------------
+    if (lane == 0) {
+      uint32_t vc = 0;
+      bool ok = true;
+      for (int i = 0; unit_at(i) < n_units && ok; ++i) {
+        const Unit cur = unit_rec(a, table, unit_at(i));
+        for (int j = 0; j < cur.nkb; ++j, ++vc) {
+          const int st = vc % kVS;
+          if (!wait1(&ctl->v_empty[st], ((vc / kVS) & 1) ^ 1, ctl, a.err, W_V_EMPTY, j)) {
+            ok = false;
+            break;
+          }
+          tc::mbar_arrive_expect_tx(&ctl->v_full[st], kTile);
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            tc::tma_load_3d(sV + st * kTile + h * kHalf, &mapV, &ctl->v_full[st], 64 * h, cur.kvh,
+                            cur.t.row0 + j * kKB);
+        }
+      }
+      for (uint32_t c = (vc > (uint32_t)kVS ? vc - kVS : 0); c < vc; ++c)
+        tc::mbar_wait(&ctl->v_full[c % kVS], (c / kVS) & 1);
+    }
+  } else if (warp == kWarpS) {
+    // ------------------------------ S = Q K^T ------------------------------
+    if (lane == 0) {
+      uint32_t kc = 0;
+      bool ok = true;
+      for (int i = 0; unit_at(i) < n_units && ok; ++i) {
+        const Unit cur = unit_rec(a, table, unit_at(i));
+        const int qb = i % kQBufs;
+        if (!wait1(&ctl->q_full[qb], (i / kQBufs) & 1, ctl, a.err, W_Q_FULL, 0)) break;
+        const uint32_t q_addr = tc::smem_u32(sQ + qb * kTile);
+        for (int j = 0; j < cur.nkb; ++j, ++kc) {
+          const int st = kc % kKS;
+          if (!wait1(&ctl->k_full[st], (kc / kKS) & 1, ctl, a.err, W_K_FULL, j)) {
+            ok = false;
+            break;
+          }
+          // buffer kc % 3 holds P of three blocks ago until that block's P.V is done
+          const uint32_t sb = kc % kSBufs;
+          if (!wait1(&ctl->pv_done[sb], ((kc / kSBufs) & 1) ^ 1, ctl, a.err, W_S_FREE, j)) {
+            ok = false;
+            break;
+          }
+          tc::tc_fence_after();
+          const uint32_t idesc_s = tc::idesc_bf16_f32(128, block_keys(cur, j));
+          const uint32_t kaddr = tc::smem_u32(sK + st * kTile);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc::mma_bf16(tmem + sb * kKB, kmajor_step(q_addr, kk), kmajor_step(kaddr, kk), idesc_s,
+                         kk != 0);
+          tc::mma_commit(&ctl->s_full[sb]);
+          tc::mma_commit(&ctl->k_empty[st]);
+        }
+        if (!ok) break;
+        tc::mma_commit(&ctl->q_empty[qb]);
+      }
+    }
+  } else if (warp == kWarpPV) {
+    // ------------------------------ O += P V ------------------------------
+    const uint32_t idesc_o = tc::idesc_bf16_f32(128, D, /*b_mn_major=*/true);
+    const uint32_t o = tmem + kColO;
+    uint32_t vc = 0;
+    bool ok = true;
+    for (int i = 0; unit_at(i) < n_units && ok; ++i) {
+      const Unit cur = unit_rec(a, table, unit_at(i));
+      // O and the fix flag were last read by the output warps for unit i - 1
+      if (!wait32(&ctl->o_empty, (i & 1) ^ 1, ctl, a.err, W_O_EMPTY, 0)) break;
+      for (int j = 0; j < cur.nkb; ++j, ++vc) {
+        const int st = vc % kVS;
+        const uint32_t sb = vc % kSBufs;
+        const int keys = block_keys(cur, j);
+        uint8_t* v = sV + st * kTile;
+        if (!wait32(&ctl->v_full[st], (vc / kVS) & 1, ctl, a.err, W_V_FULL, j)) {
+          ok = false;
+          break;
+        }
+        if (j == cur.nkb - 1) {
+          // rows after the tile's first one, four rows of 64 columns at a time
+          const int row1 = cur.t.first + 1 - j * kKB, seen = cur.t.first + cur.t.rows - j * kKB;
+          bool found = false, wrote = false;
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            for (int n = row1 + lane / 8; n < keys; n += 4) {
+              uint4* p = reinterpret_cast<uint4*>(v + h * kHalf + n * 128) + lane % 8;
+              if (n >= seen) {
+                *p = make_uint4(0, 0, 0, 0);
+                wrote = true;
+              } else {
+                uint4 x = *p;
+                bool f = false;
+                x.x = drop_nonfinite(x.x, &f);
+                x.y = drop_nonfinite(x.y, &f);
+                x.z = drop_nonfinite(x.z, &f);
+                x.w = drop_nonfinite(x.w, &f);
+                if (f) {
+                  *p = x;
+                  found = wrote = true;
+                }
+              }
+            }
+          if (wrote) tc::fence_proxy_async_smem();
+          found = __any_sync(0xffffffffu, found);
+          if (lane == 0) {
+            ctl->fix = found;
+            tc::mbar_arrive(&ctl->fix_full);
+          }
+        }
+        if (!wait32(&ctl->p_full[sb], (vc / kSBufs) & 1, ctl, a.err, W_P_FULL, j)) {
+          ok = false;
+          break;
+        }
+        tc::tc_fence_after();
+        if (lane == 0) {
+          const uint32_t vaddr = tc::smem_u32(v);
+          const uint32_t pa = tmem + sb * kKB;
+          for (int kk = 0; kk < keys / 16; ++kk)
+            tc::mma_bf16_ts(o, pa + kk * 8, tc::smem_desc_mn128(vaddr + kk * 16 * 128, kHalf),
+                            idesc_o, (j | kk) != 0 ? 1u : 0u);
+          tc::mma_commit(&ctl->pv_done[sb]);
+          tc::mma_commit(&ctl->v_empty[st]);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (lane == 0) tc::mma_commit(&ctl->o_full);
+    }
+  } else if (warp < kWarpOut) {
+    // ------------------------------- softmax -------------------------------
+    // warp w: TMEM lane quarter w % 4, half (w - 4) / 4 of it: 16 M rows
+    const int base = (warp & 3) * 32 + ((warp - kWarpSoft) >> 2) * 16;
+    const uint32_t lane_off = (uint32_t)base << 16;
+    const int c4 = lane & 3;
+    const int R0 = base + (lane >> 2), R1 = R0 + 8;    // this thread's two M rows
+    const float scale = a.scale_log2;
+    const uint32_t tO = tmem + lane_off + kColO;
+    uint32_t b = 0;
+    for (int i = 0; unit_at(i) < n_units; ++i) {
+      const Unit cur = unit_rec(a, table, unit_at(i));
+      const int p0 = cur.t.first + min(R0 / a.g, cur.t.rows - 1);
+      const int p1 = cur.t.first + min(R1 / a.g, cur.t.rows - 1);
+      float mu0 = kFloor, mu1 = kFloor;                // running maxima (log2 units)
+      float l0 = 0.f, l1 = 0.f;                        // this thread's part of the row sums
+      bool ok = true;
+      for (int j = 0; j < cur.nkb; ++j, ++b) {
+        const uint32_t sb = b % kSBufs;
+        if (!wait32(&ctl->s_full[sb], (b / kSBufs) & 1, ctl, a.err, W_S_FULL, j)) {
+          ok = false;
+          break;
+        }
+        tc::tc_fence_after();
+        const uint32_t tS = tmem + lane_off + sb * kKB;
+        uint32_t r[64];
+        tc::tmem_ld_16x256b_x8(tS, *reinterpret_cast<uint32_t(*)[32]>(r));
+        tc::tmem_ld_16x256b_x8(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
+        tc::tmem_ld_wait();
+        if (j == cur.nkb - 1) {                        // the tile's own rows: mask
+          const int key0 = j * kKB;
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            const int k = key0 + 8 * q + 2 * c4;
+            if (k > p0) r[4 * q] = __float_as_uint(-1e30f);
+            if (k + 1 > p0) r[4 * q + 1] = __float_as_uint(-1e30f);
+            if (k > p1) r[4 * q + 2] = __float_as_uint(-1e30f);
+            if (k + 1 > p1) r[4 * q + 3] = __float_as_uint(-1e30f);
+          }
+        }
+        float m0, m1;
+        {
+          float a0 = __uint_as_float(r[0]), a1 = __uint_as_float(r[1]);
+          float b0 = __uint_as_float(r[2]), b1 = __uint_as_float(r[3]);
+#pragma unroll
+          for (int q = 1; q < 15; q += 2) {                // repeats 1 .. 14 in pairs
+            a0 = max3(a0, __uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 4]));
+            a1 = max3(a1, __uint_as_float(r[4 * q + 1]), __uint_as_float(r[4 * q + 5]));
+            b0 = max3(b0, __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 6]));
+            b1 = max3(b1, __uint_as_float(r[4 * q + 3]), __uint_as_float(r[4 * q + 7]));
+          }
+          m0 = max3(a0, a1, fmaxf(__uint_as_float(r[60]), __uint_as_float(r[61])));   // repeat 15
+          m1 = max3(b0, b1, fmaxf(__uint_as_float(r[62]), __uint_as_float(r[63])));
+          m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, 1));
+          m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, 1));
+          m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, 2));
+          m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, 2));
+        }
+        const float ms0 = m0 * scale, ms1 = m1 * scale;
+        float mn0 = mu0, mn1 = mu1;
+        bool rs0 = false, rs1 = false;
+        if (j == 0) {
+          mn0 = fmaxf(ms0, kFloor);
+          mn1 = fmaxf(ms1, kFloor);
+        } else {
+          if (ms0 > mu0 + kRescaleThreshold) { mn0 = ms0; rs0 = true; }
+          if (ms1 > mu1 + kRescaleThreshold) { mn1 = ms1; rs1 = true; }
+        }
+        const float al0 = rs0 ? ex2(mu0 - mn0) : 1.f, al1 = rs1 ? ex2(mu1 - mn1) : 1.f;
+        // probabilities: key pairs packed as bf16x2, in place over the scores;
+        // the scaling and the row sums work on key pairs (f32x2)
+        const uint64_t sc2 = pack2(scale, scale);
+        const uint64_t ng0 = pack2(-mn0, -mn0), ng1 = pack2(-mn1, -mn1);
+        uint64_t acc0 = 0, acc1 = 0;                    // (even keys, odd keys) of each row
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          const float2 x01 = unpack2(fma2(pack2(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1])), sc2, ng0));
+          const float2 x23 = unpack2(fma2(pack2(__uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3])), sc2, ng1));
+          const float e0 = ex2(x01.x), e1 = ex2(x01.y), e2 = ex2(x23.x), e3 = ex2(x23.y);
+          acc0 = add2(acc0, pack2(e0, e1));
+          acc1 = add2(acc1, pack2(e2, e3));
+          r[2 * q] = pack_bf16x2(e0, e1);
+          r[2 * q + 1] = pack_bf16x2(e2, e3);
+        }
+        const float2 a0 = unpack2(acc0), a1 = unpack2(acc1);
+        const float s0 = a0.x + a0.y, s1 = a1.x + a1.y;
+        tc::tmem_st_16x128b_x16(tS, *reinterpret_cast<uint32_t(*)[32]>(r));
+        // tcgen05.ld/st are warp-collective: the whole warp rescales its rows
+        // of O when any of them needs it (the factor is 1 for the others); O
+        // must hold the previous block's P.V
+        if (__any_sync(0xffffffffu, rs0 || rs1)) {
+          if (!wait32(&ctl->pv_done[(b - 1) % kSBufs], ((b - 1) / kSBufs) & 1, ctl, a.err, W_PV_DONE, j)) {
+            ok = false;
+            break;
+          }
+          tc::tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D; c += 64) {
+            uint32_t o[32];
+            tc::tmem_ld_16x256b_x8(tO + c, o);
+            tc::tmem_ld_wait();
+            const uint64_t f0 = pack2(al0, al0), f1 = pack2(al1, al1);
+#pragma unroll
+            for (int q = 0; q < 32; q += 2) {
+              const float2 v = unpack2(mul2(pack2(__uint_as_float(o[q]), __uint_as_float(o[q + 1])), (q & 2) ? f1 : f0));
+              o[q] = __float_as_uint(v.x);
+              o[q + 1] = __float_as_uint(v.y);
+            }
+            tc::tmem_st_16x256b_x8(tO + c, o);
+          }
+        }
+        tc::tmem_st_wait();
+        tc::tc_fence_before();
+        tc::mbar_arrive(&ctl->p_full[sb]);
+        l0 = l0 * al0 + s0;
+        l1 = l1 * al1 + s1;
+        mu0 = mn0;
+        mu1 = mn1;
+      }
+      if (!ok) break;
+      // row sums: the four threads of a row, in a fixed order
+      l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+      l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+      // the row sums of unit i, once the output warps are done with unit i - 1
+      if (!wait32(&ctl->o_empty, (i & 1) ^ 1, ctl, a.err, W_O_EMPTY, cur.nkb)) break;
+      if (c4 == 0) {
+        ctl->xl[R0] = l0;
+        ctl->xl[R1] = l1;
+      }
+      tc::mbar_arrive(&ctl->l_full);
+    }
+  } else {
+    // ---------------------------- output O / l ----------------------------
+    const int quarter = warp & 3;
+    const int m = quarter * 32 + lane;
+    const uint32_t tO = tmem + ((uint32_t)(quarter * 32) << 16) + kColO;
+    const int rl = m / a.g;
+    const int hh = m % a.g;
+    for (int i = 0; unit_at(i) < n_units; ++i) {
+      const Unit cur = unit_rec(a, table, unit_at(i));
+      if (!wait32(&ctl->o_full, i & 1, ctl, a.err, W_O_FULL, cur.nkb)) break;
+      if (!wait32(&ctl->l_full, i & 1, ctl, a.err, W_L_FULL, cur.nkb)) break;
+      if (!wait32(&ctl->fix_full, i & 1, ctl, a.err, W_FIX, cur.nkb)) break;
+      tc::tc_fence_after();
+      const float inv = 1.f / ctl->xl[m];
+      const bool fix = ctl->fix != 0;
+      const bool valid = rl < cur.t.rows;
+      const int64_t row = cur.t.row0 + cur.t.first;
+      __nv_bfloat16* dst = a.O + ((row + rl) * a.Hq + cur.kvh * a.g + hh) * D;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t r[32];
+        tc::tmem_ld_32x32b_x32(tO + c, r);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * inv);
+        if (fix && valid) {
+          // elements that are not finite, of the rows that this one sees
+          for (int n = 1; n <= rl; ++n) {
+            const __nv_bfloat16* v = a.V + ((row + n) * a.Hkv + cur.kvh) * D + c;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float x = __bfloat162float(v[e]);
+              if (!isfinite(x)) r[e] = __float_as_uint(__uint_as_float(r[e]) + x);
+            }
+          }
+        }
+        if (valid && a.st32) {
+          // one 256-bit store per 16 values: the 32 bytes fill one sector
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              w[e] = pack_bf16x2(__uint_as_float(r[16 * q + 2 * e]), __uint_as_float(r[16 * q + 2 * e + 1]));
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + c + 16 * q),
+                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]),
+                         "r"(w[7])
+                         : "memory");
+          }
+        } else if (valid) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint4 w;
+            w.x = pack_bf16x2(__uint_as_float(r[8 * q + 0]), __uint_as_float(r[8 * q + 1]));
+            w.y = pack_bf16x2(__uint_as_float(r[8 * q + 2]), __uint_as_float(r[8 * q + 3]));
+            w.z = pack_bf16x2(__uint_as_float(r[8 * q + 4]), __uint_as_float(r[8 * q + 5]));
+            w.w = pack_bf16x2(__uint_as_float(r[8 * q + 6]), __uint_as_float(r[8 * q + 7]));
+            reinterpret_cast<uint4*>(dst + c)[q] = w;
+          }
+        }
+      }
+      tc::tc_fence_before();
+      tc::mbar_arrive(&ctl->o_empty);
+    }
+  }
+
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  if (warp == kWarpS) tc::tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int D>
+cudaError_t launch_d(const fuse_layer_desc_t& d, const PromptTable& p, int64_t n_tok, const void* Q,
+                     const void* K, const void* V, void* O, uint32_t* err, cudaStream_t s) {
+  const int g = d.n_q_heads / d.n_kv_heads;
+  CUtensorMap mQ, mK, mV;
+  const uint64_t dq[3] = {(uint64_t)D, (uint64_t)d.n_q_heads, (uint64_t)n_tok};
+  const uint64_t sq[2] = {(uint64_t)D * 2, (uint64_t)d.n_q_heads * D * 2};
+  const uint32_t bq[3] = {64, (uint32_t)g, (uint32_t)(128 / g)};
+  const uint64_t dk[3] = {(uint64_t)D, (uint64_t)d.n_kv_heads, (uint64_t)n_tok};
+  const uint64_t sk[2] = {(uint64_t)D * 2, (uint64_t)d.n_kv_heads * D * 2};
+  const uint32_t bk[3] = {64, 1, (uint32_t)kKB};
+  if (!make_map_3d(&mQ, Q, dq, sq, bq) || !make_map_3d(&mK, K, dk, sk, bk) ||
+      !make_map_3d(&mV, V, dk, sk, bk))
+    return cudaErrorInvalidValue;
+  PromptTcArgs a;
+  a.V = reinterpret_cast<const __nv_bfloat16*>(V);
+  a.O = reinterpret_cast<__nv_bfloat16*>(O);
+  a.Hq = d.n_q_heads;
+  a.Hkv = d.n_kv_heads;
+  a.g = g;
+  a.rtile = 128 / g;
+  a.n_units = p.n_tiles * d.n_kv_heads;
+  a.scale_log2 = 1.4426950408889634f / std::sqrt((float)D);
+  a.err = err;
+  a.st32 = (reinterpret_cast<uintptr_t>(O) & 31u) == 0;
+  cudaError_t e =
+      set_dyn_smem_once(reinterpret_cast<const void*>(prompt_tc_kernel<D>), smem_bytes<D>());
+  if (e != cudaSuccess) return e;
+  int dev = 0, sms = 1;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return launch_pdl(prompt_tc_kernel<D>, dim3(std::min(a.n_units, sms)), dim3(kThreads),
+                    smem_bytes<D>(), s, mQ, mK, mV, a, p);
+}
+
+}  // namespace
+
+bool prompt_tc_supported(const fuse_layer_desc_t& d) {
+  return d.dtype == FUSE_BF16 && tma_encode_available();
+}
+
+cudaError_t launch_prompt_tc(const fuse_layer_desc_t& d, const PromptTable& p, int64_t n_tok,
+                             const void* Q, const void* K, const void* V, void* O, uint32_t* err,
+                             cudaStream_t s) {
+  return d.head_dim == 128 ? launch_d<128>(d, p, n_tok, Q, K, V, O, err, s)
+                           : launch_d<64>(d, p, n_tok, Q, K, V, O, err, s);
+}
+
+}  // namespace fusekv
