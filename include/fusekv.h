@@ -463,7 +463,8 @@ fuse_status_t fuse_kivi_quantize(const fuse_layer_desc_t* desc, const fuse_chunk
  * Chunk storage: FUSE_U4_ASYM, FUSE_U8_ASYM or desc->dtype.  Requirements
  * (else FUSE_ERR_INVALID_ARG): 1 <= n_new <= 8 and n_new <= Qn_r; requests
  * in row order and disjoint; chunks sorted by dst_row, not overlapping, each
- * inside one request's context.  A block id outside the pool drops its
+ * inside one request's context.  A pool of more than 2^31 - 1 token rows is
+ * FUSE_ERR_UNSUPPORTED.  A block id outside the pool drops its
  * tokens, a selected index out of range or order is ignored; both are
  * recorded as FUSE_ERR_DEVICE_BOUNDS.  Softmax statistics and sums are fp32;
  * no atomics: equal inputs give equal outputs.  The workspace (of

@@ -1,5 +1,5 @@
 // Attention of new tokens over chunk caches in their storage form: the entry
-// points, the CUDA-core kernel and the kernel that joins the items.
+// points, the CUDA-core kernel (fp32 layers) and the kernel that joins the items.
 //
 // QCFuse (section 2.1.2, Eq. 4): a chunk's keys, computed at local positions,
 // belong at R^pos K; (section 2.1.3, Eq. 6): selected positions hold
@@ -34,8 +34,6 @@ constexpr int kWarps = 4;                 // items of a CTA of the CUDA-core ker
 template <int ST> __device__ __forceinline__ void load8(const uint8_t* row, int e, float (&x)[8]) {
   if constexpr (ST == FUSE_F32) {
     Vec8<float>::load(reinterpret_cast<const float*>(row) + e, x);
-  } else if constexpr (ST == FUSE_BF16) {
-    Vec8<__nv_bfloat16>::load(reinterpret_cast<const __nv_bfloat16*>(row) + e, x);
   } else if constexpr (ST == FUSE_U8_ASYM) {
     const uint2 w = *reinterpret_cast<const uint2*>(row + e);
 #pragma unroll
@@ -56,9 +54,6 @@ __device__ __forceinline__ void load_el(const uint8_t* row, int e, float (&x)[EL
   if constexpr (ST == FUSE_F32) {
 #pragma unroll
     for (int i = 0; i < EL; ++i) x[i] = reinterpret_cast<const float*>(row)[e + i];
-  } else if constexpr (ST == FUSE_BF16) {
-#pragma unroll
-    for (int i = 0; i < EL; ++i) x[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[e + i]);
   } else if constexpr (ST == FUSE_U8_ASYM) {
 #pragma unroll
     for (int i = 0; i < EL; ++i) x[i] = (float)row[e + i];
@@ -74,7 +69,7 @@ __device__ __forceinline__ void load_el(const uint8_t* row, int e, float (&x)[EL
 
 template <int ST> constexpr bool coded() { return ST == FUSE_U8_ASYM || ST == FUSE_U4_ASYM; }
 template <int ST> constexpr int row_bytes(int d) {
-  return ST == FUSE_F32 ? 4 * d : ST == FUSE_BF16 ? 2 * d : ST == FUSE_U8_ASYM ? d : d / 2;
+  return ST == FUSE_F32 ? 4 * d : ST == FUSE_U8_ASYM ? d : d / 2;
 }
 
 // The keys of an item.
@@ -90,7 +85,7 @@ struct Keys {
 
 // One warp, one item: 32 keys at a time, a lane per key for the scores, then
 // a lane per D / 32 channels for the sums.
-template <typename T, int ST, int D>
+template <int ST, int D>
 __device__ void attend_item(const AttendArgs& a, const RopeFreqs& f, const Keys& y, bool rotate,
                             int pos, const __half* ks, const __half* kz, int r, int h, int vg,
                             int64_t slot, float (*s_q)[D], float (*s_p)[kVecs]) {
@@ -106,9 +101,9 @@ __device__ void attend_item(const AttendArgs& a, const RopeFreqs& f, const Keys&
     for (int j = lane; j < D / 2; j += 32) {
       float x0 = 0.f, x1 = 0.f;
       if (vi < n_vec) {
-        const T* q = reinterpret_cast<const T*>(a.Q) +
-                     ((int64_t)(r * a.n_new + vi / a.g) * a.n_q_heads + h * a.g + vi % a.g) * D;
-        const float q0 = (float)q[j] * a.scale, q1 = (float)q[j + D / 2] * a.scale;
+        const float* q = reinterpret_cast<const float*>(a.Q) +
+                         ((int64_t)(r * a.n_new + vi / a.g) * a.n_q_heads + h * a.g + vi % a.g) * D;
+        const float q0 = q[j] * a.scale, q1 = q[j + D / 2] * a.scale;
         float c = 1.f, s = 0.f;
         if (rotate) rope_cos_sin(pos, f.hi[j], f.mid[j], f.lo[j], c, s);
         x0 = q0 * c + q1 * s;
@@ -222,14 +217,13 @@ __device__ void attend_item(const AttendArgs& a, const RopeFreqs& f, const Keys&
   }
 }
 
-template <typename T, int ST, int D>
+template <int ST, int D>
 __global__ void __launch_bounds__(kWarps * 32)
     attend_simt_kernel(const AttendArgs a, const __grid_constant__ ChunkOwners owners,
                        const __grid_constant__ RopeFreqs f, int side_ctas, int n_side_ctas) {
   __shared__ float s_q[kWarps][kVecs][D];
   __shared__ float s_p[kWarps][32][kVecs];
   const int warp = threadIdx.x / 32;
-  constexpr int TS = sizeof(T) == 4 ? FUSE_F32 : FUSE_BF16;
   pdl_trigger();
   pdl_wait();
   const int per_seg = a.n_kv_heads * a.nvg;
@@ -243,7 +237,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     const int t0 = seg * a.sseg;
     if (seg >= a.nside || t0 >= n) return;
     Keys y;
-    constexpr int RB = row_bytes<TS>(D);
+    constexpr int RB = row_bytes<FUSE_F32>(D);
     y.k = reinterpret_cast<const uint8_t*>(a.Ks) + R.out0 * a.n_kv_heads * RB;
     y.v = reinterpret_cast<const uint8_t*>(a.Vs) + R.out0 * a.n_kv_heads * RB;
     y.vs = y.vz = nullptr;
@@ -258,7 +252,7 @@ __global__ void __launch_bounds__(kWarps * 32)
           report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_ATTEND_SEL, (uint32_t)t);
       }
     }
-    attend_item<T, TS, D>(a, f, y, false, 0, nullptr, nullptr, r, h, vg,
+    attend_item<FUSE_F32, D>(a, f, y, false, 0, nullptr, nullptr, r, h, vg,
                           a.chunk_slots + (int64_t)r * a.nside + seg, s_q[warp], s_p[warp]);
     return;
   }
@@ -283,7 +277,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   y.n_skip = R.k;
   y.skip = a.idx + R.sel0;
   y.pos0 = (int)(C.dst_row - R.row0);
-  attend_item<T, ST, D>(a, f, y, C.pos != 0, C.pos, reinterpret_cast<const __half*>(C.k_scale),
+  attend_item<ST, D>(a, f, y, C.pos != 0, C.pos, reinterpret_cast<const __half*>(C.k_scale),
                         reinterpret_cast<const __half*>(C.k_zero), r, h, vg,
                         (int64_t)(a.chunk0 + ci) * a.nsub + seg, s_q[warp], s_p[warp]);
 }
@@ -390,7 +384,7 @@ __global__ void __launch_bounds__(D * kJoin)
   reinterpret_cast<T*>(a.O)[((int64_t)(r * a.n_new + u) * a.n_q_heads + hq) * D + ch] = (T)(acc / l);
 }
 
-template <typename T, int ST, int D>
+template <int ST, int D>
 cudaError_t launch_simt_t(const AttendArgs& a, const ChunkOwners& o, const RopeFreqs& f,
                           int side_reqs, cudaStream_t s) {
   const int per_seg = a.n_kv_heads * a.nvg;
@@ -398,26 +392,26 @@ cudaError_t launch_simt_t(const AttendArgs& a, const ChunkOwners& o, const RopeF
   const int ctas = (a.nsub * per_seg + kWarps - 1) / kWarps;
   const int64_t grid = (int64_t)side * side_reqs + (int64_t)ctas * a.n_chunks;
   if (grid == 0) return cudaSuccess;
-  return launch_pdl(attend_simt_kernel<T, ST, D>, dim3((unsigned)grid), dim3(kWarps * 32), 0, s, a,
+  return launch_pdl(attend_simt_kernel<ST, D>, dim3((unsigned)grid), dim3(kWarps * 32), 0, s, a,
                     o, f, std::max(side, 1), side * side_reqs);
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_simt_d(int st, const AttendArgs& a, const ChunkOwners& o, const RopeFreqs& f,
                           int side_reqs, cudaStream_t s) {
-  constexpr int TS = sizeof(T) == 4 ? FUSE_F32 : FUSE_BF16;
-  if (st == FUSE_U4_ASYM) return launch_simt_t<T, FUSE_U4_ASYM, D>(a, o, f, side_reqs, s);
-  if (st == FUSE_U8_ASYM) return launch_simt_t<T, FUSE_U8_ASYM, D>(a, o, f, side_reqs, s);
-  return launch_simt_t<T, TS, D>(a, o, f, side_reqs, s);
+  if (st == FUSE_U4_ASYM) return launch_simt_t<FUSE_U4_ASYM, D>(a, o, f, side_reqs, s);
+  if (st == FUSE_U8_ASYM) return launch_simt_t<FUSE_U8_ASYM, D>(a, o, f, side_reqs, s);
+  return launch_simt_t<FUSE_F32, D>(a, o, f, side_reqs, s);
 }
 
 // ---- host side ---------------------------------------------------------------
 
 constexpr int64_t kItems = 152 * 16;      // warps that one wave of the GPU's 152 SMs holds
+constexpr int kMaxKeys = 1024;            // keys of an item (a bit each in 32 words)
 
 int cut(int64_t keys, int64_t items, int step) {     // keys per item, a multiple of step
   const int64_t k = (keys + items - 1) / items;
-  return (int)std::max<int64_t>(step, (k + step - 1) / step * step);
+  return (int)std::min<int64_t>(kMaxKeys, std::max<int64_t>(step, (k + step - 1) / step * step));
 }
 
 // Checks everything that needs no tensor; owner[c]: request of chunk c,
@@ -434,6 +428,9 @@ fuse_status_t plan_attend(const fuse_layer_desc_t* desc, const fuse_chunks_t* ch
   if (chunks->kv_storage != FUSE_U4_ASYM && chunks->kv_storage != FUSE_U8_ASYM &&
       chunks->kv_storage != desc->dtype)
     return FUSE_ERR_UNSUPPORTED;
+  if (chunks->kv_layout == FUSE_KV_PAGED && chunks->block_size > 0 &&
+      chunks->n_pool_blocks > INT32_MAX / chunks->block_size)
+    return FUSE_ERR_UNSUPPORTED;                       // pool rows are 32-bit numbers
   fuse_chunks_t c = *chunks;
   if (!need_device && !c.d_chunks) c.d_chunks = c.h_chunks;    // only its presence is checked
   int max_len = 0;
@@ -498,11 +495,8 @@ fuse_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? FUSE_OK : F
 cudaError_t launch_attend_simt(const fuse_layer_desc_t& d, int st, const AttendArgs& a,
                                const ChunkOwners& o, const RopeFreqs& f, int side_reqs,
                                cudaStream_t s) {
-  if (d.dtype == FUSE_BF16)
-    return d.head_dim == 128 ? launch_simt_d<__nv_bfloat16, 128>(st, a, o, f, side_reqs, s)
-                             : launch_simt_d<__nv_bfloat16, 64>(st, a, o, f, side_reqs, s);
-  return d.head_dim == 128 ? launch_simt_d<float, 128>(st, a, o, f, side_reqs, s)
-                           : launch_simt_d<float, 64>(st, a, o, f, side_reqs, s);
+  return d.head_dim == 128 ? launch_simt_d<128>(st, a, o, f, side_reqs, s)
+                           : launch_simt_d<64>(st, a, o, f, side_reqs, s);
 }
 
 cudaError_t launch_attend_combine(const fuse_layer_desc_t& d, const AttendArgs& a,
@@ -595,7 +589,8 @@ fuse_status_t fuse_attend_chunks(const fuse_layer_desc_t* desc, const fuse_chunk
     a.n_chunks = std::min(kChunkBatch, chunks->n_chunks - c0);
     std::copy(owner.begin() + c0, owner.begin() + c0 + a.n_chunks, owners.req);
     st = cuda_status(traced("attend_chunks", s, [&] {
-      return launch_attend_simt(*desc, chunks->kv_storage, a, owners, f, c0 == 0 ? a.n_req : 0, s);
+      const auto launch = desc->dtype == FUSE_BF16 ? launch_attend_mma : launch_attend_simt;
+      return launch(*desc, chunks->kv_storage, a, owners, f, c0 == 0 ? a.n_req : 0, s);
     }));
     if (st != FUSE_OK) return st;
   }

@@ -55,10 +55,14 @@ struct RequestChunks {
 };
 
 // The items' kernels; side rows of all requests of the launch come with the
-// first batch of chunks (side_reqs requests from side0, 0: none).
+// first batch of chunks (side_reqs requests, 0: none).  fp32 layers.
 cudaError_t launch_attend_simt(const fuse_layer_desc_t& d, int kv_storage, const AttendArgs& a,
                                const ChunkOwners& owners, const RopeFreqs& freqs, int side_reqs,
                                cudaStream_t s);
+// The same for bf16 layers, on matrix instructions (attend_chunks_mma.cu).
+cudaError_t launch_attend_mma(const fuse_layer_desc_t& d, int kv_storage, const AttendArgs& a,
+                              const ChunkOwners& owners, const RopeFreqs& freqs, int side_reqs,
+                              cudaStream_t s);
 cudaError_t launch_attend_combine(const fuse_layer_desc_t& d, const AttendArgs& a,
                                   const RequestChunks& rc, cudaStream_t s);
 
