@@ -224,8 +224,8 @@ __global__ void __launch_bounds__(kWarps * 32)
   __shared__ float s_q[kWarps][kVecs][D];
   __shared__ float s_p[kWarps][32][kVecs];
   const int warp = threadIdx.x / 32;
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();                           // the join may read the call's inputs before it waits
   const int per_seg = a.n_kv_heads * a.nvg;
   if ((int)blockIdx.x < n_side_ctas) {
     // side rows: those before the new tokens
@@ -263,7 +263,13 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int seg = i / per_seg, h = i % per_seg / a.nvg, vg = i % a.nvg;
   const fuse_chunk_t C = a.chunks[a.chunk0 + ci];
   const int t0 = seg * a.seg;
-  if (seg >= a.nsub || t0 >= C.len) return;
+  if (seg >= a.nsub) return;
+  if (t0 >= C.len) {                       // past the chunk's end: an item without a key
+    if (threadIdx.x % 32 < kVecs)
+      a.part_ml[(((int64_t)(a.chunk0 + ci) * a.nsub + seg) * per_seg + i % per_seg) * kVecs +
+                threadIdx.x % 32] = make_float2(-INFINITY, 0.f);
+    return;
+  }
   const int r = owners.req[ci];
   const fuse_request_t R = a.reqs[r];
   Keys y;
@@ -284,104 +290,133 @@ __global__ void __launch_bounds__(kWarps * 32)
 
 // Joins the items of one query vector (blockIdx.x = new token * Hq + head)
 // of one request with the new tokens' own keys, and writes its output row.
-// Threads: D channels x kJoin slices of the items.
-constexpr int kJoin = 4;
+// An item's row is read by D / 4 lanes, four items a lane in flight; the
+// weights of up to kJoinTile items are formed first.  Latency bounds it (two
+// dependent reads), so what does not depend on the items (the table entry,
+// the own keys) is read before they are waited for.
+constexpr int kJoinThreads = 512;
 constexpr int kJoinTile = 512;            // items whose weights are held at a time
 
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+__device__ __forceinline__ void add4(float4& a, float w, const float4& x) {
+  a.x = fmaf(w, x.x, a.x);
+  a.y = fmaf(w, x.y, a.y);
+  a.z = fmaf(w, x.z, a.z);
+  a.w = fmaf(w, x.w, a.w);
+}
+
 template <typename T, int D>
-__global__ void __launch_bounds__(D * kJoin)
-    attend_combine_kernel(const AttendArgs a, const __grid_constant__ RequestChunks rc) {
+__global__ void __launch_bounds__(kJoinThreads)
+    attend_combine_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ RequestChunks rc) {
+  constexpr int kWarpsJ = kJoinThreads / 32, L = D / 4, kSub = 32 / L;   // lanes, items of a warp step
   __shared__ float s_w[kJoinTile];
   __shared__ float s_own[FUSE_ATTEND_MAX_NEW];
-  __shared__ float s_red[32];
-  __shared__ float s_o[kJoin][D];
+  __shared__ float s_red[2][kWarpsJ];
+  __shared__ float4 s_o[kWarpsJ * kSub][L];
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  constexpr int kThreads = D * kJoin;
   const int r = a.req0 + blockIdx.y;
   const int u = blockIdx.x / a.n_q_heads, hq = blockIdx.x % a.n_q_heads;
   const int h = hq / a.g;
   const int vi = u * a.g + hq % a.g;      // vector of its KV head
   const fuse_request_t R = a.reqs[r];
-  const int c0 = rc.first[blockIdx.y];
-  const int n_seg = (rc.first[blockIdx.y + 1] - c0) * a.nsub;
+  const int64_t c0 = rc.first[blockIdx.y];
+  const int n_seg = (int)(rc.first[blockIdx.y + 1] - c0) * a.nsub;
   const int n_side = R.k + R.n_query - a.n_new;           // side rows in items
   const int n = n_seg + (n_side + a.sseg - 1) / a.sseg;
-  pdl_wait();
-  // item e's slot, or -1 for a segment past its chunk's end
-  auto slot_of = [&](int e) -> int64_t {
-    if (e >= n_seg) return a.chunk_slots + (int64_t)r * a.nside + (e - n_seg);
-    const int c = c0 + e / a.nsub, sub = e % a.nsub;
-    return sub * a.seg < a.chunks[c].len ? (int64_t)c * a.nsub + sub : -1;
-  };
-  auto part = [&](int64_t slot) { return ((slot * a.n_kv_heads + h) * a.nvg + vi / kVecs) * kVecs + vi % kVecs; };
-  // own keys: warp w takes new token w
+  // own keys: warp j takes new token j
   const T* Ks = reinterpret_cast<const T*>(a.Ks);
   const T* Vs = reinterpret_cast<const T*>(a.Vs);
-  const T* q = reinterpret_cast<const T*>(a.Q) + ((int64_t)(r * a.n_new + u) * a.n_q_heads + hq) * D;
-  const int64_t own0 = R.out0 + n_side;
-  for (int j = warp; j <= u; j += kThreads / 32) {
+  const int64_t qrow = ((int64_t)(r * a.n_new + u) * a.n_q_heads + hq) * D;
+  const int64_t own = ((R.out0 + n_side) * a.n_kv_heads + h) * D, own_step = (int64_t)a.n_kv_heads * D;
+  float4 v_own = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (warp <= u) {
     float s = 0.f;
-    for (int e = lane; e < D; e += 32)
-      s = fmaf((float)q[e], (float)Ks[((own0 + j) * a.n_kv_heads + h) * D + e], s);
+    if (lane < L) {
+      const float4 q = load4(reinterpret_cast<const T*>(a.Q) + qrow + lane * 4);
+      const float4 k = load4(Ks + own + warp * own_step + lane * 4);
+      v_own = load4(Vs + own + warp * own_step + lane * 4);
+      s = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, q.w * k.w)));
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) s_own[j] = s * a.scale;
+    if (lane == 0) s_own[warp] = s * a.scale;
   }
-  // the largest maximum
-  float M = -INFINITY;
-  for (int e = tid; e < n; e += kThreads) {
-    const int64_t sl = slot_of(e);
-    if (sl >= 0) M = fmaxf(M, a.part_ml[part(sl)].x);
-  }
+  pdl_wait();
+  // item e's vector: chunk segments, then side segments
+  const int64_t step = (int64_t)a.n_kv_heads * a.nvg * kVecs;
+  const int64_t mine = ((int64_t)h * a.nvg + vi / kVecs) * kVecs + vi % kVecs;
+  const int64_t at_seg = c0 * a.nsub * step + mine;
+  const int64_t at_side = (a.chunk_slots + (int64_t)r * a.nside - n_seg) * step + mine;
+  auto part = [&](int e) { return (e < n_seg ? at_seg : at_side) + e * step; };
+  const int sub = lane / L, ch = lane % L * 4;
+  float M = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int e0 = 0; e0 == 0 || e0 < n; e0 += kJoinTile) {
+    const int cnt = min(kJoinTile, n - e0);
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (tid < cnt) ml = a.part_ml[part(e0 + tid)];
+    float t = ml.x;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) s_red[warp] = M;
-  __syncthreads();
-  M = s_red[0];
-  for (int w = 1; w < kThreads / 32; ++w) M = fmaxf(M, s_red[w]);
-  for (int j = 0; j <= u; ++j) M = fmaxf(M, s_own[j]);
-  const float ref = M == -INFINITY ? 0.f : M;
-  const int ch = tid % D, slice = tid / D;
-  float acc = 0.f, l = 0.f;
-  for (int e0 = 0; e0 < n; e0 += kJoinTile) {
-    const int m = min(kJoinTile, n - e0);
+    for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+    __syncthreads();                      // s_own written; the last tile's weights are used
+    if (lane == 0) s_red[0][warp] = t;
     __syncthreads();
-    for (int e = tid; e < m; e += kThreads) {
-      const int64_t sl = slot_of(e0 + e);
-      float w = -1.f;                     // no such item
-      if (sl >= 0) {
-        const float2 ml = a.part_ml[part(sl)];
-        w = exp2f(ml.x - ref);
-        l = fmaf(w, ml.y, l);
+    float mn = M;
+    for (int w = 0; w < kWarpsJ; ++w) mn = fmaxf(mn, s_red[0][w]);
+    if (e0 == 0)
+      for (int j = 0; j <= u; ++j) mn = fmaxf(mn, s_own[j]);
+    const float ref = mn == -INFINITY ? 0.f : mn;
+    const float al = exp2f(M - ref);      // 0 in the first tile
+    M = mn;
+    const float w = exp2f(ml.x - ref);
+    l = l * al + w * ml.y;
+    // an item without a key is not read: it may have written nothing
+    s_w[tid] = tid < cnt && !(ml.x == -INFINITY && ml.y == 0.f) ? w : -1.f;
+    acc.x *= al;
+    acc.y *= al;
+    acc.z *= al;
+    acc.w *= al;
+    __syncthreads();
+    for (int e = warp * kSub + sub; e < cnt; e += 4 * kWarpsJ * kSub) {
+      float4 x[4];
+      float we[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int ei = e + i * kWarpsJ * kSub;
+        we[i] = ei < cnt ? s_w[ei] : -1.f;
+        if (we[i] != -1.f) x[i] = *reinterpret_cast<const float4*>(a.part_o + part(e0 + ei) * D + ch);
       }
-      s_w[e] = w;
-    }
-    __syncthreads();
-#pragma unroll 4
-    for (int e = slice; e < m; e += kJoin) {
-      const float w = s_w[e];
-      // an item without keys (weight 0) holds zeros
-      if (w != -1.f) acc = fmaf(w, a.part_o[part(slot_of(e0 + e)) * D + ch], acc);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (we[i] != -1.f) add4(acc, we[i], x[i]);
     }
   }
-  s_o[slice][ch] = acc;
-  // the sum of the items' sums
-  __syncthreads();
+  if (warp <= u && lane < L) {
+    const float p = exp2f(s_own[warp] - (M == -INFINITY ? 0.f : M));
+    if (lane == 0) l += p;
+    add4(acc, p, v_own);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  if (lane == 0) s_red[warp] = l;
+  if (lane == 0) s_red[1][warp] = l;
+  s_o[warp * kSub + sub][lane % L] = acc;
   __syncthreads();
-  if (slice > 0) return;
+  if (tid >= L) return;
   l = 0.f;
-  for (int w = 0; w < kThreads / 32; ++w) l += s_red[w];
-  acc = ((s_o[0][ch] + s_o[1][ch]) + s_o[2][ch]) + s_o[3][ch];
-  for (int j = 0; j <= u; ++j) {
-    const float p = exp2f(s_own[j] - ref);
-    l += p;
-    acc = fmaf(p, (float)Vs[((own0 + j) * a.n_kv_heads + h) * D + ch], acc);
-  }
-  reinterpret_cast<T*>(a.O)[((int64_t)(r * a.n_new + u) * a.n_q_heads + hq) * D + ch] = (T)(acc / l);
+  for (int w = 0; w < kWarpsJ; ++w) l += s_red[1][w];
+  acc = s_o[0][tid];
+  for (int w = 1; w < kWarpsJ * kSub; ++w) add4(acc, 1.f, s_o[w][tid]);
+  store4(reinterpret_cast<T*>(a.O) + qrow + tid * 4,
+         make_float4(acc.x / l, acc.y / l, acc.z / l, acc.w / l));
 }
 
 template <int ST, int D>
@@ -406,7 +441,7 @@ cudaError_t launch_simt_d(int st, const AttendArgs& a, const ChunkOwners& o, con
 
 // ---- host side ---------------------------------------------------------------
 
-constexpr int64_t kItems = 152 * 16;      // warps that one wave of the GPU's 152 SMs holds
+constexpr int64_t kItems = 152 * 12;      // three quarters of the warps that 152 SMs hold
 constexpr int kMaxKeys = 1024;            // keys of an item (a bit each in 32 words)
 
 int cut(int64_t keys, int64_t items, int step) {     // keys per item, a multiple of step
@@ -467,10 +502,10 @@ fuse_status_t plan_attend(const fuse_layer_desc_t* desc, const fuse_chunks_t* ch
   const int g = desc->n_q_heads / desc->n_kv_heads;
   P->nvg = (g * n_new + kVecs - 1) / kVecs;
   const int64_t per = (int64_t)desc->n_kv_heads * P->nvg;
-  int seg = cut(n_ctx * per, kItems, 32);
+  const int seg = cut(n_ctx * per, kItems, 64);
   P->nsub = std::max(1, (max_len + seg - 1) / seg);
   P->seg = cut(std::max(max_len, 1), P->nsub, 32);
-  int sseg = cut(n_side * per, kItems, 32);
+  const int sseg = cut(n_side * per, kItems, 32);
   P->nside = (int)((max_side + sseg - 1) / sseg);
   P->sseg = sseg;
   P->chunk_slots = (int64_t)chunks->n_chunks * P->nsub;
@@ -503,7 +538,7 @@ cudaError_t launch_attend_combine(const fuse_layer_desc_t& d, const AttendArgs& 
                                   const RequestChunks& rc, cudaStream_t s) {
   const dim3 grid(a.n_new * a.n_q_heads, a.n_req);
   auto go = [&](auto kernel) {
-    return launch_pdl(kernel, grid, dim3(d.head_dim * kJoin), 0, s, a, rc);
+    return launch_pdl(kernel, grid, dim3(kJoinThreads), 0, s, a, rc);
   };
   if (d.dtype == FUSE_BF16)
     return d.head_dim == 128 ? go(attend_combine_kernel<__nv_bfloat16, 128>)

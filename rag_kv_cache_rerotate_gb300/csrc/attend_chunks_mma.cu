@@ -16,7 +16,7 @@
 // slots of 32 (4 bits), 16 (8 bits) or 8 (bf16): 4 KB at d = 128, three slots
 // of shared memory per warp filled by 16-byte cp.async two ahead.  The warps
 // of a CTA take neighbouring KV heads of the same tokens, so together they
-// read whole rows.  Nothing is shared between warps: no barrier.
+// read whole rows.  Warps share only the chunk's angles.
 //   S^T = Q K^T   A = Q (rows 0-7: the vectors' high parts, 8-15: what is
 //                 left of them, 22 bits together), B = codes of 8 keys, the
 //                 channels in whatever order the lanes hold them
@@ -74,6 +74,33 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Packed pairs of floats: one instruction does the operation on both halves.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
                : "memory");
@@ -87,20 +114,20 @@ template <bool F16>
 __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                       uint32_t a3, uint32_t b0, uint32_t b1) {
   if constexpr (F16)
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
         " {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
         " {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma8_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6},"
       " {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -156,9 +183,9 @@ __device__ __forceinline__ int warp_lower_bound(const int32_t* a, int n, int x) 
 }
 
 template <int ST, int D>
-__device__ __forceinline__ void attend_mma_item(const AttendArgs& a, const RopeFreqs& f, const Item& y,
-                                                bool rotate, int pos, const __half* ks,
-                                                const __half* kz, WarpSmem<D>& sm) {
+__device__ __forceinline__ void attend_mma_item(const AttendArgs& a, const Item& y, const float2* cs,
+                                                const __half* ks, const __half* kz,
+                                                WarpSmem<D>& sm) {
   using F = Fmt<ST, D>;
   constexpr int RB = F::RB, RC = F::RC, TOK = F::TOK, NT = F::NT, KSTEP = F::KSTEP, MT = F::MT;
   constexpr uint32_t kAll = 0xffffffffu;
@@ -183,34 +210,63 @@ __device__ __forceinline__ void attend_mma_item(const AttendArgs& a, const RopeF
   };
 
   // ---- rows of a slot's keys, one per lane ----------------------------------
-  int id = 0, rem = 0;                                 // page and row in it of the slot loaded next
-  auto load_id = [&](int s) {
-    const int t = y.t0 + s * TOK + lane;
-    id = -1;
-    if (lane < TOK && t < y.t1) {
-      if (y.table) {
-        const int b = t / a.block_size;
-        rem = t - b * a.block_size;
-        id = y.table[b];
-        if (id < 0 || id >= a.n_pool_blocks) {
-          report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_ATTEND_BLOCK, (uint32_t)id);
-          id = -1;
-        }
+  // The page id of the slot loaded next is read one slot ahead and looked at
+  // only when it is used, so that its read is not waited for.
+  int blk = 0, rem = y.t0 + lane, id = 0, t_next = y.t0 + lane;   // this lane's key of that slot
+  const int dq = y.table ? TOK / a.block_size : 0, dr = TOK - dq * a.block_size;
+  const int bs = y.table ? a.block_size : INT32_MAX;
+  if (y.table) {
+    blk = rem / bs;
+    rem -= blk * bs;
+  }
+  auto load_id = [&]() {
+    if (y.table && lane < TOK && t_next < y.t1) id = y.table[blk];
+  };
+  auto next_row = [&]() {                              // its row, -1: none; then the next slot's id
+    const bool in = lane < TOK && t_next < y.t1;
+    int row = in ? rem : -1;
+    if (y.table && in) {
+      if (id >= 0 && id < a.n_pool_blocks) {
+        row = id * bs + rem;
       } else {
-        id = 0;
-        rem = t;
+        report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_ATTEND_BLOCK, (uint32_t)id);
+        row = -1;
       }
     }
+    t_next += TOK;
+    blk += dq;
+    rem += dr;
+    if (rem >= bs) {
+      rem -= bs;
+      ++blk;
+    }
+    load_id();
+    return row;
   };
   // slot s into its buffer; returns the row of this lane's key, -1: none
   auto issue = [&](int s) {
-    int row = id < 0 ? -1 : id * a.block_size + rem;
+    int row = next_row();
     if constexpr (!F::coded)                           // what is not seen may hold anything
       if (row >= 0 && (sm.skip[(s * TOK + lane) >> 5] >> ((s * TOK + lane) & 31) & 1)) row = -1;
     const uint32_t ok = __ballot_sync(kAll, row >= 0);
     uint8_t* buf = sm.slot[s % kSlots];
     if (lane == 0) sm.keep[s % kSlots] = ok;
     const uint32_t dk = (uint32_t)__cvta_generic_to_shared(buf), dv = dk + TOK * RB;
+    const bool whole = ok == (uint32_t)((1ull << TOK) - 1);
+    if (!y.table && whole) {               // warp-uniform: TOK consecutive rows
+      const int64_t off = (int64_t)(y.t0 + s * TOK + lane / RC) * stride + lane % RC * 16;
+      const uint8_t *pk = y.k + off, *pv = y.v + off;
+#pragma unroll
+      for (int i = 0; i < TOK * RC / 32; ++i) {
+        const int key = (i * 32 + lane) / RC, c = (i * 32 + lane) % RC;
+        const int vr = v_row(key);
+        cp16(dk + key * RB + k_chunk<RC>(key, c) * 16, pk, true);
+        cp16(dv + vr * RB + v_chunk<RC>(vr, c) * 16, pv, true);
+        pk += (32 / RC) * stride;
+        pv += (32 / RC) * stride;
+      }
+      return row;
+    }
 #pragma unroll
     for (int i = 0; i < TOK * RC / 32; ++i) {
       const int key = (i * 32 + lane) / RC, c = (i * 32 + lane) % RC;
@@ -222,65 +278,88 @@ __device__ __forceinline__ void attend_mma_item(const AttendArgs& a, const RopeF
     }
     return row;
   };
-  auto load_sz = [&](int row) -> uint32_t {
-    if (!F::coded || row < 0) return 0u;
-    const int64_t at = (int64_t)row * a.n_kv_heads;
-    return (uint32_t)__half_as_ushort(y.vs[at]) | ((uint32_t)__half_as_ushort(y.vz[at]) << 16);
+  // scale and zero of a slot's values: read two slots ahead, looked at when used
+  auto load_sz = [&](int row, uint16_t& vs, uint16_t& vz) {
+    vs = vz = 0;
+    if (F::coded && row >= 0) {
+      const int64_t at = (int64_t)row * a.n_kv_heads;
+      vs = reinterpret_cast<const uint16_t*>(y.vs)[at];
+      vz = reinterpret_cast<const uint16_t*>(y.vz)[at];
+    }
   };
 
   if constexpr (!F::coded) mark_selected();
-  load_id(0);
-  const int row0 = issue(0);
+  load_id();
+  uint16_t sz0[2], sz1[2];                             // even and odd slots
+  load_sz(issue(0), sz0[0], sz0[1]);
   cp_commit();
-  load_id(1);
-  int row1 = issue(1);
+  load_sz(issue(1), sz1[0], sz1[1]);
   cp_commit();
-  load_id(2);
-  uint32_t sz_next = load_sz(row0);
 
   // ---- the query vectors, turned back and scaled, as A operands --------------
   uint32_t qa[KSTEP][4];
   float sscale, cst;                                   // score = sum * sscale + cst (vector gid)
   {
-    constexpr int NP = D / 64;                         // channel pairs of a lane
-    const int n_vec = a.g * a.n_new;
-    float x0[kVecs][NP], x1[kVecs][NP], cc[NP], ss[NP], k0[NP], k1[NP], z0[NP], z1[NP];
+    // a lane's channel pairs (j, j + D / 2): j = NP lane .. NP lane + NP - 1
+    constexpr int NP = D / 64;
+    const int n_vec = a.g * a.n_new, j0 = NP * lane;
+    auto load_pair = [](const __nv_bfloat16* p, float (&x)[NP]) {
+      if constexpr (NP == 2) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+        x[0] = bf16_lo(w);
+        x[1] = bf16_hi(w);
+      } else {
+        x[0] = __bfloat162float(*p);
+      }
+    };
+    auto load_half = [](const __half* p, float (&x)[NP]) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) x[i] = __half2float(p[i]);
+    };
+    float x0[kVecs][NP], x1[kVecs][NP], k0[NP], k1[NP], z0[NP], z1[NP];
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
       const int vi = y.vg * kVecs + v;
-      const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.Q) +
-                               ((int64_t)(y.r * a.n_new + vi / a.g) * a.n_q_heads + y.h * a.g + vi % a.g) * D;
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        x0[v][i] = vi < n_vec ? __bfloat162float(q[lane + 32 * i]) : 0.f;
-        x1[v][i] = vi < n_vec ? __bfloat162float(q[lane + 32 * i + D / 2]) : 0.f;
+      for (int i = 0; i < NP; ++i) x0[v][i] = x1[v][i] = 0.f;
+      if (vi < n_vec) {                                // warp-uniform
+        const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.Q) +
+                                 ((int64_t)(y.r * a.n_new + vi / a.g) * a.n_q_heads + y.h * a.g + vi % a.g) * D;
+        load_pair(q + j0, x0[v]);
+        load_pair(q + j0 + D / 2, x1[v]);
       }
     }
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const int j = lane + 32 * i;
-      cc[i] = 1.f;
-      ss[i] = 0.f;
-      if (rotate) rope_cos_sin(pos, f.hi[j], f.mid[j], f.lo[j], cc[i], ss[i]);
-      if constexpr (F::coded) {
-        k0[i] = __half2float(ks[y.h * D + j]);
-        k1[i] = __half2float(ks[y.h * D + j + D / 2]);
-        z0[i] = __half2float(kz[y.h * D + j]);
-        z1[i] = __half2float(kz[y.h * D + j + D / 2]);
-      }
+    if constexpr (F::coded) {
+      load_half(ks + y.h * D + j0, k0);
+      load_half(ks + y.h * D + j0 + D / 2, k1);
+      load_half(kz + y.h * D + j0, z0);
+      load_half(kz + y.h * D + j0 + D / 2, z1);
+      mark_selected();                                 // its reads run beside those above
     }
     uint32_t* sq = reinterpret_cast<uint32_t*>(sm.slot[2]);   // not in flight yet
     sscale = 1.f;
     cst = 0.f;
+    float z[kVecs];
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
-      float z = 0.f, mx = 0.f;
+      z[v] = 0.f;
+      if (y.vg * kVecs + v >= n_vec) {                 // warp-uniform: no such vector
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) sq[q_word<D>(v, lane + 32 * i)] = 0;
+        continue;
+      }
+      float mx = 0.f;
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         const float q0 = x0[v][i] * a.scale, q1 = x1[v][i] * a.scale;
-        float r0 = q0 * cc[i] + q1 * ss[i], r1 = q1 * cc[i] - q0 * ss[i];
+        float r0 = q0, r1 = q1;
+        if (cs) {
+          const float2 t = cs[j0 + i];
+          r0 = q0 * t.x + q1 * t.y;
+          r1 = q1 * t.x - q0 * t.y;
+        }
         if constexpr (F::coded) {
-          z += r0 * z0[i] + r1 * z1[i];
+          z[v] += r0 * z0[i] + r1 * z1[i];
           r0 *= k0[i];
           r1 *= k1[i];
           mx = fmaxf(mx, fmaxf(fabsf(r0), fabsf(r1)));
@@ -290,22 +369,17 @@ __device__ __forceinline__ void attend_mma_item(const AttendArgs& a, const RopeF
       }
       float up = 1.f;
       if constexpr (F::coded) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kAll, z, o);
         // fp16 parts want the largest element near 2^12: a power of two apart
         const uint32_t mb = __reduce_max_sync(kAll, __float_as_uint(mx));
         const int e = min(max((int)(mb >> 23), 27), 230);
         up = __uint_as_float((uint32_t)(266 - e) << 23);
-        if (v == gid) {
-          sscale = 16777216.f * __uint_as_float((uint32_t)(e - 12) << 23);   // 2^24 / up
-          cst = z;
-        }
+        if (v == gid) sscale = 16777216.f * __uint_as_float((uint32_t)(e - 12) << 23);   // 2^24 / up
       }
 #pragma unroll
       for (int i = 0; i < NP; ++i)
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          const int ch = lane + 32 * i + b * (D / 2);
+          const int ch = j0 + i + b * (D / 2);
           float x = (b ? x1[v][i] : x0[v][i]) * up;
           uint32_t w;
           if constexpr (F::coded) {
@@ -319,6 +393,22 @@ __device__ __forceinline__ void attend_mma_item(const AttendArgs& a, const RopeF
           sq[q_word<D>(v, ch)] = w;
         }
     }
+    if constexpr (F::coded) {
+      // the eight sums over the lanes, halving the vectors a lane carries:
+      // vector gid ends up in its four lanes
+#pragma unroll
+      for (int n = 4; n > 0; n >>= 1) {
+        const bool upper = lane & (4 * n);
+#pragma unroll
+        for (int v = 0; v < n; ++v) {
+          const float give = upper ? z[v] : z[v + n];
+          z[v] = (upper ? z[v + n] : z[v]) + __shfl_xor_sync(kAll, give, 4 * n);
+        }
+      }
+      cst = z[0];
+      cst += __shfl_xor_sync(kAll, cst, 1);
+      cst += __shfl_xor_sync(kAll, cst, 2);
+    }
     __syncwarp();
 #pragma unroll
     for (int kk = 0; kk < KSTEP; ++kk)
@@ -330,10 +420,10 @@ __device__ __forceinline__ void attend_mma_item(const AttendArgs& a, const RopeF
         qa[kk][2 * b + 1] = __byte_perm(w0, w1, 0x7632);      // row gid + 8: what is left
       }
   }
-  if constexpr (F::coded) mark_selected();
 
   // ---- the keys ------------------------------------------------------------
-  float m = -INFINITY, l = 0.f, zs = 0.f;              // vector gid (this lane's keys)
+  float m = -INFINITY;                                 // vector gid
+  uint64_t l2 = 0, z2 = 0;                             // its sums (this lane's even, odd keys)
   int ve = 0;                                          // exponent field of the largest value scale
   float acc[MT][4];
 #pragma unroll
@@ -341,16 +431,12 @@ __device__ __forceinline__ void attend_mma_item(const AttendArgs& a, const RopeF
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
 
-#pragma unroll 1
-  for (int s = 0; s < n_slots; ++s) {
+  auto step = [&](int s, uint16_t (&szr)[2]) {
     cp_wait<1>();                                      // slot s has landed
     __syncwarp();                                      // ... for every lane; slot s - 1 is done with
-    const uint32_t sz = sz_next;
-    const int row2 = issue(s + 2);
+    const uint32_t sz = (uint32_t)szr[0] | (uint32_t)szr[1] << 16;
+    load_sz(issue(s + 2), szr[0], szr[1]);
     cp_commit();
-    load_id(s + 3);
-    sz_next = load_sz(row1);
-    row1 = row2;
     const uint8_t* kb = sm.slot[s % kSlots];
     const uint8_t* vb = kb + TOK * RB;
     const int bit0 = s * TOK;
@@ -358,7 +444,7 @@ __device__ __forceinline__ void attend_mma_item(const AttendArgs& a, const RopeF
     bool raise = false;
     float fe = 1.f;                                    // factor of a raised normaliser
     if constexpr (F::coded) {
-      sm.sz[lane] = sz;
+      sm.sz[lane] = keep >> lane & 1 ? sz : 0u;        // whatever a key not seen holds
       const uint32_t top = __reduce_max_sync(kAll, (keep >> lane & 1) ? sz & 0x7fffu : 0u);
       const int e = min((int)(top >> 10), 30);
       if (e > ve) {                                    // warp-uniform
@@ -369,74 +455,104 @@ __device__ __forceinline__ void attend_mma_item(const AttendArgs& a, const RopeF
       __syncwarp();
     }
     // scores: S^T rows gid (+ 8: low parts), keys 2 tig, 2 tig + 1 of each 8
-    float sc[NT][2];
+    uint64_t sc[NT];                                   // before sscale and cst
+    // eight keys at a time form a chain of D / 16 dependent products; two such
+    // groups, each in two chains, run side by side
+    constexpr int NP2 = NT < 2 ? NT : 2;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float c[4] = {0.f, 0.f, 0.f, 0.f};
-      const int key = nt * 8 + gid;
-      const uint8_t* kr = kb + key * RB;
+    for (int nt0 = 0; nt0 < NT; nt0 += NP2) {
+      float c[NP2][2][4];
+#pragma unroll
+      for (int p = 0; p < NP2; ++p)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) c[p][e >> 2][e & 3] = 0.f;
       if constexpr (ST == FUSE_U4_ASYM) {
-        uint32_t w[D / 32];
-        if constexpr (D == 128) {
-          const uint4 x = *reinterpret_cast<const uint4*>(kr + tig * 16);
-          w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(kr + tig * 8);
-          w[0] = x.x; w[1] = x.y;
+        uint32_t w[NP2][D / 32];
+#pragma unroll
+        for (int p = 0; p < NP2; ++p) {
+          const uint8_t* kr = kb + ((nt0 + p) * 8 + gid) * RB;
+          if constexpr (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(kr + tig * 16);
+            w[p][0] = x.x; w[p][1] = x.y; w[p][2] = x.z; w[p][3] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(kr + tig * 8);
+            w[p][0] = x.x; w[p][1] = x.y;
+          }
         }
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-          const uint32_t u = w[j], t = w[j] >> 8;
-          mma16<true>(c, qa[2 * j][0], qa[2 * j][1], qa[2 * j][2], qa[2 * j][3], u & 0x000f000fu,
-                      u & 0x00f000f0u);
-          mma16<true>(c, qa[2 * j + 1][0], qa[2 * j + 1][1], qa[2 * j + 1][2], qa[2 * j + 1][3],
-                      t & 0x000f000fu, t & 0x00f000f0u);
-        }
+        for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int p = 0; p < NP2; ++p) {
+              const uint32_t u = b ? w[p][j] >> 8 : w[p][j];
+              mma16<true>(c[p][b], qa[2 * j + b][0], qa[2 * j + b][1], qa[2 * j + b][2],
+                          qa[2 * j + b][3], u & 0x000f000fu, u & 0x00f000f0u);
+            }
       } else {
         constexpr int CH = RC / 4;                     // 16-byte chunks of a lane
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-          const uint4 x = *reinterpret_cast<const uint4*>(kr + k_chunk<RC>(key, i * 4 + tig) * 16);
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          uint32_t w[NP2][4];
+#pragma unroll
+          for (int p = 0; p < NP2; ++p) {
+            const int key = (nt0 + p) * 8 + gid;
+            const uint4 x = *reinterpret_cast<const uint4*>(kb + key * RB + k_chunk<RC>(key, i * 4 + tig) * 16);
+            w[p][0] = x.x; w[p][1] = x.y; w[p][2] = x.z; w[p][3] = x.w;
+          }
           if constexpr (ST == FUSE_U8_ASYM) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int kk = i * 4 + j;
-              mma16<true>(c, qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], __byte_perm(w[j], 0, 0x4140),
-                          __byte_perm(w[j], 0, 0x4342));
-            }
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int p = 0; p < NP2; ++p) {
+                const int kk = i * 4 + j;
+                mma16<true>(c[p][j & 1], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3],
+                            __byte_perm(w[p][j], 0, 0x4140), __byte_perm(w[p][j], 0, 0x4342));
+              }
           } else {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int kk = i * 2 + j;
-              mma16<false>(c, qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], w[2 * j], w[2 * j + 1]);
-            }
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int p = 0; p < NP2; ++p) {
+                const int kk = i * 2 + j;
+                mma16<false>(c[p][j], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], w[p][2 * j],
+                             w[p][2 * j + 1]);
+              }
           }
         }
       }
-      sc[nt][0] = fmaf(c[0] + c[2], sscale, cst);
-      sc[nt][1] = fmaf(c[1] + c[3], sscale, cst);
+#pragma unroll
+      for (int p = 0; p < NP2; ++p)
+        sc[nt0 + p] = add2(add2(pack2(c[p][0][0], c[p][0][1]), pack2(c[p][1][0], c[p][1][1])),
+                           add2(pack2(c[p][0][2], c[p][0][3]), pack2(c[p][1][2], c[p][1][3])));
     }
     const uint32_t mine = keep >> (2 * tig);           // bits 8 nt, 8 nt + 1: this lane's keys
     if (keep != (uint32_t)((1ull << TOK) - 1)) {       // warp-uniform
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (!(mine >> (8 * nt + e) & 1)) sc[nt][e] = -INFINITY;
+      for (int nt = 0; nt < NT; ++nt) {
+        float2 x = unpack2(sc[nt]);
+        if (!(mine >> (8 * nt) & 1)) x.x = -INFINITY;
+        if (!(mine >> (8 * nt + 1) & 1)) x.y = -INFINITY;
+        sc[nt] = pack2(x.x, x.y);
+      }
     }
     float mt = -INFINITY;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) mt = fmaxf(mt, fmaxf(sc[nt][0], sc[nt][1]));
+    for (int nt = 0; nt < NT; ++nt) {
+      const float2 x = unpack2(sc[nt]);
+      mt = fmaxf(mt, fmaxf(x.x, x.y));
+    }
     mt = fmaxf(mt, __shfl_xor_sync(kAll, mt, 1));
     mt = fmaxf(mt, __shfl_xor_sync(kAll, mt, 2));
+    if constexpr (F::coded) mt = mt == -INFINITY ? mt : fmaf(mt, sscale, cst);
     const bool up = mt > m + kRaise;
     if (__any_sync(kAll, up) || raise) {
-      const float al = up ? ex2(m - mt) : 1.f;         // 0 at the first key
+      const float al = (up ? ex2(m - mt) : 1.f) * fe;  // 0 at the first key
       if (up) m = mt;
-      l *= al;
-      zs *= al;
-      const float f0 = __shfl_sync(kAll, al, tig * 8) * fe, f1 = __shfl_sync(kAll, al, tig * 8 + 4) * fe;
+      const uint64_t al2 = pack2(al, al);
+      l2 = mul2(l2, al2);
+      z2 = mul2(z2, al2);
+      const float f0 = __shfl_sync(kAll, al, tig * 8), f1 = __shfl_sync(kAll, al, tig * 8 + 4);
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         acc[i][0] *= f0;
@@ -445,25 +561,27 @@ __device__ __forceinline__ void attend_mma_item(const AttendArgs& a, const RopeF
         acc[i][3] *= f1;
       }
     }
-    const float ref = m == -INFINITY ? 0.f : m;
+    // weights, sums, and what multiplies the values; beside codes all carry
+    // the factor 2^(20 - ve), with which a scale stays below 2^6
+    const float ref = (m == -INFINITY ? 0.f : m) - (F::coded ? (float)(20 - ve) : 0.f);
+    const uint64_t a2 = pack2(sscale, sscale), b2 = pack2(cst - ref, cst - ref);
     uint32_t ph[NT], pl[NT];
-    const float vn = __uint_as_float((uint32_t)(127 + 20 - ve) << 23);   // scale * vn < 2^6
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const float p0 = ex2(sc[nt][0] - ref), p1 = ex2(sc[nt][1] - ref);
-      l += p0 + p1;
+      const float2 x = unpack2(F::coded ? fma2(sc[nt], a2, b2) : add2(sc[nt], b2));
+      const uint64_t p = pack2(ex2(x.x), ex2(x.y));
+      l2 = add2(l2, p);
       if constexpr (F::coded) {
         const uint2 w = *reinterpret_cast<const uint2*>(&sm.sz[nt * 8 + 2 * tig]);
-        const float2 a0 = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
-        const float2 a1 = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
-        float s0 = p0 * (a0.x * vn), s1 = p1 * (a1.x * vn), t0 = p0 * a0.y, t1 = p1 * a1.y;
-        if (!(mine >> (8 * nt) & 1)) s0 = t0 = 0.f;    // whatever its scale holds
-        if (!(mine >> (8 * nt + 1) & 1)) s1 = t1 = 0.f;
-        zs += t0 + t1;
-        ph[nt] = pack_half2(s0, s1);
+        const float2 s0 = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
+        const float2 s1 = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+        z2 = fma2(p, pack2(s0.y, s1.y), z2);
+        const float2 v = unpack2(mul2(p, pack2(s0.x, s1.x)));
+        ph[nt] = pack_half2(v.x, v.y);
       } else {
-        ph[nt] = pack_bf16x2(p0, p1);
-        pl[nt] = pack_bf16x2(p0 - bf16_lo(ph[nt]), p1 - bf16_hi(ph[nt]));
+        const float2 v = unpack2(p);
+        ph[nt] = pack_bf16x2(v.x, v.y);
+        pl[nt] = pack_bf16x2(v.x - bf16_lo(ph[nt]), v.y - bf16_hi(ph[nt]));
       }
     }
     // O^T += V^T P
@@ -522,10 +640,18 @@ __device__ __forceinline__ void attend_mma_item(const AttendArgs& a, const RopeF
         }
       }
     }
+  };
+#pragma unroll 1
+  for (int s = 0; s < n_slots; s += 2) {
+    step(s, sz0);
+    if (s + 1 < n_slots) step(s + 1, sz1);
   }
   cp_wait<0>();                                        // nothing in flight when the buffers go
 
   // ---- the item's partial ----------------------------------------------------
+  const float vu = F::coded ? __uint_as_float((uint32_t)(127 + ve - 20) << 23) : 1.f;
+  const float2 lp = unpack2(l2), zp = unpack2(z2);
+  float l = (lp.x + lp.y) * vu, zs = (zp.x + zp.y) * vu;
   l += __shfl_xor_sync(kAll, l, 1);
   l += __shfl_xor_sync(kAll, l, 2);
   zs += __shfl_xor_sync(kAll, zs, 1);
@@ -556,10 +682,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     attend_mma_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ ChunkOwners owners,
                       const __grid_constant__ RopeFreqs f, int side_ctas, int n_side_ctas) {
   extern __shared__ __align__(16) uint8_t raw[];
-  const int warp = threadIdx.x / 32;
+  __shared__ float2 s_cs[D / 2];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   WarpSmem<D>& sm = reinterpret_cast<WarpSmem<D>*>(raw)[warp];
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();                           // the join may read the call's inputs before it waits
   const int per_seg = a.n_kv_heads * a.nvg;
   Item y;
   if ((int)blockIdx.x < n_side_ctas) {
@@ -583,13 +710,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     y.n_skip = y.pos0 = 0;
     y.slot = a.chunk_slots + (int64_t)y.r * a.nside + seg;
     if (y.h == 0 && y.vg == 0) {           // the selection, checked where its rows are read
-      for (int t = y.t0 + threadIdx.x % 32; t < min(y.t1, R.k); t += 32) {
+      for (int t = y.t0 + lane; t < min(y.t1, R.k); t += 32) {
         const int v = a.idx[R.sel0 + t];
         if (v < 0 || v >= R.n_ctx || (t > 0 && a.idx[R.sel0 + t - 1] >= v))
           report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_ATTEND_SEL, (uint32_t)t);
       }
     }
-    attend_mma_item<FUSE_BF16, D>(a, f, y, false, 0, nullptr, nullptr, sm);
+    attend_mma_item<FUSE_BF16, D>(a, y, nullptr, nullptr, nullptr, sm);
     return;
   }
   const int ctas = (a.nsub * per_seg + kWarps - 1) / kWarps;
@@ -600,10 +727,34 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   y.h = i % per_seg / a.nvg;
   y.vg = i % a.nvg;
   const fuse_chunk_t C = a.chunks[a.chunk0 + ci];
-  y.t0 = seg * a.seg;
-  if (seg >= a.nsub || y.t0 >= C.len) return;
   y.r = owners.req[ci];
   const fuse_request_t R = a.reqs[y.r];
+  // the chunk's angles, D / 16 pairs a warp.  The frequencies are launch
+  // parameters, which a warp reads fast only at one address at a time.
+  if (C.pos != 0) {                        // block-uniform
+    constexpr int N = D / 2 / kWarps;
+    float hi = 0.f, mid = 0.f, lo = 0.f, c, sn;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const float h = f.hi[warp * N + k], m = f.mid[warp * N + k], l = f.lo[warp * N + k];
+      if (lane == k) {
+        hi = h;
+        mid = m;
+        lo = l;
+      }
+    }
+    rope_cos_sin(C.pos, hi, mid, lo, c, sn);
+    if (lane < N) s_cs[warp * N + lane] = make_float2(c, sn);
+  }
+  __syncthreads();
+  y.t0 = seg * a.seg;
+  if (seg >= a.nsub) return;
+  if (y.t0 >= C.len) {                     // past the chunk's end: an item without a key
+    if (lane < kVecs)
+      a.part_ml[(((int64_t)(a.chunk0 + ci) * a.nsub + seg) * per_seg + i % per_seg) * kVecs + lane] =
+          make_float2(-INFINITY, 0.f);
+    return;
+  }
   constexpr int RB = Fmt<ST, D>::RB;
   y.k = reinterpret_cast<const uint8_t*>(C.k) + y.h * RB;
   y.v = reinterpret_cast<const uint8_t*>(C.v) + y.h * RB;
@@ -615,7 +766,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   y.skip = a.idx + R.sel0;
   y.pos0 = (int)(C.dst_row - R.row0);
   y.slot = (int64_t)(a.chunk0 + ci) * a.nsub + seg;
-  attend_mma_item<ST, D>(a, f, y, C.pos != 0, C.pos, reinterpret_cast<const __half*>(C.k_scale),
+  attend_mma_item<ST, D>(a, y, C.pos != 0 ? s_cs : nullptr, reinterpret_cast<const __half*>(C.k_scale),
                          reinterpret_cast<const __half*>(C.k_zero), sm);
 }
 

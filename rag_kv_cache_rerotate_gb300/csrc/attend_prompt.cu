@@ -235,6 +235,7 @@ extern "C" fuse_status_t fuse_attend_prompt(const fuse_layer_desc_t* desc,
   }
   std::stable_sort(rows.begin(), rows.end(), [](auto& x, auto& y) { return x.second > y.second; });
   cudaStream_t s = (cudaStream_t)stream;
+  if (rows.empty()) return FUSE_OK;
   const bool tc = prompt_tc_supported(*desc);
   if (!tc && desc->dtype != FUSE_F32) return FUSE_ERR_UNSUPPORTED;   // no tensor maps: no driver
   for (size_t r0 = 0; r0 < rows.size(); r0 += kPromptBatch) {

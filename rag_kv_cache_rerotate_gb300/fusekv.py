@@ -193,8 +193,14 @@ def _ptr(t: Optional[torch.Tensor]):
     return t.data_ptr() if t.numel() > 0 else None
 
 
+# the current stream's handle without building a torch.cuda.Stream (3 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return _raw_stream(torch.cuda.current_device())
         if not torch.cuda.is_available():
             return None
         stream = torch.cuda.current_stream()
@@ -483,23 +489,34 @@ def kivi_quantize(desc, src: ChunkTable, dst: ChunkTable, stream=None):
                                      _stream(stream)), "fuse_kivi_quantize")
 
 
-def _tensor(t, name, dtype=None, shape=None, optional=False):
-    """Refuse what the raw pointer would hide: a tensor of another type, shape,
-    stride or device than the call reads."""
-    if t is None and optional:
-        return
-    if t is None or not isinstance(t, torch.Tensor):
-        raise ValueError(f"{name}: a tensor is needed")
-    if dtype is not None and t.dtype != dtype:
+def _device() -> int:
+    """The device that the calls run on; -1 without CUDA (host tensors, as for
+    the refusals that need no GPU)."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -1
+
+
+def _tensor(t, name, dtype, dev):
+    """Refuse what the raw pointer would hide: a tensor of another type, stride
+    or device than the call reads.  Returns its shape."""
+    try:
+        if t.dtype is dtype and t.is_contiguous() and t.get_device() == dev:
+            return t.shape
+    except AttributeError:
+        raise ValueError(f"{name}: a tensor is needed") from None
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: {t.dtype}, {dtype} is needed")
     if not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous tensor is needed")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, {tuple(shape)} is needed")
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {t.device}, which is not the current device")
-    if not t.is_cuda and torch.cuda.is_available():
-        raise ValueError(f"{name}: not on a CUDA device")
+    raise ValueError(f"{name}: on {t.device}, which is not the current CUDA device")
+
+
+def _rows(t, name, dtype, dev, rows, heads, dim, exact=False):
+    """A [rows (or more), heads, dim] tensor's pointer."""
+    sh = _tensor(t, name, dtype, dev)
+    if len(sh) != 3 or sh[0] < rows or sh[1] != heads or sh[2] != dim or (exact and sh[0] != rows):
+        raise ValueError(f"{name}: shape {tuple(sh)}, {'' if exact else 'at least '}{rows} rows of "
+                         f"{heads} heads of {dim} are needed")
+    return t.data_ptr() or None
 
 
 _TORCH_DTYPE = {FUSE_F32: torch.float32, FUSE_BF16: torch.bfloat16}
@@ -525,37 +542,32 @@ def attend_chunks(desc: LayerDesc, chunks: ChunkTable, reqs: RequestTable, n_new
     """Attention of the last ``n_new`` tokens of every request over its chunk
     caches as stored (codes or layer type), the selected positions ``idx``
     replaced by the refreshed rows of ``Ks``, ``Vs`` (QCFuse Eqs. 4, 6)."""
-    dt = _TORCH_DTYPE.get(desc.dtype)
-    tot = reqs.extents()
-    _tensor(Q, "Q", dt, (reqs.n * int(n_new), desc.n_q_heads, desc.head_dim))
-    _tensor(O, "O", dt, Q.shape)
-    _tensor(idx, "idx", torch.int32, optional=tot.n_sel == 0)
-    if idx is not None and idx.numel() < tot.n_sel:
+    dt, dev, tot = _TORCH_DTYPE.get(desc.dtype), _device(), reqs.extents()
+    Hq, Hkv, d, n = desc.n_q_heads, desc.n_kv_heads, desc.head_dim, reqs.n * int(n_new)
+    if idx is None:
+        if tot.n_sel > 0:
+            raise ValueError(f"idx: {tot.n_sel} entries are needed")
+    elif _tensor(idx, "idx", torch.int32, dev).numel() < tot.n_sel:
         raise ValueError(f"idx: {idx.numel()} entries, {tot.n_sel} are needed")
-    for t, name in ((Ks, "Ks"), (Vs, "Vs")):
-        _tensor(t, name, dt)
-        if t.dim() != 3 or t.shape[0] < tot.n_out or tuple(t.shape[1:]) != (desc.n_kv_heads,
-                                                                            desc.head_dim):
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, at least {tot.n_out} rows of "
-                             f"{desc.n_kv_heads} heads of {desc.head_dim} are needed")
-    _check(load().fuse_attend_chunks(_c.byref(desc), _c.byref(chunks.c), _c.byref(reqs.c),
-                                     int(n_new), _ptr(Q), _ptr(idx), _ptr(Ks), _ptr(Vs), _ptr(O),
-                                     _ptr(ws), ws.numel(), _stream(stream)), "fuse_attend_chunks")
+    st = load().fuse_attend_chunks(
+        _c.byref(desc), _c.byref(chunks.c), _c.byref(reqs.c), int(n_new),
+        _rows(Q, "Q", dt, dev, n, Hq, d, True), _ptr(idx), _rows(Ks, "Ks", dt, dev, tot.n_out, Hkv, d),
+        _rows(Vs, "Vs", dt, dev, tot.n_out, Hkv, d), _rows(O, "O", dt, dev, n, Hq, d, True),
+        _ptr(ws), ws.numel(), _stream(stream))
+    if st != FUSE_OK:
+        raise FuseError(st, "fuse_attend_chunks")
 
 
 def attend_prompt(desc: LayerDesc, reqs: RequestTable, Q, K, V, O, ws, stream=None):
     """Causal attention inside every request's rows (whole prompts, packed)."""
-    dt = _TORCH_DTYPE.get(desc.dtype)
-    n_tok = reqs.extents().n_tok
-    for t, name, h in ((Q, "Q", desc.n_q_heads), (K, "K", desc.n_kv_heads),
-                       (V, "V", desc.n_kv_heads), (O, "O", desc.n_q_heads)):
-        _tensor(t, name, dt)
-        if t.dim() != 3 or t.shape[0] < n_tok or tuple(t.shape[1:]) != (h, desc.head_dim):
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, at least {n_tok} rows of {h} heads "
-                             f"of {desc.head_dim} are needed")
-    _check(load().fuse_attend_prompt(_c.byref(desc), _c.byref(reqs.c), _ptr(Q), _ptr(K), _ptr(V),
-                                     _ptr(O), _ptr(ws), ws.numel(), _stream(stream)),
-           "fuse_attend_prompt")
+    dt, dev, n = _TORCH_DTYPE.get(desc.dtype), _device(), reqs.extents().n_tok
+    Hq, Hkv, d = desc.n_q_heads, desc.n_kv_heads, desc.head_dim
+    st = load().fuse_attend_prompt(
+        _c.byref(desc), _c.byref(reqs.c), _rows(Q, "Q", dt, dev, n, Hq, d),
+        _rows(K, "K", dt, dev, n, Hkv, d), _rows(V, "V", dt, dev, n, Hkv, d),
+        _rows(O, "O", dt, dev, n, Hq, d), _ptr(ws), ws.numel(), _stream(stream))
+    if st != FUSE_OK:
+        raise FuseError(st, "fuse_attend_prompt")
 
 
 class PagePools:
@@ -574,15 +586,20 @@ class PagePools:
         self.block_size, self.kv_storage = int(block_size), int(kv_storage)
         self.n_blocks = int(k[0].shape[0]) if len(k) else 1
         self.shape = tuple(k[0].shape) if len(k) else None
+        dev = _device()
+
+        def same(t, name, dtype, shape):
+            if tuple(_tensor(t, name, dtype, dev)) != shape:
+                raise ValueError(f"{name}: shape {tuple(t.shape)}, {shape} is needed")
         for i in range(len(k)):
-            _tensor(k[i], "k", dt, self.shape)
-            _tensor(v[i], "v", dt, self.shape)
-            if self.shape[1] != self.block_size:
-                raise ValueError(f"k: pages of {self.shape[1]} tokens, not {self.block_size}")
+            same(k[i], "k", dt, self.shape)
+            same(v[i], "v", dt, self.shape)
+            if len(self.shape) != 4 or self.shape[1] != self.block_size:
+                raise ValueError(f"k: shape {self.shape}, pages of {self.block_size} tokens are needed")
             self.host[i] = Pool(_ptr(k[i]), _ptr(v[i]), None, None)
             if quant:
-                _tensor(v_scale[i], "v_scale", torch.float16, self.shape[:3])
-                _tensor(v_zero[i], "v_zero", torch.float16, self.shape[:3])
+                same(v_scale[i], "v_scale", torch.float16, self.shape[:3])
+                same(v_zero[i], "v_zero", torch.float16, self.shape[:3])
                 self.host[i].v_scale, self.host[i].v_zero = _ptr(v_scale[i]), _ptr(v_zero[i])
         self.c = Pools(len(k), self.kv_storage, self.block_size, 0, self.n_blocks,
                        _c.addressof(self.host))
@@ -601,42 +618,46 @@ def alloc_pages_workspace(tables: Optional[ChunkTable], device="cuda") -> torch.
     return torch.zeros(int(n.value), dtype=torch.uint8, device=device)
 
 
-def _max_moves(moves) -> int:
-    _tensor(moves, "moves", torch.int32)
-    if moves.numel() < 2:
+def _max_moves(moves, dev) -> int:
+    n = _tensor(moves, "moves", torch.int32, dev).numel()
+    if n < 2:
         raise ValueError("moves: count and live pages need two entries")
-    return (moves.numel() - 2) // 2
+    return (n - 2) // 2
 
 
-def _refs(refs, tables):
-    _tensor(refs, "refs", torch.int32)
-    if refs.numel() < tables.c.n_pool_blocks:
-        raise ValueError(f"refs: {refs.numel()} entries for {tables.c.n_pool_blocks} pages")
+def _refs(refs, tables, dev):
+    n = _tensor(refs, "refs", torch.int32, dev).numel()
+    if n < tables.c.n_pool_blocks:
+        raise ValueError(f"refs: {n} entries for {tables.c.n_pool_blocks} pages")
+    return refs.data_ptr() or None
 
 
 def pages_fork(src: ChunkTable, dst: ChunkTable, refs, moves, ws, stream=None):
     """Branch off ``src``'s sequences into ``dst``'s tables: full pages shared,
     partly filled last pages listed in ``moves`` for ``pages_copy``."""
-    _refs(refs, src)
-    _check(load().fuse_pages_fork(_c.byref(src.c), _c.byref(dst.c), _ptr(refs), _ptr(moves),
-                                  _max_moves(moves), _ptr(ws), ws.numel(), _stream(stream)),
-           "fuse_pages_fork")
+    dev = _device()
+    st = load().fuse_pages_fork(_c.byref(src.c), _c.byref(dst.c), _refs(refs, src, dev), _ptr(moves),
+                                _max_moves(moves, dev), _ptr(ws), ws.numel(), _stream(stream))
+    if st != FUSE_OK:
+        raise FuseError(st, "fuse_pages_fork")
 
 
 def pages_free(tables: ChunkTable, refs, ws, stream=None):
     """Every entry of ``tables`` gives up one reference."""
-    _refs(refs, tables)
-    _check(load().fuse_pages_free(_c.byref(tables.c), _ptr(refs), _ptr(ws), ws.numel(),
-                                  _stream(stream)), "fuse_pages_free")
+    st = load().fuse_pages_free(_c.byref(tables.c), _refs(refs, tables, _device()), _ptr(ws),
+                                ws.numel(), _stream(stream))
+    if st != FUSE_OK:
+        raise FuseError(st, "fuse_pages_free")
 
 
 def pages_compact(tables: ChunkTable, refs, moves, ws, stream=None):
     """Pack the live pages to the front: tables and refs rewritten, the page
     copies listed in ``moves`` for ``pages_copy``."""
-    _refs(refs, tables)
-    _check(load().fuse_pages_compact(_c.byref(tables.c), _ptr(refs), _ptr(moves),
-                                     _max_moves(moves), _ptr(ws), ws.numel(), _stream(stream)),
-           "fuse_pages_compact")
+    dev = _device()
+    st = load().fuse_pages_compact(_c.byref(tables.c), _refs(refs, tables, dev), _ptr(moves),
+                                   _max_moves(moves, dev), _ptr(ws), ws.numel(), _stream(stream))
+    if st != FUSE_OK:
+        raise FuseError(st, "fuse_pages_compact")
 
 
 def pages_copy(desc: LayerDesc, pools: PagePools, moves, ws, stream=None):
@@ -644,9 +665,10 @@ def pages_copy(desc: LayerDesc, pools: PagePools, moves, ws, stream=None):
     per = desc.head_dim // 2 if pools.kv_storage == FUSE_U4_ASYM else desc.head_dim
     if pools.shape is not None and pools.shape[2:] != (desc.n_kv_heads, per):
         raise ValueError(f"pools: pages of {pools.shape[2:]}, {(desc.n_kv_heads, per)} are needed")
-    _check(load().fuse_pages_copy(_c.byref(desc), _c.byref(pools.c), _ptr(moves),
-                                  _max_moves(moves), _ptr(ws), ws.numel(), _stream(stream)),
-           "fuse_pages_copy")
+    st = load().fuse_pages_copy(_c.byref(desc), _c.byref(pools.c), _ptr(moves),
+                                _max_moves(moves, _device()), _ptr(ws), ws.numel(), _stream(stream))
+    if st != FUSE_OK:
+        raise FuseError(st, "fuse_pages_copy")
 
 
 def check_errors(ws, stream=None):
