@@ -48,7 +48,8 @@ __global__ void __launch_bounds__(kThreads)
   pdl_trigger();
   pdl_wait();
   const int h = blockIdx.x % a.n_kv_heads;
-  const PromptTile t = prompt_tile(p, kRows / a.g, blockIdx.x / a.n_kv_heads);
+  int part = 0;
+  const PromptTile t = prompt_tile(p, kRows / a.g, blockIdx.x / a.n_kv_heads, &part);
   const int n_rows = t.rows * a.g;
   const T* Q = reinterpret_cast<const T*>(a.Q);
   const T* K = reinterpret_cast<const T*>(a.K);
@@ -181,15 +182,14 @@ fuse_status_t make_table(const std::pair<int32_t, int32_t>* r, int n, int rtile,
   p->n_req = n;
   int64_t at = 0;
   for (int j = 0; j < n; ++j) {
-    p->row0[j] = r[j].first;
-    p->len[j] = r[j].second;
-    p->start[j] = (int32_t)at;
-    const int64_t mine = (r[j].second + rtile - 1) / rtile;
+    const int32_t mine = (r[j].second + rtile - 1) / rtile;
     const int64_t next = j + 1 < n ? (r[j + 1].second + rtile - 1) / rtile : 0;
+    p->req[j] = {(int32_t)at, r[j].first, r[j].second, mine};
     at += (mine - next) * (j + 1);
     if (at > INT32_MAX / 128) return FUSE_ERR_UNSUPPORTED;
   }
-  p->start[n] = p->n_tiles = (int32_t)at;
+  p->n_tiles = (int32_t)at;
+  p->req[n] = {p->n_tiles, 0, 0, 0};
   return FUSE_OK;
 }
 

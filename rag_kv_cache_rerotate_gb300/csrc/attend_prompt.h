@@ -13,14 +13,18 @@ constexpr int kPromptBatch = 256;         // requests of one launch (parameter s
 // over all requests that have it: heaviest first.  Between the tile counts of
 // consecutive requests the number of requests that have a tile index is
 // constant, so tile `t` (in that order) is found from the order's starts:
-// tiles [start[j], start[j + 1]) are those of indexes [tiles[j + 1],
-// tiles[j]), taken over requests 0 .. j.
+// tiles [req[j].start, req[j + 1].start) are those of indexes [tiles of j + 1,
+// tiles of j), taken over requests 0 .. j.
+struct __align__(16) PromptRequest {
+  int32_t start;                          // first tile of the order's part j
+  int32_t row0;                           // first packed row
+  int32_t len;                            // rows, descending, > 0
+  int32_t tiles;
+};
 struct PromptTable {
   int32_t n_req;
   int32_t n_tiles;                        // in all
-  int32_t row0[kPromptBatch];             // first packed row
-  int32_t len[kPromptBatch];              // rows, descending, > 0
-  int32_t start[kPromptBatch + 1];
+  PromptRequest req[kPromptBatch + 1];    // the last: start = n_tiles
 };
 
 struct PromptTile {
@@ -30,18 +34,23 @@ struct PromptTile {
   int rows;                               // its rows
 };
 
-__host__ __device__ inline PromptTile prompt_tile(const PromptTable& p, int rtile, int t) {
-  int lo = 0, hi = p.n_req - 1;           // last j with start[j] <= t
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.start[mid] <= t) lo = mid; else hi = mid - 1;
+// Tile t; *part: the order's part that it is in, at most that on entry (tiles
+// asked for in ascending order: pass the same variable, at first 0).
+__host__ __device__ inline PromptTile prompt_tile(const PromptTable& p, int rtile, int t, int* part) {
+  int j = *part;
+  while (p.req[j + 1].start <= t) ++j;    // ends: the last start is past every tile
+  *part = j;
+  const PromptRequest o = p.req[j];
+  const int u = t - o.start, n = j + 1;
+  int r = 0, index = o.tiles - 1 - u;
+  if (n > 1) {
+    r = u % n;
+    index = o.tiles - 1 - u / n;
   }
-  const int u = t - p.start[lo], n = lo + 1;
-  const int r = u % n;
-  const int index = (p.len[lo] + rtile - 1) / rtile - 1 - u / n;
+  const PromptRequest q = p.req[r];
   PromptTile x;
-  x.row0 = p.row0[r];
-  x.len = p.len[r];
+  x.row0 = q.row0;
+  x.len = q.len;
   x.first = index * rtile;
   x.rows = x.len - x.first < rtile ? x.len - x.first : rtile;
   return x;

@@ -134,10 +134,12 @@ struct Unit {
   int nkb;                // key blocks
 };
 
-__device__ __forceinline__ Unit unit_rec(const PromptTcArgs& a, const PromptTable& p, int u) {
+__device__ __forceinline__ Unit unit_rec(const PromptTcArgs& a, const PromptTable& p, int u,
+                                         int* part) {
   Unit r;
-  r.kvh = u % a.Hkv;
-  r.t = prompt_tile(p, a.rtile, u / a.Hkv);
+  const int t = u / a.Hkv;
+  r.kvh = u - t * a.Hkv;
+  r.t = prompt_tile(p, a.rtile, t, part);
   r.nkb = (r.t.first + r.t.rows - 1) / kKB + 1;
   return r;
 }
@@ -189,9 +191,9 @@ __device__ __forceinline__ uint64_t kmajor_step(uint32_t tile, int kk) {
   return tc::smem_desc_k128(tile + (kk >> 2) * kHalf + (kk & 3) * 32);
 }
 
-__device__ __forceinline__ uint32_t drop_nonfinite(uint32_t w, bool* found) {
-  if ((w & 0x7F80u) == 0x7F80u) { w &= 0xFFFF0000u; *found = true; }
-  if ((w & 0x7F800000u) == 0x7F800000u) { w &= 0xFFFFu; *found = true; }
+__device__ __forceinline__ uint32_t drop_nonfinite(uint32_t w) {
+  if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+  if ((w & 0x7F800000u) == 0x7F800000u) w &= 0xFFFFu;
   return w;
 }
 
@@ -253,8 +255,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t kc = 0;
       int i = 0;
       bool ok = true;
+      int part = 0;
       for (; unit_at(i) < n_units && ok; ++i) {
-        const Unit cur = unit_rec(a, table, unit_at(i));
+        const Unit cur = unit_rec(a, table, unit_at(i), &part);
         const int qb = i % kQBufs;
         if (!wait1(&ctl->q_empty[qb], ((i / kQBufs) & 1) ^ 1, ctl, a.err, W_Q_EMPTY, 0)) break;
         uint8_t* q = sQ + qb * kTile;
@@ -287,8 +290,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       uint32_t vc = 0;
       bool ok = true;
+      int part = 0;
       for (int i = 0; unit_at(i) < n_units && ok; ++i) {
-        const Unit cur = unit_rec(a, table, unit_at(i));
+        const Unit cur = unit_rec(a, table, unit_at(i), &part);
         for (int j = 0; j < cur.nkb; ++j, ++vc) {
           const int st = vc % kVS;
           if (!wait1(&ctl->v_empty[st], ((vc / kVS) & 1) ^ 1, ctl, a.err, W_V_EMPTY, j)) {
@@ -310,8 +314,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       uint32_t kc = 0;
       bool ok = true;
+      int part = 0;
       for (int i = 0; unit_at(i) < n_units && ok; ++i) {
-        const Unit cur = unit_rec(a, table, unit_at(i));
+        const Unit cur = unit_rec(a, table, unit_at(i), &part);
         const int qb = i % kQBufs;
         if (!wait1(&ctl->q_full[qb], (i / kQBufs) & 1, ctl, a.err, W_Q_FULL, 0)) break;
         const uint32_t q_addr = tc::smem_u32(sQ + qb * kTile);
@@ -347,68 +352,99 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t o = tmem + kColO;
     uint32_t vc = 0;
     bool ok = true;
+    int part = 0;
     for (int i = 0; unit_at(i) < n_units && ok; ++i) {
-      const Unit cur = unit_rec(a, table, unit_at(i));
+      const Unit cur = unit_rec(a, table, unit_at(i), &part);
       // O and the fix flag were last read by the output warps for unit i - 1
       if (!wait32(&ctl->o_empty, (i & 1) ^ 1, ctl, a.err, W_O_EMPTY, 0)) break;
-      for (int j = 0; j < cur.nkb; ++j, ++vc) {
-        const int st = vc % kVS;
-        const uint32_t sb = vc % kSBufs;
-        const int keys = block_keys(cur, j);
-        uint8_t* v = sV + st * kTile;
-        if (!wait32(&ctl->v_full[st], (vc / kVS) & 1, ctl, a.err, W_V_FULL, j)) {
-          ok = false;
-          break;
-        }
-        if (j == cur.nkb - 1) {
-          // rows after the tile's first one, four rows of 64 columns at a time
-          const int row1 = cur.t.first + 1 - j * kKB, seen = cur.t.first + cur.t.rows - j * kKB;
-          bool found = false, wrote = false;
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            for (int n = row1 + lane / 8; n < keys; n += 4) {
-              uint4* p = reinterpret_cast<uint4*>(v + h * kHalf + n * 128) + lane % 8;
-              if (n >= seen) {
-                *p = make_uint4(0, 0, 0, 0);
-                wrote = true;
-              } else {
-                uint4 x = *p;
-                bool f = false;
-                x.x = drop_nonfinite(x.x, &f);
-                x.y = drop_nonfinite(x.y, &f);
-                x.z = drop_nonfinite(x.z, &f);
-                x.w = drop_nonfinite(x.w, &f);
-                if (f) {
-                  *p = x;
-                  found = wrote = true;
-                }
-              }
-            }
-          if (wrote) tc::fence_proxy_async_smem();
-          found = __any_sync(0xffffffffu, found);
-          if (lane == 0) {
-            ctl->fix = found;
-            tc::mbar_arrive(&ctl->fix_full);
-          }
-        }
-        if (!wait32(&ctl->p_full[sb], (vc / kSBufs) & 1, ctl, a.err, W_P_FULL, j)) {
-          ok = false;
-          break;
-        }
-        tc::tc_fence_after();
-        if (lane == 0) {
-          const uint32_t vaddr = tc::smem_u32(v);
+      if (lane == 0) {
+        // the blocks before the last
+        for (int j = 0; j < cur.nkb - 1; ++j) {
+          const uint32_t c = vc + j;
+          const int st = c % kVS;
+          const uint32_t sb = c % kSBufs;
+          ok = wait1(&ctl->p_full[sb], (c / kSBufs) & 1, ctl, a.err, W_P_FULL, j) &&
+               wait1(&ctl->v_full[st], (c / kVS) & 1, ctl, a.err, W_V_FULL, j);
+          if (!ok) break;
+          tc::tc_fence_after();
+          const uint32_t vaddr = tc::smem_u32(sV + st * kTile);
           const uint32_t pa = tmem + sb * kKB;
-          for (int kk = 0; kk < keys / 16; ++kk)
+#pragma unroll
+          for (int kk = 0; kk < kKB / 16; ++kk)
             tc::mma_bf16_ts(o, pa + kk * 8, tc::smem_desc_mn128(vaddr + kk * 16 * 128, kHalf),
                             idesc_o, (j | kk) != 0 ? 1u : 0u);
           tc::mma_commit(&ctl->pv_done[sb]);
           tc::mma_commit(&ctl->v_empty[st]);
         }
-        __syncwarp();
       }
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      if (lane == 0) tc::mma_commit(&ctl->o_full);
+      // the last block: its values are looked through while the softmax works
+      const int j = cur.nkb - 1, keys = block_keys(cur, j);
+      vc += j;
+      const int st = vc % kVS;
+      const uint32_t sb = vc % kSBufs;
+      uint8_t* v = sV + st * kTile;
+      if (!wait32(&ctl->v_full[st], (vc / kVS) & 1, ctl, a.err, W_V_FULL, j)) break;
+      {
+        // rows after the tile's first one, four rows of 64 columns at a time
+        const int row1 = cur.t.first + 1 - j * kKB, seen = cur.t.first + cur.t.rows - j * kKB;
+        // 0 * x is 0 unless x is infinite or NaN
+        const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+        __nv_bfloat162 sum[4] = {zero, zero, zero, zero};
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h)
+#pragma unroll 4
+          for (int n = row1 + lane / 8; n < seen; n += 4) {
+            const uint4 x = reinterpret_cast<const uint4*>(v + h * kHalf + n * 128)[lane % 8];
+            sum[0] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.x), zero, sum[0]);
+            sum[1] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.y), zero, sum[1]);
+            sum[2] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.z), zero, sum[2]);
+            sum[3] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.w), zero, sum[3]);
+          }
+        const float2 t = __bfloat1622float2(__hadd2(__hadd2(sum[0], sum[1]), __hadd2(sum[2], sum[3])));
+        const bool found = __any_sync(0xffffffffu, !(t.x == 0.f && t.y == 0.f));
+        if (found || seen < keys) {                    // rare, or the request's last tile
+#pragma unroll 1
+          for (int n = row1 + lane / 8; n < keys; n += 4)
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h) {
+              uint4* p = reinterpret_cast<uint4*>(v + h * kHalf + n * 128) + lane % 8;
+              if (n >= seen) {
+                *p = make_uint4(0, 0, 0, 0);
+              } else if (found) {
+                uint4 x = *p;
+                x.x = drop_nonfinite(x.x);
+                x.y = drop_nonfinite(x.y);
+                x.z = drop_nonfinite(x.z);
+                x.w = drop_nonfinite(x.w);
+                *p = x;
+              }
+            }
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0) {
+          ctl->fix = found;
+          tc::mbar_arrive(&ctl->fix_full);
+        }
+      }
+      if (!wait32(&ctl->p_full[sb], (vc / kSBufs) & 1, ctl, a.err, W_P_FULL, j)) break;
+      tc::tc_fence_after();
+      if (lane == 0) {
+        const uint32_t vaddr = tc::smem_u32(v);
+        const uint32_t pa = tmem + sb * kKB;
+#pragma unroll
+        for (int kk = 0; kk < kKB / 16; ++kk)
+          if (kk * 16 < keys)
+            tc::mma_bf16_ts(o, pa + kk * 8, tc::smem_desc_mn128(vaddr + kk * 16 * 128, kHalf),
+                            idesc_o, (j | kk) != 0 ? 1u : 0u);
+        tc::mma_commit(&ctl->pv_done[sb]);
+        tc::mma_commit(&ctl->v_empty[st]);
+        tc::mma_commit(&ctl->o_full);
+      }
+      __syncwarp();
+      ++vc;
     }
   } else if (warp < kWarpOut) {
     // ------------------------------- softmax -------------------------------
@@ -420,8 +456,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float scale = a.scale_log2;
     const uint32_t tO = tmem + lane_off + kColO;
     uint32_t b = 0;
+    int part = 0;
     for (int i = 0; unit_at(i) < n_units; ++i) {
-      const Unit cur = unit_rec(a, table, unit_at(i));
+      const Unit cur = unit_rec(a, table, unit_at(i), &part);
       const int p0 = cur.t.first + min(R0 / a.g, cur.t.rows - 1);
       const int p1 = cur.t.first + min(R1 / a.g, cur.t.rows - 1);
       float mu0 = kFloor, mu1 = kFloor;                // running maxima (log2 units)
@@ -550,8 +587,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tO = tmem + ((uint32_t)(quarter * 32) << 16) + kColO;
     const int rl = m / a.g;
     const int hh = m % a.g;
+    int part = 0;
     for (int i = 0; unit_at(i) < n_units; ++i) {
-      const Unit cur = unit_rec(a, table, unit_at(i));
+      const Unit cur = unit_rec(a, table, unit_at(i), &part);
       if (!wait32(&ctl->o_full, i & 1, ctl, a.err, W_O_FULL, cur.nkb)) break;
       if (!wait32(&ctl->l_full, i & 1, ctl, a.err, W_L_FULL, cur.nkb)) break;
       if (!wait32(&ctl->fix_full, i & 1, ctl, a.err, W_FIX, cur.nkb)) break;
