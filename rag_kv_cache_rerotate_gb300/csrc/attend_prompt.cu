@@ -184,12 +184,13 @@ fuse_status_t make_table(const std::pair<int32_t, int32_t>* r, int n, int rtile,
   for (int j = 0; j < n; ++j) {
     const int32_t mine = (r[j].second + rtile - 1) / rtile;
     const int64_t next = j + 1 < n ? (r[j + 1].second + rtile - 1) / rtile : 0;
-    p->req[j] = {(int32_t)at, r[j].first, r[j].second, mine};
+    p->req[j] = {(int32_t)at, r[j].first, r[j].second, mine,
+                 (uint32_t)((((uint64_t)1 << 32) + j) / (j + 1)), 0};
     at += (mine - next) * (j + 1);
-    if (at > INT32_MAX / 128) return FUSE_ERR_UNSUPPORTED;
+    if (at > kMaxUnits) return FUSE_ERR_UNSUPPORTED;
   }
   p->n_tiles = (int32_t)at;
-  p->req[n] = {p->n_tiles, 0, 0, 0};
+  p->req[n] = {p->n_tiles, 0, 0, 0, 0, 0};
   return FUSE_OK;
 }
 
@@ -243,7 +244,7 @@ extern "C" fuse_status_t fuse_attend_prompt(const fuse_layer_desc_t* desc,
     st = make_table(rows.data() + r0, (int)std::min<size_t>(kPromptBatch, rows.size() - r0),
                     prompt_rtile(*desc, tc), &p);
     if (st != FUSE_OK) return st;
-    if ((int64_t)p.n_tiles * desc->n_kv_heads > INT32_MAX) return FUSE_ERR_UNSUPPORTED;
+    if ((int64_t)p.n_tiles * desc->n_kv_heads > kMaxUnits) return FUSE_ERR_UNSUPPORTED;
     st = cuda_status(traced(tc ? "attend_prompt_tc" : "attend_prompt_simt", s, [&] {
       return tc ? launch_prompt_tc(*desc, p, info.tot.n_tok, Q, K, V, O,
                                    reinterpret_cast<uint32_t*>(ws), s)

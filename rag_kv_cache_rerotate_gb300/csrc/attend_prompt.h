@@ -7,6 +7,7 @@
 namespace fusekv {
 
 constexpr int kPromptBatch = 256;         // requests of one launch (parameter space)
+constexpr int kMaxUnits = 1 << 24;        // (tile, KV head) units of one launch
 
 // Requests of one launch, longest first.  A tile is rtile consecutive rows of
 // a request.  Tiles are taken from the highest tile index down, at one index
@@ -15,11 +16,13 @@ constexpr int kPromptBatch = 256;         // requests of one launch (parameter s
 // constant, so tile `t` (in that order) is found from the order's starts:
 // tiles [req[j].start, req[j + 1].start) are those of indexes [tiles of j + 1,
 // tiles of j), taken over requests 0 .. j.
-struct __align__(16) PromptRequest {
+struct __align__(8) PromptRequest {
   int32_t start;                          // first tile of the order's part j
   int32_t row0;                           // first packed row
   int32_t len;                            // rows, descending, > 0
   int32_t tiles;
+  uint32_t inv;                           // ceil(2^32 / (j + 1)): x / (j + 1) = umulhi(x, inv), x < 2^24
+  int32_t pad;
 };
 struct PromptTable {
   int32_t n_req;
@@ -36,7 +39,7 @@ struct PromptTile {
 
 // Tile t; *part: the order's part that it is in, at most that on entry (tiles
 // asked for in ascending order: pass the same variable, at first 0).
-__host__ __device__ inline PromptTile prompt_tile(const PromptTable& p, int rtile, int t, int* part) {
+__device__ __forceinline__ PromptTile prompt_tile(const PromptTable& p, int rtile, int t, int* part) {
   int j = *part;
   while (p.req[j + 1].start <= t) ++j;    // ends: the last start is past every tile
   *part = j;
@@ -44,8 +47,9 @@ __host__ __device__ inline PromptTile prompt_tile(const PromptTable& p, int rtil
   const int u = t - o.start, n = j + 1;
   int r = 0, index = o.tiles - 1 - u;
   if (n > 1) {
-    r = u % n;
-    index = o.tiles - 1 - u / n;
+    const int q = (int)__umulhi((uint32_t)u, o.inv);
+    r = u - q * n;
+    index = o.tiles - 1 - q;
   }
   const PromptRequest q = p.req[r];
   PromptTile x;
