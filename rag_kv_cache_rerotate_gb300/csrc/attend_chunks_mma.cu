@@ -17,11 +17,6 @@
 // of shared memory per warp filled by 16-byte cp.async two ahead.  The warps
 // of a CTA take neighbouring KV heads of the same tokens, so together they
 // read whole rows.  Warps share only the chunk's angles.
-//   S^T = Q K^T   A = Q (rows 0-7: the vectors' high parts, 8-15: what is
-//                 left of them, 22 bits together), B = codes of 8 keys, the
-//                 channels in whatever order the lanes hold them
-//   O^T += V^T P  A = codes (rows: channels, 16 keys), B = P: the layout in
-//                 which S^T comes out is the one that P goes in
 // P carries the values' per-token scale, normalised by the largest so far (a
 // power of two), in fp16 (bf16 rows: in two bf16 parts).  The maximum and the
 // normaliser are raised lazily.
@@ -34,27 +29,25 @@ namespace fusekv {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kSlots = 3;
+constexpr int kWarps = 4;
+constexpr int kSlots = 2;
 constexpr float kRaise = 8.0f;            // log2: P <= 2^8, times a scale <= 2^6 stays in fp16
 
 template <int ST, int D> struct Fmt {
   static constexpr bool coded = ST != FUSE_BF16;
   static constexpr int RB = ST == FUSE_BF16 ? 2 * D : ST == FUSE_U8_ASYM ? D : D / 2;   // row bytes
   static constexpr int RC = RB / 16;                   // 16-byte chunks of a row
-  static constexpr int TOK = ST == FUSE_BF16 ? 8 : ST == FUSE_U8_ASYM ? 16 : 32;        // keys a slot
-  static constexpr int NT = TOK / 8;
-  static constexpr int KSTEP = D / 16;
-  static constexpr int MT = D / 16;
+  static constexpr int TOK = ST == FUSE_BF16 ? 16 : ST == FUSE_U8_ASYM ? 32 : 64;       // keys a slot
+  static constexpr int ROWS = TOK > 32 ? TOK / 32 : 1;                                  // of a lane
+  static constexpr uint32_t kFull = TOK >= 32 ? 0xffffffffu : (1u << TOK) - 1;          // per 32 keys
 };
-constexpr int slot_bytes(int d) { return 32 * d; }     // TOK keys and values, in every format
+constexpr int slot_bytes(int d) { return 64 * d; }     // TOK keys and values, in every format
 
 template <int D> struct WarpSmem {
   uint8_t slot[kSlots][slot_bytes(D)];
   uint32_t skip[32];                                   // bit per key: selected, not read here
-  uint32_t keep[kSlots];                               // bit per key of the slot: inside, page known
-  uint32_t pad;
-  uint32_t sz[32];                                     // (scale, zero) of the slot's values, fp16
+  uint32_t keep[kSlots][2];                            // bit per key of the slot: to be seen
+  uint32_t sz[64];                                     // (scale, zero) of the slot's values, fp16
 };
 
 struct Item {
@@ -126,12 +119,21 @@ __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, u
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma8_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
-  asm(
-      "mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6},"
-      " {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(b0));
+// c: the accumulators as (row gid, row gid + 8) pairs of columns.
+__device__ __forceinline__ void mma16p(uint64_t (&c)[2], uint32_t a0, uint32_t a1, uint32_t a2,
+                                       uint32_t a3, uint32_t b0, uint32_t b1) {
+  const float2 x = unpack2(c[0]), y = unpack2(c[1]);
+  float d[4] = {x.x, x.y, y.x, y.y};
+  mma16<true>(d, a0, a1, a2, a3, b0, b1);
+  c[0] = pack2(d[0], d[1]);
+  c[1] = pack2(d[2], d[3]);
+}
+// Transposes an 8 x 8 matrix of 16-bit elements held two a lane (row gid,
+// columns 2 tig and 2 tig + 1).
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
@@ -182,79 +184,80 @@ __device__ __forceinline__ int warp_lower_bound(const int32_t* a, int n, int x) 
   return lo;
 }
 
-template <int ST, int D>
-__device__ __forceinline__ void attend_mma_item(const AttendArgs& a, const Item& y, const float2* cs,
-                                                const __half* ks, const __half* kz,
-                                                WarpSmem<D>& sm) {
+// The keys of an item on their way to shared memory: slots of TOK keys in two
+// buffers in turn.
+template <int ST, int D> struct Feed {
   using F = Fmt<ST, D>;
-  constexpr int RB = F::RB, RC = F::RC, TOK = F::TOK, NT = F::NT, KSTEP = F::KSTEP, MT = F::MT;
-  constexpr uint32_t kAll = 0xffffffffu;
-  const int lane = threadIdx.x % 32, gid = lane >> 2, tig = lane & 3;
-  const int64_t stride = (int64_t)a.n_kv_heads * RB;
-  const int n_slots = (y.t1 - y.t0 + TOK - 1) / TOK;
+  static constexpr int RB = F::RB, RC = F::RC, TOK = F::TOK;
+  static constexpr uint32_t kAll = 0xffffffffu;
+  const AttendArgs& a;
+  const Item& y;
+  WarpSmem<D>& sm;
+  const int lane;
+  const int64_t stride;                                // bytes between rows
+  const int dq, dr, bs;                                // TOK in pages and rows
+  int blk[F::ROWS], rem[F::ROWS], id[F::ROWS];         // this lane's keys of the slot copied next
+  int row[F::ROWS];                                    // rows of those of the slot copied last, -1: none
+  int slot, buf;                                       // the slot copied next, and its buffer
 
-  // ---- selected keys of the item, a bit each -------------------------------
-  auto mark_selected = [&]() {
-    sm.skip[lane] = 0;
-    __syncwarp();
-    if (y.n_skip > 0) {
-      const int p0 = y.pos0 + y.t0, p1 = y.pos0 + y.t1;
-      for (int i = warp_lower_bound(y.skip, y.n_skip, p0);; i += 32) {
-        const int v = i + lane < y.n_skip ? y.skip[i + lane] : p1;
-        const bool in = v >= p0 && v < p1;
-        if (in) atomicOr(&sm.skip[(v - p0) >> 5], 1u << ((v - p0) & 31));
-        if (!__all_sync(kAll, in)) break;
+  __device__ __forceinline__ Feed(const AttendArgs& a_, const Item& y_, WarpSmem<D>& sm_)
+      : a(a_), y(y_), sm(sm_), lane(threadIdx.x % 32), stride((int64_t)a_.n_kv_heads * RB),
+        dq(y_.table ? TOK / a_.block_size : 0), dr(TOK - dq * (y_.table ? a_.block_size : 0)),
+        bs(y_.table ? a_.block_size : INT32_MAX), slot(0), buf(0) {
+#pragma unroll
+    for (int r = 0; r < F::ROWS; ++r) {
+      rem[r] = y.t0 + r * 32 + lane;
+      blk[r] = id[r] = 0;
+      if (y.table) {
+        blk[r] = rem[r] / bs;
+        rem[r] -= blk[r] * bs;
       }
-    }
-    __syncwarp();
-  };
-
-  // ---- rows of a slot's keys, one per lane ----------------------------------
-  // The page id of the slot loaded next is read one slot ahead and looked at
-  // only when it is used, so that its read is not waited for.
-  int blk = 0, rem = y.t0 + lane, id = 0, t_next = y.t0 + lane;   // this lane's key of that slot
-  const int dq = y.table ? TOK / a.block_size : 0, dr = TOK - dq * a.block_size;
-  const int bs = y.table ? a.block_size : INT32_MAX;
-  if (y.table) {
-    blk = rem / bs;
-    rem -= blk * bs;
-  }
-  auto load_id = [&]() {
-    if (y.table && lane < TOK && t_next < y.t1) id = y.table[blk];
-  };
-  auto next_row = [&]() {                              // its row, -1: none; then the next slot's id
-    const bool in = lane < TOK && t_next < y.t1;
-    int row = in ? rem : -1;
-    if (y.table && in) {
-      if (id >= 0 && id < a.n_pool_blocks) {
-        row = id * bs + rem;
-      } else {
-        report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_ATTEND_BLOCK, (uint32_t)id);
-        row = -1;
-      }
-    }
-    t_next += TOK;
-    blk += dq;
-    rem += dr;
-    if (rem >= bs) {
-      rem -= bs;
-      ++blk;
     }
     load_id();
-    return row;
-  };
-  // slot s into its buffer; returns the row of this lane's key, -1: none
-  auto issue = [&](int s) {
-    int row = next_row();
-    if constexpr (!F::coded)                           // what is not seen may hold anything
-      if (row >= 0 && (sm.skip[(s * TOK + lane) >> 5] >> ((s * TOK + lane) & 31) & 1)) row = -1;
-    const uint32_t ok = __ballot_sync(kAll, row >= 0);
-    uint8_t* buf = sm.slot[s % kSlots];
-    if (lane == 0) sm.keep[s % kSlots] = ok;
-    const uint32_t dk = (uint32_t)__cvta_generic_to_shared(buf), dv = dk + TOK * RB;
-    const bool whole = ok == (uint32_t)((1ull << TOK) - 1);
-    if (!y.table && whole) {               // warp-uniform: TOK consecutive rows
-      const int64_t off = (int64_t)(y.t0 + s * TOK + lane / RC) * stride + lane % RC * 16;
+  }
+  __device__ __forceinline__ bool inside(int r) const {
+    const int k = r * 32 + lane;
+    return (TOK >= 32 || k < TOK) && y.t0 + slot * TOK + k < y.t1;
+  }
+  // The page id of the slot copied next is read one slot ahead and looked at
+  // only when it is used, so that its read is not waited for.
+  __device__ __forceinline__ void load_id() {
+#pragma unroll
+    for (int r = 0; r < F::ROWS; ++r)
+      if (y.table && inside(r)) id[r] = y.table[blk[r]];
+  }
+  // Copies the next slot.  kMarked: the selected keys are known.
+  template <bool kMarked> __device__ __forceinline__ void copy() {
+    bool whole = !y.table;
+#pragma unroll
+    for (int r = 0; r < F::ROWS; ++r) {
+      row[r] = inside(r) ? rem[r] : -1;
+      if (y.table && row[r] >= 0) {
+        if (id[r] >= 0 && id[r] < a.n_pool_blocks) {
+          row[r] += id[r] * bs;
+        } else {
+          report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_ATTEND_BLOCK, (uint32_t)id[r]);
+          row[r] = -1;
+        }
+      }
+      const int k = slot * TOK + r * 32;
+      uint32_t skip = kMarked ? sm.skip[k >> 5] : 0u;
+      if constexpr (TOK < 32) skip >>= k & 31;
+      if constexpr (!F::coded)                         // what is not seen may hold anything
+        if (skip >> lane & 1) row[r] = -1;
+      const uint32_t ok = __ballot_sync(kAll, row[r] >= 0);
+      if (lane == 0) sm.keep[buf][r] = ok & ~skip;
+      whole = whole && ok == F::kFull;
+      rem[r] += dr;
+      blk[r] += dq;
+      if (rem[r] >= bs) {
+        rem[r] -= bs;
+        ++blk[r];
+      }
+    }
+    const uint32_t dk = (uint32_t)__cvta_generic_to_shared(sm.slot[buf]), dv = dk + TOK * RB;
+    if (whole) {                                       // warp-uniform: TOK consecutive rows
+      const int64_t off = (int64_t)(y.t0 + slot * TOK + lane / RC) * stride + lane % RC * 16;
       const uint8_t *pk = y.k + off, *pv = y.v + off;
 #pragma unroll
       for (int i = 0; i < TOK * RC / 32; ++i) {
@@ -265,293 +268,488 @@ __device__ __forceinline__ void attend_mma_item(const AttendArgs& a, const Item&
         pk += (32 / RC) * stride;
         pv += (32 / RC) * stride;
       }
-      return row;
-    }
+    } else {
 #pragma unroll
-    for (int i = 0; i < TOK * RC / 32; ++i) {
-      const int key = (i * 32 + lane) / RC, c = (i * 32 + lane) % RC;
-      const int kr = __shfl_sync(kAll, row, key);
-      const int64_t off = (int64_t)max(kr, 0) * stride + c * 16;
-      cp16(dk + key * RB + k_chunk<RC>(key, c) * 16, y.k + off, kr >= 0);
-      const int vr = v_row(key);
-      cp16(dv + vr * RB + v_chunk<RC>(vr, c) * 16, y.v + off, kr >= 0);
-    }
-    return row;
-  };
-  // scale and zero of a slot's values: read two slots ahead, looked at when used
-  auto load_sz = [&](int row, uint16_t& vs, uint16_t& vz) {
-    vs = vz = 0;
-    if (F::coded && row >= 0) {
-      const int64_t at = (int64_t)row * a.n_kv_heads;
-      vs = reinterpret_cast<const uint16_t*>(y.vs)[at];
-      vz = reinterpret_cast<const uint16_t*>(y.vz)[at];
-    }
-  };
-
-  if constexpr (!F::coded) mark_selected();
-  load_id();
-  uint16_t sz0[2], sz1[2];                             // even and odd slots
-  load_sz(issue(0), sz0[0], sz0[1]);
-  cp_commit();
-  load_sz(issue(1), sz1[0], sz1[1]);
-  cp_commit();
-
-  // ---- the query vectors, turned back and scaled, as A operands --------------
-  uint32_t qa[KSTEP][4];
-  float sscale, cst;                                   // score = sum * sscale + cst (vector gid)
-  {
-    // a lane's channel pairs (j, j + D / 2): j = NP lane .. NP lane + NP - 1
-    constexpr int NP = D / 64;
-    const int n_vec = a.g * a.n_new, j0 = NP * lane;
-    auto load_pair = [](const __nv_bfloat16* p, float (&x)[NP]) {
-      if constexpr (NP == 2) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-        x[0] = bf16_lo(w);
-        x[1] = bf16_hi(w);
-      } else {
-        x[0] = __bfloat162float(*p);
-      }
-    };
-    auto load_half = [](const __half* p, float (&x)[NP]) {
-#pragma unroll
-      for (int i = 0; i < NP; ++i) x[i] = __half2float(p[i]);
-    };
-    float x0[kVecs][NP], x1[kVecs][NP], k0[NP], k1[NP], z0[NP], z1[NP];
-#pragma unroll
-    for (int v = 0; v < kVecs; ++v) {
-      const int vi = y.vg * kVecs + v;
-#pragma unroll
-      for (int i = 0; i < NP; ++i) x0[v][i] = x1[v][i] = 0.f;
-      if (vi < n_vec) {                                // warp-uniform
-        const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.Q) +
-                                 ((int64_t)(y.r * a.n_new + vi / a.g) * a.n_q_heads + y.h * a.g + vi % a.g) * D;
-        load_pair(q + j0, x0[v]);
-        load_pair(q + j0 + D / 2, x1[v]);
+      for (int i = 0; i < TOK * RC / 32; ++i) {
+        const int key = (i * 32 + lane) / RC, c = (i * 32 + lane) % RC;
+        const int kr = __shfl_sync(kAll, row[i * 32 / RC / 32], key & 31);
+        const int64_t off = (int64_t)max(kr, 0) * stride + c * 16;
+        cp16(dk + key * RB + k_chunk<RC>(key, c) * 16, y.k + off, kr >= 0);
+        const int vr = v_row(key);
+        cp16(dv + vr * RB + v_chunk<RC>(vr, c) * 16, y.v + off, kr >= 0);
       }
     }
-    if constexpr (F::coded) {
-      load_half(ks + y.h * D + j0, k0);
-      load_half(ks + y.h * D + j0 + D / 2, k1);
-      load_half(kz + y.h * D + j0, z0);
-      load_half(kz + y.h * D + j0 + D / 2, z1);
-      mark_selected();                                 // its reads run beside those above
-    }
-    uint32_t* sq = reinterpret_cast<uint32_t*>(sm.slot[2]);   // not in flight yet
-    sscale = 1.f;
-    cst = 0.f;
-    float z[kVecs];
-#pragma unroll
-    for (int v = 0; v < kVecs; ++v) {
-      z[v] = 0.f;
-      if (y.vg * kVecs + v >= n_vec) {                 // warp-uniform: no such vector
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) sq[q_word<D>(v, lane + 32 * i)] = 0;
-        continue;
-      }
-      float mx = 0.f;
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const float q0 = x0[v][i] * a.scale, q1 = x1[v][i] * a.scale;
-        float r0 = q0, r1 = q1;
-        if (cs) {
-          const float2 t = cs[j0 + i];
-          r0 = q0 * t.x + q1 * t.y;
-          r1 = q1 * t.x - q0 * t.y;
-        }
-        if constexpr (F::coded) {
-          z[v] += r0 * z0[i] + r1 * z1[i];
-          r0 *= k0[i];
-          r1 *= k1[i];
-          mx = fmaxf(mx, fmaxf(fabsf(r0), fabsf(r1)));
-        }
-        x0[v][i] = r0;
-        x1[v][i] = r1;
-      }
-      float up = 1.f;
-      if constexpr (F::coded) {
-        // fp16 parts want the largest element near 2^12: a power of two apart
-        const uint32_t mb = __reduce_max_sync(kAll, __float_as_uint(mx));
-        const int e = min(max((int)(mb >> 23), 27), 230);
-        up = __uint_as_float((uint32_t)(266 - e) << 23);
-        if (v == gid) sscale = 16777216.f * __uint_as_float((uint32_t)(e - 12) << 23);   // 2^24 / up
-      }
-#pragma unroll
-      for (int i = 0; i < NP; ++i)
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const int ch = j0 + i + b * (D / 2);
-          float x = (b ? x1[v][i] : x0[v][i]) * up;
-          uint32_t w;
-          if constexpr (F::coded) {
-            if (ST == FUSE_U4_ASYM && (ch & 1)) x *= 0.0625f;   // odd codes sit 4 bits higher
-            const __half hi = __float2half_rn(x);
-            w = pack_half2(__half2float(hi), x - __half2float(hi));
-          } else {
-            const __nv_bfloat16 hi = __float2bfloat16_rn(x);
-            w = pack_bf16x2(__bfloat162float(hi), x - __bfloat162float(hi));
-          }
-          sq[q_word<D>(v, ch)] = w;
-        }
-    }
-    if constexpr (F::coded) {
-      // the eight sums over the lanes, halving the vectors a lane carries:
-      // vector gid ends up in its four lanes
-#pragma unroll
-      for (int n = 4; n > 0; n >>= 1) {
-        const bool upper = lane & (4 * n);
-#pragma unroll
-        for (int v = 0; v < n; ++v) {
-          const float give = upper ? z[v] : z[v + n];
-          z[v] = (upper ? z[v + n] : z[v]) + __shfl_xor_sync(kAll, give, 4 * n);
-        }
-      }
-      cst = z[0];
-      cst += __shfl_xor_sync(kAll, cst, 1);
-      cst += __shfl_xor_sync(kAll, cst, 2);
-    }
-    __syncwarp();
-#pragma unroll
-    for (int kk = 0; kk < KSTEP; ++kk)
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const uint32_t w0 = sq[q_word<D>(gid, q_channel<ST, D>(tig, kk, b, 0))];
-        const uint32_t w1 = sq[q_word<D>(gid, q_channel<ST, D>(tig, kk, b, 1))];
-        qa[kk][2 * b] = __byte_perm(w0, w1, 0x5410);          // row gid: high parts
-        qa[kk][2 * b + 1] = __byte_perm(w0, w1, 0x7632);      // row gid + 8: what is left
-      }
-  }
-
-  // ---- the keys ------------------------------------------------------------
-  float m = -INFINITY;                                 // vector gid
-  uint64_t l2 = 0, z2 = 0;                             // its sums (this lane's even, odd keys)
-  int ve = 0;                                          // exponent field of the largest value scale
-  float acc[MT][4];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-
-  auto step = [&](int s, uint16_t (&szr)[2]) {
-    cp_wait<1>();                                      // slot s has landed
-    __syncwarp();                                      // ... for every lane; slot s - 1 is done with
-    const uint32_t sz = (uint32_t)szr[0] | (uint32_t)szr[1] << 16;
-    load_sz(issue(s + 2), szr[0], szr[1]);
     cp_commit();
-    const uint8_t* kb = sm.slot[s % kSlots];
-    const uint8_t* vb = kb + TOK * RB;
-    const int bit0 = s * TOK;
-    const uint32_t keep = sm.keep[s % kSlots] & ~(sm.skip[bit0 >> 5] >> (bit0 & 31));
-    bool raise = false;
-    float fe = 1.f;                                    // factor of a raised normaliser
-    if constexpr (F::coded) {
-      sm.sz[lane] = keep >> lane & 1 ? sz : 0u;        // whatever a key not seen holds
-      const uint32_t top = __reduce_max_sync(kAll, (keep >> lane & 1) ? sz & 0x7fffu : 0u);
-      const int e = min((int)(top >> 10), 30);
-      if (e > ve) {                                    // warp-uniform
-        fe = __uint_as_float((uint32_t)max(127 + ve - e, 1) << 23);
-        ve = e;
-        raise = true;
+    ++slot;
+    buf ^= 1;
+    load_id();
+  }
+  // Marks the selected keys of the item, a bit each, and corrects the words of
+  // keys to be seen of slot 0 where it is on its way.
+  __device__ __forceinline__ void mark_selected() {
+    sm.skip[lane] = 0;
+    __syncwarp();
+    if (y.n_skip > 0) {
+      const int p0 = y.pos0 + y.t0, p1 = y.pos0 + y.t1;
+      for (int i = warp_lower_bound(y.skip, y.n_skip, p0);; i += 32) {
+        const int v = i + lane < y.n_skip ? y.skip[i + lane] : p1;
+        const bool in = v >= p0 && v < p1;
+        if (in) atomicOr(&sm.skip[(v - p0) >> 5], 1u << ((v - p0) & 31));
+        if (!__all_sync(kAll, in)) break;
       }
       __syncwarp();
+      if (lane < F::ROWS && slot == 1) sm.keep[0][lane] &= ~sm.skip[lane];
     }
-    // scores: S^T rows gid (+ 8: low parts), keys 2 tig, 2 tig + 1 of each 8
+    __syncwarp();
+  }
+};
+
+// The item's query vectors, turned back by the chunk's angles (cs, NULL: not
+// turned) and scaled, as operand registers: q[kk][b] holds the channel pair
+// of half b of K-step kk of vector gid, its high parts, and q[kk][2 + b] what
+// is left of them.  Beside codes: score = sum * sscale + cst (vector gid).
+// Staged in the second buffer, which is not in flight yet.
+template <int ST, int D>
+__device__ __forceinline__ void load_query(const AttendArgs& a, const Item& y, const float2* cs,
+                                           const __half* ks, const __half* kz, Feed<ST, D>& feed,
+                                           uint32_t (&qo)[D / 16][4], float& sscale, float& cst) {
+  using F = Fmt<ST, D>;
+  constexpr uint32_t kAll = 0xffffffffu;
+  const int lane = threadIdx.x % 32, gid = lane >> 2, tig = lane & 3;
+      // a lane's channel pairs (j, j + D / 2): j = NP lane .. NP lane + NP - 1
+      constexpr int NP = D / 64;
+      const int n_vec = a.g * a.n_new, j0 = NP * lane;
+      auto load_pair = [](const __nv_bfloat16* p, float (&x)[NP]) {
+        if constexpr (NP == 2) {
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+          x[0] = bf16_lo(w);
+          x[1] = bf16_hi(w);
+        } else {
+          x[0] = __bfloat162float(*p);
+        }
+      };
+      auto load_half = [](const __half* p, float (&x)[NP]) {
+  #pragma unroll
+        for (int i = 0; i < NP; ++i) x[i] = __half2float(p[i]);
+      };
+      float x0[kVecs][NP], x1[kVecs][NP], k0[NP], k1[NP], z0[NP], z1[NP];
+  #pragma unroll
+      for (int v = 0; v < kVecs; ++v) {
+        const int vi = y.vg * kVecs + v;
+  #pragma unroll
+        for (int i = 0; i < NP; ++i) x0[v][i] = x1[v][i] = 0.f;
+        if (vi < n_vec) {                                // warp-uniform
+          const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.Q) +
+                                   ((int64_t)(y.r * a.n_new + vi / a.g) * a.n_q_heads + y.h * a.g + vi % a.g) * D;
+          load_pair(q + j0, x0[v]);
+          load_pair(q + j0 + D / 2, x1[v]);
+        }
+      }
+      if constexpr (F::coded) {
+        load_half(ks + y.h * D + j0, k0);
+        load_half(ks + y.h * D + j0 + D / 2, k1);
+        load_half(kz + y.h * D + j0, z0);
+        load_half(kz + y.h * D + j0 + D / 2, z1);
+        feed.mark_selected();                            // its reads run beside those above
+      }
+      uint32_t* sq = reinterpret_cast<uint32_t*>(feed.sm.slot[1]);
+      sscale = 1.f;
+      cst = 0.f;
+      float z[kVecs];
+  #pragma unroll
+      for (int v = 0; v < kVecs; ++v) {
+        z[v] = 0.f;
+        if (y.vg * kVecs + v >= n_vec) {                 // warp-uniform: no such vector
+  #pragma unroll
+          for (int i = 0; i < D / 32; ++i) sq[q_word<D>(v, lane + 32 * i)] = 0;
+          continue;
+        }
+        float mx = 0.f;
+  #pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const float q0 = x0[v][i] * a.scale, q1 = x1[v][i] * a.scale;
+          float r0 = q0, r1 = q1;
+          if (cs) {
+            const float2 t = cs[j0 + i];
+            r0 = q0 * t.x + q1 * t.y;
+            r1 = q1 * t.x - q0 * t.y;
+          }
+          if constexpr (F::coded) {
+            z[v] += r0 * z0[i] + r1 * z1[i];
+            r0 *= k0[i];
+            r1 *= k1[i];
+            mx = fmaxf(mx, fmaxf(fabsf(r0), fabsf(r1)));
+          }
+          x0[v][i] = r0;
+          x1[v][i] = r1;
+        }
+        float up = 1.f;
+        if constexpr (F::coded) {
+          // fp16 parts want the largest element near 2^12: a power of two apart
+          const uint32_t mb = __reduce_max_sync(kAll, __float_as_uint(mx));
+          const int e = min(max((int)(mb >> 23), 27), 230);
+          up = __uint_as_float((uint32_t)(266 - e) << 23);
+          if (v == gid) sscale = 16777216.f * __uint_as_float((uint32_t)(e - 12) << 23);   // 2^24 / up
+        }
+  #pragma unroll
+        for (int i = 0; i < NP; ++i)
+  #pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const int ch = j0 + i + b * (D / 2);
+            float x = (b ? x1[v][i] : x0[v][i]) * up;
+            uint32_t w;
+            if constexpr (F::coded) {
+              if (ST == FUSE_U4_ASYM && (ch & 1)) x *= 0.0625f;   // odd codes sit 4 bits higher
+              const __half hi = __float2half_rn(x);
+              w = pack_half2(__half2float(hi), x - __half2float(hi));
+            } else {
+              const __nv_bfloat16 hi = __float2bfloat16_rn(x);
+              w = pack_bf16x2(__bfloat162float(hi), x - __bfloat162float(hi));
+            }
+            sq[q_word<D>(v, ch)] = w;
+          }
+      }
+      if constexpr (F::coded) {
+        // the eight sums over the lanes, halving the vectors a lane carries:
+        // vector gid ends up in its four lanes
+  #pragma unroll
+        for (int n = 4; n > 0; n >>= 1) {
+          const bool upper = lane & (4 * n);
+  #pragma unroll
+          for (int v = 0; v < n; ++v) {
+            const float give = upper ? z[v] : z[v + n];
+            z[v] = (upper ? z[v + n] : z[v]) + __shfl_xor_sync(kAll, give, 4 * n);
+          }
+        }
+        cst = z[0];
+        cst += __shfl_xor_sync(kAll, cst, 1);
+        cst += __shfl_xor_sync(kAll, cst, 2);
+      }
+      __syncwarp();
+  #pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+  #pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const uint32_t w0 = sq[q_word<D>(gid, q_channel<ST, D>(tig, kk, b, 0))];
+          const uint32_t w1 = sq[q_word<D>(gid, q_channel<ST, D>(tig, kk, b, 1))];
+          qo[kk][b] = __byte_perm(w0, w1, 0x5410);
+          qo[kk][2 + b] = __byte_perm(w0, w1, 0x7632);
+        }
+}
+
+// An item of codes.
+//   S = K Q^T     A = codes (rows: 16 keys), B = the vectors' high parts, then
+//                 what is left of them
+//   O^T += V^T P  A = codes (rows: 16 channels, 16 keys), B = P, which comes
+//                 from S by a transposed 8 x 8 move
+// so a lane's scores, sums and outputs belong to vectors 2 tig and 2 tig + 1.
+template <int ST, int D>
+__device__ __forceinline__ void attend_codes(const AttendArgs& a, const Item& y, const float2* cs,
+                                             const __half* ks, const __half* kz, WarpSmem<D>& sm) {
+  using F = Fmt<ST, D>;
+  constexpr int RB = F::RB, RC = F::RC, TOK = F::TOK, NT = TOK / 8, MT = D / 16;
+  constexpr uint32_t kAll = 0xffffffffu;
+  const int lane = threadIdx.x % 32, gid = lane >> 2, tig = lane & 3;
+  const int n_slots = (y.t1 - y.t0 + TOK - 1) / TOK;
+  Feed<ST, D> feed(a, y, sm);
+  // scale and zero of a slot's values: read when it is copied, looked at when used
+  uint16_t vs[F::ROWS], vz[F::ROWS];
+  auto load_sz = [&]() {
+#pragma unroll
+    for (int r = 0; r < F::ROWS; ++r) {
+      vs[r] = vz[r] = 0;
+      if (feed.row[r] >= 0) {
+        const int64_t at = (int64_t)feed.row[r] * a.n_kv_heads;
+        vs[r] = reinterpret_cast<const uint16_t*>(y.vs)[at];
+        vz[r] = reinterpret_cast<const uint16_t*>(y.vz)[at];
+      }
+    }
+  };
+  feed.template copy<false>();
+  load_sz();
+  uint32_t q[D / 16][4];
+  uint64_t ss, sb;                                     // sscale and cst of the lane's two vectors
+  {
+    float s1, c1;
+    load_query<ST, D>(a, y, cs, ks, kz, feed, q, s1, c1);
+    ss = pack2(__shfl_sync(kAll, s1, tig * 8), __shfl_sync(kAll, s1, tig * 8 + 4));
+    sb = pack2(__shfl_sync(kAll, c1, tig * 8), __shfl_sync(kAll, c1, tig * 8 + 4));
+  }
+
+  float m0 = -INFINITY, m1 = -INFINITY;                // running maxima
+  uint64_t l2 = 0, z2 = 0;                             // sums over the lane's keys
+  int ve = 0;                                          // exponent field of the largest value scale
+  uint64_t acc[MT][2];                                 // channel rows gid and gid + 8
+#pragma unroll
+  for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = 0;
+
+#pragma unroll 1
+  for (int s = 0; s < n_slots; ++s) {
+    cp_wait<0>();                                      // the slot has landed
+    __syncwarp();                                      // ... for every lane; the one before is done with
+    uint32_t keep[F::ROWS], top = 0;
+    bool full = true;
+#pragma unroll
+    for (int r = 0; r < F::ROWS; ++r) {
+      keep[r] = sm.keep[s & 1][r];
+      full = full && keep[r] == F::kFull;
+      // 0 for a key not seen, whatever it holds
+      const uint32_t w = keep[r] >> lane & 1 ? (uint32_t)vs[r] | (uint32_t)vz[r] << 16 : 0u;
+      sm.sz[r * 32 + lane] = w;
+      top = max(top, w & 0x7fffu);
+    }
+    if (s + 1 < n_slots) {
+      feed.template copy<true>();
+      load_sz();
+    }
+    top = __reduce_max_sync(kAll, top);
+    __syncwarp();
+    const uint8_t* kb = sm.slot[s & 1] + gid * RB;
+    const uint8_t* vb = sm.slot[s & 1] + TOK * RB;
+    float fe = 1.f;                                    // factor of a raised normaliser
+    const int e = min((int)(top >> 10), 30);
+    const bool raise = e > ve;                         // warp-uniform
+    if (raise) {
+      fe = __uint_as_float((uint32_t)max(127 + ve - e, 1) << 23);
+      ve = e;
+    }
+    // scores of keys 8 n + gid; 16 keys form two chains (high parts and rest)
+    // of D / 16 dependent products
     uint64_t sc[NT];                                   // before sscale and cst
-    // eight keys at a time form a chain of D / 16 dependent products; two such
-    // groups, each in two chains, run side by side
-    constexpr int NP2 = NT < 2 ? NT : 2;
 #pragma unroll
-    for (int nt0 = 0; nt0 < NT; nt0 += NP2) {
-      float c[NP2][2][4];
+    for (int p = 0; p < NT / 2; ++p) {
+      float c[2][4];
 #pragma unroll
-      for (int p = 0; p < NP2; ++p)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) c[p][e >> 2][e & 3] = 0.f;
+      for (int i = 0; i < 8; ++i) c[i >> 2][i & 3] = 0.f;
+      const uint8_t* kr = kb + p * 16 * RB;
       if constexpr (ST == FUSE_U4_ASYM) {
-        uint32_t w[NP2][D / 32];
+        uint32_t w[2][D / 32];
 #pragma unroll
-        for (int p = 0; p < NP2; ++p) {
-          const uint8_t* kr = kb + ((nt0 + p) * 8 + gid) * RB;
+        for (int r = 0; r < 2; ++r) {
           if constexpr (D == 128) {
-            const uint4 x = *reinterpret_cast<const uint4*>(kr + tig * 16);
-            w[p][0] = x.x; w[p][1] = x.y; w[p][2] = x.z; w[p][3] = x.w;
+            const uint4 x = *reinterpret_cast<const uint4*>(kr + r * 8 * RB + tig * 16);
+            w[r][0] = x.x; w[r][1] = x.y; w[r][2] = x.z; w[r][3] = x.w;
           } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(kr + tig * 8);
-            w[p][0] = x.x; w[p][1] = x.y;
+            const uint2 x = *reinterpret_cast<const uint2*>(kr + r * 8 * RB + tig * 8);
+            w[r][0] = x.x; w[r][1] = x.y;
           }
         }
 #pragma unroll
         for (int j = 0; j < D / 32; ++j)
 #pragma unroll
-          for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int p = 0; p < NP2; ++p) {
-              const uint32_t u = b ? w[p][j] >> 8 : w[p][j];
-              mma16<true>(c[p][b], qa[2 * j + b][0], qa[2 * j + b][1], qa[2 * j + b][2],
-                          qa[2 * j + b][3], u & 0x000f000fu, u & 0x00f000f0u);
-            }
-      } else {
-        constexpr int CH = RC / 4;                     // 16-byte chunks of a lane
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          uint32_t w[NP2][4];
-#pragma unroll
-          for (int p = 0; p < NP2; ++p) {
-            const int key = (nt0 + p) * 8 + gid;
-            const uint4 x = *reinterpret_cast<const uint4*>(kb + key * RB + k_chunk<RC>(key, i * 4 + tig) * 16);
-            w[p][0] = x.x; w[p][1] = x.y; w[p][2] = x.z; w[p][3] = x.w;
+          for (int b = 0; b < 2; ++b) {
+            const uint32_t u = b ? w[0][j] >> 8 : w[0][j], v = b ? w[1][j] >> 8 : w[1][j];
+            const uint32_t a0 = u & 0x000f000fu, a1 = v & 0x000f000fu, a2 = u & 0x00f000f0u,
+                           a3 = v & 0x00f000f0u;
+            mma16<true>(c[0], a0, a1, a2, a3, q[2 * j + b][0], q[2 * j + b][1]);
+            mma16<true>(c[1], a0, a1, a2, a3, q[2 * j + b][2], q[2 * j + b][3]);
           }
-          if constexpr (ST == FUSE_U8_ASYM) {
+      } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+        for (int i = 0; i < RC / 4; ++i) {             // 16-byte chunks of a lane
+          uint32_t w[2][4];
 #pragma unroll
-              for (int p = 0; p < NP2; ++p) {
-                const int kk = i * 4 + j;
-                mma16<true>(c[p][j & 1], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3],
-                            __byte_perm(w[p][j], 0, 0x4140), __byte_perm(w[p][j], 0, 0x4342));
-              }
-          } else {
+          for (int r = 0; r < 2; ++r) {
+            const uint4 x = *reinterpret_cast<const uint4*>(kr + r * 8 * RB + k_chunk<RC>(gid, i * 4 + tig) * 16);
+            w[r][0] = x.x; w[r][1] = x.y; w[r][2] = x.z; w[r][3] = x.w;
+          }
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-              for (int p = 0; p < NP2; ++p) {
-                const int kk = i * 2 + j;
-                mma16<false>(c[p][j], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], w[p][2 * j],
-                             w[p][2 * j + 1]);
-              }
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t a0 = __byte_perm(w[0][j], 0, 0x4140), a1 = __byte_perm(w[1][j], 0, 0x4140),
+                           a2 = __byte_perm(w[0][j], 0, 0x4342), a3 = __byte_perm(w[1][j], 0, 0x4342);
+            mma16<true>(c[0], a0, a1, a2, a3, q[i * 4 + j][0], q[i * 4 + j][1]);
+            mma16<true>(c[1], a0, a1, a2, a3, q[i * 4 + j][2], q[i * 4 + j][3]);
           }
         }
       }
-#pragma unroll
-      for (int p = 0; p < NP2; ++p)
-        sc[nt0 + p] = add2(add2(pack2(c[p][0][0], c[p][0][1]), pack2(c[p][1][0], c[p][1][1])),
-                           add2(pack2(c[p][0][2], c[p][0][3]), pack2(c[p][1][2], c[p][1][3])));
+      sc[2 * p] = add2(pack2(c[0][0], c[0][1]), pack2(c[1][0], c[1][1]));
+      sc[2 * p + 1] = add2(pack2(c[0][2], c[0][3]), pack2(c[1][2], c[1][3]));
     }
-    const uint32_t mine = keep >> (2 * tig);           // bits 8 nt, 8 nt + 1: this lane's keys
-    if (keep != (uint32_t)((1ull << TOK) - 1)) {       // warp-uniform
+    if (!full) {                                       // warp-uniform
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float2 x = unpack2(sc[nt]);
-        if (!(mine >> (8 * nt) & 1)) x.x = -INFINITY;
-        if (!(mine >> (8 * nt + 1) & 1)) x.y = -INFINITY;
-        sc[nt] = pack2(x.x, x.y);
+      for (int n = 0; n < NT; ++n)
+        if (!(keep[n / 4] >> (8 * (n & 3) + gid) & 1)) sc[n] = pack2(-INFINITY, -INFINITY);
+    }
+    float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float2 t = unpack2(sc[n]);
+      x0 = fmaxf(x0, t.x);
+      x1 = fmaxf(x1, t.y);
+    }
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      x0 = fmaxf(x0, __shfl_xor_sync(kAll, x0, o));
+      x1 = fmaxf(x1, __shfl_xor_sync(kAll, x1, o));
+    }
+    {
+      const float2 f = unpack2(ss), g = unpack2(sb);
+      if (x0 != -INFINITY) x0 = fmaf(x0, f.x, g.x);
+      if (x1 != -INFINITY) x1 = fmaf(x1, f.y, g.y);
+    }
+    const bool up0 = x0 > m0 + kRaise, up1 = x1 > m1 + kRaise;
+    if (__any_sync(kAll, up0 || up1) || raise) {
+      const uint64_t al = pack2((up0 ? ex2(m0 - x0) : 1.f) * fe, (up1 ? ex2(m1 - x1) : 1.f) * fe);
+      if (up0) m0 = x0;                                // (the factor is 0 at the first key)
+      if (up1) m1 = x1;
+      l2 = mul2(l2, al);
+      z2 = mul2(z2, al);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        acc[i][0] = mul2(acc[i][0], al);
+        acc[i][1] = mul2(acc[i][1], al);
       }
     }
-    float mt = -INFINITY;
+    // weights, sums, and what multiplies the values; all carry the factor
+    // 2^(20 - ve), with which a scale stays below 2^6
+    const float lift = (float)(20 - ve);
+    const uint64_t b2 =
+        add2(sb, pack2(lift - (m0 == -INFINITY ? 0.f : m0), lift - (m1 == -INFINITY ? 0.f : m1)));
+    uint32_t ph[NT];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const float2 x = unpack2(sc[nt]);
-      mt = fmaxf(mt, fmaxf(x.x, x.y));
+    for (int n = 0; n < NT; ++n) {
+      const float2 x = unpack2(fma2(sc[n], ss, b2));
+      const uint64_t p = pack2(ex2(x.x), ex2(x.y));
+      l2 = add2(l2, p);
+      const uint32_t w = sm.sz[n * 8 + gid];
+      const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w));
+      z2 = fma2(p, pack2(t.y, t.y), z2);
+      const float2 v = unpack2(mul2(p, pack2(t.x, t.x)));
+      ph[n] = transpose8x8(pack_half2(v.x, v.y));
     }
+    // O^T += V^T P
+    constexpr int VB = RB / 8;                         // bytes of a row that a lane takes
+#pragma unroll
+    for (int g2 = 0; g2 < TOK / 16; ++g2) {
+      uint32_t w[4][VB / 4];                           // keys 2 tig, 2 tig + 1, 8 + 2 tig, 9 + 2 tig
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int vr = g2 * 16 + (k >> 1) * 8 + (k & 1) * 4 + tig;
+        const uint8_t* p = vb + vr * RB + v_chunk<RC>(vr, gid * VB / 16) * 16 + gid * VB % 16;
+        if constexpr (VB == 16) {
+          const uint4 x = *reinterpret_cast<const uint4*>(p);
+          w[k][0] = x.x; w[k][1] = x.y; w[k][2] = x.z; w[k][3] = x.w;
+        } else if constexpr (VB == 8) {
+          const uint2 x = *reinterpret_cast<const uint2*>(p);
+          w[k][0] = x.x; w[k][1] = x.y;
+        } else {
+          w[k][0] = *reinterpret_cast<const uint32_t*>(p);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < VB / 4; ++j)
+#pragma unroll
+        for (int hi = 0; hi < 2; ++hi) {
+          const uint32_t u = __byte_perm(w[0][j], w[1][j], hi ? 0x7632 : 0x5410);
+          const uint32_t v = __byte_perm(w[2][j], w[3][j], hi ? 0x7632 : 0x5410);
+          if constexpr (ST == FUSE_U4_ASYM) {
+            mma16p(acc[j * 4 + hi * 2], u & 0x000f000fu, u & 0x00f000f0u, v & 0x000f000fu, v & 0x00f000f0u,
+                   ph[2 * g2], ph[2 * g2 + 1]);
+            const uint32_t us = u >> 8, vs = v >> 8;
+            mma16p(acc[j * 4 + hi * 2 + 1], us & 0x000f000fu, us & 0x00f000f0u, vs & 0x000f000fu,
+                   vs & 0x00f000f0u, ph[2 * g2], ph[2 * g2 + 1]);
+          } else {
+            mma16p(acc[j * 2 + hi], u & 0x00ff00ffu, (u >> 8) & 0x00ff00ffu, v & 0x00ff00ffu,
+                   (v >> 8) & 0x00ff00ffu, ph[2 * g2], ph[2 * g2 + 1]);
+          }
+        }
+    }
+  }
+
+  // ---- the item's partial ----------------------------------------------------
+  const float vu = __uint_as_float((uint32_t)(127 + ve - 20) << 23);
+  float2 l = unpack2(mul2(l2, pack2(vu, vu))), z = unpack2(mul2(z2, pack2(vu, vu)));
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) {
+    l.x += __shfl_xor_sync(kAll, l.x, o);
+    l.y += __shfl_xor_sync(kAll, l.y, o);
+    z.x += __shfl_xor_sync(kAll, z.x, o);
+    z.y += __shfl_xor_sync(kAll, z.y, o);
+  }
+  const int n_vec = min(kVecs, a.g * a.n_new - y.vg * kVecs);
+  const int64_t at = ((y.slot * a.n_kv_heads + y.h) * a.nvg + y.vg) * kVecs;
+  const float un = __uint_as_float((uint32_t)(127 + 24 - 20 + ve) << 23);
+  const float un1 = ST == FUSE_U4_ASYM ? un * 0.0625f : un;    // odd codes sit 4 bits higher
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int v = 2 * tig + e;
+    if (v >= n_vec) continue;
+    const float zv = e ? z.y : z.x;
+    if (gid == 0) a.part_ml[at + v] = make_float2(e ? m1 : m0, e ? l.y : l.x);
+    float* o = a.part_o + (at + v) * D + gid * (D / 8);
+#pragma unroll
+    for (int i = 0; i < MT; i += 2) {
+      const float2 r0 = unpack2(acc[i][0]), r1 = unpack2(acc[i][1]), r2 = unpack2(acc[i + 1][0]),
+                   r3 = unpack2(acc[i + 1][1]);
+      *reinterpret_cast<float4*>(o + 2 * i) =
+          e ? make_float4(fmaf(r0.y, un, zv), fmaf(r1.y, un1, zv), fmaf(r2.y, un, zv), fmaf(r3.y, un1, zv))
+            : make_float4(fmaf(r0.x, un, zv), fmaf(r1.x, un1, zv), fmaf(r2.x, un, zv), fmaf(r3.x, un1, zv));
+    }
+  }
+}
+
+// An item of bf16 rows.
+//   S^T = Q K^T   A = Q (rows 0-7: the vectors' high parts, 8-15: what is
+//                 left of them), B = 8 keys
+//   O^T += V^T P  A = values (rows: 16 channels, 8 keys), B = P in two parts;
+//                 the layout in which S^T comes out is the one P goes in
+// A lane's scores belong to vector gid, its outputs to 2 tig and 2 tig + 1.
+template <int D>
+__device__ __forceinline__ void attend_rows(const AttendArgs& a, const Item& y, const float2* cs,
+                                            WarpSmem<D>& sm) {
+  constexpr int ST = FUSE_BF16;
+  using F = Fmt<ST, D>;
+  constexpr int RB = F::RB, RC = F::RC, TOK = F::TOK, MT = D / 16;
+  constexpr uint32_t kAll = 0xffffffffu;
+  const int lane = threadIdx.x % 32, gid = lane >> 2, tig = lane & 3;
+  const int n_slots = (y.t1 - y.t0 + TOK - 1) / TOK;
+  Feed<ST, D> feed(a, y, sm);
+  feed.mark_selected();
+  feed.template copy<true>();
+  uint32_t q[D / 16][4];
+  float one, none;
+  load_query<ST, D>(a, y, cs, nullptr, nullptr, feed, q, one, none);
+  float m = -INFINITY, l = 0.f;                        // vector gid (its sum: this lane's keys)
+  float acc[MT][4];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll 1
+  for (int s = 0; s < n_slots; ++s) {
+    cp_wait<0>();                                      // the slot has landed
+    __syncwarp();                                      // ... for every lane; the one before is done with
+    const uint32_t keep = sm.keep[s & 1][0];
+    if (s + 1 < n_slots) feed.template copy<true>();
+    const uint8_t* kb = sm.slot[s & 1] + gid * RB;
+    const uint8_t* vb = sm.slot[s & 1] + TOK * RB;
+    float sc[2][2];                                    // keys 8 n + 2 tig, + 1
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      float c[2][4];                                   // two chains of products
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i >> 2][i & 3] = 0.f;
+#pragma unroll
+      for (int i = 0; i < RC / 4; ++i) {               // 16-byte chunks of a lane
+        const uint4 x =
+            *reinterpret_cast<const uint4*>(kb + n * 8 * RB + k_chunk<RC>(gid, i * 4 + tig) * 16);
+        mma16<false>(c[0], q[2 * i][0], q[2 * i][2], q[2 * i][1], q[2 * i][3], x.x, x.y);
+        mma16<false>(c[1], q[2 * i + 1][0], q[2 * i + 1][2], q[2 * i + 1][1], q[2 * i + 1][3], x.z, x.w);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        sc[n][e] = (c[0][e] + c[1][e]) + (c[0][2 + e] + c[1][2 + e]);
+        if (!(keep >> (8 * n + 2 * tig + e) & 1)) sc[n][e] = -INFINITY;
+      }
+    }
+    float mt = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
     mt = fmaxf(mt, __shfl_xor_sync(kAll, mt, 1));
     mt = fmaxf(mt, __shfl_xor_sync(kAll, mt, 2));
-    if constexpr (F::coded) mt = mt == -INFINITY ? mt : fmaf(mt, sscale, cst);
     const bool up = mt > m + kRaise;
-    if (__any_sync(kAll, up) || raise) {
-      const float al = (up ? ex2(m - mt) : 1.f) * fe;  // 0 at the first key
+    if (__any_sync(kAll, up)) {
+      const float al = up ? ex2(m - mt) : 1.f;         // 0 at the first key
       if (up) m = mt;
-      const uint64_t al2 = pack2(al, al);
-      l2 = mul2(l2, al2);
-      z2 = mul2(z2, al2);
+      l *= al;
       const float f0 = __shfl_sync(kAll, al, tig * 8), f1 = __shfl_sync(kAll, al, tig * 8 + 4);
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
@@ -561,124 +759,53 @@ __device__ __forceinline__ void attend_mma_item(const AttendArgs& a, const Item&
         acc[i][3] *= f1;
       }
     }
-    // weights, sums, and what multiplies the values; beside codes all carry
-    // the factor 2^(20 - ve), with which a scale stays below 2^6
-    const float ref = (m == -INFINITY ? 0.f : m) - (F::coded ? (float)(20 - ve) : 0.f);
-    const uint64_t a2 = pack2(sscale, sscale), b2 = pack2(cst - ref, cst - ref);
-    uint32_t ph[NT], pl[NT];
+    const float ref = m == -INFINITY ? 0.f : m;
+    uint32_t ph[2], pl[2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const float2 x = unpack2(F::coded ? fma2(sc[nt], a2, b2) : add2(sc[nt], b2));
-      const uint64_t p = pack2(ex2(x.x), ex2(x.y));
-      l2 = add2(l2, p);
-      if constexpr (F::coded) {
-        const uint2 w = *reinterpret_cast<const uint2*>(&sm.sz[nt * 8 + 2 * tig]);
-        const float2 s0 = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
-        const float2 s1 = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
-        z2 = fma2(p, pack2(s0.y, s1.y), z2);
-        const float2 v = unpack2(mul2(p, pack2(s0.x, s1.x)));
-        ph[nt] = pack_half2(v.x, v.y);
-      } else {
-        const float2 v = unpack2(p);
-        ph[nt] = pack_bf16x2(v.x, v.y);
-        pl[nt] = pack_bf16x2(v.x - bf16_lo(ph[nt]), v.y - bf16_hi(ph[nt]));
+    for (int n = 0; n < 2; ++n) {
+      const float p0 = ex2(sc[n][0] - ref), p1 = ex2(sc[n][1] - ref);
+      l += p0 + p1;
+      ph[n] = pack_bf16x2(p0, p1);
+      pl[n] = pack_bf16x2(p0 - bf16_lo(ph[n]), p1 - bf16_hi(ph[n]));
+    }
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      uint32_t w[4][4];                                // keys 2 tig, 2 tig + 1, 8 + 2 tig, 9 + 2 tig
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int vr = (k >> 1) * 8 + (k & 1) * 4 + tig;
+        const uint4 x = *reinterpret_cast<const uint4*>(vb + vr * RB + v_chunk<RC>(vr, i * 8 + gid) * 16);
+        w[k][0] = x.x; w[k][1] = x.y; w[k][2] = x.z; w[k][3] = x.w;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t a0 = __byte_perm(w[0][j], w[1][j], 0x5410), a1 = __byte_perm(w[0][j], w[1][j], 0x7632),
+                       a2 = __byte_perm(w[2][j], w[3][j], 0x5410), a3 = __byte_perm(w[2][j], w[3][j], 0x7632);
+        mma16<false>(acc[i * 4 + j], a0, a1, a2, a3, ph[0], ph[1]);
+        mma16<false>(acc[i * 4 + j], a0, a1, a2, a3, pl[0], pl[1]);
       }
     }
-    // O^T += V^T P
-    if constexpr (F::coded) {
-      constexpr int VB = RB / 8;                       // bytes of a row that a lane takes
-#pragma unroll
-      for (int g2 = 0; g2 < TOK / 16; ++g2) {
-        uint32_t w[4][VB / 4];                         // keys 2 tig, 2 tig + 1, 8 + 2 tig, 9 + 2 tig
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int vr = g2 * 16 + (k >> 1) * 8 + (k & 1) * 4 + tig;
-          const uint8_t* p = vb + vr * RB + v_chunk<RC>(vr, gid * VB / 16) * 16 + gid * VB % 16;
-          if constexpr (VB == 16) {
-            const uint4 x = *reinterpret_cast<const uint4*>(p);
-            w[k][0] = x.x; w[k][1] = x.y; w[k][2] = x.z; w[k][3] = x.w;
-          } else if constexpr (VB == 8) {
-            const uint2 x = *reinterpret_cast<const uint2*>(p);
-            w[k][0] = x.x; w[k][1] = x.y;
-          } else {
-            w[k][0] = *reinterpret_cast<const uint32_t*>(p);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < VB / 4; ++j)
-#pragma unroll
-          for (int hi = 0; hi < 2; ++hi) {
-            const uint32_t u = __byte_perm(w[0][j], w[1][j], hi ? 0x7632 : 0x5410);
-            const uint32_t v = __byte_perm(w[2][j], w[3][j], hi ? 0x7632 : 0x5410);
-            if constexpr (ST == FUSE_U4_ASYM) {
-              mma16<true>(acc[j * 4 + hi * 2], u & 0x000f000fu, u & 0x00f000f0u, v & 0x000f000fu,
-                          v & 0x00f000f0u, ph[2 * g2], ph[2 * g2 + 1]);
-              const uint32_t us = u >> 8, vs = v >> 8;
-              mma16<true>(acc[j * 4 + hi * 2 + 1], us & 0x000f000fu, us & 0x00f000f0u, vs & 0x000f000fu,
-                          vs & 0x00f000f0u, ph[2 * g2], ph[2 * g2 + 1]);
-            } else {
-              mma16<true>(acc[j * 2 + hi], u & 0x00ff00ffu, (u >> 8) & 0x00ff00ffu, v & 0x00ff00ffu,
-                          (v >> 8) & 0x00ff00ffu, ph[2 * g2], ph[2 * g2 + 1]);
-            }
-          }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < D / 64; ++i) {
-        uint32_t w[2][4];                              // keys 2 tig, 2 tig + 1
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int vr = k * 4 + tig;
-          const uint4 x = *reinterpret_cast<const uint4*>(vb + vr * RB + v_chunk<RC>(vr, i * 8 + gid) * 16);
-          w[k][0] = x.x; w[k][1] = x.y; w[k][2] = x.z; w[k][3] = x.w;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t u = __byte_perm(w[0][j], w[1][j], 0x5410), v = __byte_perm(w[0][j], w[1][j], 0x7632);
-          mma8_bf16(acc[i * 4 + j], u, v, ph[0]);
-          mma8_bf16(acc[i * 4 + j], u, v, pl[0]);
-        }
-      }
-    }
-  };
-#pragma unroll 1
-  for (int s = 0; s < n_slots; s += 2) {
-    step(s, sz0);
-    if (s + 1 < n_slots) step(s + 1, sz1);
   }
-  cp_wait<0>();                                        // nothing in flight when the buffers go
 
-  // ---- the item's partial ----------------------------------------------------
-  const float vu = F::coded ? __uint_as_float((uint32_t)(127 + ve - 20) << 23) : 1.f;
-  const float2 lp = unpack2(l2), zp = unpack2(z2);
-  float l = (lp.x + lp.y) * vu, zs = (zp.x + zp.y) * vu;
   l += __shfl_xor_sync(kAll, l, 1);
   l += __shfl_xor_sync(kAll, l, 2);
-  zs += __shfl_xor_sync(kAll, zs, 1);
-  zs += __shfl_xor_sync(kAll, zs, 2);
   const int n_vec = min(kVecs, a.g * a.n_new - y.vg * kVecs);
   const int64_t at = ((y.slot * a.n_kv_heads + y.h) * a.nvg + y.vg) * kVecs;
   if (tig == 0 && gid < n_vec) a.part_ml[at + gid] = make_float2(m, l);
-  const float un = F::coded ? __uint_as_float((uint32_t)(127 + 24 - 20 + ve) << 23) : 1.f;
-  const float un1 = ST == FUSE_U4_ASYM ? un * 0.0625f : un;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int v = 2 * tig + e;
-    const float z = __shfl_sync(kAll, zs, v * 4);
     if (v >= n_vec) continue;
-    float* o = a.part_o + (at + v) * D;
+    float* o = a.part_o + (at + v) * D + gid * 8;
 #pragma unroll
-    for (int i = 0; i < MT; i += 2) {
-      const int ch = F::coded ? gid * (D / 8) + 2 * i : ((i >> 2) * 8 + gid) * 8 + 2 * (i & 3);
-      *reinterpret_cast<float4*>(o + ch) =
-          make_float4(fmaf(acc[i][e], un, z), fmaf(acc[i][2 + e], un1, z), fmaf(acc[i + 1][e], un, z),
-                      fmaf(acc[i + 1][2 + e], un1, z));
-    }
+    for (int i = 0; i < MT; i += 2)
+      *reinterpret_cast<float4*>(o + (i >> 2) * 64 + 2 * (i & 3)) =
+          make_float4(acc[i][e], acc[i][2 + e], acc[i + 1][e], acc[i + 1][2 + e]);
   }
 }
 
 template <int ST, int D>
-__global__ void __launch_bounds__(kWarps * 32, 2)
+__global__ void __launch_bounds__(kWarps * 32, 3)
     attend_mma_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ ChunkOwners owners,
                       const __grid_constant__ RopeFreqs f, int side_ctas, int n_side_ctas) {
   extern __shared__ __align__(16) uint8_t raw[];
@@ -716,7 +843,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
           report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_ATTEND_SEL, (uint32_t)t);
       }
     }
-    attend_mma_item<FUSE_BF16, D>(a, y, nullptr, nullptr, nullptr, sm);
+    attend_rows<D>(a, y, nullptr, sm);
     return;
   }
   const int ctas = (a.nsub * per_seg + kWarps - 1) / kWarps;
@@ -766,8 +893,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   y.skip = a.idx + R.sel0;
   y.pos0 = (int)(C.dst_row - R.row0);
   y.slot = (int64_t)(a.chunk0 + ci) * a.nsub + seg;
-  attend_mma_item<ST, D>(a, y, C.pos != 0 ? s_cs : nullptr, reinterpret_cast<const __half*>(C.k_scale),
-                         reinterpret_cast<const __half*>(C.k_zero), sm);
+  const float2* cs = C.pos != 0 ? s_cs : nullptr;
+  if constexpr (ST == FUSE_BF16)
+    attend_rows<D>(a, y, cs, sm);
+  else
+    attend_codes<ST, D>(a, y, cs, reinterpret_cast<const __half*>(C.k_scale),
+                        reinterpret_cast<const __half*>(C.k_zero), sm);
 }
 
 template <int ST, int D>
