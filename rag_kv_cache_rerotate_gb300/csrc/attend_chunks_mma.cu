@@ -166,22 +166,54 @@ template <int D> __device__ __forceinline__ int q_word(int v, int ch) {
   return v * D + ((ch & ~31) | ((ch + 4 * v + (ch >> 5)) & 31));
 }
 
-// Lower bound of x in a[0, n), by all lanes of the warp, 32 probes at a time.
-__device__ __forceinline__ int warp_lower_bound(const int32_t* a, int n, int x) {
+// A place in ascending a[0, n) at most 64 before the first element >= x, by
+// all lanes of the warp, 256 probes a round (one round up to 16 384 elements).
+__device__ __forceinline__ int warp_search(const int32_t* a, int n, int x) {
   const int lane = threadIdx.x % 32;
   int lo = 0, len = n;                                 // the answer is in [lo, lo + len]
-  while (len > 0) {
-    const int step = (len + 31) / 32;
-    const int i = lo + (lane + 1) * step - 1;          // last element of the lane's part
-    const bool below = i < lo + len ? a[i] < x : false;
-    const int parts = __popc(__ballot_sync(0xffffffffu, below));
+  while (len > 64) {
+    const int step = (len + 255) / 256;
+    bool below[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {                      // last elements of 256 parts
+      const int i = lo + (j * 32 + lane + 1) * step - 1;
+      below[j] = i < lo + len ? a[i] < x : false;
+    }
+    int parts = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) parts += __popc(__ballot_sync(0xffffffffu, below[j]));
     // parts whose last element is below x are skipped whole
-    const int skip = parts * step;
-    lo += skip;
-    len = min(step - 1, len - skip);
-    if (len < 0) len = 0;
+    lo += parts * step;
+    len = min(step - 1, len - parts * step);
   }
   return lo;
+}
+
+// The query vectors of an item as they are: the lane's channel pairs
+// (j, j + D / 2), j = NP lane .. NP lane + NP - 1, NP = D / 64 to a register.
+struct RawQuery {
+  uint32_t lo[kVecs], hi[kVecs];
+};
+template <int D>
+__device__ __forceinline__ void read_query(const AttendArgs& a, int r, int h, int vg, RawQuery& x) {
+  constexpr int NP = D / 64;
+  const int lane = threadIdx.x % 32, n_vec = a.g * a.n_new;
+#pragma unroll
+  for (int v = 0; v < kVecs; ++v) {
+    const int vi = vg * kVecs + v;
+    x.lo[v] = x.hi[v] = 0;
+    if (vi < n_vec) {                                  // warp-uniform
+      const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.Q) + NP * lane +
+                               ((int64_t)(r * a.n_new + vi / a.g) * a.n_q_heads + h * a.g + vi % a.g) * D;
+      if constexpr (NP == 2) {
+        x.lo[v] = *reinterpret_cast<const uint32_t*>(q);
+        x.hi[v] = *reinterpret_cast<const uint32_t*>(q + D / 2);
+      } else {
+        x.lo[v] = *reinterpret_cast<const uint16_t*>(q);
+        x.hi[v] = *reinterpret_cast<const uint16_t*>(q + D / 2);
+      }
+    }
+  }
 }
 
 // The keys of an item on their way to shared memory: slots of TOK keys in two
@@ -291,11 +323,17 @@ template <int ST, int D> struct Feed {
     __syncwarp();
     if (y.n_skip > 0) {
       const int p0 = y.pos0 + y.t0, p1 = y.pos0 + y.t1;
-      for (int i = warp_lower_bound(y.skip, y.n_skip, p0);; i += 32) {
-        const int v = i + lane < y.n_skip ? y.skip[i + lane] : p1;
-        const bool in = v >= p0 && v < p1;
-        if (in) atomicOr(&sm.skip[(v - p0) >> 5], 1u << ((v - p0) & 31));
-        if (!__all_sync(kAll, in)) break;
+      for (int i = warp_search(y.skip, y.n_skip, p0);; i += 128) {
+        int v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int k = i + j * 32 + lane;
+          v[j] = k < y.n_skip ? y.skip[k] : INT32_MAX;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (v[j] >= p0 && v[j] < p1) atomicOr(&sm.skip[(v[j] - p0) >> 5], 1u << ((v[j] - p0) & 31));
+        if (__any_sync(kAll, v[3] >= p1)) break;
       }
       __syncwarp();
       if (lane < F::ROWS && slot == 1) sm.keep[0][lane] &= ~sm.skip[lane];
@@ -305,136 +343,116 @@ template <int ST, int D> struct Feed {
 };
 
 // The item's query vectors, turned back by the chunk's angles (cs, NULL: not
-// turned) and scaled, as operand registers: q[kk][b] holds the channel pair
-// of half b of K-step kk of vector gid, its high parts, and q[kk][2 + b] what
+// turned) and scaled, as operand registers: qo[kk][b] holds the channel pair
+// of half b of K-step kk of vector gid, its high parts, and qo[kk][2 + b] what
 // is left of them.  Beside codes: score = sum * sscale + cst (vector gid).
 // Staged in the second buffer, which is not in flight yet.
 template <int ST, int D>
-__device__ __forceinline__ void load_query(const AttendArgs& a, const Item& y, const float2* cs,
-                                           const __half* ks, const __half* kz, Feed<ST, D>& feed,
-                                           uint32_t (&qo)[D / 16][4], float& sscale, float& cst) {
+__device__ __forceinline__ void load_query(const AttendArgs& a, const Item& y, const RawQuery& raw,
+                                           const float2* cs, const __half* ks, const __half* kz,
+                                           Feed<ST, D>& feed, uint32_t (&qo)[D / 16][4],
+                                           float& sscale, float& cst) {
   using F = Fmt<ST, D>;
   constexpr uint32_t kAll = 0xffffffffu;
+  constexpr int NP = D / 64;
   const int lane = threadIdx.x % 32, gid = lane >> 2, tig = lane & 3;
-      // a lane's channel pairs (j, j + D / 2): j = NP lane .. NP lane + NP - 1
-      constexpr int NP = D / 64;
-      const int n_vec = a.g * a.n_new, j0 = NP * lane;
-      auto load_pair = [](const __nv_bfloat16* p, float (&x)[NP]) {
-        if constexpr (NP == 2) {
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-          x[0] = bf16_lo(w);
-          x[1] = bf16_hi(w);
-        } else {
-          x[0] = __bfloat162float(*p);
-        }
-      };
-      auto load_half = [](const __half* p, float (&x)[NP]) {
-  #pragma unroll
-        for (int i = 0; i < NP; ++i) x[i] = __half2float(p[i]);
-      };
-      float x0[kVecs][NP], x1[kVecs][NP], k0[NP], k1[NP], z0[NP], z1[NP];
-  #pragma unroll
-      for (int v = 0; v < kVecs; ++v) {
-        const int vi = y.vg * kVecs + v;
-  #pragma unroll
-        for (int i = 0; i < NP; ++i) x0[v][i] = x1[v][i] = 0.f;
-        if (vi < n_vec) {                                // warp-uniform
-          const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.Q) +
-                                   ((int64_t)(y.r * a.n_new + vi / a.g) * a.n_q_heads + y.h * a.g + vi % a.g) * D;
-          load_pair(q + j0, x0[v]);
-          load_pair(q + j0 + D / 2, x1[v]);
-        }
+  const int n_vec = a.g * a.n_new - y.vg * kVecs, j0 = NP * lane;
+  float k0[NP], k1[NP], z0[NP], z1[NP];
+  if constexpr (F::coded) {
+    ks += y.h * D + j0;
+    kz += y.h * D + j0;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      k0[i] = __half2float(ks[i]);
+      k1[i] = __half2float(ks[i + D / 2]);
+      z0[i] = __half2float(kz[i]);
+      z1[i] = __half2float(kz[i + D / 2]);
+    }
+    feed.mark_selected();                              // its reads run beside those above
+  }
+  uint32_t* sq = reinterpret_cast<uint32_t*>(feed.sm.slot[1]);
+  sscale = 1.f;
+  cst = 0.f;
+  float z[kVecs];
+#pragma unroll
+  for (int v = 0; v < kVecs; ++v) {
+    z[v] = 0.f;
+    if (v >= n_vec) {                                  // warp-uniform: no such vector
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) sq[q_word<D>(v, lane + 32 * i)] = 0;
+      continue;
+    }
+    float x[NP][2], mx = 0.f;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const float q0 = (i ? bf16_hi(raw.lo[v]) : bf16_lo(raw.lo[v])) * a.scale;
+      const float q1 = (i ? bf16_hi(raw.hi[v]) : bf16_lo(raw.hi[v])) * a.scale;
+      x[i][0] = q0;
+      x[i][1] = q1;
+      if (cs) {
+        const float2 t = cs[j0 + i];
+        x[i][0] = q0 * t.x + q1 * t.y;
+        x[i][1] = q1 * t.x - q0 * t.y;
       }
       if constexpr (F::coded) {
-        load_half(ks + y.h * D + j0, k0);
-        load_half(ks + y.h * D + j0 + D / 2, k1);
-        load_half(kz + y.h * D + j0, z0);
-        load_half(kz + y.h * D + j0 + D / 2, z1);
-        feed.mark_selected();                            // its reads run beside those above
+        z[v] += x[i][0] * z0[i] + x[i][1] * z1[i];
+        x[i][0] *= k0[i];
+        x[i][1] *= k1[i];
+        mx = fmaxf(mx, fmaxf(fabsf(x[i][0]), fabsf(x[i][1])));
       }
-      uint32_t* sq = reinterpret_cast<uint32_t*>(feed.sm.slot[1]);
-      sscale = 1.f;
-      cst = 0.f;
-      float z[kVecs];
-  #pragma unroll
-      for (int v = 0; v < kVecs; ++v) {
-        z[v] = 0.f;
-        if (y.vg * kVecs + v >= n_vec) {                 // warp-uniform: no such vector
-  #pragma unroll
-          for (int i = 0; i < D / 32; ++i) sq[q_word<D>(v, lane + 32 * i)] = 0;
-          continue;
-        }
-        float mx = 0.f;
-  #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          const float q0 = x0[v][i] * a.scale, q1 = x1[v][i] * a.scale;
-          float r0 = q0, r1 = q1;
-          if (cs) {
-            const float2 t = cs[j0 + i];
-            r0 = q0 * t.x + q1 * t.y;
-            r1 = q1 * t.x - q0 * t.y;
-          }
-          if constexpr (F::coded) {
-            z[v] += r0 * z0[i] + r1 * z1[i];
-            r0 *= k0[i];
-            r1 *= k1[i];
-            mx = fmaxf(mx, fmaxf(fabsf(r0), fabsf(r1)));
-          }
-          x0[v][i] = r0;
-          x1[v][i] = r1;
-        }
-        float up = 1.f;
+    }
+    float up = 1.f;
+    if constexpr (F::coded) {
+      // fp16 parts want the largest element near 2^12: a power of two apart
+      const uint32_t mb = __reduce_max_sync(kAll, __float_as_uint(mx));
+      const int e = min(max((int)(mb >> 23), 27), 230);
+      up = __uint_as_float((uint32_t)(266 - e) << 23);
+      if (v == gid) sscale = 16777216.f * __uint_as_float((uint32_t)(e - 12) << 23);   // 2^24 / up
+    }
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int ch = j0 + i + b * (D / 2);
+        float t = x[i][b] * up;
+        uint32_t w;
         if constexpr (F::coded) {
-          // fp16 parts want the largest element near 2^12: a power of two apart
-          const uint32_t mb = __reduce_max_sync(kAll, __float_as_uint(mx));
-          const int e = min(max((int)(mb >> 23), 27), 230);
-          up = __uint_as_float((uint32_t)(266 - e) << 23);
-          if (v == gid) sscale = 16777216.f * __uint_as_float((uint32_t)(e - 12) << 23);   // 2^24 / up
+          if (ST == FUSE_U4_ASYM && (ch & 1)) t *= 0.0625f;     // odd codes sit 4 bits higher
+          const __half hi = __float2half_rn(t);
+          w = pack_half2(__half2float(hi), t - __half2float(hi));
+        } else {
+          const __nv_bfloat16 hi = __float2bfloat16_rn(t);
+          w = pack_bf16x2(__bfloat162float(hi), t - __bfloat162float(hi));
         }
-  #pragma unroll
-        for (int i = 0; i < NP; ++i)
-  #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const int ch = j0 + i + b * (D / 2);
-            float x = (b ? x1[v][i] : x0[v][i]) * up;
-            uint32_t w;
-            if constexpr (F::coded) {
-              if (ST == FUSE_U4_ASYM && (ch & 1)) x *= 0.0625f;   // odd codes sit 4 bits higher
-              const __half hi = __float2half_rn(x);
-              w = pack_half2(__half2float(hi), x - __half2float(hi));
-            } else {
-              const __nv_bfloat16 hi = __float2bfloat16_rn(x);
-              w = pack_bf16x2(__bfloat162float(hi), x - __bfloat162float(hi));
-            }
-            sq[q_word<D>(v, ch)] = w;
-          }
+        sq[q_word<D>(v, ch)] = w;
       }
-      if constexpr (F::coded) {
-        // the eight sums over the lanes, halving the vectors a lane carries:
-        // vector gid ends up in its four lanes
-  #pragma unroll
-        for (int n = 4; n > 0; n >>= 1) {
-          const bool upper = lane & (4 * n);
-  #pragma unroll
-          for (int v = 0; v < n; ++v) {
-            const float give = upper ? z[v] : z[v + n];
-            z[v] = (upper ? z[v + n] : z[v]) + __shfl_xor_sync(kAll, give, 4 * n);
-          }
-        }
-        cst = z[0];
-        cst += __shfl_xor_sync(kAll, cst, 1);
-        cst += __shfl_xor_sync(kAll, cst, 2);
+  }
+  if constexpr (F::coded) {
+    // the eight sums over the lanes, halving the vectors a lane carries:
+    // vector gid ends up in its four lanes
+#pragma unroll
+    for (int n = 4; n > 0; n >>= 1) {
+      const bool upper = lane & (4 * n);
+#pragma unroll
+      for (int v = 0; v < n; ++v) {
+        const float give = upper ? z[v] : z[v + n];
+        z[v] = (upper ? z[v + n] : z[v]) + __shfl_xor_sync(kAll, give, 4 * n);
       }
-      __syncwarp();
-  #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-  #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const uint32_t w0 = sq[q_word<D>(gid, q_channel<ST, D>(tig, kk, b, 0))];
-          const uint32_t w1 = sq[q_word<D>(gid, q_channel<ST, D>(tig, kk, b, 1))];
-          qo[kk][b] = __byte_perm(w0, w1, 0x5410);
-          qo[kk][2 + b] = __byte_perm(w0, w1, 0x7632);
-        }
+    }
+    cst = z[0];
+    cst += __shfl_xor_sync(kAll, cst, 1);
+    cst += __shfl_xor_sync(kAll, cst, 2);
+  }
+  __syncwarp();
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const uint32_t w0 = sq[q_word<D>(gid, q_channel<ST, D>(tig, kk, b, 0))];
+      const uint32_t w1 = sq[q_word<D>(gid, q_channel<ST, D>(tig, kk, b, 1))];
+      qo[kk][b] = __byte_perm(w0, w1, 0x5410);
+      qo[kk][2 + b] = __byte_perm(w0, w1, 0x7632);
+    }
 }
 
 // An item of codes.
@@ -444,8 +462,9 @@ __device__ __forceinline__ void load_query(const AttendArgs& a, const Item& y, c
 //                 from S by a transposed 8 x 8 move
 // so a lane's scores, sums and outputs belong to vectors 2 tig and 2 tig + 1.
 template <int ST, int D>
-__device__ __forceinline__ void attend_codes(const AttendArgs& a, const Item& y, const float2* cs,
-                                             const __half* ks, const __half* kz, WarpSmem<D>& sm) {
+__device__ __forceinline__ void attend_codes(const AttendArgs& a, const Item& y, const RawQuery& raw,
+                                             const float2* cs, const __half* ks, const __half* kz,
+                                             WarpSmem<D>& sm) {
   using F = Fmt<ST, D>;
   constexpr int RB = F::RB, RC = F::RC, TOK = F::TOK, NT = TOK / 8, MT = D / 16;
   constexpr uint32_t kAll = 0xffffffffu;
@@ -471,7 +490,7 @@ __device__ __forceinline__ void attend_codes(const AttendArgs& a, const Item& y,
   uint64_t ss, sb;                                     // sscale and cst of the lane's two vectors
   {
     float s1, c1;
-    load_query<ST, D>(a, y, cs, ks, kz, feed, q, s1, c1);
+    load_query<ST, D>(a, y, raw, cs, ks, kz, feed, q, s1, c1);
     ss = pack2(__shfl_sync(kAll, s1, tig * 8), __shfl_sync(kAll, s1, tig * 8 + 4));
     sb = pack2(__shfl_sync(kAll, c1, tig * 8), __shfl_sync(kAll, c1, tig * 8 + 4));
   }
@@ -695,8 +714,8 @@ __device__ __forceinline__ void attend_codes(const AttendArgs& a, const Item& y,
 //                 the layout in which S^T comes out is the one P goes in
 // A lane's scores belong to vector gid, its outputs to 2 tig and 2 tig + 1.
 template <int D>
-__device__ __forceinline__ void attend_rows(const AttendArgs& a, const Item& y, const float2* cs,
-                                            WarpSmem<D>& sm) {
+__device__ __forceinline__ void attend_rows(const AttendArgs& a, const Item& y, const RawQuery& raw,
+                                            const float2* cs, WarpSmem<D>& sm) {
   constexpr int ST = FUSE_BF16;
   using F = Fmt<ST, D>;
   constexpr int RB = F::RB, RC = F::RC, TOK = F::TOK, MT = D / 16;
@@ -708,7 +727,7 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Item& y, 
   feed.template copy<true>();
   uint32_t q[D / 16][4];
   float one, none;
-  load_query<ST, D>(a, y, cs, nullptr, nullptr, feed, q, one, none);
+  load_query<ST, D>(a, y, raw, cs, nullptr, nullptr, feed, q, one, none);
   float m = -INFINITY, l = 0.f;                        // vector gid (its sum: this lane's keys)
   float acc[MT][4];
 #pragma unroll
@@ -823,6 +842,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
     const int seg = i / per_seg;
     y.h = i % per_seg / a.nvg;
     y.vg = i % a.nvg;
+    RawQuery rq;
+    if (seg < a.nside) read_query<D>(a, y.r, y.h, y.vg, rq);
     const fuse_request_t R = a.reqs[y.r];
     const int n = R.k + R.n_query - a.n_new;
     y.t0 = seg * a.sseg;
@@ -843,7 +864,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
           report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_ATTEND_SEL, (uint32_t)t);
       }
     }
-    attend_rows<D>(a, y, nullptr, sm);
+    attend_rows<D>(a, y, rq, nullptr, sm);
     return;
   }
   const int ctas = (a.nsub * per_seg + kWarps - 1) / kWarps;
@@ -853,8 +874,11 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
   const int seg = i / per_seg;
   y.h = i % per_seg / a.nvg;
   y.vg = i % a.nvg;
-  const fuse_chunk_t C = a.chunks[a.chunk0 + ci];
+  // the queries are read first: they do not depend on the tables' entries
   y.r = owners.req[ci];
+  RawQuery rq;
+  if (seg < a.nsub) read_query<D>(a, y.r, y.h, y.vg, rq);
+  const fuse_chunk_t C = a.chunks[a.chunk0 + ci];
   const fuse_request_t R = a.reqs[y.r];
   // the chunk's angles, D / 16 pairs a warp.  The frequencies are launch
   // parameters, which a warp reads fast only at one address at a time.
@@ -895,9 +919,9 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
   y.slot = (int64_t)(a.chunk0 + ci) * a.nsub + seg;
   const float2* cs = C.pos != 0 ? s_cs : nullptr;
   if constexpr (ST == FUSE_BF16)
-    attend_rows<D>(a, y, cs, sm);
+    attend_rows<D>(a, y, rq, cs, sm);
   else
-    attend_codes<ST, D>(a, y, cs, reinterpret_cast<const __half*>(C.k_scale),
+    attend_codes<ST, D>(a, y, rq, cs, reinterpret_cast<const __half*>(C.k_scale),
                         reinterpret_cast<const __half*>(C.k_zero), sm);
 }
 
