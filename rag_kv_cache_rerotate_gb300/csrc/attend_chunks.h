@@ -7,8 +7,8 @@
 namespace fusekv {
 
 constexpr int kVecs = 8;                  // query vectors (new token, query head) of an item
-constexpr int kReqBatch = 512;            // requests of one launch (parameter space)
-constexpr int kChunkBatch = 2048;         // chunks of one launch
+constexpr int kReqBatch = 128;            // requests of one launch (parameter space)
+constexpr int kChunkBatch = 512;          // chunks of one launch
 
 // How the keys of a call are cut.  A chunk's tokens are cut into nsub
 // segments of seg tokens, a request's side rows into nside segments of sseg

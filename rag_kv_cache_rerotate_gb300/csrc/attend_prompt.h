@@ -6,7 +6,7 @@
 
 namespace fusekv {
 
-constexpr int kPromptBatch = 256;         // requests of one launch (parameter space)
+constexpr int kPromptBatch = 64;          // requests of one launch (parameter space)
 constexpr int kMaxUnits = 1 << 24;        // (tile, KV head) units of one launch
 
 // Requests of one launch, longest first.  A tile is rtile consecutive rows of
