@@ -86,28 +86,28 @@ struct Keys {
 // One warp, one item: 32 keys at a time, a lane per key for the scores, then
 // a lane per D / 32 channels for the sums.
 template <int ST, int D>
-__device__ void attend_item(const AttendArgs& a, const RopeFreqs& f, const Keys& y, bool rotate,
-                            int pos, const __half* ks, const __half* kz, int r, int h, int vg,
-                            int64_t slot, float (*s_q)[D], float (*s_p)[kVecs]) {
+__device__ void attend_item(const AttendArgs& a, const Keys& y, const float2* cs, const __half* ks,
+                            const __half* kz, int r, int h, int vg, int64_t slot, float (*s_q)[D],
+                            float (*s_p)[kVecs]) {
   constexpr int EL = D / 32;
   const int lane = threadIdx.x % 32;
-  const int n_vec = a.g * a.n_new;
+  const int n_vec = min(kVecs, a.g * a.n_new - vg * kVecs);
   float cst[kVecs];
   // the query vectors, turned back by the chunk's offset and scaled
-#pragma unroll 1
+#pragma unroll
   for (int v = 0; v < kVecs; ++v) {
     const int vi = vg * kVecs + v;
     float z = 0.f;
+#pragma unroll
     for (int j = lane; j < D / 2; j += 32) {
       float x0 = 0.f, x1 = 0.f;
-      if (vi < n_vec) {
+      if (v < n_vec) {
         const float* q = reinterpret_cast<const float*>(a.Q) +
                          ((int64_t)(r * a.n_new + vi / a.g) * a.n_q_heads + h * a.g + vi % a.g) * D;
         const float q0 = q[j] * a.scale, q1 = q[j + D / 2] * a.scale;
-        float c = 1.f, s = 0.f;
-        if (rotate) rope_cos_sin(pos, f.hi[j], f.mid[j], f.lo[j], c, s);
-        x0 = q0 * c + q1 * s;
-        x1 = q1 * c - q0 * s;
+        const float2 w = cs ? cs[j] : make_float2(1.f, 0.f);
+        x0 = q0 * w.x + q1 * w.y;
+        x1 = q1 * w.x - q0 * w.y;
         if (coded<ST>() && ks) {
           z += x0 * __half2float(kz[h * D + j]) + x1 * __half2float(kz[h * D + j + D / 2]);
           x0 *= __half2float(ks[h * D + j]);
@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(kWarps * 32)
                        const __grid_constant__ RopeFreqs f, int side_ctas, int n_side_ctas) {
   __shared__ float s_q[kWarps][kVecs][D];
   __shared__ float s_p[kWarps][32][kVecs];
+  __shared__ float2 s_cs[D / 2];
   const int warp = threadIdx.x / 32;
   pdl_wait();
   pdl_trigger();                           // the join may read the call's inputs before it waits
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(kWarps * 32)
           report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_ATTEND_SEL, (uint32_t)t);
       }
     }
-    attend_item<FUSE_F32, D>(a, f, y, false, 0, nullptr, nullptr, r, h, vg,
+    attend_item<FUSE_F32, D>(a, y, nullptr, nullptr, nullptr, r, h, vg,
                           a.chunk_slots + (int64_t)r * a.nside + seg, s_q[warp], s_p[warp]);
     return;
   }
@@ -262,6 +263,25 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int i = (b % ctas) * kWarps + warp;
   const int seg = i / per_seg, h = i % per_seg / a.nvg, vg = i % a.nvg;
   const fuse_chunk_t C = a.chunks[a.chunk0 + ci];
+  // the chunk's angles, D / 16 pairs a warp.  The frequencies are launch
+  // parameters, which a warp reads fast only at one address at a time.
+  if (C.pos != 0) {                        // block-uniform
+    constexpr int N = D / 2 / kWarps;
+    const int lane = threadIdx.x % 32;
+    float hi = 0.f, mid = 0.f, lo = 0.f, c, sn;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const float fh = f.hi[warp * N + k], fm = f.mid[warp * N + k], fl = f.lo[warp * N + k];
+      if (lane == k) {
+        hi = fh;
+        mid = fm;
+        lo = fl;
+      }
+    }
+    rope_cos_sin(C.pos, hi, mid, lo, c, sn);
+    if (lane < N) s_cs[warp * N + lane] = make_float2(c, sn);
+  }
+  __syncthreads();
   const int t0 = seg * a.seg;
   if (seg >= a.nsub) return;
   if (t0 >= C.len) {                       // past the chunk's end: an item without a key
@@ -283,8 +303,8 @@ __global__ void __launch_bounds__(kWarps * 32)
   y.n_skip = R.k;
   y.skip = a.idx + R.sel0;
   y.pos0 = (int)(C.dst_row - R.row0);
-  attend_item<ST, D>(a, f, y, C.pos != 0, C.pos, reinterpret_cast<const __half*>(C.k_scale),
-                        reinterpret_cast<const __half*>(C.k_zero), r, h, vg,
+  attend_item<ST, D>(a, y, C.pos != 0 ? s_cs : nullptr, reinterpret_cast<const __half*>(C.k_scale),
+                     reinterpret_cast<const __half*>(C.k_zero), r, h, vg,
                         (int64_t)(a.chunk0 + ci) * a.nsub + seg, s_q[warp], s_p[warp]);
 }
 
@@ -441,7 +461,7 @@ cudaError_t launch_simt_d(int st, const AttendArgs& a, const ChunkOwners& o, con
 
 // ---- host side ---------------------------------------------------------------
 
-constexpr int64_t kItems = 152 * 12;      // three quarters of the warps that 152 SMs hold
+constexpr int64_t kItems = 152 * 12;      // warps of bf16 layers that 152 SMs hold
 constexpr int kMaxKeys = 1024;            // keys of an item (a bit each in 32 words)
 
 int cut(int64_t keys, int64_t items, int step) {     // keys per item, a multiple of step
@@ -502,10 +522,17 @@ fuse_status_t plan_attend(const fuse_layer_desc_t* desc, const fuse_chunks_t* ch
   const int g = desc->n_q_heads / desc->n_kv_heads;
   P->nvg = (g * n_new + kVecs - 1) / kVecs;
   const int64_t per = (int64_t)desc->n_kv_heads * P->nvg;
-  const int seg = cut(n_ctx * per, kItems, 64);
+  // Shorter segments share less of an item's start (its query vectors, the
+  // join), longer ones leave warps idle at the end.  bf16 layers, at least 64
+  // keys: 8 chunks of 512 take 12 us, with 32 or 192 keys 14; 16 requests of
+  // 0.5k to 8k tokens 45 us at the rule's 256, 59 at 96.  Side rows go to half
+  // as many items: 105 against 112 us on 8 requests of 33k tokens.  fp32 layers,
+  // whose lane takes a key: 15 us with 32 keys an item, 21 with 64.
+  const int least = desc->dtype == FUSE_BF16 ? 64 : 32;
+  const int seg = cut(n_ctx * per, kItems, least);
   P->nsub = std::max(1, (max_len + seg - 1) / seg);
   P->seg = cut(std::max(max_len, 1), P->nsub, 32);
-  const int sseg = cut(n_side * per, kItems, 32);
+  const int sseg = cut(n_side * per, kItems / 2, least);
   P->nside = (int)((max_side + sseg - 1) / sseg);
   P->sseg = sseg;
   P->chunk_slots = (int64_t)chunks->n_chunks * P->nsub;
