@@ -467,7 +467,8 @@ fuse_status_t fuse_kivi_quantize(const fuse_layer_desc_t* desc, const fuse_chunk
  * FUSE_ERR_UNSUPPORTED.  A block id outside the pool drops its
  * tokens, a selected index out of range or order is ignored; both are
  * recorded as FUSE_ERR_DEVICE_BOUNDS.  Softmax statistics and sums are fp32;
- * no atomics: equal inputs give equal outputs.  The workspace (of
+ * no atomics: equal inputs give equal outputs.  O may not overlap an input.
+ * A captured call keeps the tables' sizes of its capture.  The workspace (of
  * fuse_attend_workspace_size, convention as for fuse_workspace_size) is
  * written before it is read. */
 #define FUSE_ATTEND_MAX_NEW 8

@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int64_t c0 = rc.first[blockIdx.y];
   const int n_seg = (int)(rc.first[blockIdx.y + 1] - c0) * a.nsub;
   const int n_side = R.k + R.n_query - a.n_new;           // side rows in items
-  const int n = n_seg + (n_side + a.sseg - 1) / a.sseg;
+  const int n = n_seg + min(a.nside, (n_side + a.sseg - 1) / a.sseg);
   // own keys: warp j takes new token j
   const T* Ks = reinterpret_cast<const T*>(a.Ks);
   const T* Vs = reinterpret_cast<const T*>(a.Vs);
@@ -562,10 +562,12 @@ cudaError_t launch_attend_simt(const fuse_layer_desc_t& d, int st, const AttendA
 }
 
 cudaError_t launch_attend_combine(const fuse_layer_desc_t& d, const AttendArgs& a,
-                                  const RequestChunks& rc, cudaStream_t s) {
+                                  const RequestChunks& rc, bool early, cudaStream_t s) {
   const dim3 grid(a.n_new * a.n_q_heads, a.n_req);
   auto go = [&](auto kernel) {
-    return launch_pdl(kernel, grid, dim3(kJoinThreads), 0, s, a, rc);
+    if (early) return launch_pdl(kernel, grid, dim3(kJoinThreads), 0, s, a, rc);
+    kernel<<<grid, kJoinThreads, 0, s>>>(a, rc);
+    return cudaGetLastError();
   };
   if (d.dtype == FUSE_BF16)
     return d.head_dim == 128 ? go(attend_combine_kernel<__nv_bfloat16, 128>)
@@ -656,13 +658,17 @@ fuse_status_t fuse_attend_chunks(const fuse_layer_desc_t* desc, const fuse_chunk
     }));
     if (st != FUSE_OK) return st;
   }
+  // The join reads the call's inputs before it waits for the kernel before it,
+  // which is one of the above, begun after what wrote them had ended.  Without
+  // an item there is none, and the first join starts after what came before.
+  const bool items = chunks->n_chunks > 0 || P.nside > 0;
   for (int r0 = 0; r0 < reqs->n_req; r0 += kReqBatch) {
     RequestChunks rc;
     a.req0 = r0;
     a.n_req = std::min(kReqBatch, reqs->n_req - r0);
     std::copy(first.begin() + r0, first.begin() + r0 + a.n_req + 1, rc.first);
     st = cuda_status(traced("attend_combine", s, [&] {
-      return launch_attend_combine(*desc, a, rc, s);
+      return launch_attend_combine(*desc, a, rc, items || r0 > 0, s);
     }));
     if (st != FUSE_OK) return st;
   }

@@ -63,7 +63,8 @@ cudaError_t launch_attend_simt(const fuse_layer_desc_t& d, int kv_storage, const
 cudaError_t launch_attend_mma(const fuse_layer_desc_t& d, int kv_storage, const AttendArgs& a,
                               const ChunkOwners& owners, const RopeFreqs& freqs, int side_reqs,
                               cudaStream_t s);
+// early: the kernel before it in the stream is one of the above (or a join).
 cudaError_t launch_attend_combine(const fuse_layer_desc_t& d, const AttendArgs& a,
-                                  const RequestChunks& rc, cudaStream_t s);
+                                  const RequestChunks& rc, bool early, cudaStream_t s);
 
 }  // namespace fusekv

@@ -9,7 +9,7 @@ import torch
 
 from rag_kv_cache_rerotate_gb300 import fusekv as fk
 
-from cache_ops import Attend, AttendCase, f64
+from cache_ops import DT, KIND, Attend, AttendCase, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -192,3 +192,26 @@ def test_other_stream_and_graph():
         g.replay()
         got = a.O.clone()
         assert torch.equal(a.run(), got)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_requests_of_one_token_follow_what_writes_their_rows(dtype):
+    """Requests of a single token without context leave nothing but the join,
+    which must not read its rows before the kernel that writes them (a prompt
+    attention) has ended."""
+    T, H, d = 2048, 8, 128
+    g = torch.Generator().manual_seed(11)
+    Q, K, V = (torch.randn(T, H, d, generator=g).to(DT[dtype]).cuda() for _ in range(3))
+    desc = fk.layer_desc(64, H, H, d, 1e6, KIND[dtype])
+    prompt = fk.RequestTable([fk.Request(0, 0, 0, 0, T, 0, 0, 0)])
+    reqs = fk.RequestTable([fk.Request(i, 0, 0, i, 0, 1, 0, 0) for i in range(T)])
+    none = fk.ChunkTable([], fk.FUSE_KV_CONTIGUOUS, fk.FUSE_U4_ASYM)
+    ws, ws2 = fk.alloc_workspace(desc, prompt), fk.alloc_attend_workspace(desc, none, reqs, 1)
+    P, O = torch.zeros_like(Q), torch.zeros_like(Q)
+    for _ in range(3):
+        P.zero_()
+        fk.attend_prompt(desc, prompt, Q, K, V, P, ws)
+        fk.attend_chunks(desc, none, reqs, 1, Q, None, K, P, O, ws2)
+        # one key: its weight is 1 and the row its value
+        assert torch.equal(O, P) and bool((P != 0).any(-1).all())
+    fk.check_errors(ws2)
