@@ -58,9 +58,6 @@ constexpr int kTmemCols = 512;                // S buffers | O buffers
 // whatever its size: a reference up to 2^16 below the true maximum costs no
 // accuracy and saves rescales.
 constexpr float kRescaleThreshold = 16.0f;
-// Reference maximum above every masked score (-1e30 * scale) and below every
-// real one, so masked probabilities are exactly 0.
-constexpr float kFloor = -1.0e29f;
 
 // Ring depths: what fits beside two Q tiles in 227 KB.
 template <int D> struct Ring {
@@ -477,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int p1 = cur.t.first + min(R1 >> a.g_log2, cur.t.rows - 1);
       const int ob = i % kOBufs;
       const uint32_t tO = tmem + lane_off + kColO + ob * D;
-      float mu0 = kFloor, mu1 = kFloor;                // running maxima (log2 units)
+      float mu0 = 0.f, mu1 = 0.f;                      // running maxima (log2 units) once j > 0
       float l0 = 0.f, l1 = 0.f;                        // this thread's part of the row sums
       bool ok = true;
       for (int j = 0; j < cur.nkb; ++j, ++b) {
@@ -493,14 +490,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tmem_ld_16x256b_x8(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
         tc::tmem_ld_wait();
         if (j == cur.nkb - 1) {                        // the tile's own rows: mask
+          constexpr uint32_t kMasked = 0xff800000u;    // -infinity; every row sees a key of its own
           const int key0 = j * kKB;
 #pragma unroll
           for (int q = 0; q < 16; ++q) {
             const int k = key0 + 8 * q + 2 * c4;
-            if (k > p0) r[4 * q] = __float_as_uint(-1e30f);
-            if (k + 1 > p0) r[4 * q + 1] = __float_as_uint(-1e30f);
-            if (k > p1) r[4 * q + 2] = __float_as_uint(-1e30f);
-            if (k + 1 > p1) r[4 * q + 3] = __float_as_uint(-1e30f);
+            if (k > p0) r[4 * q] = kMasked;
+            if (k + 1 > p0) r[4 * q + 1] = kMasked;
+            if (k > p1) r[4 * q + 2] = kMasked;
+            if (k + 1 > p1) r[4 * q + 3] = kMasked;
           }
         }
         float m0, m1;
@@ -525,8 +523,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         float mn0 = mu0, mn1 = mu1;
         bool rs0 = false, rs1 = false;
         if (j == 0) {
-          mn0 = fmaxf(ms0, kFloor);
-          mn1 = fmaxf(ms1, kFloor);
+          mn0 = ms0;
+          mn1 = ms1;
         } else {
           if (ms0 > mu0 + kRescaleThreshold) { mn0 = ms0; rs0 = true; }
           if (ms1 > mu1 + kRescaleThreshold) { mn1 = ms1; rs1 = true; }

@@ -112,6 +112,23 @@ def test_masked_scores_may_be_infinite():
     assert (np.abs(got[:199] - want[:199]) <= tol[:199]).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_scores_near_the_lowest_number(dtype):
+    # equal scores of -2^127 (before the scale): every row is the mean of the
+    # values it sees.  Weights are 1 exactly; n additions in fp32, the quotient
+    # and the output's rounding are left.
+    p = Prompt([(0, 300)], (2, 1, 128), dtype)
+    p.Q.fill_(2.0 ** 60)
+    p.K.fill_(-2.0 ** 60)
+    got = f64(p.run())
+    fk.check_errors(p.ws)
+    V = f64(p.V)
+    n = np.arange(1, 301)[:, None, None]
+    want, span = np.cumsum(V, 0) / n, np.cumsum(np.abs(V), 0) / n
+    half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    assert (np.abs(got - want) <= half * np.abs(want) + (n + 4) * 2.0 ** -23 * span).all()
+
+
 def test_large_scores():
     # one key takes all of the weight
     p = Prompt([(0, 260)], (2, 1, 64), "bf16")
