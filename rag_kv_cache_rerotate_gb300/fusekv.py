@@ -227,7 +227,7 @@ def _to_device_bytes(arr, device) -> torch.Tensor:
 
 
 class RequestTable:
-    """Host and device copies of a ``fuse_request_t`` array (fixed once built)."""
+    """Host and device copies of a ``fuse_request_t`` array."""
 
     def __init__(self, reqs: Sequence[Request], device="cuda"):
         self.host = (Request * max(1, len(reqs)))(*reqs)
@@ -235,12 +235,13 @@ class RequestTable:
         self.dev = _to_device_bytes(self.host, device) if device is not None else None
         self.c = Requests(self.n, _c.addressof(self.host),
                           self.dev.data_ptr() if self.dev is not None and self.dev.numel() else None)
-        self._totals = None
+        self._totals, self._of = None, b""
 
     def extents(self) -> Totals:
-        """``totals`` of the table as first asked for."""
-        if self._totals is None:
-            self._totals = self.totals()
+        """``totals``, computed again only when the host table has changed."""
+        now = bytes(self.host)
+        if self._totals is None or now != self._of:
+            self._totals, self._of = self.totals(), now
         return self._totals
 
     def totals(self) -> Totals:
@@ -519,6 +520,13 @@ def _rows(t, name, dtype, dev, rows, heads, dim, exact=False):
     return t.data_ptr() or None
 
 
+def _ws(ws, dev):
+    """A workspace's pointer and bytes."""
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws: a contiguous tensor on the current CUDA device is needed")
+    return ws.data_ptr() or None, ws.numel() * ws.element_size()
+
+
 _TORCH_DTYPE = {FUSE_F32: torch.float32, FUSE_BF16: torch.bfloat16}
 
 
@@ -553,7 +561,7 @@ def attend_chunks(desc: LayerDesc, chunks: ChunkTable, reqs: RequestTable, n_new
         _c.byref(desc), _c.byref(chunks.c), _c.byref(reqs.c), int(n_new),
         _rows(Q, "Q", dt, dev, n, Hq, d, True), _ptr(idx), _rows(Ks, "Ks", dt, dev, tot.n_out, Hkv, d),
         _rows(Vs, "Vs", dt, dev, tot.n_out, Hkv, d), _rows(O, "O", dt, dev, n, Hq, d, True),
-        _ptr(ws), ws.numel(), _stream(stream))
+        *_ws(ws, dev), _stream(stream))
     if st != FUSE_OK:
         raise FuseError(st, "fuse_attend_chunks")
 
@@ -565,7 +573,7 @@ def attend_prompt(desc: LayerDesc, reqs: RequestTable, Q, K, V, O, ws, stream=No
     st = load().fuse_attend_prompt(
         _c.byref(desc), _c.byref(reqs.c), _rows(Q, "Q", dt, dev, n, Hq, d),
         _rows(K, "K", dt, dev, n, Hkv, d), _rows(V, "V", dt, dev, n, Hkv, d),
-        _rows(O, "O", dt, dev, n, Hq, d), _ptr(ws), ws.numel(), _stream(stream))
+        _rows(O, "O", dt, dev, n, Hq, d), *_ws(ws, dev), _stream(stream))
     if st != FUSE_OK:
         raise FuseError(st, "fuse_attend_prompt")
 
@@ -637,15 +645,16 @@ def pages_fork(src: ChunkTable, dst: ChunkTable, refs, moves, ws, stream=None):
     partly filled last pages listed in ``moves`` for ``pages_copy``."""
     dev = _device()
     st = load().fuse_pages_fork(_c.byref(src.c), _c.byref(dst.c), _refs(refs, src, dev), _ptr(moves),
-                                _max_moves(moves, dev), _ptr(ws), ws.numel(), _stream(stream))
+                                _max_moves(moves, dev), *_ws(ws, dev), _stream(stream))
     if st != FUSE_OK:
         raise FuseError(st, "fuse_pages_fork")
 
 
 def pages_free(tables: ChunkTable, refs, ws, stream=None):
     """Every entry of ``tables`` gives up one reference."""
-    st = load().fuse_pages_free(_c.byref(tables.c), _refs(refs, tables, _device()), _ptr(ws),
-                                ws.numel(), _stream(stream))
+    dev = _device()
+    st = load().fuse_pages_free(_c.byref(tables.c), _refs(refs, tables, dev), *_ws(ws, dev),
+                                _stream(stream))
     if st != FUSE_OK:
         raise FuseError(st, "fuse_pages_free")
 
@@ -655,7 +664,7 @@ def pages_compact(tables: ChunkTable, refs, moves, ws, stream=None):
     copies listed in ``moves`` for ``pages_copy``."""
     dev = _device()
     st = load().fuse_pages_compact(_c.byref(tables.c), _refs(refs, tables, dev), _ptr(moves),
-                                   _max_moves(moves, dev), _ptr(ws), ws.numel(), _stream(stream))
+                                   _max_moves(moves, dev), *_ws(ws, dev), _stream(stream))
     if st != FUSE_OK:
         raise FuseError(st, "fuse_pages_compact")
 
@@ -665,8 +674,9 @@ def pages_copy(desc: LayerDesc, pools: PagePools, moves, ws, stream=None):
     per = desc.head_dim // 2 if pools.kv_storage == FUSE_U4_ASYM else desc.head_dim
     if pools.shape is not None and pools.shape[2:] != (desc.n_kv_heads, per):
         raise ValueError(f"pools: pages of {pools.shape[2:]}, {(desc.n_kv_heads, per)} are needed")
+    dev = _device()
     st = load().fuse_pages_copy(_c.byref(desc), _c.byref(pools.c), _ptr(moves),
-                                _max_moves(moves, _device()), _ptr(ws), ws.numel(), _stream(stream))
+                                _max_moves(moves, dev), *_ws(ws, dev), _stream(stream))
     if st != FUSE_OK:
         raise FuseError(st, "fuse_pages_copy")
 

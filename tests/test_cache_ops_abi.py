@@ -227,6 +227,13 @@ def test_binding_refuses_wrong_tensors(fk):
     call(idx=None)
     call(Ks=S[:7])
     call(Vs=torch.zeros(8, 2, 64, dtype=bf))
+    grown = _reqs(fk, ONE)
+    grown.extents()
+    grown.host[0].n_query += 4                             # the table is looked at again
+    with pytest.raises(ValueError):
+        fk.attend_chunks(d, c, grown, 1, Q, idx, S, S, Q, ws)
+    with pytest.raises(ValueError):
+        fk.attend_chunks(d, c, r, 1, Q, idx, S, S, Q, ws[::2])
     with pytest.raises(ValueError):
         fk.attend_prompt(d, r, torch.zeros(104, 8, 128, dtype=bf), torch.zeros(105, 2, 128, dtype=bf),
                          torch.zeros(105, 2, 128, dtype=bf), torch.zeros(105, 8, 128, dtype=bf), ws)
