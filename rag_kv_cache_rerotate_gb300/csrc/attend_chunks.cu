@@ -220,7 +220,7 @@ __device__ void attend_item(const AttendArgs& a, const Keys& y, const float2* cs
 template <int ST, int D>
 __global__ void __launch_bounds__(kWarps * 32)
     attend_simt_kernel(const AttendArgs a, const __grid_constant__ ChunkOwners owners,
-                       const __grid_constant__ RopeFreqs f, int side_ctas, int n_side_ctas) {
+                       const __grid_constant__ RopeFreqs f, int side_ctas) {
   __shared__ float s_q[kWarps][kVecs][D];
   __shared__ float s_p[kWarps][32][kVecs];
   __shared__ float2 s_cs[D / 2];
@@ -228,10 +228,12 @@ __global__ void __launch_bounds__(kWarps * 32)
   pdl_wait();
   pdl_trigger();                           // the join may read the call's inputs before it waits
   const int per_seg = a.n_kv_heads * a.nvg;
-  if ((int)blockIdx.x < n_side_ctas) {
+  const int ctas = (a.nsub * per_seg + kWarps - 1) / kWarps;
+  const int b = (int)blockIdx.x - ctas * a.n_chunks;
+  if (b >= 0) {
     // side rows: those before the new tokens
-    const int r = a.req0 + blockIdx.x / side_ctas;
-    const int i = (blockIdx.x % side_ctas) * kWarps + warp;
+    const int r = a.req0 + b / side_ctas;
+    const int i = (b % side_ctas) * kWarps + warp;
     const int seg = i / per_seg, h = i % per_seg / a.nvg, vg = i % a.nvg;
     const fuse_request_t R = a.reqs[r];
     const int n = R.k + R.n_query - a.n_new;
@@ -257,10 +259,8 @@ __global__ void __launch_bounds__(kWarps * 32)
                           a.chunk_slots + (int64_t)r * a.nside + seg, s_q[warp], s_p[warp]);
     return;
   }
-  const int ctas = (a.nsub * per_seg + kWarps - 1) / kWarps;
-  const int b = blockIdx.x - n_side_ctas;
-  const int ci = b / ctas;
-  const int i = (b % ctas) * kWarps + warp;
+  const int ci = blockIdx.x / ctas;
+  const int i = (blockIdx.x % ctas) * kWarps + warp;
   const int seg = i / per_seg, h = i % per_seg / a.nvg, vg = i % a.nvg;
   const fuse_chunk_t C = a.chunks[a.chunk0 + ci];
   // the chunk's angles, D / 16 pairs a warp.  The frequencies are launch
@@ -448,7 +448,7 @@ cudaError_t launch_simt_t(const AttendArgs& a, const ChunkOwners& o, const RopeF
   const int64_t grid = (int64_t)side * side_reqs + (int64_t)ctas * a.n_chunks;
   if (grid == 0) return cudaSuccess;
   return launch_pdl(attend_simt_kernel<ST, D>, dim3((unsigned)grid), dim3(kWarps * 32), 0, s, a,
-                    o, f, std::max(side, 1), side * side_reqs);
+                    o, f, std::max(side, 1));
 }
 
 template <int D>
@@ -524,9 +524,9 @@ fuse_status_t plan_attend(const fuse_layer_desc_t* desc, const fuse_chunks_t* ch
   const int64_t per = (int64_t)desc->n_kv_heads * P->nvg;
   // Shorter segments share less of an item's start (its query vectors, the
   // join), longer ones leave warps idle at the end.  bf16 layers, at least 64
-  // keys: 8 chunks of 512 take 12 us, with 32 or 192 keys 14; 16 requests of
-  // 0.5k to 8k tokens 45 us at the rule's 256, 59 at 96.  Side rows go to half
-  // as many items: 105 against 112 us on 8 requests of 33k tokens.  fp32 layers,
+  // keys: 8 chunks of 512 take 12 us, with 192 keys 14; 16 requests of 0.5k
+  // to 8k tokens 41 us at the rule's 256, 48 at 128; 8 of 33k 96 us at 1024,
+  // 105 at 512.  Side rows go to half as many items (96 us against 99).  fp32 layers,
   // whose lane takes a key: 15 us with 32 keys an item, 21 with 64.
   const int least = desc->dtype == FUSE_BF16 ? 64 : 32;
   const int seg = cut(n_ctx * per, kItems, least);

@@ -22,10 +22,11 @@
 // normaliser are raised lazily.
 //
 // Measured with the join (4 bits, 8 KV heads, d = 128, 64 query heads): 8
-// requests of 33k tokens 105 us, 3.5 TB/s, where the bytes alone would take
-// 54; issue slots are a third full and the warps wait for one another's
-// results, not for HBM.  16 paged requests of 0.5k to 8k tokens 43 us, 8
-// chunks of 512 tokens 12 us (latency).  Slots of half the keys in three
+// requests of 33k tokens 96 us, 3.8 TB/s, where the bytes alone would take
+// 54; issue slots are two fifths full and a warp waits for its own results, not
+// for HBM.  16 paged requests of 0.5k to 8k tokens 41 us, 8 chunks of 512
+// tokens 12 us (latency).  Chunks go before side rows, whose items are shorter
+// and fill the end (105 us the other way round).  Slots of half the keys in three
 // buffers took 116 us.  Rows of all heads brought by bulk copies of 2 KB to 16
 // warps an SM, 32 keys at a time, took 132 us (twice the instructions); a warp
 // of its own for bulk copies of single head rows 200 us.
@@ -835,7 +836,7 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Item& y, 
 template <int ST, int D>
 __global__ void __launch_bounds__(kWarps * 32, 3)
     attend_mma_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ ChunkOwners owners,
-                      const __grid_constant__ RopeFreqs f, int side_ctas, int n_side_ctas) {
+                      const __grid_constant__ RopeFreqs f, int side_ctas) {
   extern __shared__ __align__(16) uint8_t raw[];
   __shared__ float2 s_cs[D / 2];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -844,10 +845,12 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
   pdl_trigger();                           // the join may read the call's inputs before it waits
   const int per_seg = a.n_kv_heads * a.nvg;
   Item y;
-  if ((int)blockIdx.x < n_side_ctas) {
+  const int ctas = (a.nsub * per_seg + kWarps - 1) / kWarps;
+  const int b = (int)blockIdx.x - ctas * a.n_chunks;
+  if (b >= 0) {
     // side rows: those before the new tokens
-    y.r = a.req0 + blockIdx.x / side_ctas;
-    const int i = (blockIdx.x % side_ctas) * kWarps + warp;
+    y.r = a.req0 + b / side_ctas;
+    const int i = (b % side_ctas) * kWarps + warp;
     const int seg = i / per_seg;
     y.h = i % per_seg / a.nvg;
     y.vg = i % a.nvg;
@@ -876,10 +879,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
     attend_rows<D>(a, y, rq, nullptr, sm);
     return;
   }
-  const int ctas = (a.nsub * per_seg + kWarps - 1) / kWarps;
-  const int b = blockIdx.x - n_side_ctas;
-  const int ci = b / ctas;
-  const int i = (b % ctas) * kWarps + warp;
+  const int ci = blockIdx.x / ctas;
+  const int i = (blockIdx.x % ctas) * kWarps + warp;
   const int seg = i / per_seg;
   y.h = i % per_seg / a.nvg;
   y.vg = i % a.nvg;
@@ -946,7 +947,7 @@ cudaError_t launch_mma_t(const AttendArgs& a, const ChunkOwners& o, const RopeFr
   const int64_t grid = (int64_t)side * side_reqs + (int64_t)ctas * a.n_chunks;
   if (grid == 0) return cudaSuccess;
   return launch_pdl(attend_mma_kernel<ST, D>, dim3((unsigned)grid), dim3(kWarps * 32), smem, s, a, o,
-                    f, std::max(side, 1), side * side_reqs);
+                    f, std::max(side, 1));
 }
 
 template <int D>
