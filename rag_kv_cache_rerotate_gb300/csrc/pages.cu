@@ -44,54 +44,70 @@ struct TableArgs {
   uint32_t* err;
 };
 
+// Two counts in one word: sums and scans take both at once.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair(int lo, int hi) { return (Pair)(uint32_t)hi << 32 | (uint32_t)lo; }
+__device__ __forceinline__ int lo_of(Pair p) { return (int)(uint32_t)p; }
+__device__ __forceinline__ int hi_of(Pair p) { return (int)(p >> 32); }
+
 // Sum of x over the block, in every thread.
-__device__ __forceinline__ int block_sum(int x, int* s_warp) {
+__device__ __forceinline__ Pair block_sum(Pair x, Pair* s_warp) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   __syncthreads();                                  // s_warp may still be read
   if (threadIdx.x % 32 == 0) s_warp[threadIdx.x / 32] = x;
   __syncthreads();
-  int t = s_warp[threadIdx.x % 32];
+  Pair t = s_warp[threadIdx.x % 32];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
   return t;
 }
 
 // Exclusive prefix sum of x over the block; *total receives the sum.
-__device__ __forceinline__ int block_scan(int x, int* s_warp, int* total) {
+__device__ __forceinline__ Pair block_scan(Pair x, Pair* s_warp, Pair* total) {
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  int inc = x;
+  Pair inc = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    const Pair y = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += y;
   }
   __syncthreads();
   if (lane == 31) s_warp[warp] = inc;
   __syncthreads();
-  int w = s_warp[lane];
+  Pair w = s_warp[lane];
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, w, o);
+    const Pair y = __shfl_up_sync(0xffffffffu, w, o);
     if (lane >= o) w += y;
   }
   *total = __shfl_sync(0xffffffffu, w, 31);
-  const int before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+  const Pair before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
   return (warp > 0 ? before : 0) + inc - x;
 }
 
-// Sum over the cluster's CTAs of slot i of their s_cnt (this CTA's included),
-// and over the CTAs before this one.  Call between two cluster barriers.
-__device__ __forceinline__ void cluster_counts(cg::cluster_group& cl, int* s_cnt, int i, int rank,
-                                               int* before, int* total) {
-  int b = 0, t = 0;
+// A CTA's counts and whether it met a bad entry; the other CTAs read them.
+struct Counts {
+  Pair n;
+  int bad;
+};
+
+// Sum of the counts over the cluster's CTAs, and over the CTAs before this
+// one; whether any met a bad entry.  Call between two cluster barriers.
+__device__ __forceinline__ bool cluster_counts(cg::cluster_group& cl, Counts* s_cnt, int rank,
+                                               Pair* before, Pair* total) {
+  Pair b = 0, t = 0;
+  int bad = 0;
+#pragma unroll
   for (int r = 0; r < kCtas; ++r) {
-    const int v = cl.map_shared_rank(s_cnt, r)[i];
-    t += v;
-    if (r < rank) b += v;
+    const Counts v = *cl.map_shared_rank(s_cnt, r);
+    t += v.n;
+    bad |= v.bad;
+    if (r < rank) b += v.n;
   }
   *before = b;
   *total = t;
+  return bad != 0;
 }
 
 __device__ __forceinline__ int n_entries(const fuse_chunk_t& c, int bs) {
@@ -126,8 +142,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
   const int rank = (int)cl.block_rank(), tid = threadIdx.x;
   const int lane = tid % 32, warp = rank * (kThreads / 32) + tid / 32;
   constexpr int kWarps = kCtas * kThreads / 32;
-  __shared__ int s_warp[32];
-  __shared__ int s_cnt[4];                          // free pages, partial tables, bad entries
+  __shared__ Pair s_warp[32];
+  __shared__ Counts s_cnt;                          // free pages, partly filled last pages
   pdl_trigger();
   pdl_wait();
   int lo, hi;
@@ -156,52 +172,47 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   }
-  free_n = block_sum(free_n, s_warp);
-  need_n = block_sum(need_n, s_warp);
-  bad = block_sum(bad, s_warp);
-  if (tid == 0) {
-    s_cnt[0] = free_n;
-    s_cnt[1] = need_n;
-    s_cnt[2] = bad;
-  }
+  const Pair mine = block_sum(pair(free_n, need_n), s_warp);
+  bad = __syncthreads_or(bad);
+  if (tid == 0) s_cnt = {mine, bad};
   cl.sync();
-  int f_before, f_total, n_before, need, b_before, n_bad;
-  cluster_counts(cl, s_cnt, 0, rank, &f_before, &f_total);
-  cluster_counts(cl, s_cnt, 1, rank, &n_before, &need);
-  cluster_counts(cl, s_cnt, 2, rank, &b_before, &n_bad);
-  const bool ok = n_bad == 0 && need <= f_total && need <= a.cap;
+  Pair before, all;
+  const bool any_bad = cluster_counts(cl, &s_cnt, rank, &before, &all);
+  const int f_total = lo_of(all), need = hi_of(all);
+  const bool ok = !any_bad && need <= f_total && need <= a.cap;
   if (rank == 0 && tid == 0) {
-    if (n_bad == 0 && need > f_total)
+    if (!any_bad && need > f_total)
       report_error(a.err, FUSE_ERR_NO_PAGES, SITE_PAGE_FREE, (uint32_t)(need - f_total));
-    else if (n_bad == 0 && need > a.cap)
+    else if (!any_bad && need > a.cap)
       report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_PAGE_MOVES, (uint32_t)need);
     a.moves[0] = ok ? need : 0;
     a.moves[1] = a.n_blocks - f_total + (ok ? need : 0);
   }
   // the first `need` free pages, ascending
-  int at = f_before;
+  int at = lo_of(before);
   for (int b0 = lo; ok && b0 < hi && at < need; b0 += 4 * kThreads) {
-    int r[4], cnt = 0, total;
+    int r[4], cnt = 0;
+    Pair total;
     load_refs4(a.refs, b0 + 4 * tid, hi, r);
 #pragma unroll
     for (int i = 0; i < 4; ++i) cnt += r[i] == 0;
-    int p = at + block_scan(cnt, s_warp, &total);
+    int p = at + lo_of(block_scan(cnt, s_warp, &total));
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (r[i] == 0) {
         if (p < need) a.list[p] = b0 + 4 * tid + i;
         ++p;
       }
-    at += total;
+    at += lo_of(total);
   }
   cl.sync();                                        // every count read, the list written
   if (!ok) return;
-  int rank0 = n_before;
+  int rank0 = hi_of(before);
   for (int c0 = c_lo; c0 < c_hi; c0 += kThreads) {
     const int c = c0 + tid;
     const bool mine = c < c_hi && a.src[c].len % a.block_size != 0;
-    int total;
-    const int p = rank0 + block_scan(mine ? 1 : 0, s_warp, &total);
+    Pair total;
+    const int p = rank0 + lo_of(block_scan(mine ? 1 : 0, s_warp, &total));
     if (mine) {
       const int j = a.src[c].len / a.block_size;
       const int b = a.list[p];
@@ -210,7 +221,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
       const_cast<int32_t*>(a.dst[c].block_table)[j] = b;
       a.refs[b] = 1;
     }
-    rank0 += total;
+    rank0 += lo_of(total);
   }
   for (int c = warp; c < a.n_chunks; c += kWarps) {
     const fuse_chunk_t s = a.src[c];
@@ -234,19 +245,23 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
   const int rank = (int)cl.block_rank(), tid = threadIdx.x;
   const int lane = tid % 32, warp = rank * (kThreads / 32) + tid / 32;
   constexpr int kWarps = kCtas * kThreads / 32;
-  __shared__ int s_warp[32];
-  __shared__ int s_cnt[4];                          // live pages, holes, tail pages, bad entries
+  __shared__ Pair s_warp[32];
+  __shared__ Counts s_live, s_cnt;                  // live pages; holes and tail pages
   pdl_trigger();
   pdl_wait();
   int lo, hi;
   slice(a.n_blocks, rank, &lo, &hi);
-  int live = 0, bad = 0;
-  for (int b = lo + 4 * tid; b < hi; b += 4 * kThreads) {
-    int r[4];
-    load_refs4(a.refs, b, hi, r);
+  int first[4];                                     // the counts of this thread's first four pages
+  load_refs4(a.refs, lo + 4 * tid, hi, first);
+  auto refs4 = [&](int b, int (&r)[4]) {
+    if (b < lo + 4 * kThreads) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) live += r[i] > 0;
-  }
+      for (int i = 0; i < 4; ++i) r[i] = first[i];
+    } else {
+      load_refs4(a.refs, b, hi, r);
+    }
+  };
+  int live = 0, bad = 0;
   for (int c = warp; c < a.n_chunks; c += kWarps) {
     const fuse_chunk_t s = a.src[c];
     const int n = n_entries(s, a.block_size);
@@ -259,56 +274,55 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   }
-  live = block_sum(live, s_warp);
-  bad = block_sum(bad, s_warp);
-  if (tid == 0) {
-    s_cnt[0] = live;
-    s_cnt[3] = bad;
+  for (int b = lo + 4 * tid; b < hi; b += 4 * kThreads) {
+    int r[4];
+    refs4(b, r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) live += r[i] > 0;
   }
+  const Pair here = block_sum(live, s_warp);
+  bad = __syncthreads_or(bad);
+  if (tid == 0) s_live = {here, bad};
   cl.sync();
-  int before, n_live, n_bad;
-  cluster_counts(cl, s_cnt, 0, rank, &before, &n_live);
-  cluster_counts(cl, s_cnt, 3, rank, &before, &n_bad);
+  Pair before, all;
+  const bool any_bad = cluster_counts(cl, &s_live, rank, &before, &all);
+  const int n_live = lo_of(all);
   int holes = 0, tails = 0;
   for (int b = lo + 4 * tid; b < hi; b += 4 * kThreads) {
     int r[4];
-    load_refs4(a.refs, b, hi, r);
+    refs4(b, r);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       holes += r[i] == 0 && b + i < n_live;
       tails += r[i] > 0 && b + i >= n_live;
     }
   }
-  holes = block_sum(holes, s_warp);
-  tails = block_sum(tails, s_warp);
-  if (tid == 0) {
-    s_cnt[1] = holes;
-    s_cnt[2] = tails;
-  }
+  const Pair both = block_sum(pair(holes, tails), s_warp);
+  if (tid == 0) s_cnt = {both, 0};
   cl.sync();
-  int h_at, n_moves, t_at, n_tails;
-  cluster_counts(cl, s_cnt, 1, rank, &h_at, &n_moves);
-  cluster_counts(cl, s_cnt, 2, rank, &t_at, &n_tails);
-  const bool ok = n_bad == 0 && n_moves <= a.cap;
+  Pair at;
+  cluster_counts(cl, &s_cnt, rank, &at, &all);
+  const int n_moves = lo_of(all);
+  const bool ok = !any_bad && n_moves <= a.cap;
   if (rank == 0 && tid == 0) {
-    if (n_bad == 0 && !ok)
+    if (!any_bad && !ok)
       report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_PAGE_MOVES, (uint32_t)n_moves);
     a.moves[0] = ok ? n_moves : 0;
     a.moves[1] = n_live;
   }
   for (int b0 = lo; ok && b0 < hi; b0 += 4 * kThreads) {
-    int r[4], hc = 0, tc = 0, total;
+    int r[4], hc = 0, tc = 0;
+    Pair total;
     const int b = b0 + 4 * tid;
-    load_refs4(a.refs, b, hi, r);
+    refs4(b, r);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       hc += r[i] == 0 && b + i < n_live;
       tc += r[i] > 0 && b + i >= n_live;
     }
-    int hp = h_at + block_scan(hc, s_warp, &total);
-    h_at += total;
-    int tp = t_at + block_scan(tc, s_warp, &total);
-    t_at += total;
+    const Pair p = at + block_scan(pair(hc, tc), s_warp, &total);
+    int hp = lo_of(p), tp = hi_of(p);
+    at += total;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (r[i] == 0 && b + i < n_live) a.list[hp++] = b + i;
@@ -321,14 +335,9 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
   }
   cl.sync();
   if (!ok) return;
-  for (int m = rank * kThreads + tid; m < n_moves; m += kCtas * kThreads) {
-    const int from = a.moves[kMoveHead + 2 * m], to = a.list[m];
-    a.moves[kMoveHead + 2 * m + 1] = to;
-    a.refs[to] = a.refs[from];
-    a.refs[from] = 0;
-  }
-  // two tables may be the same buffer: an entry rewritten already is below n_live
-  for (int c = warp; c < a.n_chunks; c += kWarps) {
+  // the tables by the cluster's last warps, the moves by its first ones.  Two
+  // tables may be the same buffer: an entry rewritten already is below n_live
+  for (int c = kWarps - 1 - warp; c < a.n_chunks; c += kWarps) {
     const fuse_chunk_t s = a.src[c];
     int32_t* t = const_cast<int32_t*>(s.block_table);
     const int n = n_entries(s, a.block_size);
@@ -337,6 +346,12 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
       const int b = t[j];
       if (b >= n_live) t[j] = a.list[a.map[b]];
     }
+  }
+  for (int m = rank * kThreads + tid; m < n_moves; m += kCtas * kThreads) {
+    const int from = a.moves[kMoveHead + 2 * m], to = a.list[m];
+    a.moves[kMoveHead + 2 * m + 1] = to;
+    a.refs[to] = a.refs[from];
+    a.refs[from] = 0;
   }
 }
 
