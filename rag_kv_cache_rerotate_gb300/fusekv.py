@@ -496,6 +496,18 @@ def _device() -> int:
     return torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -1
 
 
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _place(stream):
+    """The device that a call runs on and its stream's handle."""
+    if stream is None and _raw_stream is not None and _get_device is not None \
+            and torch.cuda.is_initialized():
+        dev = _get_device()
+        return dev, _raw_stream(dev)
+    return _device(), _stream(stream)
+
+
 def _tensor(t, name, dtype, dev):
     """Refuse what the raw pointer would hide: a tensor of another type, stride
     or device than the call reads.  Returns its shape."""
@@ -550,7 +562,8 @@ def attend_chunks(desc: LayerDesc, chunks: ChunkTable, reqs: RequestTable, n_new
     """Attention of the last ``n_new`` tokens of every request over its chunk
     caches as stored (codes or layer type), the selected positions ``idx``
     replaced by the refreshed rows of ``Ks``, ``Vs`` (QCFuse Eqs. 4, 6)."""
-    dt, dev, tot = _TORCH_DTYPE.get(desc.dtype), _device(), reqs.extents()
+    dt, tot = _TORCH_DTYPE.get(desc.dtype), reqs.extents()
+    dev, on = _place(stream)
     Hq, Hkv, d, n = desc.n_q_heads, desc.n_kv_heads, desc.head_dim, reqs.n * int(n_new)
     if idx is None:
         if tot.n_sel > 0:
@@ -561,19 +574,20 @@ def attend_chunks(desc: LayerDesc, chunks: ChunkTable, reqs: RequestTable, n_new
         _c.byref(desc), _c.byref(chunks.c), _c.byref(reqs.c), int(n_new),
         _rows(Q, "Q", dt, dev, n, Hq, d, True), _ptr(idx), _rows(Ks, "Ks", dt, dev, tot.n_out, Hkv, d),
         _rows(Vs, "Vs", dt, dev, tot.n_out, Hkv, d), _rows(O, "O", dt, dev, n, Hq, d, True),
-        *_ws(ws, dev), _stream(stream))
+        *_ws(ws, dev), on)
     if st != FUSE_OK:
         raise FuseError(st, "fuse_attend_chunks")
 
 
 def attend_prompt(desc: LayerDesc, reqs: RequestTable, Q, K, V, O, ws, stream=None):
     """Causal attention inside every request's rows (whole prompts, packed)."""
-    dt, dev, n = _TORCH_DTYPE.get(desc.dtype), _device(), reqs.extents().n_tok
+    dt, n = _TORCH_DTYPE.get(desc.dtype), reqs.extents().n_tok
+    dev, on = _place(stream)
     Hq, Hkv, d = desc.n_q_heads, desc.n_kv_heads, desc.head_dim
     st = load().fuse_attend_prompt(
         _c.byref(desc), _c.byref(reqs.c), _rows(Q, "Q", dt, dev, n, Hq, d),
         _rows(K, "K", dt, dev, n, Hkv, d), _rows(V, "V", dt, dev, n, Hkv, d),
-        _rows(O, "O", dt, dev, n, Hq, d), *_ws(ws, dev), _stream(stream))
+        _rows(O, "O", dt, dev, n, Hq, d), *_ws(ws, dev), on)
     if st != FUSE_OK:
         raise FuseError(st, "fuse_attend_prompt")
 
@@ -643,18 +657,18 @@ def _refs(refs, tables, dev):
 def pages_fork(src: ChunkTable, dst: ChunkTable, refs, moves, ws, stream=None):
     """Branch off ``src``'s sequences into ``dst``'s tables: full pages shared,
     partly filled last pages listed in ``moves`` for ``pages_copy``."""
-    dev = _device()
+    dev, on = _place(stream)
     st = load().fuse_pages_fork(_c.byref(src.c), _c.byref(dst.c), _refs(refs, src, dev), _ptr(moves),
-                                _max_moves(moves, dev), *_ws(ws, dev), _stream(stream))
+                                _max_moves(moves, dev), *_ws(ws, dev), on)
     if st != FUSE_OK:
         raise FuseError(st, "fuse_pages_fork")
 
 
 def pages_free(tables: ChunkTable, refs, ws, stream=None):
     """Every entry of ``tables`` gives up one reference."""
-    dev = _device()
+    dev, on = _place(stream)
     st = load().fuse_pages_free(_c.byref(tables.c), _refs(refs, tables, dev), *_ws(ws, dev),
-                                _stream(stream))
+                                on)
     if st != FUSE_OK:
         raise FuseError(st, "fuse_pages_free")
 
@@ -662,9 +676,9 @@ def pages_free(tables: ChunkTable, refs, ws, stream=None):
 def pages_compact(tables: ChunkTable, refs, moves, ws, stream=None):
     """Pack the live pages to the front: tables and refs rewritten, the page
     copies listed in ``moves`` for ``pages_copy``."""
-    dev = _device()
+    dev, on = _place(stream)
     st = load().fuse_pages_compact(_c.byref(tables.c), _refs(refs, tables, dev), _ptr(moves),
-                                   _max_moves(moves, dev), *_ws(ws, dev), _stream(stream))
+                                   _max_moves(moves, dev), *_ws(ws, dev), on)
     if st != FUSE_OK:
         raise FuseError(st, "fuse_pages_compact")
 
@@ -674,9 +688,9 @@ def pages_copy(desc: LayerDesc, pools: PagePools, moves, ws, stream=None):
     per = desc.head_dim // 2 if pools.kv_storage == FUSE_U4_ASYM else desc.head_dim
     if pools.shape is not None and pools.shape[2:] != (desc.n_kv_heads, per):
         raise ValueError(f"pools: pages of {pools.shape[2:]}, {(desc.n_kv_heads, per)} are needed")
-    dev = _device()
+    dev, on = _place(stream)
     st = load().fuse_pages_copy(_c.byref(desc), _c.byref(pools.c), _ptr(moves),
-                                _max_moves(moves, dev), *_ws(ws, dev), _stream(stream))
+                                _max_moves(moves, dev), *_ws(ws, dev), on)
     if st != FUSE_OK:
         raise FuseError(st, "fuse_pages_copy")
 
