@@ -33,6 +33,7 @@
 #include <algorithm>
 
 #include "attend_chunks.h"
+#include "checks.h"
 #include "launch.h"
 
 namespace fusekv {

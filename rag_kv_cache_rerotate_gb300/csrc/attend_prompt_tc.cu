@@ -36,6 +36,7 @@
 #include <cmath>
 
 #include "attend_prompt.h"
+#include "checks.h"
 #include "launch.h"
 #include "tc_ptx.cuh"
 

@@ -1,9 +1,20 @@
-// Argument checks shared by the files of entry points (defined in api.cu).
+// What the files of entry points share: argument checks (defined in api.cu) and
+// the cache operators' error sites.
 #pragma once
 
 #include "common.cuh"
 
 namespace fusekv {
+
+// Sites of the cache operators, behind those of ErrSite.
+enum CacheErrSite : uint32_t {
+  SITE_PAGE_ENTRY = 11,      // table entry outside the pool, or naming a page without a reference
+  SITE_PAGE_FREE = 12,       // too few free pages
+  SITE_PAGE_MOVES = 13,      // move list count or page id out of range
+  SITE_ATTEND_BLOCK = 14,    // paged block id outside the pool (attend_chunks)
+  SITE_ATTEND_SEL = 15,      // selected index out of range or order (attend_chunks)
+  SITE_PROMPT_TIMEOUT = 16,  // prompt-attention pipeline wait gave up
+};
 
 struct ReqInfo {
   fuse_totals_t tot;   // extents implied by the offsets (max over requests)

@@ -33,12 +33,6 @@ enum ErrSite : uint32_t {
   SITE_STITCH_TIMEOUT = 8,   // stitch bulk-copy wait gave up
   SITE_MASS_ROWS = 9,        // query rows past the host's count (device table differs)
   SITE_MASS_TIMEOUT = 10,    // tensor-core attention-mass pipeline wait gave up
-  SITE_PAGE_ENTRY = 11,      // table entry outside the pool, or naming a page without a reference
-  SITE_PAGE_FREE = 12,       // too few free pages
-  SITE_PAGE_MOVES = 13,      // move list count or page id out of range
-  SITE_ATTEND_BLOCK = 14,    // paged block id outside the pool (attend_chunks)
-  SITE_ATTEND_SEL = 15,      // selected index out of range or order (attend_chunks)
-  SITE_PROMPT_TIMEOUT = 16,  // prompt-attention pipeline wait gave up
 };
 
 __device__ __forceinline__ void report_error(uint32_t* err, fuse_status_t code, uint32_t site,
