@@ -63,22 +63,28 @@ constexpr float kRescaleThreshold = 16.0f;
 // Ring depths: what fits beside two Q tiles in 227 KB.
 template <int D> struct Ring {
   static constexpr int tile = (D / 64) * kHalf;
-  static constexpr int K = D == 128 ? 3 : 5;
-  static constexpr int V = D == 128 ? 2 : 5;
+  static constexpr int K = D == 128 ? 2 : 5;
+  static constexpr int V = D == 128 ? 3 : 5;
 };
 constexpr int kMaxStages = 5;
 constexpr int kMaxS = 3, kMaxO = 2;           // S and O buffers, at most
+constexpr int kLBufs = 2;                     // row sums: softmax warps run a unit ahead of the output
 
 struct Ctl {
   uint64_t q_full[kQBufs], q_empty[kQBufs];
   uint64_t k_full[kMaxStages], k_empty[kMaxStages];
   uint64_t v_full[kMaxStages], v_empty[kMaxStages];
   uint64_t s_full[kMaxS], p_full[kMaxS], pv_done[kMaxS];      // [block % S buffers]
-  uint64_t o_full[kMaxO], o_empty[kMaxO], l_full[kMaxO], fix_full[kMaxO];   // [unit % O buffers]
+  uint64_t o_full[kMaxO], o_empty[kMaxO];                     // [unit % O buffers]
+  uint64_t l_full[kLBufs], l_empty[kLBufs];                   // [unit % kLBufs]
+  // a unit's last V block: landed, looked through [unit % (V stages + 1)]
+  uint64_t vl_full[kMaxStages + 1], v_ok[kMaxStages + 1];
   uint32_t tmem_base;
   volatile int abort_flag;
-  volatile int fix[kMaxO];   // the unit's last V block held elements that are not finite
-  float xl[kMaxO][128];      // [row] softmax row sum of the unit being written
+  // [unit % (V stages + 1)][output warp] its rows of the unit's last V block
+  // held elements that are not finite
+  volatile int fix[kMaxStages + 1][4];
+  float xl[kLBufs][128];         // [row] softmax row sum of a unit
 };
 
 template <int D> constexpr int smem_bytes() {
@@ -101,18 +107,46 @@ struct PromptTcArgs {
 // Which wait gave up: info = wait id << 20 | CTA (8 bits) << 12 | key block (12 bits).
 enum PromptWait : uint32_t {
   W_Q_EMPTY = 1, W_K_EMPTY, W_V_EMPTY, W_Q_FULL, W_K_FULL, W_S_FREE, W_P_FULL, W_O_EMPTY,
-  W_V_FULL, W_S_FULL, W_PV_DONE, W_O_FULL, W_L_FULL, W_FIX
+  W_V_FULL, W_S_FULL, W_PV_DONE, W_O_FULL, W_L_FULL, W_L_EMPTY, W_VL_FULL, W_V_OK
 };
+
+// What happens when a barrier is not there at the first look.  Out of line:
+// the kernel waits in two dozen places, short prompts run through its code
+// once per unit, and an SM's instruction cache holds a part of it only.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, Ctl* ctl, uint32_t* err, uint32_t which) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t i = 0; i < tc::kWaitPollLimit; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((i & 63u) == 63u) {                // the clock is read late: most waits end before
+      if (ctl->abort_flag) return false;
+      const uint64_t now = tc::global_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > tc::kWaitLimitNs) break;
+    }
+  }
+  if (ctl->abort_flag == 0) {
+    ctl->abort_flag = 1;
+    report_error(err, FUSE_ERR_TIMEOUT, SITE_PROMPT_TIMEOUT, which);
+  }
+  return false;
+}
 
 __device__ __forceinline__ bool wait1(uint64_t* bar, uint32_t parity, Ctl* ctl, uint32_t* err,
                                       uint32_t which, int j) {
-  if (tc::mbar_wait(bar, parity, &ctl->abort_flag)) return true;
-  const bool first = ctl->abort_flag == 0;
-  ctl->abort_flag = 1;
-  if (first)
-    report_error(err, FUSE_ERR_TIMEOUT, SITE_PROMPT_TIMEOUT,
+  if (tc::mbar_try_wait(bar, parity)) return true;
+  return wait_on(tc::smem_u32(bar), parity, ctl, err,
                  (which << 20) | ((blockIdx.x & 0xFFu) << 12) | ((uint32_t)j & 0xFFFu));
-  return false;
 }
 
 // The same by every lane of a warp that goes on to warp-collective instructions.
@@ -196,6 +230,20 @@ __device__ __forceinline__ uint32_t drop_nonfinite(uint32_t w) {
   return w;
 }
 
+// Adds to a row's outputs the elements that are not finite of n rows of V
+// (`step` elements apart): with them the sum is infinite or NaN whatever it
+// was, so it does not matter that the outputs are rounded already.
+__device__ __noinline__ void add_nonfinite(__nv_bfloat16* dst, const __nv_bfloat16* v, int n, int64_t step,
+                                           int d) {
+#pragma unroll 1
+  for (int k = 0; k < n; ++k, v += step)
+#pragma unroll 1
+    for (int e = 0; e < d; ++e) {
+      const float x = __bfloat162float(v[e]);
+      if (!isfinite(x)) dst[e] = __float2bfloat16_rn(__bfloat162float(dst[e]) + x);
+    }
+}
+
 template <int D, int kSBufs, int kOBufs>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
@@ -235,8 +283,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int q = 0; q < kOBufs; ++q) {
       tc::mbar_init(&ctl->o_full[q], 1);
       tc::mbar_init(&ctl->o_empty[q], 128);
+    }
+    for (int q = 0; q < kLBufs; ++q) {
       tc::mbar_init(&ctl->l_full[q], kSoftThreads);
-      tc::mbar_init(&ctl->fix_full[q], 1);
+      tc::mbar_init(&ctl->l_empty[q], 128);
+    }
+    for (int q = 0; q <= kVS; ++q) {
+      tc::mbar_init(&ctl->vl_full[q], 1);
+      tc::mbar_init(&ctl->v_ok[q], 4);
     }
     ctl->abort_flag = 0;
     tc::fence_barrier_init();
@@ -302,15 +356,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          tc::mbar_arrive_expect_tx(&ctl->v_full[st], kTile);
+          // the last block has a barrier of its own: the output warps wait for
+          // no other, and a waiter must visit every phase of a barrier.  Its
+          // next use, kVS + 1 units on, comes after this block's P.V
+          uint64_t* bar = j == cur.nkb - 1 ? &ctl->vl_full[i % (kVS + 1)] : &ctl->v_full[st];
+          tc::mbar_arrive_expect_tx(bar, kTile);
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
-            tc::tma_load_3d(sV + st * kTile + h * kHalf, &mapV, &ctl->v_full[st], 64 * h, cur.kvh,
+            tc::tma_load_3d(sV + st * kTile + h * kHalf, &mapV, bar, 64 * h, cur.kvh,
                             cur.t.row0 + j * kKB);
         }
       }
-      for (uint32_t c = (vc > (uint32_t)kVS ? vc - kVS : 0); c < vc; ++c)
-        tc::mbar_wait(&ctl->v_full[c % kVS], (c / kVS) & 1);
+      // every block is waited for before its P.V, and that before the CTA's end
     }
   } else if (warp == kWarpS) {
     // ------------------------------ S = Q K^T ------------------------------
@@ -351,113 +408,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kWarpPV) {
     // ------------------------------ O += P V ------------------------------
-    const uint32_t idesc_o = tc::idesc_bf16_f32(128, D, /*b_mn_major=*/true);
-    uint32_t vc = 0;
-    bool ok = true;
-    int part = 0;
-    for (int i = 0; unit_at(i) < n_units && ok; ++i) {
-      const Unit cur = unit_rec(a, table, unit_at(i), &part);
-      // O and the fix flag were last read by the output warps for unit i - kOBufs
-      const int ob = i % kOBufs;
-      const uint32_t o = tmem + kColO + ob * D;
-      if (!wait32(&ctl->o_empty[ob], ((i / kOBufs) & 1) ^ 1, ctl, a.err, W_O_EMPTY, 0)) break;
-      if (lane == 0) {
-        // the blocks before the last
-        for (int j = 0; j < cur.nkb - 1; ++j) {
-          const uint32_t c = vc + j;
-          const int st = c % kVS;
-          const uint32_t sb = c % kSBufs;
-          ok = wait1(&ctl->p_full[sb], (c / kSBufs) & 1, ctl, a.err, W_P_FULL, j) &&
-               wait1(&ctl->v_full[st], (c / kVS) & 1, ctl, a.err, W_V_FULL, j);
-          if (!ok) break;
+    if (lane == 0) {
+      const uint32_t idesc_o = tc::idesc_bf16_f32(128, D, /*b_mn_major=*/true);
+      uint32_t vc = 0, vph = 0;                        // vph: a parity bit per V stage
+      bool ok = true;
+      int part = 0;
+      for (int i = 0; unit_at(i) < n_units && ok; ++i) {
+        const Unit cur = unit_rec(a, table, unit_at(i), &part);
+        // O was last read by the output warps for unit i - kOBufs
+        const int ob = i % kOBufs;
+        const uint32_t o = tmem + kColO + ob * D;
+        if (!wait1(&ctl->o_empty[ob], ((i / kOBufs) & 1) ^ 1, ctl, a.err, W_O_EMPTY, 0)) break;
+        // P.V of block j, in every step of 16 keys or in the first ones
+        auto product = [&](int j, int keys) {
+          const int st = vc % kVS;
+          const uint32_t sb = vc % kSBufs;
           tc::tc_fence_after();
           const uint32_t vaddr = tc::smem_u32(sV + st * kTile);
           const uint32_t pa = tmem + sb * kKB;
 #pragma unroll
           for (int kk = 0; kk < kKB / 16; ++kk)
-            tc::mma_bf16_ts(o, pa + kk * 8, tc::smem_desc_mn128(vaddr + kk * 16 * 128, kHalf),
-                            idesc_o, (j | kk) != 0 ? 1u : 0u);
+            if (kk * 16 < keys)
+              tc::mma_bf16_ts(o, pa + kk * 8, tc::smem_desc_mn128(vaddr + kk * 16 * 128, kHalf),
+                              idesc_o, (j | kk) != 0 ? 1u : 0u);
           tc::mma_commit(&ctl->pv_done[sb]);
           tc::mma_commit(&ctl->v_empty[st]);
-        }
-      }
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      // the last block: its values are looked through while the softmax works
-      const int j = cur.nkb - 1, keys = block_keys(cur, j);
-      vc += j;
-      const int st = vc % kVS;
-      const uint32_t sb = vc % kSBufs;
-      uint8_t* v = sV + st * kTile;
-      ok = wait32(&ctl->v_full[st], (vc / kVS) & 1, ctl, a.err, W_V_FULL, j);
-      if (!ok) break;
-      {
-        // the rows after the tile's first one: 16-byte pieces, eight a lane at a time
-        constexpr int kPieces = D / 8;                 // of a row
-        const int row1 = cur.t.first + 1 - j * kKB, seen = cur.t.first + cur.t.rows - j * kKB;
-        auto piece = [&](int e) {                      // piece e of the rows from row1 on
-          const int n = row1 + e / kPieces, c = e % kPieces;
-          return reinterpret_cast<uint4*>(v + c / 8 * kHalf + n * 128) + c % 8;
+          ++vc;
         };
-        // 0 * x is 0 unless x is infinite or NaN
-        const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
-        __nv_bfloat162 sum[4] = {zero, zero, zero, zero};
-        const int n_seen = (seen - row1) * kPieces, n_all = (keys - row1) * kPieces;
-        for (int e0 = lane; e0 < n_seen; e0 += 8 * 32) {
-          uint4 x[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            x[k] = make_uint4(0, 0, 0, 0);
-            if (e0 + 32 * k < n_seen) x[k] = *piece(e0 + 32 * k);
-          }
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            sum[0] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x[k].x), zero, sum[0]);
-            sum[1] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x[k].y), zero, sum[1]);
-            sum[2] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x[k].z), zero, sum[2]);
-            sum[3] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x[k].w), zero, sum[3]);
-          }
+        for (int j = 0; j < cur.nkb - 1; ++j) {
+          const int st = vc % kVS;
+          ok = wait1(&ctl->p_full[vc % kSBufs], (vc / kSBufs) & 1, ctl, a.err, W_P_FULL, j) &&
+               wait1(&ctl->v_full[st], (vph >> st) & 1, ctl, a.err, W_V_FULL, j);
+          if (!ok) break;
+          vph ^= 1u << st;
+          product(j, kKB);
         }
-        const float2 t = __bfloat1622float2(__hadd2(__hadd2(sum[0], sum[1]), __hadd2(sum[2], sum[3])));
-        const bool found = __any_sync(0xffffffffu, !(t.x == 0.f && t.y == 0.f));
-        if (found || seen < keys) {                    // rare, or the request's last tile
-#pragma unroll 1
-          for (int e = found ? lane : n_seen + lane; e < n_all; e += 32) {
-            uint4 x = make_uint4(0, 0, 0, 0);          // behind the tile's last row
-            if (e < n_seen) {
-              x = *piece(e);
-              x.x = drop_nonfinite(x.x);
-              x.y = drop_nonfinite(x.y);
-              x.z = drop_nonfinite(x.z);
-              x.w = drop_nonfinite(x.w);
-            }
-            *piece(e) = x;
-          }
-          tc::fence_proxy_async_smem();
-        }
-        __syncwarp();
-        if (lane == 0) {
-          ctl->fix[ob] = found;
-          tc::mbar_arrive(&ctl->fix_full[ob]);
-        }
-      }
-      ok = wait32(&ctl->p_full[sb], (vc / kSBufs) & 1, ctl, a.err, W_P_FULL, j);
-      if (!ok) break;
-      if (lane == 0) {
-        tc::tc_fence_after();
-        const uint32_t vaddr = tc::smem_u32(v);
-        const uint32_t pa = tmem + sb * kKB;
-#pragma unroll
-        for (int kk = 0; kk < kKB / 16; ++kk)
-          if (kk * 16 < keys)
-            tc::mma_bf16_ts(o, pa + kk * 8, tc::smem_desc_mn128(vaddr + kk * 16 * 128, kHalf),
-                            idesc_o, (j | kk) != 0 ? 1u : 0u);
-        tc::mma_commit(&ctl->pv_done[sb]);
-        tc::mma_commit(&ctl->v_empty[st]);
+        if (!ok) break;
+        const int j = cur.nkb - 1, vs = i % (kVS + 1);
+        const uint32_t ph = (i / (kVS + 1)) & 1;
+        ok = wait1(&ctl->vl_full[vs], ph, ctl, a.err, W_VL_FULL, j) &&
+             wait1(&ctl->v_ok[vs], ph, ctl, a.err, W_V_OK, j) &&
+             wait1(&ctl->p_full[vc % kSBufs], (vc / kSBufs) & 1, ctl, a.err, W_P_FULL, j);
+        if (!ok) break;
+        product(j, block_keys(cur, j));
         tc::mma_commit(&ctl->o_full[ob]);
       }
-      __syncwarp();
-      ++vc;
     }
   } else if (warp < kWarpOut) {
     // ------------------------------- softmax -------------------------------
@@ -587,13 +582,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
       l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
       l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-      // the row sums of unit i, once the output warps are done with unit i - kOBufs
-      if (!wait32(&ctl->o_empty[ob], ((i / kOBufs) & 1) ^ 1, ctl, a.err, W_O_EMPTY, cur.nkb)) break;
+      // the row sums of unit i, once the output warps have read those of unit i - kLBufs
+      const int lb = i % kLBufs;
+      if (!wait32(&ctl->l_empty[lb], ((i / kLBufs) & 1) ^ 1, ctl, a.err, W_L_EMPTY, cur.nkb)) break;
       if (c4 == 0) {
-        ctl->xl[ob][R0] = l0;
-        ctl->xl[ob][R1] = l1;
+        ctl->xl[lb][R0] = l0;
+        ctl->xl[lb][R1] = l1;
       }
-      tc::mbar_arrive(&ctl->l_full[ob]);
+      tc::mbar_arrive(&ctl->l_full[lb]);
     }
   } else {
     // ---------------------------- output O / l ----------------------------
@@ -601,18 +597,90 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int m = quarter * 32 + lane;
     const int rl = m >> a.g_log2;
     const int hh = m & (a.g - 1);
+    // Looks the values of unit i's last block through, each warp every fourth
+    // group of rows, before the P.V of that block.
+    uint32_t vc = 0;                                   // V blocks of the units looked through
+    auto look = [&](const Unit& u, int i) -> bool {
+      const int vs = i % (kVS + 1), j = u.nkb - 1, keys = block_keys(u, j);
+      if (!wait32(&ctl->vl_full[vs], (i / (kVS + 1)) & 1, ctl, a.err, W_VL_FULL, j)) return false;
+      // a lane takes the same 16-byte piece of every kStep-th row after the
+      // tile's first one
+      constexpr int kPieces = D / 8, kStep = 4 * 32 / kPieces;
+      const int row1 = u.t.first + 1 - j * kKB, seen = u.t.first + u.t.rows - j * kKB;
+      const int c = lane % kPieces, n0 = quarter * (32 / kPieces) + lane / kPieces;
+      uint8_t* at = sV + (vc + j) % kVS * kTile + c / 8 * kHalf + c % 8 * 16;
+      // 0 * x is 0 unless x is infinite or NaN
+      const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+      __nv_bfloat162 sum[4] = {zero, zero, zero, zero};
+      for (int n = row1 + n0; n < seen; n += 4 * kStep) {
+        const uint8_t* p = at + n * 128;
+        uint4 x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          x[k] = make_uint4(0, 0, 0, 0);
+          if (n + k * kStep < seen) x[k] = *reinterpret_cast<const uint4*>(p + k * kStep * 128);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          sum[0] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x[k].x), zero, sum[0]);
+          sum[1] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x[k].y), zero, sum[1]);
+          sum[2] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x[k].z), zero, sum[2]);
+          sum[3] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x[k].w), zero, sum[3]);
+        }
+      }
+      const float2 t = __bfloat1622float2(__hadd2(__hadd2(sum[0], sum[1]), __hadd2(sum[2], sum[3])));
+      const bool found = __any_sync(0xffffffffu, !(t.x == 0.f && t.y == 0.f));
+      if (found || seen < keys) {                      // rare, or the request's last tile
+#pragma unroll 1
+        for (int n = row1 + n0; n < keys; n += kStep) {
+          uint4* p = reinterpret_cast<uint4*>(at + n * 128);
+          uint4 x = make_uint4(0, 0, 0, 0);            // behind the tile's last row
+          if (n < seen) {
+            if (!found) continue;
+            x = *p;
+            x.x = drop_nonfinite(x.x);
+            x.y = drop_nonfinite(x.y);
+            x.z = drop_nonfinite(x.z);
+            x.w = drop_nonfinite(x.w);
+          }
+          *p = x;
+        }
+        tc::fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) {
+        ctl->fix[vs][quarter] = found;
+        tc::mbar_arrive(&ctl->v_ok[vs]);
+      }
+      vc += u.nkb;
+      return true;
+    };
     int part = 0;
+    Unit nxt = unit_rec(a, table, unit_at(0), &part);
+    bool looked = false;                               // unit nxt
     for (int i = 0; unit_at(i) < n_units; ++i) {
-      const Unit cur = unit_rec(a, table, unit_at(i), &part);
+      const Unit cur = nxt;
+      // The next unit's values are looked through before this one's output,
+      // unless they wait for it: a last block whose buffer an earlier block of
+      // its own unit has to give up first
+      const bool more = unit_at(i + 1) < n_units;
+      if (more) nxt = unit_rec(a, table, unit_at(i + 1), &part);
+      const bool early = more && nxt.nkb <= kVS;
+      bool ok = true;
+#pragma unroll 1
+      for (int k = looked ? i + 1 : i; ok && k <= (early ? i + 1 : i); ++k) ok = look(k == i ? cur : nxt, k);
+      if (!ok) break;
+      looked = early;
       const int ob = i % kOBufs;
       const uint32_t ph = (i / kOBufs) & 1;
       const uint32_t tO = tmem + ((uint32_t)(quarter * 32) << 16) + kColO + ob * D;
       if (!wait32(&ctl->o_full[ob], ph, ctl, a.err, W_O_FULL, cur.nkb)) break;
-      if (!wait32(&ctl->l_full[ob], ph, ctl, a.err, W_L_FULL, cur.nkb)) break;
-      if (!wait32(&ctl->fix_full[ob], ph, ctl, a.err, W_FIX, cur.nkb)) break;
+      const int lb = i % kLBufs, vs = i % (kVS + 1);
+      if (!wait32(&ctl->l_full[lb], (i / kLBufs) & 1, ctl, a.err, W_L_FULL, cur.nkb)) break;
       tc::tc_fence_after();
-      const float inv = 1.f / ctl->xl[ob][m];
-      const bool fix = ctl->fix[ob] != 0;
+      const float inv = 1.f / ctl->xl[lb][m];
+      const bool fix = (ctl->fix[vs][0] | ctl->fix[vs][1] | ctl->fix[vs][2] | ctl->fix[vs][3]) != 0;
+      tc::mbar_arrive(&ctl->l_empty[lb]);
       const bool valid = rl < cur.t.rows;
       const int64_t row = cur.t.row0 + cur.t.first;
       __nv_bfloat16* dst = a.O + ((row + rl) * a.Hq + cur.kvh * a.g + hh) * D;
@@ -628,17 +696,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int e = 0; e < 64; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * inv);
-        if (fix && valid) {
-          // elements that are not finite, of the rows that this one sees
-          for (int n = 1; n <= rl; ++n) {
-            const __nv_bfloat16* v = a.V + ((row + n) * a.Hkv + cur.kvh) * D + c;
-#pragma unroll
-            for (int e = 0; e < 64; ++e) {
-              const float x = __bfloat162float(v[e]);
-              if (!isfinite(x)) r[e] = __float_as_uint(__uint_as_float(r[e]) + x);
-            }
-          }
-        }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint32_t w[8];
@@ -659,12 +716,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();                                  // the loads are warp-collective
       }
+      if (fix && valid)                                // of the tile's rows that this one sees
+        add_nonfinite(dst, a.V + ((row + 1) * a.Hkv + cur.kvh) * D, rl, (int64_t)a.Hkv * D, D);
     }
   }
 
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
+  if (ctl->abort_flag)                                 // copies and products in flight get time to end
+    for (int k = 0; k < 1000; ++k) __nanosleep(1000);
   if (warp == kWarpS) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
