@@ -208,14 +208,15 @@ struct RawQuery {
 template <int D>
 __device__ __forceinline__ void read_query(const AttendArgs& a, int r, int h, int vg, RawQuery& x) {
   constexpr int NP = D / 64;
-  const int lane = threadIdx.x % 32, n_vec = a.g * a.n_new;
+  const int lane = threadIdx.x % 32, n_vec = a.g * a.n_new, gl = __ffs(a.g) - 1;   // g = 1, 2, 4, 8
+  const __nv_bfloat16* q0 = reinterpret_cast<const __nv_bfloat16*>(a.Q) + NP * lane +
+                            ((int64_t)r * a.n_new * a.n_q_heads + h * a.g) * D;
 #pragma unroll
   for (int v = 0; v < kVecs; ++v) {
     const int vi = vg * kVecs + v;
     x.lo[v] = x.hi[v] = 0;
     if (vi < n_vec) {                                  // warp-uniform
-      const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.Q) + NP * lane +
-                               ((int64_t)(r * a.n_new + vi / a.g) * a.n_q_heads + h * a.g + vi % a.g) * D;
+      const __nv_bfloat16* q = q0 + ((vi >> gl) * a.n_q_heads + (vi & (a.g - 1))) * D;
       if constexpr (NP == 2) {
         x.lo[v] = *reinterpret_cast<const uint32_t*>(q);
         x.hi[v] = *reinterpret_cast<const uint32_t*>(q + D / 2);
@@ -269,8 +270,8 @@ template <int ST, int D> struct Feed {
     for (int r = 0; r < F::ROWS; ++r)
       if (y.table && inside(r)) id[r] = y.table[blk[r]];
   }
-  // Copies the next slot.  kMarked: the selected keys are known.
-  template <bool kMarked> __device__ __forceinline__ void copy() {
+  // Copies the next slot.  marked: the selected keys are known.
+  __device__ __forceinline__ void copy(bool marked) {
     bool whole = !y.table;
 #pragma unroll
     for (int r = 0; r < F::ROWS; ++r) {
@@ -284,7 +285,7 @@ template <int ST, int D> struct Feed {
         }
       }
       const int k = slot * TOK + r * 32;
-      uint32_t skip = kMarked ? sm.skip[k >> 5] : 0u;
+      uint32_t skip = marked ? sm.skip[k >> 5] : 0u;
       if constexpr (TOK < 32) skip >>= k & 31;
       if constexpr (!F::coded)                         // what is not seen may hold anything
         if (skip >> lane & 1) row[r] = -1;
@@ -367,7 +368,7 @@ __device__ __forceinline__ void load_query(const AttendArgs& a, const Item& y, c
   constexpr uint32_t kAll = 0xffffffffu;
   constexpr int NP = D / 64;
   const int lane = threadIdx.x % 32, gid = lane >> 2, tig = lane & 3;
-  const int n_vec = a.g * a.n_new - y.vg * kVecs, j0 = NP * lane;
+  const int j0 = NP * lane;
   float k0[NP], k1[NP], z0[NP], z1[NP];
   if constexpr (F::coded) {
     ks += y.h * D + j0;
@@ -381,23 +382,22 @@ __device__ __forceinline__ void load_query(const AttendArgs& a, const Item& y, c
     }
     feed.mark_selected();                              // its reads run beside those above
   }
+  // a loop over the vectors, not eight copies of its body: an item runs
+  // through this once, and fetching the instructions took longer than they do
   uint32_t* sq = reinterpret_cast<uint32_t*>(feed.sm.slot[1]);
+  uint2* own = reinterpret_cast<uint2*>(sq + kVecs * D) + lane;   // [vector][lane]: its channels, then its sum
   sscale = 1.f;
   cst = 0.f;
-  float z[kVecs];
 #pragma unroll
+  for (int v = 0; v < kVecs; ++v) own[v * 32] = make_uint2(raw.lo[v], raw.hi[v]);
+#pragma unroll 2
   for (int v = 0; v < kVecs; ++v) {
-    z[v] = 0.f;
-    if (v >= n_vec) {                                  // warp-uniform: no such vector
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) sq[q_word<D>(v, lane + 32 * i)] = 0;
-      continue;
-    }
-    float x[NP][2], mx = 0.f;
+    const uint2 w = own[v * 32];                       // 0: no such vector
+    float x[NP][2], mx = 0.f, z = 0.f;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const float q0 = (i ? bf16_hi(raw.lo[v]) : bf16_lo(raw.lo[v])) * a.scale;
-      const float q1 = (i ? bf16_hi(raw.hi[v]) : bf16_lo(raw.hi[v])) * a.scale;
+      const float q0 = (i ? bf16_hi(w.x) : bf16_lo(w.x)) * a.scale;
+      const float q1 = (i ? bf16_hi(w.y) : bf16_lo(w.y)) * a.scale;
       x[i][0] = q0;
       x[i][1] = q1;
       if (cs) {
@@ -406,7 +406,7 @@ __device__ __forceinline__ void load_query(const AttendArgs& a, const Item& y, c
         x[i][1] = q1 * t.x - q0 * t.y;
       }
       if constexpr (F::coded) {
-        z[v] += x[i][0] * z0[i] + x[i][1] * z1[i];
+        z += x[i][0] * z0[i] + x[i][1] * z1[i];
         x[i][0] *= k0[i];
         x[i][1] *= k1[i];
         mx = fmaxf(mx, fmaxf(fabsf(x[i][0]), fabsf(x[i][1])));
@@ -414,6 +414,7 @@ __device__ __forceinline__ void load_query(const AttendArgs& a, const Item& y, c
     }
     float up = 1.f;
     if constexpr (F::coded) {
+      own[v * 32].x = __float_as_uint(z);
       // fp16 parts want the largest element near 2^12: a power of two apart
       const uint32_t mb = __reduce_max_sync(kAll, __float_as_uint(mx));
       const int e = min(max((int)(mb >> 23), 27), 230);
@@ -438,23 +439,15 @@ __device__ __forceinline__ void load_query(const AttendArgs& a, const Item& y, c
         sq[q_word<D>(v, ch)] = w;
       }
   }
+  __syncwarp();
   if constexpr (F::coded) {
-    // the eight sums over the lanes, halving the vectors a lane carries:
-    // vector gid ends up in its four lanes
+    // the sum over the lanes of vector gid: eight of them a lane
+    const float* part = reinterpret_cast<const float*>(own - lane + gid * 32 + tig * 8);
 #pragma unroll
-    for (int n = 4; n > 0; n >>= 1) {
-      const bool upper = lane & (4 * n);
-#pragma unroll
-      for (int v = 0; v < n; ++v) {
-        const float give = upper ? z[v] : z[v + n];
-        z[v] = (upper ? z[v + n] : z[v]) + __shfl_xor_sync(kAll, give, 4 * n);
-      }
-    }
-    cst = z[0];
+    for (int i = 0; i < 8; ++i) cst += part[2 * ((i + gid) & 7)];
     cst += __shfl_xor_sync(kAll, cst, 1);
     cst += __shfl_xor_sync(kAll, cst, 2);
   }
-  __syncwarp();
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
@@ -495,7 +488,7 @@ __device__ __forceinline__ void attend_codes(const AttendArgs& a, const Item& y,
       }
     }
   };
-  feed.template copy<false>();
+  feed.copy(false);
   load_sz();
   uint32_t q[D / 16][4];
   uint64_t ss, sb;                                     // sscale and cst of the lane's two vectors
@@ -529,7 +522,7 @@ __device__ __forceinline__ void attend_codes(const AttendArgs& a, const Item& y,
       top = max(top, w & 0x7fffu);
     }
     if (s + 1 < n_slots) {
-      feed.template copy<true>();
+      feed.copy(true);
       load_sz();
     }
     top = __reduce_max_sync(kAll, top);
@@ -735,7 +728,7 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Item& y, 
   const int n_slots = (y.t1 - y.t0 + TOK - 1) / TOK;
   Feed<ST, D> feed(a, y, sm);
   feed.mark_selected();
-  feed.template copy<true>();
+  feed.copy(true);
   uint32_t q[D / 16][4];
   float one, none;
   load_query<ST, D>(a, y, raw, cs, nullptr, nullptr, feed, q, one, none);
@@ -750,7 +743,7 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Item& y, 
     cp_wait<0>();                                      // the slot has landed
     __syncwarp();                                      // ... for every lane; the one before is done with
     const uint32_t keep = sm.keep[s & 1][0];
-    if (s + 1 < n_slots) feed.template copy<true>();
+    if (s + 1 < n_slots) feed.copy(true);
     const uint8_t* kb = sm.slot[s & 1] + gid * RB;
     const uint8_t* vb = sm.slot[s & 1] + TOK * RB;
     float sc[2][2];                                    // keys 8 n + 2 tig, + 1
@@ -848,15 +841,18 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
   Item y;
   const int ctas = (a.nsub * per_seg + kWarps - 1) / kWarps;
   const int b = (int)blockIdx.x - ctas * a.n_chunks;
-  if (b >= 0) {
+  // the queries are read first: they do not depend on the tables' entries
+  const bool side = b >= 0;
+  const int ci = side ? 0 : blockIdx.x / ctas;
+  const int i = (side ? b % side_ctas : blockIdx.x % ctas) * kWarps + warp;
+  const int seg = i / per_seg;
+  y.h = i % per_seg / a.nvg;
+  y.vg = i % a.nvg;
+  y.r = side ? a.req0 + b / side_ctas : owners.req[ci];
+  RawQuery rq;
+  read_query<D>(a, y.r, y.h, y.vg, rq);
+  if (side) {
     // side rows: those before the new tokens
-    y.r = a.req0 + b / side_ctas;
-    const int i = (b % side_ctas) * kWarps + warp;
-    const int seg = i / per_seg;
-    y.h = i % per_seg / a.nvg;
-    y.vg = i % a.nvg;
-    RawQuery rq;
-    if (seg < a.nside) read_query<D>(a, y.r, y.h, y.vg, rq);
     const fuse_request_t R = a.reqs[y.r];
     const int n = R.k + R.n_query - a.n_new;
     y.t0 = seg * a.sseg;
@@ -880,15 +876,6 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
     attend_rows<D>(a, y, rq, nullptr, sm);
     return;
   }
-  const int ci = blockIdx.x / ctas;
-  const int i = (blockIdx.x % ctas) * kWarps + warp;
-  const int seg = i / per_seg;
-  y.h = i % per_seg / a.nvg;
-  y.vg = i % a.nvg;
-  // the queries are read first: they do not depend on the tables' entries
-  y.r = owners.req[ci];
-  RawQuery rq;
-  if (seg < a.nsub) read_query<D>(a, y.r, y.h, y.vg, rq);
   const fuse_chunk_t C = a.chunks[a.chunk0 + ci];
   const fuse_request_t R = a.reqs[y.r];
   // the chunk's angles, D / 16 pairs a warp.  The frequencies are launch
