@@ -300,28 +300,39 @@ template <int ST, int D> struct Feed {
       }
     }
     const uint32_t dk = (uint32_t)__cvta_generic_to_shared(sm.slot[buf]), dv = dk + TOK * RB;
+    // four 16-byte pieces of K and of V a lane and turn; the order within rows
+    // repeats every 8 keys, so a turn (8 keys or a multiple) only moves on
+    constexpr int kTurns = TOK * RC / 128;
+    // pages: a loop where its code counts (24.5 -> 23.5 us on 4 drafted tokens
+    // at 8 bits); at 4 bits it costs registers that the products need (92 -> 104
+    // us on 8 requests of 33k tokens)
+    constexpr int kUnroll = F::ROWS == 1 ? 1 : kTurns;
     if (whole) {                                       // warp-uniform: TOK consecutive rows
       const int64_t off = (int64_t)(y.t0 + slot * TOK + lane / RC) * stride + lane % RC * 16;
       const uint8_t *pk = y.k + off, *pv = y.v + off;
 #pragma unroll
-      for (int i = 0; i < TOK * RC / 32; ++i) {
-        const int key = (i * 32 + lane) / RC, c = (i * 32 + lane) % RC;
-        const int vr = v_row(key);
-        cp16(dk + key * RB + k_chunk<RC>(key, c) * 16, pk, true);
-        cp16(dv + vr * RB + v_chunk<RC>(vr, c) * 16, pv, true);
-        pk += (32 / RC) * stride;
-        pv += (32 / RC) * stride;
-      }
-    } else {
+      for (int o = 0; o < kTurns; ++o)
 #pragma unroll
-      for (int i = 0; i < TOK * RC / 32; ++i) {
-        const int key = (i * 32 + lane) / RC, c = (i * 32 + lane) % RC;
-        const int kr = __shfl_sync(kAll, row[i * 32 / RC / 32], key & 31);
-        const int64_t off = (int64_t)max(kr, 0) * stride + c * 16;
-        cp16(dk + key * RB + k_chunk<RC>(key, c) * 16, y.k + off, kr >= 0);
-        const int vr = v_row(key);
-        cp16(dv + vr * RB + v_chunk<RC>(vr, c) * 16, y.v + off, kr >= 0);
-      }
+        for (int i = 0; i < 4; ++i) {
+          const int key = (i * 32 + lane) / RC, c = (i * 32 + lane) % RC, vr = v_row(key);
+          cp16(dk + o * 2048 + key * RB + k_chunk<RC>(key, c) * 16, pk, true);
+          cp16(dv + o * 2048 + vr * RB + v_chunk<RC>(vr, c) * 16, pv, true);
+          pk += (32 / RC) * stride;
+          pv += (32 / RC) * stride;
+        }
+    } else {
+#pragma unroll kUnroll
+      for (int o = 0; o < kTurns; ++o)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = (i * 32 + lane) / RC, c = (i * 32 + lane) % RC, vr = v_row(key);
+          // rows are held by 32 keys: a turn's number or a constant says which
+          const int of = F::ROWS == 1 ? row[0] : 128 / RC == 32 ? (o ? row[F::ROWS - 1] : row[0]) : row[i * 32 / RC / 32];
+          const int kr = __shfl_sync(kAll, of, (o * (128 / RC) + key) & 31);
+          const int64_t off = (int64_t)max(kr, 0) * stride + c * 16;
+          cp16(dk + o * 2048 + key * RB + k_chunk<RC>(key, c) * 16, y.k + off, kr >= 0);
+          cp16(dv + o * 2048 + vr * RB + v_chunk<RC>(vr, c) * 16, y.v + off, kr >= 0);
+        }
     }
     cp_commit();
     ++slot;
