@@ -310,12 +310,12 @@ __global__ void __launch_bounds__(kWarps * 32)
 
 // Joins the items of one query vector (blockIdx.x = new token * Hq + head)
 // of one request with the new tokens' own keys, and writes its output row.
-// An item's row is read by D / 4 lanes, four items a lane in flight; the
-// weights of up to kJoinTile items are formed first.  Latency bounds it (two
+// An item's row is read by D / 4 lanes, kRows items a lane in flight.  Latency bounds it (two
 // dependent reads), so what does not depend on the items (the table entry,
 // the own keys) is read before they are waited for.
 constexpr int kJoinThreads = 512;
 constexpr int kJoinTile = 512;            // items whose weights are held at a time
+constexpr int kRows = 4;                  // items' rows of a lane in flight
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
@@ -384,6 +384,18 @@ __global__ void __launch_bounds__(kJoinThreads)
     const int cnt = min(kJoinTile, n - e0);
     float2 ml = make_float2(-INFINITY, 0.f);
     if (tid < cnt) ml = a.part_ml[part(e0 + tid)];
+    // the first rows are read beside the weights, not after them; what an item
+    // without a key left there (nothing) is not used
+    const int e1 = warp * kSub + sub;
+    float4 x[kRows];
+    auto rows = [&](int e) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int ei = e + i * kWarpsJ * kSub;
+        if (ei < cnt) x[i] = *reinterpret_cast<const float4*>(a.part_o + part(e0 + ei) * D + ch);
+      }
+    };
+    rows(e1);
     float t = ml.x;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
@@ -406,18 +418,14 @@ __global__ void __launch_bounds__(kJoinThreads)
     acc.z *= al;
     acc.w *= al;
     __syncthreads();
-    for (int e = warp * kSub + sub; e < cnt; e += 4 * kWarpsJ * kSub) {
-      float4 x[4];
-      float we[4];
+    for (int e = e1; e < cnt; e += kRows * kWarpsJ * kSub) {
+      if (e != e1) rows(e);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kRows; ++i) {
         const int ei = e + i * kWarpsJ * kSub;
-        we[i] = ei < cnt ? s_w[ei] : -1.f;
-        if (we[i] != -1.f) x[i] = *reinterpret_cast<const float4*>(a.part_o + part(e0 + ei) * D + ch);
+        const float we = ei < cnt ? s_w[ei] : -1.f;
+        if (we != -1.f) add4(acc, we, x[i]);
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (we[i] != -1.f) add4(acc, we[i], x[i]);
     }
   }
   if (warp <= u && lane < L) {

@@ -200,6 +200,34 @@ __device__ __forceinline__ int warp_search(const int32_t* a, int n, int x) {
   return lo;
 }
 
+// The angles by which a chunk's items turn their queries back, shared by the
+// CTA: each warp forms D / 16 pairs, and load_query waits for all of them.
+// Side rows have none.
+struct Angles {
+  float2* at;                                          // (cos, sin) of each channel pair
+  int pos;                                             // the chunk's offset
+  bool chunk;                                          // block-uniform
+};
+template <int D> __device__ __forceinline__ void form_angles(const Angles& cs, const RopeFreqs& f) {
+  if (cs.pos == 0) return;                             // block-uniform
+  constexpr int N = D / 2 / kWarps;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // the frequencies are launch parameters, which a warp reads fast only at
+  // one address at a time
+  float hi = 0.f, mid = 0.f, lo = 0.f, c, sn;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const float h = f.hi[warp * N + k], m = f.mid[warp * N + k], l = f.lo[warp * N + k];
+    if (lane == k) {
+      hi = h;
+      mid = m;
+      lo = l;
+    }
+  }
+  rope_cos_sin(cs.pos, hi, mid, lo, c, sn);
+  if (lane < N) cs.at[warp * N + lane] = make_float2(c, sn);
+}
+
 // The query vectors of an item as they are: the lane's channel pairs
 // (j, j + D / 2), j = NP lane .. NP lane + NP - 1, NP = D / 64 to a register.
 struct RawQuery {
@@ -365,14 +393,14 @@ template <int ST, int D> struct Feed {
   }
 };
 
-// The item's query vectors, turned back by the chunk's angles (cs, NULL: not
+// The item's query vectors, turned back by the chunk's angles (position 0: not
 // turned) and scaled, as operand registers: qo[kk][b] holds the channel pair
 // of half b of K-step kk of vector gid, its high parts, and qo[kk][2 + b] what
 // is left of them.  Beside codes: score = sum * sscale + cst (vector gid).
 // Staged in the second buffer, which is not in flight yet.
 template <int ST, int D>
 __device__ __forceinline__ void load_query(const AttendArgs& a, const Item& y, const RawQuery& raw,
-                                           const float2* cs, const __half* ks, const __half* kz,
+                                           const Angles& cs, const __half* ks, const __half* kz,
                                            Feed<ST, D>& feed, uint32_t (&qo)[D / 16][4],
                                            float& sscale, float& cst) {
   using F = Fmt<ST, D>;
@@ -393,6 +421,7 @@ __device__ __forceinline__ void load_query(const AttendArgs& a, const Item& y, c
     }
     feed.mark_selected();                              // its reads run beside those above
   }
+  if (cs.chunk) __syncthreads();                       // every warp's angles
   // a loop over the vectors, not eight copies of its body: an item runs
   // through this once, and fetching the instructions took longer than they do
   uint32_t* sq = reinterpret_cast<uint32_t*>(feed.sm.slot[1]);
@@ -411,8 +440,8 @@ __device__ __forceinline__ void load_query(const AttendArgs& a, const Item& y, c
       const float q1 = (i ? bf16_hi(w.y) : bf16_lo(w.y)) * a.scale;
       x[i][0] = q0;
       x[i][1] = q1;
-      if (cs) {
-        const float2 t = cs[j0 + i];
+      if (cs.pos != 0) {
+        const float2 t = cs.at[j0 + i];
         x[i][0] = q0 * t.x + q1 * t.y;
         x[i][1] = q1 * t.x - q0 * t.y;
       }
@@ -478,8 +507,8 @@ __device__ __forceinline__ void load_query(const AttendArgs& a, const Item& y, c
 // so a lane's scores, sums and outputs belong to vectors 2 tig and 2 tig + 1.
 template <int ST, int D>
 __device__ __forceinline__ void attend_codes(const AttendArgs& a, const Item& y, const RawQuery& raw,
-                                             const float2* cs, const __half* ks, const __half* kz,
-                                             WarpSmem<D>& sm) {
+                                             const Angles& cs, const RopeFreqs& f, const __half* ks,
+                                             const __half* kz, WarpSmem<D>& sm) {
   using F = Fmt<ST, D>;
   constexpr int RB = F::RB, RC = F::RC, TOK = F::TOK, NT = TOK / 8, MT = D / 16;
   constexpr uint32_t kAll = 0xffffffffu;
@@ -501,6 +530,7 @@ __device__ __forceinline__ void attend_codes(const AttendArgs& a, const Item& y,
   };
   feed.copy(false);
   load_sz();
+  form_angles<D>(cs, f);                               // while the first keys are on their way
   uint32_t q[D / 16][4];
   uint64_t ss, sb;                                     // sscale and cst of the lane's two vectors
   {
@@ -730,7 +760,7 @@ __device__ __forceinline__ void attend_codes(const AttendArgs& a, const Item& y,
 // A lane's scores belong to vector gid, its outputs to 2 tig and 2 tig + 1.
 template <int D>
 __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Item& y, const RawQuery& raw,
-                                            const float2* cs, WarpSmem<D>& sm) {
+                                            const Angles& cs, const RopeFreqs& f, WarpSmem<D>& sm) {
   constexpr int ST = FUSE_BF16;
   using F = Fmt<ST, D>;
   constexpr int RB = F::RB, RC = F::RC, TOK = F::TOK, MT = D / 16;
@@ -740,6 +770,7 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Item& y, 
   Feed<ST, D> feed(a, y, sm);
   feed.mark_selected();
   feed.copy(true);
+  form_angles<D>(cs, f);
   uint32_t q[D / 16][4];
   float one, none;
   load_query<ST, D>(a, y, raw, cs, nullptr, nullptr, feed, q, one, none);
@@ -884,33 +915,17 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
           report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_ATTEND_SEL, (uint32_t)t);
       }
     }
-    attend_rows<D>(a, y, rq, nullptr, sm);
+    attend_rows<D>(a, y, rq, {nullptr, 0, false}, f, sm);
     return;
   }
   const fuse_chunk_t C = a.chunks[a.chunk0 + ci];
   const fuse_request_t R = a.reqs[y.r];
-  // the chunk's angles, D / 16 pairs a warp.  The frequencies are launch
-  // parameters, which a warp reads fast only at one address at a time.
-  if (C.pos != 0) {                        // block-uniform
-    constexpr int N = D / 2 / kWarps;
-    float hi = 0.f, mid = 0.f, lo = 0.f, c, sn;
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const float h = f.hi[warp * N + k], m = f.mid[warp * N + k], l = f.lo[warp * N + k];
-      if (lane == k) {
-        hi = h;
-        mid = m;
-        lo = l;
-      }
-    }
-    rope_cos_sin(C.pos, hi, mid, lo, c, sn);
-    if (lane < N) s_cs[warp * N + lane] = make_float2(c, sn);
-  }
-  __syncthreads();
   y.t0 = seg * a.seg;
-  if (seg >= a.nsub) return;
-  if (y.t0 >= C.len) {                     // past the chunk's end: an item without a key
-    if (lane < kVecs)
+  const Angles cs{s_cs, C.pos, true};
+  if (seg >= a.nsub || y.t0 >= C.len) {    // past the chunk's end: an item without a key
+    form_angles<D>(cs, f);                 // this warp's part for the others
+    __syncthreads();
+    if (seg < a.nsub && lane < kVecs)
       a.part_ml[(((int64_t)(a.chunk0 + ci) * a.nsub + seg) * per_seg + i % per_seg) * kVecs + lane] =
           make_float2(-INFINITY, 0.f);
     return;
@@ -926,11 +941,10 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
   y.skip = a.idx + R.sel0;
   y.pos0 = (int)(C.dst_row - R.row0);
   y.slot = (int64_t)(a.chunk0 + ci) * a.nsub + seg;
-  const float2* cs = C.pos != 0 ? s_cs : nullptr;
   if constexpr (ST == FUSE_BF16)
-    attend_rows<D>(a, y, rq, cs, sm);
+    attend_rows<D>(a, y, rq, cs, f, sm);
   else
-    attend_codes<ST, D>(a, y, rq, cs, reinterpret_cast<const __half*>(C.k_scale),
+    attend_codes<ST, D>(a, y, rq, cs, f, reinterpret_cast<const __half*>(C.k_scale),
                         reinterpret_cast<const __half*>(C.k_zero), sm);
 }
 
