@@ -310,12 +310,16 @@ __global__ void __launch_bounds__(kWarps * 32)
 
 // Joins the items of one query vector (blockIdx.x = new token * Hq + head)
 // of one request with the new tokens' own keys, and writes its output row.
-// An item's row is read by D / 4 lanes, kRows items a lane in flight.  Latency bounds it (two
-// dependent reads), so what does not depend on the items (the table entry,
-// the own keys) is read before they are waited for.
-constexpr int kJoinThreads = 512;
-constexpr int kJoinTile = 512;            // items whose weights are held at a time
+// An item's row is read by D / 4 lanes, kRows items a lane in flight.  Latency
+// bounds it (two dependent reads), so what does not depend on the items (the
+// table entry, the own keys) is read before they are waited for, and the first
+// rows beside the weights.  256 threads, so that the blocks of 16 requests fit
+// the card at once: with 512 the 16 paged requests took 38 us instead of 36,
+// with 128 one request took 12 instead of 11.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinTile = kJoinThreads;   // items whose weights are held at a time
 constexpr int kRows = 4;                  // items' rows of a lane in flight
+static_assert(kJoinThreads / 32 >= FUSE_ATTEND_MAX_NEW, "a warp takes a new token's own key");
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
@@ -532,10 +536,11 @@ fuse_status_t plan_attend(const fuse_layer_desc_t* desc, const fuse_chunks_t* ch
   const int64_t per = (int64_t)desc->n_kv_heads * P->nvg;
   // Shorter segments share less of an item's start (its query vectors, the
   // join), longer ones leave warps idle at the end.  bf16 layers, at least 64
-  // keys: 8 chunks of 512 take 12 us, with 192 keys 14; 16 requests of 0.5k
-  // to 8k tokens 41 us at the rule's 256, 48 at 128; 8 of 33k 96 us at 1024,
-  // 105 at 512.  Side rows go to half as many items (96 us against 99).  fp32 layers,
-  // whose lane takes a key: 15 us with 32 keys an item, 21 with 64.
+  // keys: 8 chunks of 512 take 11 us, with 192 keys 13; 16 requests of 0.5k to
+  // 8k tokens at the rule's 256 keys 39 us, at 128 45; 8 of 33k at 1024 keys 92
+  // us, at 512 100.  Side rows go to half as many items (92 us; as many: 94, a
+  // quarter: 100).  fp32 layers, whose lane takes a key: 14 us with 32 keys an
+  // item, 21 with 64.
   const int least = desc->dtype == FUSE_BF16 ? 64 : 32;
   const int seg = cut(n_ctx * per, kItems, least);
   P->nsub = std::max(1, (max_len + seg - 1) / seg);

@@ -22,14 +22,16 @@
 // normaliser are raised lazily.
 //
 // Measured with the join (4 bits, 8 KV heads, d = 128, 64 query heads): 8
-// requests of 33k tokens 96 us, 3.8 TB/s, where the bytes alone would take
+// requests of 33k tokens 89 us, 4.1 TB/s, where the bytes alone would take
 // 54; issue slots are two fifths full and a warp waits for its own results, not
-// for HBM.  16 paged requests of 0.5k to 8k tokens 41 us, 8 chunks of 512
-// tokens 12 us (latency).  Chunks go before side rows, whose items are shorter
-// and fill the end (105 us the other way round).  Slots of half the keys in three
-// buffers took 116 us.  Rows of all heads brought by bulk copies of 2 KB to 16
-// warps an SM, 32 keys at a time, took 132 us (twice the instructions); a warp
-// of its own for bulk copies of single head rows 200 us.
+// for HBM.  16 paged requests of 0.5k to 8k tokens 36 us, 8 chunks of 512
+// tokens 11 us (latency).  An item runs its start once, so instruction fetches
+// count: the vectors are formed in a loop (96 -> 92 us).  Chunks go before side
+// rows, whose items are shorter and fill the end (105 -> 96 us).  Slots of half
+// the keys in three buffers: 4 % slower; rows of all heads brought by bulk
+// copies of 2 KB to 16 warps an SM, 32 keys at a time: 132 us when this was
+// 112 (twice the instructions); a warp of its own for bulk copies of single
+// head rows 200 us.
 #include <algorithm>
 
 #include "attend_chunks.h"

@@ -80,6 +80,10 @@ def test_many_requests_and_chunks():
                             k=[i % 5 for i in range(n)], heads=(2, 1, 64))))
 
 
+def test_more_chunks_than_a_join_holds_at_once():
+    check(Attend(AttendCase(lens=[[2, 1, 3] * 200, [5]], n_query=[3, 1], k=[100, 0], heads=(4, 2, 128), new=1)))
+
+
 def test_constant_values_and_keys():
     # groups with scale 0, as a KIVI constant group stores them
     a = Attend(AttendCase(lens=[[48]], n_query=[2], k=[0], heads=(4, 2, 128)))
