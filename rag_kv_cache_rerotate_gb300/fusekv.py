@@ -532,6 +532,20 @@ def _rows(t, name, dtype, dev, rows, heads, dim, exact=False):
     return t.data_ptr() or None
 
 
+_I32 = torch.int32
+
+
+def _list(t, name, dev):
+    """An int32 tensor's pointer and entries."""
+    try:
+        if t.dtype is _I32 and t.is_contiguous() and t.get_device() == dev:
+            return t.data_ptr() or None, t.numel()
+    except AttributeError:
+        pass
+    _tensor(t, name, _I32, dev)
+    raise AssertionError(name)
+
+
 def _ws(ws, dev):
     """A workspace's pointer and bytes."""
     if ws.get_device() != dev or not ws.is_contiguous():
@@ -565,14 +579,12 @@ def attend_chunks(desc: LayerDesc, chunks: ChunkTable, reqs: RequestTable, n_new
     dt, tot = _TORCH_DTYPE.get(desc.dtype), reqs.extents()
     dev, on = _place(stream)
     Hq, Hkv, d, n = desc.n_q_heads, desc.n_kv_heads, desc.head_dim, reqs.n * int(n_new)
-    if idx is None:
-        if tot.n_sel > 0:
-            raise ValueError(f"idx: {tot.n_sel} entries are needed")
-    elif _tensor(idx, "idx", torch.int32, dev).numel() < tot.n_sel:
-        raise ValueError(f"idx: {idx.numel()} entries, {tot.n_sel} are needed")
+    at, entries = (None, 0) if idx is None else _list(idx, "idx", dev)
+    if entries < tot.n_sel:
+        raise ValueError(f"idx: {entries} entries, {tot.n_sel} are needed")
     st = load().fuse_attend_chunks(
         _c.byref(desc), _c.byref(chunks.c), _c.byref(reqs.c), int(n_new),
-        _rows(Q, "Q", dt, dev, n, Hq, d, True), _ptr(idx), _rows(Ks, "Ks", dt, dev, tot.n_out, Hkv, d),
+        _rows(Q, "Q", dt, dev, n, Hq, d, True), at, _rows(Ks, "Ks", dt, dev, tot.n_out, Hkv, d),
         _rows(Vs, "Vs", dt, dev, tot.n_out, Hkv, d), _rows(O, "O", dt, dev, n, Hq, d, True),
         *_ws(ws, dev), on)
     if st != FUSE_OK:
@@ -640,26 +652,27 @@ def alloc_pages_workspace(tables: Optional[ChunkTable], device="cuda") -> torch.
     return torch.zeros(int(n.value), dtype=torch.uint8, device=device)
 
 
-def _max_moves(moves, dev) -> int:
-    n = _tensor(moves, "moves", torch.int32, dev).numel()
+def _moves(moves, dev):
+    """A move list's pointer and the pairs it has room for."""
+    p, n = _list(moves, "moves", dev)
     if n < 2:
         raise ValueError("moves: count and live pages need two entries")
-    return (n - 2) // 2
+    return p, (n - 2) // 2
 
 
 def _refs(refs, tables, dev):
-    n = _tensor(refs, "refs", torch.int32, dev).numel()
+    p, n = _list(refs, "refs", dev)
     if n < tables.c.n_pool_blocks:
         raise ValueError(f"refs: {n} entries for {tables.c.n_pool_blocks} pages")
-    return refs.data_ptr() or None
+    return p
 
 
 def pages_fork(src: ChunkTable, dst: ChunkTable, refs, moves, ws, stream=None):
     """Branch off ``src``'s sequences into ``dst``'s tables: full pages shared,
     partly filled last pages listed in ``moves`` for ``pages_copy``."""
     dev, on = _place(stream)
-    st = load().fuse_pages_fork(_c.byref(src.c), _c.byref(dst.c), _refs(refs, src, dev), _ptr(moves),
-                                _max_moves(moves, dev), *_ws(ws, dev), on)
+    st = load().fuse_pages_fork(_c.byref(src.c), _c.byref(dst.c), _refs(refs, src, dev),
+                                *_moves(moves, dev), *_ws(ws, dev), on)
     if st != FUSE_OK:
         raise FuseError(st, "fuse_pages_fork")
 
@@ -677,8 +690,8 @@ def pages_compact(tables: ChunkTable, refs, moves, ws, stream=None):
     """Pack the live pages to the front: tables and refs rewritten, the page
     copies listed in ``moves`` for ``pages_copy``."""
     dev, on = _place(stream)
-    st = load().fuse_pages_compact(_c.byref(tables.c), _refs(refs, tables, dev), _ptr(moves),
-                                   _max_moves(moves, dev), *_ws(ws, dev), on)
+    st = load().fuse_pages_compact(_c.byref(tables.c), _refs(refs, tables, dev),
+                                   *_moves(moves, dev), *_ws(ws, dev), on)
     if st != FUSE_OK:
         raise FuseError(st, "fuse_pages_compact")
 
@@ -689,8 +702,8 @@ def pages_copy(desc: LayerDesc, pools: PagePools, moves, ws, stream=None):
     if pools.shape is not None and pools.shape[2:] != (desc.n_kv_heads, per):
         raise ValueError(f"pools: pages of {pools.shape[2:]}, {(desc.n_kv_heads, per)} are needed")
     dev, on = _place(stream)
-    st = load().fuse_pages_copy(_c.byref(desc), _c.byref(pools.c), _ptr(moves),
-                                _max_moves(moves, dev), *_ws(ws, dev), on)
+    st = load().fuse_pages_copy(_c.byref(desc), _c.byref(pools.c), *_moves(moves, dev),
+                                *_ws(ws, dev), on)
     if st != FUSE_OK:
         raise FuseError(st, "fuse_pages_copy")
 
