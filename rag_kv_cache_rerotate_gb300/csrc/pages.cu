@@ -10,7 +10,9 @@
 // scan or a scatter over at most a few hundred KB, bound by latency, and the
 // cluster barrier (with the counts exchanged through distributed shared
 // memory) replaces the launches that separate grids would need between the
-// steps.  A pool of 4 096 pages and 36 branches forks in one launch.
+// steps.  Sums and scans take two counts at a time, and a thread keeps the counts
+// of its first four pages.  36 branches of 12 sequences in a pool of 4 096 pages:
+// 8 us; packing such a pool 10 us, its copies (133 MB) 43 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -396,7 +398,8 @@ constexpr int kPiece = kCopyThreads * kVecs * 16;   // 16 KB
 
 // Copy pages: every (pool, move, K or V) page in pieces of 16 KB, one piece a
 // CTA at a time, four 16-byte loads of a thread in flight before the first
-// store.  Bound by HBM: every byte is read once and written once.
+// store.  Bound by HBM: every byte is read once and written once (64 pages of
+// 64 KB in 16 layers: 20.8 us, 6.4 TB/s; a plain copy reaches 6.8).
 template <int N>
 __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_constant__ CopyArgs<N> a) {
   pdl_trigger();
