@@ -60,7 +60,8 @@ __device__ __forceinline__ PromptTile prompt_tile(const PromptTable& p, int rtil
   return x;
 }
 
-cudaError_t launch_prompt_simt(const fuse_layer_desc_t& d, const PromptTable& p, const void* Q,
+// fp32 layers, CUDA cores; the tiles hold 16 r / g rows (r = 1, 2, 4).
+cudaError_t launch_prompt_simt(const fuse_layer_desc_t& d, int r, const PromptTable& p, const void* Q,
                                const void* K, const void* V, void* O, cudaStream_t s);
 
 // bf16 layers: tcgen05 tensor cores (attend_prompt_tc.cu).

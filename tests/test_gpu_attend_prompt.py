@@ -141,6 +141,13 @@ def test_more_requests_than_one_launch_takes():
     Prompt(packed([int(x) for x in rng.integers(0, 40, size=600)]), (2, 1, 64), "bf16").check()
 
 
+@pytest.mark.parametrize("lens", [[50, 3], [300, 257], [260, 33, 64] * 9 + [1, 31]])
+@pytest.mark.parametrize("heads", [(4, 2, 64), (8, 1, 128), (2, 2, 128)])
+def test_fp32_tiles_of_few_and_many_rows(lens, heads):
+    # 16, 32 and 64 rows a tile, by the number of tiles
+    Prompt(packed(lens, gap=1), heads, "f32").check()
+
+
 def test_equal_lengths_and_a_single_row_each():
     Prompt(packed([1] * 70), (8, 2, 128), "bf16").check()
 
