@@ -132,6 +132,15 @@ __device__ void attend_item(const AttendArgs& a, const Keys& y, const float2* cs
   }
   constexpr int RB = row_bytes<ST>(D);
   const int64_t stride = (int64_t)a.n_kv_heads * RB;
+  // the first selected position that is not before the item: 32 probes a round
+  int sel = 0;
+  for (int len = y.n_skip; len > 0;) {
+    const int step = (len + 31) / 32, i = sel + (lane + 1) * step - 1;
+    const bool below = i < sel + len && y.skip[i] < y.pos0 + y.t0;
+    const int parts = __popc(__ballot_sync(0xffffffffu, below));
+    sel += parts * step;
+    len = min(step - 1, len - parts * step);
+  }
   for (int t = y.t0; t < y.t1; t += 32) {
     const int key = t + lane;
     bool ok = key < y.t1;
@@ -145,14 +154,12 @@ __device__ void attend_item(const AttendArgs& a, const Keys& y, const float2* cs
         row = (int64_t)b * a.block_size + key % a.block_size;
       }
     }
-    if (ok && y.n_skip > 0) {              // is the position selected?
-      const int p = y.pos0 + key;
-      int lo = 0, hi = y.n_skip;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (y.skip[mid] < p) lo = mid + 1; else hi = mid;
-      }
-      ok = !(lo < y.n_skip && y.skip[lo] == p);
+    if (y.n_skip > 0) {                    // selected positions: at most 32 entries from `sel` on
+      const int p = y.pos0 + t, v = sel + lane < y.n_skip ? y.skip[sel + lane] : INT32_MAX;
+      const bool here = v >= p && v < p + 32;
+      const uint32_t mask = __reduce_or_sync(0xffffffffu, here ? 1u << (v - p) : 0u);
+      ok = ok && !(mask >> lane & 1);
+      sel += __popc(__ballot_sync(0xffffffffu, v < p + 32));
     }
     float s[kVecs];
 #pragma unroll
