@@ -29,6 +29,7 @@ namespace fusekv {
 namespace {
 
 constexpr int kWarps = 4;                 // items of a CTA of the CUDA-core kernel
+constexpr int kAtOnce = 8;                // keys whose values it reads at a time
 
 // Eight consecutive stored elements as fp32.
 template <int ST> __device__ __forceinline__ void load8(const uint8_t* row, int e, float (&x)[8]) {
@@ -166,7 +167,7 @@ __device__ void attend_item(const AttendArgs& a, const Keys& y, const float2* cs
     for (int v = 0; v < kVecs; ++v) s[v] = ok ? cst[v] : -INFINITY;
     if (ok) {
       const uint8_t* kr = y.k + row * stride + h * RB;
-#pragma unroll 2
+#pragma unroll 4
       for (int e = 0; e < D; e += 8) {
         float x[8];
         load8<ST>(kr, e, x);
@@ -198,15 +199,21 @@ __device__ void attend_item(const AttendArgs& a, const Keys& y, const float2* cs
     }
     __syncwarp();
     const int64_t at = ok ? row : -1;
-    for (int i = 0; i < 32; ++i) {
-      const int64_t ri = __shfl_sync(0xffffffffu, at, i);
-      if (ri < 0) continue;
-      float x[EL];
-      load_el<ST, EL>(y.v + ri * stride + h * RB, lane * EL, x);
+    for (int i = 0; i < 32; i += kAtOnce) {            // reads of several keys in flight
+      float x[kAtOnce][EL];
 #pragma unroll
-      for (int v = 0; v < kVecs; ++v)
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int64_t ri = __shfl_sync(0xffffffffu, at, i + j);
 #pragma unroll
-        for (int e = 0; e < EL; ++e) acc[v][e] = fmaf(s_p[i][v], x[e], acc[v][e]);
+        for (int e = 0; e < EL; ++e) x[j][e] = 0.f;    // of a key not seen, whose weight is 0
+        if (ri >= 0) load_el<ST, EL>(y.v + ri * stride + h * RB, lane * EL, x[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+          for (int e = 0; e < EL; ++e) acc[v][e] = fmaf(s_p[i + j][v], x[j][e], acc[v][e]);
     }
     __syncwarp();
   }
