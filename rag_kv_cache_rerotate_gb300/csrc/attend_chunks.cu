@@ -86,6 +86,9 @@ struct Keys {
 
 // One warp, one item: 32 keys at a time, a lane per key for the scores, then
 // a lane per D / 32 channels for the sums.
+// Latency bounds it (2 requests of 3 or 4 chunks of 33 to 64 keys at 4 bits: 10
+// us with the join), so several rows are read at a time; with the values read
+// one by one it took 13.6.
 template <int ST, int D>
 __device__ void attend_item(const AttendArgs& a, const Keys& y, const float2* cs, const __half* ks,
                             const __half* kz, int r, int h, int vg, int64_t slot, float (*s_q)[D],
@@ -553,8 +556,8 @@ fuse_status_t plan_attend(const fuse_layer_desc_t* desc, const fuse_chunks_t* ch
   // keys: 8 chunks of 512 take 11 us, with 192 keys 13; 16 requests of 0.5k to
   // 8k tokens at the rule's 256 keys 39 us, at 128 45; 8 of 33k at 1024 keys 92
   // us, at 512 100.  Side rows go to half as many items (92 us; as many: 94, a
-  // quarter: 100).  fp32 layers, whose lane takes a key: 14 us with 32 keys an
-  // item, 21 with 64.
+  // quarter: 100).  fp32 layers, whose lane takes a key: 10 us with 32 keys an
+  // item, 13.5 with 64.
   const int least = desc->dtype == FUSE_BF16 ? 64 : 32;
   const int seg = cut(n_ctx * per, kItems, least);
   P->nsub = std::max(1, (max_len + seg - 1) / seg);
