@@ -538,7 +538,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // probabilities: key pairs packed as bf16x2, in place over the scores;
         // the scaling and the row sums work on key pairs (f32x2)
         const uint64_t sc2 = pack2(scale, scale);
-        const uint64_t ng0 = pack2(-mn0, -mn0), ng1 = pack2(-mn1, -mn1);
+        // (a row whose every score so far is -infinity has weights of 0, not 2^(-inf + inf))
+        const float rf0 = mn0 == -INFINITY ? 0.f : mn0, rf1 = mn1 == -INFINITY ? 0.f : mn1;
+        const uint64_t ng0 = pack2(-rf0, -rf0), ng1 = pack2(-rf1, -rf1);
         uint64_t acc0 = 0, acc1 = 0;                    // (even keys, odd keys) of each row
 #pragma unroll
         for (int q = 0; q < 16; ++q) {

@@ -169,3 +169,19 @@ def test_repeated_runs_other_stream_and_graph():
     g.replay()
     got = p.O.clone()
     assert torch.equal(p.run(), got) and not torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype,heads", [("bf16", (8, 2, 128)), ("bf16", (4, 1, 64)), ("f32", (4, 2, 64))])
+@pytest.mark.parametrize("n", [1, 128, 140, 300])
+def test_keys_of_score_minus_infinity_have_no_weight(dtype, heads, n):
+    # the first n keys score -infinity: rows behind them are as without them, to
+    # the same bound (weights of 0 add nothing); rows that see no other key are
+    # NaN, 0 / 0
+    p = Prompt([(0, 400)], heads, dtype)
+    p.Q[..., 0] = 1.0
+    want, tol = prompt_reference(p.Q, p.K, p.V, [(n, 400 - n)], dtype)
+    p.K[:n, :, 0] = -float("inf")
+    got = f64(p.run())
+    fk.check_errors(p.ws)
+    assert (np.abs(got[n:] - want[n:]) <= tol[n:]).all()
+    assert np.isnan(got[:n]).all()
