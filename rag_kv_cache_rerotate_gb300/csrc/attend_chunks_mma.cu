@@ -45,6 +45,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kSlots = 2;
 constexpr float kRaise = 8.0f;            // log2: P <= 2^8, times a scale <= 2^6 stays in fp16
+constexpr float kTiny = 1.17549435e-38f;  // 2^-126
 
 template <int ST, int D> struct Fmt {
   static constexpr bool coded = ST != FUSE_BF16;
@@ -805,7 +806,9 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Item& y, 
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        sc[n][e] = (c[0][e] + c[1][e]) + (c[0][2 + e] + c[1][2 + e]);
+        // an infinite key: the vectors' high parts decide, what is left of them is 0 or of either sign
+        const float hi = c[0][e] + c[1][e], rest = c[0][2 + e] + c[1][2 + e];
+        sc[n][e] = fabsf(hi) == INFINITY ? hi : hi + rest;
         if (!(keep >> (8 * n + 2 * tig + e) & 1)) sc[n][e] = -INFINITY;
       }
     }
@@ -832,8 +835,12 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Item& y, 
     for (int n = 0; n < 2; ++n) {
       const float p0 = ex2(sc[n][0] - ref), p1 = ex2(sc[n][1] - ref);
       l += p0 + p1;
-      ph[n] = pack_bf16x2(p0, p1);
-      pl[n] = pack_bf16x2(p0 - bf16_lo(ph[n]), p1 - bf16_hi(ph[n]));
+      // the high part is cut off, not rounded (2^-16 of the weight is lost in
+      // all, 2^-17 if it were), and what is left is at least 2^-126: both parts
+      // of a weight above 0 are, so that an infinite value stays infinite
+      ph[n] = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+      pl[n] = pack_bf16x2(fmaxf(p0 - bf16_lo(ph[n]), fminf(p0, kTiny)),
+                          fmaxf(p1 - bf16_hi(ph[n]), fminf(p1, kTiny)));
     }
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {

@@ -203,8 +203,9 @@ class Attend:
                          self.Vs, self.O, self.ws, stream)
         return self.O
 
-    def reference(self, rows=None):
-        """(O, tolerance) in fp64 for every output row.
+    def reference(self, rows=None, unseen=()):
+        """(O, tolerance) in fp64 for every output row; `unseen`: side rows
+        (request-local) that have no weight.
 
         With A = sum p |v| and S = max sum |q k| / sqrt(d) (magnitudes of a
         code's zero and scaled part added), a score is off by at most
@@ -237,7 +238,8 @@ class Attend:
             mv = np.concatenate([z] + [self.mv[j] for j in ch])[keep]
             for u in range(c.new):
                 m = R.k + R.n_query - c.new + u + 1
-                sk, sv = Ks[R.out0:R.out0 + m], Vs[R.out0:R.out0 + m]
+                seen = R.out0 + np.setdiff1d(np.arange(m), np.asarray(unseen, int))
+                sk, sv = Ks[seen], Vs[seen]
                 kk, vv = np.concatenate([k, sk]), np.concatenate([v, sv])
                 ma, mb = np.concatenate([mk, np.abs(sk)]), np.concatenate([mv, np.abs(sv)])
                 for h in range(Hq):

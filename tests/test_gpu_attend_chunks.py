@@ -219,3 +219,50 @@ def test_requests_of_one_token_follow_what_writes_their_rows(dtype):
         # one key: its weight is 1 and the row its value
         assert torch.equal(O, P) and bool((P != 0).any(-1).all())
     fk.check_errors(ws2)
+
+
+WHERE = ["chunk", "side", "own"]             # of a key: a cached chunk, an earlier query token, the token itself
+
+
+@pytest.mark.parametrize("dtype,heads", [("bf16", (4, 2, 128)), ("bf16", (8, 1, 64)), ("f32", (4, 2, 64))])
+@pytest.mark.parametrize("where", WHERE)
+def test_a_key_of_score_minus_infinity_has_no_weight(dtype, heads, where):
+    a = Attend(AttendCase(lens=[[40, 30]], n_query=[3], k=[0], storage=dtype, dtype=dtype, heads=heads))
+    a.Q[..., 0] = 1.0
+    if where == "chunk":
+        a.idx_list = [np.array([7])]
+    want, tol = a.reference(unseen={"chunk": [], "side": [0], "own": [2]}[where])
+    rows, i = {"chunk": (a.K, 7), "side": (a.Ks, 0), "own": (a.Ks, 2)}[where]
+    rows[i, :, 0] = -float("inf")
+    got = f64(a.run())
+    fk.check_errors(a.ws)
+    assert (np.abs(got - want) <= tol).all()
+
+
+@pytest.mark.parametrize("dtype,heads", [("bf16", (4, 2, 128)), ("bf16", (8, 1, 64)), ("f32", (4, 2, 64))])
+@pytest.mark.parametrize("where", WHERE)
+@pytest.mark.parametrize("value", [float("inf"), -float("inf")])
+def test_an_infinite_value_gives_infinity(dtype, heads, where, value):
+    a = Attend(AttendCase(lens=[[40, 30]], n_query=[3], k=[0], storage=dtype, dtype=dtype, heads=heads))
+    want, tol = a.reference()
+    rows, i = {"chunk": (a.V, 7), "side": (a.Vs, 0), "own": (a.Vs, 2)}[where]
+    rows[i, 0, 3] = value
+    got = f64(a.run())
+    g = heads[0] // heads[1]
+    assert (got[:, :g, 3] == value).all()
+    got[:, :g, 3] = want[:, :g, 3]
+    assert (np.abs(got - want) <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_an_infinite_value_of_the_only_key(dtype):
+    # its weight is 1, which 16 bits hold without a remainder
+    a = Attend(AttendCase(lens=[[1]], n_query=[1], k=[0], storage=dtype, dtype=dtype, heads=(4, 2, 128)))
+    a.Ks[0].zero_()
+    a.Q.zero_()
+    want, tol = a.reference()
+    a.V[0, 1, 5] = float("inf")
+    got = f64(a.run())
+    assert (got[:, 2:, 5] == np.inf).all()
+    got[:, 2:, 5] = want[:, 2:, 5]
+    assert (np.abs(got - want) <= tol).all()
