@@ -474,7 +474,8 @@ __device__ __forceinline__ void load_query(const AttendArgs& a, const Item& y, c
         if constexpr (F::coded) {
           if (ST == FUSE_U4_ASYM && (ch & 1)) t *= 0.0625f;     // odd codes sit 4 bits higher
           const __half hi = __float2half_rn(t);
-          w = pack_half2(__half2float(hi), t - __half2float(hi));
+          // an infinite scale: no remainder, whose product with a code would be NaN
+          w = pack_half2(__half2float(hi), fabsf(t) == INFINITY ? 0.f : t - __half2float(hi));
         } else {
           const __nv_bfloat16 hi = __float2bfloat16_rn(t);
           w = pack_bf16x2(__bfloat162float(hi), t - __bfloat162float(hi));

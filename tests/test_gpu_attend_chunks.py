@@ -266,3 +266,18 @@ def test_an_infinite_value_of_the_only_key(dtype):
     assert (got[:, 2:, 5] == np.inf).all()
     got[:, 2:, 5] = want[:, 2:, 5]
     assert (np.abs(got - want) <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("storage", ["u4", "u8"])
+def test_an_infinite_key_scale(storage, dtype):
+    # every key of the first chunk scores -infinity; the second one is left
+    a = Attend(AttendCase(lens=[[30, 40]], n_query=[3], k=[0], storage=storage, dtype=dtype, heads=(4, 2, 128)))
+    a.Q[..., 5] = -1.0
+    a.idx_list = [np.arange(30)]
+    want, tol = a.reference()
+    a.ks[0, :, 5] = float("inf")
+    a.K[:30, :, 2 if storage == "u4" else 5] |= 0x10     # no code of channel 5 is 0
+    got = f64(a.run())
+    fk.check_errors(a.ws)
+    assert (np.abs(got - want) <= tol).all()
