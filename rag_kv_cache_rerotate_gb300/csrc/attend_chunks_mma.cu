@@ -547,6 +547,7 @@ __device__ __forceinline__ void attend_codes(const AttendArgs& a, const Item& y,
   float m0 = -INFINITY, m1 = -INFINITY;                // running maxima
   uint64_t l2 = 0, z2 = 0;                             // sums over the lane's keys
   int ve = 0;                                          // exponent field of the largest value scale
+  uint32_t seen = 0;                                   // bits of keys to be seen, of all slots
   uint64_t acc[MT][2];                                 // channel rows gid and gid + 8
 #pragma unroll
   for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = 0;
@@ -561,6 +562,7 @@ __device__ __forceinline__ void attend_codes(const AttendArgs& a, const Item& y,
     for (int r = 0; r < F::ROWS; ++r) {
       keep[r] = sm.keep[s & 1][r];
       full = full && keep[r] == F::kFull;
+      seen |= keep[r];
       // 0 for a key not seen, whatever it holds
       const uint32_t w = keep[r] >> lane & 1 ? (uint32_t)vs[r] | (uint32_t)vz[r] << 16 : 0u;
       sm.sz[r * 32 + lane] = w;
@@ -734,6 +736,8 @@ __device__ __forceinline__ void attend_codes(const AttendArgs& a, const Item& y,
     z.x += __shfl_xor_sync(kAll, z.x, o);
     z.y += __shfl_xor_sync(kAll, z.y, o);
   }
+  // no key to see: an item without one, whatever the chunk's scales and zeros hold
+  if (seen == 0) l = make_float2(0.f, 0.f);
   const int n_vec = min(kVecs, a.g * a.n_new - y.vg * kVecs);
   const int64_t at = ((y.slot * a.n_kv_heads + y.h) * a.nvg + y.vg) * kVecs;
   const float un = __uint_as_float((uint32_t)(127 + 24 - 20 + ve) << 23);

@@ -281,3 +281,16 @@ def test_an_infinite_key_scale(storage, dtype):
     got = f64(a.run())
     fk.check_errors(a.ws)
     assert (np.abs(got - want) <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("storage", ["u4", "u8"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("paged", [False, True])
+def test_scales_of_a_wholly_selected_chunk_do_not_reach_a_row(storage, dtype, value, paged):
+    a = Attend(AttendCase(lens=[[70, 45]], n_query=[4], k=[70], storage=storage, dtype=dtype, paged=paged,
+                          heads=(4, 2, 128)))
+    a.idx_list = [np.arange(70)]
+    a.idx.copy_(torch.arange(70, dtype=torch.int32))
+    a.ks[0], a.kz[0] = value, value
+    check(a)
