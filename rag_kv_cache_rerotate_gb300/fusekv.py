@@ -227,7 +227,12 @@ def _to_device_bytes(arr, device) -> torch.Tensor:
 
 
 class RequestTable:
-    """Host and device copies of a ``fuse_request_t`` array."""
+    """Host and device copies of a ``fuse_request_t`` array.
+
+    ``host`` may be edited in place (a decode loop raises ``n_query``):
+    ``attend_chunks`` and ``attend_prompt`` then write the device copy anew on
+    their stream before they read it; before any other call, or one on another
+    stream, ``update`` does."""
 
     def __init__(self, reqs: Sequence[Request], device="cuda"):
         self.host = (Request * max(1, len(reqs)))(*reqs)
@@ -236,13 +241,47 @@ class RequestTable:
         self.c = Requests(self.n, _c.addressof(self.host),
                           self.dev.data_ptr() if self.dev is not None and self.dev.numel() else None)
         self._totals, self._of = None, b""
+        self._sent = bytes(self.host)              # what the device copy holds
 
     def extents(self) -> Totals:
         """``totals``, computed again only when the host table has changed."""
-        now = bytes(self.host)
+        return self._extents(bytes(self.host))
+
+    def _extents(self, now: bytes) -> Totals:
         if self._totals is None or now != self._of:
             self._totals, self._of = self.totals(), now
         return self._totals
+
+    def update(self, stream=None) -> None:
+        """Write the host table to the device copy where it has changed, on the
+        stream (None: the current one): calls enqueued there before keep the
+        old table, later ones and replays of captured ones read the new one.
+        Refused while the stream is captured."""
+        self._update(bytes(self.host), stream)
+
+    def _update(self, now: bytes, stream) -> None:
+        if self.dev is None or now == self._sent:
+            return
+        src = torch.frombuffer(bytearray(now), dtype=torch.uint8)
+        if not self.dev.is_cuda:
+            self.dev.copy_(src)
+        else:
+            if stream is not None and not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=self.dev.device)
+            with torch.cuda.stream(stream):
+                if torch.cuda.is_current_stream_capturing():
+                    raise ValueError("reqs: the host table has changed since it was uploaded; "
+                                     "call update() before the capture")
+                # from pinned memory, so that the copy waits for the stream, not the host
+                self.dev.copy_(src.pin_memory(), non_blocking=True)
+        self._sent = now
+
+    def _ready(self, stream) -> Totals:
+        """``extents`` and ``update``."""
+        now = bytes(self.host)
+        if now != self._sent:
+            self._update(now, stream)
+        return self._extents(now)
 
     def totals(self) -> Totals:
         t = Totals()
@@ -576,7 +615,7 @@ def attend_chunks(desc: LayerDesc, chunks: ChunkTable, reqs: RequestTable, n_new
     """Attention of the last ``n_new`` tokens of every request over its chunk
     caches as stored (codes or layer type), the selected positions ``idx``
     replaced by the refreshed rows of ``Ks``, ``Vs`` (QCFuse Eqs. 4, 6)."""
-    dt, tot = _TORCH_DTYPE.get(desc.dtype), reqs.extents()
+    dt, tot = _TORCH_DTYPE.get(desc.dtype), reqs._ready(stream)
     dev, on = _place(stream)
     Hq, Hkv, d, n = desc.n_q_heads, desc.n_kv_heads, desc.head_dim, reqs.n * int(n_new)
     at, entries = (None, 0) if idx is None else _list(idx, "idx", dev)
@@ -593,7 +632,7 @@ def attend_chunks(desc: LayerDesc, chunks: ChunkTable, reqs: RequestTable, n_new
 
 def attend_prompt(desc: LayerDesc, reqs: RequestTable, Q, K, V, O, ws, stream=None):
     """Causal attention inside every request's rows (whole prompts, packed)."""
-    dt, n = _TORCH_DTYPE.get(desc.dtype), reqs.extents().n_tok
+    dt, n = _TORCH_DTYPE.get(desc.dtype), reqs._ready(stream).n_tok
     dev, on = _place(stream)
     Hq, Hkv, d = desc.n_q_heads, desc.n_kv_heads, desc.head_dim
     st = load().fuse_attend_prompt(

@@ -243,3 +243,18 @@ def test_binding_refuses_wrong_tensors(fk):
         fk.pages_free(_tables(fk, [20]), torch.zeros(8), ws)
     with pytest.raises(ValueError):
         fk.PagePools([torch.zeros(8, 16, 2, 128)], [torch.zeros(8, 16, 2, 64)], fk.FUSE_F32, 16)
+
+
+def test_request_table_device_copy_follows_the_host_table(fk):
+    t = fk.RequestTable([fk.Request(*r) for r in ONE], device="cpu")
+    assert bytes(t.dev.numpy()) == bytes(t.host)
+    t.host[0].n_query += 4
+    t.update()
+    assert bytes(t.dev.numpy()) == bytes(t.host) and t.extents().n_tok == 109
+    t.host[0].n_query -= 1
+    S = torch.zeros(12, 2, 128, dtype=torch.bfloat16)
+    Q = torch.zeros(1, 8, 128, dtype=torch.bfloat16)
+    with pytest.raises(fk.FuseError):                      # refused: no workspace to speak of
+        fk.attend_chunks(_desc(fk), _chunks(fk, [(0, 100)]), t, 1, Q, torch.zeros(3, dtype=torch.int32), S, S, Q,
+                         torch.zeros(0, dtype=torch.uint8))
+    assert bytes(t.dev.numpy()) == bytes(t.host)           # the call brought the copy up to date first

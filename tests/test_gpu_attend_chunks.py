@@ -294,3 +294,54 @@ def test_scales_of_a_wholly_selected_chunk_do_not_reach_a_row(storage, dtype, va
     a.idx.copy_(torch.arange(70, dtype=torch.int32))
     a.ks[0], a.kz[0] = value, value
     check(a)
+
+
+def test_a_request_table_that_grows_in_place():
+    """A decode loop raises n_query of the host table's last request by one a
+    step: each step's rows are those of tables built anew."""
+    c = AttendCase(lens=[[70, 33], [50]], n_query=[2, 4], k=[9, 0], heads=(4, 2, 128), gap=5)
+    a = Attend(c)
+    room = [torch.full_like(x, float("nan")) for x in (a.Ks, a.Vs)]
+    for x, y in zip(room, (a.Ks, a.Vs)):
+        x.normal_(generator=torch.Generator("cuda").manual_seed(3))
+        x[~torch.isnan(y)] = y[~torch.isnan(y)]
+    a.Ks, a.Vs = room
+    for step in range(5):
+        if step:
+            a.reqs.host[1].n_query += 1
+        a.ws = fk.alloc_attend_workspace(a.desc, a.chunks, a.reqs, 1)
+        got = a.run().clone()
+        fresh = fk.RequestTable([fk.Request(r.row0, r.score0, r.sel0, r.out0, r.n_ctx, r.n_query, r.k, 0)
+                                 for r in a.reqs.host[:a.reqs.n]])
+        want = torch.zeros_like(got)
+        fk.attend_chunks(a.desc, a.chunks, fresh, 1, a.Q, a.idx, a.Ks, a.Vs, want, a.ws)
+        fk.check_errors(a.ws)
+        assert torch.equal(got, want), step
+
+
+def test_a_request_table_edited_in_place_on_another_stream_and_before_a_capture():
+    c = AttendCase(lens=[[40]], n_query=[4], k=[3], heads=(4, 2, 64))
+    a = Attend(c)
+    s = torch.cuda.Stream()
+    a.reqs.host[0].n_query = 3                           # the last row is dropped again
+    torch.cuda.synchronize()
+    a.run(stream=s)
+    s.synchronize()
+    got, want = a.O.clone(), torch.zeros_like(a.O)
+    fresh = fk.RequestTable([fk.Request(0, 0, 0, 0, 40, 3, 3, 0)])
+    fk.attend_chunks(a.desc, a.chunks, fresh, 1, a.Q, a.idx, a.Ks, a.Vs, want, a.ws)
+    assert torch.equal(got, want)
+    a.reqs.host[0].n_query = 2
+    g = torch.cuda.CUDAGraph()
+    with pytest.raises(ValueError):
+        with torch.cuda.graph(g, stream=s):
+            a.run(stream=s)
+    a.reqs.update()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        a.run(stream=s)
+    g.replay()
+    got = a.O.clone()
+    assert torch.equal(a.run(stream=s.cuda_stream), got) and not torch.equal(got, want)
+    fk.check_errors(a.ws)
