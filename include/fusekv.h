@@ -521,9 +521,9 @@ fuse_status_t fuse_pages_workspace_size(const fuse_chunks_t* tables, size_t* byt
  * source may appear any number of times; no dst table may overlap another or
  * a source.  src and dst have the same lengths.  max_moves must be at least
  * the number of partly filled last pages (else FUSE_ERR_WORKSPACE).  When a
- * source entry is outside the pool or names a free page
- * (FUSE_ERR_DEVICE_BOUNDS), or too few pages are free (FUSE_ERR_NO_PAGES),
- * nothing changes and the move list is empty. */
+ * source entry is outside the pool or names a free page, or any page's count
+ * is negative (FUSE_ERR_DEVICE_BOUNDS), or too few pages are free
+ * (FUSE_ERR_NO_PAGES), nothing changes and the move list is empty. */
 fuse_status_t fuse_pages_fork(const fuse_chunks_t* src, const fuse_chunks_t* dst, int32_t* refs,
                               int32_t* moves, int32_t max_moves, void* ws, size_t ws_bytes,
                               fuse_stream_t stream);
@@ -539,8 +539,9 @@ fuse_status_t fuse_pages_free(const fuse_chunks_t* tables, int32_t* refs, void* 
  * in order, to the free ids below n (as few moves as can be; sources and
  * destinations are disjoint); tables and refs are rewritten.  max_moves must
  * be at least n_pool_blocks / 2 (else FUSE_ERR_WORKSPACE).  An entry outside
- * the pool or naming a free page is recorded as FUSE_ERR_DEVICE_BOUNDS, and
- * then nothing changes and the move list is empty. */
+ * the pool or naming a free page, or a negative count of any page, is recorded
+ * as FUSE_ERR_DEVICE_BOUNDS, and then nothing changes and the move list is
+ * empty. */
 fuse_status_t fuse_pages_compact(const fuse_chunks_t* tables, int32_t* refs, int32_t* moves,
                                  int32_t max_moves, void* ws, size_t ws_bytes,
                                  fuse_stream_t stream);

@@ -14,6 +14,7 @@ enum CacheErrSite : uint32_t {
   SITE_ATTEND_BLOCK = 14,    // paged block id outside the pool (attend_chunks)
   SITE_ATTEND_SEL = 15,      // selected index out of range or order (attend_chunks)
   SITE_PROMPT_TIMEOUT = 16,  // prompt-attention pipeline wait gave up
+  SITE_PAGE_COUNT = 17,      // negative reference count
 };
 
 struct ReqInfo {

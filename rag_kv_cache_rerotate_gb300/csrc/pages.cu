@@ -134,10 +134,24 @@ __device__ __forceinline__ void load_refs4(const int32_t* refs, int b, int hi, i
   }
 }
 
+// Whether any of the counts that load_refs4 read is negative (reported): such a
+// page is neither free nor live, and a compaction would have more pages to move
+// than places for them.
+__device__ __forceinline__ int negative_count(uint32_t* err, int b, int hi, const int (&r)[4]) {
+  int bad = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (r[i] < 0 && b + i < hi) {
+      bad = 1;
+      report_error(err, FUSE_ERR_DEVICE_BOUNDS, SITE_PAGE_COUNT, (uint32_t)(b + i));
+    }
+  return bad;
+}
+
 // Fork: dst[i] shares the full pages of src[i] and gets a page of its own
 // for the last, partly filled one: the lowest-numbered free pages, in table
-// order.  Nothing changes unless every source entry names a live page, the
-// free pages suffice and the move list has room.
+// order.  Nothing changes unless every source entry names a live page, no count
+// is negative, the free pages suffice and the move list has room.
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
     pages_fork_kernel(const TableArgs a) {
   cg::cluster_group cl = cg::this_cluster();
@@ -150,10 +164,11 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
   pdl_wait();
   int lo, hi;
   slice(a.n_blocks, rank, &lo, &hi);
-  int free_n = 0;
+  int free_n = 0, bad = 0;
   for (int b = lo + 4 * tid; b < hi; b += 4 * kThreads) {
     int r[4];
     load_refs4(a.refs, b, hi, r);
+    bad |= negative_count(a.err, b, hi, r);
 #pragma unroll
     for (int i = 0; i < 4; ++i) free_n += r[i] == 0;
   }
@@ -161,7 +176,6 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
   const int c_lo = min(a.n_chunks, c_per * rank), c_hi = min(a.n_chunks, c_per * (rank + 1));
   int need_n = 0;
   for (int c = c_lo + tid; c < c_hi; c += kThreads) need_n += a.src[c].len % a.block_size != 0;
-  int bad = 0;
   for (int c = warp; c < a.n_chunks; c += kWarps) {
     const fuse_chunk_t s = a.src[c];
     const int n = n_entries(s, a.block_size);
@@ -279,6 +293,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
   for (int b = lo + 4 * tid; b < hi; b += 4 * kThreads) {
     int r[4];
     refs4(b, r);
+    bad |= negative_count(a.err, b, hi, r);
 #pragma unroll
     for (int i = 0; i < 4; ++i) live += r[i] > 0;
   }

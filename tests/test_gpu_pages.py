@@ -348,3 +348,29 @@ def test_prompt_quantize_attend_together():
         e = 8 * S * ((d + 16) * 2.0 ** -23 + 2.0 ** -20)
         tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -9 + 2 * e) * A
         assert (np.abs(f64(o1[0, h]) - o) <= tol).all()
+
+
+@pytest.mark.parametrize("call", ["fork", "compact"])
+@pytest.mark.parametrize("n_blocks,page", [(8, 1), (8, 7), (9, 8), (33003, 4), (33003, 33002), (33003, 20000)])
+def test_a_negative_count_is_refused_as_a_whole(call, n_blocks, page):
+    """A page whose count is negative and that no table names: below the live
+    pages' number it would leave fewer holes than pages to move."""
+    top = n_blocks - 2 if page == n_blocks - 1 else n_blocks - 1
+    tab, lens = dev([[0, top], [3]]), [20, 16]
+    refs = torch.zeros(n_blocks, dtype=torch.int32, device="cuda")
+    refs[torch.tensor([0, top, 3])] = 1
+    refs[page] = -1
+    r0, t0 = refs.clone(), lists(tab)
+    out = dev([[-9, -9], [-9]])
+    src, dst = page_table(tab, lens, 16, n_blocks), page_table(out, lens, 16, n_blocks)
+    moves, ws = fk.alloc_moves(n_blocks // 2), fk.alloc_pages_workspace(src)
+    moves.fill_(99)
+    if call == "fork":
+        fk.pages_fork(src, dst, refs, moves, ws)
+    else:
+        fk.pages_compact(src, refs, moves, ws)
+    with pytest.raises(fk.FuseError) as e:
+        fk.check_errors(ws)
+    assert e.value.status == fk.FUSE_ERR_DEVICE_BOUNDS
+    assert torch.equal(refs, r0) and lists(tab) == t0 and lists(out) == [[-9, -9], [-9]]
+    assert int(moves[0]) == 0 and (moves[2:] == 99).all()
