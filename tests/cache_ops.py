@@ -52,6 +52,9 @@ class AttendCase:
     gap: int = 0                          # unused side rows behind each request
     pos_shift: int = 0                    # added to every chunk's angle offset
     spare_blocks: int = 0                 # pool pages before the used ones
+    # stairs of a chunk's tokens: (tokens of a step, steps until they start over,
+    # what a step adds to a score, to the logarithm (base 2) of the values)
+    rise: Optional[tuple] = None
     seed: int = 0
 
 
@@ -69,6 +72,12 @@ class Attend:
         f32 = lambda *s: rng.standard_normal(s).astype(np.float32).astype(np.float64)  # noqa: E731
         K = f32(T, Hkv, d) * np.exp(0.4 * f32(1, Hkv, d)) + 0.5 * f32(1, Hkv, d)
         V = f32(T, Hkv, d)
+        if c.rise:
+            # by the first channel of the slowest pair, which an offset hardly turns
+            each, steps, score, value = c.rise
+            at = (np.concatenate([np.arange(n) for n in flat]) // each % steps)[:, None]
+            K[..., d // 2 - 1] = score * np.sqrt(d) / 4.0 * at
+            V = (V * 2.0 ** (value * at)[..., None]).astype(np.float32).astype(np.float64)
         bits = {"u4": 4, "u8": 8}.get(c.storage)
         keys, vals, mk, mv = [], [], [], []
         codes = {"K": [], "V": [], "ks": [], "kz": [], "vs": [], "vz": []}
@@ -162,7 +171,10 @@ class Attend:
                 dst[r.out0:r.out0 + n] = torch.from_numpy(f32(n, Hkv, d)).to(DT[c.dtype]).cuda()
         self.idx_list = [np.sort(rng.permutation(n)[:k]) for n, k in zip(n_ctx, c.k)]
         self.idx = torch.from_numpy(np.concatenate(self.idx_list).astype(np.int32)).cuda()
-        self.Q = torch.from_numpy(1.5 * f32(len(reqs) * c.new, Hq, d)).to(DT[c.dtype]).cuda()
+        Q = 1.5 * f32(len(reqs) * c.new, Hq, d)
+        if c.rise:
+            Q[..., d // 2 - 1], Q[..., d - 1] = 4.0, 0.0
+        self.Q = torch.from_numpy(Q).to(DT[c.dtype]).cuda()
         self.O = torch.full_like(self.Q, 7.0)
         self.chunks = self.table()
         self.ws = fk.alloc_attend_workspace(self.desc, self.chunks, self.reqs, c.new)
@@ -203,9 +215,17 @@ class Attend:
                          self.Vs, self.O, self.ws, stream)
         return self.O
 
+    def segments(self, n_new=None):
+        """Segments that the plan has cut the call's keys into."""
+        Hq, Hkv, d = self.c.heads
+        per = Hkv * -(-(Hq // Hkv) * (n_new or self.c.new) // 8)
+        size = fk.attend_workspace_size(self.desc, self.chunks, self.reqs, n_new or self.c.new)
+        return (size - 256) // (per * 8 * (8 + 4 * d))
+
     def reference(self, rows=None, unseen=()):
-        """(O, tolerance) in fp64 for every output row; `unseen`: side rows
-        (request-local) that have no weight.
+        """(O, tolerance) in fp64 for every output row, or for the (row, head)
+        pairs of `rows`, the others NaN; `unseen`: side rows (request-local)
+        that have no weight.
 
         With A = sum p |v| and S = max sum |q k| / sqrt(d) (magnitudes of a
         code's zero and scaled part added), a score is off by at most
@@ -218,7 +238,7 @@ class Attend:
         c = self.c
         Hq, Hkv, d = c.heads
         offs = self.offsets()
-        O = np.zeros((len(c.lens) * c.new, Hq, d))
+        O = np.full((len(c.lens) * c.new, Hq, d), np.nan if rows is not None else 0.0)
         tol = np.zeros_like(O)
         Ks, Vs, Q = f64(self.Ks), f64(self.Vs), f64(self.Q)
         i = 0
@@ -243,6 +263,8 @@ class Attend:
                 kk, vv = np.concatenate([k, sk]), np.concatenate([v, sv])
                 ma, mb = np.concatenate([mk, np.abs(sk)]), np.concatenate([mv, np.abs(sv)])
                 for h in range(Hq):
+                    if rows is not None and (r * c.new + u, h) not in rows:
+                        continue
                     g = h * Hkv // Hq
                     o, A, S = attention(Q[r * c.new + u, h], kk[:, g], vv[:, g], ma[:, g], mb[:, g])
                     n = len(kk)

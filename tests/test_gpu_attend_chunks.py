@@ -345,3 +345,45 @@ def test_a_request_table_edited_in_place_on_another_stream_and_before_a_capture(
     got = a.O.clone()
     assert torch.equal(a.run(stream=s.cuda_stream), got) and not torch.equal(got, want)
     fk.check_errors(a.ws)
+
+
+SLOT = {"u4": 64, "u8": 32, "bf16": 16, "f32": 32}       # keys that an item takes at a time
+
+
+def check_long(a: Attend, at_least):
+    """A call whose items hold at_least keys on average, at six rows and heads
+    (a key's weight, scales and position show in each)."""
+    Hq, new = a.c.heads[0], a.c.new
+    n = sum(a.n_ctx) + sum(r.k + r.n_query - new for r in a.reqs.host[:a.reqs.n])
+    assert n / a.segments() >= at_least > SLOT[a.c.storage]
+    got = f64(a.run())
+    fk.check_errors(a.ws)
+    rows = [(u, h) for u in (0, len(got) - 1) for h in (0, Hq // 3, Hq - 1)]
+    want, tol = a.reference(rows)
+    for i in rows:
+        err = np.abs(got[i] - want[i])
+        assert (err <= tol[i]).all(), (i, float(np.nanmax(err / tol[i])))
+
+
+@pytest.mark.parametrize("score,value", [(6.0, 0.0), (0.0, 10.0), (6.0, 10.0)])
+@pytest.mark.parametrize("dtype,storage,paged,d", [
+    ("bf16", "u4", False, 128), ("bf16", "u4", True, 128), ("bf16", "u4", True, 64), ("bf16", "u8", False, 128),
+    ("bf16", "u8", True, 64), ("bf16", "bf16", False, 64), ("bf16", "bf16", True, 128), ("f32", "u4", False, 64),
+    ("f32", "u8", True, 128), ("f32", "f32", False, 128)])
+def test_items_of_several_slots(dtype, storage, paged, d, score, value):
+    # 256 keys an item; from slot to slot the scores rise by 6 (8.7 in log2: past
+    # what the running maximum may lag) or stay, the values' scales by 2^10 over
+    # an item; the selection hides every third key or so
+    steps = 256 // SLOT[storage]
+    a = Attend(AttendCase(lens=[[30000, 27000]], n_query=[9], k=[18000], dtype=dtype, storage=storage, paged=paged,
+                          block_size=24, heads=(8, 1, d), new=8, rise=(SLOT[storage], steps, score, value / (steps - 1))))
+    check_long(a, 160)
+
+
+@pytest.mark.parametrize("dtype,storage,paged", [("bf16", "u4", True), ("bf16", "u8", False), ("bf16", "bf16", False),
+                                                 ("f32", "u4", False)])
+def test_items_of_1024_keys(dtype, storage, paged):
+    steps = 1024 // SLOT[storage]
+    a = Attend(AttendCase(lens=[[120000, 105000]], n_query=[9], k=[500], dtype=dtype, storage=storage, paged=paged,
+                          block_size=1000, heads=(8, 1, 64), new=8, rise=(SLOT[storage], steps, 6.0, 10.0 / steps)))
+    check_long(a, 850)                                   # fp32 items: 992, in whole steps of 32
