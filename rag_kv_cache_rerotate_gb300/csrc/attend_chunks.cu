@@ -28,7 +28,7 @@ namespace fusekv {
 
 namespace {
 
-constexpr int kWarps = 4;                 // items of a CTA of the CUDA-core kernel
+constexpr int kWarps = kItemWarps;
 constexpr int kAtOnce = 8;                // keys whose values it reads at a time
 
 // Eight consecutive stored elements as fp32.
@@ -236,26 +236,27 @@ __device__ void attend_item(const AttendArgs& a, const Keys& y, const float2* cs
 
 template <int ST, int D>
 __global__ void __launch_bounds__(kWarps * 32)
-    attend_simt_kernel(const AttendArgs a, const __grid_constant__ ChunkOwners owners,
-                       const __grid_constant__ RopeFreqs f, int side_ctas) {
+    attend_simt_kernel(const AttendArgs a, const __grid_constant__ ItemTable tab,
+                       const __grid_constant__ RopeFreqs f) {
   __shared__ float s_q[kWarps][kVecs][D];
   __shared__ float s_p[kWarps][32][kVecs];
   __shared__ float2 s_cs[D / 2];
   const int warp = threadIdx.x / 32;
+  const ItemPlace at = item_place(a, tab);
   pdl_wait();
   pdl_trigger();                           // the join may read the call's inputs before it waits
-  const int per_seg = a.n_kv_heads * a.nvg;
-  const int ctas = (a.nsub * per_seg + kWarps - 1) / kWarps;
-  const int b = (int)blockIdx.x - ctas * a.n_chunks;
-  if (b >= 0) {
+  if (at.none) return;
+  const int h = at.h, vg = at.vg;
+  if (at.side) {
     // side rows: those before the new tokens
-    const int r = a.req0 + b / side_ctas;
-    const int i = (b % side_ctas) * kWarps + warp;
-    const int seg = i / per_seg, h = i % per_seg / a.nvg, vg = i % a.nvg;
+    const int r = a.req0 + at.part;
     const fuse_request_t R = a.reqs[r];
     const int n = R.k + R.n_query - a.n_new;
-    const int t0 = seg * a.sseg;
-    if (seg >= a.nside || t0 >= n) return;
+    const int t0 = at.seg * a.sseg;
+    if (t0 >= n) {                         // only where the two copies of the table differ
+      no_keys(a, at);
+      return;
+    }
     Keys y;
     constexpr int RB = row_bytes<FUSE_F32>(D);
     y.k = reinterpret_cast<const uint8_t*>(a.Ks) + R.out0 * a.n_kv_heads * RB;
@@ -272,14 +273,10 @@ __global__ void __launch_bounds__(kWarps * 32)
           report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_ATTEND_SEL, (uint32_t)t);
       }
     }
-    attend_item<FUSE_F32, D>(a, y, nullptr, nullptr, nullptr, r, h, vg,
-                          a.chunk_slots + (int64_t)r * a.nside + seg, s_q[warp], s_p[warp]);
+    attend_item<FUSE_F32, D>(a, y, nullptr, nullptr, nullptr, r, h, vg, at.slot, s_q[warp], s_p[warp]);
     return;
   }
-  const int ci = blockIdx.x / ctas;
-  const int i = (blockIdx.x % ctas) * kWarps + warp;
-  const int seg = i / per_seg, h = i % per_seg / a.nvg, vg = i % a.nvg;
-  const fuse_chunk_t C = a.chunks[a.chunk0 + ci];
+  const fuse_chunk_t C = a.chunks[a.chunk0 + at.part];
   // the chunk's angles, D / 16 pairs a warp.  The frequencies are launch
   // parameters, which a warp reads fast only at one address at a time.
   if (C.pos != 0) {                        // block-uniform
@@ -299,15 +296,12 @@ __global__ void __launch_bounds__(kWarps * 32)
     if (lane < N) s_cs[warp * N + lane] = make_float2(c, sn);
   }
   __syncthreads();
-  const int t0 = seg * a.seg;
-  if (seg >= a.nsub) return;
-  if (t0 >= C.len) {                       // past the chunk's end: an item without a key
-    if (threadIdx.x % 32 < kVecs)
-      a.part_ml[(((int64_t)(a.chunk0 + ci) * a.nsub + seg) * per_seg + i % per_seg) * kVecs +
-                threadIdx.x % 32] = make_float2(-INFINITY, 0.f);
+  const int t0 = at.seg * a.seg;
+  if (t0 >= C.len) {                       // past the chunk's end
+    no_keys(a, at);
     return;
   }
-  const int r = owners.req[ci];
+  const int r = tab.owner[at.part];
   const fuse_request_t R = a.reqs[r];
   Keys y;
   y.k = reinterpret_cast<const uint8_t*>(C.k);
@@ -321,8 +315,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   y.skip = a.idx + R.sel0;
   y.pos0 = (int)(C.dst_row - R.row0);
   attend_item<ST, D>(a, y, C.pos != 0 ? s_cs : nullptr, reinterpret_cast<const __half*>(C.k_scale),
-                     reinterpret_cast<const __half*>(C.k_zero), r, h, vg,
-                        (int64_t)(a.chunk0 + ci) * a.nsub + seg, s_q[warp], s_p[warp]);
+                     reinterpret_cast<const __half*>(C.k_zero), r, h, vg, at.slot, s_q[warp], s_p[warp]);
 }
 
 // Joins the items of one query vector (blockIdx.x = new token * Hq + head)
@@ -356,7 +349,7 @@ __device__ __forceinline__ void add4(float4& a, float w, const float4& x) {
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads)
-    attend_combine_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ RequestChunks rc) {
+    attend_combine_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ JoinTable tab) {
   constexpr int kWarpsJ = kJoinThreads / 32, L = D / 4, kSub = 32 / L;   // lanes, items of a warp step
   __shared__ float s_w[kJoinTile];
   __shared__ float s_own[FUSE_ATTEND_MAX_NEW];
@@ -369,10 +362,10 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int h = hq / a.g;
   const int vi = u * a.g + hq % a.g;      // vector of its KV head
   const fuse_request_t R = a.reqs[r];
-  const int64_t c0 = rc.first[blockIdx.y];
-  const int n_seg = (int)(rc.first[blockIdx.y + 1] - c0) * a.nsub;
+  const int seg0 = tab.seg[blockIdx.y], side0 = tab.side[blockIdx.y];
+  const int n_seg = tab.seg[blockIdx.y + 1] - seg0;
   const int n_side = R.k + R.n_query - a.n_new;           // side rows in items
-  const int n = n_seg + min(a.nside, (n_side + a.sseg - 1) / a.sseg);
+  const int n = n_seg + tab.side[blockIdx.y + 1] - side0;
   // own keys: warp j takes new token j
   const T* Ks = reinterpret_cast<const T*>(a.Ks);
   const T* Vs = reinterpret_cast<const T*>(a.Vs);
@@ -395,8 +388,8 @@ __global__ void __launch_bounds__(kJoinThreads)
   // item e's vector: chunk segments, then side segments
   const int64_t step = (int64_t)a.n_kv_heads * a.nvg * kVecs;
   const int64_t mine = ((int64_t)h * a.nvg + vi / kVecs) * kVecs + vi % kVecs;
-  const int64_t at_seg = c0 * a.nsub * step + mine;
-  const int64_t at_side = (a.chunk_slots + (int64_t)r * a.nside - n_seg) * step + mine;
+  const int64_t at_seg = seg0 * step + mine;
+  const int64_t at_side = (side0 - n_seg) * step + mine;
   auto part = [&](int e) { return (e < n_seg ? at_seg : at_side) + e * step; };
   const int sub = lane / L, ch = lane % L * 4;
   float M = -INFINITY, l = 0.f;
@@ -469,23 +462,17 @@ __global__ void __launch_bounds__(kJoinThreads)
 }
 
 template <int ST, int D>
-cudaError_t launch_simt_t(const AttendArgs& a, const ChunkOwners& o, const RopeFreqs& f,
-                          int side_reqs, cudaStream_t s) {
-  const int per_seg = a.n_kv_heads * a.nvg;
-  const int side = (a.nside * per_seg + kWarps - 1) / kWarps;
-  const int ctas = (a.nsub * per_seg + kWarps - 1) / kWarps;
-  const int64_t grid = (int64_t)side * side_reqs + (int64_t)ctas * a.n_chunks;
-  if (grid == 0) return cudaSuccess;
-  return launch_pdl(attend_simt_kernel<ST, D>, dim3((unsigned)grid), dim3(kWarps * 32), 0, s, a,
-                    o, f, std::max(side, 1));
+cudaError_t launch_simt_t(const AttendArgs& a, const ItemTable& t, const RopeFreqs& f, cudaStream_t s) {
+  return launch_pdl(attend_simt_kernel<ST, D>, dim3((unsigned)item_ctas(a, t)), dim3(kWarps * 32), 0, s, a,
+                    t, f);
 }
 
 template <int D>
-cudaError_t launch_simt_d(int st, const AttendArgs& a, const ChunkOwners& o, const RopeFreqs& f,
-                          int side_reqs, cudaStream_t s) {
-  if (st == FUSE_U4_ASYM) return launch_simt_t<FUSE_U4_ASYM, D>(a, o, f, side_reqs, s);
-  if (st == FUSE_U8_ASYM) return launch_simt_t<FUSE_U8_ASYM, D>(a, o, f, side_reqs, s);
-  return launch_simt_t<FUSE_F32, D>(a, o, f, side_reqs, s);
+cudaError_t launch_simt_d(int st, const AttendArgs& a, const ItemTable& t, const RopeFreqs& f,
+                          cudaStream_t s) {
+  if (st == FUSE_U4_ASYM) return launch_simt_t<FUSE_U4_ASYM, D>(a, t, f, s);
+  if (st == FUSE_U8_ASYM) return launch_simt_t<FUSE_U8_ASYM, D>(a, t, f, s);
+  return launch_simt_t<FUSE_F32, D>(a, t, f, s);
 }
 
 // ---- host side ---------------------------------------------------------------
@@ -498,11 +485,18 @@ int cut(int64_t keys, int64_t items, int step) {     // keys per item, a multipl
   return (int)std::min<int64_t>(kMaxKeys, std::max<int64_t>(step, (k + step - 1) / step * step));
 }
 
-// Checks everything that needs no tensor; owner[c]: request of chunk c,
-// first[r]: first chunk of request r (n_req + 1 entries).
+// Where a call's segments are: owner[c], seg0[c]: request and first segment of
+// chunk c; first[r], side0[r]: first chunk and first side segment of request r
+// (seg0, first, side0: one entry more than there are chunks or requests).
+struct AttendTables {
+  std::vector<uint16_t> owner;
+  std::vector<int32_t> seg0, first, side0;
+};
+
+// Checks everything that needs no tensor, and fills T if it is not null.
 fuse_status_t plan_attend(const fuse_layer_desc_t* desc, const fuse_chunks_t* chunks,
                           const fuse_requests_t* reqs, int n_new, bool need_device, ReqInfo* info,
-                          AttendPlan* P, uint16_t* owner, int32_t* first) {
+                          AttendPlan* P, AttendTables* T) {
   fuse_status_t st = check_desc(desc);
   if (st != FUSE_OK) return st;
   st = check_reqs(reqs, info, need_device);
@@ -520,9 +514,9 @@ fuse_status_t plan_attend(const fuse_layer_desc_t* desc, const fuse_chunks_t* ch
   int max_len = 0;
   st = check_chunks(*desc, &c, info->tot.n_tok, &max_len);
   if (st != FUSE_OK) return st;
-  int64_t n_ctx = 0, n_side = 0, max_side = 0;
+  int64_t n_ctx = 0, n_side = 0;
   int r = 0;
-  if (first) first[0] = 0;
+  if (T) T->first[0] = 0;
   const fuse_request_t* R = reqs->h_req;
   int64_t end = 0;
   for (int i = 0; i < chunks->n_chunks; ++i) {
@@ -533,20 +527,18 @@ fuse_status_t plan_attend(const fuse_layer_desc_t* desc, const fuse_chunks_t* ch
     // request before it)
     while (r < reqs->n_req && q.dst_row + (q.len > 0) > R[r].row0 + R[r].n_ctx) {
       ++r;
-      if (first) first[r] = i;
+      if (T) T->first[r] = i;
     }
     if (q.len > 0 && (r >= reqs->n_req || q.dst_row < R[r].row0 || end > R[r].row0 + R[r].n_ctx))
       return FUSE_ERR_INVALID_ARG;
-    if (owner) owner[i] = (uint16_t)std::min(r, std::max(0, reqs->n_req - 1));
+    if (T) T->owner[i] = (uint16_t)std::min(r, std::max(0, reqs->n_req - 1));
     n_ctx += q.len;
   }
-  if (first)
-    for (int k = r + 1; k <= reqs->n_req; ++k) first[k] = chunks->n_chunks;
+  if (T)
+    for (int k = r + 1; k <= reqs->n_req; ++k) T->first[k] = chunks->n_chunks;
   for (int i = 0; i < reqs->n_req; ++i) {
     if (R[i].n_query < n_new) return FUSE_ERR_INVALID_ARG;
-    const int64_t n = (int64_t)R[i].k + R[i].n_query - n_new;
-    n_side += n;
-    max_side = std::max(max_side, n);
+    n_side += (int64_t)R[i].k + R[i].n_query - n_new;
   }
   const int g = desc->n_q_heads / desc->n_kv_heads;
   P->nvg = (g * n_new + kVecs - 1) / kVecs;
@@ -560,19 +552,31 @@ fuse_status_t plan_attend(const fuse_layer_desc_t* desc, const fuse_chunks_t* ch
   // item, 13.5 with 64.
   const int least = desc->dtype == FUSE_BF16 ? 64 : 32;
   const int seg = cut(n_ctx * per, kItems, least);
-  P->nsub = std::max(1, (max_len + seg - 1) / seg);
-  P->seg = cut(std::max(max_len, 1), P->nsub, 32);
-  const int sseg = cut(n_side * per, kItems / 2, least);
-  P->nside = (int)((max_side + sseg - 1) / sseg);
-  P->sseg = sseg;
-  P->chunk_slots = (int64_t)chunks->n_chunks * P->nsub;
-  P->slots = P->chunk_slots + (int64_t)reqs->n_req * P->nside;
+  // the longest chunk's segments are evened out
+  P->seg = cut(std::max(max_len, 1), std::max(1, (max_len + seg - 1) / seg), 32);
+  P->sseg = cut(n_side * per, kItems / 2, least);
+  // a chunk's segments fill whole CTAs
+  const int pad = per % kItemWarps == 0 ? 1 : per % 2 == 0 ? 2 : kItemWarps;
+  static_assert(kItemWarps == 4, "pad: what makes pad * per a multiple of kItemWarps");
+  int64_t slots = 0;
+  for (int i = 0; i < chunks->n_chunks; ++i) {
+    if (T) T->seg0[i] = (int32_t)slots;
+    const int n = (chunks->h_chunks[i].len + P->seg - 1) / P->seg;
+    slots += (n + pad - 1) / pad * pad;
+  }
+  if (T) T->seg0[chunks->n_chunks] = (int32_t)slots;
+  for (int i = 0; i < reqs->n_req; ++i) {
+    if (T) T->side0[i] = (int32_t)slots;
+    slots += ((int64_t)R[i].k + R[i].n_query - n_new + P->sseg - 1) / P->sseg;
+  }
+  if (T) T->side0[reqs->n_req] = (int32_t)slots;
+  P->slots = slots;
+  // an item count past a launch's grid is far past what a card holds
+  if (slots > INT32_MAX / per) return FUSE_ERR_UNSUPPORTED;
   const size_t vecs = (size_t)P->slots * per * kVecs;
   P->part_ml = sizeof(WsHeader);
   P->part_o = align_up(P->part_ml + vecs * sizeof(float2), 256);
   P->total = align_up(P->part_o + vecs * desc->head_dim * sizeof(float), 256);
-  // an item count past a launch's grid is far past what a card holds
-  if (P->slots * per > INT32_MAX) return FUSE_ERR_UNSUPPORTED;
   return FUSE_OK;
 }
 
@@ -585,18 +589,16 @@ fuse_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? FUSE_OK : F
 }  // namespace
 
 cudaError_t launch_attend_simt(const fuse_layer_desc_t& d, int st, const AttendArgs& a,
-                               const ChunkOwners& o, const RopeFreqs& f, int side_reqs,
-                               cudaStream_t s) {
-  return d.head_dim == 128 ? launch_simt_d<128>(st, a, o, f, side_reqs, s)
-                           : launch_simt_d<64>(st, a, o, f, side_reqs, s);
+                               const ItemTable& t, const RopeFreqs& f, cudaStream_t s) {
+  return d.head_dim == 128 ? launch_simt_d<128>(st, a, t, f, s) : launch_simt_d<64>(st, a, t, f, s);
 }
 
 cudaError_t launch_attend_combine(const fuse_layer_desc_t& d, const AttendArgs& a,
-                                  const RequestChunks& rc, bool early, cudaStream_t s) {
+                                  const JoinTable& t, bool early, cudaStream_t s) {
   const dim3 grid(a.n_new * a.n_q_heads, a.n_req);
   auto go = [&](auto kernel) {
-    if (early) return launch_pdl(kernel, grid, dim3(kJoinThreads), 0, s, a, rc);
-    kernel<<<grid, kJoinThreads, 0, s>>>(a, rc);
+    if (early) return launch_pdl(kernel, grid, dim3(kJoinThreads), 0, s, a, t);
+    kernel<<<grid, kJoinThreads, 0, s>>>(a, t);
     return cudaGetLastError();
   };
   if (d.dtype == FUSE_BF16)
@@ -618,7 +620,7 @@ fuse_status_t fuse_attend_workspace_size(const fuse_layer_desc_t* desc, const fu
   if (!bytes) return FUSE_ERR_INVALID_ARG;
   ReqInfo info;
   AttendPlan P;
-  const fuse_status_t st = plan_attend(desc, chunks, reqs, n_new, false, &info, &P, nullptr, nullptr);
+  const fuse_status_t st = plan_attend(desc, chunks, reqs, n_new, false, &info, &P, nullptr);
   if (st != FUSE_OK) return st;
   *bytes = P.total;
   return FUSE_OK;
@@ -631,15 +633,16 @@ fuse_status_t fuse_attend_chunks(const fuse_layer_desc_t* desc, const fuse_chunk
   if (!chunks || chunks->n_chunks < 0 || !reqs || reqs->n_req < 0) return FUSE_ERR_INVALID_ARG;
   ReqInfo info;
   AttendPlan P;
-  std::vector<uint16_t> owner;
-  std::vector<int32_t> first;
+  AttendTables T;
   try {
-    owner.resize(chunks->n_chunks);
-    first.resize((size_t)reqs->n_req + 1);
+    T.owner.resize(chunks->n_chunks);
+    T.seg0.resize((size_t)chunks->n_chunks + 1);
+    T.first.resize((size_t)reqs->n_req + 1);
+    T.side0.resize((size_t)reqs->n_req + 1);
   } catch (...) {
     return FUSE_ERR_INVALID_ARG;
   }
-  fuse_status_t st = plan_attend(desc, chunks, reqs, n_new, true, &info, &P, owner.data(), first.data());
+  fuse_status_t st = plan_attend(desc, chunks, reqs, n_new, true, &info, &P, &T);
   if (st != FUSE_OK) return st;
   if (reqs->n_req > 0 && (!Q || !Ks || !Vs || !O)) return FUSE_ERR_INVALID_ARG;
   if (info.tot.n_sel > 0 && !idx) return FUSE_ERR_INVALID_ARG;
@@ -661,44 +664,61 @@ fuse_status_t fuse_attend_chunks(const fuse_layer_desc_t* desc, const fuse_chunk
   a.part_ml = at<float2>(ws, P.part_ml);
   a.err = at<uint32_t>(ws, 0);
   a.n_pool_blocks = chunks->n_pool_blocks;
-  a.chunk_slots = P.chunk_slots;
   a.n_q_heads = desc->n_q_heads;
   a.n_kv_heads = desc->n_kv_heads;
   a.g = desc->n_q_heads / desc->n_kv_heads;
   a.n_new = n_new;
   a.nvg = P.nvg;
   a.seg = P.seg;
-  a.nsub = P.nsub;
   a.sseg = P.sseg;
-  a.nside = P.nside;
   a.block_size = chunks->kv_layout == FUSE_KV_PAGED ? chunks->block_size : 0;
   a.scale = 1.4426950408889634f / std::sqrt((float)desc->head_dim);
   cudaStream_t s = (cudaStream_t)stream;
-  // the side rows of all requests and the first chunks; then the other chunks
-  ChunkOwners owners;
-  a.req0 = 0;
-  a.n_req = reqs->n_req;
-  for (int c0 = 0; c0 == 0 || c0 < chunks->n_chunks; c0 += kChunkBatch) {
-    a.chunk0 = c0;
-    a.n_chunks = std::min(kChunkBatch, chunks->n_chunks - c0);
-    std::copy(owner.begin() + c0, owner.begin() + c0 + a.n_chunks, owners.req);
+  // items: as many chunks, and as many requests' side rows, as a launch takes
+  ItemTable t;
+  const int per = a.n_kv_heads * a.nvg;
+  auto take = [](const std::vector<int32_t>& start, int i, int n, int most, uint16_t* out) {
+    int k = 0;
+    out[0] = 0;
+    while (i + k < n && k < most && start[i + k + 1] - start[i] <= kSegBatch) {
+      ++k;
+      out[k] = (uint16_t)(start[i + k] - start[i]);
+    }
+    return k;
+  };
+  bool items = false;
+  for (int c = 0, r = 0; c < chunks->n_chunks || r < reqs->n_req; c += a.n_chunks, r += a.n_req) {
+    a.chunk0 = c;
+    a.n_chunks = take(T.seg0, c, chunks->n_chunks, kChunkBatch, t.seg);
+    a.chunk_slot0 = T.seg0[c];
+    a.chunk_ctas = (int)((int64_t)t.seg[a.n_chunks] * per / kItemWarps);
+    a.chunk_inv = (float)a.n_chunks / std::max<int>(1, t.seg[a.n_chunks]);
+    a.req0 = r;
+    a.n_req = take(T.side0, r, reqs->n_req, kSideBatch, t.side);
+    a.side_slot0 = T.side0[r];
+    a.side_inv = (float)a.n_req / std::max<int>(1, t.side[a.n_req]);
+    std::copy(T.owner.begin() + c, T.owner.begin() + c + a.n_chunks, t.owner);
+    if (item_ctas(a, t) == 0) continue;
+    items = true;
     st = cuda_status(traced("attend_chunks", s, [&] {
       const auto launch = desc->dtype == FUSE_BF16 ? launch_attend_mma : launch_attend_simt;
-      return launch(*desc, chunks->kv_storage, a, owners, f, c0 == 0 ? a.n_req : 0, s);
+      return launch(*desc, chunks->kv_storage, a, t, f, s);
     }));
     if (st != FUSE_OK) return st;
   }
   // The join reads the call's inputs before it waits for the kernel before it,
   // which is one of the above, begun after what wrote them had ended.  Without
   // an item there is none, and the first join starts after what came before.
-  const bool items = chunks->n_chunks > 0 || P.nside > 0;
   for (int r0 = 0; r0 < reqs->n_req; r0 += kReqBatch) {
-    RequestChunks rc;
+    JoinTable j;
     a.req0 = r0;
     a.n_req = std::min(kReqBatch, reqs->n_req - r0);
-    std::copy(first.begin() + r0, first.begin() + r0 + a.n_req + 1, rc.first);
+    for (int i = 0; i <= a.n_req; ++i) {
+      j.seg[i] = T.seg0[T.first[r0 + i]];
+      j.side[i] = T.side0[r0 + i];
+    }
     st = cuda_status(traced("attend_combine", s, [&] {
-      return launch_attend_combine(*desc, a, rc, items || r0 > 0, s);
+      return launch_attend_combine(*desc, a, j, items || r0 > 0, s);
     }));
     if (st != FUSE_OK) return st;
   }

@@ -42,7 +42,7 @@ namespace fusekv {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = kItemWarps;
 constexpr int kSlots = 2;
 constexpr float kRaise = 8.0f;            // log2: P <= 2^8, times a scale <= 2^6 stays in fp16
 constexpr float kTiny = 1.17549435e-38f;  // 2^-126
@@ -885,34 +885,33 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Item& y, 
 
 template <int ST, int D>
 __global__ void __launch_bounds__(kWarps * 32, 3)
-    attend_mma_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ ChunkOwners owners,
-                      const __grid_constant__ RopeFreqs f, int side_ctas) {
+    attend_mma_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ ItemTable t,
+                      const __grid_constant__ RopeFreqs f) {
   extern __shared__ __align__(16) uint8_t raw[];
   __shared__ float2 s_cs[D / 2];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   WarpSmem<D>& sm = reinterpret_cast<WarpSmem<D>*>(raw)[warp];
+  const ItemPlace at = item_place(a, t);
   pdl_wait();
   pdl_trigger();                           // the join may read the call's inputs before it waits
-  const int per_seg = a.n_kv_heads * a.nvg;
+  if (at.none) return;
   Item y;
-  const int ctas = (a.nsub * per_seg + kWarps - 1) / kWarps;
-  const int b = (int)blockIdx.x - ctas * a.n_chunks;
+  y.h = at.h;
+  y.vg = at.vg;
+  y.slot = at.slot;
   // the queries are read first: they do not depend on the tables' entries
-  const bool side = b >= 0;
-  const int ci = side ? 0 : blockIdx.x / ctas;
-  const int i = (side ? b % side_ctas : blockIdx.x % ctas) * kWarps + warp;
-  const int seg = i / per_seg;
-  y.h = i % per_seg / a.nvg;
-  y.vg = i % a.nvg;
-  y.r = side ? a.req0 + b / side_ctas : owners.req[ci];
+  y.r = at.side ? a.req0 + at.part : t.owner[at.part];
   RawQuery rq;
   read_query<D>(a, y.r, y.h, y.vg, rq);
-  if (side) {
+  if (at.side) {
     // side rows: those before the new tokens
     const fuse_request_t R = a.reqs[y.r];
     const int n = R.k + R.n_query - a.n_new;
-    y.t0 = seg * a.sseg;
-    if (seg >= a.nside || y.t0 >= n) return;
+    y.t0 = at.seg * a.sseg;
+    if (y.t0 >= n) {                       // only where the two copies of the table differ
+      no_keys(a, at);
+      return;
+    }
     constexpr int RB = Fmt<FUSE_BF16, D>::RB;
     const int64_t row = R.out0 * a.n_kv_heads + y.h;
     y.k = reinterpret_cast<const uint8_t*>(a.Ks) + row * RB;
@@ -921,7 +920,6 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
     y.table = y.skip = nullptr;
     y.t1 = min(n, y.t0 + a.sseg);
     y.n_skip = y.pos0 = 0;
-    y.slot = a.chunk_slots + (int64_t)y.r * a.nside + seg;
     if (y.h == 0 && y.vg == 0) {           // the selection, checked where its rows are read
       for (int t = y.t0 + lane; t < min(y.t1, R.k); t += 32) {
         const int v = a.idx[R.sel0 + t];
@@ -932,16 +930,14 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
     attend_rows<D>(a, y, rq, {nullptr, 0, false}, f, sm);
     return;
   }
-  const fuse_chunk_t C = a.chunks[a.chunk0 + ci];
+  const fuse_chunk_t C = a.chunks[a.chunk0 + at.part];
   const fuse_request_t R = a.reqs[y.r];
-  y.t0 = seg * a.seg;
+  y.t0 = at.seg * a.seg;
   const Angles cs{s_cs, C.pos, true};
-  if (seg >= a.nsub || y.t0 >= C.len) {    // past the chunk's end: an item without a key
+  if (y.t0 >= C.len) {                     // past the chunk's end
     form_angles<D>(cs, f);                 // this warp's part for the others
     __syncthreads();
-    if (seg < a.nsub && lane < kVecs)
-      a.part_ml[(((int64_t)(a.chunk0 + ci) * a.nsub + seg) * per_seg + i % per_seg) * kVecs + lane] =
-          make_float2(-INFINITY, 0.f);
+    no_keys(a, at);
     return;
   }
   constexpr int RB = Fmt<ST, D>::RB;
@@ -954,7 +950,6 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
   y.n_skip = R.k;
   y.skip = a.idx + R.sel0;
   y.pos0 = (int)(C.dst_row - R.row0);
-  y.slot = (int64_t)(a.chunk0 + ci) * a.nsub + seg;
   if constexpr (ST == FUSE_BF16)
     attend_rows<D>(a, y, rq, cs, f, sm);
   else
@@ -963,35 +958,27 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
 }
 
 template <int ST, int D>
-cudaError_t launch_mma_t(const AttendArgs& a, const ChunkOwners& o, const RopeFreqs& f,
-                         int side_reqs, cudaStream_t s) {
+cudaError_t launch_mma_t(const AttendArgs& a, const ItemTable& t, const RopeFreqs& f, cudaStream_t s) {
   const int smem = kWarps * (int)sizeof(WarpSmem<D>);
   const cudaError_t e = set_dyn_smem_once(reinterpret_cast<const void*>(attend_mma_kernel<ST, D>), smem);
   if (e != cudaSuccess) return e;
-  const int per_seg = a.n_kv_heads * a.nvg;
-  const int side = (a.nside * per_seg + kWarps - 1) / kWarps;
-  const int ctas = (a.nsub * per_seg + kWarps - 1) / kWarps;
-  const int64_t grid = (int64_t)side * side_reqs + (int64_t)ctas * a.n_chunks;
-  if (grid == 0) return cudaSuccess;
-  return launch_pdl(attend_mma_kernel<ST, D>, dim3((unsigned)grid), dim3(kWarps * 32), smem, s, a, o,
-                    f, std::max(side, 1));
+  return launch_pdl(attend_mma_kernel<ST, D>, dim3((unsigned)item_ctas(a, t)), dim3(kWarps * 32), smem, s,
+                    a, t, f);
 }
 
 template <int D>
-cudaError_t launch_mma_d(int st, const AttendArgs& a, const ChunkOwners& o, const RopeFreqs& f,
-                         int side_reqs, cudaStream_t s) {
-  if (st == FUSE_U4_ASYM) return launch_mma_t<FUSE_U4_ASYM, D>(a, o, f, side_reqs, s);
-  if (st == FUSE_U8_ASYM) return launch_mma_t<FUSE_U8_ASYM, D>(a, o, f, side_reqs, s);
-  return launch_mma_t<FUSE_BF16, D>(a, o, f, side_reqs, s);
+cudaError_t launch_mma_d(int st, const AttendArgs& a, const ItemTable& t, const RopeFreqs& f,
+                         cudaStream_t s) {
+  if (st == FUSE_U4_ASYM) return launch_mma_t<FUSE_U4_ASYM, D>(a, t, f, s);
+  if (st == FUSE_U8_ASYM) return launch_mma_t<FUSE_U8_ASYM, D>(a, t, f, s);
+  return launch_mma_t<FUSE_BF16, D>(a, t, f, s);
 }
 
 }  // namespace
 
 cudaError_t launch_attend_mma(const fuse_layer_desc_t& d, int st, const AttendArgs& a,
-                              const ChunkOwners& o, const RopeFreqs& f, int side_reqs,
-                              cudaStream_t s) {
-  return d.head_dim == 128 ? launch_mma_d<128>(st, a, o, f, side_reqs, s)
-                           : launch_mma_d<64>(st, a, o, f, side_reqs, s);
+                              const ItemTable& t, const RopeFreqs& f, cudaStream_t s) {
+  return d.head_dim == 128 ? launch_mma_d<128>(st, a, t, f, s) : launch_mma_d<64>(st, a, t, f, s);
 }
 
 }  // namespace fusekv

@@ -258,3 +258,35 @@ def test_request_table_device_copy_follows_the_host_table(fk):
         fk.attend_chunks(_desc(fk), _chunks(fk, [(0, 100)]), t, 1, Q, torch.zeros(3, dtype=torch.int32), S, S, Q,
                          torch.zeros(0, dtype=torch.uint8))
     assert bytes(t.dev.numpy()) == bytes(t.host)           # the call brought the copy up to date first
+
+
+@pytest.mark.parametrize("heads,n_new", [((32, 8), 1), ((64, 8), 8), ((4, 2), 1), ((3, 3), 1)])
+@pytest.mark.parametrize("long,short,n", [(8192, 32, 500), (32768, 16, 2000), (4096, 1, 4000)])
+def test_attend_workspace_does_not_grow_with_the_longest_chunk(fk, heads, n_new, long, short, n):
+    # one long chunk beside short ones takes what as many equal ones of the same
+    # tokens take, but for the short ones' partly filled segments
+    d = _desc(fk, n_q_heads=heads[0], n_kv_heads=heads[1])
+    total = long + short * n
+
+    def size(lens):
+        spans, at = [], 0
+        for x in lens:
+            spans.append((at, x))
+            at += x
+        r = _reqs(fk, [(0, 0, 0, 0, at, n_new, 0, 0)])
+        return fk.attend_workspace_size(d, _chunks(fk, spans), r, n_new)
+    assert size([short] * (n // 2) + [long] + [short] * (n - n // 2)) <= 1.5 * size([total // n] * n)
+
+
+@pytest.mark.parametrize("n,long", [(1000, 30000), (200, 4096)])
+def test_attend_workspace_does_not_grow_with_the_longest_generation(fk, n, long):
+    # requests that have generated little beside one that has generated much
+    d = _desc(fk, n_q_heads=32, n_kv_heads=8)
+
+    def size(queries):
+        reqs, row, out = [], 0, 0
+        for q in queries:
+            reqs.append((row, 0, 0, out, 0, q, 0, 0))
+            row, out = row + q, out + q
+        return fk.attend_workspace_size(d, _chunks(fk, []), _reqs(fk, reqs), 1)
+    assert size([2] * (n // 2) + [long] + [2] * (n // 2)) <= 1.5 * size([2 + long // n] * n)

@@ -387,3 +387,21 @@ def test_items_of_1024_keys(dtype, storage, paged):
     a = Attend(AttendCase(lens=[[120000, 105000]], n_query=[9], k=[500], dtype=dtype, storage=storage, paged=paged,
                           block_size=1000, heads=(8, 1, 64), new=8, rise=(SLOT[storage], steps, 6.0, 10.0 / steps)))
     check_long(a, 850)                                   # fp32 items: 992, in whole steps of 32
+
+
+@pytest.mark.parametrize("dtype,storage", [("bf16", "u4"), ("bf16", "bf16"), ("f32", "u8")])
+@pytest.mark.parametrize("heads,new", [((4, 2, 64), 1), ((3, 3, 64), 2), ((8, 1, 128), 3)])
+def test_long_chunks_beside_short_ones(dtype, storage, heads, new):
+    # chunks of very different lengths, empty ones, requests without any, long
+    # and short generations; segments that do and do not fill a CTA
+    lens = [[5] * 40 + [1500, 0, 0, 3], [], [1, 0, 700], [0], [2] * 300 + [900] + [1] * 300]
+    check(Attend(AttendCase(lens=lens, n_query=[3, 300, 7, 4, 9], k=[100, 0, 1, 0, 400], dtype=dtype, storage=storage,
+                            heads=heads, new=new)))
+
+
+def test_one_long_generation_among_many_requests():
+    # more requests than a launch takes the side rows of, most with none
+    n = 600
+    q = [1 + (i % 7 == 0) * (i % 40) for i in range(n)]
+    q[333] = 2000
+    check(Attend(AttendCase(lens=[[3] if i % 3 else [] for i in range(n)], n_query=q, k=[0] * n, heads=(2, 1, 64))))
