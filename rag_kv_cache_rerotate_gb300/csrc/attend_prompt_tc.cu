@@ -89,6 +89,10 @@ struct Ctl {
   // a unit's last V block: landed, looked through [unit % (V stages + 1)]
   uint64_t vl_full[kMaxStages + 1], v_ok[kMaxStages + 1];
   uint32_t tmem_base;
+  // the V copies asked for: a bit per stage, v_full was used, and the parity of
+  // its next phase; units whose last block was asked for
+  uint32_t v_used, v_phase;
+  int v_lasts;
   volatile int abort_flag;
   // [unit % (V stages + 1)][output warp] its rows of the unit's last V block
   // held elements that are not finite
@@ -149,6 +153,18 @@ __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, Ctl* ctl, ui
     report_error(err, FUSE_ERR_TIMEOUT, SITE_PROMPT_TIMEOUT, which);
   }
   return false;
+}
+
+// Waits (bounded) until the V copies asked for have landed: the last phase of
+// every barrier, which nothing follows.
+__device__ __noinline__ void land_v(Ctl* ctl, int stages) {
+  const int lasts = ctl->v_lasts;
+#pragma unroll 1
+  for (int st = 0; st < stages; ++st)
+    if (ctl->v_used >> st & 1) tc::mbar_wait(&ctl->v_full[st], (~ctl->v_phase >> st) & 1);
+#pragma unroll 1
+  for (int i = lasts > stages + 1 ? lasts - stages - 1 : 0; i < lasts; ++i)
+    tc::mbar_wait(&ctl->vl_full[i % (stages + 1)], (i / (stages + 1)) & 1);
 }
 
 __device__ __forceinline__ bool wait1(uint64_t* bar, uint32_t parity, Ctl* ctl, uint32_t* err,
@@ -354,7 +370,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kWarpV) {
     // ------------------------------ V loads ------------------------------
     if (lane == 0) {
-      uint32_t vc = 0;
+      uint32_t vc = 0, vph = 0, used = 0;              // v_full: a parity bit per stage, and whether it was used
+      int lasts = 0;                                   // units whose last block was asked for
       bool ok = true;
       int part = 0;
       for (int i = 0; unit_at(i) < n_units && ok; ++i) {
@@ -368,7 +385,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the last block has a barrier of its own: the output warps wait for
           // no other, and a waiter must visit every phase of a barrier.  Its
           // next use, kVS + 1 units on, comes after this block's P.V
-          uint64_t* bar = j == cur.nkb - 1 ? &ctl->vl_full[i % (kVS + 1)] : &ctl->v_full[st];
+          const bool last = j == cur.nkb - 1;
+          uint64_t* bar = last ? &ctl->vl_full[i % (kVS + 1)] : &ctl->v_full[st];
+          if (last) {
+            ++lasts;
+          } else {
+            used |= 1u << st;
+            vph ^= 1u << st;
+          }
           tc::mbar_arrive_expect_tx(bar, kTile);
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
@@ -376,7 +400,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             cur.t.row0 + j * kKB);
         }
       }
-      // every block is waited for before its P.V, and that before the CTA's end
+      // every block is waited for before its P.V, and that before the CTA's end,
+      // unless a wait gives up
+      ctl->v_used = used;
+      ctl->v_phase = vph;
+      ctl->v_lasts = lasts;
     }
   } else if (warp == kWarpS) {
     // ------------------------------ S = Q K^T ------------------------------
@@ -735,9 +763,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  if (ctl->abort_flag)                                 // copies and products in flight get time to end
+  if (ctl->abort_flag) {                               // copies land, products in flight get time to end
+    if (threadIdx.x == 0) land_v(ctl, kVS);
 #pragma unroll 1
     for (int k = 0; k < 1000; ++k) __nanosleep(1000);
+    __syncthreads();
+  }
   if (warp == kWarpS) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
