@@ -467,7 +467,12 @@ fuse_status_t fuse_kivi_quantize(const fuse_layer_desc_t* desc, const fuse_chunk
  * FUSE_ERR_UNSUPPORTED.  A block id outside the pool drops its
  * tokens, a selected index out of range or order is ignored; both are
  * recorded as FUSE_ERR_DEVICE_BOUNDS.  Softmax statistics and sums are fp32;
- * no atomics: equal inputs give equal outputs.  O may not overlap an input.
+ * no atomics: equal inputs give equal outputs.  In bf16 layers a weight meets
+ * the values in fp16 beside codes (with the value's scale), in two bf16 parts
+ * beside rows.  What a row does not see does not reach it, infinities and NaN
+ * included (the scales of a chunk whose every token is selected among them); of
+ * what it sees, a key of score -infinity has no weight and an infinite value
+ * makes its element infinite.  O may not overlap an input.
  * A captured call keeps the tables' sizes of its capture.  The workspace (of
  * fuse_attend_workspace_size, convention as for fuse_workspace_size) is
  * written before it is read. */
@@ -489,8 +494,10 @@ fuse_status_t fuse_attend_chunks(const fuse_layer_desc_t* desc, const fuse_chunk
  * without reuse.  Q, O: [T_total, Hq, d]; K, V: [T_total, Hkv, d]; Q and K
  * rotated by the caller.  Rows outside every request are neither read nor
  * written, and nothing that a row does not see reaches it, infinities and
- * NaN included.  Requests must be in row order and disjoint (else
- * FUSE_ERR_INVALID_ARG).  O may not overlap Q, K or V.  Needs the workspace
+ * NaN included; a key of score -infinity has no weight.  Statistics and sums
+ * are fp32; in bf16 layers the weights are rounded to bf16 where they meet the
+ * values (their sum is that of the unrounded ones).  Requests must be in row
+ * order and disjoint (else FUSE_ERR_INVALID_ARG).  O may not overlap Q, K or V.  Needs the workspace
  * of fuse_workspace_size. */
 fuse_status_t fuse_attend_prompt(const fuse_layer_desc_t* desc, const fuse_requests_t* reqs,
                                  const void* Q, const void* K, const void* V, void* O, void* ws,

@@ -22,7 +22,7 @@
 // normaliser are raised lazily.
 //
 // Measured with the join (4 bits, 8 KV heads, d = 128, 64 query heads): 8
-// requests of 33k tokens 89 us, 4.1 TB/s, where the bytes alone would take
+// requests of 33k tokens 90 us, 4.1 TB/s, where the bytes alone would take
 // 54; issue slots are two fifths full and a warp waits for its own results, not
 // for HBM.  16 paged requests of 0.5k to 8k tokens 36 us, 8 chunks of 512
 // tokens 11 us (latency).  An item runs its start once, so instruction fetches
