@@ -231,8 +231,9 @@ class RequestTable:
 
     ``host`` may be edited in place (a decode loop raises ``n_query``):
     ``attend_chunks`` and ``attend_prompt`` then write the device copy anew on
-    their stream before they read it; before any other call, or one on another
-    stream, ``update`` does."""
+    their stream before they read it; before the other calls ``update`` has to.
+    There is one device copy: streams that share an edited table are ordered by
+    the caller."""
 
     def __init__(self, reqs: Sequence[Request], device="cuda"):
         self.host = (Request * max(1, len(reqs)))(*reqs)

@@ -405,3 +405,42 @@ def test_one_long_generation_among_many_requests():
     q = [1 + (i % 7 == 0) * (i % 40) for i in range(n)]
     q[333] = 2000
     check(Attend(AttendCase(lens=[[3] if i % 3 else [] for i in range(n)], n_query=q, k=[0] * n, heads=(2, 1, 64))))
+
+
+def test_more_segments_than_a_launch_takes():
+    """515 chunks of 132 segments each: past the 65535 that a launch counts.
+    Every page of every chunk is the same one, so the sum over its keys counts
+    n times.  Fp32 sums: 1024 keys an item, then the items one by one."""
+    Hq, d, bs, pages, per_req, n_req = 8, 64, 1024, 132, 103, 5
+    g = torch.Generator().manual_seed(2)
+    mk = lambda *s: torch.randn(*s, generator=g).bfloat16().cuda()  # noqa: E731
+    K, V = mk(1, bs, 1, d), mk(1, bs, 1, d)
+    Q, Ks, Vs = 1.5 * mk(n_req, Hq, d), mk(n_req, 1, d), mk(n_req, 1, d)
+    table = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    n_ctx = per_req * pages * bs
+    reqs = fk.RequestTable([fk.Request(i * (n_ctx + 1), 0, 0, i, n_ctx, 1, 0, 0) for i in range(n_req)])
+    entries = []
+    for c in range(n_req * per_req):
+        e = fk.Chunk()
+        e.k, e.v, e.block_table = K.data_ptr(), V.data_ptr(), table.data_ptr()
+        e.dst_row, e.pos, e.len = c // per_req * (n_ctx + 1) + c % per_req * pages * bs, 0, pages * bs
+        entries.append(e)
+    chunks = fk.ChunkTable(entries, fk.FUSE_KV_PAGED, fk.FUSE_BF16, block_size=bs, n_pool_blocks=1, keep=[K, V, table])
+    desc = fk.layer_desc(64, Hq, 1, d, 1e6, fk.FUSE_BF16)
+    ws, O = fk.alloc_attend_workspace(desc, chunks, reqs, 1), torch.zeros_like(Q)
+    assert (ws.numel() - 256) // (8 * (8 + 4 * d)) == n_req * per_req * pages
+    fk.attend_chunks(desc, chunks, reqs, 1, Q, None, Ks, Vs, O, ws)
+    fk.check_errors(ws)
+    k, v, n = f64(K)[0, :, 0], f64(V)[0, :, 0], per_req * pages
+    for r in range(n_req):
+        for h in range(Hq):
+            q = f64(Q)[r, h] / np.sqrt(d)
+            s, s1 = k @ q, f64(Ks)[r, 0] @ q
+            m = max(s.max(), s1)
+            w, w1 = n * np.exp(s - m), np.exp(s1 - m)
+            l = w.sum() + w1
+            want, A = (w @ v + w1 * f64(Vs)[r, 0]) / l, (w @ np.abs(v) + w1 * np.abs(f64(Vs)[r, 0])) / l
+            S = max((np.abs(k) @ np.abs(q)).max(), np.abs(f64(Ks)[r, 0]) @ np.abs(q))
+            e = S * ((d + 16) * 2.0 ** -23 + 2.0 ** -20)
+            tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2 * e + (bs + n) * 2.0 ** -24) * A
+            assert (np.abs(f64(O)[r, h] - want) <= tol).all(), (r, h)
