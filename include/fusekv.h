@@ -583,6 +583,169 @@ fuse_status_t fuse_pages_copy(const fuse_layer_desc_t* desc, const fuse_pools_t*
                               const int32_t* moves, int32_t max_moves, void* ws, size_t ws_bytes,
                               fuse_stream_t stream);
 
+/* ---------------------------------------------------------------------- */
+/* A speculative step over a paged cache: rotate new rows and write them to
+ * their pages, attend a tree of drafted tokens, verify the drafts, keep the
+ * accepted ones.                                                           */
+
+/* Sequences held in pages, their lengths and tables on the device (written by
+ * fuse_cache_keep, or by the caller): nothing of a step needs the host.
+ * Sequence s holds lens[s] tokens in the pages tables[s][0 ..]: token t in row
+ * t % block_size of page tables[s][t / block_size].  A call brings it the rows
+ * rows[s] .. rows[s + 1] - 1 of its row tensors (none is fine), its new tokens
+ * 0, 1, ..; new token i belongs in slot lens[s] + i.  A contiguous cache is
+ * one of large pages.  Rows in front of rows[0] and from rows[n_seq] on are
+ * neither read nor written.
+ * Trees.  parents [n_rows] int32 (device) gives each new token the number,
+ * within its sequence, of the one that it follows: a smaller one, or -1 for
+ * what follows the held tokens.  NULL: each follows the one before it.
+ * A sequence whose row starts descend or pass n_rows, that has more than
+ * max_new rows, whose length is negative, or whose slots pass the table's row
+ * is recorded as FUSE_ERR_DEVICE_BOUNDS and left out.  A parent out of range is
+ * recorded and read as -1. */
+typedef struct {
+  int32_t n_seq;
+  int32_t block_size;      /* tokens per page (> 0)                              */
+  int32_t max_blocks;      /* entries of a table row (> 0)                       */
+  int32_t max_new;         /* rows of a sequence in a call, at most (> 0)        */
+  int64_t n_pool_blocks;   /* pages of the pool                                  */
+  const int32_t* tables;   /* device [n_seq, max_blocks]                         */
+  int32_t* lens;           /* device [n_seq]                                     */
+  const int32_t* rows;     /* device [n_seq + 1], ascending                      */
+} fuse_seqs_t;
+
+#define FUSE_TREE_MAX_NEW 64   /* new tokens of a sequence in a tree */
+
+/* Workspace of the calls below that say so: its header only. */
+#define FUSE_CACHE_WORKSPACE 256
+
+/* Rotary positions of fuse_cache_append.  The first rot_dim channels of a head
+ * are rotated (0: all; a multiple of 16), in pairs m = 0 .. rot_dim / 2 - 1:
+ *   FUSE_ROPE_HALF         channels m and m + rot_dim / 2
+ *   FUSE_ROPE_INTERLEAVED  channels 2m and 2m + 1
+ * by position * theta'_m; the rest is copied.  With theta_m = rope_base^(-2m / rot_dim):
+ *   FUSE_ROPE_PLAIN   theta' = theta
+ *   FUSE_ROPE_LINEAR  theta' = theta / factor
+ *   FUSE_ROPE_LLAMA3  theta' = (1 - c) theta / factor + c theta, with
+ *                     c = clamp((original_len theta / 2 pi - low) / (high - low), 0, 1)
+ *   FUSE_ROPE_YARN    theta' = (1 - r) theta + r theta / factor, with
+ *                     r = clamp((m - a) / max(b - a, 0.001), 0, 1),
+ *                     a = max(0, floor(t(high))), b = min(rot_dim - 1, ceil(t(low))),
+ *                     t(x) = rot_dim ln(original_len / (2 pi x)) / (2 ln rope_base)
+ * mscale (1 without one) multiplies the rotated channels.  Angles are reduced
+ * exactly (64-bit fractions of a turn), whatever the position. */
+typedef enum { FUSE_ROPE_HALF = 0, FUSE_ROPE_INTERLEAVED = 1 } fuse_rope_layout_t;
+typedef enum {
+  FUSE_ROPE_PLAIN = 0,
+  FUSE_ROPE_LINEAR = 1,
+  FUSE_ROPE_LLAMA3 = 2,
+  FUSE_ROPE_YARN = 3
+} fuse_rope_scaling_t;
+typedef struct {
+  int32_t layout;          /* fuse_rope_layout_t  */
+  int32_t rot_dim;
+  int32_t scaling;         /* fuse_rope_scaling_t */
+  int32_t original_len;
+  double factor;           /* >= 1 (LINEAR, LLAMA3, YARN) */
+  double low, high;        /* 0 < low < high (LLAMA3, YARN) */
+  double mscale;           /* > 0 */
+} fuse_rope_t;
+
+/* The rows of fuse_cache_append, in desc->dtype.  Q, K and V may be parts of
+ * wider rows (one fused projection): row i starts stride * i elements on, its
+ * heads are contiguous.  Strides are multiples of 16 bytes. */
+typedef struct {
+  const void* Q;           /* [n_rows, Hq, d]; NULL: none                        */
+  const void* K;           /* [n_rows, Hkv, d]                                   */
+  const void* V;           /* [n_rows, Hkv, d]                                   */
+  int64_t q_stride, k_stride, v_stride;
+  void* Qr;                /* [n_rows, Hq, d] rotated, contiguous (Q's memory if
+                              Q is contiguous); NULL with Q NULL                 */
+  void* Kr;                /* [n_rows, Hkv, d] the same for K; may be NULL       */
+  void* k_pool;            /* [n_pool_blocks, block_size, Hkv, d]                */
+  void* v_pool;
+} fuse_append_t;
+
+/* Rotate the new rows ([KVBoost] Eq. 3) and write them to their pages: row i of
+ * sequence s has position lens[s] + depth(i), depth the number of its ancestors
+ * among the new tokens, and goes to slot lens[s] + i:
+ *   Qr = R^pos Q,  k_pool[slot] = R^pos K (also Kr),  v_pool[slot] = V.
+ * lens is not changed: fuse_cache_keep (or the caller) raises it.  Rounded once,
+ * to desc->dtype; parts that are not rotated are copied bit for bit.  A page
+ * outside the pool is recorded as FUSE_ERR_DEVICE_BOUNDS and not written.
+ * With parents, max_new is at most FUSE_TREE_MAX_NEW.  Outputs may not overlap
+ * inputs, Qr and Kr in place aside.  ws: FUSE_CACHE_WORKSPACE bytes. */
+fuse_status_t fuse_cache_append(const fuse_layer_desc_t* desc, const fuse_rope_t* rope,
+                                const fuse_seqs_t* seqs, int64_t n_rows, const int32_t* parents,
+                                const fuse_append_t* io, void* ws, size_t ws_bytes,
+                                fuse_stream_t stream);
+
+/* Attention of the new tokens of every sequence, already in their pages, over
+ * the held tokens and, of the new ones, themselves and their ancestors:
+ *   O[i, h] = softmax_k(Q[i, h] . k[h/g] / sqrt(d)) v[h/g]
+ * over the slots 0 .. lens[s] - 1 and lens[s] + j for j = i and its ancestors.
+ * Q (rotated), O: [n_rows, Hq, d]; max_new <= FUSE_TREE_MAX_NEW; one new token
+ * a sequence is the ordinary next-token attention of a paged cache, parents
+ * NULL a causal run.  Softmax statistics and sums are fp32; in bf16 layers the
+ * weights are rounded to bf16 where they meet the values (their sum is that of
+ * the unrounded ones).  What a row does not see does not reach it, infinities
+ * and NaN included (rows behind a sequence's last slot among it); a key of
+ * score -infinity has no weight.  The slots of a page outside the pool are
+ * recorded as FUSE_ERR_DEVICE_BOUNDS and count as not there.  No atomics on
+ * sums: equal inputs give equal outputs.  O may not overlap an input.
+ * The workspace (of fuse_tree_workspace_size, which depends on the shapes and
+ * n_seq only, not on lengths) follows the convention of fuse_workspace_size. */
+fuse_status_t fuse_tree_workspace_size(const fuse_layer_desc_t* desc, const fuse_seqs_t* seqs,
+                                       size_t* bytes);
+fuse_status_t fuse_attend_tree(const fuse_layer_desc_t* desc, const fuse_seqs_t* seqs,
+                               int64_t n_rows, const int32_t* parents, const void* Q,
+                               const void* k_pool, const void* v_pool, void* O, void* ws,
+                               size_t ws_bytes, fuse_stream_t stream);
+
+/* Verify drafted tokens against the target's probabilities, with given random
+ * numbers.  Sequence s has the nodes rows[s] .. rows[s + 1] - 1: node 0, the
+ * last token that stands, and drafts below it (parents; node 0's is -1).
+ *   P   [n_rows, vocab] fp32, row i: the target's distribution after node i
+ *   Qd  [n_rows, vocab] fp32, row i: the distribution that node i's children
+ *       were drawn from, independently; NULL: drafts were chosen, not drawn
+ *   u   [n_rows] in [0, 1): of node i's own acceptance; u_next [n_seq]
+ * The walk starts at node 0 with r = P[0], S = 1.  The children c of the node
+ * where it stands, in order, with token x = tokens[c]: if r(x) > 0 and
+ *   u_c S Qd(x) < r(x)        (Qd NULL: u_c S < r(x))
+ * it goes on to c, with r = P[c] and S = 1; else
+ *   r = max(r - S Qd, 0), S = sum r   (Qd NULL: S = S - r(x), then r(x) = 0).
+ * After the last child, next = the lowest x with r(0) + .. + r(x) > u_next sum r
+ * (r = P of the node where nothing of r is left).  Kept tokens and the next one
+ * are then distributed as the target's, whatever the drafts.
+ *   path [n_seq, max_path]  the nodes walked, node 0 first, then -1
+ *   count [n_seq]           their number (0 without rows, next then -1)
+ *   next [n_seq]
+ * 1 <= max_path <= FUSE_TREE_MAX_NEW; a sequence with more rows is recorded as
+ * FUSE_ERR_DEVICE_BOUNDS and treated as one without.  Rows of P and Qd are
+ * p_stride and q_stride elements apart.  Sums keep about 48 bits.  Entries that
+ * are negative, infinite or NaN count as 0; they, tokens outside the vocabulary
+ * and parents out of range (never accepted) are recorded where they are read.
+ * u below 0, above the last float before 1 or NaN: as 0, that float, 0 for
+ * u_next; NaN in u accepts nothing.  ws: FUSE_CACHE_WORKSPACE bytes. */
+fuse_status_t fuse_verify_tree(int32_t n_seq, int64_t n_rows, int32_t vocab, const int32_t* rows,
+                               const int32_t* parents, const int32_t* tokens, const float* P,
+                               int64_t p_stride, const float* Qd, int64_t q_stride, const float* u,
+                               const float* u_next, int32_t max_path, int32_t* path,
+                               int32_t* count, int32_t* next, void* ws, size_t ws_bytes,
+                               fuse_stream_t stream);
+
+/* Keep the rows of a path in every pool and drop the other new ones: for i <
+ * count[s], slot lens[s] + i receives what slot lens[s] + path[s][i] held, and
+ * then lens[s] += count[s].  pools: F32 or BF16, as fuse_pages_copy's; seqs:
+ * as the rows were appended.  A path that does not ascend or names a row that
+ * the sequence does not have, or a count outside [0, max_path], is recorded as
+ * FUSE_ERR_DEVICE_BOUNDS and leaves the sequence as it is; so does a page
+ * outside the pool.  ws: FUSE_CACHE_WORKSPACE bytes. */
+fuse_status_t fuse_cache_keep(const fuse_layer_desc_t* desc, const fuse_pools_t* pools,
+                              const fuse_seqs_t* seqs, const int32_t* path, int32_t max_path,
+                              const int32_t* count, void* ws, size_t ws_bytes,
+                              fuse_stream_t stream);
+
 /* Synchronise the stream, read the workspace's error word, clear it, and
  * return it (FUSE_OK if no device-side error was recorded).  If detail is
  * not NULL it receives a code locating the failed check. */

@@ -1,0 +1,333 @@
+// Attention of trees of new tokens over a paged cache: the entry points, the
+// CUDA-core kernel and the kernel that joins the workers' parts.
+//
+// Every new token sees all held tokens and, of the new ones, itself and its
+// ancestors, 64 bits of a row's own.  Held and new tokens lie in the same
+// pages, so a unit's keys are one list with the mask at its end.
+#include <algorithm>
+#include <cmath>
+
+#include "attend_tree.h"
+#include "checks.h"
+#include "launch.h"
+#include "trace.h"
+
+namespace fusekv {
+
+namespace {
+
+constexpr int kWarps = 4;                 // workers of a CTA
+constexpr int kVecs = 8;                  // query vectors of a unit
+constexpr int kTile = 32;                 // keys of a tile: one a lane
+constexpr int kAtOnce = 8;                // keys whose values it reads at a time
+
+template <typename T> __device__ __forceinline__ float to_f(T x);
+template <> __device__ __forceinline__ float to_f(float x) { return x; }
+template <> __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T> __device__ __forceinline__ T from_f(float x);
+template <> __device__ __forceinline__ float from_f(float x) { return x; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __float2bfloat16_rn(x); }
+
+// A warp's units, 32 keys at a time: a lane per key for the scores, then a lane
+// per D / 32 channels for the sums.
+template <typename T, int D>
+__global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const __grid_constant__ TreeArgs a) {
+  constexpr int EL = D / 32;
+  __shared__ float s_q[kWarps][kVecs][D];
+  __shared__ float s_p[kWarps][32][kVecs];
+  __shared__ int64_t s_warp[kWarps];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  pdl_wait();
+  pdl_trigger();
+  const int64_t total = count_tiles<kWarps * 32>(a, s_warp);
+  const int64_t per = per_worker(a, total);
+  const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
+  const int64_t begin = w * per, end = min(total, begin + per);
+  if (begin >= end) return;
+  TreeAt at = find_tile(a, begin);
+  int64_t t = begin;
+  while (t < end) {
+    const int nt = tiles_of(a, at.q), groups = units_of(a, at.q) / a.n_kv_heads;
+    const int64_t seq_end = at.first + (int64_t)a.n_kv_heads * groups * nt;
+    if (t >= seq_end) {                   // the next sequence
+      at.first = seq_end;
+      if (++at.s >= a.seq.n_seq) break;
+      seq_of(a.seq, at.s, &at.q);
+      continue;
+    }
+    const int unit = (int)((t - at.first) / nt), h = unit / groups, vg = unit % groups;
+    const int64_t u0 = at.first + (int64_t)unit * nt;
+    const int64_t stop = min(end, u0 + nt);
+    const int n_vec = min(kVecs, at.q.n * a.g - vg * kVecs);
+    uint64_t seen[kVecs];
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+      const int vi = vg * kVecs + min(v, n_vec - 1), i = vi / a.g;
+      seen[v] = seen_by(a.parents, at.q, i, a.seq.err);
+      const T* q = reinterpret_cast<const T*>(a.Q) +
+                   ((int64_t)(at.q.row0 + i) * a.n_q_heads + h * a.g + vi % a.g) * D;
+      for (int e = lane; e < D; e += 32) s_q[warp][v][e] = to_f(q[e]) * a.scale;
+    }
+    __syncwarp();
+    float m[kVecs], l[kVecs], acc[kVecs][EL];
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+      m[v] = -INFINITY;
+      l[v] = 0.f;
+#pragma unroll
+      for (int e = 0; e < EL; ++e) acc[v][e] = 0.f;
+    }
+    const int64_t u_first = t;
+    for (; t < stop; ++t) {
+      const int key = (int)(t - u0) * kTile + lane;
+      int64_t row = -1;
+      if (key < at.q.len + at.q.n) row = pool_row(a.seq, at.s, key);
+      const int rel = key - at.q.len;     // of a new token
+      const T* kr = reinterpret_cast<const T*>(a.k_pool) + (row * a.n_kv_heads + h) * D;
+      float s[kVecs];
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v) s[v] = 0.f;
+      if (row >= 0) {
+#pragma unroll 4
+        for (int e = 0; e < D; e += 8) {
+          float x[8];
+          Vec8<T>::load(kr + e, x);
+#pragma unroll
+          for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[v] = fmaf(s_q[warp][v][e + i], x[i], s[v]);
+        }
+      }
+      uint32_t any = 0;                   // bit v: some vector sees this key
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v) {
+        const bool ok = row >= 0 && (rel < 0 || (seen[v] >> rel & 1));
+        if (!ok) s[v] = -INFINITY;
+        float mt = s[v];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+        const float mn = fmaxf(m[v], mt);
+        const float ref = mn == -INFINITY ? 0.f : mn;
+        const float al = exp2f(m[v] - ref), p = ok ? exp2f(s[v] - ref) : 0.f;
+        m[v] = mn;
+        l[v] = l[v] * al + p;
+        s_p[warp][lane][v] = p;
+        any |= (uint32_t)ok << v;
+#pragma unroll
+        for (int e = 0; e < EL; ++e) acc[v][e] *= al;
+      }
+      __syncwarp();
+      const int64_t mine = any ? row : -1;
+      for (int i = 0; i < 32; i += kAtOnce) {
+        float x[kAtOnce][EL];
+        uint32_t who[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+          const int64_t ri = __shfl_sync(0xffffffffu, mine, i + j);
+          who[j] = __shfl_sync(0xffffffffu, any, i + j);
+#pragma unroll
+          for (int e = 0; e < EL; ++e) x[j][e] = 0.f;
+          if (ri >= 0) {
+            const T* vr = reinterpret_cast<const T*>(a.v_pool) + (ri * a.n_kv_heads + h) * D + lane * EL;
+#pragma unroll
+            for (int e = 0; e < EL; ++e) x[j][e] = to_f(vr[e]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j)
+#pragma unroll
+          for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+            for (int e = 0; e < EL; ++e) {
+              // 0 * V is not 0 for an infinite or NaN V
+              const float xv = who[j] >> v & 1 ? x[j][e] : 0.f;
+              acc[v][e] = fmaf(s_p[warp][i + j][v], xv, acc[v][e]);
+            }
+      }
+      __syncwarp();
+    }
+    const bool whole = u_first == u0 && stop == u0 + nt;
+    const int64_t slot = (w * 2 + (u_first == u0 ? 1 : 0)) * kVecs;
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l[v] += __shfl_xor_sync(0xffffffffu, l[v], o);
+      const int vi = vg * kVecs + v;
+      if (v >= n_vec) continue;
+      if (whole) {
+        T* out = reinterpret_cast<T*>(a.O) +
+                 ((int64_t)(at.q.row0 + vi / a.g) * a.n_q_heads + h * a.g + vi % a.g) * D + lane * EL;
+#pragma unroll
+        for (int e = 0; e < EL; ++e) out[e] = from_f<T>(acc[v][e] / l[v]);
+      } else {
+        if (lane == 0) a.part_ml[slot + v] = make_float2(m[v], l[v]);
+#pragma unroll
+        for (int e = 0; e < EL; ++e) a.part_o[(slot + v) * D + lane * EL + e] = acc[v][e];
+      }
+    }
+    __syncwarp();
+  }
+}
+
+// Joins the parts of one new token's query heads of one KV head (blockIdx.y).
+// A part's row is read by D / 4 lanes.
+constexpr int kJoinThreads = 256;
+
+template <typename T> __device__ __forceinline__ void store4(T* p, float4 v);
+template <> __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+template <> __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeArgs a) {
+  constexpr int L = D / 4, kGroups = kJoinThreads / L;     // lanes of a row, rows at a time
+  __shared__ float4 s_o[kGroups][L];
+  __shared__ float s_l[kGroups];
+  pdl_trigger();
+  pdl_wait();
+  const int row = blockIdx.x, h = blockIdx.y;
+  const int s = seq_of_row(a.seq.rows, a.seq.n_seq, row);
+  if (s < 0 || s >= a.seq.n_seq) return;
+  Seq q;
+  if (!seq_of(a.seq, s, &q) || row < q.row0 || row >= q.row0 + q.n) return;
+  const int64_t total = a.start[a.seq.n_seq], per = per_worker(a, total);
+  const int nt = tiles_of(a, q), groups = units_of(a, q) / a.n_kv_heads;
+  const int lane = threadIdx.x % L, grp = threadIdx.x / L;
+  for (int j = 0; j < a.g; ++j) {
+    const int vi = (row - q.row0) * a.g + j, vg = vi / a.vecs, v = vi % a.vecs;
+    const int64_t u0 = a.start[s] + (int64_t)(h * groups + vg) * nt;
+    const int64_t c0 = u0 / per, c1 = min((u0 + nt - 1) / per, (int64_t)a.workers - 1);
+    if (c0 == c1) continue;               // written by its one worker
+    auto slot = [&](int64_t c) { return (c * 2 + (c == c0 ? 1 : 0)) * a.vecs + v; };
+    float M = -INFINITY;
+    for (int64_t c = c0; c <= c1; ++c) M = fmaxf(M, a.part_ml[slot(c)].x);
+    const float ref = M == -INFINITY ? 0.f : M;
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int64_t c = c0 + grp; c <= c1; c += kGroups) {
+      const float2 ml = a.part_ml[slot(c)];
+      if (ml.x == -INFINITY && ml.y == 0.f) continue;      // saw no key
+      const float w = exp2f(ml.x - ref);
+      const float4 x = *reinterpret_cast<const float4*>(a.part_o + slot(c) * D + lane * 4);
+      l = fmaf(w, ml.y, l);
+      o.x = fmaf(w, x.x, o.x);
+      o.y = fmaf(w, x.y, o.y);
+      o.z = fmaf(w, x.z, o.z);
+      o.w = fmaf(w, x.w, o.w);
+    }
+    s_o[grp][lane] = o;
+    if (lane == 0) s_l[grp] = l;
+    __syncthreads();
+    if (grp == 0) {
+      for (int k = 1; k < kGroups; ++k) {
+        const float4 x = s_o[k][lane];
+        o.x += x.x;
+        o.y += x.y;
+        o.z += x.z;
+        o.w += x.w;
+        l += s_l[k];
+      }
+      store4(reinterpret_cast<T*>(a.O) + ((int64_t)row * a.n_q_heads + h * a.g + j) * D + lane * 4,
+             make_float4(o.x / l, o.y / l, o.z / l, o.w / l));
+    }
+    __syncthreads();
+  }
+}
+
+template <typename T>
+cudaError_t launch_join(const TreeArgs& a, int d, cudaStream_t s) {
+  const dim3 grid((unsigned)a.seq.n_rows, a.n_kv_heads);
+  return d == 128 ? launch_pdl(tree_join_kernel<T, 128>, grid, dim3(kJoinThreads), 0, s, a)
+                  : launch_pdl(tree_join_kernel<T, 64>, grid, dim3(kJoinThreads), 0, s, a);
+}
+
+// ---- host side ---------------------------------------------------------------
+
+fuse_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? FUSE_OK : FUSE_ERR_CUDA; }
+
+TreePlan plan_tree(const fuse_layer_desc_t& d, int n_seq) {
+  TreePlan P;
+  P.vecs = kVecs;
+  P.tile = kTile;
+  P.workers = 152 * 8 * kWarps;
+  P.start = sizeof(WsHeader);
+  P.part_ml = align_up(P.start + ((size_t)n_seq + 1) * sizeof(int64_t), 256);
+  const size_t rows = (size_t)P.workers * 2 * P.vecs;
+  P.part_o = align_up(P.part_ml + rows * sizeof(float2), 256);
+  P.total = align_up(P.part_o + rows * d.head_dim * sizeof(float), 256);
+  return P;
+}
+
+}  // namespace
+
+cudaError_t launch_tree_simt(const fuse_layer_desc_t& d, const TreeArgs& a, cudaStream_t s) {
+  const dim3 grid(a.workers / kWarps), block(kWarps * 32);
+  if (d.dtype == FUSE_BF16)
+    return d.head_dim == 128 ? launch_pdl(tree_simt_kernel<__nv_bfloat16, 128>, grid, block, 0, s, a)
+                             : launch_pdl(tree_simt_kernel<__nv_bfloat16, 64>, grid, block, 0, s, a);
+  return d.head_dim == 128 ? launch_pdl(tree_simt_kernel<float, 128>, grid, block, 0, s, a)
+                           : launch_pdl(tree_simt_kernel<float, 64>, grid, block, 0, s, a);
+}
+
+}  // namespace fusekv
+
+using namespace fusekv;
+
+extern "C" {
+
+fuse_status_t fuse_tree_workspace_size(const fuse_layer_desc_t* desc, const fuse_seqs_t* seqs,
+                                       size_t* bytes) {
+  if (!bytes) return FUSE_ERR_INVALID_ARG;
+  fuse_status_t st = check_desc(desc);
+  if (st != FUSE_OK) return st;
+  if (!seqs || seqs->n_seq < 0) return FUSE_ERR_INVALID_ARG;
+  if (seqs->n_seq > 65535) return FUSE_ERR_UNSUPPORTED;
+  *bytes = plan_tree(*desc, seqs->n_seq).total;
+  return FUSE_OK;
+}
+
+fuse_status_t fuse_attend_tree(const fuse_layer_desc_t* desc, const fuse_seqs_t* seqs, int64_t n_rows,
+                               const int32_t* parents, const void* Q, const void* k_pool,
+                               const void* v_pool, void* O, void* ws, size_t ws_bytes,
+                               fuse_stream_t stream) {
+  fuse_status_t st = check_desc(desc);
+  if (st != FUSE_OK) return st;
+  TreeArgs a;
+  st = check_seqs(seqs, n_rows, FUSE_TREE_MAX_NEW, &a.seq, ws);
+  if (st != FUSE_OK) return st;
+  if (n_rows > 0 && (!Q || !k_pool || !v_pool || !O)) return FUSE_ERR_INVALID_ARG;
+  if (!aligned16(Q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(O)) return FUSE_ERR_MISALIGNED;
+  if (reinterpret_cast<uintptr_t>(parents) & 3u) return FUSE_ERR_MISALIGNED;
+  if (desc->n_kv_heads > 65535) return FUSE_ERR_UNSUPPORTED;
+  const TreePlan P = plan_tree(*desc, seqs->n_seq);
+  st = check_ws(ws, ws_bytes, P.total);
+  if (st != FUSE_OK) return st;
+  if (n_rows == 0 || seqs->n_seq == 0) return FUSE_OK;
+  auto at = [&](size_t off) { return reinterpret_cast<char*>(ws) + off; };
+  a.parents = parents;
+  a.Q = Q;
+  a.k_pool = k_pool;
+  a.v_pool = v_pool;
+  a.O = O;
+  a.n_q_heads = desc->n_q_heads;
+  a.n_kv_heads = desc->n_kv_heads;
+  a.g = desc->n_q_heads / desc->n_kv_heads;
+  a.g_log2 = a.g == 8 ? 3 : a.g == 4 ? 2 : a.g == 2 ? 1 : 0;
+  a.vecs = P.vecs;
+  a.tile = P.tile;
+  a.workers = P.workers;
+  a.scale = 1.4426950408889634f / std::sqrt((float)desc->head_dim);
+  a.start = reinterpret_cast<int64_t*>(at(P.start));
+  a.part_ml = reinterpret_cast<float2*>(at(P.part_ml));
+  a.part_o = reinterpret_cast<float*>(at(P.part_o));
+  cudaStream_t s = (cudaStream_t)stream;
+  st = cuda_status(traced("attend_tree", s, [&] { return launch_tree_simt(*desc, a, s); }));
+  if (st != FUSE_OK) return st;
+  return cuda_status(traced("attend_tree_join", s, [&] {
+    return desc->dtype == FUSE_BF16 ? launch_join<__nv_bfloat16>(a, desc->head_dim, s)
+                                    : launch_join<float>(a, desc->head_dim, s);
+  }));
+}
+
+}  // extern "C"

@@ -15,6 +15,13 @@ enum CacheErrSite : uint32_t {
   SITE_ATTEND_SEL = 15,      // selected index out of range or order (attend_chunks)
   SITE_PROMPT_TIMEOUT = 16,  // prompt-attention pipeline wait gave up
   SITE_PAGE_COUNT = 17,      // negative reference count
+  SITE_SEQ_ROWS = 18,        // a sequence's rows, length or table row (fuse_seqs_t)
+  SITE_SEQ_PARENT = 19,      // parent out of range
+  SITE_SEQ_PAGE = 20,        // page outside the pool
+  SITE_TREE_TIMEOUT = 21,    // tree-attention pipeline wait gave up
+  SITE_VERIFY_TOKEN = 22,    // drafted token outside the vocabulary
+  SITE_VERIFY_PROB = 23,     // probability negative, infinite or NaN
+  SITE_KEEP_PATH = 24,       // path or count out of range or order
 };
 
 struct ReqInfo {

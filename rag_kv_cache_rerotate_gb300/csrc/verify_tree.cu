@@ -1,0 +1,458 @@
+// Verification of drafted tokens against the target's probabilities
+// (fuse_verify_tree).
+//
+// A draft x drawn from q is kept with probability min(1, r(x) / (S q(x))); after
+// a refusal the target's remainder is max(r - S q, 0), unnormalised, S its sum.
+// As q >= 0, an entry that has reached 0 stays there, so that after k refusals
+//   r = max(p - A q, 0),   A = S_0 + .. + S_(k-1),  S_0 = 1:
+// nothing of the vocabulary's size is stored.  Only a refusal and the draw of
+// the next token pass over a row; what the walk looks at besides (p and q at the
+// drafted tokens) is read for all nodes at once.
+//
+// The next token is the first x whose running sum passes u' S.  A rounding of
+// the sums to fp32 would move that border over several tokens of a large
+// vocabulary, so entries and sums are pairs of floats (48 bits) and sums
+// of sums are fp64.
+//
+// One cluster per sequence, the vocabulary split over its CTAs, their warps'
+// sums exchanged through distributed shared memory.  Latency bounds it: a chain of
+// reads (parents and tokens, probabilities of the drafts, a row, the part of it
+// with the border).
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "cache_seqs.cuh"
+#include "launch.h"
+#include "trace.h"
+
+namespace fusekv {
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kNodes = FUSE_TREE_MAX_NEW;
+constexpr int kAhead = 4;                 // groups of four entries that a thread reads at a time
+
+struct VerifyArgs {
+  const int32_t* rows;
+  const int32_t* parents;
+  const int32_t* tokens;
+  const float* P;
+  const float* Q;                         // null: drafts that were not drawn
+  const float* u;
+  const float* u_next;
+  int32_t *path, *count, *next;
+  int64_t p_stride, q_stride, n_rows;
+  int32_t vocab, max_path;
+  uint32_t* err;
+};
+
+// x + y as a pair: s + e exactly.
+__device__ __forceinline__ void two_sum(float x, float y, float& s, float& e) {
+  s = x + y;
+  const float b = s - x;
+  e = (x - (s - b)) + (y - b);
+}
+
+// max(p - A q, 0) as a pair of floats, A = ah + al.
+__device__ __forceinline__ void remainder_of(float p, float q, float ah, float al, float& hi, float& lo) {
+  const float m = ah * q;
+  const float me = fmaf(ah, q, -m);
+  float s, e;
+  two_sum(p, -m, s, e);
+  e = (e - me) - al * q;
+  const bool pos = s + e > 0.f;
+  hi = pos ? s : 0.f;
+  lo = pos ? e : 0.f;
+}
+
+// A row's entries [4 i - lead, 4 i - lead + 4), those outside the row as 0.  The rows of a
+// large vocabulary need not be aligned: `lead` entries are missing in front of a
+// row's first aligned group of four.  wide: whole groups are read at once.
+__device__ __forceinline__ float4 read4(const float* row, int lead, bool wide, int i, int vocab) {
+  const int e = 4 * i - lead;
+  if (wide && e >= 0 && e + 4 <= vocab) return __ldg(reinterpret_cast<const float4*>(row + e));
+  float4 x;
+  x.x = e >= 0 && e < vocab ? __ldg(row + e) : 0.f;
+  x.y = e + 1 >= 0 && e + 1 < vocab ? __ldg(row + e + 1) : 0.f;
+  x.z = e + 2 >= 0 && e + 2 < vocab ? __ldg(row + e + 2) : 0.f;
+  x.w = e + 3 >= 0 && e + 3 < vocab ? __ldg(row + e + 3) : 0.f;
+  return x;
+}
+
+__device__ __forceinline__ float usable(float x, bool& bad) {
+  const bool ok = x >= 0.f && x <= 3.402823466e38f;
+  bad |= !ok;
+  return ok ? x : 0.f;
+}
+
+// What a pass over a row forms its entries from.
+struct Pass {
+  const float* p;
+  const float* q;                         // null: p alone
+  float ah, al;
+  int lead;
+  bool wide;
+  int n_gone;                             // refused tokens whose entry is 0 (without q)
+};
+
+__device__ __forceinline__ void entries(const Pass& y, const float4& pv, const float4& qv, int i,
+                                        const int* s_gone, bool& bad, float (&hi)[4], float (&lo)[4]) {
+  const float p[4] = {pv.x, pv.y, pv.z, pv.w}, q[4] = {qv.x, qv.y, qv.z, qv.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    hi[k] = usable(p[k], bad);
+    lo[k] = 0.f;
+    if (y.q) remainder_of(hi[k], usable(q[k], bad), y.ah, y.al, hi[k], lo[k]);
+  }
+  for (int g = 0; g < y.n_gone; ++g) {
+    const int at = s_gone[g] - (4 * i - y.lead);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (at == k) hi[k] = 0.f;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant__ VerifyArgs a) {
+  cg::cluster_group cl = cg::this_cluster();
+  const int n_ctas = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  const int s = blockIdx.x / n_ctas;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  __shared__ double s_sum[2][kWarps];     // this CTA's warps' sums, by the pass's parity
+  __shared__ double s_all[kMaxCluster * kWarps];
+  __shared__ double s_scan[kWarps];
+  __shared__ int s_parent[kNodes], s_token[kNodes], s_gone[kNodes], s_path[kNodes];
+  __shared__ float s_p[kNodes], s_q[kNodes], s_u[kNodes];
+  __shared__ int s_found[2];
+  pdl_wait();
+  pdl_trigger();
+  const int r0 = a.rows[s], r1 = a.rows[s + 1];
+  const float un = a.u_next[s];
+  int n = (int)((uint32_t)r1 - (uint32_t)r0);
+  if (r0 < 0 || r1 < r0 || r1 > a.n_rows || n > a.max_path) {
+    if (tid == 0) report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_SEQ_ROWS, (uint32_t)s);
+    n = 0;
+  }
+  // every node's parent, token and probabilities at its parent
+  if (tid < n) {
+    const int row = r0 + tid;
+    int par = a.parents[row], tok = a.tokens[row];
+    float p = 0.f, q = 0.f;
+    bool bad = false;
+    if (tid > 0) {
+      if (par < 0 || par >= tid) {
+        report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_SEQ_PARENT, (uint32_t)row);
+        par = -1;                         // no node's child
+      } else if (tok < 0 || tok >= a.vocab) {
+        report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_VERIFY_TOKEN, (uint32_t)row);
+        par = -1;
+      } else {
+        p = usable(a.P[(int64_t)(r0 + par) * a.p_stride + tok], bad);
+        if (a.Q) q = usable(a.Q[(int64_t)(r0 + par) * a.q_stride + tok], bad);
+      }
+    }
+    if (bad) report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_VERIFY_PROB, (uint32_t)row);
+    s_parent[tid] = par;
+    s_token[tid] = tok;
+    s_p[tid] = p;
+    s_q[tid] = q;
+    s_u[tid] = a.u[row];
+  }
+  __syncthreads();
+  const int W = n_ctas * kWarps;
+  Pass y;
+  y.q = nullptr;
+  y.ah = y.al = 0.f;
+  y.n_gone = 0;
+  int groups = 0, seg = 0;                // groups of four of a row, and of a warp's part
+  int parity = 0;
+  // the remainder's sums: every warp's of the cluster in s_all; returns their total
+  auto pass = [&](int node, double A) -> double {
+    y.p = a.P + (int64_t)(r0 + node) * a.p_stride;
+    y.q = A > 0.0 ? a.Q + (int64_t)(r0 + node) * a.q_stride : nullptr;
+    y.ah = (float)A;
+    y.al = (float)(A - (double)y.ah);
+    y.lead = (int)((reinterpret_cast<uintptr_t>(y.p) >> 2) & 3u);
+    y.wide = !y.q || (int)((reinterpret_cast<uintptr_t>(y.q) >> 2) & 3u) == y.lead;
+    groups = (a.vocab + y.lead + 3) / 4;
+    seg = (groups + W - 1) / W;
+    const int g0 = (rank * kWarps + warp) * seg, g1 = min(groups, g0 + seg);
+    float sh = 0.f, sl = 0.f;
+    bool bad = false;
+    for (int g = g0 + lane; g < g1; g += 32 * kAhead) {
+      float4 pv[kAhead], qv[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = g + 32 * k;
+        pv[k] = qv[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < g1) {
+          pv[k] = read4(y.p, y.lead, y.wide, i, a.vocab);
+          if (y.q) qv[k] = read4(y.q, y.lead, y.wide, i, a.vocab);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        float hi[4], lo[4];
+        entries(y, pv[k], qv[k], g + 32 * k, s_gone, bad, hi, lo);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float t;
+          two_sum(sh, hi[e], sh, t);
+          sl += t + lo[e];
+        }
+      }
+    }
+    double t = (double)sh + (double)sl;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if (lane == 0) s_sum[parity][warp] = t;
+    if (bad) report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_VERIFY_PROB, (uint32_t)(r0 + node));
+    cl.sync();
+    if (tid < W) s_all[tid] = *cl.map_shared_rank(&s_sum[parity][tid % kWarps], tid / kWarps);
+    __syncthreads();
+    parity ^= 1;
+    double all = 0.0;
+#pragma unroll
+    for (int k = 0; k < kMaxCluster * kWarps / 32; ++k)
+      if (lane + 32 * k < W) all += s_all[lane + 32 * k];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    return all;
+  };
+
+  // the walk, the same in every thread of the cluster
+  int cur = 0, kept = n > 0 ? 1 : 0;
+  double A = 0.0, S = 1.0;
+  bool summed = false;                    // s_all holds the sums of the remainder as it stands
+  if (tid == 0) s_path[0] = 0;
+  for (int i = 1; i < n; ++i) {
+    if (s_parent[i] != cur) continue;     // uniform
+    const int x = s_token[i];
+    const double p = s_p[i], u = s_u[i];
+    double r = p;
+    bool yes;
+    if (a.Q) {
+      const double q = s_q[i];
+      r = fmax(p - A * q, 0.0);
+      yes = r > 0.0 && u * S * q < r;
+    } else {
+      for (int g = 0; g < y.n_gone; ++g)
+        if (s_gone[g] == x) r = 0.0;
+      yes = r > 0.0 && u * S < r;
+    }
+    if (yes) {
+      cur = i;
+      if (tid == 0) s_path[kept] = i;
+      ++kept;
+      A = 0.0;
+      S = 1.0;
+      __syncthreads();                    // s_gone is read above
+      y.n_gone = 0;
+      summed = false;
+    } else if (a.Q) {
+      A += S;
+      S = pass(cur, A);
+      summed = true;
+    } else {
+      S -= r;
+      __syncthreads();
+      if (tid == 0) s_gone[y.n_gone] = x;
+      ++y.n_gone;
+      __syncthreads();
+    }
+  }
+  int token = -1;
+  if (n > 0) {
+    double sum = summed ? S : pass(cur, A);
+    if (!(sum > 0.0)) {                   // nothing left: the target's own row
+      y.n_gone = 0;
+      sum = pass(cur, 0.0);
+    }
+    // the first warp's part whose running sum passes t
+    const double t = (un > 0.f ? (double)fminf(un, 0.99999994f) : 0.0) * sum;
+    double before = 0.0;
+    int part = -1, last = -1;             // last: the last part that holds anything
+    {
+      constexpr int kEach = kMaxCluster * kWarps / 32;
+      double v[kEach], own = 0.0;
+      int full = -1;
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        const int w = lane * kEach + k;
+        v[k] = w < W ? s_all[w] : 0.0;
+        own += v[k];
+        if (v[k] > 0.0) full = w;
+      }
+      double inc = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double z = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += z;
+      }
+      double c = inc - own;
+      int mine = INT32_MAX;
+      double mine_before = 0.0;
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        if (mine == INT32_MAX && v[k] > 0.0 && c + v[k] > t) {
+          mine = lane * kEach + k;
+          mine_before = c;
+        }
+        c += v[k];
+      }
+      part = (int)__reduce_min_sync(0xffffffffu, (unsigned)mine);
+      last = __reduce_max_sync(0xffffffffu, full);
+      const unsigned who = __ballot_sync(0xffffffffu, mine == part && part != INT32_MAX);
+      if (who) {
+        before = __shfl_sync(0xffffffffu, mine_before, __ffs(who) - 1);
+      } else {
+        part = last;                      // t within the sums' rounding of their total
+        before = INFINITY;                // its last entry
+      }
+    }
+    if (part >= 0 && part / kWarps == rank) {
+      // this CTA looks the part through, four entries a thread
+      if (tid == 0) {
+        s_found[0] = INT32_MAX;
+        s_found[1] = -1;
+      }
+      __syncthreads();
+      const int g0 = part * seg, g1 = min(groups, g0 + seg);
+      for (int b = g0; b < g1; b += kThreads) {
+        const int i = b + tid;
+        float hi[4] = {0.f, 0.f, 0.f, 0.f}, lo[4] = {0.f, 0.f, 0.f, 0.f};
+        bool bad = false;
+        if (i < g1) {
+          const float4 pv = read4(y.p, y.lead, y.wide, i, a.vocab);
+          const float4 qv = y.q ? read4(y.q, y.lead, y.wide, i, a.vocab) : make_float4(0.f, 0.f, 0.f, 0.f);
+          entries(y, pv, qv, i, s_gone, bad, hi, lo);
+        }
+        double v[4], own = 0.0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v[k] = (double)hi[k] + (double)lo[k];
+          own += v[k];
+        }
+        double inc = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const double z = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += z;
+        }
+        if (lane == 31) s_scan[warp] = inc;
+        __syncthreads();
+        double c = before + inc - own, tot = 0.0;
+        for (int w = 0; w < kWarps; ++w) {
+          if (w < warp) c += s_scan[w];
+          tot += s_scan[w];
+        }
+        int first = INT32_MAX, any = -1;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          c += v[k];
+          if (v[k] > 0.0) {
+            any = 4 * i - y.lead + k;
+            if (first == INT32_MAX && c > t && before != INFINITY) first = any;
+          }
+        }
+        if (first != INT32_MAX) atomicMin(&s_found[0], first);
+        if (any >= 0) atomicMax(&s_found[1], any);
+        before += tot;
+        __syncthreads();
+        if (s_found[0] != INT32_MAX) break;
+      }
+      token = s_found[0] != INT32_MAX ? s_found[0] : s_found[1];
+    } else if (part < 0 && rank == 0) {
+      if (tid == 0) report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_VERIFY_PROB, (uint32_t)(r0 + cur));
+    } else {
+      cl.sync();                          // the sums of the last pass are read elsewhere until here
+      return;
+    }
+  } else if (rank != 0) {
+    cl.sync();
+    return;
+  }
+  // by the CTA that found the token, or the first
+  if (tid == 0) {
+    a.next[s] = token;
+    a.count[s] = kept;
+  }
+  for (int i = tid; i < a.max_path; i += kThreads)
+    a.path[(int64_t)s * a.max_path + i] = i < kept ? s_path[i] : -1;
+  cl.sync();
+}
+
+fuse_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? FUSE_OK : FUSE_ERR_CUDA; }
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+}  // namespace
+}  // namespace fusekv
+
+using namespace fusekv;
+
+extern "C" fuse_status_t fuse_verify_tree(int32_t n_seq, int64_t n_rows, int32_t vocab, const int32_t* rows,
+                                          const int32_t* parents, const int32_t* tokens, const float* P,
+                                          int64_t p_stride, const float* Qd, int64_t q_stride,
+                                          const float* u, const float* u_next, int32_t max_path,
+                                          int32_t* path, int32_t* count, int32_t* next, void* ws,
+                                          size_t ws_bytes, fuse_stream_t stream) {
+  if (n_seq < 0 || n_rows < 0 || vocab < 1 || max_path < 1) return FUSE_ERR_INVALID_ARG;
+  if (n_seq > 65535 || n_rows > INT32_MAX || vocab > INT32_MAX / 8 || max_path > FUSE_TREE_MAX_NEW)
+    return FUSE_ERR_UNSUPPORTED;
+  if (n_seq > 0 && (!rows || !u_next || !path || !count || !next)) return FUSE_ERR_INVALID_ARG;
+  if (n_rows > 0 && (!parents || !tokens || !P || !u)) return FUSE_ERR_INVALID_ARG;
+  if (p_stride < vocab || (Qd && q_stride < vocab)) return FUSE_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)rows, (const void*)parents, (const void*)tokens, (const void*)P,
+                        (const void*)Qd, (const void*)u, (const void*)u_next, (const void*)path,
+                        (const void*)count, (const void*)next})
+    if (!aligned4(p)) return FUSE_ERR_MISALIGNED;
+  const fuse_status_t st = check_ws(ws, ws_bytes, FUSE_CACHE_WORKSPACE);
+  if (st != FUSE_OK) return st;
+  if (n_seq == 0) return FUSE_OK;
+  VerifyArgs a;
+  a.rows = rows;
+  a.parents = parents;
+  a.tokens = tokens;
+  a.P = P;
+  a.Q = Qd;
+  a.u = u;
+  a.u_next = u_next;
+  a.path = path;
+  a.count = count;
+  a.next = next;
+  a.p_stride = p_stride;
+  a.q_stride = q_stride;
+  a.n_rows = n_rows;
+  a.vocab = vocab;
+  a.max_path = max_path;
+  a.err = reinterpret_cast<uint32_t*>(ws);
+  cudaStream_t s = (cudaStream_t)stream;
+  // as many CTAs a sequence as run at a time
+  int dev = 0, sms = 1;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  int ctas = kMaxCluster;
+  while (ctas > 1 && (int64_t)n_seq * ctas > 4 * (int64_t)sms) ctas /= 2;
+  return cuda_status(traced("verify_tree", s, [&] {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(n_seq * ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, verify_kernel, a);
+  }));
+}

@@ -33,6 +33,11 @@ FUSE_ERR_NO_PAGES = 8
 FUSE_F32, FUSE_BF16, FUSE_U8_ASYM, FUSE_U4_ASYM = 0, 1, 2, 3
 FUSE_KV_CONTIGUOUS, FUSE_KV_PAGED = 0, 1
 FUSE_ROPE_ROTATE_HALF = 0
+# fuse_rope_layout_t, fuse_rope_scaling_t
+FUSE_ROPE_HALF, FUSE_ROPE_INTERLEAVED = 0, 1
+FUSE_ROPE_PLAIN, FUSE_ROPE_LINEAR, FUSE_ROPE_LLAMA3, FUSE_ROPE_YARN = 0, 1, 2, 3
+FUSE_TREE_MAX_NEW = 64
+FUSE_CACHE_WORKSPACE = 256
 
 _c = ctypes
 
@@ -97,6 +102,25 @@ class Pools(_c.Structure):
                 ("reserved", _c.c_int32), ("n_blocks", _c.c_int64), ("h_pools", _c.c_void_p)]
 
 
+class Seqs(_c.Structure):
+    _fields_ = [("n_seq", _c.c_int32), ("block_size", _c.c_int32), ("max_blocks", _c.c_int32),
+                ("max_new", _c.c_int32), ("n_pool_blocks", _c.c_int64), ("tables", _c.c_void_p),
+                ("lens", _c.c_void_p), ("rows", _c.c_void_p)]
+
+
+class Rope(_c.Structure):
+    _fields_ = [("layout", _c.c_int32), ("rot_dim", _c.c_int32), ("scaling", _c.c_int32),
+                ("original_len", _c.c_int32), ("factor", _c.c_double), ("low", _c.c_double),
+                ("high", _c.c_double), ("mscale", _c.c_double)]
+
+
+class Append(_c.Structure):
+    _fields_ = [("Q", _c.c_void_p), ("K", _c.c_void_p), ("V", _c.c_void_p),
+                ("q_stride", _c.c_int64), ("k_stride", _c.c_int64), ("v_stride", _c.c_int64),
+                ("Qr", _c.c_void_p), ("Kr", _c.c_void_p), ("k_pool", _c.c_void_p),
+                ("v_pool", _c.c_void_p)]
+
+
 class Totals(_c.Structure):
     _fields_ = [("n_tok", _c.c_int64), ("n_ctx", _c.c_int64), ("n_sel", _c.c_int64),
                 ("n_out", _c.c_int64), ("max_ctx", _c.c_int32), ("max_tok", _c.c_int32)]
@@ -152,6 +176,13 @@ _SIGS = {
     "fuse_pages_free": (_c.c_int, [_P, _P, _P, _c.c_size_t, _P]),
     "fuse_pages_compact": (_c.c_int, [_P, _P, _P, _c.c_int32, _P, _c.c_size_t, _P]),
     "fuse_pages_copy": (_c.c_int, [_P, _P, _P, _c.c_int32, _P, _c.c_size_t, _P]),
+    "fuse_cache_append": (_c.c_int, [_P, _P, _P, _c.c_int64, _P, _P, _P, _c.c_size_t, _P]),
+    "fuse_tree_workspace_size": (_c.c_int, [_P, _P, _c.POINTER(_c.c_size_t)]),
+    "fuse_attend_tree": (_c.c_int, [_P, _P, _c.c_int64, _P, _P, _P, _P, _P, _P, _c.c_size_t, _P]),
+    "fuse_verify_tree": (_c.c_int, [_c.c_int32, _c.c_int64, _c.c_int32, _P, _P, _P, _P, _c.c_int64,
+                                    _P, _c.c_int64, _P, _P, _c.c_int32, _P, _P, _P, _P,
+                                    _c.c_size_t, _P]),
+    "fuse_cache_keep": (_c.c_int, [_P, _P, _P, _P, _c.c_int32, _P, _P, _c.c_size_t, _P]),
     "fuse_check_errors": (_c.c_int, [_P, _P, _c.POINTER(_c.c_uint32)]),
     "fuse_static_select_count": (_c.c_int, [_P, _P, _c.c_int32, _c.c_int32, _P]),
     "fuse_static_select": (_c.c_int, [_P, _P, _c.c_int32, _c.c_int32, _P, _P]),
@@ -746,6 +777,206 @@ def pages_copy(desc: LayerDesc, pools: PagePools, moves, ws, stream=None):
                                 *_ws(ws, dev), on)
     if st != FUSE_OK:
         raise FuseError(st, "fuse_pages_copy")
+
+
+class Sequences:
+    """Sequences held in pages, their state on the device (``fuse_seqs_t``):
+    ``tables`` [n_seq, max_blocks], ``lens`` [n_seq] and ``rows`` [n_seq + 1]
+    int32.  The tensors are kept and used where they are: ``cache_keep`` raises
+    ``lens``, and the caller may write any of them between calls.  ``max_new``:
+    no sequence brings more rows to a call."""
+
+    def __init__(self, tables: torch.Tensor, lens: torch.Tensor, rows: torch.Tensor, block_size: int,
+                 n_pool_blocks: int, max_new: int):
+        dev = _device()
+        shape = _tensor(tables, "tables", _I32, dev)
+        if len(shape) != 2 or shape[1] < 1:
+            raise ValueError(f"tables: shape {tuple(shape)}, [sequences, pages] is needed")
+        for t, name, n in ((lens, "lens", shape[0]), (rows, "rows", shape[0] + 1)):
+            if tuple(_tensor(t, name, _I32, dev)) != (n,):
+                raise ValueError(f"{name}: shape {tuple(t.shape)}, {(n,)} is needed")
+        self.tables, self.lens, self.rows, self.device = tables, lens, rows, dev
+        self.n, self.block_size, self.n_pool_blocks = shape[0], int(block_size), int(n_pool_blocks)
+        self.c = Seqs(shape[0], self.block_size, shape[1], int(max_new), self.n_pool_blocks,
+                      _ptr(tables), _ptr(lens), _ptr(rows))
+        self.ref = _c.byref(self.c)
+
+    def on(self, dev):
+        """The descriptor, for a call on this device."""
+        if dev != self.device:
+            raise ValueError("seqs: on another device than the current one")
+        return self.ref
+
+
+def rope_desc(layout: int = FUSE_ROPE_HALF, rot_dim: int = 0, scaling: int = FUSE_ROPE_PLAIN,
+              factor: float = 1.0, original_len: int = 0, low: float = 0.0, high: float = 0.0,
+              mscale: float = 1.0) -> Rope:
+    """Rotary positions of ``cache_append`` (``fuse_rope_t``)."""
+    return Rope(int(layout), int(rot_dim), int(scaling), int(original_len), float(factor), float(low),
+                float(high), float(mscale))
+
+
+def alloc_cache_workspace(device="cuda") -> torch.Tensor:
+    """A zeroed workspace for ``cache_append``, ``verify_tree`` and ``cache_keep``."""
+    return torch.zeros(FUSE_CACHE_WORKSPACE, dtype=torch.uint8, device=device)
+
+
+def tree_workspace_size(desc: LayerDesc, seqs: Sequences) -> int:
+    n = _c.c_size_t(0)
+    _check(load().fuse_tree_workspace_size(_c.byref(desc), seqs.ref, _c.byref(n)),
+           "fuse_tree_workspace_size")
+    return int(n.value)
+
+
+def alloc_tree_workspace(desc: LayerDesc, seqs: Sequences, device="cuda") -> torch.Tensor:
+    """A zeroed workspace for ``attend_tree`` (the calls above take it too)."""
+    return torch.zeros(tree_workspace_size(desc, seqs), dtype=torch.uint8, device=device)
+
+
+def _strided(t, name, dtype, dev, rows, heads, dim):
+    """A [rows, heads, dim] tensor's pointer and row stride, its heads contiguous."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.shape == (rows, heads, dim):
+            st = t.stride()
+            if st[2] == 1 and (st[1] == dim or heads == 1):
+                # a single row, or none, may have any stride
+                return t.data_ptr() or None, (st[0] if rows > 1 else heads * dim)
+    except AttributeError:
+        raise ValueError(f"{name}: a tensor is needed") from None
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: {t.dtype}, {dtype} is needed")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, which is not the current CUDA device")
+    if tuple(t.shape) != (rows, heads, dim):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, {(rows, heads, dim)} is needed")
+    raise ValueError(f"{name}: strides {t.stride()}, contiguous heads are needed")
+
+
+def _pool(t, name, dtype, dev, seqs, heads, dim):
+    """A page pool's pointer."""
+    sh = _tensor(t, name, dtype, dev)
+    if sh != (seqs.n_pool_blocks, seqs.block_size, heads, dim):
+        raise ValueError(f"{name}: shape {tuple(sh)}, "
+                         f"{(seqs.n_pool_blocks, seqs.block_size, heads, dim)} is needed")
+    return t.data_ptr() or None
+
+
+def _parents(parents, dev, rows):
+    if parents is None:
+        return None
+    at, n = _list(parents, "parents", dev)
+    if n < rows:
+        raise ValueError(f"parents: {n} entries, {rows} are needed")
+    return at
+
+
+def cache_append(desc: LayerDesc, rope: Rope, seqs: Sequences, parents, Q, K, V, Qr, Kr, k_pool, v_pool,
+                 ws, stream=None):
+    """Rotate the new rows at their positions (KVBoost Eq. 3) and write keys and
+    values to their pages; ``Qr`` (and ``Kr``, if not None) receive the rotated
+    rows.  ``Q``, ``K``, ``V`` may be parts of wider rows; ``Q`` None: keys and
+    values alone; ``parents`` None: each row follows the one before it."""
+    dt = _TORCH_DTYPE.get(desc.dtype)
+    dev, on = _place(stream)
+    Hq, Hkv, d, n = desc.n_q_heads, desc.n_kv_heads, desc.head_dim, K.shape[0]
+    io = Append()
+    if (Q is None) != (Qr is None):
+        raise ValueError("Q and Qr go together")
+    if Q is not None:
+        io.Q, io.q_stride = _strided(Q, "Q", dt, dev, n, Hq, d)
+        io.Qr = _rows(Qr, "Qr", dt, dev, n, Hq, d, True)
+    io.K, io.k_stride = _strided(K, "K", dt, dev, n, Hkv, d)
+    io.V, io.v_stride = _strided(V, "V", dt, dev, n, Hkv, d)
+    if Kr is not None:
+        io.Kr = _rows(Kr, "Kr", dt, dev, n, Hkv, d, True)
+    io.k_pool = _pool(k_pool, "k_pool", dt, dev, seqs, Hkv, d)
+    io.v_pool = _pool(v_pool, "v_pool", dt, dev, seqs, Hkv, d)
+    st = load().fuse_cache_append(_c.byref(desc), _c.byref(rope), seqs.on(dev), n,
+                                  _parents(parents, dev, n), _c.byref(io), *_ws(ws, dev), on)
+    if st != FUSE_OK:
+        raise FuseError(st, "fuse_cache_append")
+
+
+def attend_tree(desc: LayerDesc, seqs: Sequences, parents, Q, k_pool, v_pool, O, ws, stream=None):
+    """Attention of the new tokens of every sequence over the held tokens and
+    their own ancestors, keys and values read from the pages (``cache_append``
+    has written the new tokens').  ``parents`` None: a causal run."""
+    dt = _TORCH_DTYPE.get(desc.dtype)
+    dev, on = _place(stream)
+    Hq, Hkv, d, n = desc.n_q_heads, desc.n_kv_heads, desc.head_dim, Q.shape[0]
+    st = load().fuse_attend_tree(
+        _c.byref(desc), seqs.on(dev), n, _parents(parents, dev, n),
+        _rows(Q, "Q", dt, dev, n, Hq, d, True), _pool(k_pool, "k_pool", dt, dev, seqs, Hkv, d),
+        _pool(v_pool, "v_pool", dt, dev, seqs, Hkv, d), _rows(O, "O", dt, dev, n, Hq, d, True),
+        *_ws(ws, dev), on)
+    if st != FUSE_OK:
+        raise FuseError(st, "fuse_attend_tree")
+
+
+def _probs(t, name, dev, rows, vocab):
+    """A [rows, vocab] fp32 tensor's pointer and row stride."""
+    if t.dtype is not torch.float32:
+        raise ValueError(f"{name}: {t.dtype}, torch.float32 is needed")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, which is not the current CUDA device")
+    if tuple(t.shape) != (rows, vocab) or (vocab > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: shape {tuple(t.shape)} and strides {t.stride()}, rows of {vocab} "
+                         f"entries for {rows} nodes are needed")
+    return t.data_ptr() or None, (t.stride(0) if rows > 1 else vocab)
+
+
+def verify_tree(rows, parents, tokens, P, Qd, u, u_next, path, count, next, ws, stream=None):
+    """Verify drafted tokens against the target's probabilities ``P`` with given
+    random numbers: ``path`` [n_seq, max_path], ``count`` and ``next`` [n_seq]
+    int32 receive the nodes that stand, their number and the token that follows.
+    ``Qd``: the distributions that the drafts were drawn from; None: drafts that
+    were chosen."""
+    dev, on = _place(stream)
+    if P.dim() != 2:
+        raise ValueError(f"P: shape {tuple(P.shape)}, [nodes, vocabulary] is needed")
+    n, vocab = P.shape
+    at, m = _list(rows, "rows", dev)
+    n_seq = m - 1
+    if n_seq < 0:
+        raise ValueError("rows: an entry more than there are sequences is needed")
+
+    def f32(t, name, k):
+        if _tensor(t, name, torch.float32, dev).numel() < k:
+            raise ValueError(f"{name}: {t.numel()} entries, {k} are needed")
+        return t.data_ptr() or None
+
+    def i32(t, name, k):
+        p, have = _list(t, name, dev)
+        if have < k:
+            raise ValueError(f"{name}: {have} entries, {k} are needed")
+        return p
+    way = _tensor(path, "path", _I32, dev)
+    if len(way) != 2 or way[0] != n_seq:
+        raise ValueError(f"path: shape {tuple(way)}, [{n_seq}, nodes] is needed")
+    st = load().fuse_verify_tree(
+        n_seq, n, vocab, at, i32(parents, "parents", n), i32(tokens, "tokens", n),
+        *_probs(P, "P", dev, n, vocab), *(_probs(Qd, "Qd", dev, n, vocab) if Qd is not None else (None, 0)),
+        f32(u, "u", n), f32(u_next, "u_next", n_seq), way[1], path.data_ptr() or None,
+        i32(count, "count", n_seq), i32(next, "next", n_seq), *_ws(ws, dev), on)
+    if st != FUSE_OK:
+        raise FuseError(st, "fuse_verify_tree")
+
+
+def cache_keep(desc: LayerDesc, pools: PagePools, seqs: Sequences, path, count, ws, stream=None):
+    """Keep the rows of every sequence's ``path`` (``count`` of them) in all
+    pools, drop its other new rows and raise ``seqs.lens``."""
+    dev, on = _place(stream)
+    if pools.shape is not None and pools.shape[2:] != (desc.n_kv_heads, desc.head_dim):
+        raise ValueError(f"pools: pages of {pools.shape[2:]}, "
+                         f"{(desc.n_kv_heads, desc.head_dim)} are needed")
+    way = _tensor(path, "path", _I32, dev)
+    at, n = _list(count, "count", dev)
+    if len(way) != 2 or way[0] != seqs.n or n != seqs.n:
+        raise ValueError(f"path, count: shapes {tuple(way)} and {n} for {seqs.n} sequences")
+    st = load().fuse_cache_keep(_c.byref(desc), _c.byref(pools.c), seqs.on(dev), path.data_ptr() or None,
+                                way[1], at, *_ws(ws, dev), on)
+    if st != FUSE_OK:
+        raise FuseError(st, "fuse_cache_keep")
 
 
 def check_errors(ws, stream=None):
