@@ -1,5 +1,5 @@
 // Attention of trees of new tokens over a paged cache: the entry points, the
-// CUDA-core kernel and the kernel that joins the workers' parts.
+// CUDA-core kernel (fp32 layers) and the kernel that joins the workers' parts.
 //
 // Every new token sees all held tokens and, of the new ones, itself and its
 // ancestors, 64 bits of a row's own.  Held and new tokens lie in the same
@@ -21,16 +21,9 @@ constexpr int kVecs = 8;                  // query vectors of a unit
 constexpr int kTile = 32;                 // keys of a tile: one a lane
 constexpr int kAtOnce = 8;                // keys whose values it reads at a time
 
-template <typename T> __device__ __forceinline__ float to_f(T x);
-template <> __device__ __forceinline__ float to_f(float x) { return x; }
-template <> __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <typename T> __device__ __forceinline__ T from_f(float x);
-template <> __device__ __forceinline__ float from_f(float x) { return x; }
-template <> __device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __float2bfloat16_rn(x); }
-
 // A warp's units, 32 keys at a time: a lane per key for the scores, then a lane
 // per D / 32 channels for the sums.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const __grid_constant__ TreeArgs a) {
   constexpr int EL = D / 32;
   __shared__ float s_q[kWarps][kVecs][D];
@@ -44,29 +37,21 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const __grid_con
   const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
   const int64_t begin = w * per, end = min(total, begin + per);
   if (begin >= end) return;
-  TreeAt at = find_tile(a, begin);
-  int64_t t = begin;
-  while (t < end) {
-    const int nt = tiles_of(a, at.q), groups = units_of(a, at.q) / a.n_kv_heads;
-    const int64_t seq_end = at.first + (int64_t)a.n_kv_heads * groups * nt;
-    if (t >= seq_end) {                   // the next sequence
-      at.first = seq_end;
-      if (++at.s >= a.seq.n_seq) break;
-      seq_of(a.seq, at.s, &at.q);
-      continue;
-    }
-    const int unit = (int)((t - at.first) / nt), h = unit / groups, vg = unit % groups;
-    const int64_t u0 = at.first + (int64_t)unit * nt;
-    const int64_t stop = min(end, u0 + nt);
-    const int n_vec = min(kVecs, at.q.n * a.g - vg * kVecs);
+  TreeWalk walk;
+  walk.at = find_tile(a, begin);
+  walk.t = begin;
+  walk.end = end;
+  TreePart at;
+  while (next_part(a, walk, at)) {
+    const int h = at.h, vg = at.vg, n_vec = at.n_vec;
     uint64_t seen[kVecs];
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
       const int vi = vg * kVecs + min(v, n_vec - 1), i = vi / a.g;
       seen[v] = seen_by(a.parents, at.q, i, a.seq.err);
-      const T* q = reinterpret_cast<const T*>(a.Q) +
+      const float* q = reinterpret_cast<const float*>(a.Q) +
                    ((int64_t)(at.q.row0 + i) * a.n_q_heads + h * a.g + vi % a.g) * D;
-      for (int e = lane; e < D; e += 32) s_q[warp][v][e] = to_f(q[e]) * a.scale;
+      for (int e = lane; e < D; e += 32) s_q[warp][v][e] = q[e] * a.scale;
     }
     __syncwarp();
     float m[kVecs], l[kVecs], acc[kVecs][EL];
@@ -77,13 +62,12 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const __grid_con
 #pragma unroll
       for (int e = 0; e < EL; ++e) acc[v][e] = 0.f;
     }
-    const int64_t u_first = t;
-    for (; t < stop; ++t) {
-      const int key = (int)(t - u0) * kTile + lane;
+    for (int j = at.j0; j < at.j1; ++j) {
+      const int key = j * kTile + lane;
       int64_t row = -1;
       if (key < at.q.len + at.q.n) row = pool_row(a.seq, at.s, key);
       const int rel = key - at.q.len;     // of a new token
-      const T* kr = reinterpret_cast<const T*>(a.k_pool) + (row * a.n_kv_heads + h) * D;
+      const float* kr = reinterpret_cast<const float*>(a.k_pool) + (row * a.n_kv_heads + h) * D;
       float s[kVecs];
 #pragma unroll
       for (int v = 0; v < kVecs; ++v) s[v] = 0.f;
@@ -91,7 +75,7 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const __grid_con
 #pragma unroll 4
         for (int e = 0; e < D; e += 8) {
           float x[8];
-          Vec8<T>::load(kr + e, x);
+          Vec8<float>::load(kr + e, x);
 #pragma unroll
           for (int v = 0; v < kVecs; ++v)
 #pragma unroll
@@ -128,9 +112,9 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const __grid_con
 #pragma unroll
           for (int e = 0; e < EL; ++e) x[j][e] = 0.f;
           if (ri >= 0) {
-            const T* vr = reinterpret_cast<const T*>(a.v_pool) + (ri * a.n_kv_heads + h) * D + lane * EL;
+            const float* vr = reinterpret_cast<const float*>(a.v_pool) + (ri * a.n_kv_heads + h) * D + lane * EL;
 #pragma unroll
-            for (int e = 0; e < EL; ++e) x[j][e] = to_f(vr[e]);
+            for (int e = 0; e < EL; ++e) x[j][e] = vr[e];
           }
         }
 #pragma unroll
@@ -146,8 +130,8 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const __grid_con
       }
       __syncwarp();
     }
-    const bool whole = u_first == u0 && stop == u0 + nt;
-    const int64_t slot = (w * 2 + (u_first == u0 ? 1 : 0)) * kVecs;
+    const bool whole = at.j0 == 0 && at.j1 == at.nt;
+    const int64_t slot = (w * 2 + (at.j0 == 0 ? 1 : 0)) * kVecs;
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
 #pragma unroll
@@ -155,10 +139,10 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const __grid_con
       const int vi = vg * kVecs + v;
       if (v >= n_vec) continue;
       if (whole) {
-        T* out = reinterpret_cast<T*>(a.O) +
+        float* out = reinterpret_cast<float*>(a.O) +
                  ((int64_t)(at.q.row0 + vi / a.g) * a.n_q_heads + h * a.g + vi % a.g) * D + lane * EL;
 #pragma unroll
-        for (int e = 0; e < EL; ++e) out[e] = from_f<T>(acc[v][e] / l[v]);
+        for (int e = 0; e < EL; ++e) out[e] = acc[v][e] / l[v];
       } else {
         if (lane == 0) a.part_ml[slot + v] = make_float2(m[v], l[v]);
 #pragma unroll
@@ -244,13 +228,17 @@ cudaError_t launch_join(const TreeArgs& a, int d, cudaStream_t s) {
 
 // ---- host side ---------------------------------------------------------------
 
+constexpr int kCtas = 152;                // SMs
+constexpr int kSimtCtas = 8;              // CTAs of an SM (fp32 layers)
+
 fuse_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? FUSE_OK : FUSE_ERR_CUDA; }
 
 TreePlan plan_tree(const fuse_layer_desc_t& d, int n_seq) {
   TreePlan P;
-  P.vecs = kVecs;
-  P.tile = kTile;
-  P.workers = 152 * 8 * kWarps;
+  const bool tc = d.dtype == FUSE_BF16;
+  P.vecs = tc ? kTreeTcVecs : kVecs;
+  P.tile = tc ? kTreeTcTile : kTile;
+  P.workers = tc ? kCtas : kCtas * kSimtCtas * kWarps;
   P.start = sizeof(WsHeader);
   P.part_ml = align_up(P.start + ((size_t)n_seq + 1) * sizeof(int64_t), 256);
   const size_t rows = (size_t)P.workers * 2 * P.vecs;
@@ -263,11 +251,8 @@ TreePlan plan_tree(const fuse_layer_desc_t& d, int n_seq) {
 
 cudaError_t launch_tree_simt(const fuse_layer_desc_t& d, const TreeArgs& a, cudaStream_t s) {
   const dim3 grid(a.workers / kWarps), block(kWarps * 32);
-  if (d.dtype == FUSE_BF16)
-    return d.head_dim == 128 ? launch_pdl(tree_simt_kernel<__nv_bfloat16, 128>, grid, block, 0, s, a)
-                             : launch_pdl(tree_simt_kernel<__nv_bfloat16, 64>, grid, block, 0, s, a);
-  return d.head_dim == 128 ? launch_pdl(tree_simt_kernel<float, 128>, grid, block, 0, s, a)
-                           : launch_pdl(tree_simt_kernel<float, 64>, grid, block, 0, s, a);
+  return d.head_dim == 128 ? launch_pdl(tree_simt_kernel<128>, grid, block, 0, s, a)
+                           : launch_pdl(tree_simt_kernel<64>, grid, block, 0, s, a);
 }
 
 }  // namespace fusekv
@@ -322,7 +307,9 @@ fuse_status_t fuse_attend_tree(const fuse_layer_desc_t* desc, const fuse_seqs_t*
   a.part_ml = reinterpret_cast<float2*>(at(P.part_ml));
   a.part_o = reinterpret_cast<float*>(at(P.part_o));
   cudaStream_t s = (cudaStream_t)stream;
-  st = cuda_status(traced("attend_tree", s, [&] { return launch_tree_simt(*desc, a, s); }));
+  st = cuda_status(traced("attend_tree", s, [&] {
+    return desc->dtype == FUSE_BF16 ? launch_tree_tc(*desc, a, s) : launch_tree_simt(*desc, a, s);
+  }));
   if (st != FUSE_OK) return st;
   return cuda_status(traced("attend_tree_join", s, [&] {
     return desc->dtype == FUSE_BF16 ? launch_join<__nv_bfloat16>(a, desc->head_dim, s)

@@ -120,14 +120,75 @@ __device__ __forceinline__ TreeAt find_tile(const TreeArgs& a, int64_t t) {
   return r;
 }
 
-// The new tokens that new token i sees: itself and its ancestors, a bit each.
-__device__ __forceinline__ uint64_t seen_by(const int32_t* parents, const Seq& q, int i, uint32_t* err) {
-  if (!parents) return ~(uint64_t)0 >> (63 - i);
-  uint64_t seen = 0;
-  for (int j = i; j >= 0; j = parent_of(parents, q, j, err)) seen |= (uint64_t)1 << j;
-  return seen;
+// The new tokens that a new token sees, itself and its ancestors, a bit each: by
+// a whole warp for all of a sequence's, then handed to the lane that asks for `node`.
+// Pointer jumping: after k rounds a node's mask holds its 2^k nearest.
+__device__ __forceinline__ uint64_t seen_by(const int32_t* parents, const Seq& q, int node, uint32_t* err) {
+  if (!parents) return ~(uint64_t)0 >> (63 - node);
+  const int lane = threadIdx.x % 32;
+  // of nodes `lane` and `lane + 32`: what they see, and the next one up
+  unsigned long long m0 = 1ull << lane, m1 = m0 << 32;
+  int u0 = lane < q.n ? parent_of(parents, q, lane, err) : -1;
+  int u1 = lane + 32 < q.n ? parent_of(parents, q, lane + 32, err) : -1;
+  while (__any_sync(0xffffffffu, u0 >= 0 || u1 >= 0)) {
+    const unsigned long long a0 = __shfl_sync(0xffffffffu, m0, u0 & 31), a1 = __shfl_sync(0xffffffffu, m1, u0 & 31);
+    const unsigned long long b0 = __shfl_sync(0xffffffffu, m0, u1 & 31), b1 = __shfl_sync(0xffffffffu, m1, u1 & 31);
+    const int c0 = __shfl_sync(0xffffffffu, u0, u0 & 31), c1 = __shfl_sync(0xffffffffu, u1, u0 & 31);
+    const int d0 = __shfl_sync(0xffffffffu, u0, u1 & 31), d1 = __shfl_sync(0xffffffffu, u1, u1 & 31);
+    if (u0 >= 0) {
+      m0 |= u0 < 32 ? a0 : a1;
+      u0 = u0 < 32 ? c0 : c1;
+    }
+    if (u1 >= 0) {
+      m1 |= u1 < 32 ? b0 : b1;
+      u1 = u1 < 32 ? d0 : d1;
+    }
+  }
+  const unsigned long long lo = __shfl_sync(0xffffffffu, m0, node & 31), hi = __shfl_sync(0xffffffffu, m1, node & 31);
+  return node < 32 ? lo : hi;
+}
+
+// A worker's way through its tiles, unit by unit.
+struct TreeWalk {
+  TreeAt at;
+  int64_t t, end;
+};
+struct TreePart {
+  int s;
+  Seq q;
+  int h, vg;                              // KV head, group of vectors
+  int n_vec;                              // its vectors
+  int j0, j1, nt;                         // tiles taken, of the unit's nt
+};
+__device__ __forceinline__ bool next_part(const TreeArgs& a, TreeWalk& w, TreePart& p) {
+  while (w.t < w.end) {
+    const int nt = tiles_of(a, w.at.q), units = units_of(a, w.at.q);
+    const int64_t rel = w.t - w.at.first, all = (int64_t)units * nt;
+    if (rel >= all) {                     // the next sequence
+      w.at.first += all;
+      if (++w.at.s >= a.seq.n_seq) return false;
+      seq_of(a.seq, w.at.s, &w.at.q);
+      continue;
+    }
+    const int groups = units / a.n_kv_heads;
+    const int unit = rel >> 32 ? (int)(rel / nt) : (int)((uint32_t)rel / (uint32_t)nt);
+    p.s = w.at.s;
+    p.q = w.at.q;
+    p.h = unit / groups;
+    p.vg = unit - p.h * groups;
+    p.n_vec = min(a.vecs, p.q.n * a.g - p.vg * a.vecs);
+    p.nt = nt;
+    p.j0 = (int)(rel - (int64_t)unit * nt);
+    p.j1 = (int)min((int64_t)nt, p.j0 + (w.end - w.t));
+    w.t += p.j1 - p.j0;
+    return true;
+  }
+  return false;
 }
 
 cudaError_t launch_tree_simt(const fuse_layer_desc_t& d, const TreeArgs& a, cudaStream_t s);
+// bf16 layers, on the tensor cores (attend_tree_tc.cu).
+constexpr int kTreeTcVecs = 256, kTreeTcTile = 128;
+cudaError_t launch_tree_tc(const fuse_layer_desc_t& d, const TreeArgs& a, cudaStream_t s);
 
 }  // namespace fusekv

@@ -1,0 +1,706 @@
+// Attention of trees over a paged cache on tcgen05 tensor cores (bf16 layers).
+//
+// Work unit: one sequence, KV head and up to 256 query vectors (new token, query
+// head of the KV head), as one or two M = 128 tiles; keys stream in tiles of 128
+// through a ring in shared memory.  Two streams run side by side, each with a score
+// buffer, an accumulator and a softmax warpgroup of its own (one row a thread):
+//   two M tiles   stream w takes M tile w, both with the same keys
+//   one M tile    stream w takes every second key tile; the two softmaxes are
+//                 joined when the unit ends
+// so that one stream's products run beside the other's softmax.  Per step
+//   S = Q K^T     tcgen05.mma into TMEM columns [128 w, 128 w + 128)
+//   P = 2^(S - m) in registers, bf16, written back over S
+//   O += P V      tcgen05.mma with A = P in TMEM, V MN-major in shared memory
+// The running maximum m is raised only when a tile exceeds it by more than
+// 2^16 (then O and the running sum are rescaled).
+//
+// Keys and values lie in pages of any size, so their rows are gathered by
+// 16-byte cp.async, rows that are not there as zeros, in the 128-byte swizzle that the
+// MMAs read.  A row's copies count on the tile's mbarrier when they land; the
+// thread that issues the MMAs fences the generic proxy's writes.
+//
+// What a row does not see must not reach it: its scores are replaced where they
+// are masked, and as 0 * V is not 0 for an infinite or NaN V, one warp looks
+// the new tokens' values through before their product, clears what is not
+// finite, and the rows that do see such an element get it back at the end.
+// (Held tokens are seen by every row.)
+#include <algorithm>
+
+#include "attend_tree.h"
+#include "launch.h"
+#include "tc_ptx.cuh"
+
+namespace fusekv {
+
+namespace {
+
+constexpr int kKB = kTreeTcTile;              // keys per tile
+constexpr int kHalf = 128 * 64 * 2;           // 64 columns of a 128-row tile (16 KB)
+constexpr int kWarpLoad = 8, kLoadWarps = 4, kWarpS = 12, kWarpPV = 13, kWarpLook = 14;
+constexpr int kThreads = 15 * 32;
+constexpr int kLoadThreads = kLoadWarps * 32;
+constexpr int kTmemCols = 512;                // S of both streams | O of both
+constexpr float kRescaleThreshold = 16.0f;    // P and its sum keep their relative precision up to 2^16 over m
+constexpr int kMaxStages = 10;
+constexpr int kFix = 8;                       // parts with new tokens that the look may be ahead by, and more
+
+template <int D> struct Ring {
+  static constexpr int tile = (D / 64) * kHalf;
+  static constexpr int stages = D == 128 ? 5 : 10;
+};
+
+struct Ctl {
+  uint64_t q_full[2], q_empty[2];
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t look_full[kMaxStages], look_ok[kMaxStages];   // value tiles with new tokens, by ring slot
+  uint64_t s_full[2], p_full[2], pv_done[2];             // by stream
+  uint64_t x_full, o_empty;
+  unsigned long long fix[kFix];               // new tokens with values that are not finite
+  uint32_t tmem_base;
+  volatile int abort_flag;
+  volatile int bad_page;                      // some page of this CTA's units is outside the pool
+  float2 ml[2][128];                          // maximum and sum of each stream's rows
+  int64_t s_warp[kThreads / 32];
+};
+
+constexpr int kCtlBytes = 3072;               // in front of the tiles, which start at multiples of 1024
+static_assert(sizeof(Ctl) <= kCtlBytes, "shared memory");
+template <int D> constexpr int smem_bytes() { return kCtlBytes + (2 + Ring<D>::stages) * Ring<D>::tile; }
+static_assert(smem_bytes<128>() <= 227 * 1024 && smem_bytes<64>() <= 227 * 1024, "shared memory");
+
+// Which wait gave up: info = wait id << 16 | CTA.
+enum TreeWait : uint32_t {
+  W_Q_EMPTY = 1, W_EMPTY, W_Q_FULL, W_S_FREE, W_K_FULL, W_P_FULL, W_V_FULL, W_LOOK_OK, W_O_EMPTY, W_LOOK_FULL,
+  W_S_FULL, W_PV_DONE, W_O_FULL, W_X_FULL
+};
+
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, Ctl* ctl, uint32_t* err, uint32_t which) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t i = 0; i < tc::kWaitPollLimit; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((i & 63u) == 63u) {
+      if (ctl->abort_flag) return false;
+      const uint64_t now = tc::global_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > tc::kWaitLimitNs) break;
+    }
+  }
+  if (ctl->abort_flag == 0) {
+    ctl->abort_flag = 1;
+    report_error(err, FUSE_ERR_TIMEOUT, SITE_TREE_TIMEOUT, which);
+  }
+  return false;
+}
+__device__ __forceinline__ bool wait1(uint64_t* bar, uint32_t parity, Ctl* ctl, uint32_t* err, uint32_t which) {
+  if (tc::mbar_try_wait(bar, parity & 1)) return true;
+  return wait_on(tc::smem_u32(bar), parity & 1, ctl, err, (which << 16) | (blockIdx.x & 0xFFFFu));
+}
+__device__ __forceinline__ bool wait32(uint64_t* bar, uint32_t parity, Ctl* ctl, uint32_t* err, uint32_t which) {
+  return __all_sync(0xffffffffu, wait1(bar, parity, ctl, err, which));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Packed pairs of floats: one instruction does the operation on both halves.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// Arrives on the barrier, whose count provides for it, once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
+}
+
+// K-step kk (16 columns) of a 128-row K-major tile stored in 64-column halves.
+__device__ __forceinline__ uint64_t kmajor_step(uint32_t tile, int kk) {
+  return tc::smem_desc_k128(tile + (kk >> 2) * kHalf + (kk & 3) * 32);
+}
+
+__device__ __forceinline__ bool nonfinite2(uint32_t w) {
+  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+__device__ __forceinline__ uint32_t drop_nonfinite(uint32_t w) {
+  if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+  if ((w & 0x7F800000u) == 0x7F800000u) w &= 0xFFFFu;
+  return w;
+}
+
+// What every role derives from a part.
+struct Steps {
+  bool dual;                                  // two M tiles
+  int tiles, n;                               // key tiles, steps (of both streams)
+  __device__ __forceinline__ explicit Steps(const TreePart& p) {
+    dual = p.n_vec > 128;
+    tiles = p.j1 - p.j0;
+    n = dual ? 2 * tiles : tiles;
+  }
+  __device__ __forceinline__ int tile(int k) const { return dual ? k >> 1 : k; }
+  // Ring items in the order in which the products take them:
+  // K0 V0 K1 V1 .. for two M tiles, K0 K1 V0 K2 V1 .. for one.
+  __device__ __forceinline__ int k_item(int i) const { return dual || i == 0 ? 2 * i : 2 * i - 1; }
+  __device__ __forceinline__ int v_item(int i) const {
+    return dual ? 2 * i + 1 : i < tiles - 1 ? 2 * i + 2 : 2 * tiles - 1;
+  }
+};
+// Whether the keys of tile j go past the held tokens.
+__device__ __forceinline__ bool has_new(const TreePart& p, int j) { return (j + 1) * kKB > p.q.len; }
+
+// 32 keys' bits of a row: those that it sees, the first of them `rel` past the held tokens.
+__device__ __forceinline__ uint32_t seen_word(uint64_t seen, int rel) {
+  if (rel <= -32) return 0xffffffffu;
+  if (rel < 0) return ((1u << -rel) - 1u) | (uint32_t)(seen << -rel);
+  return rel < 64 ? (uint32_t)(seen >> rel) : 0u;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_constant__ TreeArgs a) {
+  constexpr int kTile = Ring<D>::tile, kSt = Ring<D>::stages;
+  constexpr int kColO = 2 * kKB;
+  static_assert(kColO + 2 * D <= kTmemCols, "tensor memory");
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem);
+  uint8_t* sQ = smem + kCtlBytes;
+  uint8_t* sR = sQ + 2 * kTile;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  uint32_t* const err = a.seq.err;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&ctl->q_full[i], kLoadThreads);
+      tc::mbar_init(&ctl->q_empty[i], 1);
+      tc::mbar_init(&ctl->s_full[i], 1);
+      tc::mbar_init(&ctl->p_full[i], 128);
+      tc::mbar_init(&ctl->pv_done[i], 1);
+    }
+    for (int i = 0; i < kSt; ++i) {
+      tc::mbar_init(&ctl->full[i], kLoadThreads);
+      tc::mbar_init(&ctl->empty[i], 1);
+      tc::mbar_init(&ctl->look_full[i], kLoadThreads);
+      tc::mbar_init(&ctl->look_ok[i], 1);
+    }
+    tc::mbar_init(&ctl->x_full, 256);
+    tc::mbar_init(&ctl->o_empty, 256);
+    ctl->abort_flag = 0;
+    ctl->bad_page = 0;
+    tc::fence_barrier_init();
+  }
+  if (warp == kWarpS) tc::tmem_alloc(&ctl->tmem_base, kTmemCols);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  pdl_wait();
+  pdl_trigger();
+  const int64_t total = count_tiles<kThreads>(a, ctl->s_warp);
+  const int64_t per = per_worker(a, total);
+  TreeWalk walk;
+  walk.t = min(total, (int64_t)blockIdx.x * per);
+  walk.end = min(total, walk.t + per);
+  const bool work = walk.t < walk.end;        // uniform
+  if (work) walk.at = find_tile(a, walk.t);
+  TreePart p{};
+
+  if (!work) {
+  } else if (warp >= kWarpLoad && warp < kWarpLoad + kLoadWarps) {
+    // -------------------------------- loads --------------------------------
+    // a warp takes 32 rows of every tile: a lane finds a row's place, then D / 8
+    // lanes copy a row
+    constexpr int kPieces = D / 8, kRows = 32 / kPieces;
+    const int row0 = (warp - kWarpLoad) * 32;
+    const int piece = lane % kPieces, sub = lane / kPieces;
+    uint32_t it = 0, qn0 = 0, qn1 = 0;
+    int qb = 0;
+    bool ok = true;
+    const int64_t stride = (int64_t)a.n_kv_heads * D;
+    // the copies of 32 rows; row < 0: zeros
+    auto copy = [&](uint8_t* tile, const __nv_bfloat16* base, int64_t step, int64_t row) {
+      const uint32_t dst = tc::smem_u32(tile) + (piece >> 3) * kHalf;
+#pragma unroll
+      for (int i = 0; i < 32 / kRows; ++i) {
+        const int r = i * kRows + sub, m = row0 + r;
+        const int64_t x = __shfl_sync(0xffffffffu, row, r);
+        cp16(dst + m * 128 + (((piece & 7) ^ (m & 7)) << 4), base + max(x, (int64_t)0) * step + piece * 8, x >= 0);
+      }
+    };
+    auto entry = [&](int j) {                 // the page of this lane's key of tile j; -2: no key
+      const int key = j * kKB + row0 + lane;
+      return key < p.q.len + p.q.n ? a.seq.tables[(int64_t)p.s * a.seq.max_blocks + key / a.seq.block_size] : -2;
+    };
+    auto place = [&](int j, int page) -> int64_t {
+      if (page == -2) return -1;
+      if (page < 0 || page >= a.seq.n_pool_blocks) {
+        report_error(err, FUSE_ERR_DEVICE_BOUNDS, SITE_SEQ_PAGE, (uint32_t)page);
+        ctl->bad_page = 1;
+        return -1;
+      }
+      return (int64_t)page * a.seq.block_size + (j * kKB + row0 + lane) % a.seq.block_size;
+    };
+    auto issue = [&](const void* pool, int64_t row, bool look) {
+      const int st = it % kSt;
+      if (!ok || !wait32(&ctl->empty[st], (it / kSt) ^ 1, ctl, err, W_EMPTY)) {
+        ok = false;
+        return;
+      }
+      copy(sR + st * kTile, reinterpret_cast<const __nv_bfloat16*>(pool) + (int64_t)p.h * D, stride, row);
+      if (ctl->bad_page) {                    // the flag has to be seen by who sees the tile
+        cp_wait_all();
+        tc::mbar_arrive(&ctl->full[st]);
+        if (look) tc::mbar_arrive(&ctl->look_full[st]);
+      } else {
+        cp_arrive(&ctl->full[st]);
+        if (look) cp_arrive(&ctl->look_full[st]);
+      }
+      ++it;
+    };
+    while (ok && next_part(a, walk, p)) {
+      const Steps u(p);
+      int page = entry(p.j0);
+      for (int m = 0; m < (u.dual ? 2 : 1); ++m) {
+        const int b = u.dual ? m : qb;
+        uint32_t& qn = b ? qn1 : qn0;
+        if (!wait32(&ctl->q_empty[b], qn ^ 1, ctl, err, W_Q_EMPTY)) {
+          ok = false;
+          break;
+        }
+        ++qn;
+        const int v = m * 128 + row0 + lane, vi = p.vg * a.vecs + v;
+        const int64_t row = v < p.n_vec
+                                ? (int64_t)(p.q.row0 + (vi >> a.g_log2)) * a.n_q_heads + p.h * a.g + (vi & (a.g - 1))
+                                : -1;
+        copy(sQ + b * kTile, reinterpret_cast<const __nv_bfloat16*>(a.Q), D, row);
+        cp_arrive(&ctl->q_full[b]);
+      }
+      if (!ok) break;
+      if (!u.dual) qb ^= 1;
+      int64_t cur = place(p.j0, page), nxt = -1;
+      if (p.j0 + 1 < p.j1) page = entry(p.j0 + 1);
+      issue(a.k_pool, cur, false);
+      for (int j = p.j0; ok && j < p.j1; ++j) {
+        const bool more = j + 1 < p.j1;
+        if (more) {
+          nxt = place(j + 1, page);
+          if (j + 2 < p.j1) page = entry(j + 2);
+        }
+        if (more && !u.dual) issue(a.k_pool, nxt, false);
+        issue(a.v_pool, cur, has_new(p, j));
+        if (more && u.dual) issue(a.k_pool, nxt, false);
+        cur = nxt;
+      }
+    }
+    cp_wait_all();
+  } else if (warp == kWarpS) {
+    // ------------------------------ S = Q K^T ------------------------------
+    if (lane == 0) {
+      constexpr uint32_t idesc = tc::idesc_bf16_f32(128, kKB);
+      uint32_t it = 0, c[2] = {0, 0}, qn0 = 0, qn1 = 0;
+      int qb = 0;
+      bool ok = true;
+      while (ok && next_part(a, walk, p)) {
+        const Steps u(p);
+        if (u.dual || qb == 0) ok = wait1(&ctl->q_full[0], qn0++, ctl, err, W_Q_FULL);
+        if (ok && (u.dual || qb == 1)) ok = wait1(&ctl->q_full[1], qn1++, ctl, err, W_Q_FULL);
+        if (!ok) break;
+        for (int k = 0; k < u.n; ++k) {
+          const int w = k & 1;
+          // the buffer holds P of the stream's step before until that step's P.V is done
+          // (and with it every ring item up to this one's slot has been full)
+          if (c[w] > 0 && !wait1(&ctl->pv_done[w], c[w] - 1, ctl, err, W_S_FREE)) {
+            ok = false;
+            break;
+          }
+          const uint32_t q = it + u.k_item(u.tile(k));
+          const int st = q % kSt;
+          if (!wait1(&ctl->full[st], q / kSt, ctl, err, W_K_FULL)) {
+            ok = false;
+            break;
+          }
+          tc::fence_proxy_async_smem();
+          tc::tc_fence_after();
+          const uint32_t qa = tc::smem_u32(sQ + (u.dual ? w : qb) * kTile), ka = tc::smem_u32(sR + st * kTile);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc::mma_bf16(tmem + w * kKB, kmajor_step(qa, kk), kmajor_step(ka, kk), idesc, kk != 0);
+          tc::mma_commit(&ctl->s_full[w]);
+          if (!u.dual || w == 1) tc::mma_commit(&ctl->empty[st]);
+          ++c[w];
+        }
+        if (!ok) break;
+        if (u.dual || qb == 0) tc::mma_commit(&ctl->q_empty[0]);
+        if (u.dual || qb == 1) tc::mma_commit(&ctl->q_empty[1]);
+        if (!u.dual) qb ^= 1;
+        it += 2 * u.tiles;
+      }
+    }
+  } else if (warp == kWarpPV) {
+    // ------------------------------- O += P V -------------------------------
+    if (lane == 0) {
+      constexpr uint32_t idesc = tc::idesc_bf16_f32(128, D, /*b_mn_major=*/true);
+      uint32_t it = 0, c[2] = {0, 0}, parts = 0, look = 0;       // look: look_ok's next parity by slot
+      bool ok = true;
+      while (ok && next_part(a, walk, p)) {
+        const Steps u(p);
+        for (int k = 0; k < u.n; ++k) {
+          const int w = k & 1, i = u.tile(k);
+          const uint32_t q = it + u.v_item(i);
+          const int st = q % kSt;
+          // P first: the ring's earlier items have been full by then
+          ok = wait1(&ctl->p_full[w], c[w], ctl, err, W_P_FULL) && wait1(&ctl->full[st], q / kSt, ctl, err, W_V_FULL);
+          if (ok && (!u.dual || w == 0) && has_new(p, p.j0 + i)) {
+            ok = wait1(&ctl->look_ok[st], look >> st, ctl, err, W_LOOK_OK);
+            look ^= 1u << st;
+          }
+          // the accumulators were last read at the end of the part before
+          if (ok && k == 0) ok = wait1(&ctl->o_empty, parts ^ 1, ctl, err, W_O_EMPTY);
+          if (!ok) break;
+          tc::fence_proxy_async_smem();
+          tc::tc_fence_after();
+          const uint32_t va = tc::smem_u32(sR + st * kTile);
+#pragma unroll
+          for (int kk = 0; kk < kKB / 16; ++kk)
+            tc::mma_bf16_ts(tmem + kColO + w * D, tmem + w * kKB + kk * 8,
+                            tc::smem_desc_mn128(va + kk * 16 * 128, kHalf), idesc, (k > 1 || kk != 0) ? 1u : 0u);
+          tc::mma_commit(&ctl->pv_done[w]);
+          if (!u.dual || w == 1) tc::mma_commit(&ctl->empty[st]);
+          ++c[w];
+        }
+        if (!ok) break;
+        ++parts;
+        it += 2 * u.tiles;
+      }
+    }
+  } else if (warp == kWarpLook) {
+    // ------------------- values of new tokens looked through -------------------
+    constexpr int kPieces = D / 8, kRows = 32 / kPieces;
+    uint32_t it = 0, look = 0, with_new = 0;
+    bool ok = true;
+    while (ok && next_part(a, walk, p)) {
+      const Steps u(p);
+      unsigned long long found = 0;
+      bool any = false;
+      for (int i = 0; i < u.tiles; ++i) {
+        const int j = p.j0 + i;
+        if (!has_new(p, j)) continue;
+        any = true;
+        const int st = (it + u.v_item(i)) % kSt;
+        if (!wait32(&ctl->look_full[st], look >> st, ctl, err, W_LOOK_FULL)) {
+          ok = false;
+          break;
+        }
+        look ^= 1u << st;
+        const int key0 = j * kKB;
+        const int m0 = max(p.q.len - key0, 0), m1 = min(kKB, p.q.len + p.q.n - key0);
+        const int piece = lane % kPieces;
+        bool changed = false;
+        for (int m = m0 + lane / kPieces; m < m1; m += kRows) {
+          uint4* at = reinterpret_cast<uint4*>(sR + st * kTile + (piece >> 3) * kHalf + m * 128 +
+                                               (((piece & 7) ^ (m & 7)) << 4));
+          uint4 x = *at;
+          if (nonfinite2(x.x) || nonfinite2(x.y) || nonfinite2(x.z) || nonfinite2(x.w)) {
+            x.x = drop_nonfinite(x.x);
+            x.y = drop_nonfinite(x.y);
+            x.z = drop_nonfinite(x.z);
+            x.w = drop_nonfinite(x.w);
+            *at = x;
+            found |= 1ull << (key0 + m - p.q.len);
+            changed = true;
+          }
+        }
+        if (__any_sync(0xffffffffu, changed)) tc::fence_proxy_async_smem();
+        found = (unsigned long long)__reduce_or_sync(0xffffffffu, (uint32_t)(found >> 32)) << 32 |
+                __reduce_or_sync(0xffffffffu, (uint32_t)found);
+        __syncwarp();
+        if (lane == 0) {
+          ctl->fix[with_new % kFix] = found;
+          tc::mbar_arrive(&ctl->look_ok[st]);
+        }
+      }
+      with_new += any;
+      it += 2 * u.tiles;
+    }
+  } else if (warp < kWarpLoad) {
+    // ------------------------------- softmax -------------------------------
+    const int w = warp >> 2, quarter = warp & 3;
+    const int r = quarter * 32 + lane;            // M row
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const uint32_t tS = tmem + lane_off + w * kKB;
+    const float scale = a.scale;
+    const uint64_t sc2 = pack2(scale, scale);
+    uint32_t c = 0, parts = 0, with_new = 0;
+    bool ok = true;
+    while (ok && next_part(a, walk, p)) {
+      const Steps u(p);
+      const int v = (u.dual ? w * 128 : 0) + r;   // the row's vector of the unit
+      const int vi = p.vg * a.vecs + min(v, p.n_vec - 1), node = vi >> a.g_log2;
+      uint64_t seen = ~(uint64_t)0;
+      const bool news = has_new(p, p.j1 - 1);
+      if (news) seen = seen_by(a.parents, p.q, node, err);
+      float mr = -INFINITY, mu = -INFINITY, l = 0.f;       // reference (score, log2 units), sum
+      bool first = true;
+      for (int k = w; k < u.n; k += 2, ++c) {
+        const int j = p.j0 + u.tile(k);
+        if (!wait32(&ctl->s_full[w], c, ctl, err, W_S_FULL)) {
+          ok = false;
+          break;
+        }
+        tc::tc_fence_after();
+        uint32_t x[64];
+        auto load = [&](int half) {
+          tc::tmem_ld_32x32b_x32(tS + 64 * half, *reinterpret_cast<uint32_t(*)[32]>(x));
+          tc::tmem_ld_32x32b_x32(tS + 64 * half + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
+          tc::tmem_ld_wait();
+        };
+        const bool bad = ctl->bad_page != 0;
+        const bool masked = has_new(p, j) || bad;
+        uint32_t word[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+        if (masked) {
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            word[b] = seen_word(seen, j * kKB + 32 * b - p.q.len);
+            if (bad) {                        // keys whose page is not in the pool
+              const int key = j * kKB + 32 * b + lane;
+              int page = 0;
+              if (key < p.q.len + p.q.n)
+                page = a.seq.tables[(int64_t)p.s * a.seq.max_blocks + key / a.seq.block_size];
+              word[b] &= __ballot_sync(0xffffffffu, page >= 0 && page < a.seq.n_pool_blocks);
+            }
+          }
+        }
+        auto mask = [&](int half) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            if (!(word[2 * half] >> e & 1)) x[e] = 0xff800000u;
+            if (!(word[2 * half + 1] >> e & 1)) x[32 + e] = 0xff800000u;
+          }
+        };
+        auto top = [&](float m0) {
+          float m1 = __uint_as_float(x[0]), m2 = __uint_as_float(x[1]), m3 = __uint_as_float(x[2]);
+#pragma unroll
+          for (int e = 3; e < 63; e += 6) {
+            m1 = max3(m1, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+            m2 = max3(m2, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+            m3 = max3(m3, __uint_as_float(x[e + 4]), __uint_as_float(x[e + 5]));
+          }
+          return max3(max3(m0, m1, m2), m3, __uint_as_float(x[63]));
+        };
+        load(1);
+        if (masked) mask(1);
+        float m = top(-INFINITY);
+        load(0);
+        if (masked) mask(0);
+        m = top(m);
+        const float ms = m * scale;
+        float mn = mu;
+        bool rescale = false;
+        if (first) {
+          mn = ms;
+          mr = m;
+        } else if (ms > mu + kRescaleThreshold) {
+          mn = ms;
+          mr = m;
+          rescale = true;
+        }
+        const float al = rescale ? ex2(mu - mn) : 1.f;
+        // (a row whose every score so far is -infinity has weights of 0, not 2^(-inf + inf))
+        const float ref = mn == -INFINITY ? 0.f : mn;
+        // scores so large that the rounding of their maximum's product would show:
+        // their difference is taken first
+        const bool far = __any_sync(0xffffffffu, fabsf(ref) > 1048576.f);
+        const uint64_t ng = far ? 0ull : pack2(-ref, -ref);
+        auto nearer = [&] {
+          const float mf = mr == -INFINITY ? 0.f : mr;
+#pragma unroll
+          for (int e = 0; e < 64; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) - mf);
+        };
+        uint64_t s0 = 0, s1 = 0;
+        auto weights = [&](int half) {            // and their place: over scores that are read
+#pragma unroll
+          for (int e = 0; e < 64; e += 4) {
+            const float2 y = unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), sc2, ng));
+            const float2 z = unpack2(fma2(pack2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), sc2, ng));
+            const float e0 = ex2(y.x), e1 = ex2(y.y), e2 = ex2(z.x), e3 = ex2(z.y);
+            s0 = add2(s0, pack2(e0, e1));
+            s1 = add2(s1, pack2(e2, e3));
+            x[e / 2] = pack_bf16x2(e0, e1);
+            x[e / 2 + 1] = pack_bf16x2(e2, e3);
+          }
+          tc::tmem_st_32x32b_x32(tS + 32 * half, *reinterpret_cast<uint32_t(*)[32]>(x));
+        };
+        if (far) nearer();
+        weights(0);
+        load(1);
+        if (masked) mask(1);
+        if (far) nearer();
+        weights(1);
+        // the accumulator's rows, by the whole warp when any of them needs it
+        // (the factor is 1 for the others), once the step before has been added
+        if (__any_sync(0xffffffffu, rescale)) {
+          if (!wait32(&ctl->pv_done[w], c - 1, ctl, err, W_PV_DONE)) {
+            ok = false;
+            break;
+          }
+          tc::tc_fence_after();
+#pragma unroll 1
+          for (int e0 = 0; e0 < D; e0 += 32) {
+            uint32_t o[32];
+            const uint32_t tO = tmem + lane_off + kColO + w * D + e0;
+            tc::tmem_ld_32x32b_x32(tO, o);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+            tc::tmem_st_32x32b_x32(tO, o);
+          }
+        }
+        tc::tmem_st_wait();
+        tc::tc_fence_before();
+        tc::mbar_arrive(&ctl->p_full[w]);
+        const float2 t0 = unpack2(s0), t1 = unpack2(s1);
+        l = l * al + ((t0.x + t0.y) + (t1.x + t1.y));
+        mu = mn;
+        first = false;
+      }
+      if (!ok) break;
+      // both streams are at their end: their rows' maxima and sums meet
+      if (!first && !wait32(&ctl->pv_done[w], c - 1, ctl, err, W_O_FULL)) break;
+      ctl->ml[w][r] = make_float2(mu, l);
+      tc::mbar_arrive(&ctl->x_full);
+      if (!wait32(&ctl->x_full, parts, ctl, err, W_X_FULL)) break;
+      tc::tc_fence_after();
+      // one M tile: the streams' sums are added, each warpgroup takes half of the columns
+      const float2 other = u.dual ? make_float2(-INFINITY, 0.f) : ctl->ml[1 - w][r];
+      const bool two = !u.dual && u.n > 1;
+      const float M = fmaxf(mu, other.x), ref = M == -INFINITY ? 0.f : M;
+      const float fo = two ? ex2(other.x - ref) : 0.f, fm = two ? ex2(mu - ref) : 1.f;
+      const float sum = two ? l * fm + other.y * fo : u.dual || !first ? l : other.y;
+      const float f0 = u.dual || w == 0 ? fm : fo, f1 = w == 0 ? fo : fm;     // of O[0] (own O), O[1]
+      const bool whole = p.j0 == 0 && p.j1 == p.nt;
+      const float inv = whole ? 1.f / sum : 1.f;
+      unsigned long long fix = 0;
+      if (news) {
+        fix = *(volatile unsigned long long*)&ctl->fix[with_new % kFix] & seen;
+        ++with_new;
+      }
+      const bool valid = v < p.n_vec;
+      const int e_begin = u.dual ? 0 : w * (D / 2), e_end = u.dual ? D : e_begin + D / 2;
+      const uint32_t tO = tmem + lane_off + kColO + (u.dual ? w * D : 0);
+      const int64_t slot = ((int64_t)blockIdx.x * 2 + (p.j0 == 0 ? 1 : 0)) * kTreeTcVecs + v;
+      __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.O) +
+                           ((int64_t)(p.q.row0 + node) * a.n_q_heads + p.h * a.g + (vi & (a.g - 1))) * D;
+#pragma unroll 1
+      for (int e0 = e_begin; e0 < e_end; e0 += 32) {
+        uint32_t o[32];
+        tc::tmem_ld_32x32b_x32(tO + e0, o);
+        if (two) {
+          uint32_t o1[32];
+          tc::tmem_ld_32x32b_x32(tO + D + e0, o1);
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            o[e] = __float_as_uint(fmaf(__uint_as_float(o[e]), f0, __uint_as_float(o1[e]) * f1));
+        } else {
+          tc::tmem_ld_wait();
+        }
+        if (fix) {                            // rare: elements that are not finite, of new tokens that this row sees
+#pragma unroll 1
+          for (unsigned long long left = fix; left; left &= left - 1) {
+            const int64_t row = pool_row(a.seq, p.s, p.q.len + __ffsll(left) - 1);
+            if (row < 0) continue;
+            const __nv_bfloat16* vr =
+                reinterpret_cast<const __nv_bfloat16*>(a.v_pool) + (row * a.n_kv_heads + p.h) * D + e0;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float y = __bfloat162float(vr[e]);
+              if (!isfinite(y)) o[e] = __float_as_uint(__uint_as_float(o[e]) + y);
+            }
+          }
+        }
+        if (e0 + 32 == e_end) {               // read: the next part's first products may start
+          tc::tc_fence_before();
+          tc::mbar_arrive(&ctl->o_empty);
+        }
+        if (valid && whole) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              y[e] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * e]) * inv, __uint_as_float(o[8 * q + 2 * e + 1]) * inv);
+            *reinterpret_cast<uint4*>(out + e0 + 8 * q) = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        } else if (valid) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<uint4*>(a.part_o + slot * D + e0 + 4 * q) =
+                make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+        }
+        __syncwarp();
+      }
+      if (valid && !whole && (u.dual || w == 0)) a.part_ml[slot] = make_float2(M, sum);
+      ++parts;
+    }
+  }
+
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  if (ctl->abort_flag) {                      // products in flight get time to end
+#pragma unroll 1
+    for (int k = 0; k < 1000; ++k) __nanosleep(1000);
+    __syncthreads();
+  }
+  if (warp == kWarpS) tc::tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int D>
+cudaError_t launch_d(const TreeArgs& a, cudaStream_t s) {
+  const cudaError_t e = set_dyn_smem_once(reinterpret_cast<const void*>(tree_tc_kernel<D>), smem_bytes<D>());
+  if (e != cudaSuccess) return e;
+  return launch_pdl(tree_tc_kernel<D>, dim3(a.workers), dim3(kThreads), smem_bytes<D>(), s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_tc(const fuse_layer_desc_t& d, const TreeArgs& a, cudaStream_t s) {
+  return d.head_dim == 128 ? launch_d<128>(a, s) : launch_d<64>(a, s);
+}
+
+}  // namespace fusekv
