@@ -45,10 +45,11 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const __grid_con
   while (next_part(a, walk, at)) {
     const int h = at.h, vg = at.vg, n_vec = at.n_vec;
     uint64_t seen[kVecs];
+    const Seen all = seen_of_all(a.parents, at.q, a.seq.err);
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
       const int vi = vg * kVecs + min(v, n_vec - 1), i = vi / a.g;
-      seen[v] = seen_by(a.parents, at.q, i, a.seq.err);
+      seen[v] = seen_by(all, i);
       const float* q = reinterpret_cast<const float*>(a.Q) +
                    ((int64_t)(at.q.row0 + i) * a.n_q_heads + h * a.g + vi % a.g) * D;
       for (int e = lane; e < D; e += 32) s_q[warp][v][e] = q[e] * a.scale;
@@ -153,9 +154,12 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const __grid_con
   }
 }
 
-// Joins the parts of one new token's query heads of one KV head (blockIdx.y).
-// A part's row is read by D / 4 lanes.
-constexpr int kJoinThreads = 256;
+// Joins the parts of one new token's query heads of one KV head (blockIdx.y), which
+// are vectors of the same unit.  8 / g warps take a vector, every one of them a
+// share of its parts, kRows of them in flight.  Latency bounds it, so what the
+// attention does not write (rows, lengths) is read before it is waited for.
+constexpr int kJoinWarps = 8;             // g is at most 8
+constexpr int kRows = 8;
 
 template <typename T> __device__ __forceinline__ void store4(T* p, float4 v);
 template <> __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
@@ -164,66 +168,89 @@ template <> __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeArgs a) {
-  constexpr int L = D / 4, kGroups = kJoinThreads / L;     // lanes of a row, rows at a time
-  __shared__ float4 s_o[kGroups][L];
-  __shared__ float s_l[kGroups];
+__global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid_constant__ TreeArgs a) {
+  constexpr int L = D / 4, kSub = 32 / L;  // lanes of a row, rows of a warp's read
+  __shared__ float4 s_o[kJoinWarps * kSub][L];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   pdl_trigger();
-  pdl_wait();
   const int row = blockIdx.x, h = blockIdx.y;
   const int s = seq_of_row(a.seq.rows, a.seq.n_seq, row);
   if (s < 0 || s >= a.seq.n_seq) return;
   Seq q;
   if (!seq_of(a.seq, s, &q) || row < q.row0 || row >= q.row0 + q.n) return;
-  const int64_t total = a.start[a.seq.n_seq], per = per_worker(a, total);
   const int nt = tiles_of(a, q), groups = units_of(a, q) / a.n_kv_heads;
-  const int lane = threadIdx.x % L, grp = threadIdx.x / L;
-  for (int j = 0; j < a.g; ++j) {
-    const int vi = (row - q.row0) * a.g + j, vg = vi / a.vecs, v = vi % a.vecs;
-    const int64_t u0 = a.start[s] + (int64_t)(h * groups + vg) * nt;
-    const int64_t c0 = u0 / per, c1 = min((u0 + nt - 1) / per, (int64_t)a.workers - 1);
-    if (c0 == c1) continue;               // written by its one worker
-    auto slot = [&](int64_t c) { return (c * 2 + (c == c0 ? 1 : 0)) * a.vecs + v; };
-    float M = -INFINITY;
-    for (int64_t c = c0; c <= c1; ++c) M = fmaxf(M, a.part_ml[slot(c)].x);
-    const float ref = M == -INFINITY ? 0.f : M;
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int64_t c = c0 + grp; c <= c1; c += kGroups) {
-      const float2 ml = a.part_ml[slot(c)];
-      if (ml.x == -INFINITY && ml.y == 0.f) continue;      // saw no key
-      const float w = exp2f(ml.x - ref);
-      const float4 x = *reinterpret_cast<const float4*>(a.part_o + slot(c) * D + lane * 4);
-      l = fmaf(w, ml.y, l);
-      o.x = fmaf(w, x.x, o.x);
-      o.y = fmaf(w, x.y, o.y);
-      o.z = fmaf(w, x.z, o.z);
-      o.w = fmaf(w, x.w, o.w);
-    }
-    s_o[grp][lane] = o;
-    if (lane == 0) s_l[grp] = l;
-    __syncthreads();
-    if (grp == 0) {
-      for (int k = 1; k < kGroups; ++k) {
-        const float4 x = s_o[k][lane];
-        o.x += x.x;
-        o.y += x.y;
-        o.z += x.z;
-        o.w += x.w;
-        l += s_l[k];
+  const int per_vec = kJoinWarps >> a.g_log2;
+  const int j = warp / per_vec, share = warp % per_vec;
+  const int vi = (row - q.row0) * a.g + j, vg = vi / a.vecs, v = vi % a.vecs;
+  pdl_wait();
+  const int64_t per = per_worker(a, a.start[a.seq.n_seq]);
+  const int64_t u0 = a.start[s] + (int64_t)(h * groups + vg) * nt;
+  const int64_t c0 = u0 / per, c1 = min((u0 + nt - 1) / per, (int64_t)a.workers - 1);
+  if (c0 == c1) return;                   // written by its one worker
+  const int parts = (int)(c1 - c0) + 1;
+  auto slot = [&](int i) { return ((c0 + i) * 2 + (i == 0 ? 1 : 0)) * a.vecs + v; };
+  float M = -INFINITY;
+  for (int i = lane; i < parts; i += 32) M = fmaxf(M, a.part_ml[slot(i)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float ref = M == -INFINITY ? 0.f : M;
+  const int sub = lane / L, ch = lane % L * 4;
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < parts; i0 += 32) {
+    const int n = min(32, parts - i0);
+    float w = -1.f;                       // of a part that saw no key, which is passed over
+    if (lane < n) {
+      const float2 ml = a.part_ml[slot(i0 + lane)];
+      if (!(ml.x == -INFINITY && ml.y == 0.f)) {
+        w = exp2f(ml.x - ref);
+        l = fmaf(w, ml.y, l);
       }
-      store4(reinterpret_cast<T*>(a.O) + ((int64_t)row * a.n_q_heads + h * a.g + j) * D + lane * 4,
-             make_float4(o.x / l, o.y / l, o.z / l, o.w / l));
     }
-    __syncthreads();
+    const int step = per_vec * kSub;
+    for (int i = share * kSub; i < n; i += kRows * step) {
+      float4 x[kRows];
+      float f[kRows];
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        const int at = i + k * step + sub;
+        f[k] = __shfl_sync(0xffffffffu, w, at & 31);
+        if (at >= n) f[k] = -1.f;
+        if (f[k] != -1.f) x[k] = *reinterpret_cast<const float4*>(a.part_o + slot(i0 + at) * D + ch);
+      }
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        if (f[k] == -1.f) continue;
+        o.x = fmaf(f[k], x[k].x, o.x);
+        o.y = fmaf(f[k], x[k].y, o.y);
+        o.z = fmaf(f[k], x[k].z, o.z);
+        o.w = fmaf(f[k], x[k].w, o.w);
+      }
+    }
   }
+#pragma unroll
+  for (int e = 16; e > 0; e >>= 1) l += __shfl_xor_sync(0xffffffffu, l, e);
+  if (per_vec * kSub > 1) {
+    s_o[warp * kSub + sub][lane % L] = o;
+    __syncthreads();
+    if (share != 0 || sub != 0) return;
+    for (int k = 1; k < per_vec * kSub; ++k) {
+      const float4 x = s_o[warp * kSub + k][lane];
+      o.x += x.x;
+      o.y += x.y;
+      o.z += x.z;
+      o.w += x.w;
+    }
+  }
+  store4(reinterpret_cast<T*>(a.O) + ((int64_t)row * a.n_q_heads + h * a.g + j) * D + ch,
+         make_float4(o.x / l, o.y / l, o.z / l, o.w / l));
 }
 
 template <typename T>
 cudaError_t launch_join(const TreeArgs& a, int d, cudaStream_t s) {
   const dim3 grid((unsigned)a.seq.n_rows, a.n_kv_heads);
-  return d == 128 ? launch_pdl(tree_join_kernel<T, 128>, grid, dim3(kJoinThreads), 0, s, a)
-                  : launch_pdl(tree_join_kernel<T, 64>, grid, dim3(kJoinThreads), 0, s, a);
+  return d == 128 ? launch_pdl(tree_join_kernel<T, 128>, grid, dim3(kJoinWarps * 32), 0, s, a)
+                  : launch_pdl(tree_join_kernel<T, 64>, grid, dim3(kJoinWarps * 32), 0, s, a);
 }
 
 // ---- host side ---------------------------------------------------------------

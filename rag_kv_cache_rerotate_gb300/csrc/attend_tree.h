@@ -120,31 +120,44 @@ __device__ __forceinline__ TreeAt find_tile(const TreeArgs& a, int64_t t) {
   return r;
 }
 
-// The new tokens that a new token sees, itself and its ancestors, a bit each: by
-// a whole warp for all of a sequence's, then handed to the lane that asks for `node`.
-// Pointer jumping: after k rounds a node's mask holds its 2^k nearest.
-__device__ __forceinline__ uint64_t seen_by(const int32_t* parents, const Seq& q, int node, uint32_t* err) {
-  if (!parents) return ~(uint64_t)0 >> (63 - node);
+// What new tokens see of the new ones, themselves and their ancestors, a bit each:
+// a warp's lanes hold the masks of nodes `lane` and `lane + 32`.  Pointer jumping:
+// after k rounds a mask holds a node's 2^k nearest.
+struct Seen {
+  unsigned long long m0, m1;
+};
+__device__ __forceinline__ Seen seen_of_all(const int32_t* parents, const Seq& q, uint32_t* err) {
   const int lane = threadIdx.x % 32;
-  // of nodes `lane` and `lane + 32`: what they see, and the next one up
-  unsigned long long m0 = 1ull << lane, m1 = m0 << 32;
+  Seen s;
+  if (!parents) {
+    s.m0 = ~0ull >> (63 - lane);
+    s.m1 = ~0ull >> (31 - lane);
+    return s;
+  }
+  s.m0 = 1ull << lane;
+  s.m1 = s.m0 << 32;
+  // the next ones up
   int u0 = lane < q.n ? parent_of(parents, q, lane, err) : -1;
   int u1 = lane + 32 < q.n ? parent_of(parents, q, lane + 32, err) : -1;
   while (__any_sync(0xffffffffu, u0 >= 0 || u1 >= 0)) {
-    const unsigned long long a0 = __shfl_sync(0xffffffffu, m0, u0 & 31), a1 = __shfl_sync(0xffffffffu, m1, u0 & 31);
-    const unsigned long long b0 = __shfl_sync(0xffffffffu, m0, u1 & 31), b1 = __shfl_sync(0xffffffffu, m1, u1 & 31);
+    const unsigned long long a0 = __shfl_sync(0xffffffffu, s.m0, u0 & 31), a1 = __shfl_sync(0xffffffffu, s.m1, u0 & 31);
+    const unsigned long long b0 = __shfl_sync(0xffffffffu, s.m0, u1 & 31), b1 = __shfl_sync(0xffffffffu, s.m1, u1 & 31);
     const int c0 = __shfl_sync(0xffffffffu, u0, u0 & 31), c1 = __shfl_sync(0xffffffffu, u1, u0 & 31);
     const int d0 = __shfl_sync(0xffffffffu, u0, u1 & 31), d1 = __shfl_sync(0xffffffffu, u1, u1 & 31);
     if (u0 >= 0) {
-      m0 |= u0 < 32 ? a0 : a1;
+      s.m0 |= u0 < 32 ? a0 : a1;
       u0 = u0 < 32 ? c0 : c1;
     }
     if (u1 >= 0) {
-      m1 |= u1 < 32 ? b0 : b1;
+      s.m1 |= u1 < 32 ? b0 : b1;
       u1 = u1 < 32 ? d0 : d1;
     }
   }
-  const unsigned long long lo = __shfl_sync(0xffffffffu, m0, node & 31), hi = __shfl_sync(0xffffffffu, m1, node & 31);
+  return s;
+}
+// The mask of the node that a lane asks for (by a whole warp).
+__device__ __forceinline__ uint64_t seen_by(const Seen& s, int node) {
+  const unsigned long long lo = __shfl_sync(0xffffffffu, s.m0, node & 31), hi = __shfl_sync(0xffffffffu, s.m1, node & 31);
   return node < 32 ? lo : hi;
 }
 

@@ -2,14 +2,14 @@
 //
 // Work unit: one sequence, KV head and up to 256 query vectors (new token, query
 // head of the KV head), as one or two M = 128 tiles; keys stream in tiles of 128
-// through a ring in shared memory.  Two streams run side by side, each with a score
-// buffer, an accumulator and a softmax warpgroup of its own (one row a thread):
+// through a ring in shared memory.  Two streams alternate, each with a score
+// buffer and an accumulator of its own:
 //   two M tiles   stream w takes M tile w, both with the same keys
 //   one M tile    stream w takes every second key tile; the two softmaxes are
 //                 joined when the unit ends
 // so that one stream's products run beside the other's softmax.  Per step
 //   S = Q K^T     tcgen05.mma into TMEM columns [128 w, 128 w + 128)
-//   P = 2^(S - m) in registers, bf16, written back over S
+//   P = 2^(S - m) eight warps in registers, bf16, written back over S
 //   O += P V      tcgen05.mma with A = P in TMEM, V MN-major in shared memory
 // The running maximum m is raised only when a tile exceeds it by more than
 // 2^16 (then O and the running sum are rescaled).
@@ -131,6 +131,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -209,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
       tc::mbar_init(&ctl->q_full[i], kLoadThreads);
       tc::mbar_init(&ctl->q_empty[i], 1);
       tc::mbar_init(&ctl->s_full[i], 1);
-      tc::mbar_init(&ctl->p_full[i], 128);
+      tc::mbar_init(&ctl->p_full[i], 256);
       tc::mbar_init(&ctl->pv_done[i], 1);
     }
     for (int i = 0; i < kSt; ++i) {
@@ -459,222 +464,278 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     }
   } else if (warp < kWarpLoad) {
     // ------------------------------- softmax -------------------------------
-    const int w = warp >> 2, quarter = warp & 3;
-    const int r = quarter * 32 + lane;            // M row
-    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t tS = tmem + lane_off + w * kKB;
+    // warp w: TMEM lane quarter w % 4, half w / 4 of it: 16 M rows, a thread two
+    // of them with 32 keys each
+    const int quarter = warp & 3, half = warp >> 2;
+    const int base = quarter * 32 + half * 16;
+    const int c4 = lane & 3;
+    const int R0 = base + (lane >> 2), R1 = R0 + 8;
     const float scale = a.scale;
     const uint64_t sc2 = pack2(scale, scale);
-    uint32_t c = 0, parts = 0, with_new = 0;
-    bool ok = true;
-    while (ok && next_part(a, walk, p)) {
+    uint32_t c0 = 0, c1 = 0, parts = 0, with_new = 0;       // steps of each stream, parts
+    while (next_part(a, walk, p)) {
       const Steps u(p);
-      const int v = (u.dual ? w * 128 : 0) + r;   // the row's vector of the unit
-      const int vi = p.vg * a.vecs + min(v, p.n_vec - 1), node = vi >> a.g_log2;
-      uint64_t seen = ~(uint64_t)0;
       const bool news = has_new(p, p.j1 - 1);
-      if (news) seen = seen_by(a.parents, p.q, node, err);
-      float mr = -INFINITY, mu = -INFINITY, l = 0.f;       // reference (score, log2 units), sum
-      bool first = true;
-      for (int k = w; k < u.n; k += 2, ++c) {
-        const int j = p.j0 + u.tile(k);
+      Seen all{};
+      if (news) all = seen_of_all(a.parents, p.q, err);
+      // of the stream at hand (m, l) and the other one (n, k): the rows' references
+      // (scores) and this thread's part of their sums
+      float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+      float n0 = -INFINITY, n1 = -INFINITY, k0 = 0.f, k1 = 0.f;
+      bool ok = true;
+      for (int k = 0; k < u.n; ++k) {
+        const int w = k & 1, j = p.j0 + u.tile(k);
+        const uint32_t c = w ? c1 : c0;
         if (!wait32(&ctl->s_full[w], c, ctl, err, W_S_FULL)) {
           ok = false;
           break;
         }
         tc::tc_fence_after();
-        uint32_t x[64];
-        auto load = [&](int half) {
-          tc::tmem_ld_32x32b_x32(tS + 64 * half, *reinterpret_cast<uint32_t(*)[32]>(x));
-          tc::tmem_ld_32x32b_x32(tS + 64 * half + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
-          tc::tmem_ld_wait();
-        };
+        const uint32_t tS = tmem + ((uint32_t)base << 16) + w * kKB;
+        uint32_t r[64];
+        tc::tmem_ld_16x256b_x8(tS, *reinterpret_cast<uint32_t(*)[32]>(r));
+        tc::tmem_ld_16x256b_x8(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
+        tc::tmem_ld_wait();
         const bool bad = ctl->bad_page != 0;
-        const bool masked = has_new(p, j) || bad;
-        uint32_t word[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
-        if (masked) {
+        if (has_new(p, j) || bad) {
+          constexpr uint32_t kMasked = 0xff800000u;        // -infinity
+          uint64_t seen0 = ~(uint64_t)0, seen1 = seen0;
+          if (news) {
+            const int v0 = (u.dual ? w * 128 : 0) + R0;
+            seen0 = seen_by(all, (p.vg * a.vecs + min(v0, p.n_vec - 1)) >> a.g_log2);
+            seen1 = seen_by(all, (p.vg * a.vecs + min(v0 + 8, p.n_vec - 1)) >> a.g_log2);
+          }
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
-            word[b] = seen_word(seen, j * kKB + 32 * b - p.q.len);
+            const int rel = j * kKB + 32 * b - p.q.len;
+            uint32_t w0 = seen_word(seen0, rel), w1 = seen_word(seen1, rel);
             if (bad) {                        // keys whose page is not in the pool
               const int key = j * kKB + 32 * b + lane;
               int page = 0;
               if (key < p.q.len + p.q.n)
                 page = a.seq.tables[(int64_t)p.s * a.seq.max_blocks + key / a.seq.block_size];
-              word[b] &= __ballot_sync(0xffffffffu, page >= 0 && page < a.seq.n_pool_blocks);
+              const uint32_t there = __ballot_sync(0xffffffffu, page >= 0 && page < a.seq.n_pool_blocks);
+              w0 &= there;
+              w1 &= there;
+            }
+            w0 >>= 2 * c4;
+            w1 >>= 2 * c4;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t* x = r + 4 * (4 * b + q);
+              if (!(w0 >> (8 * q) & 1)) x[0] = kMasked;
+              if (!(w0 >> (8 * q) & 2)) x[1] = kMasked;
+              if (!(w1 >> (8 * q) & 1)) x[2] = kMasked;
+              if (!(w1 >> (8 * q) & 2)) x[3] = kMasked;
             }
           }
         }
-        auto mask = [&](int half) {
+        float t0, t1;                         // the rows' maxima
+        {
+          float a0 = __uint_as_float(r[0]), a1 = __uint_as_float(r[1]);
+          float b0 = __uint_as_float(r[2]), b1 = __uint_as_float(r[3]);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            if (!(word[2 * half] >> e & 1)) x[e] = 0xff800000u;
-            if (!(word[2 * half + 1] >> e & 1)) x[32 + e] = 0xff800000u;
+          for (int q = 1; q < 15; q += 2) {
+            a0 = max3(a0, __uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 4]));
+            a1 = max3(a1, __uint_as_float(r[4 * q + 1]), __uint_as_float(r[4 * q + 5]));
+            b0 = max3(b0, __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 6]));
+            b1 = max3(b1, __uint_as_float(r[4 * q + 3]), __uint_as_float(r[4 * q + 7]));
           }
-        };
-        auto top = [&](float m0) {
-          float m1 = __uint_as_float(x[0]), m2 = __uint_as_float(x[1]), m3 = __uint_as_float(x[2]);
-#pragma unroll
-          for (int e = 3; e < 63; e += 6) {
-            m1 = max3(m1, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-            m2 = max3(m2, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
-            m3 = max3(m3, __uint_as_float(x[e + 4]), __uint_as_float(x[e + 5]));
-          }
-          return max3(max3(m0, m1, m2), m3, __uint_as_float(x[63]));
-        };
-        load(1);
-        if (masked) mask(1);
-        float m = top(-INFINITY);
-        load(0);
-        if (masked) mask(0);
-        m = top(m);
-        const float ms = m * scale;
-        float mn = mu;
-        bool rescale = false;
-        if (first) {
-          mn = ms;
-          mr = m;
-        } else if (ms > mu + kRescaleThreshold) {
-          mn = ms;
-          mr = m;
-          rescale = true;
+          t0 = max3(a0, a1, fmaxf(__uint_as_float(r[60]), __uint_as_float(r[61])));
+          t1 = max3(b0, b1, fmaxf(__uint_as_float(r[62]), __uint_as_float(r[63])));
+          t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
+          t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
+          t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
+          t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
         }
-        const float al = rescale ? ex2(mu - mn) : 1.f;
-        // (a row whose every score so far is -infinity has weights of 0, not 2^(-inf + inf))
-        const float ref = mn == -INFINITY ? 0.f : mn;
-        // scores so large that the rounding of their maximum's product would show:
-        // their difference is taken first
-        const bool far = __any_sync(0xffffffffu, fabsf(ref) > 1048576.f);
-        const uint64_t ng = far ? 0ull : pack2(-ref, -ref);
-        auto nearer = [&] {
-          const float mf = mr == -INFINITY ? 0.f : mr;
-#pragma unroll
-          for (int e = 0; e < 64; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) - mf);
-        };
-        uint64_t s0 = 0, s1 = 0;
-        auto weights = [&](int half) {            // and their place: over scores that are read
-#pragma unroll
-          for (int e = 0; e < 64; e += 4) {
-            const float2 y = unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), sc2, ng));
-            const float2 z = unpack2(fma2(pack2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), sc2, ng));
-            const float e0 = ex2(y.x), e1 = ex2(y.y), e2 = ex2(z.x), e3 = ex2(z.y);
-            s0 = add2(s0, pack2(e0, e1));
-            s1 = add2(s1, pack2(e2, e3));
-            x[e / 2] = pack_bf16x2(e0, e1);
-            x[e / 2 + 1] = pack_bf16x2(e2, e3);
+        float al0 = 1.f, al1 = 1.f;
+        bool rescale = false;
+        if (k < 2) {                          // the stream's first step
+          m0 = t0;
+          m1 = t1;
+        } else {
+          const float s0 = m0 * scale, s1 = m1 * scale;
+          if (t0 * scale > s0 + kRescaleThreshold) {
+            al0 = ex2(s0 - t0 * scale);
+            m0 = t0;
+            rescale = true;
           }
-          tc::tmem_st_32x32b_x32(tS + 32 * half, *reinterpret_cast<uint32_t(*)[32]>(x));
-        };
-        if (far) nearer();
-        weights(0);
-        load(1);
-        if (masked) mask(1);
-        if (far) nearer();
-        weights(1);
-        // the accumulator's rows, by the whole warp when any of them needs it
-        // (the factor is 1 for the others), once the step before has been added
+          if (t1 * scale > s1 + kRescaleThreshold) {
+            al1 = ex2(s1 - t1 * scale);
+            m1 = t1;
+            rescale = true;
+          }
+        }
+        // (a row whose every score so far is -infinity has weights of 0, not 2^(-inf + inf))
+        float f0 = m0 == -INFINITY ? 0.f : m0, f1 = m1 == -INFINITY ? 0.f : m1;
+        // scores so large that the rounding of their reference's product would
+        // show: their difference is taken first
+        if (__any_sync(0xffffffffu, fmaxf(fabsf(f0), fabsf(f1)) * scale > 1048576.f)) {
+#pragma unroll
+          for (int q = 0; q < 64; ++q) r[q] = __float_as_uint(__uint_as_float(r[q]) - ((q & 2) ? f1 : f0));
+          f0 = f1 = 0.f;
+        }
+        const uint64_t ng0 = pack2(-f0 * scale, -f0 * scale), ng1 = pack2(-f1 * scale, -f1 * scale);
+        uint64_t acc0 = 0, acc1 = 0;          // (even keys, odd keys) of each row
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          const float2 x01 = unpack2(fma2(pack2(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1])), sc2, ng0));
+          const float2 x23 = unpack2(fma2(pack2(__uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3])), sc2, ng1));
+          const float e0 = ex2(x01.x), e1 = ex2(x01.y), e2 = ex2(x23.x), e3 = ex2(x23.y);
+          acc0 = add2(acc0, pack2(e0, e1));
+          acc1 = add2(acc1, pack2(e2, e3));
+          r[2 * q] = pack_bf16x2(e0, e1);
+          r[2 * q + 1] = pack_bf16x2(e2, e3);
+        }
+        tc::tmem_st_16x128b_x16(tS, *reinterpret_cast<uint32_t(*)[32]>(r));
+        // the accumulator's rows, by the whole warp when any of them needs it (the
+        // factor is 1 for the others), once the stream's step before has been added
         if (__any_sync(0xffffffffu, rescale)) {
           if (!wait32(&ctl->pv_done[w], c - 1, ctl, err, W_PV_DONE)) {
             ok = false;
             break;
           }
           tc::tc_fence_after();
+          const uint64_t g0 = pack2(al0, al0), g1 = pack2(al1, al1);
 #pragma unroll 1
-          for (int e0 = 0; e0 < D; e0 += 32) {
+          for (int e = 0; e < D; e += 64) {
             uint32_t o[32];
-            const uint32_t tO = tmem + lane_off + kColO + w * D + e0;
-            tc::tmem_ld_32x32b_x32(tO, o);
+            const uint32_t tO = tmem + ((uint32_t)base << 16) + kColO + w * D + e;
+            tc::tmem_ld_16x256b_x8(tO, o);
             tc::tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-            tc::tmem_st_32x32b_x32(tO, o);
+            for (int q = 0; q < 32; q += 2) {
+              const float2 y = unpack2(mul2(pack2(__uint_as_float(o[q]), __uint_as_float(o[q + 1])), (q & 2) ? g1 : g0));
+              o[q] = __float_as_uint(y.x);
+              o[q + 1] = __float_as_uint(y.y);
+            }
+            tc::tmem_st_16x256b_x8(tO, o);
           }
         }
         tc::tmem_st_wait();
         tc::tc_fence_before();
         tc::mbar_arrive(&ctl->p_full[w]);
-        const float2 t0 = unpack2(s0), t1 = unpack2(s1);
-        l = l * al + ((t0.x + t0.y) + (t1.x + t1.y));
-        mu = mn;
-        first = false;
+        const float2 y0 = unpack2(acc0), y1 = unpack2(acc1);
+        l0 = l0 * al0 + (y0.x + y0.y);
+        l1 = l1 * al1 + (y1.x + y1.y);
+        if (w)
+          ++c1;
+        else
+          ++c0;
+        // the other stream's turn
+        float z;
+        z = m0; m0 = n0; n0 = z;
+        z = m1; m1 = n1; n1 = z;
+        z = l0; l0 = k0; k0 = z;
+        z = l1; l1 = k1; k1 = z;
       }
       if (!ok) break;
-      // both streams are at their end: their rows' maxima and sums meet
-      if (!first && !wait32(&ctl->pv_done[w], c - 1, ctl, err, W_O_FULL)) break;
-      ctl->ml[w][r] = make_float2(mu, l);
+      // the rows' references and sums to shared memory, in a fixed order
+      if (u.n & 1) {
+        float z;
+        z = m0; m0 = n0; n0 = z;
+        z = m1; m1 = n1; n1 = z;
+        z = l0; l0 = k0; k0 = z;
+        z = l1; l1 = k1; k1 = z;
+      }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, o);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+        k0 += __shfl_xor_sync(0xffffffffu, k0, o);
+        k1 += __shfl_xor_sync(0xffffffffu, k1, o);
+      }
+      // (of the part before they have been read once its accumulators have)
+      if (parts > 0 && !wait32(&ctl->o_empty, parts - 1, ctl, err, W_O_EMPTY)) break;
+      if (c4 == 0) {
+        ctl->ml[0][R0] = make_float2(m0 * scale, l0);
+        ctl->ml[0][R1] = make_float2(m1 * scale, l1);
+        ctl->ml[1][R0] = make_float2(n0 * scale, k0);
+        ctl->ml[1][R1] = make_float2(n1 * scale, k1);
+      }
       tc::mbar_arrive(&ctl->x_full);
       if (!wait32(&ctl->x_full, parts, ctl, err, W_X_FULL)) break;
+      if (!wait32(&ctl->pv_done[0], c0 - 1, ctl, err, W_O_FULL)) break;
+      if (u.n > 1 && !wait32(&ctl->pv_done[1], c1 - 1, ctl, err, W_O_FULL)) break;
       tc::tc_fence_after();
-      // one M tile: the streams' sums are added, each warpgroup takes half of the columns
-      const float2 other = u.dual ? make_float2(-INFINITY, 0.f) : ctl->ml[1 - w][r];
-      const bool two = !u.dual && u.n > 1;
-      const float M = fmaxf(mu, other.x), ref = M == -INFINITY ? 0.f : M;
-      const float fo = two ? ex2(other.x - ref) : 0.f, fm = two ? ex2(mu - ref) : 1.f;
-      const float sum = two ? l * fm + other.y * fo : u.dual || !first ? l : other.y;
-      const float f0 = u.dual || w == 0 ? fm : fo, f1 = w == 0 ? fo : fm;     // of O[0] (own O), O[1]
+      // outputs: a thread one M row and half of its columns
+      const int row = quarter * 32 + lane;
       const bool whole = p.j0 == 0 && p.j1 == p.nt;
-      const float inv = whole ? 1.f / sum : 1.f;
-      unsigned long long fix = 0;
+      const bool two = !u.dual && u.n > 1;    // one M tile: the streams' sums are added
+      const int64_t slot = ((int64_t)blockIdx.x * 2 + (p.j0 == 0 ? 1 : 0)) * kTreeTcVecs;
+      unsigned long long found = 0;
       if (news) {
-        fix = *(volatile unsigned long long*)&ctl->fix[with_new % kFix] & seen;
+        found = *(volatile unsigned long long*)&ctl->fix[with_new % kFix];
         ++with_new;
       }
-      const bool valid = v < p.n_vec;
-      const int e_begin = u.dual ? 0 : w * (D / 2), e_end = u.dual ? D : e_begin + D / 2;
-      const uint32_t tO = tmem + lane_off + kColO + (u.dual ? w * D : 0);
-      const int64_t slot = ((int64_t)blockIdx.x * 2 + (p.j0 == 0 ? 1 : 0)) * kTreeTcVecs + v;
-      __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.O) +
-                           ((int64_t)(p.q.row0 + node) * a.n_q_heads + p.h * a.g + (vi & (a.g - 1))) * D;
-#pragma unroll 1
-      for (int e0 = e_begin; e0 < e_end; e0 += 32) {
-        uint32_t o[32];
-        tc::tmem_ld_32x32b_x32(tO + e0, o);
+      for (int mt = 0; mt < (u.dual ? 2 : 1); ++mt) {
+        const int v = mt * 128 + row;
+        const bool valid = v < p.n_vec;
+        const int vi = p.vg * a.vecs + min(v, p.n_vec - 1), node = vi >> a.g_log2;
+        const float2 x = ctl->ml[mt][row];
+        float M = x.x, sum = x.y, f0 = 1.f, f1 = 0.f;
         if (two) {
-          uint32_t o1[32];
-          tc::tmem_ld_32x32b_x32(tO + D + e0, o1);
-          tc::tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            o[e] = __float_as_uint(fmaf(__uint_as_float(o[e]), f0, __uint_as_float(o1[e]) * f1));
-        } else {
-          tc::tmem_ld_wait();
+          const float2 y = ctl->ml[1][row];
+          M = fmaxf(x.x, y.x);
+          const float ref = M == -INFINITY ? 0.f : M;
+          f0 = ex2(x.x - ref);
+          f1 = ex2(y.x - ref);
+          sum = f0 * x.y + f1 * y.y;
         }
-        if (fix) {                            // rare: elements that are not finite, of new tokens that this row sees
+        const unsigned long long fix = found ? found & seen_by(all, node) : 0;
+        const float inv = 1.f / sum;
+        __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.O) +
+                             ((int64_t)(p.q.row0 + node) * a.n_q_heads + p.h * a.g + (vi & (a.g - 1))) * D;
+        const uint32_t tO = tmem + ((uint32_t)(quarter * 32) << 16) + kColO + mt * D;
 #pragma unroll 1
-          for (unsigned long long left = fix; left; left &= left - 1) {
-            const int64_t row = pool_row(a.seq, p.s, p.q.len + __ffsll(left) - 1);
-            if (row < 0) continue;
-            const __nv_bfloat16* vr =
-                reinterpret_cast<const __nv_bfloat16*>(a.v_pool) + (row * a.n_kv_heads + p.h) * D + e0;
+        for (int e0 = half * (D / 2); e0 < (half + 1) * (D / 2); e0 += 32) {
+          uint32_t o[32];
+          tc::tmem_ld_32x32b_x32(tO + e0, o);
+          if (two) {
+            uint32_t o1[32];
+            tc::tmem_ld_32x32b_x32(tO + D + e0, o1);
+            tc::tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float y = __bfloat162float(vr[e]);
-              if (!isfinite(y)) o[e] = __float_as_uint(__uint_as_float(o[e]) + y);
+            for (int e = 0; e < 32; ++e)
+              o[e] = __float_as_uint(fmaf(__uint_as_float(o[e]), f0, __uint_as_float(o1[e]) * f1));
+          } else {
+            tc::tmem_ld_wait();
+          }
+          if (fix) {                          // rare: elements that are not finite, of new tokens that this row sees
+#pragma unroll 1
+            for (unsigned long long left = fix; left; left &= left - 1) {
+              const int64_t vrow = pool_row(a.seq, p.s, p.q.len + __ffsll(left) - 1);
+              if (vrow < 0) continue;
+              const __nv_bfloat16* vr =
+                  reinterpret_cast<const __nv_bfloat16*>(a.v_pool) + (vrow * a.n_kv_heads + p.h) * D + e0;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float y = __bfloat162float(vr[e]);
+                if (!isfinite(y)) o[e] = __float_as_uint(__uint_as_float(o[e]) + y);
+              }
             }
           }
-        }
-        if (e0 + 32 == e_end) {               // read: the next part's first products may start
-          tc::tc_fence_before();
-          tc::mbar_arrive(&ctl->o_empty);
-        }
-        if (valid && whole) {
+          if (valid && whole) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t y[4];
+            for (int q = 0; q < 4; ++q) {
+              uint32_t y[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              y[e] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * e]) * inv, __uint_as_float(o[8 * q + 2 * e + 1]) * inv);
-            *reinterpret_cast<uint4*>(out + e0 + 8 * q) = make_uint4(y[0], y[1], y[2], y[3]);
+              for (int e = 0; e < 4; ++e)
+                y[e] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * e]) * inv, __uint_as_float(o[8 * q + 2 * e + 1]) * inv);
+              *reinterpret_cast<uint4*>(out + e0 + 8 * q) = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+          } else if (valid) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              *reinterpret_cast<uint4*>(a.part_o + (slot + v) * D + e0 + 4 * q) =
+                  make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
           }
-        } else if (valid) {
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            *reinterpret_cast<uint4*>(a.part_o + slot * D + e0 + 4 * q) =
-                make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          __syncwarp();
         }
-        __syncwarp();
+        if (valid && !whole && half == 0) a.part_ml[slot + v] = make_float2(M, sum);
       }
-      if (valid && !whole && (u.dual || w == 0)) a.part_ml[slot] = make_float2(M, sum);
+      tc::tc_fence_before();
+      tc::mbar_arrive(&ctl->o_empty);         // read: the next part's first products may start
       ++parts;
     }
   }
