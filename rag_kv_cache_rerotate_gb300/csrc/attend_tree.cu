@@ -20,6 +20,7 @@ constexpr int kWarps = 4;                 // workers of a CTA
 constexpr int kVecs = 8;                  // query vectors of a unit
 constexpr int kTile = 32;                 // keys of a tile: one a lane
 constexpr int kAtOnce = 8;                // keys whose values it reads at a time
+static_assert(kVecs == 1 << 3 && kTile == 1 << 5 && kTreeTcVecs == 1 << 8 && kTreeTcTile == 1 << 7, "logarithms");
 
 // A warp's units, 32 keys at a time: a lane per key for the scores, then a lane
 // per D / 32 channels for the sums.
@@ -32,15 +33,8 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const __grid_con
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   pdl_wait();
   pdl_trigger();
-  const int64_t total = count_tiles<kWarps * 32>(a, s_warp);
-  const int64_t per = per_worker(a, total);
   const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
-  const int64_t begin = w * per, end = min(total, begin + per);
-  if (begin >= end) return;
-  TreeWalk walk;
-  walk.at = find_tile(a, begin);
-  walk.t = begin;
-  walk.end = end;
+  TreeWalk walk = start_walk<kWarps * 32>(a, w, s_warp);
   TreePart at;
   while (next_part(a, walk, at)) {
     const int h = at.h, vg = at.vg, n_vec = at.n_vec;
@@ -178,10 +172,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid
   if (s < 0 || s >= a.seq.n_seq) return;
   Seq q;
   if (!seq_of(a.seq, s, &q) || row < q.row0 || row >= q.row0 + q.n) return;
-  const int nt = tiles_of(a, q), groups = units_of(a, q) / a.n_kv_heads;
+  const int nt = tiles_of(a, q), groups = (q.n * a.g + a.vecs - 1) >> a.vecs_log2;
   const int per_vec = kJoinWarps >> a.g_log2;
   const int j = warp / per_vec, share = warp % per_vec;
-  const int vi = (row - q.row0) * a.g + j, vg = vi / a.vecs, v = vi % a.vecs;
+  const int vi = (row - q.row0) * a.g + j, vg = vi >> a.vecs_log2, v = vi & (a.vecs - 1);
   pdl_wait();
   const int64_t per = per_worker(a, a.start[a.seq.n_seq]);
   const int64_t u0 = a.start[s] + (int64_t)(h * groups + vg) * nt;
@@ -327,7 +321,9 @@ fuse_status_t fuse_attend_tree(const fuse_layer_desc_t* desc, const fuse_seqs_t*
   a.g = desc->n_q_heads / desc->n_kv_heads;
   a.g_log2 = a.g == 8 ? 3 : a.g == 4 ? 2 : a.g == 2 ? 1 : 0;
   a.vecs = P.vecs;
+  a.vecs_log2 = desc->dtype == FUSE_BF16 ? 8 : 3;
   a.tile = P.tile;
+  a.tile_log2 = desc->dtype == FUSE_BF16 ? 7 : 5;
   a.workers = P.workers;
   a.scale = 1.4426950408889634f / std::sqrt((float)desc->head_dim);
   a.start = reinterpret_cast<int64_t*>(at(P.start));

@@ -25,8 +25,8 @@ struct TreeArgs {
   void* O;
   int n_q_heads, n_kv_heads, g;           // g = n_q_heads / n_kv_heads
   int g_log2;
-  int vecs;                               // query vectors of a unit
-  int tile;                               // keys of a tile
+  int vecs, vecs_log2;                    // query vectors of a unit
+  int tile, tile_log2;                    // keys of a tile
   int workers;
   float scale;                            // log2(e) / sqrt(d)
   int64_t* start;                         // [n_seq + 1]: tiles in front of each sequence (for the join)
@@ -40,80 +40,92 @@ struct TreePlan {
 };
 
 __device__ __forceinline__ int units_of(const TreeArgs& a, const Seq& q) {
-  return a.n_kv_heads * ((q.n * a.g + a.vecs - 1) / a.vecs);
+  return a.n_kv_heads * ((q.n * a.g + a.vecs - 1) >> a.vecs_log2);
 }
 __device__ __forceinline__ int tiles_of(const TreeArgs& a, const Seq& q) {
-  return q.n == 0 ? 0 : (q.len + q.n + a.tile - 1) / a.tile;
+  return q.n == 0 ? 0 : (int)(((uint32_t)q.len + q.n + a.tile - 1) >> a.tile_log2);
 }
 __device__ __forceinline__ int64_t per_worker(const TreeArgs& a, int64_t tiles) {
-  return max((int64_t)1, (tiles + a.workers - 1) / a.workers);
+  // (divisions of 64 bits take a few hundred cycles)
+  if (tiles <= UINT32_MAX / 2) return max(1u, ((uint32_t)tiles + a.workers - 1) / (uint32_t)a.workers);
+  return (tiles + a.workers - 1) / a.workers;
 }
 
-// Where a worker stands.
-struct TreeAt {
+// Where a worker stands, and the end of its tiles.
+struct TreeWalk {
   int s;                                  // sequence
-  int64_t first;                          // its first tile
   Seq q;
+  int64_t first;                          // its first tile
+  int64_t t, end;                         // the worker's next tile, and its last one's next
 };
 
-// The tiles of all sequences, and each sequence's first one (written to a.start
-// by block 0 of the grid, for the join): by a whole block.  s_warp: 33 words.
-template <int kThreads>
-__device__ __forceinline__ int64_t count_tiles(const TreeArgs& a, int64_t* s_warp) {
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  constexpr int kWarps = kThreads / 32;
-  const bool keep = blockIdx.x == 0;
-  int64_t total = 0;
-  for (int s0 = 0; s0 < a.seq.n_seq; s0 += kThreads) {
-    Seq q{0, 0, 0};
-    if (s0 + tid < a.seq.n_seq) seq_of(a.seq, s0 + tid, &q);
-    const int64_t own = (int64_t)units_of(a, q) * tiles_of(a, q);
-    int64_t inc = own;
+// 32 sequences from s0 on, one a lane: their tiles, and those up to and with each.
+__device__ __forceinline__ int64_t scan_tiles(const TreeArgs& a, int s0, Seq* q, int64_t* inc) {
+  const int lane = threadIdx.x % 32;
+  *q = Seq{0, 0, 0};
+  if (s0 + lane < a.seq.n_seq) seq_of(a.seq, s0 + lane, q);
+  const int64_t own = (int64_t)units_of(a, *q) * tiles_of(a, *q);
+  *inc = own;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t z = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += z;
-    }
-    if (lane == 31) s_warp[warp] = inc;
-    __syncthreads();
-    int64_t before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += s_warp[w];
-      all += s_warp[w];
-    }
-    if (keep && s0 + tid < a.seq.n_seq) a.start[s0 + tid] = total + before + inc - own;
-    total += all;
-    __syncthreads();
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t z = __shfl_up_sync(0xffffffffu, *inc, o);
+    if (lane >= o) *inc += z;
   }
-  if (keep && tid == 0) a.start[a.seq.n_seq] = total;
-  return total;
+  return own;
 }
 
-// The sequence that tile t lies in (by a whole warp).
-__device__ __forceinline__ TreeAt find_tile(const TreeArgs& a, int64_t t) {
-  const int lane = threadIdx.x % 32;
-  TreeAt r{a.seq.n_seq, 0, {0, 0, 0}};
+// The walk of worker w, found by its warp (all threads of a block call this);
+// block 0 also writes each sequence's first tile, for the join.  s_warp: a word per
+// warp.  Up to 32 sequences need one look at them; more are counted by the block
+// first and then passed over once again.
+template <int kThreads>
+__device__ __forceinline__ TreeWalk start_walk(const TreeArgs& a, int64_t w, int64_t* s_warp) {
+  constexpr int kWarps = kThreads / 32;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  TreeWalk r{a.seq.n_seq, {0, 0, 0}, 0, 0, 0};
+  Seq q;
+  int64_t inc, own = 0, total = 0;
+  const bool one = a.seq.n_seq <= 32;
+  if (one) {
+    own = scan_tiles(a, 0, &q, &inc);
+    total = __shfl_sync(0xffffffffu, inc, 31);
+    if (blockIdx.x == 0 && warp == 0) {
+      if (lane < a.seq.n_seq) a.start[lane] = inc - own;
+      if (lane == 0) a.start[a.seq.n_seq] = total;
+    }
+  } else {
+    for (int s0 = 0; s0 < a.seq.n_seq; s0 += kThreads) {
+      own = scan_tiles(a, s0 + warp * 32, &q, &inc);
+      if (lane == 31) s_warp[warp] = inc;
+      __syncthreads();
+      int64_t before = 0, all = 0;
+      for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) before += s_warp[i];
+        all += s_warp[i];
+      }
+      const int s = s0 + threadIdx.x;
+      if (blockIdx.x == 0 && s < a.seq.n_seq) a.start[s] = total + before + inc - own;
+      total += all;
+      __syncthreads();
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.start[a.seq.n_seq] = total;
+  }
+  const int64_t per = per_worker(a, total);
+  r.t = min(total, w * per);
+  r.end = min(total, r.t + per);
+  if (r.t == r.end) return r;
   int64_t before = 0;
   for (int s0 = 0; s0 < a.seq.n_seq; s0 += 32) {
-    Seq q{0, 0, 0};
-    if (s0 + lane < a.seq.n_seq) seq_of(a.seq, s0 + lane, &q);
-    const int64_t own = (int64_t)units_of(a, q) * tiles_of(a, q);
-    int64_t inc = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t z = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += z;
-    }
-    const unsigned past = __ballot_sync(0xffffffffu, before + inc > t);
+    if (!one) own = scan_tiles(a, s0, &q, &inc);
+    const unsigned past = __ballot_sync(0xffffffffu, before + inc > r.t);
     if (past) {
-      const int w = __ffs(past) - 1;
-      r.s = s0 + w;
-      r.first = before + __shfl_sync(0xffffffffu, inc - own, w);
-      r.q.row0 = __shfl_sync(0xffffffffu, q.row0, w);
-      r.q.n = __shfl_sync(0xffffffffu, q.n, w);
-      r.q.len = __shfl_sync(0xffffffffu, q.len, w);
-      return r;
+      const int k = __ffs(past) - 1;
+      r.s = s0 + k;
+      r.first = before + __shfl_sync(0xffffffffu, inc - own, k);
+      r.q.row0 = __shfl_sync(0xffffffffu, q.row0, k);
+      r.q.n = __shfl_sync(0xffffffffu, q.n, k);
+      r.q.len = __shfl_sync(0xffffffffu, q.len, k);
+      break;
     }
     before += __shfl_sync(0xffffffffu, inc, 31);
   }
@@ -161,11 +173,7 @@ __device__ __forceinline__ uint64_t seen_by(const Seen& s, int node) {
   return node < 32 ? lo : hi;
 }
 
-// A worker's way through its tiles, unit by unit.
-struct TreeWalk {
-  TreeAt at;
-  int64_t t, end;
-};
+// A worker's share of a unit.
 struct TreePart {
   int s;
   Seq q;
@@ -175,19 +183,19 @@ struct TreePart {
 };
 __device__ __forceinline__ bool next_part(const TreeArgs& a, TreeWalk& w, TreePart& p) {
   while (w.t < w.end) {
-    const int nt = tiles_of(a, w.at.q), units = units_of(a, w.at.q);
-    const int64_t rel = w.t - w.at.first, all = (int64_t)units * nt;
+    const int nt = tiles_of(a, w.q), units = units_of(a, w.q);
+    const int64_t rel = w.t - w.first, all = (int64_t)units * nt;
     if (rel >= all) {                     // the next sequence
-      w.at.first += all;
-      if (++w.at.s >= a.seq.n_seq) return false;
-      seq_of(a.seq, w.at.s, &w.at.q);
+      w.first += all;
+      if (++w.s >= a.seq.n_seq) return false;
+      seq_of(a.seq, w.s, &w.q);
       continue;
     }
-    const int groups = units / a.n_kv_heads;
+    const int groups = (w.q.n * a.g + a.vecs - 1) >> a.vecs_log2;
     const int unit = rel >> 32 ? (int)(rel / nt) : (int)((uint32_t)rel / (uint32_t)nt);
-    p.s = w.at.s;
-    p.q = w.at.q;
-    p.h = unit / groups;
+    p.s = w.s;
+    p.q = w.q;
+    p.h = groups == 1 ? unit : (int)((uint32_t)unit / (uint32_t)groups);
     p.vg = unit - p.h * groups;
     p.n_vec = min(a.vecs, p.q.n * a.g - p.vg * a.vecs);
     p.nt = nt;

@@ -14,16 +14,21 @@
 // The running maximum m is raised only when a tile exceeds it by more than
 // 2^16 (then O and the running sum are rescaled).
 //
-// Keys and values lie in pages of any size, so their rows are gathered by
-// 16-byte cp.async, rows that are not there as zeros, in the 128-byte swizzle that the
-// MMAs read.  A row's copies count on the tile's mbarrier when they land; the
-// thread that issues the MMAs fences the generic proxy's writes.
+// Keys and values lie in pages.  With pages of a multiple of 8 tokens a tile is
+// copied by TMA boxes of as many rows as always lie in one page; what lies
+// behind a sequence's last slot in its page comes along and is masked, its values
+// cleared.  With other pages the rows are gathered four at a time, and a group that is
+// not whole (the sequence's end, a page outside the pool) is copied by a lane
+// itself.  (Gathering by 16-byte cp.async, four warps, kept the load/store path so
+// busy that the softmax's shuffles waited: 550 us instead of @@ on 8 trees of 64 over 33k.)
 //
 // What a row does not see must not reach it: its scores are replaced where they
 // are masked, and as 0 * V is not 0 for an infinite or NaN V, one warp looks
 // the new tokens' values through before their product, clears what is not
 // finite, and the rows that do see such an element get it back at the end.
 // (Held tokens are seen by every row.)
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 
 #include "attend_tree.h"
@@ -32,15 +37,19 @@
 
 namespace fusekv {
 
+bool make_map_3d(CUtensorMap* m, const void* base, const uint64_t dims[3], const uint64_t strides[2],
+                 const uint32_t box[3]);
+bool make_map_gather(CUtensorMap* m, const void* base, int64_t rows, int64_t cols);
+
 namespace {
 
 constexpr int kKB = kTreeTcTile;              // keys per tile
 constexpr int kHalf = 128 * 64 * 2;           // 64 columns of a 128-row tile (16 KB)
-constexpr int kWarpLoad = 8, kLoadWarps = 4, kWarpS = 12, kWarpPV = 13, kWarpLook = 14;
-constexpr int kThreads = 15 * 32;
-constexpr int kLoadThreads = kLoadWarps * 32;
+constexpr int kWarpLoad = 8, kWarpS = 9, kWarpPV = 10, kWarpLook = 11;
+constexpr int kThreads = 12 * 32;
 constexpr int kTmemCols = 512;                // S of both streams | O of both
 constexpr float kRescaleThreshold = 16.0f;    // P and its sum keep their relative precision up to 2^16 over m
+constexpr float kFar = 1048576.f;             // of a score in log2 units: 2^-4 is its last place
 constexpr int kMaxStages = 10;
 constexpr int kFix = 8;                       // parts with new tokens that the look may be ahead by, and more
 
@@ -52,7 +61,7 @@ template <int D> struct Ring {
 struct Ctl {
   uint64_t q_full[2], q_empty[2];
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t look_full[kMaxStages], look_ok[kMaxStages];   // value tiles with new tokens, by ring slot
+  uint64_t look_full[kMaxStages];             // value tiles that are looked through first, by ring slot
   uint64_t s_full[2], p_full[2], pv_done[2];             // by stream
   uint64_t x_full, o_empty;
   unsigned long long fix[kFix];               // new tokens with values that are not finite
@@ -70,7 +79,7 @@ static_assert(smem_bytes<128>() <= 227 * 1024 && smem_bytes<64>() <= 227 * 1024,
 
 // Which wait gave up: info = wait id << 16 | CTA.
 enum TreeWait : uint32_t {
-  W_Q_EMPTY = 1, W_EMPTY, W_Q_FULL, W_S_FREE, W_K_FULL, W_P_FULL, W_V_FULL, W_LOOK_OK, W_O_EMPTY, W_LOOK_FULL,
+  W_Q_EMPTY = 1, W_EMPTY, W_Q_FULL, W_S_FREE, W_K_FULL, W_P_FULL, W_V_FULL, W_O_EMPTY, W_LOOK_FULL,
   W_S_FULL, W_PV_DONE, W_O_FULL, W_X_FULL
 };
 
@@ -147,15 +156,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-// Arrives on the barrier, whose count provides for it, once this thread's copies so far have landed.
-__device__ __forceinline__ void cp_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
-}
-
 // K-step kk (16 columns) of a 128-row K-major tile stored in 64-column halves.
 __device__ __forceinline__ uint64_t kmajor_step(uint32_t tile, int kk) {
   return tc::smem_desc_k128(tile + (kk >> 2) * kHalf + (kk & 3) * 32);
@@ -170,6 +170,27 @@ __device__ __forceinline__ uint32_t drop_nonfinite(uint32_t w) {
   return w;
 }
 
+// Out of line, as six roles call it once per part.
+__device__ __noinline__ bool next_of(const TreeArgs& a, TreeWalk& w, TreePart& p) { return next_part(a, w, p); }
+
+// Adds to a row of outputs (or of a part) the elements that are not finite of the values
+// of the new tokens in `left`: with them a sum is infinite or NaN whatever it was.
+template <typename T>
+__device__ __noinline__ void add_nonfinite(T* dst, int n, unsigned long long left, const TreeArgs& a, const TreePart& p,
+                                           int e0, int d) {
+#pragma unroll 1
+  for (; left; left &= left - 1) {
+    const int64_t row = pool_row(a.seq, p.s, p.q.len + __ffsll(left) - 1);
+    if (row < 0) continue;
+    const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(a.v_pool) + (row * a.n_kv_heads + p.h) * d + e0;
+#pragma unroll 1
+    for (int e = 0; e < n; ++e) {
+      const float x = __bfloat162float(v[e]);
+      if (!isfinite(x)) dst[e] = (T)((float)dst[e] + x);
+    }
+  }
+}
+
 // What every role derives from a part.
 struct Steps {
   bool dual;                                  // two M tiles
@@ -180,12 +201,9 @@ struct Steps {
     n = dual ? 2 * tiles : tiles;
   }
   __device__ __forceinline__ int tile(int k) const { return dual ? k >> 1 : k; }
-  // Ring items in the order in which the products take them:
-  // K0 V0 K1 V1 .. for two M tiles, K0 K1 V0 K2 V1 .. for one.
-  __device__ __forceinline__ int k_item(int i) const { return dual || i == 0 ? 2 * i : 2 * i - 1; }
-  __device__ __forceinline__ int v_item(int i) const {
-    return dual ? 2 * i + 1 : i < tiles - 1 ? 2 * i + 2 : 2 * tiles - 1;
-  }
+  // Ring items, keys a tile ahead of values: K0 K1 V0 K2 V1 ..
+  __device__ __forceinline__ int k_item(int i) const { return i == 0 ? 0 : 2 * i - 1; }
+  __device__ __forceinline__ int v_item(int i) const { return i < tiles - 1 ? 2 * i + 2 : 2 * tiles - 1; }
 };
 // Whether the keys of tile j go past the held tokens.
 __device__ __forceinline__ bool has_new(const TreePart& p, int j) { return (j + 1) * kKB > p.q.len; }
@@ -197,8 +215,11 @@ __device__ __forceinline__ uint32_t seen_word(uint64_t seen, int rel) {
   return rel < 64 ? (uint32_t)(seen >> rel) : 0u;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_constant__ TreeArgs a) {
+// kGather: pages that are not multiples of 8 tokens; else box rows of them are copied at a time.
+template <int D, bool kGather>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
+                   const __grid_constant__ CUtensorMap mapV, const __grid_constant__ TreeArgs a, const int box) {
   constexpr int kTile = Ring<D>::tile, kSt = Ring<D>::stages;
   constexpr int kColO = 2 * kKB;
   static_assert(kColO + 2 * D <= kTmemCols, "tensor memory");
@@ -211,23 +232,25 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&ctl->q_full[i], kLoadThreads);
+      tc::mbar_init(&ctl->q_full[i], 1);
       tc::mbar_init(&ctl->q_empty[i], 1);
       tc::mbar_init(&ctl->s_full[i], 1);
       tc::mbar_init(&ctl->p_full[i], 256);
       tc::mbar_init(&ctl->pv_done[i], 1);
     }
     for (int i = 0; i < kSt; ++i) {
-      tc::mbar_init(&ctl->full[i], kLoadThreads);
+      tc::mbar_init(&ctl->full[i], 1);
       tc::mbar_init(&ctl->empty[i], 1);
-      tc::mbar_init(&ctl->look_full[i], kLoadThreads);
-      tc::mbar_init(&ctl->look_ok[i], 1);
+      tc::mbar_init(&ctl->look_full[i], 1);
     }
     tc::mbar_init(&ctl->x_full, 256);
     tc::mbar_init(&ctl->o_empty, 256);
     ctl->abort_flag = 0;
     ctl->bad_page = 0;
     tc::fence_barrier_init();
+    tc::tma_prefetch_desc(&mapQ);
+    tc::tma_prefetch_desc(&mapK);
+    tc::tma_prefetch_desc(&mapV);
   }
   if (warp == kWarpS) tc::tmem_alloc(&ctl->tmem_base, kTmemCols);
   tc::tc_fence_before();
@@ -236,70 +259,101 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
   const uint32_t tmem = ctl->tmem_base;
   pdl_wait();
   pdl_trigger();
-  const int64_t total = count_tiles<kThreads>(a, ctl->s_warp);
-  const int64_t per = per_worker(a, total);
-  TreeWalk walk;
-  walk.t = min(total, (int64_t)blockIdx.x * per);
-  walk.end = min(total, walk.t + per);
+  TreeWalk walk = start_walk<kThreads>(a, blockIdx.x, ctl->s_warp);
   const bool work = walk.t < walk.end;        // uniform
-  if (work) walk.at = find_tile(a, walk.t);
   TreePart p{};
 
   if (!work) {
-  } else if (warp >= kWarpLoad && warp < kWarpLoad + kLoadWarps) {
+  } else if (warp == kWarpLoad) {
     // -------------------------------- loads --------------------------------
-    // a warp takes 32 rows of every tile: a lane finds a row's place, then D / 8
-    // lanes copy a row
-    constexpr int kPieces = D / 8, kRows = 32 / kPieces;
-    const int row0 = (warp - kWarpLoad) * 32;
-    const int piece = lane % kPieces, sub = lane / kPieces;
+    // a lane copies one box, or gathers a group of four rows
     uint32_t it = 0, qn0 = 0, qn1 = 0;
     int qb = 0;
     bool ok = true;
-    const int64_t stride = (int64_t)a.n_kv_heads * D;
-    // the copies of 32 rows; row < 0: zeros
-    auto copy = [&](uint8_t* tile, const __nv_bfloat16* base, int64_t step, int64_t row) {
-      const uint32_t dst = tc::smem_u32(tile) + (piece >> 3) * kHalf;
+    constexpr int kG = kGather ? 4 : 1;       // pages that a lane looks up per tile
+    const int n_box = kGather ? 0 : kKB / box;
+    const int group = kGather ? lane : lane % n_box;
+    const int rows = kGather ? 4 : box;       // of a group
+    const bool mine = kGather || lane < n_box * (D / 64);
+    const int none = (int)(a.seq.n_pool_blocks * a.seq.block_size);       // a row outside the pool: reads as zeros
+    // the pages of this lane's rows of tile j (-2: no key there), and their first slot's place
+    auto entries = [&](int j, int (&page)[kG], int& in_page) {
+      const int key = j * kKB + group * rows, end = p.q.len + p.q.n;
+      const int32_t* table = a.seq.tables + (int64_t)p.s * a.seq.max_blocks;
+      int b = page_of(a.seq, key, &in_page), at = in_page;
 #pragma unroll
-      for (int i = 0; i < 32 / kRows; ++i) {
-        const int r = i * kRows + sub, m = row0 + r;
-        const int64_t x = __shfl_sync(0xffffffffu, row, r);
-        cp16(dst + m * 128 + (((piece & 7) ^ (m & 7)) << 4), base + max(x, (int64_t)0) * step + piece * 8, x >= 0);
+      for (int i = 0; i < kG; ++i) {
+        page[i] = mine && key + i < end ? table[b] : -2;
+        if (++at == a.seq.block_size) {
+          at = 0;
+          ++b;
+        }
       }
     };
-    auto entry = [&](int j) {                 // the page of this lane's key of tile j; -2: no key
-      const int key = j * kKB + row0 + lane;
-      return key < p.q.len + p.q.n ? a.seq.tables[(int64_t)p.s * a.seq.max_blocks + key / a.seq.block_size] : -2;
-    };
-    auto place = [&](int j, int page) -> int64_t {
-      if (page == -2) return -1;
-      if (page < 0 || page >= a.seq.n_pool_blocks) {
-        report_error(err, FUSE_ERR_DEVICE_BOUNDS, SITE_SEQ_PAGE, (uint32_t)page);
+    auto places = [&](const int (&page)[kG], int in_page, int (&row)[kG]) {
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < kG; ++i) {
+        int at = in_page + i;
+        if (kG > 1 && at >= a.seq.block_size) at %= a.seq.block_size;
+        const bool there = page[i] >= 0 && page[i] < a.seq.n_pool_blocks;
+        row[i] = there ? page[i] * a.seq.block_size + at : none;
+        bad |= !there && page[i] != -2;
+      }
+      if (bad) {
+        report_error(err, FUSE_ERR_DEVICE_BOUNDS, SITE_SEQ_PAGE, (uint32_t)p.s);
         ctl->bad_page = 1;
-        return -1;
       }
-      return (int64_t)page * a.seq.block_size + (j * kKB + row0 + lane) % a.seq.block_size;
     };
-    auto issue = [&](const void* pool, int64_t row, bool look) {
+    auto issue = [&](const CUtensorMap* map, const void* pool, const int (&row)[kG], bool look) {
       const int st = it % kSt;
-      if (!ok || !wait32(&ctl->empty[st], (it / kSt) ^ 1, ctl, err, W_EMPTY)) {
-        ok = false;
-        return;
+      if (!wait32(&ctl->empty[st], (it / kSt) ^ 1, ctl, err, W_EMPTY)) return false;
+      uint64_t* bar = look ? &ctl->look_full[st] : &ctl->full[st];
+      uint8_t* tile = sR + st * kTile;
+      uint32_t bytes = kTile;
+      bool whole = true;
+      if constexpr (kGather) {
+        // groups that are not whole: by the lane's own loads and stores
+        whole = row[0] != none && row[1] != none && row[2] != none && row[3] != none;
+        const unsigned self = __ballot_sync(0xffffffffu, !whole);
+        if (self) {
+          if (!whole) {
+#pragma unroll 1
+            for (int i = 0; i < 4 * (D / 8); ++i) {
+              const int m = i / (D / 8), c = i % (D / 8);
+              const int y = m == 0 ? row[0] : m == 1 ? row[1] : m == 2 ? row[2] : row[3];
+              uint4 x = make_uint4(0, 0, 0, 0);
+              if (y != none)
+                x = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(pool) +
+                                                    ((int64_t)y * a.n_kv_heads + p.h) * D + c * 8);
+              const int at = group * 4 + m;
+              *reinterpret_cast<uint4*>(tile + (c >> 3) * kHalf + at * 128 + (((c & 7) ^ (at & 7)) << 4)) = x;
+            }
+            tc::fence_proxy_async_smem();
+          }
+          bytes -= __popc(self) * 4 * D * 2;
+          __syncwarp();
+        }
       }
-      copy(sR + st * kTile, reinterpret_cast<const __nv_bfloat16*>(pool) + (int64_t)p.h * D, stride, row);
-      if (ctl->bad_page) {                    // the flag has to be seen by who sees the tile
-        cp_wait_all();
-        tc::mbar_arrive(&ctl->full[st]);
-        if (look) tc::mbar_arrive(&ctl->look_full[st]);
-      } else {
-        cp_arrive(&ctl->full[st]);
-        if (look) cp_arrive(&ctl->look_full[st]);
+      __syncwarp();                           // (bad_page is set before the barrier's phase can end)
+      if (lane == 0) tc::mbar_arrive_expect_tx(bar, bytes);
+      __syncwarp();
+      if constexpr (kGather) {
+        if (whole)
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            tc::tma_gather4(tile + h * kHalf + group * 512, map, bar, p.h * D + 64 * h, row[0], row[1], row[2], row[3]);
+      } else if (mine) {
+        const int h = lane / n_box;
+        tc::tma_load_3d(tile + h * kHalf + group * box * 128, map, bar, 64 * h, p.h, row[0]);
       }
       ++it;
+      return true;
     };
-    while (ok && next_part(a, walk, p)) {
+    while (ok && next_of(a, walk, p)) {
       const Steps u(p);
-      int page = entry(p.j0);
+      int page[kG], in_page = 0, rc[kG], rn[kG];       // rows of the values' tile, of the keys'
+      entries(p.j0, page, in_page);
       for (int m = 0; m < (u.dual ? 2 : 1); ++m) {
         const int b = u.dual ? m : qb;
         uint32_t& qn = b ? qn1 : qn0;
@@ -308,31 +362,34 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
           break;
         }
         ++qn;
-        const int v = m * 128 + row0 + lane, vi = p.vg * a.vecs + v;
-        const int64_t row = v < p.n_vec
-                                ? (int64_t)(p.q.row0 + (vi >> a.g_log2)) * a.n_q_heads + p.h * a.g + (vi & (a.g - 1))
-                                : -1;
-        copy(sQ + b * kTile, reinterpret_cast<const __nv_bfloat16*>(a.Q), D, row);
-        cp_arrive(&ctl->q_full[b]);
-      }
-      if (!ok) break;
-      if (!u.dual) qb ^= 1;
-      int64_t cur = place(p.j0, page), nxt = -1;
-      if (p.j0 + 1 < p.j1) page = entry(p.j0 + 1);
-      issue(a.k_pool, cur, false);
-      for (int j = p.j0; ok && j < p.j1; ++j) {
-        const bool more = j + 1 < p.j1;
-        if (more) {
-          nxt = place(j + 1, page);
-          if (j + 2 < p.j1) page = entry(j + 2);
+        if (lane == 0) {
+          // the rows of the next sequences come along: their products are not used
+          tc::mbar_arrive_expect_tx(&ctl->q_full[b], kTile);
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            tc::tma_load_3d(sQ + b * kTile + h * kHalf, &mapQ, &ctl->q_full[b], 64 * h, p.h * a.g,
+                            p.q.row0 + ((p.vg * a.vecs + m * 128) >> a.g_log2));
         }
-        if (more && !u.dual) issue(a.k_pool, nxt, false);
-        issue(a.v_pool, cur, has_new(p, j));
-        if (more && u.dual) issue(a.k_pool, nxt, false);
-        cur = nxt;
+      }
+      if (!u.dual) qb ^= 1;
+      for (int i = 0; ok && i <= u.tiles; ++i) {
+        if (i < u.tiles) {
+          places(page, in_page, rn);
+          if (i + 1 < u.tiles) entries(p.j0 + i + 1, page, in_page);
+          ok = issue(&mapK, a.k_pool, rn, false);
+        }
+        if (ok && i > 0) ok = issue(&mapV, a.v_pool, rc, has_new(p, p.j0 + i - 1));
+#pragma unroll
+        for (int k = 0; k < kG; ++k) rc[k] = rn[k];
       }
     }
-    cp_wait_all();
+    // copies in flight land before the CTA may end: all have been waited for where no
+    // wait gave up
+    if (!ok || ctl->abort_flag) {
+      for (uint32_t c = it > (uint32_t)kSt ? it - kSt : 0; c < it; ++c) {
+        tc::mbar_wait(&ctl->full[c % kSt], (c / kSt) & 1);
+      }
+    }
   } else if (warp == kWarpS) {
     // ------------------------------ S = Q K^T ------------------------------
     if (lane == 0) {
@@ -340,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
       uint32_t it = 0, c[2] = {0, 0}, qn0 = 0, qn1 = 0;
       int qb = 0;
       bool ok = true;
-      while (ok && next_part(a, walk, p)) {
+      while (ok && next_of(a, walk, p)) {
         const Steps u(p);
         if (u.dual || qb == 0) ok = wait1(&ctl->q_full[0], qn0++, ctl, err, W_Q_FULL);
         if (ok && (u.dual || qb == 1)) ok = wait1(&ctl->q_full[1], qn1++, ctl, err, W_Q_FULL);
@@ -359,7 +416,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
             ok = false;
             break;
           }
-          tc::fence_proxy_async_smem();
           tc::tc_fence_after();
           const uint32_t qa = tc::smem_u32(sQ + (u.dual ? w : qb) * kTile), ka = tc::smem_u32(sR + st * kTile);
 #pragma unroll
@@ -380,9 +436,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     // ------------------------------- O += P V -------------------------------
     if (lane == 0) {
       constexpr uint32_t idesc = tc::idesc_bf16_f32(128, D, /*b_mn_major=*/true);
-      uint32_t it = 0, c[2] = {0, 0}, parts = 0, look = 0;       // look: look_ok's next parity by slot
+      uint32_t it = 0, c[2] = {0, 0}, parts = 0;
       bool ok = true;
-      while (ok && next_part(a, walk, p)) {
+      while (ok && next_of(a, walk, p)) {
         const Steps u(p);
         for (int k = 0; k < u.n; ++k) {
           const int w = k & 1, i = u.tile(k);
@@ -390,14 +446,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
           const int st = q % kSt;
           // P first: the ring's earlier items have been full by then
           ok = wait1(&ctl->p_full[w], c[w], ctl, err, W_P_FULL) && wait1(&ctl->full[st], q / kSt, ctl, err, W_V_FULL);
-          if (ok && (!u.dual || w == 0) && has_new(p, p.j0 + i)) {
-            ok = wait1(&ctl->look_ok[st], look >> st, ctl, err, W_LOOK_OK);
-            look ^= 1u << st;
-          }
           // the accumulators were last read at the end of the part before
           if (ok && k == 0) ok = wait1(&ctl->o_empty, parts ^ 1, ctl, err, W_O_EMPTY);
           if (!ok) break;
-          tc::fence_proxy_async_smem();
           tc::tc_fence_after();
           const uint32_t va = tc::smem_u32(sR + st * kTile);
 #pragma unroll
@@ -418,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     constexpr int kPieces = D / 8, kRows = 32 / kPieces;
     uint32_t it = 0, look = 0, with_new = 0;
     bool ok = true;
-    while (ok && next_part(a, walk, p)) {
+    while (ok && next_of(a, walk, p)) {
       const Steps u(p);
       unsigned long long found = 0;
       bool any = false;
@@ -433,12 +484,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         }
         look ^= 1u << st;
         const int key0 = j * kKB;
+        // the new tokens' rows, and those behind them that a box brought along
         const int m0 = max(p.q.len - key0, 0), m1 = min(kKB, p.q.len + p.q.n - key0);
+        const int m2 = kGather ? m1 : (m1 + box - 1) / box * box;
         const int piece = lane % kPieces;
         bool changed = false;
-        for (int m = m0 + lane / kPieces; m < m1; m += kRows) {
+        for (int m = m0 + lane / kPieces; m < m2; m += kRows) {
           uint4* at = reinterpret_cast<uint4*>(sR + st * kTile + (piece >> 3) * kHalf + m * 128 +
                                                (((piece & 7) ^ (m & 7)) << 4));
+          if (m >= m1) {
+            *at = make_uint4(0, 0, 0, 0);
+            changed = true;
+            continue;
+          }
           uint4 x = *at;
           if (nonfinite2(x.x) || nonfinite2(x.y) || nonfinite2(x.z) || nonfinite2(x.w)) {
             x.x = drop_nonfinite(x.x);
@@ -450,13 +508,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
             changed = true;
           }
         }
-        if (__any_sync(0xffffffffu, changed)) tc::fence_proxy_async_smem();
+        if (changed) tc::fence_proxy_async_smem();
         found = (unsigned long long)__reduce_or_sync(0xffffffffu, (uint32_t)(found >> 32)) << 32 |
                 __reduce_or_sync(0xffffffffu, (uint32_t)found);
         __syncwarp();
         if (lane == 0) {
           ctl->fix[with_new % kFix] = found;
-          tc::mbar_arrive(&ctl->look_ok[st]);
+          tc::mbar_arrive(&ctl->full[st]);
         }
       }
       with_new += any;
@@ -473,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     const float scale = a.scale;
     const uint64_t sc2 = pack2(scale, scale);
     uint32_t c0 = 0, c1 = 0, parts = 0, with_new = 0;       // steps of each stream, parts
-    while (next_part(a, walk, p)) {
+    while (next_of(a, walk, p)) {
       const Steps u(p);
       const bool news = has_new(p, p.j1 - 1);
       Seen all{};
@@ -492,12 +550,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         }
         tc::tc_fence_after();
         const uint32_t tS = tmem + ((uint32_t)base << 16) + w * kKB;
+        const bool bad = ctl->bad_page != 0;
         uint32_t r[64];
         tc::tmem_ld_16x256b_x8(tS, *reinterpret_cast<uint32_t(*)[32]>(r));
         tc::tmem_ld_16x256b_x8(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
         tc::tmem_ld_wait();
-        const bool bad = ctl->bad_page != 0;
-        if (has_new(p, j) || bad) {
+        if (__builtin_expect(has_new(p, j) || bad, 0)) {
           constexpr uint32_t kMasked = 0xff800000u;        // -infinity
           uint64_t seen0 = ~(uint64_t)0, seen1 = seen0;
           if (news) {
@@ -548,34 +606,36 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
           t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
           t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
         }
+        // The references: the first step's maxima, raised where a score passes them by more
+        // than the threshold; also where one is -infinity (a row that has seen
+        // nothing but such scores has weights of 0, not 2^(-inf + inf)) or so large
+        // that the rounding of its product would show.
         float al0 = 1.f, al1 = 1.f;
         bool rescale = false;
-        if (k < 2) {                          // the stream's first step
-          m0 = t0;
-          m1 = t1;
-        } else {
+        float g0 = -m0 * scale, g1 = -m1 * scale;
+        const bool steady = k >= 2 && fmaf(t0, scale, g0) <= kRescaleThreshold &&
+                            fmaf(t1, scale, g1) <= kRescaleThreshold && fmaxf(fabsf(g0), fabsf(g1)) < kFar;
+        if (__builtin_expect(!__all_sync(0xffffffffu, steady), 0)) {
           const float s0 = m0 * scale, s1 = m1 * scale;
-          if (t0 * scale > s0 + kRescaleThreshold) {
-            al0 = ex2(s0 - t0 * scale);
+          if (k < 2 || t0 * scale > s0 + kRescaleThreshold) {
+            if (k >= 2) al0 = ex2(s0 - t0 * scale);
             m0 = t0;
-            rescale = true;
           }
-          if (t1 * scale > s1 + kRescaleThreshold) {
-            al1 = ex2(s1 - t1 * scale);
+          if (k < 2 || t1 * scale > s1 + kRescaleThreshold) {
+            if (k >= 2) al1 = ex2(s1 - t1 * scale);
             m1 = t1;
-            rescale = true;
           }
-        }
-        // (a row whose every score so far is -infinity has weights of 0, not 2^(-inf + inf))
-        float f0 = m0 == -INFINITY ? 0.f : m0, f1 = m1 == -INFINITY ? 0.f : m1;
-        // scores so large that the rounding of their reference's product would
-        // show: their difference is taken first
-        if (__any_sync(0xffffffffu, fmaxf(fabsf(f0), fabsf(f1)) * scale > 1048576.f)) {
+          rescale = __any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f);
+          float f0 = m0 == -INFINITY ? 0.f : m0, f1 = m1 == -INFINITY ? 0.f : m1;
+          if (__any_sync(0xffffffffu, fmaxf(fabsf(f0), fabsf(f1)) * scale >= kFar)) {
 #pragma unroll
-          for (int q = 0; q < 64; ++q) r[q] = __float_as_uint(__uint_as_float(r[q]) - ((q & 2) ? f1 : f0));
-          f0 = f1 = 0.f;
+            for (int q = 0; q < 64; ++q) r[q] = __float_as_uint(__uint_as_float(r[q]) - ((q & 2) ? f1 : f0));
+            f0 = f1 = 0.f;
+          }
+          g0 = -f0 * scale;
+          g1 = -f1 * scale;
         }
-        const uint64_t ng0 = pack2(-f0 * scale, -f0 * scale), ng1 = pack2(-f1 * scale, -f1 * scale);
+        const uint64_t ng0 = pack2(g0, g0), ng1 = pack2(g1, g1);
         uint64_t acc0 = 0, acc1 = 0;          // (even keys, odd keys) of each row
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
@@ -590,13 +650,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         tc::tmem_st_16x128b_x16(tS, *reinterpret_cast<uint32_t(*)[32]>(r));
         // the accumulator's rows, by the whole warp when any of them needs it (the
         // factor is 1 for the others), once the stream's step before has been added
-        if (__any_sync(0xffffffffu, rescale)) {
+        if (__builtin_expect(rescale, 0)) {
           if (!wait32(&ctl->pv_done[w], c - 1, ctl, err, W_PV_DONE)) {
             ok = false;
             break;
           }
           tc::tc_fence_after();
-          const uint64_t g0 = pack2(al0, al0), g1 = pack2(al1, al1);
+          const uint64_t a0 = pack2(al0, al0), a1 = pack2(al1, al1);
 #pragma unroll 1
           for (int e = 0; e < D; e += 64) {
             uint32_t o[32];
@@ -605,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
             tc::tmem_ld_wait();
 #pragma unroll
             for (int q = 0; q < 32; q += 2) {
-              const float2 y = unpack2(mul2(pack2(__uint_as_float(o[q]), __uint_as_float(o[q + 1])), (q & 2) ? g1 : g0));
+              const float2 y = unpack2(mul2(pack2(__uint_as_float(o[q]), __uint_as_float(o[q + 1])), (q & 2) ? a1 : a0));
               o[q] = __float_as_uint(y.x);
               o[q + 1] = __float_as_uint(y.y);
             }
@@ -701,20 +761,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
           } else {
             tc::tmem_ld_wait();
           }
-          if (fix) {                          // rare: elements that are not finite, of new tokens that this row sees
-#pragma unroll 1
-            for (unsigned long long left = fix; left; left &= left - 1) {
-              const int64_t vrow = pool_row(a.seq, p.s, p.q.len + __ffsll(left) - 1);
-              if (vrow < 0) continue;
-              const __nv_bfloat16* vr =
-                  reinterpret_cast<const __nv_bfloat16*>(a.v_pool) + (vrow * a.n_kv_heads + p.h) * D + e0;
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const float y = __bfloat162float(vr[e]);
-                if (!isfinite(y)) o[e] = __float_as_uint(__uint_as_float(o[e]) + y);
-              }
-            }
-          }
           if (valid && whole) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -733,6 +779,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
           __syncwarp();
         }
         if (valid && !whole && half == 0) a.part_ml[slot + v] = make_float2(M, sum);
+        if (fix && valid) {                   // rare
+          const int e0 = half * (D / 2);
+          if (whole)
+            add_nonfinite(out + e0, D / 2, fix, a, p, e0, D);
+          else
+            add_nonfinite(a.part_o + (slot + v) * D + e0, D / 2, fix, a, p, e0, D);
+        }
+        __syncwarp();
       }
       tc::tc_fence_before();
       tc::mbar_arrive(&ctl->o_empty);         // read: the next part's first products may start
@@ -751,11 +805,37 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
   if (warp == kWarpS) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int D>
-cudaError_t launch_d(const TreeArgs& a, cudaStream_t s) {
-  const cudaError_t e = set_dyn_smem_once(reinterpret_cast<const void*>(tree_tc_kernel<D>), smem_bytes<D>());
+template <int D, bool kGather>
+cudaError_t launch_g(const CUtensorMap& mQ, const CUtensorMap& mK, const CUtensorMap& mV, const TreeArgs& a, int box,
+                     cudaStream_t s) {
+  const cudaError_t e =
+      set_dyn_smem_once(reinterpret_cast<const void*>(tree_tc_kernel<D, kGather>), smem_bytes<D>());
   if (e != cudaSuccess) return e;
-  return launch_pdl(tree_tc_kernel<D>, dim3(a.workers), dim3(kThreads), smem_bytes<D>(), s, a);
+  return launch_pdl(tree_tc_kernel<D, kGather>, dim3(a.workers), dim3(kThreads), smem_bytes<D>(), s, mQ, mK, mV, a,
+                    box);
+}
+
+template <int D> cudaError_t launch_d(const TreeArgs& a, cudaStream_t s) {
+  CUtensorMap mQ, mK, mV;
+  const uint64_t dq[3] = {(uint64_t)D, (uint64_t)a.n_q_heads, (uint64_t)a.seq.n_rows};
+  const uint64_t sq[2] = {(uint64_t)D * 2, (uint64_t)a.n_q_heads * D * 2};
+  const uint32_t bq[3] = {64, (uint32_t)a.g, (uint32_t)(128 / a.g)};
+  if (!make_map_3d(&mQ, a.Q, dq, sq, bq)) return cudaErrorInvalidValue;
+  const int64_t rows = a.seq.n_pool_blocks * a.seq.block_size;
+  // the rows of a box: a power of two that divides a page
+  const int box = std::min(kKB, a.seq.block_size & -a.seq.block_size);
+  if (box < 8) {
+    if (!make_map_gather(&mK, a.k_pool, rows, (int64_t)a.n_kv_heads * D) ||
+        !make_map_gather(&mV, a.v_pool, rows, (int64_t)a.n_kv_heads * D))
+      return cudaErrorInvalidValue;
+    return launch_g<D, true>(mQ, mK, mV, a, box, s);
+  }
+  const uint64_t dk[3] = {(uint64_t)D, (uint64_t)a.n_kv_heads, (uint64_t)rows};
+  const uint64_t sk[2] = {(uint64_t)D * 2, (uint64_t)a.n_kv_heads * D * 2};
+  const uint32_t bk[3] = {64, 1, (uint32_t)box};
+  if (!make_map_3d(&mK, a.k_pool, dk, sk, bk) || !make_map_3d(&mV, a.v_pool, dk, sk, bk))
+    return cudaErrorInvalidValue;
+  return launch_g<D, false>(mQ, mK, mV, a, box, s);
 }
 
 }  // namespace

@@ -379,7 +379,9 @@ fuse_status_t check_seqs(const fuse_seqs_t* q, int64_t n_rows, int max_new, SeqA
   if (q->block_size <= 0 || q->max_blocks <= 0 || q->max_new <= 0 || q->n_pool_blocks <= 0)
     return FUSE_ERR_INVALID_ARG;
   if (q->max_new > max_new) return FUSE_ERR_UNSUPPORTED;
-  if ((int64_t)q->max_blocks * q->block_size > INT32_MAX) return FUSE_ERR_UNSUPPORTED;   // slots are 32-bit numbers
+  // slots and pool rows are 32-bit numbers
+  if ((int64_t)q->max_blocks * q->block_size > INT32_MAX || q->n_pool_blocks > INT32_MAX / q->block_size)
+    return FUSE_ERR_UNSUPPORTED;
   if (q->n_seq > 0 && (!q->tables || !q->lens || !q->rows)) return FUSE_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(q->tables) | reinterpret_cast<uintptr_t>(q->lens) |
        reinterpret_cast<uintptr_t>(q->rows)) & 3u)
@@ -391,6 +393,7 @@ fuse_status_t check_seqs(const fuse_seqs_t* q, int64_t n_rows, int max_new, SeqA
   a->block_size = q->block_size;
   a->max_blocks = q->max_blocks;
   a->max_new = q->max_new;
+  a->block_inv = q->block_size > 1 ? (uint32_t)((((uint64_t)1 << 32) + q->block_size - 1) / q->block_size) : 0;
   a->n_pool_blocks = q->n_pool_blocks;
   a->n_rows = n_rows;
   a->err = reinterpret_cast<uint32_t*>(ws);

@@ -12,9 +12,23 @@ struct SeqArgs {
   int32_t* lens;
   const int32_t* rows;
   int32_t n_seq, block_size, max_blocks, max_new;
+  uint32_t block_inv;                     // ceil(2^32 / block_size), 0 for pages of one token
   int64_t n_pool_blocks, n_rows;
   uint32_t* err;
 };
+
+// The page of a slot, and the slot's place in it.  The product with the rounded-up
+// inverse gives the quotient or one more.
+__device__ __forceinline__ int page_of(const SeqArgs& a, int slot, int* in_page) {
+  int b = a.block_inv ? (int)__umulhi((uint32_t)slot, a.block_inv) : slot;
+  int r = slot - b * a.block_size;
+  if (r < 0) {
+    --b;
+    r += a.block_size;
+  }
+  *in_page = r;
+  return b;
+}
 
 // A sequence in a call: its rows [row0, row0 + n), its held tokens.
 struct Seq {
@@ -47,13 +61,13 @@ __device__ __forceinline__ int parent_of(const int32_t* parents, const Seq& q, i
 
 // The pool row of a slot; -1 where its page is outside the pool (recorded).
 __device__ __forceinline__ int64_t pool_row(const SeqArgs& a, int s, int slot) {
-  const int b = slot / a.block_size;
-  const int page = a.tables[(int64_t)s * a.max_blocks + b];
+  int in_page;
+  const int page = a.tables[(int64_t)s * a.max_blocks + page_of(a, slot, &in_page)];
   if (page < 0 || page >= a.n_pool_blocks) {
     report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_SEQ_PAGE, (uint32_t)page);
     return -1;
   }
-  return (int64_t)page * a.block_size + (slot - b * a.block_size);
+  return (int64_t)page * a.block_size + in_page;
 }
 
 // The sequence whose rows hold `row`: the last s with rows[s] <= row (by a whole

@@ -713,6 +713,20 @@ bool make_map_3d(CUtensorMap* m, const void* base, const uint64_t dims[3], const
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Rows of `cols` elements from which single rows of 64 elements are gathered (tile::gather4:
+// the box is one row high).
+bool make_map_gather(CUtensorMap* m, const void* base, int64_t rows, int64_t cols) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t gd[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t gs[1] = {(cuuint64_t)cols * 2};
+  cuuint32_t bx[2] = {64, 1};
+  cuuint32_t es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), gd, gs, bx, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool tc_gemm_supported(const fuse_layer_desc_t& d) {
   // tiles pair heads: even head counts keep a pair inside Q, inside K/V or
   // across the K/V boundary (handled by per-half weight maps)
