@@ -11,8 +11,10 @@
 //   S = Q K^T     tcgen05.mma into TMEM columns [128 w, 128 w + 128)
 //   P = 2^(S - m) eight warps in registers, bf16, written back over S
 //   O += P V      tcgen05.mma with A = P in TMEM, V MN-major in shared memory
-// The running maximum m is raised only when a tile exceeds it by more than
-// 2^16 (then O and the running sum are rescaled).
+// The reference m is the first tile's maximum.  A later tile is weighed against it
+// as it stands, without its maximum being looked for: only where a thread's sum of
+// its weights passes 2^16 (no weight does otherwise) is the reference raised, O and
+// the running sum rescaled and the tile weighed once more.
 //
 // Keys and values lie in pages.  With pages of a multiple of 8 tokens a tile is
 // copied by TMA boxes of as many rows as always lie in one page; what lies
@@ -45,10 +47,13 @@ namespace {
 
 constexpr int kKB = kTreeTcTile;              // keys per tile
 constexpr int kHalf = 128 * 64 * 2;           // 64 columns of a 128-row tile (16 KB)
-constexpr int kWarpLoad = 8, kWarpS = 9, kWarpPV = 10, kWarpLook = 11;
-constexpr int kThreads = 12 * 32;
+// four warps load: a copy instruction takes its operands from uniform registers, so
+// that a warp's lanes issue theirs one after another, about 75 cycles each
+constexpr int kWarpLoad = 8, kLoadWarps = 4, kWarpS = 12, kWarpPV = 13, kWarpLook = 14;
+constexpr int kThreads = 15 * 32;
+constexpr int kAhead = 3;                     // tiles whose pages are looked up ahead of their copies
 constexpr int kTmemCols = 512;                // S of both streams | O of both
-constexpr float kRescaleThreshold = 16.0f;    // P and its sum keep their relative precision up to 2^16 over m
+constexpr float kMaxSum = 65536.f;            // of a thread's 32 weights: they keep their relative precision up to there
 constexpr float kFar = 1048576.f;             // of a score in log2 units: 2^-4 is its last place
 constexpr int kMaxStages = 10;
 constexpr int kFix = 8;                       // parts with new tokens that the look may be ahead by, and more
@@ -156,6 +161,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+__device__ __forceinline__ void arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(tc::smem_u32(bar)), "r"(n) : "memory");
+}
+
 // K-step kk (16 columns) of a 128-row K-major tile stored in 64-column halves.
 __device__ __forceinline__ uint64_t kmajor_step(uint32_t tile, int kk) {
   return tc::smem_desc_k128(tile + (kk >> 2) * kHalf + (kk & 3) * 32);
@@ -239,9 +248,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&ctl->pv_done[i], 1);
     }
     for (int i = 0; i < kSt; ++i) {
-      tc::mbar_init(&ctl->full[i], 1);
+      tc::mbar_init(&ctl->full[i], kLoadWarps);
       tc::mbar_init(&ctl->empty[i], 1);
-      tc::mbar_init(&ctl->look_full[i], 1);
+      tc::mbar_init(&ctl->look_full[i], kLoadWarps);
     }
     tc::mbar_init(&ctl->x_full, 256);
     tc::mbar_init(&ctl->o_empty, 256);
@@ -264,17 +273,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   TreePart p{};
 
   if (!work) {
-  } else if (warp == kWarpLoad) {
+  } else if (warp >= kWarpLoad && warp < kWarpLoad + kLoadWarps) {
     // -------------------------------- loads --------------------------------
     // a lane copies one box, or gathers a group of four rows
     uint32_t it = 0, qn0 = 0, qn1 = 0;
     int qb = 0;
     bool ok = true;
     constexpr int kG = kGather ? 4 : 1;       // pages that a lane looks up per tile
-    const int n_box = kGather ? 0 : kKB / box;
-    const int group = kGather ? lane : lane % n_box;
+    const int lw = warp - kWarpLoad;
+    const int n_box = kGather ? 32 : kKB / box;
     const int rows = kGather ? 4 : box;       // of a group
-    const bool mine = kGather || lane < n_box * (D / 64);
+    // this lane's copy of a tile: its group (and half of the columns; a gathering lane takes both)
+    const int op = lane * kLoadWarps + lw, group = kGather ? op : op % n_box;
+    const int ops = kGather ? n_box : n_box * (D / 64);
+    const bool mine = op < ops;
+    const uint32_t share = (uint32_t)(ops - lw + kLoadWarps - 1) / kLoadWarps * (kTile / ops);       // bytes of the warp's
     const int none = (int)(a.seq.n_pool_blocks * a.seq.block_size);       // a row outside the pool: reads as zeros
     // the pages of this lane's rows of tile j (-2: no key there), and their first slot's place
     auto entries = [&](int j, int (&page)[kG], int& in_page) {
@@ -310,14 +323,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait32(&ctl->empty[st], (it / kSt) ^ 1, ctl, err, W_EMPTY)) return false;
       uint64_t* bar = look ? &ctl->look_full[st] : &ctl->full[st];
       uint8_t* tile = sR + st * kTile;
-      uint32_t bytes = kTile;
+      uint32_t bytes = share;
       bool whole = true;
       if constexpr (kGather) {
         // groups that are not whole: by the lane's own loads and stores
         whole = row[0] != none && row[1] != none && row[2] != none && row[3] != none;
-        const unsigned self = __ballot_sync(0xffffffffu, !whole);
+        const unsigned self = __ballot_sync(0xffffffffu, mine && !whole);
         if (self) {
-          if (!whole) {
+          if (mine && !whole) {
 #pragma unroll 1
             for (int i = 0; i < 4 * (D / 8); ++i) {
               const int m = i / (D / 8), c = i % (D / 8);
@@ -339,12 +352,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) tc::mbar_arrive_expect_tx(bar, bytes);
       __syncwarp();
       if constexpr (kGather) {
-        if (whole)
+        if (mine && whole)
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
             tc::tma_gather4(tile + h * kHalf + group * 512, map, bar, p.h * D + 64 * h, row[0], row[1], row[2], row[3]);
       } else if (mine) {
-        const int h = lane / n_box;
+        const int h = op / n_box;
         tc::tma_load_3d(tile + h * kHalf + group * box * 128, map, bar, 64 * h, p.h, row[0]);
       }
       ++it;
@@ -352,9 +365,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     while (ok && next_of(a, walk, p)) {
       const Steps u(p);
-      int page[kG], in_page = 0, rc[kG], rn[kG];       // rows of the values' tile, of the keys'
-      entries(p.j0, page, in_page);
-      for (int m = 0; m < (u.dual ? 2 : 1); ++m) {
+      int page[kAhead][kG], in_page[kAhead], rc[kG], rn[kG];       // pages ahead; rows of the values' tile, of the keys'
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) entries(min(p.j0 + k, p.j1 - 1), page[k], in_page[k]);
+      for (int m = 0; lw == 0 && m < (u.dual ? 2 : 1); ++m) {
         const int b = u.dual ? m : qb;
         uint32_t& qn = b ? qn1 : qn0;
         if (!wait32(&ctl->q_empty[b], qn ^ 1, ctl, err, W_Q_EMPTY)) {
@@ -374,8 +388,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!u.dual) qb ^= 1;
       for (int i = 0; ok && i <= u.tiles; ++i) {
         if (i < u.tiles) {
-          places(page, in_page, rn);
-          if (i + 1 < u.tiles) entries(p.j0 + i + 1, page, in_page);
+          places(page[0], in_page[0], rn);
+#pragma unroll
+          for (int k = 0; k + 1 < kAhead; ++k) {
+#pragma unroll
+            for (int g = 0; g < kG; ++g) page[k][g] = page[k + 1][g];
+            in_page[k] = in_page[k + 1];
+          }
+          entries(min(p.j0 + i + kAhead, p.j1 - 1), page[kAhead - 1], in_page[kAhead - 1]);
           ok = issue(&mapK, a.k_pool, rn, false);
         }
         if (ok && i > 0) ok = issue(&mapV, a.v_pool, rc, has_new(p, p.j0 + i - 1));
@@ -392,77 +412,88 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kWarpS) {
     // ------------------------------ S = Q K^T ------------------------------
-    if (lane == 0) {
-      constexpr uint32_t idesc = tc::idesc_bf16_f32(128, kKB);
-      uint32_t it = 0, c[2] = {0, 0}, qn0 = 0, qn1 = 0;
-      int qb = 0;
-      bool ok = true;
-      while (ok && next_of(a, walk, p)) {
-        const Steps u(p);
-        if (u.dual || qb == 0) ok = wait1(&ctl->q_full[0], qn0++, ctl, err, W_Q_FULL);
-        if (ok && (u.dual || qb == 1)) ok = wait1(&ctl->q_full[1], qn1++, ctl, err, W_Q_FULL);
-        if (!ok) break;
-        for (int k = 0; k < u.n; ++k) {
-          const int w = k & 1;
-          // the buffer holds P of the stream's step before until that step's P.V is done
-          // (and with it every ring item up to this one's slot has been full)
-          if (c[w] > 0 && !wait1(&ctl->pv_done[w], c[w] - 1, ctl, err, W_S_FREE)) {
-            ok = false;
-            break;
-          }
-          const uint32_t q = it + u.k_item(u.tile(k));
-          const int st = q % kSt;
-          if (!wait1(&ctl->full[st], q / kSt, ctl, err, W_K_FULL)) {
-            ok = false;
-            break;
-          }
-          tc::tc_fence_after();
-          const uint32_t qa = tc::smem_u32(sQ + (u.dual ? w : qb) * kTile), ka = tc::smem_u32(sR + st * kTile);
+    constexpr uint32_t idesc = tc::idesc_bf16_f32(128, kKB);
+    uint32_t it = 0, c0 = 0, c1 = 0, qn0 = 0, qn1 = 0;
+    int qb = 0;
+    bool ok = true;
+    while (ok && next_of(a, walk, p)) {
+      const Steps u(p);
+      if (u.dual || qb == 0) ok = wait32(&ctl->q_full[0], qn0++, ctl, err, W_Q_FULL);
+      if (ok && (u.dual || qb == 1)) ok = wait32(&ctl->q_full[1], qn1++, ctl, err, W_Q_FULL);
+      if (!ok) break;
+      for (int k = 0; k < u.n; ++k) {
+        const int w = k & 1;
+        const uint32_t c = w ? c1 : c0;
+        // the buffer holds P of the stream's step before until that step's P.V is done
+        // (and with it every ring item up to this one's slot has been full)
+        if (c > 0 && !wait32(&ctl->pv_done[w], c - 1, ctl, err, W_S_FREE)) {
+          ok = false;
+          break;
+        }
+        const uint32_t q = it + u.k_item(u.tile(k));
+        const int st = q % kSt;
+        if (!wait32(&ctl->full[st], q / kSt, ctl, err, W_K_FULL)) {
+          ok = false;
+          break;
+        }
+        tc::tc_fence_after();
+        const uint32_t qa = tc::smem_u32(sQ) + (u.dual ? w : qb) * kTile, ka = tc::smem_u32(sR) + st * kTile;
+        if (tc::elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
             tc::mma_bf16(tmem + w * kKB, kmajor_step(qa, kk), kmajor_step(ka, kk), idesc, kk != 0);
           tc::mma_commit(&ctl->s_full[w]);
           if (!u.dual || w == 1) tc::mma_commit(&ctl->empty[st]);
-          ++c[w];
+          if (k == u.n - 1) {
+            if (u.dual || qb == 0) tc::mma_commit(&ctl->q_empty[0]);
+            if (u.dual || qb == 1) tc::mma_commit(&ctl->q_empty[1]);
+          }
         }
-        if (!ok) break;
-        if (u.dual || qb == 0) tc::mma_commit(&ctl->q_empty[0]);
-        if (u.dual || qb == 1) tc::mma_commit(&ctl->q_empty[1]);
-        if (!u.dual) qb ^= 1;
-        it += 2 * u.tiles;
+        __syncwarp();
+        if (w)
+          ++c1;
+        else
+          ++c0;
       }
+      if (!u.dual) qb ^= 1;
+      it += 2 * u.tiles;
     }
   } else if (warp == kWarpPV) {
     // ------------------------------- O += P V -------------------------------
-    if (lane == 0) {
-      constexpr uint32_t idesc = tc::idesc_bf16_f32(128, D, /*b_mn_major=*/true);
-      uint32_t it = 0, c[2] = {0, 0}, parts = 0;
-      bool ok = true;
-      while (ok && next_of(a, walk, p)) {
-        const Steps u(p);
-        for (int k = 0; k < u.n; ++k) {
-          const int w = k & 1, i = u.tile(k);
-          const uint32_t q = it + u.v_item(i);
-          const int st = q % kSt;
-          // P first: the ring's earlier items have been full by then
-          ok = wait1(&ctl->p_full[w], c[w], ctl, err, W_P_FULL) && wait1(&ctl->full[st], q / kSt, ctl, err, W_V_FULL);
-          // the accumulators were last read at the end of the part before
-          if (ok && k == 0) ok = wait1(&ctl->o_empty, parts ^ 1, ctl, err, W_O_EMPTY);
-          if (!ok) break;
-          tc::tc_fence_after();
-          const uint32_t va = tc::smem_u32(sR + st * kTile);
+    constexpr uint32_t idesc = tc::idesc_bf16_f32(128, D, /*b_mn_major=*/true);
+    uint32_t it = 0, c0 = 0, c1 = 0, parts = 0;
+    bool ok = true;
+    while (ok && next_of(a, walk, p)) {
+      const Steps u(p);
+      for (int k = 0; k < u.n; ++k) {
+        const int w = k & 1, i = u.tile(k);
+        const uint32_t q = it + u.v_item(i);
+        const int st = q % kSt;
+        // P first: the ring's earlier items have been full by then
+        ok = wait32(&ctl->p_full[w], w ? c1 : c0, ctl, err, W_P_FULL) &&
+             wait32(&ctl->full[st], q / kSt, ctl, err, W_V_FULL);
+        // the accumulators were last read at the end of the part before
+        if (ok && k == 0) ok = wait32(&ctl->o_empty, parts ^ 1, ctl, err, W_O_EMPTY);
+        if (!ok) break;
+        tc::tc_fence_after();
+        const uint32_t va = tc::smem_u32(sR) + st * kTile;
+        if (tc::elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kKB / 16; ++kk)
             tc::mma_bf16_ts(tmem + kColO + w * D, tmem + w * kKB + kk * 8,
                             tc::smem_desc_mn128(va + kk * 16 * 128, kHalf), idesc, (k > 1 || kk != 0) ? 1u : 0u);
           tc::mma_commit(&ctl->pv_done[w]);
           if (!u.dual || w == 1) tc::mma_commit(&ctl->empty[st]);
-          ++c[w];
         }
-        if (!ok) break;
-        ++parts;
-        it += 2 * u.tiles;
+        __syncwarp();
+        if (w)
+          ++c1;
+        else
+          ++c0;
       }
+      if (!ok) break;
+      ++parts;
+      it += 2 * u.tiles;
     }
   } else if (warp == kWarpLook) {
     // ------------------- values of new tokens looked through -------------------
@@ -514,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) {
           ctl->fix[with_new % kFix] = found;
-          tc::mbar_arrive(&ctl->full[st]);
+          arrive_n(&ctl->full[st], kLoadWarps);
         }
       }
       with_new += any;
@@ -537,9 +568,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       Seen all{};
       if (news) all = seen_of_all(a.parents, p.q, err);
       // of the stream at hand (m, l) and the other one (n, k): the rows' references
-      // (scores) and this thread's part of their sums
+      // (scores) and this thread's part of their sums; odd: some reference of the warp
+      // is -infinity or so large that the rounding of its product would show
       float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
       float n0 = -INFINITY, n1 = -INFINITY, k0 = 0.f, k1 = 0.f;
+      bool odd = true, odd_n = true;
       bool ok = true;
       for (int k = 0; k < u.n; ++k) {
         const int w = k & 1, j = p.j0 + u.tile(k);
@@ -551,19 +584,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tc_fence_after();
         const uint32_t tS = tmem + ((uint32_t)base << 16) + w * kKB;
         const bool bad = ctl->bad_page != 0;
-        uint32_t r[64];
-        tc::tmem_ld_16x256b_x8(tS, *reinterpret_cast<uint32_t(*)[32]>(r));
-        tc::tmem_ld_16x256b_x8(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
-        tc::tmem_ld_wait();
         if (__builtin_expect(has_new(p, j) || bad, 0)) {
-          constexpr uint32_t kMasked = 0xff800000u;        // -infinity
+          // the scores of keys that a row does not see, replaced where they are
           uint64_t seen0 = ~(uint64_t)0, seen1 = seen0;
           if (news) {
             const int v0 = (u.dual ? w * 128 : 0) + R0;
             seen0 = seen_by(all, (p.vg * a.vecs + min(v0, p.n_vec - 1)) >> a.g_log2);
             seen1 = seen_by(all, (p.vg * a.vecs + min(v0 + 8, p.n_vec - 1)) >> a.g_log2);
           }
-#pragma unroll
+#pragma unroll 1
           for (int b = 0; b < 4; ++b) {
             const int rel = j * kKB + 32 * b - p.q.len;
             uint32_t w0 = seen_word(seen0, rel), w1 = seen_word(seen1, rel);
@@ -576,81 +605,90 @@ __global__ void __launch_bounds__(kThreads, 1)
               w0 &= there;
               w1 &= there;
             }
-            w0 >>= 2 * c4;
-            w1 >>= 2 * c4;
+            uint32_t x[16];
+            tc::tmem_ld_16x256b_x4(tS + 32 * b, x);
+            tc::tmem_ld_wait();
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              uint32_t* x = r + 4 * (4 * b + q);
-              if (!(w0 >> (8 * q) & 1)) x[0] = kMasked;
-              if (!(w0 >> (8 * q) & 2)) x[1] = kMasked;
-              if (!(w1 >> (8 * q) & 1)) x[2] = kMasked;
-              if (!(w1 >> (8 * q) & 2)) x[3] = kMasked;
+              constexpr uint32_t kMasked = 0xff800000u;    // -infinity
+              if (!(w0 >> (8 * q + 2 * c4) & 1)) x[4 * q] = kMasked;
+              if (!(w0 >> (8 * q + 2 * c4) & 2)) x[4 * q + 1] = kMasked;
+              if (!(w1 >> (8 * q + 2 * c4) & 1)) x[4 * q + 2] = kMasked;
+              if (!(w1 >> (8 * q + 2 * c4) & 2)) x[4 * q + 3] = kMasked;
             }
+            tc::tmem_st_16x256b_x4(tS + 32 * b, x);
           }
+          tc::tmem_st_wait();
         }
-        float t0, t1;                         // the rows' maxima
-        {
-          float a0 = __uint_as_float(r[0]), a1 = __uint_as_float(r[1]);
-          float b0 = __uint_as_float(r[2]), b1 = __uint_as_float(r[3]);
+        float al0 = 1.f, al1 = 1.f, s0, s1;   // factors of the sums so far; this tile's sums
+        bool raise = odd || k < 2;            // uniform; a stream's first step sets the references
+        uint32_t r[64];
+#pragma unroll 1
+        while (true) {
+          tc::tmem_ld_16x256b_x8(tS, *reinterpret_cast<uint32_t(*)[32]>(r));
+          tc::tmem_ld_16x256b_x8(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
+          tc::tmem_ld_wait();
+          float g0 = -m0 * scale, g1 = -m1 * scale;
+          if (__builtin_expect(raise, 0)) {
+            float a0 = __uint_as_float(r[0]), a1 = __uint_as_float(r[1]);
+            float b0 = __uint_as_float(r[2]), b1 = __uint_as_float(r[3]);
 #pragma unroll
-          for (int q = 1; q < 15; q += 2) {
-            a0 = max3(a0, __uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 4]));
-            a1 = max3(a1, __uint_as_float(r[4 * q + 1]), __uint_as_float(r[4 * q + 5]));
-            b0 = max3(b0, __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 6]));
-            b1 = max3(b1, __uint_as_float(r[4 * q + 3]), __uint_as_float(r[4 * q + 7]));
-          }
-          t0 = max3(a0, a1, fmaxf(__uint_as_float(r[60]), __uint_as_float(r[61])));
-          t1 = max3(b0, b1, fmaxf(__uint_as_float(r[62]), __uint_as_float(r[63])));
-          t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
-          t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
-          t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
-          t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
-        }
-        // The references: the first step's maxima, raised where a score passes them by more
-        // than the threshold; also where one is -infinity (a row that has seen
-        // nothing but such scores has weights of 0, not 2^(-inf + inf)) or so large
-        // that the rounding of its product would show.
-        float al0 = 1.f, al1 = 1.f;
-        bool rescale = false;
-        float g0 = -m0 * scale, g1 = -m1 * scale;
-        const bool steady = k >= 2 && fmaf(t0, scale, g0) <= kRescaleThreshold &&
-                            fmaf(t1, scale, g1) <= kRescaleThreshold && fmaxf(fabsf(g0), fabsf(g1)) < kFar;
-        if (__builtin_expect(!__all_sync(0xffffffffu, steady), 0)) {
-          const float s0 = m0 * scale, s1 = m1 * scale;
-          if (k < 2 || t0 * scale > s0 + kRescaleThreshold) {
-            if (k >= 2) al0 = ex2(s0 - t0 * scale);
-            m0 = t0;
-          }
-          if (k < 2 || t1 * scale > s1 + kRescaleThreshold) {
-            if (k >= 2) al1 = ex2(s1 - t1 * scale);
-            m1 = t1;
-          }
-          rescale = __any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f);
-          float f0 = m0 == -INFINITY ? 0.f : m0, f1 = m1 == -INFINITY ? 0.f : m1;
-          if (__any_sync(0xffffffffu, fmaxf(fabsf(f0), fabsf(f1)) * scale >= kFar)) {
+            for (int q = 1; q < 15; q += 2) {
+              a0 = max3(a0, __uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 4]));
+              a1 = max3(a1, __uint_as_float(r[4 * q + 1]), __uint_as_float(r[4 * q + 5]));
+              b0 = max3(b0, __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 6]));
+              b1 = max3(b1, __uint_as_float(r[4 * q + 3]), __uint_as_float(r[4 * q + 7]));
+            }
+            a0 = max3(a0, a1, fmaxf(__uint_as_float(r[60]), __uint_as_float(r[61])));
+            b0 = max3(b0, b1, fmaxf(__uint_as_float(r[62]), __uint_as_float(r[63])));
 #pragma unroll
-            for (int q = 0; q < 64; ++q) r[q] = __float_as_uint(__uint_as_float(r[q]) - ((q & 2) ? f1 : f0));
-            f0 = f1 = 0.f;
-          }
-          g0 = -f0 * scale;
-          g1 = -f1 * scale;
-        }
-        const uint64_t ng0 = pack2(g0, g0), ng1 = pack2(g1, g1);
-        uint64_t acc0 = 0, acc1 = 0;          // (even keys, odd keys) of each row
+            for (int o = 1; o < 4; o <<= 1) {
+              a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, o));
+              b0 = fmaxf(b0, __shfl_xor_sync(0xffffffffu, b0, o));
+            }
+            if (k < 2) {
+              m0 = a0;
+              m1 = b0;
+            } else {
+              if (a0 > m0) al0 = ex2((m0 - a0) * scale);
+              if (b0 > m1) al1 = ex2((m1 - b0) * scale);
+              m0 = fmaxf(m0, a0);
+              m1 = fmaxf(m1, b0);
+            }
+            // (a row whose every score so far is -infinity has weights of 0, not 2^(-inf + inf))
+            float f0 = m0 == -INFINITY ? 0.f : m0, f1 = m1 == -INFINITY ? 0.f : m1;
+            const bool far = __any_sync(0xffffffffu, fmaxf(fabsf(f0), fabsf(f1)) * scale >= kFar);
+            odd = far || __any_sync(0xffffffffu, m0 == -INFINITY || m1 == -INFINITY);
+            if (far) {                        // the differences first
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          const float2 x01 = unpack2(fma2(pack2(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1])), sc2, ng0));
-          const float2 x23 = unpack2(fma2(pack2(__uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3])), sc2, ng1));
-          const float e0 = ex2(x01.x), e1 = ex2(x01.y), e2 = ex2(x23.x), e3 = ex2(x23.y);
-          acc0 = add2(acc0, pack2(e0, e1));
-          acc1 = add2(acc1, pack2(e2, e3));
-          r[2 * q] = pack_bf16x2(e0, e1);
-          r[2 * q + 1] = pack_bf16x2(e2, e3);
+              for (int q = 0; q < 64; ++q) r[q] = __float_as_uint(__uint_as_float(r[q]) - ((q & 2) ? f1 : f0));
+              f0 = f1 = 0.f;
+            }
+            g0 = -f0 * scale;
+            g1 = -f1 * scale;
+          }
+          const uint64_t ng0 = pack2(g0, g0), ng1 = pack2(g1, g1);
+          uint64_t acc0 = 0, acc1 = 0;        // (even keys, odd keys) of each row
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            const float2 x01 = unpack2(fma2(pack2(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1])), sc2, ng0));
+            const float2 x23 = unpack2(fma2(pack2(__uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3])), sc2, ng1));
+            const float e0 = ex2(x01.x), e1 = ex2(x01.y), e2 = ex2(x23.x), e3 = ex2(x23.y);
+            acc0 = add2(acc0, pack2(e0, e1));
+            acc1 = add2(acc1, pack2(e2, e3));
+            r[2 * q] = pack_bf16x2(e0, e1);
+            r[2 * q + 1] = pack_bf16x2(e2, e3);
+          }
+          const float2 y0 = unpack2(acc0), y1 = unpack2(acc1);
+          s0 = y0.x + y0.y;
+          s1 = y1.x + y1.y;
+          if (raise || __all_sync(0xffffffffu, fmaxf(s0, s1) <= kMaxSum && s0 == s0 && s1 == s1)) break;
+          raise = true;                       // (a sum that is not a number among them)
         }
         tc::tmem_st_16x128b_x16(tS, *reinterpret_cast<uint32_t(*)[32]>(r));
         // the accumulator's rows, by the whole warp when any of them needs it (the
         // factor is 1 for the others), once the stream's step before has been added
-        if (__builtin_expect(rescale, 0)) {
+        if (__builtin_expect(raise && __any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f), 0)) {
           if (!wait32(&ctl->pv_done[w], c - 1, ctl, err, W_PV_DONE)) {
             ok = false;
             break;
@@ -675,9 +713,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tmem_st_wait();
         tc::tc_fence_before();
         tc::mbar_arrive(&ctl->p_full[w]);
-        const float2 y0 = unpack2(acc0), y1 = unpack2(acc1);
-        l0 = l0 * al0 + (y0.x + y0.y);
-        l1 = l1 * al1 + (y1.x + y1.y);
+        l0 = l0 * al0 + s0;
+        l1 = l1 * al1 + s1;
         if (w)
           ++c1;
         else
@@ -688,6 +725,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         z = m1; m1 = n1; n1 = z;
         z = l0; l0 = k0; k0 = z;
         z = l1; l1 = k1; k1 = z;
+        const bool y = odd;
+        odd = odd_n;
+        odd_n = y;
       }
       if (!ok) break;
       // the rows' references and sums to shared memory, in a fixed order
@@ -747,34 +787,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.O) +
                              ((int64_t)(p.q.row0 + node) * a.n_q_heads + p.h * a.g + (vi & (a.g - 1))) * D;
         const uint32_t tO = tmem + ((uint32_t)(quarter * 32) << 16) + kColO + mt * D;
+        // (a short loop: a part's end runs once, out of a cold instruction cache)
 #pragma unroll 1
-        for (int e0 = half * (D / 2); e0 < (half + 1) * (D / 2); e0 += 32) {
-          uint32_t o[32];
-          tc::tmem_ld_32x32b_x32(tO + e0, o);
-          if (two) {
-            uint32_t o1[32];
-            tc::tmem_ld_32x32b_x32(tO + D + e0, o1);
-            tc::tmem_ld_wait();
+        for (int e0 = half * (D / 2); e0 < (half + 1) * (D / 2); e0 += 8) {
+          uint32_t o[8], o1[8];
+          tc::tmem_ld_32x32b_x8(tO + e0, o);
+          if (two) tc::tmem_ld_32x32b_x8(tO + D + e0, o1);
+          tc::tmem_ld_wait();
+          float y[8];
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              o[e] = __float_as_uint(fmaf(__uint_as_float(o[e]), f0, __uint_as_float(o1[e]) * f1));
-          } else {
-            tc::tmem_ld_wait();
+          for (int e = 0; e < 8; ++e) {
+            y[e] = __uint_as_float(o[e]) * f0;
+            if (two) y[e] = fmaf(__uint_as_float(o1[e]), f1, y[e]);
           }
           if (valid && whole) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t y[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                y[e] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * e]) * inv, __uint_as_float(o[8 * q + 2 * e + 1]) * inv);
-              *reinterpret_cast<uint4*>(out + e0 + 8 * q) = make_uint4(y[0], y[1], y[2], y[3]);
-            }
+            for (int e = 0; e < 8; ++e) y[e] *= inv;
+            Vec8<__nv_bfloat16>::store(out + e0, y);
           } else if (valid) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              *reinterpret_cast<uint4*>(a.part_o + (slot + v) * D + e0 + 4 * q) =
-                  make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            Vec8<float>::store(a.part_o + (slot + v) * D + e0, y);
           }
           __syncwarp();
         }
