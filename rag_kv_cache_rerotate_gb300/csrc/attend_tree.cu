@@ -29,12 +29,11 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const __grid_con
   constexpr int EL = D / 32;
   __shared__ float s_q[kWarps][kVecs][D];
   __shared__ float s_p[kWarps][32][kVecs];
-  __shared__ int64_t s_warp[kWarps];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   pdl_wait();
   pdl_trigger();
   const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
-  TreeWalk walk = start_walk<kWarps * 32>(a, w, s_warp);
+  TreeWalk walk = start_walk(a, w, w == 0);
   TreePart at;
   while (next_part(a, walk, at)) {
     const int h = at.h, vg = at.vg, n_vec = at.n_vec;

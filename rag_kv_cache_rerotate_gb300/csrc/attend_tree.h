@@ -59,75 +59,91 @@ struct TreeWalk {
   int64_t t, end;                         // the worker's next tile, and its last one's next
 };
 
-// 32 sequences from s0 on, one a lane: their tiles, and those up to and with each.
-__device__ __forceinline__ int64_t scan_tiles(const TreeArgs& a, int s0, Seq* q, int64_t* inc) {
+// 128 sequences from s0 on, four a lane: their tiles, and the lane's first tile among them.
+struct TileScan {
+  Seq q[4];
+  int64_t own[4];
+  int64_t before, all;
+};
+__device__ __forceinline__ TileScan scan_tiles(const TreeArgs& a, int s0) {
   const int lane = threadIdx.x % 32;
-  *q = Seq{0, 0, 0};
-  if (s0 + lane < a.seq.n_seq) seq_of(a.seq, s0 + lane, q);
-  const int64_t own = (int64_t)units_of(a, *q) * tiles_of(a, *q);
-  *inc = own;
+  TileScan r;
+  int64_t sum = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r.q[i] = Seq{0, 0, 0};
+    const int s = s0 + lane * 4 + i;
+    if (s < a.seq.n_seq) seq_of(a.seq, s, &r.q[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r.own[i] = (int64_t)units_of(a, r.q[i]) * tiles_of(a, r.q[i]);
+    sum += r.own[i];
+  }
+  int64_t inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t z = __shfl_up_sync(0xffffffffu, *inc, o);
-    if (lane >= o) *inc += z;
+    const int64_t z = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += z;
   }
-  return own;
+  r.before = inc - sum;
+  r.all = __shfl_sync(0xffffffffu, inc, 31);
+  return r;
 }
 
-// The walk of worker w, found by its warp (all threads of a block call this);
-// block 0 also writes each sequence's first tile, for the join.  s_warp: a word per
-// warp.  Up to 32 sequences need one look at them; more are counted by the block
-// first and then passed over once again.
-template <int kThreads>
-__device__ __forceinline__ TreeWalk start_walk(const TreeArgs& a, int64_t w, int64_t* s_warp) {
-  constexpr int kWarps = kThreads / 32;
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+// The walk of worker w, by its warp; `keep`: also writes each sequence's first tile,
+// for the join.  Up to 128 sequences need one look at them.
+__device__ __forceinline__ TreeWalk start_walk(const TreeArgs& a, int64_t w, bool keep) {
+  const int lane = threadIdx.x % 32;
   TreeWalk r{a.seq.n_seq, {0, 0, 0}, 0, 0, 0};
-  Seq q;
-  int64_t inc, own = 0, total = 0;
-  const bool one = a.seq.n_seq <= 32;
-  if (one) {
-    own = scan_tiles(a, 0, &q, &inc);
-    total = __shfl_sync(0xffffffffu, inc, 31);
-    if (blockIdx.x == 0 && warp == 0) {
-      if (lane < a.seq.n_seq) a.start[lane] = inc - own;
-      if (lane == 0) a.start[a.seq.n_seq] = total;
-    }
-  } else {
-    for (int s0 = 0; s0 < a.seq.n_seq; s0 += kThreads) {
-      own = scan_tiles(a, s0 + warp * 32, &q, &inc);
-      if (lane == 31) s_warp[warp] = inc;
-      __syncthreads();
-      int64_t before = 0, all = 0;
-      for (int i = 0; i < kWarps; ++i) {
-        if (i < warp) before += s_warp[i];
-        all += s_warp[i];
+  TileScan x;
+  int64_t total = 0;
+#pragma unroll 1
+  for (int s0 = 0; s0 < a.seq.n_seq; s0 += 128) {
+    x = scan_tiles(a, s0);
+    if (keep) {
+      int64_t at = total + x.before;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int s = s0 + lane * 4 + i;
+        if (s < a.seq.n_seq) a.start[s] = at;
+        at += x.own[i];
       }
-      const int s = s0 + threadIdx.x;
-      if (blockIdx.x == 0 && s < a.seq.n_seq) a.start[s] = total + before + inc - own;
-      total += all;
-      __syncthreads();
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.start[a.seq.n_seq] = total;
+    total += x.all;
   }
+  if (keep && lane == 0) a.start[a.seq.n_seq] = total;
   const int64_t per = per_worker(a, total);
   r.t = min(total, w * per);
   r.end = min(total, r.t + per);
   if (r.t == r.end) return r;
   int64_t before = 0;
-  for (int s0 = 0; s0 < a.seq.n_seq; s0 += 32) {
-    if (!one) own = scan_tiles(a, s0, &q, &inc);
-    const unsigned past = __ballot_sync(0xffffffffu, before + inc > r.t);
-    if (past) {
-      const int k = __ffs(past) - 1;
-      r.s = s0 + k;
-      r.first = before + __shfl_sync(0xffffffffu, inc - own, k);
+#pragma unroll 1
+  for (int s0 = 0; s0 < a.seq.n_seq; s0 += 128) {
+    if (a.seq.n_seq > 128) x = scan_tiles(a, s0);
+    // the last lane whose first tile is not behind it, and the last such sequence of its
+    // four (sequences without tiles before it share that tile)
+    const unsigned in = __ballot_sync(0xffffffffu, before + x.before <= r.t);
+    if (r.t < before + x.all) {
+      const int k = 31 - __clz(in);
+      int64_t first = before + x.before;
+      int s = s0 + lane * 4;
+      Seq q = x.q[0];
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (r.t >= first + x.own[i] && s == s0 + lane * 4 + i) {
+          first += x.own[i];
+          q = x.q[i + 1];
+          ++s;
+        }
+      r.s = __shfl_sync(0xffffffffu, s, k);
+      r.first = __shfl_sync(0xffffffffu, first, k);
       r.q.row0 = __shfl_sync(0xffffffffu, q.row0, k);
       r.q.n = __shfl_sync(0xffffffffu, q.n, k);
       r.q.len = __shfl_sync(0xffffffffu, q.len, k);
       break;
     }
-    before += __shfl_sync(0xffffffffu, inc, 31);
+    before += x.all;
   }
   return r;
 }

@@ -9,7 +9,7 @@
 //                 joined when the unit ends
 // so that one stream's products run beside the other's softmax.  Per step
 //   S = Q K^T     tcgen05.mma into TMEM columns [128 w, 128 w + 128)
-//   P = 2^(S - m) eight warps in registers, bf16, written back over S
+//   P = 2^(S - m) eight warps a stream, in registers, bf16, written back over S
 //   O += P V      tcgen05.mma with A = P in TMEM, V MN-major in shared memory
 // The reference m is the first tile's maximum.  A later tile is weighed against it
 // as it stands, without its maximum being looked for: only where a thread's sum of
@@ -17,12 +17,13 @@
 // the running sum rescaled and the tile weighed once more.
 //
 // Keys and values lie in pages.  With pages of a multiple of 8 tokens a tile is
-// copied by TMA boxes of as many rows as always lie in one page; what lies
-// behind a sequence's last slot in its page comes along and is masked, its values
-// cleared.  With other pages the rows are gathered four at a time, and a group that is
-// not whole (the sequence's end, a page outside the pool) is copied by a lane
-// itself.  (Gathering by 16-byte cp.async, four warps, kept the load/store path so
-// busy that the softmax's shuffles waited: 550 us instead of @@ on 8 trees of 64 over 33k.)
+// copied by TMA boxes of as many rows as always lie in one page, whole heads: a copy
+// costs the SM's copy unit about 100 cycles whatever its size, so that boxes of 64
+// columns kept pages of 16 tokens at 5.3 TB/s of the 6.6 that pages of 128 reach.  What
+// lies behind a sequence's last slot in its page comes along and is masked, its values
+// cleared.  With other pages the rows are gathered by 16-byte cp.async (about 4 TB/s;
+// single rows as tile::gather4 copies: 2).
+// A tile lies in shared memory as [group of 8 rows][64 columns][8 rows], 128-byte swizzled.
 //
 // What a row does not see must not reach it: its scores are replaced where they
 // are masked, and as 0 * V is not 0 for an infinite or NaN V, one warp looks
@@ -41,16 +42,19 @@ namespace fusekv {
 
 bool make_map_3d(CUtensorMap* m, const void* base, const uint64_t dims[3], const uint64_t strides[2],
                  const uint32_t box[3]);
-bool make_map_gather(CUtensorMap* m, const void* base, int64_t rows, int64_t cols);
+bool make_map_groups(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int col_blocks,
+                     int row_groups);
 
 namespace {
 
 constexpr int kKB = kTreeTcTile;              // keys per tile
 constexpr int kHalf = 128 * 64 * 2;           // 64 columns of a 128-row tile (16 KB)
-// four warps load: a copy instruction takes its operands from uniform registers, so
-// that a warp's lanes issue theirs one after another, about 75 cycles each
-constexpr int kWarpLoad = 8, kLoadWarps = 4, kWarpS = 12, kWarpPV = 13, kWarpLook = 14;
-constexpr int kThreads = 15 * 32;
+constexpr int kAtom = 1024;                   // 8 rows of 64 columns
+// Two warps load: a copy instruction takes its operands from uniform registers, so
+// that a warp's lanes issue theirs one after another.
+constexpr int kSoftWarps = 16, kWarpLoad = 16, kLoadWarps = 2, kWarpS = 18, kWarpPV = 19;
+constexpr int kThreads = 20 * 32;
+constexpr int kParts = 4;                     // parts planned ahead, at most
 constexpr int kAhead = 3;                     // tiles whose pages are looked up ahead of their copies
 constexpr int kTmemCols = 512;                // S of both streams | O of both
 constexpr float kMaxSum = 65536.f;            // of a thread's 32 weights: they keep their relative precision up to there
@@ -60,21 +64,22 @@ constexpr int kFix = 8;                       // parts with new tokens that the 
 
 template <int D> struct Ring {
   static constexpr int tile = (D / 64) * kHalf;
+  static constexpr int group = (D / 64) * kAtom;         // 8 rows
   static constexpr int stages = D == 128 ? 5 : 10;
 };
 
 struct Ctl {
   uint64_t q_full[2], q_empty[2];
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t look_full[kMaxStages];             // value tiles that are looked through first, by ring slot
   uint64_t s_full[2], p_full[2], pv_done[2];             // by stream
   uint64_t x_full, o_empty;
+  uint64_t part_full[kParts], part_empty[kParts];
   unsigned long long fix[kFix];               // new tokens with values that are not finite
   uint32_t tmem_base;
   volatile int abort_flag;
   volatile int bad_page;                      // some page of this CTA's units is outside the pool
   float2 ml[2][128];                          // maximum and sum of each stream's rows
-  int64_t s_warp[kThreads / 32];
+  TreePart part[kParts];                      // what the CTA works at, planned ahead by the first load warp
 };
 
 constexpr int kCtlBytes = 3072;               // in front of the tiles, which start at multiples of 1024
@@ -84,8 +89,8 @@ static_assert(smem_bytes<128>() <= 227 * 1024 && smem_bytes<64>() <= 227 * 1024,
 
 // Which wait gave up: info = wait id << 16 | CTA.
 enum TreeWait : uint32_t {
-  W_Q_EMPTY = 1, W_EMPTY, W_Q_FULL, W_S_FREE, W_K_FULL, W_P_FULL, W_V_FULL, W_O_EMPTY, W_LOOK_FULL,
-  W_S_FULL, W_PV_DONE, W_O_FULL, W_X_FULL
+  W_Q_EMPTY = 1, W_EMPTY, W_Q_FULL, W_S_FREE, W_K_FULL, W_P_FULL, W_V_FULL, W_O_EMPTY,
+  W_S_FULL, W_PV_DONE, W_O_FULL, W_X_FULL, W_PART_FULL, W_PART_EMPTY
 };
 
 __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, Ctl* ctl, uint32_t* err, uint32_t which) {
@@ -161,13 +166,16 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-__device__ __forceinline__ void arrive_n(uint64_t* bar, uint32_t n) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(tc::smem_u32(bar)), "r"(n) : "memory");
+// Where piece c (16 bytes) of row m lies in a tile.
+template <int D> __device__ __forceinline__ uint32_t piece_at(int m, int c) {
+  return (m >> 3) * Ring<D>::group + (c >> 3) * kAtom + (m & 7) * 128 + (((c & 7) ^ (m & 7)) << 4);
 }
-
-// K-step kk (16 columns) of a 128-row K-major tile stored in 64-column halves.
-__device__ __forceinline__ uint64_t kmajor_step(uint32_t tile, int kk) {
-  return tc::smem_desc_k128(tile + (kk >> 2) * kHalf + (kk & 3) * 32);
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+// Arrives on the barrier, whose count provides for it, once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
 }
 
 __device__ __forceinline__ bool nonfinite2(uint32_t w) {
@@ -178,9 +186,6 @@ __device__ __forceinline__ uint32_t drop_nonfinite(uint32_t w) {
   if ((w & 0x7F800000u) == 0x7F800000u) w &= 0xFFFFu;
   return w;
 }
-
-// Out of line, as six roles call it once per part.
-__device__ __noinline__ bool next_of(const TreeArgs& a, TreeWalk& w, TreePart& p) { return next_part(a, w, p); }
 
 // Adds to a row of outputs (or of a part) the elements that are not finite of the values
 // of the new tokens in `left`: with them a sum is infinite or NaN whatever it was.
@@ -198,6 +203,17 @@ __device__ __noinline__ void add_nonfinite(T* dst, int n, unsigned long long lef
       if (!isfinite(x)) dst[e] = (T)((float)dst[e] + x);
     }
   }
+}
+
+// The CTA's part i (by a whole warp); false behind the last one.
+__device__ __forceinline__ bool take_part(Ctl* ctl, uint32_t& i, TreePart& p, uint32_t* err) {
+  const int at = i % kParts;
+  if (!wait32(&ctl->part_full[at], i / kParts, ctl, err, W_PART_FULL)) return false;
+  p = ctl->part[at];
+  __syncwarp();
+  if (threadIdx.x % 32 == 0) tc::mbar_arrive(&ctl->part_empty[at]);
+  ++i;
+  return p.nt > 0;
 }
 
 // What every role derives from a part.
@@ -229,7 +245,7 @@ template <int D, bool kGather>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                    const __grid_constant__ CUtensorMap mapV, const __grid_constant__ TreeArgs a, const int box) {
-  constexpr int kTile = Ring<D>::tile, kSt = Ring<D>::stages;
+  constexpr int kTile = Ring<D>::tile, kGroup = Ring<D>::group, kSt = Ring<D>::stages;
   constexpr int kColO = 2 * kKB;
   static_assert(kColO + 2 * D <= kTmemCols, "tensor memory");
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -248,12 +264,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&ctl->pv_done[i], 1);
     }
     for (int i = 0; i < kSt; ++i) {
-      tc::mbar_init(&ctl->full[i], kLoadWarps);
+      tc::mbar_init(&ctl->full[i], kGather ? kLoadWarps * 32 : kLoadWarps);
       tc::mbar_init(&ctl->empty[i], 1);
-      tc::mbar_init(&ctl->look_full[i], kLoadWarps);
     }
-    tc::mbar_init(&ctl->x_full, 256);
-    tc::mbar_init(&ctl->o_empty, 256);
+    tc::mbar_init(&ctl->x_full, kSoftWarps * 32);
+    tc::mbar_init(&ctl->o_empty, kSoftWarps * 32);
+    for (int i = 0; i < kParts; ++i) {
+      tc::mbar_init(&ctl->part_full[i], 1);
+      tc::mbar_init(&ctl->part_empty[i], kThreads / 32 - 1);       // every warp but the planning one
+    }
     ctl->abort_flag = 0;
     ctl->bad_page = 0;
     tc::fence_barrier_init();
@@ -268,49 +287,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = ctl->tmem_base;
   pdl_wait();
   pdl_trigger();
-  TreeWalk walk = start_walk<kThreads>(a, blockIdx.x, ctl->s_warp);
-  const bool work = walk.t < walk.end;        // uniform
   TreePart p{};
+  uint32_t part_at = 0;
 
-  if (!work) {
-  } else if (warp >= kWarpLoad && warp < kWarpLoad + kLoadWarps) {
+  if (warp >= kWarpLoad && warp < kWarpLoad + kLoadWarps) {
     // -------------------------------- loads --------------------------------
-    // a lane copies one box, or gathers a group of four rows
+    const int lw = warp - kWarpLoad;
     uint32_t it = 0, qn0 = 0, qn1 = 0;
     int qb = 0;
     bool ok = true;
-    constexpr int kG = kGather ? 4 : 1;       // pages that a lane looks up per tile
-    const int lw = warp - kWarpLoad;
-    const int n_box = kGather ? 32 : kKB / box;
-    const int rows = kGather ? 4 : box;       // of a group
-    // this lane's copy of a tile: its group (and half of the columns; a gathering lane takes both)
-    const int op = lane * kLoadWarps + lw, group = kGather ? op : op % n_box;
-    const int ops = kGather ? n_box : n_box * (D / 64);
-    const bool mine = op < ops;
-    const uint32_t share = (uint32_t)(ops - lw + kLoadWarps - 1) / kLoadWarps * (kTile / ops);       // bytes of the warp's
-    const int none = (int)(a.seq.n_pool_blocks * a.seq.block_size);       // a row outside the pool: reads as zeros
-    // the pages of this lane's rows of tile j (-2: no key there), and their first slot's place
-    auto entries = [&](int j, int (&page)[kG], int& in_page) {
-      const int key = j * kKB + group * rows, end = p.q.len + p.q.n;
-      const int32_t* table = a.seq.tables + (int64_t)p.s * a.seq.max_blocks;
-      int b = page_of(a.seq, key, &in_page), at = in_page;
+    // Boxes: every warp copies every second one, lane i knows its i-th one's page.
+    // Gathered rows: every warp takes 64 rows, a lane looks two pages up and copies
+    // pieces of all.
+    constexpr int kG = kGather ? 2 : 1;
+    const int n_box = kKB / box, my_ops = (n_box - lw + kLoadWarps - 1) / kLoadWarps;
+    const int none = -1, outside = (int)(a.seq.n_pool_blocks * a.seq.block_size / 8);       // its first group outside the pool
+    // the pages of this lane's keys of tile j (-2: no key there), and the slots' places
+    auto entries = [&](int j, int (&page)[kG], int (&in_page)[kG]) {
 #pragma unroll
       for (int i = 0; i < kG; ++i) {
-        page[i] = mine && key + i < end ? table[b] : -2;
-        if (++at == a.seq.block_size) {
-          at = 0;
-          ++b;
-        }
+        const int m = kGather ? lw * 64 + i * 32 + lane : (lane * kLoadWarps + lw) * box, key = j * kKB + m;
+        const int b = page_of(a.seq, key, &in_page[i]);
+        page[i] = m < kKB && key < p.q.len + p.q.n ? a.seq.tables[(int64_t)p.s * a.seq.max_blocks + b] : -2;
       }
     };
-    auto places = [&](const int (&page)[kG], int in_page, int (&row)[kG]) {
+    auto places = [&](const int (&page)[kG], const int (&in_page)[kG], int (&row)[kG]) {
       bool bad = false;
 #pragma unroll
       for (int i = 0; i < kG; ++i) {
-        int at = in_page + i;
-        if (kG > 1 && at >= a.seq.block_size) at %= a.seq.block_size;
         const bool there = page[i] >= 0 && page[i] < a.seq.n_pool_blocks;
-        row[i] = there ? page[i] * a.seq.block_size + at : none;
+        row[i] = there ? page[i] * a.seq.block_size + in_page[i] : none;
         bad |= !there && page[i] != -2;
       }
       if (bad) {
@@ -318,54 +324,76 @@ __global__ void __launch_bounds__(kThreads, 1)
         ctl->bad_page = 1;
       }
     };
-    auto issue = [&](const CUtensorMap* map, const void* pool, const int (&row)[kG], bool look) {
+    auto issue = [&](const CUtensorMap* map, const void* pool, const int (&row)[kG]) {
       const int st = it % kSt;
       if (!wait32(&ctl->empty[st], (it / kSt) ^ 1, ctl, err, W_EMPTY)) return false;
-      uint64_t* bar = look ? &ctl->look_full[st] : &ctl->full[st];
+      uint64_t* bar = &ctl->full[st];
       uint8_t* tile = sR + st * kTile;
-      uint32_t bytes = share;
-      bool whole = true;
       if constexpr (kGather) {
-        // groups that are not whole: by the lane's own loads and stores
-        whole = row[0] != none && row[1] != none && row[2] != none && row[3] != none;
-        const unsigned self = __ballot_sync(0xffffffffu, mine && !whole);
-        if (self) {
-          if (mine && !whole) {
-#pragma unroll 1
-            for (int i = 0; i < 4 * (D / 8); ++i) {
-              const int m = i / (D / 8), c = i % (D / 8);
-              const int y = m == 0 ? row[0] : m == 1 ? row[1] : m == 2 ? row[2] : row[3];
-              uint4 x = make_uint4(0, 0, 0, 0);
-              if (y != none)
-                x = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(pool) +
-                                                    ((int64_t)y * a.n_kv_heads + p.h) * D + c * 8);
-              const int at = group * 4 + m;
-              *reinterpret_cast<uint4*>(tile + (c >> 3) * kHalf + at * 128 + (((c & 7) ^ (at & 7)) << 4)) = x;
-            }
-            tc::fence_proxy_async_smem();
+        constexpr int kPieces = D / 8, kRows = 32 / kPieces;       // lanes of a row, rows at a time
+        const int c = lane % kPieces, sub = lane / kPieces;
+        const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(pool) + (int64_t)p.h * D + c * 8;
+        const int64_t step = (int64_t)a.n_kv_heads * D;
+        const uint32_t dst = tc::smem_u32(tile);
+#pragma unroll
+        for (int i = 0; i < kG; ++i)
+#pragma unroll
+          for (int k0 = 0; k0 < 32 / kRows; k0 += 8) {
+            int y[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = __shfl_sync(0xffffffffu, row[i], (k0 + k) * kRows + sub);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              cp16(dst + piece_at<D>(lw * 64 + i * 32 + (k0 + k) * kRows + sub, c), src + max(y[k], 0) * step, y[k] >= 0);
           }
-          bytes -= __popc(self) * 4 * D * 2;
+        if (ctl->bad_page) {                  // the flag has to be seen by who sees the tile
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          tc::mbar_arrive(bar);
+        } else {
+          cp_arrive(bar);
+        }
+      } else {
+        __syncwarp();                         // (bad_page is set before the barrier's phase can end)
+        if (lane == 0) tc::mbar_arrive_expect_tx(bar, my_ops * box * D * 2);
+        __syncwarp();
+        const int group = row[0] >= 0 ? row[0] >> 3 : outside;      // a group outside the pool reads as zeros
+#pragma unroll 1
+        for (int i = 0; i < my_ops; ++i) {
+          const int y = __shfl_sync(0xffffffffu, group, i);
+          if (tc::elect_one())
+            tc::tma_load_4d(tile + (i * kLoadWarps + lw) * box * D * 2, map, bar, 0, 0, p.h * (D / 64), y);
           __syncwarp();
         }
-      }
-      __syncwarp();                           // (bad_page is set before the barrier's phase can end)
-      if (lane == 0) tc::mbar_arrive_expect_tx(bar, bytes);
-      __syncwarp();
-      if constexpr (kGather) {
-        if (mine && whole)
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            tc::tma_gather4(tile + h * kHalf + group * 512, map, bar, p.h * D + 64 * h, row[0], row[1], row[2], row[3]);
-      } else if (mine) {
-        const int h = op / n_box;
-        tc::tma_load_3d(tile + h * kHalf + group * box * 128, map, bar, 64 * h, p.h, row[0]);
       }
       ++it;
       return true;
     };
-    while (ok && next_of(a, walk, p)) {
+    // the first warp plans: a part while the one before it is being loaded
+    TreeWalk walk;
+    if (lw == 0) walk = start_walk(a, blockIdx.x, blockIdx.x == 0);
+    auto plan = [&] {
+      TreePart next;
+      if (!next_part(a, walk, next)) next.nt = 0;
+      const int at = part_at % kParts;
+      if (!wait32(&ctl->part_empty[at], (part_at / kParts) ^ 1, ctl, err, W_PART_EMPTY)) next.nt = 0;
+      if (lane == 0) {
+        ctl->part[at] = next;
+        tc::mbar_arrive(&ctl->part_full[at]);
+      }
+      ++part_at;
+      return next;
+    };
+    TreePart ahead;
+    if (lw == 0) ahead = plan();
+    while (ok) {
+      if (lw == 0) {
+        p = ahead;
+        if (p.nt == 0) break;
+      } else if (!take_part(ctl, part_at, p, err)) {
+        break;
+      }
       const Steps u(p);
-      int page[kAhead][kG], in_page[kAhead], rc[kG], rn[kG];       // pages ahead; rows of the values' tile, of the keys'
+      int page[kAhead][kG], in_page[kAhead][kG], rc[kG], rn[kG];       // pages ahead; rows of the values' tile, of the keys'
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) entries(min(p.j0 + k, p.j1 - 1), page[k], in_page[k]);
       for (int m = 0; lw == 0 && m < (u.dual ? 2 : 1); ++m) {
@@ -386,23 +414,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!u.dual) qb ^= 1;
+      if (ok && lw == 0) ahead = plan();
       for (int i = 0; ok && i <= u.tiles; ++i) {
         if (i < u.tiles) {
           places(page[0], in_page[0], rn);
 #pragma unroll
           for (int k = 0; k + 1 < kAhead; ++k) {
 #pragma unroll
-            for (int g = 0; g < kG; ++g) page[k][g] = page[k + 1][g];
-            in_page[k] = in_page[k + 1];
+            for (int g = 0; g < kG; ++g) {
+              page[k][g] = page[k + 1][g];
+              in_page[k][g] = in_page[k + 1][g];
+            }
           }
           entries(min(p.j0 + i + kAhead, p.j1 - 1), page[kAhead - 1], in_page[kAhead - 1]);
-          ok = issue(&mapK, a.k_pool, rn, false);
+          ok = issue(&mapK, a.k_pool, rn);
         }
-        if (ok && i > 0) ok = issue(&mapV, a.v_pool, rc, has_new(p, p.j0 + i - 1));
+        if (ok && i > 0) ok = issue(&mapV, a.v_pool, rc);
 #pragma unroll
         for (int k = 0; k < kG; ++k) rc[k] = rn[k];
       }
     }
+    if (kGather) asm volatile("cp.async.wait_all;" ::: "memory");
     // copies in flight land before the CTA may end: all have been waited for where no
     // wait gave up
     if (!ok || ctl->abort_flag) {
@@ -416,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = 0, c0 = 0, c1 = 0, qn0 = 0, qn1 = 0;
     int qb = 0;
     bool ok = true;
-    while (ok && next_of(a, walk, p)) {
+    while (ok && take_part(ctl, part_at, p, err)) {
       const Steps u(p);
       if (u.dual || qb == 0) ok = wait32(&ctl->q_full[0], qn0++, ctl, err, W_Q_FULL);
       if (ok && (u.dual || qb == 1)) ok = wait32(&ctl->q_full[1], qn1++, ctl, err, W_Q_FULL);
@@ -436,12 +468,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
+        if (kGather) tc::fence_proxy_async_smem();         // the copies' writes are the generic proxy's
         tc::tc_fence_after();
         const uint32_t qa = tc::smem_u32(sQ) + (u.dual ? w : qb) * kTile, ka = tc::smem_u32(sR) + st * kTile;
         if (tc::elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            tc::mma_bf16(tmem + w * kKB, kmajor_step(qa, kk), kmajor_step(ka, kk), idesc, kk != 0);
+            tc::mma_bf16(tmem + w * kKB, tc::smem_desc_k128(qa + (kk >> 2) * kHalf + (kk & 3) * 32),
+                         tc::smem_desc_k128(ka + (kk >> 2) * kAtom + (kk & 3) * 32, kGroup), idesc, kk != 0);
           tc::mma_commit(&ctl->s_full[w]);
           if (!u.dual || w == 1) tc::mma_commit(&ctl->empty[st]);
           if (k == u.n - 1) {
@@ -461,27 +495,60 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kWarpPV) {
     // ------------------------------- O += P V -------------------------------
     constexpr uint32_t idesc = tc::idesc_bf16_f32(128, D, /*b_mn_major=*/true);
-    uint32_t it = 0, c0 = 0, c1 = 0, parts = 0;
+    uint32_t it = 0, c0 = 0, c1 = 0, parts = 0, with_new = 0;
     bool ok = true;
-    while (ok && next_of(a, walk, p)) {
+    while (ok && take_part(ctl, part_at, p, err)) {
       const Steps u(p);
+      unsigned long long found = 0;
       for (int k = 0; k < u.n; ++k) {
         const int w = k & 1, i = u.tile(k);
         const uint32_t q = it + u.v_item(i);
         const int st = q % kSt;
-        // P first: the ring's earlier items have been full by then
-        ok = wait32(&ctl->p_full[w], w ? c1 : c0, ctl, err, W_P_FULL) &&
-             wait32(&ctl->full[st], q / kSt, ctl, err, W_V_FULL);
+        // (what was in the ring's slot before has been full: it is a value tile of an
+        // earlier step, or a key tile whose weights have been waited for)
+        if (!wait32(&ctl->full[st], q / kSt, ctl, err, W_V_FULL)) {
+          ok = false;
+          break;
+        }
+        if (has_new(p, p.j0 + i) && (!u.dual || w == 0)) {
+          // the values of new tokens, and the rows behind them that a box brought along
+          constexpr int kPieces = D / 8, kRows = 32 / kPieces;
+          const int key0 = (p.j0 + i) * kKB;
+          const int n0 = max(p.q.len - key0, 0), n1 = min(kKB, p.q.len + p.q.n - key0);
+          const int n2 = kGather ? n1 : (n1 + box - 1) / box * box;
+          const int piece = lane % kPieces;
+          for (int m = n0 + lane / kPieces; m < n2; m += kRows) {
+            uint4* at = reinterpret_cast<uint4*>(sR + st * kTile + piece_at<D>(m, piece));
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (m < n1) {
+              x = *at;
+              if (!(nonfinite2(x.x) || nonfinite2(x.y) || nonfinite2(x.z) || nonfinite2(x.w))) continue;
+              x.x = drop_nonfinite(x.x);
+              x.y = drop_nonfinite(x.y);
+              x.z = drop_nonfinite(x.z);
+              x.w = drop_nonfinite(x.w);
+              found |= 1ull << (key0 + m - p.q.len);
+            }
+            *at = x;
+          }
+          tc::fence_proxy_async_smem();
+          found = (unsigned long long)__reduce_or_sync(0xffffffffu, (uint32_t)(found >> 32)) << 32 |
+                  __reduce_or_sync(0xffffffffu, (uint32_t)found);
+          if (lane == 0) ctl->fix[with_new % kFix] = found;     // read once this product is done
+          __syncwarp();
+        }
+        ok = wait32(&ctl->p_full[w], w ? c1 : c0, ctl, err, W_P_FULL);
         // the accumulators were last read at the end of the part before
         if (ok && k == 0) ok = wait32(&ctl->o_empty, parts ^ 1, ctl, err, W_O_EMPTY);
         if (!ok) break;
+        if (kGather) tc::fence_proxy_async_smem();
         tc::tc_fence_after();
         const uint32_t va = tc::smem_u32(sR) + st * kTile;
         if (tc::elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kKB / 16; ++kk)
             tc::mma_bf16_ts(tmem + kColO + w * D, tmem + w * kKB + kk * 8,
-                            tc::smem_desc_mn128(va + kk * 16 * 128, kHalf), idesc, (k > 1 || kk != 0) ? 1u : 0u);
+                            tc::smem_desc_mn128(va + kk * 2 * kGroup, kAtom, kGroup), idesc, (k > 1 || kk != 0) ? 1u : 0u);
           tc::mma_commit(&ctl->pv_done[w]);
           if (!u.dual || w == 1) tc::mma_commit(&ctl->empty[st]);
         }
@@ -493,96 +560,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       ++parts;
-      it += 2 * u.tiles;
-    }
-  } else if (warp == kWarpLook) {
-    // ------------------- values of new tokens looked through -------------------
-    constexpr int kPieces = D / 8, kRows = 32 / kPieces;
-    uint32_t it = 0, look = 0, with_new = 0;
-    bool ok = true;
-    while (ok && next_of(a, walk, p)) {
-      const Steps u(p);
-      unsigned long long found = 0;
-      bool any = false;
-      for (int i = 0; i < u.tiles; ++i) {
-        const int j = p.j0 + i;
-        if (!has_new(p, j)) continue;
-        any = true;
-        const int st = (it + u.v_item(i)) % kSt;
-        if (!wait32(&ctl->look_full[st], look >> st, ctl, err, W_LOOK_FULL)) {
-          ok = false;
-          break;
-        }
-        look ^= 1u << st;
-        const int key0 = j * kKB;
-        // the new tokens' rows, and those behind them that a box brought along
-        const int m0 = max(p.q.len - key0, 0), m1 = min(kKB, p.q.len + p.q.n - key0);
-        const int m2 = kGather ? m1 : (m1 + box - 1) / box * box;
-        const int piece = lane % kPieces;
-        bool changed = false;
-        for (int m = m0 + lane / kPieces; m < m2; m += kRows) {
-          uint4* at = reinterpret_cast<uint4*>(sR + st * kTile + (piece >> 3) * kHalf + m * 128 +
-                                               (((piece & 7) ^ (m & 7)) << 4));
-          if (m >= m1) {
-            *at = make_uint4(0, 0, 0, 0);
-            changed = true;
-            continue;
-          }
-          uint4 x = *at;
-          if (nonfinite2(x.x) || nonfinite2(x.y) || nonfinite2(x.z) || nonfinite2(x.w)) {
-            x.x = drop_nonfinite(x.x);
-            x.y = drop_nonfinite(x.y);
-            x.z = drop_nonfinite(x.z);
-            x.w = drop_nonfinite(x.w);
-            *at = x;
-            found |= 1ull << (key0 + m - p.q.len);
-            changed = true;
-          }
-        }
-        if (changed) tc::fence_proxy_async_smem();
-        found = (unsigned long long)__reduce_or_sync(0xffffffffu, (uint32_t)(found >> 32)) << 32 |
-                __reduce_or_sync(0xffffffffu, (uint32_t)found);
-        __syncwarp();
-        if (lane == 0) {
-          ctl->fix[with_new % kFix] = found;
-          arrive_n(&ctl->full[st], kLoadWarps);
-        }
-      }
-      with_new += any;
+      if (has_new(p, p.j1 - 1)) ++with_new;
       it += 2 * u.tiles;
     }
   } else if (warp < kWarpLoad) {
     // ------------------------------- softmax -------------------------------
-    // warp w: TMEM lane quarter w % 4, half w / 4 of it: 16 M rows, a thread two
-    // of them with 32 keys each
-    const int quarter = warp & 3, half = warp >> 2;
+    // a stream has eight warps: warp i of them TMEM lane quarter i % 4, half i / 4 of
+    // it: 16 M rows, a thread two of them with 32 keys each.  (Eight warps for both
+    // streams in turn: 440 us instead of @@ on 8 trees of 64 over 33k.)
+    const int w = warp >> 3, quarter = warp & 3, half = warp >> 2 & 1;
     const int base = quarter * 32 + half * 16;
     const int c4 = lane & 3;
     const int R0 = base + (lane >> 2), R1 = R0 + 8;
     const float scale = a.scale;
     const uint64_t sc2 = pack2(scale, scale);
-    uint32_t c0 = 0, c1 = 0, parts = 0, with_new = 0;       // steps of each stream, parts
-    while (next_of(a, walk, p)) {
+    const uint32_t tS = tmem + ((uint32_t)base << 16) + w * kKB;
+    uint32_t c = 0, other = 0, parts = 0, with_new = 0;     // steps of this stream and the other one, parts
+    while (take_part(ctl, part_at, p, err)) {
       const Steps u(p);
       const bool news = has_new(p, p.j1 - 1);
       Seen all{};
       if (news) all = seen_of_all(a.parents, p.q, err);
-      // of the stream at hand (m, l) and the other one (n, k): the rows' references
-      // (scores) and this thread's part of their sums; odd: some reference of the warp
-      // is -infinity or so large that the rounding of its product would show
+      // the rows' references (scores) and this thread's part of their sums; odd: some
+      // reference of the warp is -infinity or so large that the rounding of its
+      // product would show
       float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-      float n0 = -INFINITY, n1 = -INFINITY, k0 = 0.f, k1 = 0.f;
-      bool odd = true, odd_n = true;
-      bool ok = true;
-      for (int k = 0; k < u.n; ++k) {
-        const int w = k & 1, j = p.j0 + u.tile(k);
-        const uint32_t c = w ? c1 : c0;
+      bool odd = true, ok = true;
+      for (int k = w; k < u.n; k += 2, ++c) {
+        const int j = p.j0 + u.tile(k);
         if (!wait32(&ctl->s_full[w], c, ctl, err, W_S_FULL)) {
           ok = false;
           break;
         }
         tc::tc_fence_after();
-        const uint32_t tS = tmem + ((uint32_t)base << 16) + w * kKB;
         const bool bad = ctl->bad_page != 0;
         if (__builtin_expect(has_new(p, j) || bad, 0)) {
           // the scores of keys that a row does not see, replaced where they are
@@ -622,25 +632,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float al0 = 1.f, al1 = 1.f, s0, s1;   // factors of the sums so far; this tile's sums
         bool raise = odd || k < 2;            // uniform; a stream's first step sets the references
-        uint32_t r[64];
+        uint32_t y[32];                       // weights: key pairs of both rows
 #pragma unroll 1
         while (true) {
-          tc::tmem_ld_16x256b_x8(tS, *reinterpret_cast<uint32_t(*)[32]>(r));
-          tc::tmem_ld_16x256b_x8(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
-          tc::tmem_ld_wait();
-          float g0 = -m0 * scale, g1 = -m1 * scale;
+          float g0 = -m0 * scale, g1 = -m1 * scale, f0 = 0.f, f1 = 0.f;
           if (__builtin_expect(raise, 0)) {
-            float a0 = __uint_as_float(r[0]), a1 = __uint_as_float(r[1]);
-            float b0 = __uint_as_float(r[2]), b1 = __uint_as_float(r[3]);
+            float a0 = -INFINITY, b0 = -INFINITY;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              uint32_t r[32];
+              tc::tmem_ld_16x256b_x8(tS + 64 * h, r);
+              tc::tmem_ld_wait();
 #pragma unroll
-            for (int q = 1; q < 15; q += 2) {
-              a0 = max3(a0, __uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 4]));
-              a1 = max3(a1, __uint_as_float(r[4 * q + 1]), __uint_as_float(r[4 * q + 5]));
-              b0 = max3(b0, __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 6]));
-              b1 = max3(b1, __uint_as_float(r[4 * q + 3]), __uint_as_float(r[4 * q + 7]));
+              for (int q = 0; q < 8; ++q) {
+                a0 = max3(a0, __uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]));
+                b0 = max3(b0, __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
+              }
             }
-            a0 = max3(a0, a1, fmaxf(__uint_as_float(r[60]), __uint_as_float(r[61])));
-            b0 = max3(b0, b1, fmaxf(__uint_as_float(r[62]), __uint_as_float(r[63])));
 #pragma unroll
             for (int o = 1; o < 4; o <<= 1) {
               a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, o));
@@ -656,36 +664,43 @@ __global__ void __launch_bounds__(kThreads, 1)
               m1 = fmaxf(m1, b0);
             }
             // (a row whose every score so far is -infinity has weights of 0, not 2^(-inf + inf))
-            float f0 = m0 == -INFINITY ? 0.f : m0, f1 = m1 == -INFINITY ? 0.f : m1;
+            f0 = m0 == -INFINITY ? 0.f : m0;
+            f1 = m1 == -INFINITY ? 0.f : m1;
             const bool far = __any_sync(0xffffffffu, fmaxf(fabsf(f0), fabsf(f1)) * scale >= kFar);
             odd = far || __any_sync(0xffffffffu, m0 == -INFINITY || m1 == -INFINITY);
-            if (far) {                        // the differences first
-#pragma unroll
-              for (int q = 0; q < 64; ++q) r[q] = __float_as_uint(__uint_as_float(r[q]) - ((q & 2) ? f1 : f0));
-              f0 = f1 = 0.f;
-            }
-            g0 = -f0 * scale;
-            g1 = -f1 * scale;
+            g0 = far ? 0.f : -f0 * scale;     // far: the differences first
+            g1 = far ? 0.f : -f1 * scale;
+            if (!far) f0 = f1 = 0.f;
           }
           const uint64_t ng0 = pack2(g0, g0), ng1 = pack2(g1, g1);
           uint64_t acc0 = 0, acc1 = 0;        // (even keys, odd keys) of each row
 #pragma unroll
-          for (int q = 0; q < 16; ++q) {
-            const float2 x01 = unpack2(fma2(pack2(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1])), sc2, ng0));
-            const float2 x23 = unpack2(fma2(pack2(__uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3])), sc2, ng1));
-            const float e0 = ex2(x01.x), e1 = ex2(x01.y), e2 = ex2(x23.x), e3 = ex2(x23.y);
-            acc0 = add2(acc0, pack2(e0, e1));
-            acc1 = add2(acc1, pack2(e2, e3));
-            r[2 * q] = pack_bf16x2(e0, e1);
-            r[2 * q + 1] = pack_bf16x2(e2, e3);
+          for (int h = 0; h < 2; ++h) {
+            uint32_t r[32];
+            tc::tmem_ld_16x256b_x8(tS + 64 * h, r);
+            tc::tmem_ld_wait();
+            if (__builtin_expect(raise, 0)) {
+#pragma unroll
+              for (int q = 0; q < 32; ++q) r[q] = __float_as_uint(__uint_as_float(r[q]) - ((q & 2) ? f1 : f0));
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const float2 x01 = unpack2(fma2(pack2(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1])), sc2, ng0));
+              const float2 x23 = unpack2(fma2(pack2(__uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3])), sc2, ng1));
+              const float e0 = ex2(x01.x), e1 = ex2(x01.y), e2 = ex2(x23.x), e3 = ex2(x23.y);
+              acc0 = add2(acc0, pack2(e0, e1));
+              acc1 = add2(acc1, pack2(e2, e3));
+              y[16 * h + 2 * q] = pack_bf16x2(e0, e1);
+              y[16 * h + 2 * q + 1] = pack_bf16x2(e2, e3);
+            }
           }
-          const float2 y0 = unpack2(acc0), y1 = unpack2(acc1);
-          s0 = y0.x + y0.y;
-          s1 = y1.x + y1.y;
+          const float2 z0 = unpack2(acc0), z1 = unpack2(acc1);
+          s0 = z0.x + z0.y;
+          s1 = z1.x + z1.y;
           if (raise || __all_sync(0xffffffffu, fmaxf(s0, s1) <= kMaxSum && s0 == s0 && s1 == s1)) break;
           raise = true;                       // (a sum that is not a number among them)
         }
-        tc::tmem_st_16x128b_x16(tS, *reinterpret_cast<uint32_t(*)[32]>(r));
+        tc::tmem_st_16x128b_x16(tS, y);
         // the accumulator's rows, by the whole warp when any of them needs it (the
         // factor is 1 for the others), once the stream's step before has been added
         if (__builtin_expect(raise && __any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f), 0)) {
@@ -715,50 +730,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::mbar_arrive(&ctl->p_full[w]);
         l0 = l0 * al0 + s0;
         l1 = l1 * al1 + s1;
-        if (w)
-          ++c1;
-        else
-          ++c0;
-        // the other stream's turn
-        float z;
-        z = m0; m0 = n0; n0 = z;
-        z = m1; m1 = n1; n1 = z;
-        z = l0; l0 = k0; k0 = z;
-        z = l1; l1 = k1; k1 = z;
-        const bool y = odd;
-        odd = odd_n;
-        odd_n = y;
       }
       if (!ok) break;
+      other += (u.n + w) / 2;
       // the rows' references and sums to shared memory, in a fixed order
-      if (u.n & 1) {
-        float z;
-        z = m0; m0 = n0; n0 = z;
-        z = m1; m1 = n1; n1 = z;
-        z = l0; l0 = k0; k0 = z;
-        z = l1; l1 = k1; k1 = z;
-      }
 #pragma unroll
       for (int o = 1; o < 4; o <<= 1) {
         l0 += __shfl_xor_sync(0xffffffffu, l0, o);
         l1 += __shfl_xor_sync(0xffffffffu, l1, o);
-        k0 += __shfl_xor_sync(0xffffffffu, k0, o);
-        k1 += __shfl_xor_sync(0xffffffffu, k1, o);
       }
       // (of the part before they have been read once its accumulators have)
       if (parts > 0 && !wait32(&ctl->o_empty, parts - 1, ctl, err, W_O_EMPTY)) break;
       if (c4 == 0) {
-        ctl->ml[0][R0] = make_float2(m0 * scale, l0);
-        ctl->ml[0][R1] = make_float2(m1 * scale, l1);
-        ctl->ml[1][R0] = make_float2(n0 * scale, k0);
-        ctl->ml[1][R1] = make_float2(n1 * scale, k1);
+        ctl->ml[w][R0] = make_float2(m0 * scale, l0);
+        ctl->ml[w][R1] = make_float2(m1 * scale, l1);
       }
       tc::mbar_arrive(&ctl->x_full);
       if (!wait32(&ctl->x_full, parts, ctl, err, W_X_FULL)) break;
-      if (!wait32(&ctl->pv_done[0], c0 - 1, ctl, err, W_O_FULL)) break;
-      if (u.n > 1 && !wait32(&ctl->pv_done[1], c1 - 1, ctl, err, W_O_FULL)) break;
+      if (w < u.n && !wait32(&ctl->pv_done[w], c - 1, ctl, err, W_O_FULL)) break;
+      if (1 - w < u.n && !wait32(&ctl->pv_done[1 - w], other - 1, ctl, err, W_O_FULL)) break;
       tc::tc_fence_after();
-      // outputs: a thread one M row and half of its columns
+      // outputs: a thread one M row, with a half of its columns (of two M tiles) or a quarter
       const int row = quarter * 32 + lane;
       const bool whole = p.j0 == 0 && p.j1 == p.nt;
       const bool two = !u.dual && u.n > 1;    // one M tile: the streams' sums are added
@@ -768,7 +760,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         found = *(volatile unsigned long long*)&ctl->fix[with_new % kFix];
         ++with_new;
       }
-      for (int mt = 0; mt < (u.dual ? 2 : 1); ++mt) {
+      {
+        const int mt = u.dual ? w : 0, cols = u.dual ? D / 2 : D / 4;
+        const int e_begin = (u.dual ? half : warp >> 2) * cols;
         const int v = mt * 128 + row;
         const bool valid = v < p.n_vec;
         const int vi = p.vg * a.vecs + min(v, p.n_vec - 1), node = vi >> a.g_log2;
@@ -789,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tO = tmem + ((uint32_t)(quarter * 32) << 16) + kColO + mt * D;
         // (a short loop: a part's end runs once, out of a cold instruction cache)
 #pragma unroll 1
-        for (int e0 = half * (D / 2); e0 < (half + 1) * (D / 2); e0 += 8) {
+        for (int e0 = e_begin; e0 < e_begin + cols; e0 += 8) {
           uint32_t o[8], o1[8];
           tc::tmem_ld_32x32b_x8(tO + e0, o);
           if (two) tc::tmem_ld_32x32b_x8(tO + D + e0, o1);
@@ -809,13 +803,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
-        if (valid && !whole && half == 0) a.part_ml[slot + v] = make_float2(M, sum);
+        if (valid && !whole && e_begin == 0) a.part_ml[slot + v] = make_float2(M, sum);
         if (fix && valid) {                   // rare
-          const int e0 = half * (D / 2);
           if (whole)
-            add_nonfinite(out + e0, D / 2, fix, a, p, e0, D);
+            add_nonfinite(out + e_begin, cols, fix, a, p, e_begin, D);
           else
-            add_nonfinite(a.part_o + (slot + v) * D + e0, D / 2, fix, a, p, e0, D);
+            add_nonfinite(a.part_o + (slot + v) * D + e_begin, cols, fix, a, p, e_begin, D);
         }
         __syncwarp();
       }
@@ -852,19 +845,12 @@ template <int D> cudaError_t launch_d(const TreeArgs& a, cudaStream_t s) {
   const uint64_t sq[2] = {(uint64_t)D * 2, (uint64_t)a.n_q_heads * D * 2};
   const uint32_t bq[3] = {64, (uint32_t)a.g, (uint32_t)(128 / a.g)};
   if (!make_map_3d(&mQ, a.Q, dq, sq, bq)) return cudaErrorInvalidValue;
-  const int64_t rows = a.seq.n_pool_blocks * a.seq.block_size;
   // the rows of a box: a power of two that divides a page
   const int box = std::min(kKB, a.seq.block_size & -a.seq.block_size);
-  if (box < 8) {
-    if (!make_map_gather(&mK, a.k_pool, rows, (int64_t)a.n_kv_heads * D) ||
-        !make_map_gather(&mV, a.v_pool, rows, (int64_t)a.n_kv_heads * D))
-      return cudaErrorInvalidValue;
-    return launch_g<D, true>(mQ, mK, mV, a, box, s);
-  }
-  const uint64_t dk[3] = {(uint64_t)D, (uint64_t)a.n_kv_heads, (uint64_t)rows};
-  const uint64_t sk[2] = {(uint64_t)D * 2, (uint64_t)a.n_kv_heads * D * 2};
-  const uint32_t bk[3] = {64, 1, (uint32_t)box};
-  if (!make_map_3d(&mK, a.k_pool, dk, sk, bk) || !make_map_3d(&mV, a.v_pool, dk, sk, bk))
+  if (box < 8) return launch_g<D, true>(mQ, mQ, mQ, a, kKB, s);
+  const int64_t rows = a.seq.n_pool_blocks * a.seq.block_size, cols = (int64_t)a.n_kv_heads * D;
+  if (!make_map_groups(&mK, a.k_pool, rows, cols, D / 64, box / 8) ||
+      !make_map_groups(&mV, a.v_pool, rows, cols, D / 64, box / 8))
     return cudaErrorInvalidValue;
   return launch_g<D, false>(mQ, mK, mV, a, box, s);
 }

@@ -713,16 +713,18 @@ bool make_map_3d(CUtensorMap* m, const void* base, const uint64_t dims[3], const
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows of `cols` elements from which single rows of 64 elements are gathered (tile::gather4:
-// the box is one row high).
-bool make_map_gather(CUtensorMap* m, const void* base, int64_t rows, int64_t cols) {
+// Rows of `cols` elements (a multiple of 64; the rows a multiple of 8) as (64 elements, 8
+// rows, column blocks, row groups): a box of col_blocks and row_groups arrives as
+// [row group][column block][8 rows][64 elements].
+bool make_map_groups(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int col_blocks,
+                     int row_groups) {
   auto fn = encode_fn();
   if (!fn) return false;
-  cuuint64_t gd[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  cuuint64_t gs[1] = {(cuuint64_t)cols * 2};
-  cuuint32_t bx[2] = {64, 1};
-  cuuint32_t es[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), gd, gs, bx, es,
+  cuuint64_t gd[4] = {64, 8, (cuuint64_t)cols / 64, (cuuint64_t)rows / 8};
+  cuuint64_t gs[3] = {(cuuint64_t)cols * 2, 128, (cuuint64_t)cols * 16};
+  cuuint32_t bx[4] = {64, 8, (cuuint32_t)col_blocks, (cuuint32_t)row_groups};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), gd, gs, bx, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

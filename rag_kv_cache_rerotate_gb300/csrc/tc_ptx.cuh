@@ -225,14 +225,13 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
-// Four rows of a 2-D tensor, 64 elements each from column x on, one below the other.
-__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, uint64_t* bar, int x,
-                                            int y0, int y1, int y2, int y3) {
+// 4-D tiled load; x innermost (elements).
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int x, int y, int z, int w) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3),
-      "r"(smem_u32(bar))
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
 }
 
@@ -447,15 +446,15 @@ __device__ __forceinline__ void tmem_st_wait() {
 }
 
 // Shared-memory matrix descriptor of a K-major operand tile written by TMA
-// with 128-byte swizzling: rows of 128 bytes (64 bf16), 8-row groups 1024
-// bytes apart (stride byte offset), leading byte offset unused for this
+// with 128-byte swizzling: rows of 128 bytes (64 bf16), 8-row groups 1024 (or
+// group_bytes) bytes apart (stride byte offset), leading byte offset unused for this
 // layout, descriptor version 1 (bits 46-48), swizzle mode 2 = 128B (bits
 // 61-63).  The tile base must be 1024-byte aligned.
-__device__ __forceinline__ uint64_t smem_desc_k128(uint32_t saddr) {
+__device__ __forceinline__ uint64_t smem_desc_k128(uint32_t saddr, uint32_t group_bytes = 1024) {
   uint64_t d = 0;
   d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);           // start address
   d |= (uint64_t)(16u >> 4) << 16;                    // leading byte offset (unused)
-  d |= (uint64_t)(1024u >> 4) << 32;                  // stride byte offset
+  d |= (uint64_t)(group_bytes >> 4) << 32;            // stride byte offset
   d |= (uint64_t)1 << 46;                             // version
   d |= (uint64_t)2 << 61;                             // 128B swizzle
   return d;
@@ -466,11 +465,12 @@ __device__ __forceinline__ uint64_t smem_desc_k128(uint32_t saddr) {
 // index, 8 K rows form a 1024-byte swizzle atom (stride byte offset between
 // 8-row K groups), and the next 64 MN elements start mn_atom_bytes later
 // (leading byte offset).
-__device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t saddr, uint32_t mn_atom_bytes) {
+__device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t saddr, uint32_t mn_atom_bytes,
+                                                    uint32_t group_bytes = 1024) {
   uint64_t d = 0;
   d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
   d |= (uint64_t)((mn_atom_bytes >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)(group_bytes >> 4) << 32;
   d |= (uint64_t)1 << 46;
   d |= (uint64_t)2 << 61;
   return d;
