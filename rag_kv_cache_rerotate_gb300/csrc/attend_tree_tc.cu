@@ -2,7 +2,7 @@
 //
 // Work unit: one sequence, KV head and up to 256 query vectors (new token, query
 // head of the KV head), as one or two M = 128 tiles; keys stream in tiles of 128
-// through a ring in shared memory.  Two streams alternate, each with a score
+// through a ring in shared memory.  Two streams run side by side, each with a score
 // buffer and an accumulator of its own:
 //   two M tiles   stream w takes M tile w, both with the same keys
 //   one M tile    stream w takes every second key tile; the two softmaxes are
@@ -11,10 +11,13 @@
 //   S = Q K^T     tcgen05.mma into TMEM columns [128 w, 128 w + 128)
 //   P = 2^(S - m) eight warps a stream, in registers, bf16, written back over S
 //   O += P V      tcgen05.mma with A = P in TMEM, V MN-major in shared memory
+// (Two score buffers of 64 keys a stream would hide the hand-overs, but products of
+// N = 64 run at half the rate of N = 128: 526 us instead of 412 on 8 trees of 64
+// over 33k.  P in two halves, the first one's product beside the second's softmax: 479.)
 // The reference m is the first tile's maximum.  A later tile is weighed against it
 // as it stands, without its maximum being looked for: only where a thread's sum of
-// its weights passes 2^16 (no weight does otherwise) is the reference raised, O and
-// the running sum rescaled and the tile weighed once more.
+// its weights passes 2^16 (no weight does otherwise) is the row's reference raised, O
+// and the running sum rescaled and the tile weighed once more.
 //
 // Keys and values lie in pages.  With pages of a multiple of 8 tokens a tile is
 // copied by TMA boxes of as many rows as always lie in one page, whole heads: a copy
@@ -631,12 +634,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::tmem_st_wait();
         }
         float al0 = 1.f, al1 = 1.f, s0, s1;   // factors of the sums so far; this tile's sums
-        bool raise = odd || k < 2;            // uniform; a stream's first step sets the references
+        // Rows whose reference is set or raised now, and whose was in this step: each row by
+        // its own scores alone (the four lanes of a row agree).
+        bool want0 = k < 2 || m0 == -INFINITY, want1 = k < 2 || m1 == -INFINITY;
+        bool done0 = false, done1 = false;
+        bool any_want = odd;                  // uniform; `odd` before the first step
         uint32_t y[32];                       // weights: key pairs of both rows
 #pragma unroll 1
         while (true) {
-          float g0 = -m0 * scale, g1 = -m1 * scale, f0 = 0.f, f1 = 0.f;
-          if (__builtin_expect(raise, 0)) {
+          if (__builtin_expect(any_want, 0)) {
             float a0 = -INFINITY, b0 = -INFINITY;
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
@@ -654,23 +660,29 @@ __global__ void __launch_bounds__(kThreads, 1)
               a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, o));
               b0 = fmaxf(b0, __shfl_xor_sync(0xffffffffu, b0, o));
             }
-            if (k < 2) {
-              m0 = a0;
-              m1 = b0;
-            } else {
-              if (a0 > m0) al0 = ex2((m0 - a0) * scale);
-              if (b0 > m1) al1 = ex2((m1 - b0) * scale);
-              m0 = fmaxf(m0, a0);
-              m1 = fmaxf(m1, b0);
+            if (want0) {
+              if (k > 1 && m0 != -INFINITY && a0 > m0) al0 = ex2((m0 - a0) * scale);
+              m0 = k < 2 ? a0 : fmaxf(m0, a0);
+              done0 = true;
             }
-            // (a row whose every score so far is -infinity has weights of 0, not 2^(-inf + inf))
+            if (want1) {
+              if (k > 1 && m1 != -INFINITY && b0 > m1) al1 = ex2((m1 - b0) * scale);
+              m1 = k < 2 ? b0 : fmaxf(m1, b0);
+              done1 = true;
+            }
+            odd = __any_sync(0xffffffffu, !(fmaxf(fabsf(m0), fabsf(m1)) * scale < kFar));
+          }
+          float g0 = -m0 * scale, g1 = -m1 * scale, f0 = 0.f, f1 = 0.f;
+          if (__builtin_expect(odd, 0)) {
+            // rows whose every score so far is -infinity: weights of 0, not 2^(-inf + inf);
+            // rows whose scores are far: the differences first
             f0 = m0 == -INFINITY ? 0.f : m0;
             f1 = m1 == -INFINITY ? 0.f : m1;
-            const bool far = __any_sync(0xffffffffu, fmaxf(fabsf(f0), fabsf(f1)) * scale >= kFar);
-            odd = far || __any_sync(0xffffffffu, m0 == -INFINITY || m1 == -INFINITY);
-            g0 = far ? 0.f : -f0 * scale;     // far: the differences first
-            g1 = far ? 0.f : -f1 * scale;
-            if (!far) f0 = f1 = 0.f;
+            const bool far0 = fabsf(f0) * scale >= kFar, far1 = fabsf(f1) * scale >= kFar;
+            g0 = far0 ? 0.f : -f0 * scale;
+            g1 = far1 ? 0.f : -f1 * scale;
+            if (!far0) f0 = 0.f;
+            if (!far1) f1 = 0.f;
           }
           const uint64_t ng0 = pack2(g0, g0), ng1 = pack2(g1, g1);
           uint64_t acc0 = 0, acc1 = 0;        // (even keys, odd keys) of each row
@@ -679,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t r[32];
             tc::tmem_ld_16x256b_x8(tS + 64 * h, r);
             tc::tmem_ld_wait();
-            if (__builtin_expect(raise, 0)) {
+            if (__builtin_expect(odd, 0)) {
 #pragma unroll
               for (int q = 0; q < 32; ++q) r[q] = __float_as_uint(__uint_as_float(r[q]) - ((q & 2) ? f1 : f0));
             }
@@ -697,13 +709,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float2 z0 = unpack2(acc0), z1 = unpack2(acc1);
           s0 = z0.x + z0.y;
           s1 = z1.x + z1.y;
-          if (raise || __all_sync(0xffffffffu, fmaxf(s0, s1) <= kMaxSum && s0 == s0 && s1 == s1)) break;
-          raise = true;                       // (a sum that is not a number among them)
+          // (a sum that is not a number passes it too)
+          const bool over0 = !done0 && !(s0 <= kMaxSum), over1 = !done1 && !(s1 <= kMaxSum);
+          if (!__any_sync(0xffffffffu, over0 || over1)) break;
+          const uint32_t row = 0xFu << (lane & 28);
+          want0 = (__ballot_sync(0xffffffffu, over0) & row) != 0;
+          want1 = (__ballot_sync(0xffffffffu, over1) & row) != 0;
+          any_want = true;
         }
         tc::tmem_st_16x128b_x16(tS, y);
         // the accumulator's rows, by the whole warp when any of them needs it (the
         // factor is 1 for the others), once the stream's step before has been added
-        if (__builtin_expect(raise && __any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f), 0)) {
+        if (__builtin_expect(any_want && __any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f), 0)) {
           if (!wait32(&ctl->pv_done[w], c - 1, ctl, err, W_PV_DONE)) {
             ok = false;
             break;
