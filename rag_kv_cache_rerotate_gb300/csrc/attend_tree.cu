@@ -148,11 +148,12 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const __grid_con
 }
 
 // Joins the parts of one new token's query heads of one KV head (blockIdx.y), which
-// are vectors of the same unit.  8 / g warps take a vector, every one of them a
-// share of its parts, kRows of them in flight.  Latency bounds it, so what the
-// attention does not write (rows, lengths) is read before it is waited for.
-constexpr int kJoinWarps = 8;             // g is at most 8
-constexpr int kRows = 8;
+// are vectors of the same unit.  kWarps / g warps take a vector (a warp several, where
+// g is more), every one of them a share of its parts, kRows of them in flight.
+// Latency bounds it, so what the attention does not write (rows, lengths) is read
+// before it is waited for, and the first parts beside their weights.  Many rows have few
+// parts each: four warps.  Few rows may have many: sixteen.
+constexpr int kRows = 4;
 
 template <typename T> __device__ __forceinline__ void store4(T* p, float4 v);
 template <> __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
@@ -160,7 +161,7 @@ template <> __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
-template <typename T, int D>
+template <typename T, int D, int kJoinWarps>
 __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid_constant__ TreeArgs a) {
   constexpr int L = D / 4, kSub = 32 / L;  // lanes of a row, rows of a warp's read
   __shared__ float4 s_o[kJoinWarps * kSub][L];
@@ -172,78 +173,94 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid
   Seq q;
   if (!seq_of(a.seq, s, &q) || row < q.row0 || row >= q.row0 + q.n) return;
   const int nt = tiles_of(a, q), groups = (q.n * a.g + a.vecs - 1) >> a.vecs_log2;
-  const int per_vec = kJoinWarps >> a.g_log2;
-  const int j = warp / per_vec, share = warp % per_vec;
-  const int vi = (row - q.row0) * a.g + j, vg = vi >> a.vecs_log2, v = vi & (a.vecs - 1);
+  const int per_vec = max(1, kJoinWarps >> a.g_log2), share = warp % per_vec;
+  const int sub = lane / L, ch = lane % L * 4, step = per_vec * kSub, mine = share * kSub + sub;
   pdl_wait();
   const int64_t per = per_worker(a, a.start[a.seq.n_seq]);
+  const int v0 = (row - q.row0) * a.g, vg = v0 >> a.vecs_log2;
   const int64_t u0 = a.start[s] + (int64_t)(h * groups + vg) * nt;
-  const int64_t c0 = u0 / per, c1 = min((u0 + nt - 1) / per, (int64_t)a.workers - 1);
+  const int64_t u1 = u0 + nt - 1;
+  const int64_t c0 = u1 >> 32 ? u0 / per : (uint32_t)u0 / (uint32_t)per;
+  const int64_t c1 = min(u1 >> 32 ? u1 / per : (int64_t)((uint32_t)u1 / (uint32_t)per), (int64_t)a.workers - 1);
   if (c0 == c1) return;                   // written by its one worker
   const int parts = (int)(c1 - c0) + 1;
-  auto slot = [&](int i) { return ((c0 + i) * 2 + (i == 0 ? 1 : 0)) * a.vecs + v; };
-  float M = -INFINITY;
-  for (int i = lane; i < parts; i += 32) M = fmaxf(M, a.part_ml[slot(i)].x);
+  for (int j = warp / per_vec; j < a.g; j += kJoinWarps / per_vec) {
+    const int v = (v0 + j) & (a.vecs - 1);
+    auto slot = [&](int i) { return ((c0 + i) * 2 + (i == 0 ? 1 : 0)) * a.vecs + v; };
+    float4 x[kRows];
+    auto read = [&](int i) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float ref = M == -INFINITY ? 0.f : M;
-  const int sub = lane / L, ch = lane % L * 4;
-  float l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < parts; i0 += 32) {
-    const int n = min(32, parts - i0);
-    float w = -1.f;                       // of a part that saw no key, which is passed over
-    if (lane < n) {
-      const float2 ml = a.part_ml[slot(i0 + lane)];
-      if (!(ml.x == -INFINITY && ml.y == 0.f)) {
-        w = exp2f(ml.x - ref);
-        l = fmaf(w, ml.y, l);
-      }
-    }
-    const int step = per_vec * kSub;
-    for (int i = share * kSub; i < n; i += kRows * step) {
-      float4 x[kRows];
-      float f[kRows];
+      for (int k = 0; k < kRows; ++k)
+        if (i + k * step + mine < parts)
+          x[k] = *reinterpret_cast<const float4*>(a.part_o + slot(i + k * step + mine) * D + ch);
+    };
+    read(0);
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < parts) ml = a.part_ml[slot(lane)];
+    float M = ml.x;
+    for (int i = lane + 32; i < parts; i += 32) M = fmaxf(M, a.part_ml[slot(i)].x);
 #pragma unroll
-      for (int k = 0; k < kRows; ++k) {
-        const int at = i + k * step + sub;
-        f[k] = __shfl_sync(0xffffffffu, w, at & 31);
-        if (at >= n) f[k] = -1.f;
-        if (f[k] != -1.f) x[k] = *reinterpret_cast<const float4*>(a.part_o + slot(i0 + at) * D + ch);
-      }
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float ref = M == -INFINITY ? 0.f : M;
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < parts; i += kRows * step) {
+      if (i > 0) read(i);
 #pragma unroll
       for (int k = 0; k < kRows; ++k) {
-        if (f[k] == -1.f) continue;
-        o.x = fmaf(f[k], x[k].x, o.x);
-        o.y = fmaf(f[k], x[k].y, o.y);
-        o.z = fmaf(f[k], x[k].z, o.z);
-        o.w = fmaf(f[k], x[k].w, o.w);
+        const int at = i + k * step + mine;
+        // a lane's weight (of a part that saw no key: none; what is there is not used)
+        float2 w = ml;
+        if (parts > 32) {                 // uniform
+          w = at < parts ? a.part_ml[slot(at)] : make_float2(-INFINITY, 0.f);
+        } else {
+          w.x = __shfl_sync(0xffffffffu, ml.x, at & 31);
+          w.y = __shfl_sync(0xffffffffu, ml.y, at & 31);
+        }
+        if (at >= parts || (w.x == -INFINITY && w.y == 0.f)) continue;
+        const float f = exp2f(w.x - ref);
+        l = fmaf(f, w.y, l);
+        o.x = fmaf(f, x[k].x, o.x);
+        o.y = fmaf(f, x[k].y, o.y);
+        o.z = fmaf(f, x[k].z, o.z);
+        o.w = fmaf(f, x[k].w, o.w);
       }
     }
-  }
-#pragma unroll
-  for (int e = 16; e > 0; e >>= 1) l += __shfl_xor_sync(0xffffffffu, l, e);
-  if (per_vec * kSub > 1) {
-    s_o[warp * kSub + sub][lane % L] = o;
-    __syncthreads();
-    if (share != 0 || sub != 0) return;
-    for (int k = 1; k < per_vec * kSub; ++k) {
-      const float4 x = s_o[warp * kSub + k][lane];
-      o.x += x.x;
-      o.y += x.y;
-      o.z += x.z;
-      o.w += x.w;
+    if (step > 1) {                       // the vector's shares (one pass where there are several)
+      __shared__ float s_l[kJoinWarps * kSub];
+      s_o[warp * kSub + sub][lane % L] = o;
+      if (lane % L == 0) s_l[warp * kSub + sub] = l;
+      if (per_vec > 1)
+        __syncthreads();
+      else
+        __syncwarp();
+      if (mine == 0) {
+        for (int k = 1; k < step; ++k) {
+          const float4 y = s_o[warp * kSub + k][lane];
+          o.x += y.x;
+          o.y += y.y;
+          o.z += y.z;
+          o.w += y.w;
+          l += s_l[warp * kSub + k];
+        }
+      }
+      __syncwarp();
     }
+    if (mine == 0)
+      store4(reinterpret_cast<T*>(a.O) + ((int64_t)row * a.n_q_heads + h * a.g + j) * D + ch,
+             make_float4(o.x / l, o.y / l, o.z / l, o.w / l));
   }
-  store4(reinterpret_cast<T*>(a.O) + ((int64_t)row * a.n_q_heads + h * a.g + j) * D + ch,
-         make_float4(o.x / l, o.y / l, o.z / l, o.w / l));
 }
 
-template <typename T>
-cudaError_t launch_join(const TreeArgs& a, int d, cudaStream_t s) {
+template <typename T, int D>
+cudaError_t launch_join_d(const TreeArgs& a, cudaStream_t s) {
   const dim3 grid((unsigned)a.seq.n_rows, a.n_kv_heads);
-  return d == 128 ? launch_pdl(tree_join_kernel<T, 128>, grid, dim3(kJoinWarps * 32), 0, s, a)
-                  : launch_pdl(tree_join_kernel<T, 64>, grid, dim3(kJoinWarps * 32), 0, s, a);
+  if (a.seq.n_rows * a.n_kv_heads <= 304)
+    return launch_pdl(tree_join_kernel<T, D, 16>, grid, dim3(16 * 32), 0, s, a);
+  return launch_pdl(tree_join_kernel<T, D, 4>, grid, dim3(4 * 32), 0, s, a);
+}
+template <typename T> cudaError_t launch_join(const TreeArgs& a, int d, cudaStream_t s) {
+  return d == 128 ? launch_join_d<T, 128>(a, s) : launch_join_d<T, 64>(a, s);
 }
 
 // ---- host side ---------------------------------------------------------------
