@@ -69,14 +69,17 @@ __device__ __forceinline__ TileScan scan_tiles(const TreeArgs& a, int s0) {
   const int lane = threadIdx.x % 32;
   TileScan r;
   int64_t sum = 0;
+  // (all reads before the first check, whose report would hold the next ones up)
+  const int s1 = s0 + lane * 4;
+  int row[5], len[4];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) row[i] = a.seq.rows[min(s1 + i, a.seq.n_seq)];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) len[i] = a.seq.lens[min(s1 + i, a.seq.n_seq - 1)];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     r.q[i] = Seq{0, 0, 0};
-    const int s = s0 + lane * 4 + i;
-    if (s < a.seq.n_seq) seq_of(a.seq, s, &r.q[i]);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
+    if (s1 + i < a.seq.n_seq) check_seq(a.seq, s1 + i, row[i], row[i + 1], len[i], &r.q[i]);
     r.own[i] = (int64_t)units_of(a, r.q[i]) * tiles_of(a, r.q[i]);
     sum += r.own[i];
   }

@@ -35,9 +35,9 @@ struct Seq {
   int row0, n, len;
 };
 
-// Whether sequence s can be used as it stands (else it is recorded, and has no rows).
-__device__ __forceinline__ bool seq_of(const SeqArgs& a, int s, Seq* q) {
-  const int r0 = a.rows[s], r1 = a.rows[s + 1], len = a.lens[s];
+// Whether sequence s, whose row starts and length these are, can be used as it stands (else
+// it is recorded, and has no rows).
+__device__ __forceinline__ bool check_seq(const SeqArgs& a, int s, int r0, int r1, int len, Seq* q) {
   q->row0 = r0;
   q->len = len;
   q->n = (int)((uint32_t)r1 - (uint32_t)r0);
@@ -48,6 +48,10 @@ __device__ __forceinline__ bool seq_of(const SeqArgs& a, int s, Seq* q) {
     return false;
   }
   return true;
+}
+__device__ __forceinline__ bool seq_of(const SeqArgs& a, int s, Seq* q) {
+  const int r0 = a.rows[s], r1 = a.rows[s + 1], len = a.lens[s];
+  return check_seq(a, s, r0, r1, len, q);
 }
 
 // The parent of new token i (-1: none); one out of range is recorded.

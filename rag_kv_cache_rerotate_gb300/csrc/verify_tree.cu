@@ -11,8 +11,10 @@
 //
 // The next token is the first x whose running sum passes u' S.  A rounding of
 // the sums to fp32 would move that border over several tokens of a large
-// vocabulary, so entries and sums are pairs of floats (48 bits) and sums
-// of sums are fp64.
+// vocabulary, so entries and sums are pairs of floats (48 bits).  fp64 is left to
+// the tests of acceptance, a node a thread: an fp64 instruction of sixteen warps keeps
+// an SM busy for some 250 cycles (with fp64 sums and tests in every thread the
+// call on 64 trees took 114 us instead of @@).
 //
 // One cluster per sequence, the vocabulary split over its CTAs, their warps'
 // sums exchanged through distributed shared memory.  Latency bounds it: a chain of
@@ -58,17 +60,46 @@ __device__ __forceinline__ void two_sum(float x, float y, float& s, float& e) {
   const float b = s - x;
   e = (x - (s - b)) + (y - b);
 }
+// A number as the sum of two floats, the second below half a step of the first.
+struct Pair {
+  float h, l;
+};
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  float s, e;
+  two_sum(a.h, b.h, s, e);
+  e += a.l + b.l;
+  Pair r;
+  r.h = s + e;
+  r.l = e - (r.h - s);
+  return r;
+}
+__device__ __forceinline__ bool greater(Pair a, Pair b) {
+  float s, e;
+  two_sum(a.h, -b.h, s, e);
+  return s + (e + (a.l - b.l)) > 0.f;
+}
+__device__ __forceinline__ Pair shfl_xor(Pair a, int o) {
+  return Pair{__shfl_xor_sync(0xffffffffu, a.h, o), __shfl_xor_sync(0xffffffffu, a.l, o)};
+}
+// Sum over the lanes before this one and this one.
+__device__ __forceinline__ Pair scan(Pair a) {
+  const int lane = threadIdx.x % 32;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Pair z{__shfl_up_sync(0xffffffffu, a.h, o), __shfl_up_sync(0xffffffffu, a.l, o)};
+    if (lane >= o) a = add(z, a);
+  }
+  return a;
+}
 
-// max(p - A q, 0) as a pair of floats, A = ah + al.
-__device__ __forceinline__ void remainder_of(float p, float q, float ah, float al, float& hi, float& lo) {
-  const float m = ah * q;
-  const float me = fmaf(ah, q, -m);
+// max(p - A q, 0) as a pair.
+__device__ __forceinline__ Pair remainder_of(float p, float q, Pair A) {
+  const float m = A.h * q;
+  const float me = fmaf(A.h, q, -m);
   float s, e;
   two_sum(p, -m, s, e);
-  e = (e - me) - al * q;
-  const bool pos = s + e > 0.f;
-  hi = pos ? s : 0.f;
-  lo = pos ? e : 0.f;
+  e = (e - me) - A.l * q;
+  return s + e > 0.f ? Pair{s, e} : Pair{0.f, 0.f};
 }
 
 // A row's entries [4 i - lead, 4 i - lead + 4), those outside the row as 0.  The rows of a
@@ -95,26 +126,25 @@ __device__ __forceinline__ float usable(float x, bool& bad) {
 struct Pass {
   const float* p;
   const float* q;                         // null: p alone
-  float ah, al;
+  Pair A;
   int lead;
   bool wide;
   int n_gone;                             // refused tokens whose entry is 0 (without q)
 };
 
 __device__ __forceinline__ void entries(const Pass& y, const float4& pv, const float4& qv, int i,
-                                        const int* s_gone, bool& bad, float (&hi)[4], float (&lo)[4]) {
+                                        const int* s_gone, bool& bad, Pair (&r)[4]) {
   const float p[4] = {pv.x, pv.y, pv.z, pv.w}, q[4] = {qv.x, qv.y, qv.z, qv.w};
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    hi[k] = usable(p[k], bad);
-    lo[k] = 0.f;
-    if (y.q) remainder_of(hi[k], usable(q[k], bad), y.ah, y.al, hi[k], lo[k]);
+    r[k] = Pair{usable(p[k], bad), 0.f};
+    if (y.q) r[k] = remainder_of(r[k].h, usable(q[k], bad), y.A);
   }
   for (int g = 0; g < y.n_gone; ++g) {
     const int at = s_gone[g] - (4 * i - y.lead);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (at == k) hi[k] = 0.f;
+      if (at == k) r[k].h = 0.f;
   }
 }
 
@@ -123,11 +153,13 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
   const int n_ctas = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   const int s = blockIdx.x / n_ctas;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  __shared__ double s_sum[2][kWarps];     // this CTA's warps' sums, by the pass's parity
-  __shared__ double s_all[kMaxCluster * kWarps];
-  __shared__ double s_scan[kWarps];
-  __shared__ int s_parent[kNodes], s_token[kNodes], s_gone[kNodes], s_path[kNodes];
-  __shared__ float s_p[kNodes], s_q[kNodes], s_u[kNodes];
+  constexpr int kEach = kMaxCluster * kWarps / 32;         // sums a lane holds
+  __shared__ Pair s_sum[2][kWarps];       // this CTA's warps' sums, by the pass's parity
+  __shared__ Pair s_scan[kWarps];
+  __shared__ int s_token[kNodes], s_gone[kNodes], s_path[kNodes];
+  __shared__ float s_p[kNodes];
+  __shared__ unsigned long long s_child[kNodes];           // a node's children, a bit each
+  __shared__ unsigned int s_ok[2];        // nodes that pass the test as it stands
   __shared__ int s_found[2];
   pdl_wait();
   pdl_trigger();
@@ -138,11 +170,16 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
     if (tid == 0) report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_SEQ_ROWS, (uint32_t)s);
     n = 0;
   }
-  // every node's parent, token and probabilities at its parent
+  // every node's parent, token and probabilities at its parent, a node a thread
+  int par = -1, tok = 0;
+  float pd = 0.f, qd = 0.f, ud = 0.f;
+  if (tid < kNodes) s_child[tid] = 0;
+  if (tid < 2) s_ok[tid] = 0;
   if (tid < n) {
     const int row = r0 + tid;
-    int par = a.parents[row], tok = a.tokens[row];
-    float p = 0.f, q = 0.f;
+    par = a.parents[row];
+    tok = a.tokens[row];
+    ud = a.u[row];
     bool bad = false;
     if (tid > 0) {
       if (par < 0 || par >= tid) {
@@ -152,37 +189,61 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
         report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_VERIFY_TOKEN, (uint32_t)row);
         par = -1;
       } else {
-        p = usable(a.P[(int64_t)(r0 + par) * a.p_stride + tok], bad);
-        if (a.Q) q = usable(a.Q[(int64_t)(r0 + par) * a.q_stride + tok], bad);
+        pd = a.P[(int64_t)(r0 + par) * a.p_stride + tok];
+        if (a.Q) qd = a.Q[(int64_t)(r0 + par) * a.q_stride + tok];
+        pd = usable(pd, bad);
+        qd = usable(qd, bad);
       }
+    } else {
+      par = -1;
     }
     if (bad) report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_VERIFY_PROB, (uint32_t)row);
-    s_parent[tid] = par;
     s_token[tid] = tok;
-    s_p[tid] = p;
-    s_q[tid] = q;
-    s_u[tid] = a.u[row];
+    s_p[tid] = pd;
   }
   __syncthreads();
-  const int W = n_ctas * kWarps;
+  if (par >= 0) atomicOr(&s_child[par], 1ull << tid);
+  // the tests of the nodes in `which` against the remainder A, S: bits in s_ok (call
+  // between barriers)
   Pass y;
   y.q = nullptr;
-  y.ah = y.al = 0.f;
+  y.A = Pair{0.f, 0.f};
   y.n_gone = 0;
+  auto test = [&](unsigned long long which, Pair A, double S) {
+    if (warp >= kNodes / 32) return;
+    bool yes = false;
+    if (par >= 0 && (which >> tid & 1)) {
+      double r = pd;
+      if (a.Q) {
+        r = (double)pd - ((double)A.h + A.l) * (double)qd;
+        yes = r > 0.0 && (double)ud * S * (double)qd < r;
+      } else {
+        for (int g = 0; g < y.n_gone; ++g)
+          if (s_gone[g] == tok) r = 0.0;
+        yes = r > 0.0 && (double)ud * S < r;
+      }
+    }
+    const unsigned int bits = __ballot_sync(0xffffffffu, yes);
+    if (lane == 0) s_ok[warp] = bits;
+  };
+  test(~0ull, y.A, 1.0);                  // as first children
+  __syncthreads();
+  const unsigned long long first_ok = (unsigned long long)s_ok[1] << 32 | s_ok[0];
+  const int W = n_ctas * kWarps;
   int groups = 0, seg = 0;                // groups of four of a row, and of a warp's part
   int parity = 0;
-  // the remainder's sums: every warp's of the cluster in s_all; returns their total
-  auto pass = [&](int node, double A) -> double {
+  Pair v[kEach];                          // every warp's sum of the last pass: lane L holds those from kEach L on
+  // the remainder's sums; returns their total
+  auto pass = [&](int node, Pair A) -> Pair {
     y.p = a.P + (int64_t)(r0 + node) * a.p_stride;
-    y.q = A > 0.0 ? a.Q + (int64_t)(r0 + node) * a.q_stride : nullptr;
-    y.ah = (float)A;
-    y.al = (float)(A - (double)y.ah);
+    y.q = A.h > 0.f ? a.Q + (int64_t)(r0 + node) * a.q_stride : nullptr;
+    y.A = A;
     y.lead = (int)((reinterpret_cast<uintptr_t>(y.p) >> 2) & 3u);
     y.wide = !y.q || (int)((reinterpret_cast<uintptr_t>(y.q) >> 2) & 3u) == y.lead;
     groups = (a.vocab + y.lead + 3) / 4;
     seg = (groups + W - 1) / W;
     const int g0 = (rank * kWarps + warp) * seg, g1 = min(groups, g0 + seg);
-    float sh = 0.f, sl = 0.f;
+    Pair sum{0.f, 0.f};
     bool bad = false;
     for (int g = g0 + lane; g < g1; g += 32 * kAhead) {
       float4 pv[kAhead], qv[kAhead];
@@ -197,125 +258,129 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
       }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        float hi[4], lo[4];
-        entries(y, pv[k], qv[k], g + 32 * k, s_gone, bad, hi, lo);
+        Pair r[4];
+        entries(y, pv[k], qv[k], g + 32 * k, s_gone, bad, r);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float t;
-          two_sum(sh, hi[e], sh, t);
-          sl += t + lo[e];
+          two_sum(sum.h, r[e].h, sum.h, t);
+          sum.l += t + r[e].l;
         }
       }
     }
-    double t = (double)sh + (double)sl;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    if (lane == 0) s_sum[parity][warp] = t;
+    for (int o = 16; o > 0; o >>= 1) sum = add(sum, shfl_xor(sum, o));
+    if (lane == 0) s_sum[parity][warp] = sum;
     if (bad) report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_VERIFY_PROB, (uint32_t)(r0 + node));
     cl.sync();
-    if (tid < W) s_all[tid] = *cl.map_shared_rank(&s_sum[parity][tid % kWarps], tid / kWarps);
-    __syncthreads();
+    Pair all{0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int w = lane * kEach + k;
+      v[k] = Pair{0.f, 0.f};
+      if (w < W) v[k] = *cl.map_shared_rank(&s_sum[parity][w % kWarps], w / kWarps);
+      all = add(all, v[k]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) all = add(all, shfl_xor(all, o));
     parity ^= 1;
-    double all = 0.0;
-#pragma unroll
-    for (int k = 0; k < kMaxCluster * kWarps / 32; ++k)
-      if (lane + 32 * k < W) all += s_all[lane + 32 * k];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
     return all;
   };
 
   // the walk, the same in every thread of the cluster
   int cur = 0, kept = n > 0 ? 1 : 0;
-  double A = 0.0, S = 1.0;
-  bool summed = false;                    // s_all holds the sums of the remainder as it stands
+  Pair A{0.f, 0.f}, S{1.f, 0.f};
+  double s_left = 1.0;                    // without q: what refusals leave of 1
+  bool summed = false;                    // v holds the sums of the remainder as it stands
+  unsigned long long left = n > 0 ? s_child[0] : 0, ok = first_ok;
   if (tid == 0) s_path[0] = 0;
-  for (int i = 1; i < n; ++i) {
-    if (s_parent[i] != cur) continue;     // uniform
-    const int x = s_token[i];
-    const double p = s_p[i], u = s_u[i];
-    double r = p;
-    bool yes;
-    if (a.Q) {
-      const double q = s_q[i];
-      r = fmax(p - A * q, 0.0);
-      yes = r > 0.0 && u * S * q < r;
-    } else {
-      for (int g = 0; g < y.n_gone; ++g)
-        if (s_gone[g] == x) r = 0.0;
-      yes = r > 0.0 && u * S < r;
-    }
-    if (yes) {
-      cur = i;
-      if (tid == 0) s_path[kept] = i;
+  while (left) {
+    const int c = __ffsll(left) - 1;
+    left &= left - 1;
+    if (ok >> c & 1) {                    // on to it
+      cur = c;
+      if (tid == 0) s_path[kept] = c;
       ++kept;
-      A = 0.0;
-      S = 1.0;
-      __syncthreads();                    // s_gone is read above
+      A = Pair{0.f, 0.f};
+      S = Pair{1.f, 0.f};
+      s_left = 1.0;
       y.n_gone = 0;
       summed = false;
-    } else if (a.Q) {
-      A += S;
+      left = s_child[c];
+      ok = first_ok;
+      continue;
+    }
+    if (a.Q) {
+      A = add(A, S);
       S = pass(cur, A);
       summed = true;
     } else {
-      S -= r;
+      const int x = s_token[c];
+      bool again = false;
+      for (int g = 0; g < y.n_gone; ++g) again |= s_gone[g] == x;
+      __syncthreads();                    // s_gone is read above
+      if (!again) {
+        s_left -= (double)s_p[c];
+        if (tid == 0) s_gone[y.n_gone] = x;
+        ++y.n_gone;
+      }
+    }
+    if (left) {
+      __syncthreads();                    // s_gone; s_ok has been read
+      test(left, A, a.Q ? (double)S.h + S.l : s_left);
       __syncthreads();
-      if (tid == 0) s_gone[y.n_gone] = x;
-      ++y.n_gone;
-      __syncthreads();
+      ok = (unsigned long long)s_ok[1] << 32 | s_ok[0];
     }
   }
+  __syncthreads();                        // s_gone, s_path
   int token = -1;
+  bool mine = rank == 0;                  // this CTA writes the results
   if (n > 0) {
-    double sum = summed ? S : pass(cur, A);
-    if (!(sum > 0.0)) {                   // nothing left: the target's own row
+    Pair sum = summed ? S : pass(cur, A);
+    if (!(sum.h > 0.f)) {                 // nothing left: the target's own row
       y.n_gone = 0;
-      sum = pass(cur, 0.0);
+      sum = pass(cur, Pair{0.f, 0.f});
     }
-    // the first warp's part whose running sum passes t
-    const double t = (un > 0.f ? (double)fminf(un, 0.99999994f) : 0.0) * sum;
-    double before = 0.0;
-    int part = -1, last = -1;             // last: the last part that holds anything
-    {
-      constexpr int kEach = kMaxCluster * kWarps / 32;
-      double v[kEach], own = 0.0;
-      int full = -1;
+    // t = u' sum; the first warp's part whose running sum passes it
+    const float uc = un > 0.f ? fminf(un, 0.99999994f) : 0.f;
+    Pair t;
+    t.h = uc * sum.h;
+    t.l = fmaf(uc, sum.h, -t.h) + uc * sum.l;
+    Pair own{0.f, 0.f};
+    int full = -1;                        // the last part that holds anything
 #pragma unroll
-      for (int k = 0; k < kEach; ++k) {
-        const int w = lane * kEach + k;
-        v[k] = w < W ? s_all[w] : 0.0;
-        own += v[k];
-        if (v[k] > 0.0) full = w;
-      }
-      double inc = own;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double z = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += z;
-      }
-      double c = inc - own;
-      int mine = INT32_MAX;
-      double mine_before = 0.0;
-#pragma unroll
-      for (int k = 0; k < kEach; ++k) {
-        if (mine == INT32_MAX && v[k] > 0.0 && c + v[k] > t) {
-          mine = lane * kEach + k;
-          mine_before = c;
-        }
-        c += v[k];
-      }
-      part = (int)__reduce_min_sync(0xffffffffu, (unsigned)mine);
-      last = __reduce_max_sync(0xffffffffu, full);
-      const unsigned who = __ballot_sync(0xffffffffu, mine == part && part != INT32_MAX);
-      if (who) {
-        before = __shfl_sync(0xffffffffu, mine_before, __ffs(who) - 1);
-      } else {
-        part = last;                      // t within the sums' rounding of their total
-        before = INFINITY;                // its last entry
-      }
+    for (int k = 0; k < kEach; ++k) {
+      own = add(own, v[k]);
+      if (v[k].h > 0.f) full = lane * kEach + k;
     }
-    if (part >= 0 && part / kWarps == rank) {
+    const Pair inc = scan(own);
+    Pair c = Pair{__shfl_up_sync(0xffffffffu, inc.h, 1), __shfl_up_sync(0xffffffffu, inc.l, 1)};
+    if (lane == 0) c = Pair{0.f, 0.f};
+    int at = INT32_MAX;
+    Pair before{0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const Pair next = add(c, v[k]);
+      if (at == INT32_MAX && v[k].h > 0.f && greater(next, t)) {
+        at = lane * kEach + k;
+        before = c;
+      }
+      c = next;
+    }
+    int part = (int)__reduce_min_sync(0xffffffffu, (unsigned)at);
+    const int last = __reduce_max_sync(0xffffffffu, full);
+    const unsigned who = __ballot_sync(0xffffffffu, at == part && part != INT32_MAX);
+    const bool end = who == 0;            // t within the sums' rounding of their total: the last entry
+    if (end) {
+      part = last;
+    } else {
+      before.h = __shfl_sync(0xffffffffu, before.h, __ffs(who) - 1);
+      before.l = __shfl_sync(0xffffffffu, before.l, __ffs(who) - 1);
+    }
+    mine = part >= 0 ? part / kWarps == rank : rank == 0;
+    if (part < 0 && mine && tid == 0)
+      report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_VERIFY_PROB, (uint32_t)(r0 + cur));
+    if (part >= 0 && mine) {
       // this CTA looks the part through, four entries a thread
       if (tid == 0) {
         s_found[0] = INT32_MAX;
@@ -325,66 +390,52 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
       const int g0 = part * seg, g1 = min(groups, g0 + seg);
       for (int b = g0; b < g1; b += kThreads) {
         const int i = b + tid;
-        float hi[4] = {0.f, 0.f, 0.f, 0.f}, lo[4] = {0.f, 0.f, 0.f, 0.f};
+        Pair r[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
         bool bad = false;
         if (i < g1) {
           const float4 pv = read4(y.p, y.lead, y.wide, i, a.vocab);
           const float4 qv = y.q ? read4(y.q, y.lead, y.wide, i, a.vocab) : make_float4(0.f, 0.f, 0.f, 0.f);
-          entries(y, pv, qv, i, s_gone, bad, hi, lo);
+          entries(y, pv, qv, i, s_gone, bad, r);
         }
-        double v[4], own = 0.0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          v[k] = (double)hi[k] + (double)lo[k];
-          own += v[k];
-        }
-        double inc = own;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const double z = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += z;
-        }
-        if (lane == 31) s_scan[warp] = inc;
+        const Pair four = add(add(r[0], r[1]), add(r[2], r[3]));
+        const Pair upto = scan(four);
+        if (lane == 31) s_scan[warp] = upto;
+        Pair z = Pair{__shfl_up_sync(0xffffffffu, upto.h, 1), __shfl_up_sync(0xffffffffu, upto.l, 1)};
+        if (lane == 0) z = Pair{0.f, 0.f};
         __syncthreads();
-        double c = before + inc - own, tot = 0.0;
+        Pair base = before, tot = before;
         for (int w = 0; w < kWarps; ++w) {
-          if (w < warp) c += s_scan[w];
-          tot += s_scan[w];
+          if (w == warp) base = tot;
+          tot = add(tot, s_scan[w]);
         }
+        z = add(base, z);
         int first = INT32_MAX, any = -1;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          c += v[k];
-          if (v[k] > 0.0) {
+          z = add(z, r[k]);
+          if (r[k].h > 0.f) {
             any = 4 * i - y.lead + k;
-            if (first == INT32_MAX && c > t && before != INFINITY) first = any;
+            if (first == INT32_MAX && !end && greater(z, t)) first = any;
           }
         }
         if (first != INT32_MAX) atomicMin(&s_found[0], first);
         if (any >= 0) atomicMax(&s_found[1], any);
-        before += tot;
+        before = tot;
         __syncthreads();
         if (s_found[0] != INT32_MAX) break;
       }
       token = s_found[0] != INT32_MAX ? s_found[0] : s_found[1];
-    } else if (part < 0 && rank == 0) {
-      if (tid == 0) report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_VERIFY_PROB, (uint32_t)(r0 + cur));
-    } else {
-      cl.sync();                          // the sums of the last pass are read elsewhere until here
-      return;
     }
-  } else if (rank != 0) {
-    cl.sync();
-    return;
   }
-  // by the CTA that found the token, or the first
-  if (tid == 0) {
-    a.next[s] = token;
-    a.count[s] = kept;
+  if (mine) {
+    if (tid == 0) {
+      a.next[s] = token;
+      a.count[s] = kept;
+    }
+    for (int i = tid; i < a.max_path; i += kThreads)
+      a.path[(int64_t)s * a.max_path + i] = i < kept ? s_path[i] : -1;
   }
-  for (int i = tid; i < a.max_path; i += kThreads)
-    a.path[(int64_t)s * a.max_path + i] = i < kept ? s_path[i] : -1;
-  cl.sync();
+  cl.sync();                              // the sums of the last pass are read elsewhere until here
 }
 
 fuse_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? FUSE_OK : FUSE_ERR_CUDA; }
