@@ -16,8 +16,8 @@
 // an SM busy for some 250 cycles (with fp64 sums and tests in every thread the
 // call on 64 trees took 114 us instead of @@).
 //
-// One cluster per sequence, the vocabulary split over its CTAs, their warps'
-// sums exchanged through distributed shared memory.  Latency bounds it: a chain of
+// One cluster per sequence, the vocabulary split over its CTAs; every warp writes its
+// sum into all of them (distributed shared memory).  Latency bounds it: a chain of
 // reads (parents and tokens, probabilities of the drafts, a row, the part of it
 // with the border).
 #include <cooperative_groups.h>
@@ -102,18 +102,26 @@ __device__ __forceinline__ Pair remainder_of(float p, float q, Pair A) {
   return s + e > 0.f ? Pair{s, e} : Pair{0.f, 0.f};
 }
 
-// A row's entries [4 i - lead, 4 i - lead + 4), those outside the row as 0.  The rows of a
-// large vocabulary need not be aligned: `lead` entries are missing in front of a
-// row's first aligned group of four.  wide: whole groups are read at once.
-__device__ __forceinline__ float4 read4(const float* row, int lead, bool wide, int i, int vocab) {
-  const int e = 4 * i - lead;
-  if (wide && e >= 0 && e + 4 <= vocab) return __ldg(reinterpret_cast<const float4*>(row + e));
-  float4 x;
-  x.x = e >= 0 && e < vocab ? __ldg(row + e) : 0.f;
-  x.y = e + 1 >= 0 && e + 1 < vocab ? __ldg(row + e + 1) : 0.f;
-  x.z = e + 2 >= 0 && e + 2 < vocab ? __ldg(row + e + 2) : 0.f;
-  x.w = e + 3 >= 0 && e + 3 < vocab ? __ldg(row + e + 3) : 0.f;
-  return x;
+// What a pass over a row forms its entries from.  Rows of a large vocabulary need not
+// be aligned: `lead` entries are missing in front of a row's first aligned group of
+// four.  wide: whole groups are read at once.
+struct Pass {
+  const float* p;
+  const float* q;                         // null: p alone
+  Pair A;
+  int lead, vocab;
+  bool wide;
+  int n_gone;                             // refused tokens whose entry is 0 (without q)
+};
+
+// Entries [4 i - lead, 4 i - lead + 4) of a row, those outside the row as 0.
+__device__ __forceinline__ float4 read4(const float* row, const Pass& y, int i) {
+  const int e = 4 * i - y.lead;
+  if (y.wide && e >= 0 && e + 4 <= y.vocab) return __ldg(reinterpret_cast<const float4*>(row + e));
+  float x[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x[k] = e + k >= 0 && e + k < y.vocab ? __ldg(row + e + k) : 0.f;
+  return make_float4(x[0], x[1], x[2], x[3]);
 }
 
 __device__ __forceinline__ float usable(float x, bool& bad) {
@@ -122,45 +130,103 @@ __device__ __forceinline__ float usable(float x, bool& bad) {
   return ok ? x : 0.f;
 }
 
-// What a pass over a row forms its entries from.
-struct Pass {
-  const float* p;
-  const float* q;                         // null: p alone
-  Pair A;
-  int lead;
-  bool wide;
-  int n_gone;                             // refused tokens whose entry is 0 (without q)
+// The four entries of group i.  Out of line: where entries may not be usable or tokens are
+// refused, and for the part that is looked through.
+struct Four {
+  Pair r[4];
 };
-
-__device__ __forceinline__ void entries(const Pass& y, const float4& pv, const float4& qv, int i,
-                                        const int* s_gone, bool& bad, Pair (&r)[4]) {
+__device__ __noinline__ Four entries(const Pass& y, int i, const int* s_gone, uint32_t* err) {
+  const float4 pv = read4(y.p, y, i), qv = y.q ? read4(y.q, y, i) : make_float4(0.f, 0.f, 0.f, 0.f);
   const float p[4] = {pv.x, pv.y, pv.z, pv.w}, q[4] = {qv.x, qv.y, qv.z, qv.w};
+  Four f;
+  bool bad = false;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    r[k] = Pair{usable(p[k], bad), 0.f};
-    if (y.q) r[k] = remainder_of(r[k].h, usable(q[k], bad), y.A);
+    f.r[k] = Pair{usable(p[k], bad), 0.f};
+    if (y.q) f.r[k] = remainder_of(f.r[k].h, usable(q[k], bad), y.A);
   }
   for (int g = 0; g < y.n_gone; ++g) {
     const int at = s_gone[g] - (4 * i - y.lead);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (at == k) r[k].h = 0.f;
+      if (at == k) f.r[k].h = 0.f;
   }
+  if (bad) report_error(err, FUSE_ERR_DEVICE_BOUNDS, SITE_VERIFY_PROB, (uint32_t)i);
+  return f;
 }
 
-__global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant__ VerifyArgs a) {
+__device__ __forceinline__ void tally(Pair& sum, Pair x) {
+  float t;
+  two_sum(sum.h, x.h, sum.h, t);
+  sum.l += t + x.l;
+}
+
+// A thread's sum over the groups g0 + its lane, + 32, .. below g1.  Numbers that are not
+// usable have a bit pattern past the largest float's; a warp that meets one, or a refused
+// token's group, goes over its kAhead groups entry by entry.
+template <bool kQ>
+__device__ __forceinline__ Pair sum_groups(const Pass& y, int g0, int g1, const int* s_gone, uint32_t* err) {
+  const int lane = threadIdx.x % 32;
+  Pair sum{0.f, 0.f};
+#pragma unroll 1
+  for (int g = g0; g < g1; g += 32 * kAhead) {
+    const int e0 = 4 * g - y.lead, e1 = 4 * (g + 32 * kAhead) - y.lead;      // of the warp
+    bool plain = y.wide && e0 >= 0 && e1 <= y.vocab && g + 32 * kAhead <= g1;
+    for (int k = 0; k < y.n_gone; ++k) plain &= s_gone[k] < e0 || s_gone[k] >= e1;
+    float4 p[kAhead], q[kAhead];
+    if (plain) {                          // uniform
+      uint32_t top = 0;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        p[k] = __ldg(reinterpret_cast<const float4*>(y.p + e0 + 4 * (32 * k + lane)));
+        if (kQ) q[k] = __ldg(reinterpret_cast<const float4*>(y.q + e0 + 4 * (32 * k + lane)));
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        top = max(max(top, __float_as_uint(p[k].x)), __float_as_uint(p[k].y));
+        top = max(max(top, __float_as_uint(p[k].z)), __float_as_uint(p[k].w));
+        if (kQ) {
+          top = max(max(top, __float_as_uint(q[k].x)), __float_as_uint(q[k].y));
+          top = max(max(top, __float_as_uint(q[k].z)), __float_as_uint(q[k].w));
+        }
+      }
+      plain = __all_sync(0xffffffffu, top <= 0x7F7FFFFFu);
+    }
+    if (plain) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const float pe[4] = {p[k].x, p[k].y, p[k].z, p[k].w}, qe[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) tally(sum, kQ ? remainder_of(pe[e], qe[e], y.A) : Pair{pe[e], 0.f});
+      }
+    } else {
+#pragma unroll 1
+      for (int i = g + lane; i < min(g1, g + 32 * kAhead); i += 32) {
+        const Four f = entries(y, i, s_gone, err);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) tally(sum, f.r[e]);
+      }
+    }
+  }
+  return sum;
+}
+
+__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_constant__ VerifyArgs a) {
   cg::cluster_group cl = cg::this_cluster();
   const int n_ctas = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   const int s = blockIdx.x / n_ctas;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   constexpr int kEach = kMaxCluster * kWarps / 32;         // sums a lane holds
-  __shared__ Pair s_sum[2][kWarps];       // this CTA's warps' sums, by the pass's parity
+  __shared__ Pair s_sum[2][kMaxCluster * kWarps];          // the cluster's warps' sums, by the pass's parity
   __shared__ Pair s_scan[kWarps];
   __shared__ int s_token[kNodes], s_gone[kNodes], s_path[kNodes];
   __shared__ float s_p[kNodes];
   __shared__ unsigned long long s_child[kNodes];           // a node's children, a bit each
   __shared__ unsigned int s_ok[2];        // nodes that pass the test as it stands
   __shared__ int s_found[2];
+  // (a CTA's shared memory may be written once it runs: waited for before the first sums)
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  bool begun = false;
   pdl_wait();
   pdl_trigger();
   const int r0 = a.rows[s], r1 = a.rows[s + 1];
@@ -209,6 +275,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
   y.q = nullptr;
   y.A = Pair{0.f, 0.f};
   y.n_gone = 0;
+  y.vocab = a.vocab;
   auto test = [&](unsigned long long which, Pair A, double S) {
     if (warp >= kNodes / 32) return;
     bool yes = false;
@@ -243,42 +310,20 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
     groups = (a.vocab + y.lead + 3) / 4;
     seg = (groups + W - 1) / W;
     const int g0 = (rank * kWarps + warp) * seg, g1 = min(groups, g0 + seg);
-    Pair sum{0.f, 0.f};
-    bool bad = false;
-    for (int g = g0 + lane; g < g1; g += 32 * kAhead) {
-      float4 pv[kAhead], qv[kAhead];
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int i = g + 32 * k;
-        pv[k] = qv[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i < g1) {
-          pv[k] = read4(y.p, y.lead, y.wide, i, a.vocab);
-          if (y.q) qv[k] = read4(y.q, y.lead, y.wide, i, a.vocab);
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        Pair r[4];
-        entries(y, pv[k], qv[k], g + 32 * k, s_gone, bad, r);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float t;
-          two_sum(sum.h, r[e].h, sum.h, t);
-          sum.l += t + r[e].l;
-        }
-      }
-    }
+    Pair sum = y.q ? sum_groups<true>(y, g0, g1, s_gone, a.err) : sum_groups<false>(y, g0, g1, s_gone, a.err);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum = add(sum, shfl_xor(sum, o));
-    if (lane == 0) s_sum[parity][warp] = sum;
-    if (bad) report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_VERIFY_PROB, (uint32_t)(r0 + node));
+    if (!begun) {
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      begun = true;
+    }
+    if (lane < n_ctas) *cl.map_shared_rank(&s_sum[parity][rank * kWarps + warp], lane) = sum;
     cl.sync();
     Pair all{0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
       const int w = lane * kEach + k;
-      v[k] = Pair{0.f, 0.f};
-      if (w < W) v[k] = *cl.map_shared_rank(&s_sum[parity][w % kWarps], w / kWarps);
+      v[k] = w < W ? s_sum[parity][w] : Pair{0.f, 0.f};
       all = add(all, v[k]);
     }
 #pragma unroll
@@ -391,11 +436,10 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
       for (int b = g0; b < g1; b += kThreads) {
         const int i = b + tid;
         Pair r[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
-        bool bad = false;
         if (i < g1) {
-          const float4 pv = read4(y.p, y.lead, y.wide, i, a.vocab);
-          const float4 qv = y.q ? read4(y.q, y.lead, y.wide, i, a.vocab) : make_float4(0.f, 0.f, 0.f, 0.f);
-          entries(y, pv, qv, i, s_gone, bad, r);
+          const Four f = entries(y, i, s_gone, a.err);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) r[k] = f.r[k];
         }
         const Pair four = add(add(r[0], r[1]), add(r[2], r[3]));
         const Pair upto = scan(four);
@@ -435,7 +479,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
     for (int i = tid; i < a.max_path; i += kThreads)
       a.path[(int64_t)s * a.max_path + i] = i < kept ? s_path[i] : -1;
   }
-  cl.sync();                              // the sums of the last pass are read elsewhere until here
+  if (!begun) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 fuse_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? FUSE_OK : FUSE_ERR_CUDA; }
