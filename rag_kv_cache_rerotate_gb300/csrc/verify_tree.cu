@@ -73,6 +73,14 @@ __device__ __forceinline__ Pair add(Pair a, Pair b) {
   r.l = e - (r.h - s);
   return r;
 }
+__device__ __forceinline__ Pair mul(Pair a, Pair b) {
+  Pair r;
+  const float h = a.h * b.h;
+  const float l = fmaf(a.h, b.h, -h) + (a.h * b.l + a.l * b.h);
+  r.h = h + l;
+  r.l = l - (r.h - h);
+  return r;
+}
 __device__ __forceinline__ bool greater(Pair a, Pair b) {
   float s, e;
   two_sum(a.h, -b.h, s, e);
@@ -162,24 +170,29 @@ __device__ __forceinline__ void tally(Pair& sum, Pair x) {
 }
 
 // A thread's sum over the groups g0 + its lane, + 32, .. below g1.  Numbers that are not
-// usable have a bit pattern past the largest float's; a warp that meets one, or a refused
-// token's group, goes over its kAhead groups entry by entry.
+// usable have a bit pattern past the largest float's; a warp that meets one goes over
+// its groups entry by entry, as for rows that are not read in groups.  The row's first
+// and last group, where they are not whole, are left out (part_groups).
 template <bool kQ>
 __device__ __forceinline__ Pair sum_groups(const Pass& y, int g0, int g1, const int* s_gone, uint32_t* err) {
   const int lane = threadIdx.x % 32;
   Pair sum{0.f, 0.f};
+  const int first = y.lead > 0, last = (y.vocab + y.lead) / 4;             // whole groups
+  const int h0 = max(g0, first), h1 = min(g1, last);
 #pragma unroll 1
-  for (int g = g0; g < g1; g += 32 * kAhead) {
-    const int e0 = 4 * g - y.lead, e1 = 4 * (g + 32 * kAhead) - y.lead;      // of the warp
-    bool plain = y.wide && e0 >= 0 && e1 <= y.vocab && g + 32 * kAhead <= g1;
-    for (int k = 0; k < y.n_gone; ++k) plain &= s_gone[k] < e0 || s_gone[k] >= e1;
+  for (int g = h0; g < h1; g += 32 * kAhead) {
     float4 p[kAhead], q[kAhead];
-    if (plain) {                          // uniform
+    bool plain = y.wide;                  // uniform
+    if (plain) {
       uint32_t top = 0;
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        p[k] = __ldg(reinterpret_cast<const float4*>(y.p + e0 + 4 * (32 * k + lane)));
-        if (kQ) q[k] = __ldg(reinterpret_cast<const float4*>(y.q + e0 + 4 * (32 * k + lane)));
+        const int i = g + 32 * k + lane, e = 4 * i - y.lead;
+        p[k] = q[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < h1) {
+          p[k] = __ldg(reinterpret_cast<const float4*>(y.p + e));
+          if (kQ) q[k] = __ldg(reinterpret_cast<const float4*>(y.q + e));
+        }
       }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
@@ -193,6 +206,19 @@ __device__ __forceinline__ Pair sum_groups(const Pass& y, int g0, int g1, const 
       plain = __all_sync(0xffffffffu, top <= 0x7F7FFFFFu);
     }
     if (plain) {
+      if (!kQ) {
+        for (int n = 0; n < y.n_gone; ++n) {             // refused tokens
+          const int at = s_gone[n] + y.lead;
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k)
+            if (at / 4 == g + 32 * k + lane) {
+              if (at % 4 == 0) p[k].x = 0.f;
+              if (at % 4 == 1) p[k].y = 0.f;
+              if (at % 4 == 2) p[k].z = 0.f;
+              if (at % 4 == 3) p[k].w = 0.f;
+            }
+        }
+      }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         const float pe[4] = {p[k].x, p[k].y, p[k].z, p[k].w}, qe[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
@@ -201,12 +227,25 @@ __device__ __forceinline__ Pair sum_groups(const Pass& y, int g0, int g1, const 
       }
     } else {
 #pragma unroll 1
-      for (int i = g + lane; i < min(g1, g + 32 * kAhead); i += 32) {
+      for (int i = g + lane; i < min(h1, g + 32 * kAhead); i += 32) {
         const Four f = entries(y, i, s_gone, err);
 #pragma unroll
         for (int e = 0; e < 4; ++e) tally(sum, f.r[e]);
       }
     }
+  }
+  return sum;
+}
+// The row's first and last group, where they are not whole and this warp's.
+__device__ __forceinline__ Pair part_groups(const Pass& y, int g0, int g1, const int* s_gone, uint32_t* err) {
+  const int lane = threadIdx.x % 32, last = (y.vocab + y.lead) / 4;
+  Pair sum{0.f, 0.f};
+  const int i = lane == 0 ? 0 : last;
+  const bool there = lane == 0 ? y.lead > 0 : lane == 1 && (y.vocab + y.lead) % 4 != 0 && (last > 0 || y.lead == 0);
+  if (there && i >= g0 && i < g1) {
+    const Four f = entries(y, i, s_gone, err);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) tally(sum, f.r[e]);
   }
   return sum;
 }
@@ -276,24 +315,24 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
   y.A = Pair{0.f, 0.f};
   y.n_gone = 0;
   y.vocab = a.vocab;
-  auto test = [&](unsigned long long which, Pair A, double S) {
+  auto test = [&](unsigned long long which, Pair A, Pair S) {
     if (warp >= kNodes / 32) return;
     bool yes = false;
     if (par >= 0 && (which >> tid & 1)) {
-      double r = pd;
+      Pair r{pd, 0.f}, need = mul(Pair{ud, 0.f}, S);
       if (a.Q) {
-        r = (double)pd - ((double)A.h + A.l) * (double)qd;
-        yes = r > 0.0 && (double)ud * S * (double)qd < r;
+        r = remainder_of(pd, qd, A);
+        need = mul(need, Pair{qd, 0.f});
       } else {
         for (int g = 0; g < y.n_gone; ++g)
-          if (s_gone[g] == tok) r = 0.0;
-        yes = r > 0.0 && (double)ud * S < r;
+          if (s_gone[g] == tok) r.h = 0.f;
       }
+      yes = r.h > 0.f && greater(r, need);             // a number that is none: no
     }
     const unsigned int bits = __ballot_sync(0xffffffffu, yes);
     if (lane == 0) s_ok[warp] = bits;
   };
-  test(~0ull, y.A, 1.0);                  // as first children
+  test(~0ull, y.A, Pair{1.f, 0.f});                  // as first children
   __syncthreads();
   const unsigned long long first_ok = (unsigned long long)s_ok[1] << 32 | s_ok[0];
   const int W = n_ctas * kWarps;
@@ -311,6 +350,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
     seg = (groups + W - 1) / W;
     const int g0 = (rank * kWarps + warp) * seg, g1 = min(groups, g0 + seg);
     Pair sum = y.q ? sum_groups<true>(y, g0, g1, s_gone, a.err) : sum_groups<false>(y, g0, g1, s_gone, a.err);
+    if (g0 == 0 || g1 == groups) sum = add(sum, part_groups(y, g0, g1, s_gone, a.err));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum = add(sum, shfl_xor(sum, o));
     if (!begun) {
@@ -335,7 +375,6 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
   // the walk, the same in every thread of the cluster
   int cur = 0, kept = n > 0 ? 1 : 0;
   Pair A{0.f, 0.f}, S{1.f, 0.f};
-  double s_left = 1.0;                    // without q: what refusals leave of 1
   bool summed = false;                    // v holds the sums of the remainder as it stands
   unsigned long long left = n > 0 ? s_child[0] : 0, ok = first_ok;
   if (tid == 0) s_path[0] = 0;
@@ -348,7 +387,6 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
       ++kept;
       A = Pair{0.f, 0.f};
       S = Pair{1.f, 0.f};
-      s_left = 1.0;
       y.n_gone = 0;
       summed = false;
       left = s_child[c];
@@ -365,14 +403,14 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
       for (int g = 0; g < y.n_gone; ++g) again |= s_gone[g] == x;
       __syncthreads();                    // s_gone is read above
       if (!again) {
-        s_left -= (double)s_p[c];
+        S = add(S, Pair{-s_p[c], 0.f});  // what refusals leave of 1
         if (tid == 0) s_gone[y.n_gone] = x;
         ++y.n_gone;
       }
     }
     if (left) {
       __syncthreads();                    // s_gone; s_ok has been read
-      test(left, A, a.Q ? (double)S.h + S.l : s_left);
+      test(left, A, S);
       __syncthreads();
       ok = (unsigned long long)s_ok[1] << 32 | s_ok[0];
     }
