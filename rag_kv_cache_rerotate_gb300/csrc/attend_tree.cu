@@ -266,7 +266,7 @@ template <typename T> cudaError_t launch_join(const TreeArgs& a, int d, cudaStre
 // ---- host side ---------------------------------------------------------------
 
 constexpr int kCtas = 152;                // SMs
-constexpr int kSimtCtas = 8;              // CTAs of an SM (fp32 layers)
+constexpr int kSimtCtas = 3;              // CTAs of an SM (fp32 layers)
 
 fuse_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? FUSE_OK : FUSE_ERR_CUDA; }
 
@@ -340,7 +340,11 @@ fuse_status_t fuse_attend_tree(const fuse_layer_desc_t* desc, const fuse_seqs_t*
   a.vecs_log2 = desc->dtype == FUSE_BF16 ? 8 : 3;
   a.tile = P.tile;
   a.tile_log2 = desc->dtype == FUSE_BF16 ? 7 : 5;
-  a.workers = P.workers;
+  // no more workers than the tables' rows could give tiles to
+  const int64_t cap = ((int64_t)seqs->max_blocks * seqs->block_size + P.tile - 1) / P.tile;
+  const int64_t groups = ((int64_t)seqs->max_new * a.g + P.vecs - 1) / P.vecs;
+  const int64_t most = std::min<int64_t>(P.workers, cap * groups * seqs->n_seq * a.n_kv_heads);
+  a.workers = desc->dtype == FUSE_BF16 ? (int)most : (int)((most + kWarps - 1) / kWarps * kWarps);
   a.scale = 1.4426950408889634f / std::sqrt((float)desc->head_dim);
   a.start = reinterpret_cast<int64_t*>(at(P.start));
   a.part_ml = reinterpret_cast<float2*>(at(P.part_ml));

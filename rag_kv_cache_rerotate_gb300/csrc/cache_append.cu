@@ -32,14 +32,11 @@ struct AppendArgs {
   int n_q_heads, n_kv_heads;              // n_q_heads: 0 without Q
   int rot, interleaved;
   float mscale;
-  int rows_cta;                           // rows of a CTA
-  int units;                              // units of 16 channels of a row
-  uint32_t units_inv;                     // ceil(2^32 / units)
+  int parts, parts_log2;                  // warps that share a row, a power of two
 };
 
-constexpr int kThreads = 256;
-constexpr int kMaxRows = 8;               // rows of a CTA at most
-constexpr int kAhead = 2;                 // units that a thread reads at a time
+constexpr int kThreads = 128;
+constexpr int kAhead = 3;                 // units that a lane reads at a time
 
 // 8 consecutive elements: two registers of 16 bytes for fp32, one for bf16.
 template <typename T> struct Raw8;
@@ -76,7 +73,7 @@ template <> struct Raw8<__nv_bfloat16> {
   }
 };
 
-// What a CTA knows of its rows.
+// What a warp knows of its row.
 struct RowPlace {
   int64_t pool;                           // pool row, -1: not written
   int row;                                // -1: no sequence's
@@ -112,125 +109,112 @@ __device__ __forceinline__ RowPlace place_row(const AppendArgs& a, int row) {
   return p;
 }
 
-// One unit: 16 channels of a head, two runs of 8 (apart by half the rotated
-// channels in the half layout).  A CTA takes rows_cta rows; memory bounds it on
-// prompts, the chain of reads in front of the angles on single tokens, so a
-// thread's first units are read before that chain.
+// A warp takes a row, or a share of its heads; D / 16 lanes a head, a lane 16 channels of
+// it, two runs of 8 (apart by half the rotated channels in the half layout) and of all
+// heads the same ones, so that it reads their angles once.  Memory bounds it on prompts
+// (10368 rows of 32 query and 8 KV heads, d = 128: @@ us, @@ TB/s; with a row's angles
+// shared by a block of 256 threads, which has to wait for them, 52 us), the chain of reads
+// in front of the angles on single tokens, so the first units are read before that chain.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
     append_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ Turns turns) {
-  __shared__ RowPlace s_row[kMaxRows];
-  __shared__ float2 s_cs[kMaxRows][kMaxHalfDim];
-  constexpr int kPer = D / 16;            // units of a head
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  const int row0 = blockIdx.x * a.rows_cta;
-  const int n_rows = (int)min((int64_t)a.rows_cta, a.seq.n_rows - row0);
-  const int total = n_rows * a.units;
+  constexpr int kPer = D / 16, kHeads = 32 / kPer;         // lanes of a head, heads at a time
+  __shared__ float2 s_cs[kThreads / 32][kMaxHalfDim];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + warp;
+  const int64_t row = w >> a.parts_log2;
+  const int part = (int)w & (a.parts - 1);
   pdl_wait();
   pdl_trigger();
-
-  struct Unit {
-    const T* src;
-    int r, head, e0, e1, m;               // m: first pair, -1: copied
-    int kind;                             // 0: Q, 1: K, 2: V
-  };
-  auto unit = [&](int x) {
-    Unit u;
-    u.r = __umulhi((uint32_t)x, a.units_inv);
-    const int y = x - u.r * a.units;
-    const int h = y / kPer, c = y % kPer;
-    u.kind = h < a.n_q_heads ? 0 : h < a.n_q_heads + a.n_kv_heads ? 1 : 2;
-    u.head = u.kind == 0 ? h : u.kind == 1 ? h - a.n_q_heads : h - a.n_q_heads - a.n_kv_heads;
-    const int64_t row = row0 + u.r;
-    u.src = u.kind == 0   ? reinterpret_cast<const T*>(a.Q) + row * a.q_stride
-            : u.kind == 1 ? reinterpret_cast<const T*>(a.K) + row * a.k_stride
-                          : reinterpret_cast<const T*>(a.V) + row * a.v_stride;
-    u.src += u.head * D;
-    u.e0 = 16 * c;
-    u.e1 = u.e0 + 8;
-    u.m = -1;
-    if (u.kind < 2 && u.e0 < a.rot) {
-      u.m = 8 * c;
-      if (!a.interleaved) {
-        u.e0 = u.m;
-        u.e1 = u.m + a.rot / 2;
-      }
-    }
-    return u;
-  };
+  if (row >= a.seq.n_rows) return;        // uniform in the warp
+  const int c = lane % kPer;
+  const bool turned = 16 * c < a.rot;     // (of queries and keys)
+  const int e0 = turned && !a.interleaved ? 8 * c : 16 * c;
+  const int e1 = turned && !a.interleaved ? e0 + a.rot / 2 : e0 + 8;
+  const T* q = reinterpret_cast<const T*>(a.Q) + row * a.q_stride;
+  const T* k = reinterpret_cast<const T*>(a.K) + row * a.k_stride;
+  const T* v = reinterpret_cast<const T*>(a.V) + row * a.v_stride;
+  const int heads = a.n_q_heads + 2 * a.n_kv_heads, step = a.parts * kHeads;
+  const int first = part * kHeads + lane / kPer;
   Raw8<T> x[kAhead][2];
-  auto read = [&](int base) {
+  // head h's run at e: a value's channels are copied as they lie
+  auto read = [&](int h0) {
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int i = base + k * kThreads + tid;
-      if (i < total) {
-        const Unit u = unit(i);
-        x[k][0].load(u.src + u.e0);
-        x[k][1].load(u.src + u.e1);
+    for (int i = 0; i < kAhead; ++i) {
+      const int h = h0 + i * step;
+      if (h < heads) {
+        const bool value = h >= a.n_q_heads + a.n_kv_heads;
+        const T* src = h < a.n_q_heads ? q + h * D : value ? v + (h - a.n_q_heads - a.n_kv_heads) * D
+                                                           : k + (h - a.n_q_heads) * D;
+        x[i][0].load(src + (value ? 16 * c : e0));
+        x[i][1].load(src + (value ? 16 * c + 8 : e1));
       }
     }
   };
-  read(0);
-  for (int r = warp; r < n_rows; r += kThreads / 32) {
-    const RowPlace p = place_row(a, row0 + r);
-    if (lane == 0) s_row[r] = p;
-    for (int m = lane; m < a.rot / 2; m += 32) {
-      const uint64_t t = (uint64_t)(uint32_t)p.pos * turns.f[m];
-      float c, sn;
-      sincospif((float)(int32_t)(t >> 32) * (1.f / 2147483648.f), &sn, &c);
-      s_cs[r][m] = make_float2(c * a.mscale, sn * a.mscale);
-    }
+  read(first);
+  const RowPlace p = place_row(a, (int)row);
+  if (p.row < 0) return;                  // uniform
+  for (int m = lane; m < a.rot / 2; m += 32) {
+    const uint64_t t = (uint64_t)(uint32_t)p.pos * turns.f[m];
+    float co, si;
+    sincospif((float)(int32_t)(t >> 32) * (1.f / 2147483648.f), &si, &co);
+    s_cs[warp][m] = make_float2(co * a.mscale, si * a.mscale);
   }
-  __syncthreads();
-  for (int base = 0; base < total; base += kAhead * kThreads) {
-    if (base > 0) read(base);
+  __syncwarp();
+  float2 cs[8];                           // of the lane's pairs
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int i = base + k * kThreads + tid;
-      if (i >= total) continue;
-      const Unit u = unit(i);
-      const RowPlace p = s_row[u.r];
-      if (p.row < 0) continue;
-      if (u.m >= 0) {
+  for (int e = 0; e < 8; ++e) cs[e] = turned ? s_cs[warp][8 * c + e] : make_float2(1.f, 0.f);
+  T* qr = reinterpret_cast<T*>(a.Qr) + row * a.n_q_heads * D;
+  T* kr = a.Kr ? reinterpret_cast<T*>(a.Kr) + row * a.n_kv_heads * D : nullptr;
+  T* kp = reinterpret_cast<T*>(a.k_pool) + p.pool * a.n_kv_heads * D;
+  T* vp = reinterpret_cast<T*>(a.v_pool) + p.pool * a.n_kv_heads * D;
+  for (int h0 = first; h0 < heads; h0 += kAhead * step) {
+    if (h0 != first) read(h0);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int h = h0 + i * step;
+      if (h >= heads) continue;
+      const int hk = h - a.n_q_heads, hv = hk - a.n_kv_heads;
+      if (hv >= 0) {
+        if (p.pool >= 0) {
+          x[i][0].store(vp + hv * D + 16 * c);
+          x[i][1].store(vp + hv * D + 16 * c + 8);
+        }
+        continue;
+      }
+      if (turned) {
         float y[8], z[8];
-        x[k][0].get(y);
-        x[k][1].get(z);
-        const float2* cs = s_cs[u.r] + u.m;
+        x[i][0].get(y);
+        x[i][1].get(z);
         if (a.interleaved) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 w = cs[e], v = cs[4 + e];
+            const float2 f = cs[e], g = cs[4 + e];
             const float y0 = y[2 * e], z0 = z[2 * e];
-            y[2 * e] = y0 * w.x - y[2 * e + 1] * w.y;
-            y[2 * e + 1] = y[2 * e + 1] * w.x + y0 * w.y;
-            z[2 * e] = z0 * v.x - z[2 * e + 1] * v.y;
-            z[2 * e + 1] = z[2 * e + 1] * v.x + z0 * v.y;
+            y[2 * e] = y0 * f.x - y[2 * e + 1] * f.y;
+            y[2 * e + 1] = y[2 * e + 1] * f.x + y0 * f.y;
+            z[2 * e] = z0 * g.x - z[2 * e + 1] * g.y;
+            z[2 * e + 1] = z[2 * e + 1] * g.x + z0 * g.y;
           }
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float2 w = cs[e];
             const float y0 = y[e];
-            y[e] = y0 * w.x - z[e] * w.y;
-            z[e] = z[e] * w.x + y0 * w.y;
+            y[e] = y0 * cs[e].x - z[e] * cs[e].y;
+            z[e] = z[e] * cs[e].x + y0 * cs[e].y;
           }
         }
-        x[k][0].set(y);
-        x[k][1].set(z);
+        x[i][0].set(y);
+        x[i][1].set(z);
       }
-      if (u.kind < 2) {
-        T* out = reinterpret_cast<T*>(u.kind == 0 ? a.Qr : a.Kr);
-        if (out) {
-          out += ((int64_t)p.row * (u.kind == 0 ? a.n_q_heads : a.n_kv_heads) + u.head) * D;
-          x[k][0].store(out + u.e0);
-          x[k][1].store(out + u.e1);
-        }
+      T* out = hk < 0 ? qr + h * D : kr ? kr + hk * D : nullptr;
+      if (out) {
+        x[i][0].store(out + e0);
+        x[i][1].store(out + e1);
       }
-      if (u.kind > 0 && p.pool >= 0) {
-        T* out = reinterpret_cast<T*>(u.kind == 1 ? a.k_pool : a.v_pool) +
-                 (p.pool * a.n_kv_heads + u.head) * D;
-        x[k][0].store(out + u.e0);
-        x[k][1].store(out + u.e1);
+      if (hk >= 0 && p.pool >= 0) {
+        x[i][0].store(kp + hk * D + e0);
+        x[i][1].store(kp + hk * D + e1);
       }
     }
   }
@@ -450,16 +434,20 @@ fuse_status_t fuse_cache_append(const fuse_layer_desc_t* desc, const fuse_rope_t
   a.rot = rot;
   a.interleaved = rope->layout == FUSE_ROPE_INTERLEAVED;
   a.mscale = (float)rope->mscale;
-  const int64_t units = ((int64_t)a.n_q_heads + 2 * a.n_kv_heads) * (d / 16);
-  if (units > 16384) return FUSE_ERR_UNSUPPORTED;         // units_inv is exact for kMaxRows rows of so many
-  a.units = (int)units;
-  a.units_inv = (uint32_t)((((uint64_t)1 << 32) + units - 1) / units);
+  const int64_t heads = (int64_t)a.n_q_heads + 2 * a.n_kv_heads;
+  if (heads > 65535) return FUSE_ERR_UNSUPPORTED;
   int dev = 0, sms = 1;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  // a CTA takes several rows once the card holds no more CTAs at a time
-  a.rows_cta = (int)std::min<int64_t>(kMaxRows, std::max<int64_t>(1, n_rows / (sms * 8)));
-  const int grid = (int)((n_rows + a.rows_cta - 1) / a.rows_cta);
+  // a row is shared while the card holds more warps and they have heads to take
+  a.parts = 1;
+  a.parts_log2 = 0;
+  while (n_rows * a.parts < (int64_t)sms * 16 && a.parts * (512 / d) < heads) {
+    a.parts *= 2;
+    ++a.parts_log2;
+  }
+  const int64_t ctas = (n_rows * a.parts + kThreads / 32 - 1) / (kThreads / 32);
+  const int grid = (int)ctas;
   const Turns& t = make_turns(desc->rope_base, *rope, rot);
   cudaStream_t s = (cudaStream_t)stream;
   return cuda_status(traced("cache_append", s, [&] {
