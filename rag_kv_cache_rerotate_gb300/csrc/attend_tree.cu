@@ -16,113 +16,198 @@ namespace fusekv {
 
 namespace {
 
-constexpr int kWarps = 4;                 // workers of a CTA
+constexpr int kWarps = 2;                 // workers of a CTA
 constexpr int kVecs = 8;                  // query vectors of a unit
+constexpr uint32_t kAll = (1u << kVecs) - 1;
+constexpr float kRaise = 16.f;            // a reference is raised by scores 2^16 times as heavy
 constexpr int kTile = 32;                 // keys of a tile: one a lane
-constexpr int kAtOnce = 8;                // keys whose values it reads at a time
 static_assert(kVecs == 1 << 3 && kTile == 1 << 5 && kTreeTcVecs == 1 << 8 && kTreeTcTile == 1 << 7, "logarithms");
 
 // A warp's units, 32 keys at a time: a lane per key for the scores, then a lane
-// per D / 32 channels for the sums.
+// per D / 32 channels for the sums.  Keys and values are copied to shared memory a
+// tile ahead of their use: while a warp sums one tile's values the next one's keys
+// are on their way, and its values during the scores.  A vector's reference is not
+// its maximum: scores up to 2^kRaise times as heavy do not raise it, so most tiles go
+// without the maximum over the lanes (P and its sum have 24 bits at any size).
+//
+// A few short sequences (5 of up to 300 keys and 12 new tokens, 4 heads of 64) take
+// 10 us of dependent reads, sums and code that is fetched for the first time, with
+// the join 13; lanes that read keys and values themselves, a few at a time, took 19
+// (22).  Many keys (16 sequences of 1000 to 4000 keys and 4 to 12 new tokens, 32 heads
+// of 128 on 8) take 277 us, bound by the instructions, a tile's 1024 FMAs of two floats
+// and the 384 reads of shared memory that feed them; that took 462.
+template <int D> struct SimtShared {        // of a warp
+  float4 k[kTile][D / 4];                   // 16-byte pieces swapped by key: lanes read a column of them
+  float4 v[kTile][D / 4];
+  float q[kVecs][D];
+  float p[kTile][kVecs];
+};
+
+// 16 bytes, or as many zeros
+__device__ __forceinline__ void copy16(void* to, const void* from, bool zeros) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),
+               "r"(zeros ? 0 : 16)
+               : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all groups but the last one
+__device__ __forceinline__ void copies_wait1() {
+  asm volatile("cp.async.wait_group 1;" ::: "memory");
+  __syncwarp();
+}
+
+// d + a b, two at a time (half the instructions)
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 d) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)),
+        "l"(reinterpret_cast<const uint64_t&>(d)));
+  return reinterpret_cast<const float2&>(r);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const __grid_constant__ TreeArgs a) {
-  constexpr int EL = D / 32;
-  __shared__ float s_q[kWarps][kVecs][D];
-  __shared__ float s_p[kWarps][32][kVecs];
+  constexpr int EL = D / 32, kPieces = D / 4, kRowsOnce = 32 / kPieces;
+  extern __shared__ __align__(16) uint8_t smem[];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  SimtShared<D>& S = reinterpret_cast<SimtShared<D>*>(smem)[warp];
   pdl_wait();
   pdl_trigger();
   const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
   TreeWalk walk = start_walk(a, w, w == 0);
   TreePart at;
   while (next_part(a, walk, at)) {
-    const int h = at.h, vg = at.vg, n_vec = at.n_vec;
-    uint64_t seen[kVecs];
-    const Seen all = seen_of_all(a.parents, at.q, a.seq.err);
+    const int h = at.h, vg = at.vg, n_vec = at.n_vec, n_keys = at.q.len + at.q.n;
+    auto row_of = [&](int j) {              // of a lane's key
+      const int key = j * kTile + lane;
+      return j < at.j1 && key < n_keys ? (int)pool_row(a.seq, at.s, key) : -1;
+    };
+    // (a key without a row gets zeros)
+    auto copy = [&](const void* pool, int row, bool swap, float4 (*to)[kPieces]) {
+      const int r0 = lane / kPieces, c = lane % kPieces;
+      const float4* from = reinterpret_cast<const float4*>(pool) + h * kPieces + c;
+#pragma unroll 8
+      for (int i = 0; i < kTile; i += kRowsOnce) {
+        const int r = i + r0, ri = __shfl_sync(0xffffffffu, row, r);
+        copy16(&to[r][swap ? c ^ (r & 7) : c], from + (int64_t)max(ri, 0) * (a.n_kv_heads * kPieces), ri < 0);
+      }
+      copies_end();
+    };
+    // Few keys make few tiles, and then latency is all there is: reads come first,
+    // the checks and sums that wait for them after.
+    int row = row_of(at.j0);
+    float x[kVecs][EL];
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
-      const int vi = vg * kVecs + min(v, n_vec - 1), i = vi / a.g;
-      seen[v] = seen_by(all, i);
+      const int vi = vg * kVecs + min(v, n_vec - 1), i = vi >> a.g_log2;
       const float* q = reinterpret_cast<const float*>(a.Q) +
-                   ((int64_t)(at.q.row0 + i) * a.n_q_heads + h * a.g + vi % a.g) * D;
-      for (int e = lane; e < D; e += 32) s_q[warp][v][e] = q[e] * a.scale;
+                       ((int64_t)(at.q.row0 + i) * a.n_q_heads + h * a.g + (vi & (a.g - 1))) * D;
+#pragma unroll
+      for (int e = 0; e < EL; ++e) x[v][e] = q[e * 32 + lane];
     }
-    __syncwarp();
-    float m[kVecs], l[kVecs], acc[kVecs][EL];
+    copy(a.k_pool, row, true, S.k);
+    copy(a.v_pool, row, false, S.v);
+    uint64_t seen[kVecs];
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) seen[v] = 0;
+    if (at.j1 * kTile > at.q.len) {         // (uniform) some are new tokens
+      const Seen all = seen_of_all(a.parents, at.q, a.seq.err);
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v) seen[v] = seen_by(all, (vg * kVecs + min(v, n_vec - 1)) >> a.g_log2);
+    }
+    float m[kVecs], l[kVecs];
+    float2 acc[kVecs / 2][EL];              // of two vectors
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
       m[v] = -INFINITY;
       l[v] = 0.f;
 #pragma unroll
-      for (int e = 0; e < EL; ++e) acc[v][e] = 0.f;
+      for (int e = 0; e < EL; ++e) {
+        S.q[v][e * 32 + lane] = x[v][e] * a.scale;
+        acc[v / 2][e] = make_float2(0.f, 0.f);
+      }
     }
     for (int j = at.j0; j < at.j1; ++j) {
-      const int key = j * kTile + lane;
-      int64_t row = -1;
-      if (key < at.q.len + at.q.n) row = pool_row(a.seq, at.s, key);
-      const int rel = key - at.q.len;     // of a new token
-      const float* kr = reinterpret_cast<const float*>(a.k_pool) + (row * a.n_kv_heads + h) * D;
-      float s[kVecs];
+      const int rel = j * kTile + lane - at.q.len;  // of a new token
+      const int next = row_of(j + 1);
+      copies_wait1();                       // this tile's keys
+      float2 s2[kVecs];                     // over even and odd channels
 #pragma unroll
-      for (int v = 0; v < kVecs; ++v) s[v] = 0.f;
-      if (row >= 0) {
+      for (int v = 0; v < kVecs; ++v) s2[v] = make_float2(0.f, 0.f);
 #pragma unroll 4
-        for (int e = 0; e < D; e += 8) {
-          float x[8];
-          Vec8<float>::load(kr + e, x);
+      for (int c = 0; c < kPieces; ++c) {
+        const float4 kx = S.k[lane][c ^ (lane & 7)];
 #pragma unroll
-          for (int v = 0; v < kVecs; ++v)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s[v] = fmaf(s_q[warp][v][e + i], x[i], s[v]);
+        for (int v = 0; v < kVecs; ++v) {
+          const float4 qx = *reinterpret_cast<const float4*>(&S.q[v][c * 4]);
+          s2[v] = fma2(make_float2(qx.x, qx.y), make_float2(kx.x, kx.y), s2[v]);
+          s2[v] = fma2(make_float2(qx.z, qx.w), make_float2(kx.z, kx.w), s2[v]);
         }
       }
-      uint32_t any = 0;                   // bit v: some vector sees this key
+      __syncwarp();
+      copy(a.k_pool, next, true, S.k);
+      uint32_t any = 0;                     // bit v: that vector sees this key
+      float s[kVecs];
+      bool more = false;
 #pragma unroll
       for (int v = 0; v < kVecs; ++v) {
         const bool ok = row >= 0 && (rel < 0 || (seen[v] >> rel & 1));
-        if (!ok) s[v] = -INFINITY;
-        float mt = s[v];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
-        const float mn = fmaxf(m[v], mt);
-        const float ref = mn == -INFINITY ? 0.f : mn;
-        const float al = exp2f(m[v] - ref), p = ok ? exp2f(s[v] - ref) : 0.f;
-        m[v] = mn;
-        l[v] = l[v] * al + p;
-        s_p[warp][lane][v] = p;
         any |= (uint32_t)ok << v;
-#pragma unroll
-        for (int e = 0; e < EL; ++e) acc[v][e] *= al;
+        s[v] = ok ? s2[v].x + s2[v].y : -INFINITY;
+        more |= s[v] > m[v] + kRaise;
       }
-      __syncwarp();
-      const int64_t mine = any ? row : -1;
-      for (int i = 0; i < 32; i += kAtOnce) {
-        float x[kAtOnce][EL];
-        uint32_t who[kAtOnce];
+      if (__any_sync(0xffffffffu, more)) {  // raise the references to the maxima
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
-          const int64_t ri = __shfl_sync(0xffffffffu, mine, i + j);
-          who[j] = __shfl_sync(0xffffffffu, any, i + j);
+        for (int v = 0; v < kVecs; ++v) {
+          float mn = s[v];
 #pragma unroll
-          for (int e = 0; e < EL; ++e) x[j][e] = 0.f;
-          if (ri >= 0) {
-            const float* vr = reinterpret_cast<const float*>(a.v_pool) + (ri * a.n_kv_heads + h) * D + lane * EL;
+          for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+          mn = fmaxf(m[v], mn);
+          const float al = exp2f(m[v] - (mn == -INFINITY ? 0.f : mn));
+          m[v] = mn;
+          l[v] *= al;
 #pragma unroll
-            for (int e = 0; e < EL; ++e) x[j][e] = vr[e];
-          }
+          for (int e = 0; e < EL; ++e) (v % 2 ? acc[v / 2][e].y : acc[v / 2][e].x) *= al;
         }
+      }
+      float4 p4[kVecs / 4];
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j)
+      for (int v = 0; v < kVecs; ++v) {
+        const float p = any >> v & 1 ? exp2f(s[v] - (m[v] == -INFINITY ? 0.f : m[v])) : 0.f;
+        l[v] += p;
+        reinterpret_cast<float*>(p4)[v] = p;
+      }
 #pragma unroll
-          for (int v = 0; v < kVecs; ++v)
+      for (int v = 0; v < kVecs; v += 4) *reinterpret_cast<float4*>(&S.p[lane][v]) = p4[v / 4];
+      copies_wait1();                       // its values
+      auto sum = [&](int i, uint32_t who) {
+        float vx[EL];
+        if constexpr (EL == 4) {
+          const float4 y = S.v[i][lane];
+          vx[0] = y.x, vx[1] = y.y, vx[2] = y.z, vx[3] = y.w;
+        } else {
+          const float2 y = reinterpret_cast<const float2*>(S.v[i])[lane];
+          vx[0] = y.x, vx[1] = y.y;
+        }
+        const float2* px = reinterpret_cast<const float2*>(S.p[i]);
 #pragma unroll
-            for (int e = 0; e < EL; ++e) {
-              // 0 * V is not 0 for an infinite or NaN V
-              const float xv = who[j] >> v & 1 ? x[j][e] : 0.f;
-              acc[v][e] = fmaf(s_p[warp][i + j][v], xv, acc[v][e]);
-            }
+        for (int v = 0; v < kVecs / 2; ++v)
+#pragma unroll
+          for (int e = 0; e < EL; ++e)
+            acc[v][e] = fma2(px[v], make_float2(who >> (2 * v) & 1 ? vx[e] : 0.f, who >> (2 * v + 1) & 1 ? vx[e] : 0.f),
+                             acc[v][e]);
+      };
+      if (__all_sync(0xffffffffu, any == kAll)) {
+#pragma unroll 4
+        for (int i = 0; i < kTile; ++i) sum(i, kAll);
+      } else {                              // 0 * V is not 0 for an infinite or NaN V
+#pragma unroll 2
+        for (int i = 0; i < kTile; ++i) sum(i, __shfl_sync(0xffffffffu, any, i));
       }
       __syncwarp();
+      copy(a.v_pool, next, false, S.v);
+      row = next;
     }
     const bool whole = at.j0 == 0 && at.j1 == at.nt;
     const int64_t slot = (w * 2 + (at.j0 == 0 ? 1 : 0)) * kVecs;
@@ -136,11 +221,11 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const __grid_con
         float* out = reinterpret_cast<float*>(a.O) +
                  ((int64_t)(at.q.row0 + vi / a.g) * a.n_q_heads + h * a.g + vi % a.g) * D + lane * EL;
 #pragma unroll
-        for (int e = 0; e < EL; ++e) out[e] = acc[v][e] / l[v];
+        for (int e = 0; e < EL; ++e) out[e] = (v % 2 ? acc[v / 2][e].y : acc[v / 2][e].x) / l[v];
       } else {
         if (lane == 0) a.part_ml[slot + v] = make_float2(m[v], l[v]);
 #pragma unroll
-        for (int e = 0; e < EL; ++e) a.part_o[(slot + v) * D + lane * EL + e] = acc[v][e];
+        for (int e = 0; e < EL; ++e) a.part_o[(slot + v) * D + lane * EL + e] = v % 2 ? acc[v / 2][e].y : acc[v / 2][e].x;
       }
     }
     __syncwarp();
@@ -266,7 +351,7 @@ template <typename T> cudaError_t launch_join(const TreeArgs& a, int d, cudaStre
 // ---- host side ---------------------------------------------------------------
 
 constexpr int kCtas = 152;                // SMs
-constexpr int kSimtCtas = 3;              // CTAs of an SM (fp32 layers)
+constexpr int kSimtCtas = 5;              // CTAs of an SM (fp32 layers): as many fit where d = 64, three where d = 128
 
 fuse_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? FUSE_OK : FUSE_ERR_CUDA; }
 
@@ -287,9 +372,12 @@ TreePlan plan_tree(const fuse_layer_desc_t& d, int n_seq) {
 }  // namespace
 
 cudaError_t launch_tree_simt(const fuse_layer_desc_t& d, const TreeArgs& a, cudaStream_t s) {
-  const dim3 grid(a.workers / kWarps), block(kWarps * 32);
-  return d.head_dim == 128 ? launch_pdl(tree_simt_kernel<128>, grid, block, 0, s, a)
-                           : launch_pdl(tree_simt_kernel<64>, grid, block, 0, s, a);
+  auto run = [&](auto kernel, int smem) {
+    if (cudaError_t e = set_dyn_smem_once(reinterpret_cast<const void*>(kernel), smem)) return e;
+    return launch_pdl(kernel, dim3(a.workers / kWarps), dim3(kWarps * 32), smem, s, a);
+  };
+  return d.head_dim == 128 ? run(tree_simt_kernel<128>, sizeof(SimtShared<128>) * kWarps)
+                           : run(tree_simt_kernel<64>, sizeof(SimtShared<64>) * kWarps);
 }
 
 }  // namespace fusekv
