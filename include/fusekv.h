@@ -599,6 +599,8 @@ fuse_status_t fuse_pages_copy(const fuse_layer_desc_t* desc, const fuse_pools_t*
  * Trees.  parents [n_rows] int32 (device) gives each new token the number,
  * within its sequence, of the one that it follows: a smaller one, or -1 for
  * what follows the held tokens.  NULL: each follows the one before it.
+ * The tokens of a table's row and of the pool number less than 2^31 - 256 (else
+ * FUSE_ERR_UNSUPPORTED), sequences at most 65535.
  * A sequence whose row starts descend or pass n_rows, that has more than
  * max_new rows, whose length is negative, or whose slots pass the table's row
  * is recorded as FUSE_ERR_DEVICE_BOUNDS and left out.  A parent out of range is
@@ -690,7 +692,8 @@ fuse_status_t fuse_cache_append(const fuse_layer_desc_t* desc, const fuse_rope_t
  * weights are rounded to bf16 where they meet the values (their sum is that of
  * the unrounded ones).  What a row does not see does not reach it, infinities
  * and NaN included (rows behind a sequence's last slot among it); a key of
- * score -infinity has no weight.  The slots of a page outside the pool are
+ * score -infinity has no weight.  (Sums are formed before they are divided, with
+ * weights of up to 2^16: values have to stay below 2^80.)  The slots of a page outside the pool are
  * recorded as FUSE_ERR_DEVICE_BOUNDS and count as not there.  No atomics on
  * sums: equal inputs give equal outputs.  O may not overlap an input.
  * The workspace (of fuse_tree_workspace_size, which depends on the shapes and
@@ -737,7 +740,7 @@ fuse_status_t fuse_verify_tree(int32_t n_seq, int64_t n_rows, int32_t vocab, con
 /* Keep the rows of a path in every pool and drop the other new ones: for i <
  * count[s], slot lens[s] + i receives what slot lens[s] + path[s][i] held, and
  * then lens[s] += count[s].  pools: F32 or BF16, as fuse_pages_copy's; seqs:
- * as the rows were appended.  A path that does not ascend or names a row that
+ * as the rows were appended.  No pool is listed twice (FUSE_ERR_INVALID_ARG).  A path that does not ascend or names a row that
  * the sequence does not have, or a count outside [0, max_path], is recorded as
  * FUSE_ERR_DEVICE_BOUNDS and leaves the sequence as it is; so does a page
  * outside the pool.  ws: FUSE_CACHE_WORKSPACE bytes. */

@@ -254,9 +254,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid
   pdl_trigger();
   const int row = blockIdx.x, h = blockIdx.y;
   const int s = seq_of_row(a.seq.rows, a.seq.n_seq, row);
-  if (s < 0 || s >= a.seq.n_seq) return;
-  Seq q;
-  if (!seq_of(a.seq, s, &q) || row < q.row0 || row >= q.row0 + q.n) return;
+  Seq q{0, 0, 0};
+  if (s < 0 || s >= a.seq.n_seq || !seq_of(a.seq, s, &q) || row < q.row0 || row >= q.row0 + q.n) {
+    pdl_wait();                           // who waits for this kernel waits for the one before it, too
+    return;
+  }
   const int nt = tiles_of(a, q), groups = (q.n * a.g + a.vecs - 1) >> a.vecs_log2;
   const int per_vec = max(1, kJoinWarps >> a.g_log2), share = warp % per_vec;
   const int sub = lane / L, ch = lane % L * 4, step = per_vec * kSub, mine = share * kSub + sub;
@@ -431,7 +433,9 @@ fuse_status_t fuse_attend_tree(const fuse_layer_desc_t* desc, const fuse_seqs_t*
   // no more workers than the tables' rows could give tiles to
   const int64_t cap = ((int64_t)seqs->max_blocks * seqs->block_size + P.tile - 1) / P.tile;
   const int64_t groups = ((int64_t)seqs->max_new * a.g + P.vecs - 1) / P.vecs;
-  const int64_t most = std::min<int64_t>(P.workers, cap * groups * seqs->n_seq * a.n_kv_heads);
+  int64_t most = 1;
+  for (const int64_t f : {cap, groups, (int64_t)seqs->n_seq, (int64_t)a.n_kv_heads})
+    most = std::min<int64_t>(P.workers, most * f);
   a.workers = desc->dtype == FUSE_BF16 ? (int)most : (int)((most + kWarps - 1) / kWarps * kWarps);
   a.scale = 1.4426950408889634f / std::sqrt((float)desc->head_dim);
   a.start = reinterpret_cast<int64_t*>(at(P.start));

@@ -112,7 +112,7 @@ __device__ __forceinline__ RowPlace place_row(const AppendArgs& a, int row) {
 // A warp takes a row, or a share of its heads; D / 16 lanes a head, a lane 16 channels of
 // it, two runs of 8 (apart by half the rotated channels in the half layout) and of all
 // heads the same ones, so that it reads their angles once.  Memory bounds it on prompts
-// (10368 rows of 32 query and 8 KV heads, d = 128: @@ us, @@ TB/s; with a row's angles
+// (10368 rows of 32 query and 8 KV heads, d = 128: 49 us, 5.2 TB/s; with a row's angles
 // shared by a block of 256 threads, which has to wait for them, 52 us), the chain of reads
 // in front of the angles on single tokens, so the first units are read before that chain.
 template <typename T, int D>
@@ -363,8 +363,9 @@ fuse_status_t check_seqs(const fuse_seqs_t* q, int64_t n_rows, int max_new, SeqA
   if (q->block_size <= 0 || q->max_blocks <= 0 || q->max_new <= 0 || q->n_pool_blocks <= 0)
     return FUSE_ERR_INVALID_ARG;
   if (q->max_new > max_new) return FUSE_ERR_UNSUPPORTED;
-  // slots and pool rows are 32-bit numbers
-  if ((int64_t)q->max_blocks * q->block_size > INT32_MAX || q->n_pool_blocks > INT32_MAX / q->block_size)
+  // slots and pool rows are 32-bit numbers, up to the end of their tile
+  constexpr int64_t kMost = INT32_MAX - 256;
+  if ((int64_t)q->max_blocks * q->block_size > kMost || q->n_pool_blocks > kMost / q->block_size)
     return FUSE_ERR_UNSUPPORTED;
   if (q->n_seq > 0 && (!q->tables || !q->lens || !q->rows)) return FUSE_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(q->tables) | reinterpret_cast<uintptr_t>(q->lens) |
@@ -473,6 +474,12 @@ fuse_status_t fuse_cache_keep(const fuse_layer_desc_t* desc, const fuse_pools_t*
   for (int i = 0; i < pools->n_pools; ++i) {
     if (!pools->h_pools[i].k || !pools->h_pools[i].v) return FUSE_ERR_INVALID_ARG;
     if (!aligned16(pools->h_pools[i].k) || !aligned16(pools->h_pools[i].v)) return FUSE_ERR_MISALIGNED;
+    // rows are moved in place: twice is once too often
+    bool again = pools->h_pools[i].k == pools->h_pools[i].v;
+    for (int j = 0; j < i; ++j)
+      again |= pools->h_pools[j].k == pools->h_pools[i].k || pools->h_pools[j].v == pools->h_pools[i].v ||
+               pools->h_pools[j].k == pools->h_pools[i].v || pools->h_pools[j].v == pools->h_pools[i].k;
+    if (again) return FUSE_ERR_INVALID_ARG;
   }
   if (max_path < 1) return FUSE_ERR_INVALID_ARG;
   if (max_path > FUSE_TREE_MAX_NEW) return FUSE_ERR_UNSUPPORTED;

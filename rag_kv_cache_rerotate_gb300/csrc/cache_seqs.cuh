@@ -21,7 +21,7 @@ struct SeqArgs {
 // inverse gives the quotient or one more.
 __device__ __forceinline__ int page_of(const SeqArgs& a, int slot, int* in_page) {
   int b = a.block_inv ? (int)__umulhi((uint32_t)slot, a.block_inv) : slot;
-  int r = slot - b * a.block_size;
+  int r = (int)((uint32_t)slot - (uint32_t)b * (uint32_t)a.block_size);
   if (r < 0) {
     --b;
     r += a.block_size;

@@ -56,6 +56,26 @@ def test_long_contexts(dtype, heads):
     check(s, rows=[0, 1, 2, 33, 65, 66, 70])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("slope", [0.05, 0.28, 4.0, -0.28])
+def test_scores_that_rise_or_fall(dtype, slope):
+    # from key to key by 1.44 * slope (log2): a worker's tiles outweigh the ones before them by a little or by far
+    s = Step(StepCase(lens=[20000], new=[64], heads=(16, 4, 64), dtype=dtype, block_size=32, width=3, scale=0.1))
+    s.Qr[..., 0] = 8.0
+    page, at = s.slots(0, range(20064))
+    s.kp[torch.as_tensor(page).cuda(), torch.as_tensor(at).cuda(), :, 0] = (
+        slope * torch.arange(20064, device="cuda")[:, None]).to(s.kp.dtype)
+    check(s, rows=[0, 1, 31, 63])
+
+
+def test_calls_without_rows_of_a_sequence():
+    # every row lies outside the sequences; what follows finds the lengths as the call did
+    s = Step(StepCase(lens=[40, 7], new=[0, 0], front=5, behind=3))             # tables of 48 and 16 slots
+    for _ in range(8):
+        check(s)
+        s.lens.add_(1)
+
+
 def test_many_sequences():
     # workers take several units; sequences without rows between them
     n = 300

@@ -32,6 +32,7 @@ def _seqs(fk, **kw):
 BAD_SEQS = [("n_seq", -1, "INVALID_ARG"), ("n_seq", 65536, "UNSUPPORTED"), ("block_size", 0, "INVALID_ARG"),
             ("max_blocks", 0, "INVALID_ARG"), ("max_new", 0, "INVALID_ARG"), ("max_new", 65, "UNSUPPORTED"),
             ("n_pool_blocks", 0, "INVALID_ARG"), ("max_blocks", 1 << 28, "UNSUPPORTED"),
+            ("max_blocks", (1 << 27) - 15, "UNSUPPORTED"), ("n_pool_blocks", (1 << 27) - 15, "UNSUPPORTED"),
             ("tables", None, "INVALID_ARG"), ("lens", None, "INVALID_ARG"), ("rows", None, "INVALID_ARG"),
             ("tables", A + 2, "MISALIGNED"), ("lens", A + 1, "MISALIGNED"), ("rows", A + 2, "MISALIGNED")]
 
@@ -120,7 +121,7 @@ def test_verify_refusals(fk):
 
 
 def test_keep_refusals(fk):
-    pool = (fk.Pool * 1)(fk.Pool(A, A, None, None))
+    pool = (fk.Pool * 2)(fk.Pool(A, 2 * A, None, None), fk.Pool(3 * A, 4 * A, None, None))
 
     def pools(**kw):
         a = dict(n_pools=1, kv_storage=fk.FUSE_BF16, block_size=16, reserved=0, n_blocks=30,
@@ -143,9 +144,13 @@ def test_keep_refusals(fk):
     assert call(ws=None) == fk.FUSE_ERR_WORKSPACE
     assert call(seqs=_seqs(fk, n_seq=0)) == fk.FUSE_OK
     for name, value, status in BAD_SEQS:
-        assert call(seqs=_seqs(fk, **{name: value})) == (
-            fk.FUSE_ERR_INVALID_ARG if name in ("block_size", "n_pool_blocks") else
-            getattr(fk, "FUSE_ERR_" + status)), name
+        assert call(seqs=_seqs(fk, **{name: value})) == getattr(fk, "FUSE_ERR_" + status), name
+    assert call(pools(n_pools=2), seqs=_seqs(fk, n_seq=0)) == fk.FUSE_OK
+    for name, value in (("k", A), ("k", 2 * A), ("v", A), ("v", 2 * A), ("v", 3 * A)):    # moved twice
+        saved = getattr(pool[1], name)
+        setattr(pool[1], name, value)
+        assert call(pools(n_pools=2)) == fk.FUSE_ERR_INVALID_ARG, (name, value)
+        setattr(pool[1], name, saved)
     pool[0].v = None
     assert call() == fk.FUSE_ERR_INVALID_ARG
     pool[0].v = A + 8
