@@ -208,6 +208,12 @@ __device__ __noinline__ void add_nonfinite(T* dst, int n, unsigned long long lef
   }
 }
 
+// A number that the warp's lanes share, as one that the compiler knows them to share:
+// the products' operands are formed once, not by lanes.
+__device__ __forceinline__ uint64_t uniform64(uint64_t x) {
+  return (uint64_t)__shfl_sync(0xffffffffu, (uint32_t)(x >> 32), 0) << 32 | __shfl_sync(0xffffffffu, (uint32_t)x, 0);
+}
+
 // The CTA's part i (by a whole warp); false behind the last one.
 __device__ __forceinline__ bool take_part(Ctl* ctl, uint32_t& i, TreePart& p, uint32_t* err) {
   const int at = i % kParts;
@@ -417,7 +423,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!u.dual) qb ^= 1;
-      if (ok && lw == 0) ahead = plan();
       for (int i = 0; ok && i <= u.tiles; ++i) {
         if (i < u.tiles) {
           places(page[0], in_page[0], rn);
@@ -431,6 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           entries(min(p.j0 + i + kAhead, p.j1 - 1), page[kAhead - 1], in_page[kAhead - 1]);
           ok = issue(&mapK, a.k_pool, rn);
+          if (ok && i == 0 && lw == 0) ahead = plan();
         }
         if (ok && i > 0) ok = issue(&mapV, a.v_pool, rc);
 #pragma unroll
@@ -473,12 +479,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (kGather) tc::fence_proxy_async_smem();         // the copies' writes are the generic proxy's
         tc::tc_fence_after();
-        const uint32_t qa = tc::smem_u32(sQ) + (u.dual ? w : qb) * kTile, ka = tc::smem_u32(sR) + st * kTile;
+        const uint64_t qd = uniform64(tc::smem_desc_k128(tc::smem_u32(sQ) + (u.dual ? w : qb) * kTile));
+        const uint64_t kd = uniform64(tc::smem_desc_k128(tc::smem_u32(sR) + st * kTile, kGroup));
+        const uint32_t d = __shfl_sync(0xffffffffu, tmem + w * kKB, 0);
         if (tc::elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            tc::mma_bf16(tmem + w * kKB, tc::smem_desc_k128(qa + (kk >> 2) * kHalf + (kk & 3) * 32),
-                         tc::smem_desc_k128(ka + (kk >> 2) * kAtom + (kk & 3) * 32, kGroup), idesc, kk != 0);
+            tc::mma_bf16(d, qd + ((kk >> 2) * kHalf + (kk & 3) * 32) / 16,
+                         kd + ((kk >> 2) * kAtom + (kk & 3) * 32) / 16, idesc, kk != 0);
           tc::mma_commit(&ctl->s_full[w]);
           if (!u.dual || w == 1) tc::mma_commit(&ctl->empty[st]);
           if (k == u.n - 1) {
@@ -546,12 +554,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         if (kGather) tc::fence_proxy_async_smem();
         tc::tc_fence_after();
-        const uint32_t va = tc::smem_u32(sR) + st * kTile;
+        const uint64_t vd = uniform64(tc::smem_desc_mn128(tc::smem_u32(sR) + st * kTile, kAtom, kGroup));
+        const uint32_t d = __shfl_sync(0xffffffffu, tmem + kColO + w * D, 0), ad = __shfl_sync(0xffffffffu, tmem + w * kKB, 0);
         if (tc::elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kKB / 16; ++kk)
-            tc::mma_bf16_ts(tmem + kColO + w * D, tmem + w * kKB + kk * 8,
-                            tc::smem_desc_mn128(va + kk * 2 * kGroup, kAtom, kGroup), idesc, (k > 1 || kk != 0) ? 1u : 0u);
+            tc::mma_bf16_ts(d, ad + kk * 8, vd + kk * 2 * kGroup / 16, idesc, (k > 1 || kk != 0) ? 1u : 0u);
           tc::mma_commit(&ctl->pv_done[w]);
           if (!u.dual || w == 1) tc::mma_commit(&ctl->empty[st]);
         }
