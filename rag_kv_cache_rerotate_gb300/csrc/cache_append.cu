@@ -80,21 +80,51 @@ struct RowPlace {
   int pos;
 };
 
+// The sequence of new row `row`, by a whole warp; false where it has none.  Up to 128
+// sequences are all read at once, four a lane, so that one read's latency finds it
+// (64 next tokens: 5.7 us, with a search and then a look at what it found 6.0; a prompt
+// of 10368: 44 and 49).
+__device__ __forceinline__ bool find_seq(const SeqArgs& a, int row, int* s, Seq* q) {
+  if (a.n_seq > 128) {
+    *s = seq_of_row(a.rows, a.n_seq, row);
+    return *s >= 0 && *s < a.n_seq && seq_of(a, *s, q);
+  }
+  const int s0 = threadIdx.x % 32 * 4;
+  int start[5], len[4];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) start[i] = a.rows[min(s0 + i, a.n_seq)];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) len[i] = a.lens[min(s0 + i, a.n_seq - 1)];
+  int below = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) below += s0 + i < a.n_seq && start[i] <= row;
+  *s = __reduce_add_sync(0xffffffffu, below) - 1;
+  if (*s < 0) return false;
+  const int k = *s & 3, from = *s >> 2;
+  const int r0 = __shfl_sync(0xffffffffu, k == 0 ? start[0] : k == 1 ? start[1] : k == 2 ? start[2] : start[3], from);
+  const int r1 = __shfl_sync(0xffffffffu, k == 0 ? start[1] : k == 1 ? start[2] : k == 2 ? start[3] : start[4], from);
+  const int l = __shfl_sync(0xffffffffu, k == 0 ? len[0] : k == 1 ? len[1] : k == 2 ? len[2] : len[3], from);
+  return check_seq(a, *s, r0, r1, l, q);
+}
+
 // Position and pool row of new row `row`, by a whole warp.
 __device__ __forceinline__ RowPlace place_row(const AppendArgs& a, int row) {
   const int lane = threadIdx.x % 32;
   RowPlace p{-1, -1, 0};
-  const int s = seq_of_row(a.seq.rows, a.seq.n_seq, row);
-  if (s < 0 || s >= a.seq.n_seq) return p;
+  int s;
   Seq q;
-  if (!seq_of(a.seq, s, &q) || row < q.row0 || row >= q.row0 + q.n) return p;
+  if (!find_seq(a.seq, row, &s, &q) || row < q.row0 || row >= q.row0 + q.n) return p;
   const int i = row - q.row0;
+  // its page and the parents of the new tokens up to it (lanes hold those of the first
+  // 32 and of the others): read before any is looked at
+  int in_page, up0 = -1, up1 = -1;
+  const int page = a.seq.tables[(int64_t)s * a.seq.max_blocks + page_of(a.seq, q.len + i, &in_page)];
+  if (a.parents && lane <= i) up0 = a.parents[q.row0 + lane];
+  if (a.parents && lane + 32 <= i) up1 = a.parents[q.row0 + lane + 32];
   int depth = i;
   if (a.parents) {
-    // lanes hold the parents of the first 32 new tokens and of the others
-    int up0 = -1, up1 = -1;
-    if (lane <= i) up0 = parent_of(a.parents, q, lane, a.seq.err);
-    if (lane + 32 <= i) up1 = parent_of(a.parents, q, lane + 32, a.seq.err);
+    up0 = checked_parent(up0, q, lane, a.seq.err);
+    up1 = checked_parent(up1, q, lane + 32, a.seq.err);
     depth = 0;
     for (int j = i;;) {
       const int lo = __shfl_sync(0xffffffffu, up0, j & 31), hi = __shfl_sync(0xffffffffu, up1, j & 31);
@@ -105,15 +135,15 @@ __device__ __forceinline__ RowPlace place_row(const AppendArgs& a, int row) {
   }
   p.row = row;
   p.pos = q.len + depth;
-  p.pool = pool_row(a.seq, s, q.len + i);
+  p.pool = checked_page(a.seq, page, in_page);
   return p;
 }
 
 // A warp takes a row, or a share of its heads; D / 16 lanes a head, a lane 16 channels of
 // it, two runs of 8 (apart by half the rotated channels in the half layout) and of all
 // heads the same ones, so that it reads their angles once.  Memory bounds it on prompts
-// (10368 rows of 32 query and 8 KV heads, d = 128: 49 us, 5.2 TB/s; with a row's angles
-// shared by a block of 256 threads, which has to wait for them, 52 us), the chain of reads
+// (10368 rows of 32 query and 8 KV heads, d = 128: 44 us, 5.8 TB/s; with a row's angles
+// shared by a block of 256 threads, which has to wait for them, 52 us when that took 49), the chain of reads
 // in front of the angles on single tokens, so the first units are read before that chain.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
@@ -238,19 +268,22 @@ struct KeepArgs {
 // A sequence's path: whether it can be kept (by a whole block; s_row receives
 // the pool rows of the nodes and of the slots that they go to).
 __device__ __forceinline__ int kept(const KeepArgs& a, int s, int64_t (*s_row)[2]) {
+  // (all reads before the first check)
+  const int n = a.count[s], i = threadIdx.x;
+  const int32_t* path = a.path + (int64_t)s * a.max_path;
+  const int p = i < a.max_path ? path[i] : -1, before = i > 0 && i < a.max_path ? path[i - 1] : -1;
   Seq q;
   const bool ok = seq_of(a.seq, s, &q);
-  const int n = a.count[s];
   bool bad = !ok || n < 0 || n > a.max_path || n > q.n;
-  if (!bad && (int)threadIdx.x < n) {
-    const int i = threadIdx.x;
-    const int32_t* path = a.path + (int64_t)s * a.max_path;
-    const int p = path[i], before = i > 0 ? path[i - 1] : -1;
+  if (!bad && i < n) {
     bad = p <= before || p < 0 || p >= q.n;
     if (!bad) {
-      s_row[i][0] = pool_row(a.seq, s, q.len + p);
-      s_row[i][1] = p == i ? s_row[i][0] : pool_row(a.seq, s, q.len + i);
-      if (s_row[i][0] < 0 || s_row[i][1] < 0) bad = true;
+      int at0, at1;
+      const int page0 = a.seq.tables[(int64_t)s * a.seq.max_blocks + page_of(a.seq, q.len + p, &at0)];
+      const int page1 = a.seq.tables[(int64_t)s * a.seq.max_blocks + page_of(a.seq, q.len + i, &at1)];
+      s_row[i][0] = checked_page(a.seq, page0, at0);
+      s_row[i][1] = checked_page(a.seq, page1, at1);
+      bad = s_row[i][0] < 0 || s_row[i][1] < 0;
     }
   }
   if (__syncthreads_or(bad)) {

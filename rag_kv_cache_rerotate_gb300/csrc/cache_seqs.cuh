@@ -55,23 +55,28 @@ __device__ __forceinline__ bool seq_of(const SeqArgs& a, int s, Seq* q) {
 }
 
 // The parent of new token i (-1: none); one out of range is recorded.
-__device__ __forceinline__ int parent_of(const int32_t* parents, const Seq& q, int i, uint32_t* err) {
-  if (!parents) return i - 1;
-  const int p = parents[q.row0 + i];
+__device__ __forceinline__ int checked_parent(int p, const Seq& q, int i, uint32_t* err) {
   if (p >= -1 && p < i) return p;
   report_error(err, FUSE_ERR_DEVICE_BOUNDS, SITE_SEQ_PARENT, (uint32_t)(q.row0 + i));
   return -1;
 }
+__device__ __forceinline__ int parent_of(const int32_t* parents, const Seq& q, int i, uint32_t* err) {
+  if (!parents) return i - 1;
+  return checked_parent(parents[q.row0 + i], q, i, err);
+}
 
 // The pool row of a slot; -1 where its page is outside the pool (recorded).
-__device__ __forceinline__ int64_t pool_row(const SeqArgs& a, int s, int slot) {
-  int in_page;
-  const int page = a.tables[(int64_t)s * a.max_blocks + page_of(a, slot, &in_page)];
+__device__ __forceinline__ int64_t checked_page(const SeqArgs& a, int page, int in_page) {
   if (page < 0 || page >= a.n_pool_blocks) {
     report_error(a.err, FUSE_ERR_DEVICE_BOUNDS, SITE_SEQ_PAGE, (uint32_t)page);
     return -1;
   }
   return (int64_t)page * a.block_size + in_page;
+}
+__device__ __forceinline__ int64_t pool_row(const SeqArgs& a, int s, int slot) {
+  int in_page;
+  const int page = a.tables[(int64_t)s * a.max_blocks + page_of(a, slot, &in_page)];
+  return checked_page(a, page, in_page);
 }
 
 // The sequence whose rows hold `row`: the last s with rows[s] <= row (by a whole
