@@ -142,8 +142,8 @@ __device__ __forceinline__ RowPlace place_row(const AppendArgs& a, int row) {
 // A warp takes a row, or a share of its heads; D / 16 lanes a head, a lane 16 channels of
 // it, two runs of 8 (apart by half the rotated channels in the half layout) and of all
 // heads the same ones, so that it reads their angles once.  Memory bounds it on prompts
-// (10368 rows of 32 query and 8 KV heads, d = 128: 44 us, 5.8 TB/s; with a row's angles
-// shared by a block of 256 threads, which has to wait for them, 52 us when that took 49), the chain of reads
+// (10368 rows of 32 query and 8 KV heads, d = 128: 44 us, 5.8 TB/s; a row's angles shared
+// by a block of 256 threads, which waits for them, made 52 of 49), the chain of reads
 // in front of the angles on single tokens, so the first units are read before that chain.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
