@@ -85,7 +85,7 @@ struct Ctl {
   TreePart part[kParts];                      // what the CTA works at, planned ahead by the first load warp
 };
 
-constexpr int kCtlBytes = 3072;               // in front of the tiles, which start at multiples of 1024
+constexpr int kCtlBytes = 3 * 1024;           // in front of the tiles, which start at multiples of 1024
 static_assert(sizeof(Ctl) <= kCtlBytes, "shared memory");
 template <int D> constexpr int smem_bytes() { return kCtlBytes + (2 + Ring<D>::stages) * Ring<D>::tile; }
 static_assert(smem_bytes<128>() <= 227 * 1024 && smem_bytes<64>() <= 227 * 1024, "shared memory");
