@@ -83,12 +83,13 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const __grid_con
       const int key = j * kTile + lane;
       return j < at.j1 && key < n_keys ? (int)pool_row(a.seq, at.s, key) : -1;
     };
-    // (a key without a row gets zeros)
-    auto copy = [&](const void* pool, int row, bool swap, float4 (*to)[kPieces]) {
+    // Rows of a tile (a key without one gets zeros), or of none: copies have no order among
+    // themselves, so that none may be on its way to a place when the next one to it starts.
+    auto copy = [&](const void* pool, int row, bool swap, float4 (*to)[kPieces], bool tile) {
       const int r0 = lane / kPieces, c = lane % kPieces;
       const float4* from = reinterpret_cast<const float4*>(pool) + h * kPieces + c;
 #pragma unroll 8
-      for (int i = 0; i < kTile; i += kRowsOnce) {
+      for (int i = 0; tile && i < kTile; i += kRowsOnce) {
         const int r = i + r0, ri = __shfl_sync(0xffffffffu, row, r);
         copy16(&to[r][swap ? c ^ (r & 7) : c], from + (int64_t)max(ri, 0) * (a.n_kv_heads * kPieces), ri < 0);
       }
@@ -106,8 +107,8 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const __grid_con
 #pragma unroll
       for (int e = 0; e < EL; ++e) x[v][e] = q[e * 32 + lane];
     }
-    copy(a.k_pool, row, true, S.k);
-    copy(a.v_pool, row, false, S.v);
+    copy(a.k_pool, row, true, S.k, true);
+    copy(a.v_pool, row, false, S.v, true);
     uint64_t seen[kVecs];
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) seen[v] = 0;
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const __grid_con
         }
       }
       __syncwarp();
-      copy(a.k_pool, next, true, S.k);
+      copy(a.k_pool, next, true, S.k, j + 1 < at.j1);
       uint32_t any = 0;                     // bit v: that vector sees this key
       float s[kVecs];
       bool more = false;
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const __grid_con
         for (int i = 0; i < kTile; ++i) sum(i, __shfl_sync(0xffffffffu, any, i));
       }
       __syncwarp();
-      copy(a.v_pool, next, false, S.v);
+      copy(a.v_pool, next, false, S.v, j + 1 < at.j1);
       row = next;
     }
     const bool whole = at.j0 == 0 && at.j1 == at.nt;
