@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&ctl->q_full[i], 1);
       tc::mbar_init(&ctl->q_empty[i], 1);
       tc::mbar_init(&ctl->s_full[i], 1);
-      tc::mbar_init(&ctl->p_full[i], 256);
+      tc::mbar_init(&ctl->p_full[i], kSoftWarps / 2);
       tc::mbar_init(&ctl->pv_done[i], 1);
     }
     for (int i = 0; i < kSt; ++i) {
@@ -465,23 +465,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < u.n; ++k) {
         const int w = k & 1;
         const uint32_t c = w ? c1 : c0;
-        // the buffer holds P of the stream's step before until that step's P.V is done
-        // (and with it every ring item up to this one's slot has been full)
-        if (c > 0 && !wait32(&ctl->pv_done[w], c - 1, ctl, err, W_S_FREE)) {
-          ok = false;
-          break;
-        }
+        // (What was in the ring's slot before has been full: keys of an earlier step, waited for here,
+        // or values of a step three before this one or earlier: of the last two steps, which alone
+        // need not have been waited for, the values lie at most three places in front.)
         const uint32_t q = it + u.k_item(u.tile(k));
         const int st = q % kSt;
         if (!wait32(&ctl->full[st], q / kSt, ctl, err, W_K_FULL)) {
           ok = false;
           break;
         }
-        if (kGather) tc::fence_proxy_async_smem();         // the copies' writes are the generic proxy's
-        tc::tc_fence_after();
         const uint64_t qd = uniform64(tc::smem_desc_k128(tc::smem_u32(sQ) + (u.dual ? w : qb) * kTile));
         const uint64_t kd = uniform64(tc::smem_desc_k128(tc::smem_u32(sR) + st * kTile, kGroup));
         const uint32_t d = __shfl_sync(0xffffffffu, tmem + w * kKB, 0);
+        // the buffer holds P of the stream's step before until that step's P.V is done: waited for
+        // last, as it is what the product waits for
+        if (c > 0 && !wait32(&ctl->pv_done[w], c - 1, ctl, err, W_S_FREE)) {
+          ok = false;
+          break;
+        }
+        if (kGather) tc::fence_proxy_async_smem();         // the copies' writes are the generic proxy's
+        tc::tc_fence_after();
         if (tc::elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
@@ -548,14 +551,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) ctl->fix[with_new % kFix] = found;     // read once this product is done
           __syncwarp();
         }
+        const uint64_t vd = uniform64(tc::smem_desc_mn128(tc::smem_u32(sR) + st * kTile, kAtom, kGroup));
+        const uint32_t d = __shfl_sync(0xffffffffu, tmem + kColO + w * D, 0), ad = __shfl_sync(0xffffffffu, tmem + w * kKB, 0);
         ok = wait32(&ctl->p_full[w], w ? c1 : c0, ctl, err, W_P_FULL);
         // the accumulators were last read at the end of the part before
         if (ok && k == 0) ok = wait32(&ctl->o_empty, parts ^ 1, ctl, err, W_O_EMPTY);
         if (!ok) break;
         if (kGather) tc::fence_proxy_async_smem();
         tc::tc_fence_after();
-        const uint64_t vd = uniform64(tc::smem_desc_mn128(tc::smem_u32(sR) + st * kTile, kAtom, kGroup));
-        const uint32_t d = __shfl_sync(0xffffffffu, tmem + kColO + w * D, 0), ad = __shfl_sync(0xffffffffu, tmem + w * kKB, 0);
         if (tc::elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kKB / 16; ++kk)
@@ -752,7 +755,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc::tmem_st_wait();
         tc::tc_fence_before();
-        tc::mbar_arrive(&ctl->p_full[w]);
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&ctl->p_full[w]);
         l0 = l0 * al0 + s0;
         l1 = l1 * al1 + s1;
       }
