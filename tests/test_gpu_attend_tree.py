@@ -83,6 +83,26 @@ def test_many_sequences():
     check(Step(StepCase(lens=rng.integers(0, 90, n).tolist(), new=rng.integers(0, 4, n).tolist(), heads=(4, 2, 64))))
 
 
+@pytest.mark.parametrize("bs", [16, 5])
+@pytest.mark.parametrize("d", [128, 64])
+def test_many_short_parts(d, bs):
+    # a worker takes a dozen units of one to six tiles, whose tiles take turns in its ring
+    n = 120
+    rng = np.random.default_rng(d + bs)
+    check(Step(StepCase(lens=rng.integers(0, 700, n).tolist(), new=rng.integers(1, 9, n).tolist(), width=2,
+                        heads=(16, 16, d), block_size=bs, seed=bs)))
+
+
+@pytest.mark.parametrize("d", [128, 64])
+def test_many_full_trees(d):
+    # both accumulators of a worker in use, units of one to four tiles, several a worker
+    n = 60
+    rng = np.random.default_rng(d)
+    new = rng.integers(40, 65, n).tolist()
+    s = Step(StepCase(lens=rng.integers(0, 400, n).tolist(), new=new, width=5, heads=(64, 16, d), seed=d))
+    check(s, rows=[r for a, b in zip(s.starts, s.starts[1:]) for r in (a, a + 31, b - 1)])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_large_and_lowest_scores(dtype):
     # one key takes all of a row's weight; scores near the type's range
