@@ -238,7 +238,8 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const __grid_con
 // g is more), every one of them a share of its parts, kRows of them in flight.
 // Latency bounds it, so what the attention does not write (rows, lengths) is read
 // before it is waited for, and the first parts beside their weights.  Many rows have few
-// parts each: four warps.  Few rows may have many: sixteen.
+// parts each: four warps.  Few rows may have many: sixteen.  (One token over 4096: 3 us of 16;
+// 8 trees of 64 over 33k: about 14 of 405, with 28 MB of parts.)
 constexpr int kRows = 4;
 
 template <typename T> __device__ __forceinline__ void store4(T* p, float4 v);

@@ -14,6 +14,10 @@
 // (Two score buffers of 64 keys a stream would hide the hand-overs, but products of
 // N = 64 run at half the rate of N = 128: 526 us instead of 412 on 8 trees of 64
 // over 33k.  P in two halves, the first one's product beside the second's softmax: 479.)
+// With 64 vectors and less a tile of keys and values takes as long as HBM needs for it (16 trees
+// over 512 to 8192: 64 us, 6.5 TB/s between the start and the end).  With 256 the chain of a
+// stream's step binds it, 2990 cycles: S 610 (its operands come from shared memory), softmax
+// 1150, P V 480, hand-overs 750; 8 trees of 64 over 33k take 405 us, 1.37 PFLOP/s.
 // The reference m is the first tile's maximum.  A later tile is weighed against it
 // as it stands, without its maximum being looked for: only where a thread's sum of
 // its weights passes 2^16 (no weight does otherwise) is the row's reference raised, O

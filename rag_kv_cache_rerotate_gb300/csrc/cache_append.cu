@@ -295,7 +295,8 @@ __device__ __forceinline__ int kept(const KeepArgs& a, int s, int64_t (*s_row)[2
 
 // A CTA: one sequence in one pool's keys or values.  path[i] >= i, so a thread
 // that takes a column of 16 bytes through the rows in order reads each before
-// it is written over.
+// it is written over.  Latency bounds it: with the lengths 4 to 5 us behind the copy of a few
+// bytes, on one sequence of 32 layers as on 96 of 8.
 __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constant__ KeepArgs a) {
   __shared__ int64_t s_row[FUSE_TREE_MAX_NEW][2];
   static_assert(FUSE_TREE_MAX_NEW <= kKeepThreads, "a thread a path entry");
@@ -317,7 +318,8 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constan
   }
 }
 
-// The lengths, once every CTA of the copies has read them.
+// The lengths, once every CTA of the copies has read them.  (One kernel for both, a cluster a
+// sequence, saves 0.2 us on 8 sequences of one layer and takes 3 more on one of 32, 8 on 3 of 80.)
 __global__ void __launch_bounds__(FUSE_TREE_MAX_NEW) keep_lens_kernel(const __grid_constant__ KeepArgs a) {
   __shared__ int64_t s_row[FUSE_TREE_MAX_NEW][2];
   pdl_wait();
