@@ -100,7 +100,9 @@ __device__ __forceinline__ Pair scan(Pair a) {
   return a;
 }
 
-// max(p - A q, 0) as a pair.
+// max(p - A q, 0) as a sum of two floats.  Where p is the rounding of A q the first of them is 0 and
+// the second all there is, so what asks for the remainder's sign takes `normal` of it first;
+// sums take it as it is.
 __device__ __forceinline__ Pair remainder_of(float p, float q, Pair A) {
   const float m = A.h * q;
   const float me = fmaf(A.h, q, -m);
@@ -108,6 +110,13 @@ __device__ __forceinline__ Pair remainder_of(float p, float q, Pair A) {
   two_sum(p, -m, s, e);
   e = (e - me) - A.l * q;
   return s + e > 0.f ? Pair{s, e} : Pair{0.f, 0.f};
+}
+
+// The same number with its sign in h.
+__device__ __forceinline__ Pair normal(Pair a) {
+  Pair r;
+  two_sum(a.h, a.l, r.h, r.l);
+  return r;
 }
 
 // What a pass over a row forms its entries from.  Rows of a large vocabulary need not
@@ -151,7 +160,7 @@ __device__ __noinline__ Four entries(const Pass& y, int i, const int* s_gone, ui
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     f.r[k] = Pair{usable(p[k], bad), 0.f};
-    if (y.q) f.r[k] = remainder_of(f.r[k].h, usable(q[k], bad), y.A);
+    if (y.q) f.r[k] = normal(remainder_of(f.r[k].h, usable(q[k], bad), y.A));
   }
   for (int g = 0; g < y.n_gone; ++g) {
     const int at = s_gone[g] - (4 * i - y.lead);
@@ -322,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
     if (par >= 0 && (which >> tid & 1)) {
       Pair r{pd, 0.f}, need = mul(Pair{ud, 0.f}, S);
       if (a.Q) {
-        r = remainder_of(pd, qd, A);
+        r = normal(remainder_of(pd, qd, A));
         need = mul(need, Pair{qd, 0.f});
       } else {
         for (int g = 0; g < y.n_gone; ++g)
