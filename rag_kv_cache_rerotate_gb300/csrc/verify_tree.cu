@@ -101,8 +101,8 @@ __device__ __forceinline__ Pair scan(Pair a) {
 }
 
 // max(p - A q, 0) as a sum of two floats.  Where p is the rounding of A q the first of them is 0 and
-// the second all there is, so what asks for the remainder's sign takes `normal` of it first;
-// sums take it as it is.
+// the second all there is, so that its sign is that of both (`positive`): pairs whose first float
+// has it, formed where entries are looked at, took 39.9 us instead of 38.6 on 64 sampled trees.
 __device__ __forceinline__ Pair remainder_of(float p, float q, Pair A) {
   const float m = A.h * q;
   const float me = fmaf(A.h, q, -m);
@@ -112,12 +112,7 @@ __device__ __forceinline__ Pair remainder_of(float p, float q, Pair A) {
   return s + e > 0.f ? Pair{s, e} : Pair{0.f, 0.f};
 }
 
-// The same number with its sign in h.
-__device__ __forceinline__ Pair normal(Pair a) {
-  Pair r;
-  two_sum(a.h, a.l, r.h, r.l);
-  return r;
-}
+__device__ __forceinline__ bool positive(Pair a) { return a.h + a.l > 0.f; }
 
 // What a pass over a row forms its entries from.  Rows of a large vocabulary need not
 // be aligned: `lead` entries are missing in front of a row's first aligned group of
@@ -160,7 +155,7 @@ __device__ __noinline__ Four entries(const Pass& y, int i, const int* s_gone, ui
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     f.r[k] = Pair{usable(p[k], bad), 0.f};
-    if (y.q) f.r[k] = normal(remainder_of(f.r[k].h, usable(q[k], bad), y.A));
+    if (y.q) f.r[k] = remainder_of(f.r[k].h, usable(q[k], bad), y.A);
   }
   for (int g = 0; g < y.n_gone; ++g) {
     const int at = s_gone[g] - (4 * i - y.lead);
@@ -331,13 +326,13 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
     if (par >= 0 && (which >> tid & 1)) {
       Pair r{pd, 0.f}, need = mul(Pair{ud, 0.f}, S);
       if (a.Q) {
-        r = normal(remainder_of(pd, qd, A));
+        r = remainder_of(pd, qd, A);
         need = mul(need, Pair{qd, 0.f});
       } else {
         for (int g = 0; g < y.n_gone; ++g)
           if (s_gone[g] == tok) r.h = 0.f;
       }
-      yes = r.h > 0.f && greater(r, need);             // a number that is none: no
+      yes = positive(r) && greater(r, need);             // a number that is none: no
     }
     const unsigned int bits = __ballot_sync(0xffffffffu, yes);
     if (lane == 0) s_ok[warp] = bits;
@@ -503,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           z = add(z, r[k]);
-          if (r[k].h > 0.f) {
+          if (positive(r[k])) {
             any = 4 * i - y.lead + k;
             if (first == INT32_MAX && !end && greater(z, t)) first = any;
           }
