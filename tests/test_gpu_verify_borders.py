@@ -71,3 +71,73 @@ def test_star_of_refused_tokens(children, vocab):
     if children > 1:
         want = [exact(parents, tokens[s], P[s], Q[s], u[s], un[s]) for s in range(n)]
         assert run(parents, tokens, P, Q, u, un) == ([w[0] for w in want], [w[1] for w in want])
+
+
+def close(a, b, lo=2.0 ** -42, hi=2.0 ** -28):
+    """Whether a and b differ by that much, relative to b.  The kernel's pairs have 48 bits: a sum or a product
+    of them is off by some 2^-46, so that from 2^-42 on both sides agree on the order; 24 bits do not tell."""
+    return b != 0 and lo <= abs(a / b - 1) <= hi
+
+
+def draw(rng, *shape):
+    # (numbers of 24 bits, between a quarter and a half)
+    return (rng.integers(1 << 23, 1 << 24, shape) * 2.0 ** -25).astype(np.float32)
+
+
+def test_drafts_next_to_their_border():
+    # u q against p, and u S q against p - q behind a refusal
+    rng = np.random.default_rng(0)
+    F = lambda x: Fraction(float(x))  # noqa: E731
+    cases = []
+    while len(cases) < 600:
+        p, q, u = draw(rng, 3), draw(rng, 3), np.float32(rng.random())
+        p[1] = u * q[1]                                    # rounded
+        if close(F(u) * F(q[1]), F(p[1])):
+            cases.append((p, q, [0, 0, u], [0, 1, 1]))     # the first child's token, or the second one's
+        p, q = draw(rng, 3), draw(rng, 3)
+        p[0] = 0                                           # the first child is refused
+        left = [max(F(a) - F(b), Fraction(0)) for a, b in zip(p, q)]
+        if left[1] > 0:
+            u = np.float32(float(left[1] / (sum(left) * F(q[1]))))
+            if u < 1 and close(F(u) * sum(left) * F(q[1]), left[1]):
+                cases.append((p, q, [0, 0, u], [0, 0, 1]))
+    P, Q = (np.stack([np.stack([c[i]] * 3) for c in cases]) for i in range(2))
+    u, tokens = np.array([c[2] for c in cases], np.float32), np.array([c[3] for c in cases])
+    for c, row in zip(cases, u):
+        if c[3][1] == 1:
+            row[1] = c[2][2]                               # the first child itself is next to its border
+    un = rng.random(len(cases)).astype(np.float32)
+    parents = [-1, 0, 0]
+    want = [exact(parents, tokens[s], P[s], Q[s], u[s], un[s])[0] for s in range(len(cases))]
+    assert 100 < sum(len(w) > 1 for w in want) < 500       # both sides of the border
+    assert run(parents, tokens, P, Q, u, un)[0] == want
+
+
+@pytest.mark.parametrize("refused", [0, 1, 2])
+@pytest.mark.parametrize("vocab", [4, 5003])
+def test_next_tokens_next_to_their_border(refused, vocab):
+    # u' sum r against r(0) + .. + r(x), where r is what refusals leave
+    rng = np.random.default_rng(refused)
+    F = lambda x: Fraction(float(x))  # noqa: E731
+    at = [0, 1, vocab // 2 + 1, vocab - 1]
+    cases = []
+    while len(cases) < 300:
+        p, q = draw(rng, 4), draw(rng, 4) / 2
+        p[0] = 0                                           # the children's token
+        r, S = [F(x) for x in p], Fraction(1)
+        for _ in range(refused):
+            r = [max(a - S * F(b), Fraction(0)) for a, b in zip(r, q)]
+            S = sum(r)
+        part = r[0] + r[1] + (r[2] if len(cases) % 2 else 0)
+        un = np.float32(float(part / sum(r)))
+        # (p, q and sums are about 1: 2^-42 of that, however small the part is)
+        if un < 1 and abs(F(un) * sum(r) - part) >= 2.0 ** -42 and close(F(un) * sum(r), part):
+            cases.append((p, q, un))
+    n, k = len(cases), refused + 1
+    P, Q = np.zeros((n, k, vocab), np.float32), np.zeros((n, k, vocab), np.float32)
+    P[..., at], Q[..., at] = (np.stack([c[i] for c in cases])[:, None] for i in range(2))
+    un = np.array([c[2] for c in cases], np.float32)
+    parents, tokens, u = [-1] + [0] * refused, np.zeros((n, k), np.int32), np.full((n, k), 0.5, np.float32)
+    want = [exact(parents, tokens[s], P[s], Q[s], u[s], un[s])[1] for s in range(n)]
+    got = run(parents, tokens, P, Q if refused else None, u, un)[1]
+    assert [(s, a, b) for s, (a, b) in enumerate(zip(got, want)) if a != b] == []
