@@ -728,8 +728,8 @@ fuse_status_t fuse_attend_tree(const fuse_layer_desc_t* desc, const fuse_seqs_t*
  * p_stride and q_stride elements apart.  Sums keep about 48 bits.  Entries that
  * are negative, infinite or NaN count as 0; they, tokens outside the vocabulary
  * and parents out of range (never accepted) are recorded where they are read.
- * u below 0, above the last float before 1 or NaN: as 0, that float, 0 for
- * u_next; NaN in u accepts nothing.  ws: FUSE_CACHE_WORKSPACE bytes. */
+ * Random numbers below 0 are read as 0, those from 1 on as the last float before
+ * 1; NaN as 0 in u_next, and in u it accepts nothing.  ws: FUSE_CACHE_WORKSPACE bytes. */
 fuse_status_t fuse_verify_tree(int32_t n_seq, int64_t n_rows, int32_t vocab, const int32_t* rows,
                                const int32_t* parents, const int32_t* tokens, const float* P,
                                int64_t p_stride, const float* Qd, int64_t q_stride, const float* u,

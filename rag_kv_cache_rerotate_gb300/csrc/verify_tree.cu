@@ -292,6 +292,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
     par = a.parents[row];
     tok = a.tokens[row];
     ud = a.u[row];
+    ud = ud < 0.f ? 0.f : ud >= 1.f ? 0.99999994f : ud;              // (NaN stays)
     bool bad = false;
     if (tid > 0) {
       if (par < 0 || par >= tid) {

@@ -141,3 +141,26 @@ def test_next_tokens_next_to_their_border(refused, vocab):
     want = [exact(parents, tokens[s], P[s], Q[s], u[s], un[s])[1] for s in range(n)]
     got = run(parents, tokens, P, Q if refused else None, u, un)[1]
     assert [(s, a, b) for s, (a, b) in enumerate(zip(got, want)) if a != b] == []
+
+
+@pytest.mark.parametrize("drawn", [True, False])
+def test_random_numbers_out_of_range(drawn):
+    # below 0 as 0, from 1 on as the last float before 1, NaN accepts nothing
+    values = [-1.0, -np.inf, -0.0, 1.0, 1.5, np.inf, 3e38, np.nan]
+    as_if = [0.0, 0.0, 0.0] + [0.99999994] * 4
+    n = len(values)
+    P = np.zeros((n, 2, 5), np.float32)
+    P[..., 1:4] = [0.25, 0.25, 0.5]
+    P[:, 0, 2] = 0.25 if drawn else 1.0                    # accepted whatever its number is, 1 and more aside
+    if not drawn:
+        P[:, 0, [1, 3]] = 0.0
+    Q = P.copy() if drawn else None
+    tokens, un = np.full((n, 2), 2), np.full(n, 0.5, np.float32)
+    u = np.array([[0.0, x] for x in values], np.float32)
+    got = run([-1, 0], tokens, P, Q, u, un)[0]
+    assert got == [[0, 1]] * len(as_if) + [[0]]
+    if drawn:                                              # a draft that its distribution does not have
+        Q[:, 0, 2] = 0.0
+        assert run([-1, 0], tokens, P, Q, u, un)[0] == got
+        P[:, 0, 2] = 0.0                                   # one that the target does not have
+        assert run([-1, 0], tokens, P, Q, u, un)[0] == [[0]] * n
