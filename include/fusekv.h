@@ -692,7 +692,8 @@ fuse_status_t fuse_cache_append(const fuse_layer_desc_t* desc, const fuse_rope_t
  * weights are rounded to bf16 where they meet the values (their sum is that of
  * the unrounded ones).  What a row does not see does not reach it, infinities
  * and NaN included (rows behind a sequence's last slot among it); a key of
- * score -infinity has no weight.  (Sums are formed before they are divided, with
+ * score -infinity has no weight, and a row for which nothing has weight is zero.
+ * (Sums are formed before they are divided, with
  * weights of up to 2^16: values have to stay below 2^80.)  The slots of a page outside the pool are
  * recorded as FUSE_ERR_DEVICE_BOUNDS and count as not there.  No atomics on
  * sums: equal inputs give equal outputs.  O may not overlap an input.

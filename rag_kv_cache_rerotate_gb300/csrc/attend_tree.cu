@@ -222,7 +222,8 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const __grid_con
         float* out = reinterpret_cast<float*>(a.O) +
                  ((int64_t)(at.q.row0 + vi / a.g) * a.n_q_heads + h * a.g + vi % a.g) * D + lane * EL;
 #pragma unroll
-        for (int e = 0; e < EL; ++e) out[e] = (v % 2 ? acc[v / 2][e].y : acc[v / 2][e].x) / l[v];
+        for (int e = 0; e < EL; ++e)
+          out[e] = l[v] == 0.f ? 0.f : (v % 2 ? acc[v / 2][e].y : acc[v / 2][e].x) / l[v];     // (nothing has weight: zeros)
       } else {
         if (lane == 0) a.part_ml[slot + v] = make_float2(m[v], l[v]);
 #pragma unroll
@@ -335,6 +336,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid
       }
       __syncwarp();
     }
+    if (l == 0.f) l = 1.f;                  // no part has weight, and o is 0
     if (mine == 0)
       store4(reinterpret_cast<T*>(a.O) + ((int64_t)row * a.n_q_heads + h * a.g + j) * D + ch,
              make_float4(o.x / l, o.y / l, o.z / l, o.w / l));

@@ -810,6 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           sum = f0 * x.y + f1 * y.y;
         }
         const unsigned long long fix = found ? found & seen_by(all, node) : 0;
+        const bool none = sum == 0.f;         // no key that the row sees has weight: zeros
         const float inv = 1.f / sum;
         __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.O) +
                              ((int64_t)(p.q.row0 + node) * a.n_q_heads + p.h * a.g + (vi & (a.g - 1))) * D;
@@ -829,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (valid && whole) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] *= inv;
+            for (int e = 0; e < 8; ++e) y[e] = none ? 0.f : y[e] * inv;
             Vec8<__nv_bfloat16>::store(out + e0, y);
           } else if (valid) {
             Vec8<float>::store(a.part_o + (slot + v) * D + e0, y);
