@@ -83,9 +83,11 @@ struct RowPlace {
 // The sequence of new row `row`, by a whole warp; false where it has none.  Up to 128
 // sequences are all read at once, four a lane, so that one read's latency finds it
 // (64 next tokens: 5.7 us, with a search and then a look at what it found 6.0; a prompt
-// of 10368: 44 and 49).
-__device__ __forceinline__ bool find_seq(const SeqArgs& a, int row, int* s, Seq* q) {
+// of 10368: 44 and 49).  Between them the warps look at every sequence, so that a bad one
+// is recorded that no row leads to (w: this warp's number).
+__device__ __forceinline__ bool find_seq(const SeqArgs& a, int row, int64_t w, int64_t warps, int* s, Seq* q) {
   if (a.n_seq > 128) {
+    for (int64_t i = w * 32 + threadIdx.x % 32; i < a.n_seq; i += warps * 32) seq_of(a, (int)i, q);      // (*q: below)
     *s = seq_of_row(a.rows, a.n_seq, row);
     return *s >= 0 && *s < a.n_seq && seq_of(a, *s, q);
   }
@@ -99,6 +101,11 @@ __device__ __forceinline__ bool find_seq(const SeqArgs& a, int row, int* s, Seq*
 #pragma unroll
   for (int i = 0; i < 4; ++i) below += s0 + i < a.n_seq && start[i] <= row;
   *s = __reduce_add_sync(0xffffffffu, below) - 1;
+  if (w == 0) {                           // (all of them are here: the first warp checks them)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (s0 + i < a.n_seq) check_seq(a, s0 + i, start[i], start[i + 1], len[i], q);
+  }
   if (*s < 0) return false;
   const int k = *s & 3, from = *s >> 2;
   const int r0 = __shfl_sync(0xffffffffu, k == 0 ? start[0] : k == 1 ? start[1] : k == 2 ? start[2] : start[3], from);
@@ -108,12 +115,12 @@ __device__ __forceinline__ bool find_seq(const SeqArgs& a, int row, int* s, Seq*
 }
 
 // Position and pool row of new row `row`, by a whole warp.
-__device__ __forceinline__ RowPlace place_row(const AppendArgs& a, int row) {
+__device__ __forceinline__ RowPlace place_row(const AppendArgs& a, int row, int64_t w) {
   const int lane = threadIdx.x % 32;
   RowPlace p{-1, -1, 0};
   int s;
   Seq q;
-  if (!find_seq(a.seq, row, &s, &q) || row < q.row0 || row >= q.row0 + q.n) return p;
+  if (!find_seq(a.seq, row, w, a.seq.n_rows << a.parts_log2, &s, &q) || row < q.row0 || row >= q.row0 + q.n) return p;
   const int i = row - q.row0;
   // its page and the parents of the new tokens up to it (lanes hold those of the first
   // 32 and of the others): read before any is looked at
@@ -182,7 +189,7 @@ __global__ void __launch_bounds__(kThreads)
     }
   };
   read(first);
-  const RowPlace p = place_row(a, (int)row);
+  const RowPlace p = place_row(a, (int)row, w);
   if (p.row < 0) return;                  // uniform
   for (int m = lane; m < a.rot / 2; m += 32) {
     const uint64_t t = (uint64_t)(uint32_t)p.pos * turns.f[m];

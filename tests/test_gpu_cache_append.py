@@ -232,3 +232,33 @@ def test_keep_leaves_a_bad_path(path, count):
     assert s.lens.tolist() == [5, 11]
     page, at = s.slots(0, range(14))
     assert all(torch.equal(a[page, at], b[page, at]) for a, b in zip(k, k0))
+
+
+@pytest.mark.parametrize("n", [3, 128, 129, 5000])
+@pytest.mark.parametrize("what", ["negative length", "past the table", "rows behind n_rows", "descending rows"])
+def test_bad_sequences_without_rows_are_recorded(what, n):
+    # no row leads to them; what the others bring is appended
+    lens, new = [9] * n, [0] * n
+    new[0], new[n // 2] = 3, 5
+    s = Step(StepCase(lens=lens, new=new, heads=(2, 1, 64), width=0))
+    bad = n - 1
+    if what == "negative length":
+        s.lens[bad] = -1
+    elif what == "past the table":
+        s.lens[bad] = s.tab.shape[1] * 16 + 1
+    elif what == "rows behind n_rows":
+        s.rows[n] = s.n_rows + 2
+    else:
+        s.rows[n] = s.n_rows - 1
+    t = Step(StepCase(lens=lens, new=new, heads=(2, 1, 64), width=0))
+    run(s, dict())
+    run(t, dict())
+    fk.check_errors(t.ws)
+    with pytest.raises(fk.FuseError) as e:
+        fk.check_errors(s.ws)
+    assert e.value.status == fk.FUSE_ERR_DEVICE_BOUNDS
+    last = 8 if what != "descending rows" else 7           # (a start that descends may cost rows next to it)
+    assert torch.equal(s.Qr[:last], t.Qr[:last])
+    for q in (0, n // 2):
+        page, at = s.slots(q, range(9, 9 + new[q] - (what == "descending rows")))
+        assert torch.equal(s.kp[page, at], t.kp[page, at]) and torch.equal(s.vp[page, at], t.vp[page, at])
