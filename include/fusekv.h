@@ -650,7 +650,7 @@ typedef struct {
   int32_t original_len;
   double factor;           /* >= 1 (LINEAR, LLAMA3, YARN) */
   double low, high;        /* 0 < low < high (LLAMA3, YARN) */
-  double mscale;           /* > 0 */
+  double mscale;           /* > 0, as a float */
 } fuse_rope_t;
 
 /* The rows of fuse_cache_append, in desc->dtype.  Q, K and V may be parts of

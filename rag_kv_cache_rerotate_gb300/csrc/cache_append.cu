@@ -345,7 +345,8 @@ fuse_status_t check_rope(const fuse_rope_t* r, int head_dim, int* rot) {
   *rot = r->rot_dim == 0 ? head_dim : r->rot_dim;
   if (*rot < 0 || *rot > head_dim) return FUSE_ERR_INVALID_ARG;
   if (*rot % 16 != 0) return FUSE_ERR_UNSUPPORTED;
-  if (!(r->mscale > 0.0) || !std::isfinite(r->mscale)) return FUSE_ERR_INVALID_ARG;
+  // (a float on the device)
+  if (!((float)r->mscale > 0.f) || !std::isfinite((float)r->mscale)) return FUSE_ERR_INVALID_ARG;
   if (r->scaling < FUSE_ROPE_PLAIN || r->scaling > FUSE_ROPE_YARN) return FUSE_ERR_INVALID_ARG;
   if (r->scaling == FUSE_ROPE_PLAIN) return FUSE_OK;
   if (!(r->factor >= 1.0) || !std::isfinite(r->factor)) return FUSE_ERR_INVALID_ARG;

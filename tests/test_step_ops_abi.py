@@ -196,3 +196,9 @@ def test_binding_refuses_what_a_pointer_hides(fk):
     pools = fk.PagePools([pool], [pool], fk.FUSE_BF16, 16)
     with pytest.raises(ValueError, match="count"):
         fk.cache_keep(d, pools, seqs, z(3, 4), z(2), ws)
+
+
+def test_mscale_is_a_float(fk):
+    for x in (1e-60, 1e60, float("inf"), -1.0):            # 0, infinite, infinite, negative as a float
+        assert _append(fk, rope=fk.rope_desc(mscale=x)) == fk.FUSE_ERR_INVALID_ARG, x
+    assert _append(fk, rope=fk.rope_desc(mscale=1.25), n_rows=0) == fk.FUSE_OK
