@@ -454,6 +454,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t c = it > (uint32_t)kSt ? it - kSt : 0; c < it; ++c) {
         tc::mbar_wait(&ctl->full[c % kSt], (c / kSt) & 1);
       }
+      if (qn0 > 0) tc::mbar_wait(&ctl->q_full[0], (qn0 - 1) & 1);
+      if (qn1 > 0) tc::mbar_wait(&ctl->q_full[1], (qn1 - 1) & 1);
     }
   } else if (warp == kWarpS) {
     // ------------------------------ S = Q K^T ------------------------------
