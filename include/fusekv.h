@@ -593,9 +593,13 @@ fuse_status_t fuse_pages_copy(const fuse_layer_desc_t* desc, const fuse_pools_t*
  * Sequence s holds lens[s] tokens in the pages tables[s][0 ..]: token t in row
  * t % block_size of page tables[s][t / block_size].  A call brings it the rows
  * rows[s] .. rows[s + 1] - 1 of its row tensors (none is fine), its new tokens
- * 0, 1, ..; new token i belongs in slot lens[s] + i.  A contiguous cache is
- * one of large pages.  Rows in front of rows[0] and from rows[n_seq] on are
- * neither read nor written.
+ * 0, 1, ..; new token i belongs in slot lens[s] + i.  Rows in front of rows[0]
+ * and from rows[n_seq] on are not written, and what they hold reaches nothing
+ * (they may be read, up to n_rows).
+ * A contiguous cache is one of large pages.  So is the fused cache of a request
+ * where its row0 is a multiple of block_size; requests packed at any row have
+ * pages of one token (table entry t: row0 + t).  Pages behind the fused rows
+ * take the new tokens.
  * Trees.  parents [n_rows] int32 (device) gives each new token the number,
  * within its sequence, of the one that it follows: a smaller one, or -1 for
  * what follows the held tokens.  NULL: each follows the one before it.
@@ -603,7 +607,8 @@ fuse_status_t fuse_pages_copy(const fuse_layer_desc_t* desc, const fuse_pools_t*
  * FUSE_ERR_UNSUPPORTED), sequences at most 65535.
  * A sequence whose row starts descend or pass n_rows, that has more than
  * max_new rows, whose length is negative, or whose slots pass the table's row
- * is recorded as FUSE_ERR_DEVICE_BOUNDS and left out.  A parent out of range is
+ * is recorded as FUSE_ERR_DEVICE_BOUNDS and left out (where row starts descend,
+ * rows that two sequences claim may be, too).  A parent out of range is
  * recorded and read as -1. */
 typedef struct {
   int32_t n_seq;
@@ -693,10 +698,10 @@ fuse_status_t fuse_cache_append(const fuse_layer_desc_t* desc, const fuse_rope_t
  * the unrounded ones).  What a row does not see does not reach it, infinities
  * and NaN included (rows behind a sequence's last slot among it); a key of
  * score -infinity has no weight, and a row for which nothing has weight is zero.
- * (Sums are formed before they are divided, with
- * weights of up to 2^16: values have to stay below 2^80.)  The slots of a page outside the pool are
- * recorded as FUSE_ERR_DEVICE_BOUNDS and count as not there.  No atomics on
- * sums: equal inputs give equal outputs.  O may not overlap an input.
+ * (Sums are formed before they are divided, with weights of up to 2^16: values
+ * have to stay below 2^80.)  The slots of a page outside the pool are recorded
+ * as FUSE_ERR_DEVICE_BOUNDS and count as not there.  No atomics on sums: equal
+ * inputs give equal outputs.  O may not overlap an input.
  * The workspace (of fuse_tree_workspace_size, which depends on the shapes and
  * n_seq only, not on lengths) follows the convention of fuse_workspace_size. */
 fuse_status_t fuse_tree_workspace_size(const fuse_layer_desc_t* desc, const fuse_seqs_t* seqs,
@@ -726,7 +731,9 @@ fuse_status_t fuse_attend_tree(const fuse_layer_desc_t* desc, const fuse_seqs_t*
  *   next [n_seq]
  * 1 <= max_path <= FUSE_TREE_MAX_NEW; a sequence with more rows is recorded as
  * FUSE_ERR_DEVICE_BOUNDS and treated as one without.  Rows of P and Qd are
- * p_stride and q_stride elements apart.  Sums keep about 48 bits.  Entries that
+ * p_stride and q_stride elements apart (where a row of P lies otherwise against
+ * 16 bytes than that of Qd, both are read entry by entry: about twice the time
+ * on large vocabularies).  Sums keep about 48 bits.  Entries that
  * are negative, infinite or NaN count as 0; they, tokens outside the vocabulary
  * and parents out of range (never accepted) are recorded where they are read.
  * Random numbers below 0 are read as 0, those from 1 on as the last float before
@@ -741,10 +748,10 @@ fuse_status_t fuse_verify_tree(int32_t n_seq, int64_t n_rows, int32_t vocab, con
 /* Keep the rows of a path in every pool and drop the other new ones: for i <
  * count[s], slot lens[s] + i receives what slot lens[s] + path[s][i] held, and
  * then lens[s] += count[s].  pools: F32 or BF16, as fuse_pages_copy's; seqs:
- * as the rows were appended.  No pool is listed twice (FUSE_ERR_INVALID_ARG).  A path that does not ascend or names a row that
- * the sequence does not have, or a count outside [0, max_path], is recorded as
- * FUSE_ERR_DEVICE_BOUNDS and leaves the sequence as it is; so does a page
- * outside the pool.  ws: FUSE_CACHE_WORKSPACE bytes. */
+ * as the rows were appended.  No pool is listed twice (FUSE_ERR_INVALID_ARG).
+ * A path that does not ascend or names a row that the sequence does not have, or
+ * a count outside [0, max_path], is recorded as FUSE_ERR_DEVICE_BOUNDS and leaves
+ * the sequence as it is; so does a page outside the pool.  ws: FUSE_CACHE_WORKSPACE bytes. */
 fuse_status_t fuse_cache_keep(const fuse_layer_desc_t* desc, const fuse_pools_t* pools,
                               const fuse_seqs_t* seqs, const int32_t* path, int32_t max_path,
                               const int32_t* count, void* ws, size_t ws_bytes,

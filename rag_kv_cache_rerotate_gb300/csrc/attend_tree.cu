@@ -34,8 +34,9 @@ static_assert(kVecs == 1 << 3 && kTile == 1 << 5 && kTreeTcVecs == 1 << 8 && kTr
 // 10 us of dependent reads, sums and code that is fetched for the first time, with
 // the join 13; lanes that read keys and values themselves, a few at a time, took 19
 // (22).  Many keys (16 sequences of 1000 to 4000 keys and 4 to 12 new tokens, 32 heads
-// of 128 on 8) take 277 us, bound by the instructions, a tile's 1024 FMAs of two floats
-// and the 384 reads of shared memory that feed them; that took 462.
+// of 128 on 8) take 277 to 285 us; that took 462.  Latency bounds them: a warp's 37 KB leave
+// 1.3 warps a scheduler, which issue in 37 % of the cycles (HBM is at 42 %), and units of
+// eight vectors copy the same keys once each.
 template <int D> struct SimtShared {        // of a warp
   float4 k[kTile][D / 4];                   // 16-byte pieces swapped by key: lanes read a column of them
   float4 v[kTile][D / 4];
@@ -239,7 +240,8 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const __grid_con
 // g is more), every one of them a share of its parts, kRows of them in flight.
 // Latency bounds it, so what the attention does not write (rows, lengths) is read
 // before it is waited for, and the first parts beside their weights.  Many rows have few
-// parts each: four warps.  Few rows may have many: sixteen.  (One token over 4096: 3 us of 16;
+// parts each: four warps.  Few rows may have many: sixteen.  (Here and in the other files of
+// the step times are those of graphs of a few calls, whose launch adds 1 to 2 us to each.  One token over 4096: 3 us of 16;
 // 8 trees of 64 over 33k: about 14 of 405, with 28 MB of parts.)
 constexpr int kRows = 4;
 
@@ -357,7 +359,10 @@ template <typename T> cudaError_t launch_join(const TreeArgs& a, int d, cudaStre
 // ---- host side ---------------------------------------------------------------
 
 constexpr int kCtas = 152;                // SMs
-constexpr int kSimtCtas = 5;              // CTAs of an SM (fp32 layers): as many fit where d = 64, three where d = 128
+// CTAs of an SM (fp32 layers): as many fit where d = 64, three where d = 128.  There, too, more
+// and shorter runs are faster, as units differ in length: 285 us with five, 368 with three (one
+// token over 3000 to 6000, 4 sequences: 53 and 48; d = 64: 32 and 41).
+constexpr int kSimtCtas = 5;
 
 fuse_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? FUSE_OK : FUSE_ERR_CUDA; }
 

@@ -17,7 +17,8 @@
 // With 64 vectors and less a tile of keys and values takes as long as HBM needs for it (16 trees
 // over 512 to 8192: 64 us, 6.5 TB/s between the start and the end).  With 256 the chain of a
 // stream's step binds it, 2990 cycles: S 610 (its operands come from shared memory), softmax
-// 1150, P V 480, hand-overs 750; 8 trees of 64 over 33k take 405 us, 1.37 PFLOP/s.
+// 1150, P V 480, hand-overs 750; 8 trees of 64 over 33k take 400 to 420 us, 1.33 to 1.39
+// PFLOP/s, and 450 to 475 called back to back, where the power cap holds the clock down.
 // The reference m is the first tile's maximum.  A later tile is weighed against it
 // as it stands, without its maximum being looked for: only where a thread's sum of
 // its weights passes 2^16 (no weight does otherwise) is the row's reference raised, O
@@ -28,8 +29,8 @@
 // costs the SM's copy unit about 100 cycles whatever its size, so that boxes of 64
 // columns kept pages of 16 tokens at 5.3 TB/s of the 6.6 that pages of 128 reach.  What
 // lies behind a sequence's last slot in its page comes along and is masked, its values
-// cleared.  With other pages the rows are gathered by 16-byte cp.async (about 4 TB/s;
-// single rows as tile::gather4 copies: 2).
+// cleared.  With other pages the rows are gathered by 16-byte cp.async (one token over 8 times
+// 33k: 4.6 TB/s, with boxes 6.25; single rows as tile::gather4 copies: 2).
 // A tile lies in shared memory as [group of 8 rows][64 columns][8 rows], 128-byte swizzled.
 //
 // What a row does not see must not reach it: its scores are replaced where they

@@ -13,11 +13,13 @@
 // the sums to fp32 would move that border over several tokens of a large
 // vocabulary, so entries, sums and the tests of acceptance are in pairs of floats (48
 // bits).  fp64 would be simpler, but an fp64 instruction of sixteen warps keeps an SM busy for
-// some 250 cycles: one chain of 8 over 32000 takes 9 us, with fp64 in the sums it took 27.
-// 64 sampled trees over 150001 tokens take 40 us.
+// some 250 cycles: one chain of 8 over 32000 took 27 us with fp64 in the sums and 14 with pairs
+// (7.0 now).  64 sampled trees over 150001 tokens take 38.5 us, a star of 63 refusals over
+// 32000 155, over 150001 393 (2.5 to 6.2 us a pass).
 //
-// One cluster per sequence, the vocabulary split over its CTAs; every warp writes its
-// sum into all of them (distributed shared memory).  Latency bounds it: a chain of
+// One cluster per sequence, the vocabulary split over its CTAs, which lie on SMs of their own
+// (of 64 clusters of 8 each does); every warp writes its sum into all of them (distributed
+// shared memory).  Latency bounds it: a chain of
 // reads (parents and tokens, probabilities of the drafts, a row, the part of it
 // with the border).
 #include <cooperative_groups.h>
@@ -118,7 +120,8 @@ __device__ __forceinline__ bool positive(Pair a) { return a.h + a.l > 0.f; }
 
 // What a pass over a row forms its entries from.  Rows of a large vocabulary need not
 // be aligned: `lead` entries are missing in front of a row's first aligned group of
-// four.  wide: whole groups are read at once.
+// four.  wide: whole groups are read at once (p and q lie alike; else entry by entry: 74 us
+// instead of 38 on 64 sampled trees).
 struct Pass {
   const float* p;
   const float* q;                         // null: p alone
@@ -574,7 +577,7 @@ extern "C" fuse_status_t fuse_verify_tree(int32_t n_seq, int64_t n_rows, int32_t
   cudaStream_t s = (cudaStream_t)stream;
   // As many CTAs a sequence as run at a time, and as have 8 entries a thread: 58 sequences
   // of a vocabulary of 2300 take 11 us with one or two, 17 with eight; 64 of 150 001 take 45
-  // with eight, 71 with two; one of 32 000 9 with eight.
+  // with eight, 71 with two; one of 32 000 9 with eight (graphs of a few calls).
   int dev = 0, sms = 1;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
